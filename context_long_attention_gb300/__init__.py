@@ -7,7 +7,8 @@ The functions keep the C names:
 
     cp_shard_plan, cp_prefill_attn, cp_decode_plan, cp_decode_plan_ex,
     cp_kv_shard_pack, cp_decode_attn, cp_lse_merge, cp_lse_fold,
-    cp_device_error_check
+    cp_mla_expand, cp_mla_absorb, cp_mla_project, cp_mla_prefill_attn,
+    cp_page_slots, cp_cache_append, cp_device_error_check
 
 There is no CPU fallback: importing the package loads the library, and
 raises if it has not been built (``__graft_entry__.build()``).
@@ -23,11 +24,16 @@ from ._binding import (  # noqa: F401
     CP_FP8_E4M3,
     CP_FP32,
     CP_INTERLEAVE,
+    CP_SLOTS_BAD_LENGTH,
+    CP_SLOTS_NO_PAGES,
+    CP_SLOTS_TABLE_FULL,
+    CP_SLOTS_TOO_MANY,
     CP_ZIGZAG,
     CpError,
     DecodePlan,
     PageTable,
     PrefillPlan,
+    cp_cache_append,
     cp_decode_attn,
     cp_decode_attn_merged,
     cp_decode_attn_noalloc,
@@ -41,6 +47,11 @@ from ._binding import (  # noqa: F401
     cp_kv_shard_pack_paged,
     cp_lse_fold,
     cp_lse_merge,
+    cp_mla_absorb,
+    cp_mla_expand,
+    cp_mla_prefill_attn,
+    cp_mla_project,
+    cp_page_slots,
     cp_plan_size,
     cp_prefill_attn,
     cp_shard_plan,

@@ -45,6 +45,7 @@ if os.path.isdir(os.path.join(_HERE, "csrc")):
 lib = ctypes.CDLL(lib_path)
 
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_i64 = ctypes.c_int64
 _szp = ctypes.POINTER(ctypes.c_size_t)
 _SIGS = {
     "cp_last_error": (ctypes.c_char_p, []),
@@ -82,6 +83,12 @@ _SIGS = {
                                    _vp, _vp, _vp, _sz, _vp]),
     "cp_sparse_decode_attn_merged": (_i, [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f,
                                           _vp, _i, _vp, _vp, _sz, _vp]),
+    "cp_mla_expand": (_i, [_vp, _i64, _vp, _i, _i, _vp, _vp]),
+    "cp_mla_absorb": (_i, [_vp, _vp, _i, _i, _vp, _vp]),
+    "cp_mla_project": (_i, [_vp, _vp, _i, _i, _vp, _vp]),
+    "cp_mla_prefill_attn": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i64, _i, _f, _vp, _vp, _vp]),
+    "cp_page_slots": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp]),
+    "cp_cache_append": (_i, [_vp, _i, _i, _vp, _i64, _vp, _i64, _vp, _i, _i, _vp, _vp, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -363,9 +370,33 @@ class PageTable:
         self.num_pages = int(num_pages)
         self.dev = torch.from_numpy(self.host).to(device) if device is not None else None
 
+    @classmethod
+    def on_device(cls, table, page_size: int, num_pages: int):
+        """A table [C * R, max_pages] int32 that lives on the GPU
+        (cp_page_slots fills it in place); it has no host copy until
+        sync_host()."""
+        if table.dtype != torch.int32 or table.dim() != 2 or not table.is_cuda or not table.is_contiguous():
+            raise ValueError("the table must be a contiguous int32 CUDA tensor [C * R, max_pages]")
+        self = cls.__new__(cls)
+        self.host, self.dev = None, table
+        self.max_pages, self.page_size, self.num_pages = int(table.shape[1]), int(page_size), int(num_pages)
+        return self
+
+    def sync_host(self):
+        """Copies the device table to the host copy that the paged pack and
+        decode check (waits for the current stream)."""
+        self.host = self.dev.cpu().numpy()
+        return self
+
     @property
     def pool_rows(self) -> int:
         return self.num_pages * self.page_size
+
+
+def _host_table(pages: PageTable):
+    if pages.host is None:
+        raise ValueError("the page table has no host copy: call sync_host() first")
+    return _np_ptr(pages.host)
 
 
 def cp_kv_shard_pack_paged(plan: DecodePlan, pages: PageTable, kv, kv_scale=None, pool=None,
@@ -383,7 +414,7 @@ def cp_kv_shard_pack_paged(plan: DecodePlan, pages: PageTable, kv, kv_scale=None
     _check(lib.cp_kv_shard_pack_paged(_np_ptr(plan.host), _ptr(plan.dev), _dtype_code(kv), _ptr(kv),
                                       _ptr(kv_scale), row_elems, _ptr(pool),
                                       _ptr(scale_pool) if kv_scale is not None else None,
-                                      _np_ptr(pages.host), _ptr(pages.dev), pages.max_pages,
+                                      _host_table(pages), _ptr(pages.dev), pages.max_pages,
                                       pages.page_size, pages.num_pages, _stream(kv.device)))
     return pool, (scale_pool if kv_scale is not None else None)
 
@@ -412,7 +443,7 @@ def cp_decode_attn_paged(plan: DecodePlan, pages: PageTable, mode: int, q, k_poo
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.cp_decode_attn_paged(_np_ptr(plan.host), _ptr(plan.dev), mode, kv_dtype, _ptr(q),
-                                    _ptr(kp), _ptr(v_pool), _ptr(scale_pool), _np_ptr(pages.host),
+                                    _ptr(kp), _ptr(v_pool), _ptr(scale_pool), _host_table(pages),
                                     _ptr(pages.dev), pages.max_pages, pages.page_size,
                                     pages.num_pages, H, Hkv, Dqk, Dv, float(sm_scale), _ptr(o_part),
                                     _ptr(lse_part), _ptr(ws), ws_bytes, _stream(q.device)))
@@ -704,6 +735,213 @@ def cp_sparse_decode_attn_merged(plan: DecodePlan, pair_count, mode: int, q, sel
                                             H, Hkv, Dqk, Dv, float(sm_scale), _ptr(o), _dtype_code(o), _ptr(lse),
                                             _ptr(ws), ws_bytes, _stream(q.device)))
     return o, lse
+
+
+# ---------------------------------------------------------------- latent attention
+
+LATENT_DIM, MLA_NOPE_DIM, MLA_ROPE_DIM, MLA_V_DIM = 512, 128, 64, 128
+
+
+def _need(name, t, dtype, shape, device=None):
+    """A contiguous CUDA tensor of this dtype and shape (None: any extent),
+    on `device` if given."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: need {dtype}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: need shape {shape}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+
+
+def _rows(name, t, cols, dtype, device=None):
+    """(pointer, row stride) of a CUDA tensor [n, >= cols] whose rows are
+    dense and may lie apart (a view of a wider tensor)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: need {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 2 or t.shape[1] < cols or t.stride(1) != 1:
+        raise ValueError(f"{name}: need [n, {cols}] with dense rows, got {tuple(t.shape)}, strides {t.stride()}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) on the device's current stream, with the device
+    current (kernels launch on the current device)."""
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != 0:
+        _check(st)
+
+
+def _w_kv(w_kv, device):
+    _need("w_kv", w_kv, torch.bfloat16, (None, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), device)
+    return w_kv.shape[0]
+
+
+def _out(name, out, dtype, shape, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(name, out, dtype, shape, device)
+    return out
+
+
+def cp_mla_expand(latent, w_kv, out=None):
+    """Keys and values of latent rows: latent [T, >= 512] bf16 (its first 512
+    columns; rows may be a view of the 576-wide cache), w_kv [H, 256, 512]
+    -> kv [T, H, 256] (128 key dims, then 128 value dims of each head)."""
+    dev = latent.device
+    ptr, stride = _rows("latent", latent, LATENT_DIM, torch.bfloat16)
+    H = _w_kv(w_kv, dev)
+    out = _out("out", out, torch.bfloat16, (latent.shape[0], H, MLA_NOPE_DIM + MLA_V_DIM), dev)
+    _call(dev, lib.cp_mla_expand, ptr, stride, w_kv.data_ptr(), latent.shape[0], H, out.data_ptr())
+    return out
+
+
+def _per_head(name, x, w_kv, cols, out_cols, out, fn):
+    dev = x.device
+    H = _w_kv(w_kv, dev)
+    _need(name, x, torch.bfloat16, (None,) * (x.dim() - 2) + (H, cols))
+    lead = x.shape[:-2]
+    out = _out("out", out, torch.bfloat16, (*lead, H, out_cols), dev)
+    _call(dev, fn, x.data_ptr(), w_kv.data_ptr(), lead.numel(), H, out.data_ptr())
+    return out
+
+
+def cp_mla_absorb(q, w_kv, out=None):
+    """Queries into the latent space: q [..., H, 192] bf16 (128 dims, 64
+    rotated), w_kv [H, 256, 512] -> [..., H, 576], the query of
+    cp_decode_attn(mode CP_DECODE_MLA)."""
+    return _per_head("q", q, w_kv, MLA_NOPE_DIM + MLA_ROPE_DIM, LATENT_DIM + MLA_ROPE_DIM, out, lib.cp_mla_absorb)
+
+
+def cp_mla_project(o_lat, w_kv, out=None):
+    """Latent outputs of the MLA decode to value dims: o_lat [..., H, 512]
+    bf16, w_kv [H, 256, 512] -> [..., H, 128]."""
+    return _per_head("o_lat", o_lat, w_kv, LATENT_DIM, MLA_V_DIM, out, lib.cp_mla_project)
+
+
+def cp_mla_prefill_attn(plan: PrefillPlan, q, kv, k_rope, sm_scale=None, rank: int = -1, out=None, lse=None):
+    """Causal latent attention in its expanded form for the queries of
+    ``rank`` (-1: all ranks, rank-major).  q [T, H, 192]; kv [KV, H, 256]
+    (cp_mla_expand); k_rope [KV, 64], a view of the latent cache's last
+    columns or a tensor of its own; returns (o [rows, H, 128], lse [rows, H])."""
+    dev = q.device
+    _need("q", q, torch.bfloat16, (plan.T, None, MLA_NOPE_DIM + MLA_ROPE_DIM))
+    H = q.shape[1]
+    _need("kv", kv, torch.bfloat16, (plan.KV, H, MLA_NOPE_DIM + MLA_V_DIM), dev)
+    rope, stride = _rows("k_rope", k_rope, MLA_ROPE_DIM, torch.bfloat16, dev)
+    if k_rope.shape[0] != plan.KV:
+        raise ValueError(f"k_rope has {k_rope.shape[0]} rows, the plan {plan.KV}")
+    if plan.dev is None or plan.dev.device != dev:
+        raise ValueError(f"the plan has no device part on {dev}")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(MLA_NOPE_DIM + MLA_ROPE_DIM)
+    rows = plan.rank_rows(rank)
+    out = _out("out", out, torch.bfloat16, (rows, H, MLA_V_DIM), dev)
+    lse = _out("lse", lse, torch.float32, (rows, H), dev)
+    _call(dev, lib.cp_mla_prefill_attn, plan.host.ctypes.data, plan.dev.data_ptr(), rank, q.data_ptr(), kv.data_ptr(),
+          rope, stride, H, sm_scale, out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+# ---------------------------------------------------------------- pages, slots, new tokens
+
+CP_SLOTS_BAD_LENGTH, CP_SLOTS_TABLE_FULL, CP_SLOTS_NO_PAGES, CP_SLOTS_TOO_MANY = 1, 2, 4, 8
+
+
+def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos, max_tokens: int, slots=None,
+                  cu_new=None, info=None):
+    """Pages and slots of a step's new tokens, from lengths on the GPU.
+
+    ctx_len, new_len [B] int32: cached and new tokens of every request; the
+    pages that the new ones need are taken from free_ids at free_pos ([1]
+    int32, or an earlier call's info[1:2]) on and written into
+    ``pages.dev`` (its host copy is brought up to date by
+    ``pages.sync_host()`` where a decode call needs it).  Returns (slots
+    [max_tokens], cu_new [B + 1], info [4] = status, next free_pos, pages
+    taken, new tokens), all int32 on the GPU; see cpattn.h for the status."""
+    i32, table = torch.int32, pages.dev
+    if table is None:
+        raise ValueError("the page table has no device copy")
+    dev = table.device
+    B = ctx_len.shape[0]
+    _need("page table", table, i32, (C * B, pages.max_pages))
+    _need("ctx_len", ctx_len, i32, (B,), dev)
+    _need("new_len", new_len, i32, (B,), dev)
+    _need("free_ids", free_ids, i32, (None,), dev)
+    _need("free_pos", free_pos, i32, (1,), dev)
+    slots = _out("slots", slots, i32, (max_tokens,), dev)
+    if cu_new is None and info is None:
+        both = torch.empty(B + 5, dtype=i32, device=dev)  # one allocation for the two small outputs
+        info, cu_new = both[:4], both[4:]
+    cu_new = _out("cu_new", cu_new, i32, (B + 1,), dev)
+    info = _out("info", info, i32, (4,), dev)
+    _call(dev, lib.cp_page_slots, C, B, ctx_len.data_ptr(), new_len.data_ptr(), table.data_ptr(), pages.max_pages,
+          pages.page_size, pages.num_pages, free_ids.data_ptr(), free_ids.shape[0], free_pos.data_ptr(),
+          slots.data_ptr(), max_tokens, cu_new.data_ptr(), info.data_ptr())
+    return slots, cu_new, info
+
+
+def _new_rows(name, t, n, pool, dev):
+    """(pointer, row stride) of new tokens' rows [n, ...] shaped like the
+    pool's; only the first dimension may be strided."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.shape[0] != n or t.shape[1:] != pool.shape[1:]:
+        raise ValueError(f"{name}: need {(n, *pool.shape[1:])}, got {tuple(t.shape)}")
+    row = pool.shape[1:].numel()
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    inner = 1
+    for size, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if st != inner and size != 1:
+            raise ValueError(f"{name}: a row must be dense, got strides {t.stride()}")
+        inner *= size
+    return t.data_ptr(), t.stride(0)
+
+
+def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=None, new_scale=None):
+    """New tokens' rows into a paged pool at slots [n] int32 (a slot outside
+    the pool, such as -1, is skipped; slots must differ).
+
+    k_new [n, ...] and, for a GQA cache, v_new [n, ...] into k_pool / v_pool
+    [pool_rows, ...] of the same row shape.  Pools of the rows' own dtype take
+    them as they are (E4M3 codes with new_scale [n]); bf16 or fp32 rows into
+    an E4M3 pool (uint8 or float8_e4m3fn) are quantised with one scale a
+    token, amax / 448 over its K and V, written to scale_pool [pool_rows]."""
+    dev = k_pool.device
+    n = slots.shape[0]
+    if not k_pool.is_cuda or not k_pool.is_contiguous():
+        raise ValueError("k_pool must be a contiguous CUDA tensor")
+    _need("slots", slots, torch.int32, (None,), dev)
+    rows = k_pool.shape[0]
+    kp, ks = _new_rows("k_new", k_new, n, k_pool, dev)
+    src, pool = _dtype_code(k_new), _dtype_code(k_pool)
+    vp = vs = vpool = 0
+    if (v_new is None) != (v_pool is None):
+        raise ValueError("v_new and v_pool must both be given or both None")
+    if v_new is not None:
+        if _dtype_code(v_new) != src or _dtype_code(v_pool) != pool:
+            raise TypeError("V must have K's dtypes")
+        if v_pool.shape != k_pool.shape or v_pool.device != dev or not v_pool.is_contiguous():
+            raise ValueError("v_pool must be a contiguous tensor like k_pool")
+        vp, vs = _new_rows("v_new", v_new, n, v_pool, dev)
+        vpool = v_pool.data_ptr()
+    if scale_pool is not None:
+        _need("scale_pool", scale_pool, torch.float32, (rows,), dev)
+    if new_scale is not None:
+        _need("new_scale", new_scale, torch.float32, (n,), dev)
+    _call(dev, lib.cp_cache_append, slots.data_ptr(), n, src, kp, ks, vp or None, vs,
+          None if new_scale is None else new_scale.data_ptr(), k_pool.shape[1:].numel(), pool, k_pool.data_ptr(),
+          vpool or None, None if scale_pool is None else scale_pool.data_ptr(), rows)
 
 
 # ---------------------------------------------------------------- NVTX ranges

@@ -1,0 +1,372 @@
+// Pages, slots and new tokens of a paged token-sharded decode cache.
+//
+// * page_slots_kernel: from request lengths on the GPU, the pages that a
+//   step's new tokens need (into the page table) and every new token's pool
+//   row ("How GPUs Share a Long Context During LLM Inference" §3.1, "Storing
+//   each token once": token p on shard p mod C at row p / C; serving caches keep
+//   those rows in pages, "DeepSeek-V4 Attention Inference Systems" §9.2).
+// * append kernels: the new tokens' rows into those pool rows, as they are or
+//   as E4M3 codes with one fp32 scale a token.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+
+namespace cpattn {
+namespace {
+
+// ------------------------------------------------------------------ slots
+//
+// L tokens over C shards: with q = L / C and m = L mod C, shards r < m hold
+// q + 1 rows and the others q.  So the pages of shards 0..r-1 have a closed
+// form, and only the requests need a running sum:
+//   F(L, r) = min(r, m) ceil((q + 1) / page) + max(0, r - m) ceil(q / page)
+// New pages are taken in the order of requests, then shards, then pages.
+// Every block runs the sum over the requests for itself (a few loads a
+// thread) and writes its own part of the table and the slots, so the step is
+// one launch without a barrier between blocks.
+constexpr int kSlotThreads = 512;
+constexpr int kSlotTokens = 4;  // consecutive tokens a thread
+
+struct PageCount {
+  int q, m, small, big;  // rows and pages of a shard: q (small pages), or q + 1 (big) for the first m
+};
+__device__ __forceinline__ PageCount page_count(int L, int C, int page) {
+  PageCount c;
+  c.q = L / C;
+  c.m = L - c.q * C;
+  c.small = c.q / page + (c.q % page != 0);
+  c.big = c.q / page + 1;
+  return c;
+}
+__device__ __forceinline__ long long pages_before(const PageCount& c, int r) {
+  return (long long)min(r, c.m) * c.big + (long long)max(0, r - c.m) * c.small;
+}
+__device__ __forceinline__ int pages_of(const PageCount& c, int r) { return r < c.m ? c.big : c.small; }
+
+__global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageSlotsArgs a) {
+  extern __shared__ int32_t sm[];
+  int32_t* s_cu = sm;              // [B + 1] new tokens before request b
+  int32_t* s_take = sm + a.B + 1;  // [B] pages taken before request b
+  __shared__ long long w_tok[kSlotThreads / 32], w_take[kSlotThreads / 32];
+  __shared__ int w_bad[kSlotThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = a.B, C = a.C, page = a.page_size;
+
+  // running sums over the requests: a thread takes `per` consecutive ones
+  const int per = (B + kSlotThreads - 1) / kSlotThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  long long tok = 0, take = 0;
+  int bad = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int L = a.ctx_len[b], n = a.new_len[b];
+    if (L < 0 || n < 0 || L > 0x7FFFFFFF - n) {
+      bad |= CP_SLOTS_BAD_LENGTH;
+      continue;
+    }
+    const PageCount want = page_count(L + n, C, page), have = page_count(L, C, page);
+    if (pages_of(want, 0) > a.max_pages) bad |= CP_SLOTS_TABLE_FULL;
+    tok += n;
+    take += pages_before(want, C) - pages_before(have, C);
+  }
+  long long tok_in = tok, take_in = take;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, tok_in, d), y = __shfl_up_sync(0xffffffffu, take_in, d);
+    if (lane >= d) {
+      tok_in += x;
+      take_in += y;
+    }
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (lane == 31) {
+    w_tok[warp] = tok_in;
+    w_take[warp] = take_in;
+    w_bad[warp] = bad;
+  }
+  __syncthreads();
+  long long tok0 = tok_in - tok, take0 = take_in - take, total = 0, taken = 0;
+#pragma unroll
+  for (int w = 0; w < kSlotThreads / 32; ++w) {
+    if (w < warp) {
+      tok0 += w_tok[w];
+      take0 += w_take[w];
+    }
+    total += w_tok[w];
+    taken += w_take[w];
+    bad |= w_bad[w];
+  }
+  const int pos = *a.free_pos;
+  if (pos < 0 || pos > a.n_free || taken > a.n_free - pos) bad |= CP_SLOTS_NO_PAGES;
+  if (total > a.max_tokens) bad |= CP_SLOTS_TOO_MANY;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.info[0] = bad;
+    a.info[1] = bad ? pos : pos + (int)taken;
+    a.info[2] = bad ? 0 : (int)taken;
+    a.info[3] = bad ? 0 : (int)total;
+  }
+  if (bad) {  // nothing is taken: no table entry changes, no token has a slot
+    for (int b = tid; b <= B && blockIdx.x == 0; b += kSlotThreads) a.cu_new[b] = 0;
+    for (long long t = (long long)blockIdx.x * kSlotThreads + tid; t < a.max_tokens;
+         t += (long long)gridDim.x * kSlotThreads)
+      a.slots[t] = -1;
+    return;
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int L = a.ctx_len[b], n = a.new_len[b];
+    s_cu[b] = (int)tok0;
+    s_take[b] = (int)take0;
+    tok0 += n;
+    take0 += pages_before(page_count(L + n, C, page), C) - pages_before(page_count(L, C, page), C);
+  }
+  if (tid == 0) s_cu[B] = (int)total;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= B; b += kSlotThreads) a.cu_new[b] = s_cu[b];
+
+  auto id_of = [&](long long i) {  // a page id of the free list, -1 if it names no page
+    const int id = a.free_ids[i];
+    return id >= 0 && id < a.num_pages ? id : -1;
+  };
+  // new table entries: a warp per (request, shard) pair where the grid has
+  // warps enough (few pairs with many pages each), else a thread per pair
+  {
+    const int pairs = B * C;
+    const int warps = gridDim.x * (kSlotThreads / 32);
+    const bool wide = pairs <= warps;
+    const int step = wide ? 32 : 1, off = wide ? lane : 0;
+    const int first = wide ? warp * gridDim.x + blockIdx.x : blockIdx.x * kSlotThreads + tid;
+    const int stride = wide ? warps : gridDim.x * kSlotThreads;
+    for (int u = first; u < pairs; u += stride) {
+      const int b = u / C, r = u - b * C;
+      const int L = a.ctx_len[b], n = a.new_len[b];
+      if (n == 0) continue;
+      const PageCount want = page_count(L + n, C, page), have = page_count(L, C, page);
+      const int h0 = pages_of(have, r), h1 = pages_of(want, r);
+      const long long src = (long long)pos + s_take[b] + pages_before(want, r) - pages_before(have, r) - h0;
+      int32_t* row = a.table + ((long long)r * B + b) * a.max_pages;
+      for (int i = h0 + off; i < h1; i += step) row[i] = id_of(src + i);
+    }
+  }
+  // slots: four consecutive tokens a thread
+  const long long stride = (long long)gridDim.x * kSlotThreads * kSlotTokens;
+  for (long long t0 = ((long long)blockIdx.x * kSlotThreads + tid) * kSlotTokens; t0 < a.max_tokens; t0 += stride) {
+    int out[kSlotTokens];
+    int lo = 0, hi = B - 1;  // the last request starting at or before t0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_cu[mid] <= t0) lo = mid; else hi = mid - 1;
+    }
+    int b = lo, L = 0;
+    PageCount want, have;
+    bool fresh = true;
+#pragma unroll
+    for (int k = 0; k < kSlotTokens; ++k) {
+      const long long t = t0 + k;
+      out[k] = -1;
+      if (t >= total) continue;
+      while (t >= s_cu[b + 1]) {  // requests without new tokens are passed over
+        ++b;
+        fresh = true;
+      }
+      if (fresh) {
+        L = a.ctx_len[b];
+        want = page_count(s_cu[b + 1] - s_cu[b] + L, C, page);
+        have = page_count(L, C, page);
+        fresh = false;
+      }
+      const int p = L + (int)(t - s_cu[b]);
+      const int i = p / C, r = p - i * C, pg = i / page;
+      const int h0 = pages_of(have, r);
+      int id;
+      if (pg < h0) {
+        id = a.table[((long long)r * B + b) * a.max_pages + pg];
+        if (id < 0 || id >= a.num_pages) id = -1;
+      } else {
+        id = id_of((long long)pos + s_take[b] + pages_before(want, r) - pages_before(have, r) + pg - h0);
+      }
+      if (id >= 0) out[k] = id * page + (i - pg * page);
+    }
+    if (t0 + kSlotTokens <= a.max_tokens) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(out[0], out[1], out[2], out[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kSlotTokens; ++k)
+        if (t0 + k < a.max_tokens) a.slots[t0 + k] = out[k];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ append
+
+constexpr int kAppendThreads = 128;
+
+// Rows as they are: LPR lanes a row, 16-byte pieces of K then of V.
+template <int LPR>
+__global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const AppendArgs a, int elem) {
+  const int per_block = kAppendThreads / LPR;
+  const long long row = (long long)blockIdx.x * per_block + threadIdx.x / LPR;
+  const int lane = threadIdx.x % LPR;
+  if (row >= a.n) return;
+  const int slot = a.slots[row];
+  if (slot < 0 || slot >= a.pool_rows) return;
+  const int vec = a.row_elems * elem / 16;
+  const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k) + row * a.k_stride * elem);
+  uint4* kd = static_cast<uint4*>(a.k_pool) + (long long)slot * vec;
+#pragma unroll 4
+  for (int c = lane; c < vec; c += LPR) kd[c] = k[c];
+  if (a.v) {
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.v) + row * a.v_stride * elem);
+    uint4* vd = static_cast<uint4*>(a.v_pool) + (long long)slot * vec;
+#pragma unroll 4
+    for (int c = lane; c < vec; c += LPR) vd[c] = v[c];
+  }
+  if (a.scale_pool && lane == 0) a.scale_pool[slot] = a.new_scale[row];
+}
+
+// Eight elements of a row as floats.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+  uint4 x;
+  __device__ void load(const void* p) { x = __ldg(static_cast<const uint4*>(p)); }
+  __device__ void zero() { x = make_uint4(0, 0, 0, 0); }
+  __device__ float at(int i) const {
+    const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <>
+struct Piece<float> {
+  uint4 x, y;
+  __device__ void load(const void* p) {
+    x = __ldg(static_cast<const uint4*>(p));
+    y = __ldg(static_cast<const uint4*>(p) + 1);
+  }
+  __device__ void zero() { x = y = make_uint4(0, 0, 0, 0); }
+  __device__ float at(int i) const {
+    const uint4& w = i < 4 ? x : y;
+    const int k = i & 3;
+    return __uint_as_float(k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
+  }
+};
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// Codes of eight elements: rn_E4M3(x / scale), the quotient rounded to fp32
+// first as a division gives it.
+template <typename T>
+__device__ __forceinline__ uint2 codes_of(const Piece<T>& x, float scale) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x.at(i), scale);
+  return make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+}
+
+// Rows to E4M3 codes with one scale a token, amax / 448 (1 for a row of
+// zeros) over its K row and, where there is one, its V row: a warp a token,
+// PIECES pieces of eight elements a lane kept in registers between the
+// maximum and the codes (PIECES = 0: any row length, read twice).
+template <typename T, int PIECES>
+__global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const AppendArgs a) {
+  const long long row = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= a.n) return;
+  const int slot = a.slots[row];
+  if (slot < 0 || slot >= a.pool_rows) return;
+  const int vec = a.row_elems / 8, all = a.v ? 2 * vec : vec;
+  const T* k = static_cast<const T*>(a.k) + row * a.k_stride;
+  const T* v = a.v ? static_cast<const T*>(a.v) + row * a.v_stride : nullptr;
+  uint2* kd = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_pool) + (long long)slot * a.row_elems);
+  uint2* vd = a.v ? reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_pool) + (long long)slot * a.row_elems) : nullptr;
+  auto src = [&](int c) { return static_cast<const void*>(c < vec ? k + 8 * c : v + 8 * (c - vec)); };
+  auto dst = [&](int c) { return c < vec ? kd + c : vd + (c - vec); };
+  float amax = 0.f;
+  Piece<T> x[PIECES ? PIECES : 1];
+  if (PIECES) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int c = lane + 32 * i;
+      if (c < all) x[i].load(src(c)); else x[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[i].at(e)));
+  } else {
+    for (int c = lane; c < all; c += 32) {
+      x[0].load(src(c));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[0].at(e)));
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  if (lane == 0) a.scale_pool[slot] = scale;
+  if (PIECES) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int c = lane + 32 * i;
+      if (c < all) *dst(c) = codes_of(x[i], scale);
+    }
+  } else {
+    for (int c = lane; c < all; c += 32) {
+      x[0].load(src(c));
+      *dst(c) = codes_of(x[0], scale);
+    }
+  }
+}
+
+template <typename T>
+void append_e4m3(const AppendArgs& a, cudaStream_t s) {
+  const int per_lane = ((a.v ? 2 : 1) * a.row_elems / 8 + 31) / 32;
+  const unsigned grid = (unsigned)((a.n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+  if (per_lane <= 3) append_e4m3_kernel<T, 3><<<grid, kAppendThreads, 0, s>>>(a);
+  else if (per_lane <= 8) append_e4m3_kernel<T, 8><<<grid, kAppendThreads, 0, s>>>(a);
+  else append_e4m3_kernel<T, 0><<<grid, kAppendThreads, 0, s>>>(a);
+}
+
+template <int LPR>
+void append_copy(const AppendArgs& a, int elem, cudaStream_t s) {
+  const int per_block = kAppendThreads / LPR;
+  append_copy_kernel<LPR><<<(unsigned)((a.n + per_block - 1) / per_block), kAppendThreads, 0, s>>>(a, elem);
+}
+
+}  // namespace
+
+cudaError_t launch_page_slots(const PageSlotsArgs& a, cudaStream_t s) {
+  const size_t smem = (size_t)(2 * a.B + 1) * sizeof(int32_t);
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const long long by_tok = ((long long)a.max_tokens + kSlotThreads * kSlotTokens - 1) / (kSlotThreads * kSlotTokens);
+  const long long by_pair = ((long long)a.B * a.C + 4 * kSlotThreads - 1) / (4 * kSlotThreads);
+  long long grid = by_tok > by_pair ? by_tok : by_pair;
+  if (grid > 304) grid = 304;
+  page_slots_kernel<<<(unsigned)grid, kSlotThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const AppendArgs& a, cp_dtype src, cp_dtype pool, cudaStream_t s) {
+  if (src == pool) {
+    const int elem = src == CP_FP32 ? 4 : src == CP_BF16 ? 2 : 1;
+    const int vec = a.row_elems * elem / 16;
+    if (vec <= 8) append_copy<8>(a, elem, s);
+    else if (vec <= 16) append_copy<16>(a, elem, s);
+    else append_copy<32>(a, elem, s);
+  } else if (src == CP_BF16) {
+    append_e4m3<__nv_bfloat16>(a, s);
+  } else {
+    append_e4m3<float>(a, s);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace cpattn

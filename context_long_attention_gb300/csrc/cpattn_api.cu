@@ -44,6 +44,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int align4(int w) { return (w + 3) & ~3; }
 
+constexpr int64_t kMaxRowStride = 1LL << 31;  // elements between rows of a strided input (a tensor map's limit is 2^40 bytes)
+
 // Status words of the bounded waits, one copy per device.
 __device__ unsigned g_cp_status[4];
 
@@ -1292,6 +1294,126 @@ cp_status cp_sparse_decode_attn_merged(const void* host_plan, const void* dev_pl
   }
   return run_decode_merged(h, (const int32_t*)host_plan, dev_plan, mode, kv_dtype, q, K, V, S, shard_rows, Hq,
                            Hkv, Dqk, Dv, sm_scale, o, o_dtype, lse, ws, ws_bytes, stream, pair_count);
+}
+
+// ------------------------------------------------------------------ latent attention
+
+cp_status cp_mla_expand(const void* latent, int64_t latent_stride, const void* w_kv, int T, int H, void* kv,
+                        void* stream) {
+  if (T < 0 || H < 1) return fail(CP_ERR_INVALID_ARG, "T=%d, H=%d: need T >= 0, H >= 1", T, H);
+  if (T == 0) return ok();
+  if (!latent || !w_kv || !kv) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(latent) || !aligned16(w_kv) || !aligned16(kv))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  if (latent_stride < 512 || latent_stride % 8 || latent_stride > kMaxRowStride)
+    return fail(CP_ERR_INVALID_ARG, "latent_stride=%lld: need a multiple of 8 from 512 on", (long long)latent_stride);
+  const cudaError_t e = launch_mla_expand(latent, latent_stride, w_kv, T, H, kv, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "latent expansion kernel");
+  return ok();
+}
+
+cp_status cp_mla_absorb(const void* q, const void* w_kv, int N, int H, void* q_lat, void* stream) {
+  if (N < 0 || H < 1) return fail(CP_ERR_INVALID_ARG, "N=%d, H=%d: need N >= 0, H >= 1", N, H);
+  if (N == 0) return ok();
+  if (!q || !w_kv || !q_lat) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(q) || !aligned16(w_kv) || !aligned16(q_lat))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  const cudaError_t e = launch_mla_absorb(q, w_kv, N, H, q_lat, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "query absorption kernel");
+  return ok();
+}
+
+cp_status cp_mla_project(const void* o_lat, const void* w_kv, int N, int H, void* o, void* stream) {
+  if (N < 0 || H < 1) return fail(CP_ERR_INVALID_ARG, "N=%d, H=%d: need N >= 0, H >= 1", N, H);
+  if (N == 0) return ok();
+  if (!o_lat || !w_kv || !o) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(o_lat) || !aligned16(w_kv) || !aligned16(o))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  const cudaError_t e = launch_mla_project(o_lat, w_kv, N, H, o, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "value projection kernel");
+  return ok();
+}
+
+cp_status cp_mla_prefill_attn(const void* host_plan, const void* dev_plan, int rank, const void* q,
+                              const void* kv, const void* k_rope, int64_t rope_stride, int H, float sm_scale,
+                              void* o, float* lse, void* stream) {
+  cp_plan_header h;
+  cp_status st = read_header(host_plan, 0, &h);
+  if (st != CP_OK) return st;
+  if (rank < -1 || rank >= h.C) return fail(CP_ERR_INVALID_ARG, "rank=%d outside [-1, %d)", rank, h.C);
+  if (H < 1) return fail(CP_ERR_INVALID_ARG, "H=%d must be >= 1", H);
+  if (!(sm_scale > 0.f)) return fail(CP_ERR_INVALID_ARG, "sm_scale must be > 0");
+  const int32_t* W = (const int32_t*)host_plan;
+  const int n_rows = rank < 0 ? h.T : W[h.off_rank + rank + 1] - W[h.off_rank + rank];
+  if (n_rows == 0) return ok();
+  if (!dev_plan || !q || !kv || !k_rope || !o || !lse) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(dev_plan) || !aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o) ||
+      !aligned16(lse))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  if (rope_stride < 64 || rope_stride % 8 || rope_stride > kMaxRowStride)
+    return fail(CP_ERR_INVALID_ARG, "rope_stride=%lld: need a multiple of 8 from 64 on", (long long)rope_stride);
+  const cudaError_t e = launch_mla_prefill((const int32_t*)dev_plan, W, h, rank, q, kv, k_rope, rope_stride, H,
+                                           sm_scale, o, lse, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "latent prefill kernel");
+  return ok();
+}
+
+// ------------------------------------------------------------------ pages, slots, new tokens
+
+cp_status cp_page_slots(int C, int B, const int32_t* ctx_len, const int32_t* new_len, int32_t* page_table,
+                        int max_pages, int page_size, int num_pages, const int32_t* free_ids, int n_free,
+                        const int32_t* free_pos, int32_t* slots, int max_tokens, int32_t* cu_new,
+                        int32_t* info, void* stream) {
+  if (C < 1 || C > CP_MAX_SHARDS) return fail(CP_ERR_INVALID_ARG, "C=%d outside [1, %d]", C, CP_MAX_SHARDS);
+  if (B < 1 || B > CP_SLOTS_MAX_B) return fail(CP_ERR_INVALID_ARG, "B=%d outside [1, %d]", B, CP_SLOTS_MAX_B);
+  if (page_size < 64 || page_size % 64) return fail(CP_ERR_UNSUPPORTED, "page_size=%d is not a positive multiple of 64", page_size);
+  if (max_pages < 1 || num_pages < 1) return fail(CP_ERR_INVALID_ARG, "max_pages=%d, num_pages=%d must be >= 1", max_pages, num_pages);
+  if ((long long)num_pages * page_size > 0x7FFFFF00LL)
+    return fail(CP_ERR_UNSUPPORTED, "pool of %lld rows is too large", (long long)num_pages * page_size);
+  if (n_free < 0 || max_tokens < 0) return fail(CP_ERR_INVALID_ARG, "n_free=%d, max_tokens=%d must be >= 0", n_free, max_tokens);
+  if (!ctx_len || !new_len || !page_table || !free_pos || !cu_new || !info || (n_free && !free_ids) ||
+      (max_tokens && !slots))
+    return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (slots && !aligned16(slots)) return fail(CP_ERR_INVALID_ARG, "slots is not 16-byte aligned");
+  if (free_pos >= info && free_pos < info + 4)
+    return fail(CP_ERR_INVALID_ARG, "free_pos lies in this call's info: pass an earlier call's");
+  const PageSlotsArgs a = {C, B, ctx_len, new_len, page_table, max_pages, page_size, num_pages,
+                           free_ids, n_free, free_pos, slots, max_tokens, cu_new, info};
+  const cudaError_t e = launch_page_slots(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "page slots kernel");
+  return ok();
+}
+
+cp_status cp_cache_append(const int32_t* slots, int n, cp_dtype src_dtype, const void* k_new, int64_t k_stride,
+                          const void* v_new, int64_t v_stride, const float* new_scale, int row_elems,
+                          cp_dtype pool_dtype, void* k_pool, void* v_pool, float* scale_pool,
+                          int64_t pool_rows, void* stream) {
+  for (cp_dtype d : {src_dtype, pool_dtype})
+    if (d != CP_BF16 && d != CP_FP32 && d != CP_FP8_E4M3) return fail(CP_ERR_INVALID_ARG, "bad dtype");
+  if (src_dtype != pool_dtype && (pool_dtype != CP_FP8_E4M3 || src_dtype == CP_FP8_E4M3))
+    return fail(CP_ERR_UNSUPPORTED, "rows go into a pool of their own dtype, or bf16 / fp32 rows into E4M3");
+  if (n < 0 || pool_rows < 1 || pool_rows > 0x7FFFFF00LL)
+    return fail(CP_ERR_INVALID_ARG, "n=%d, pool_rows=%lld out of range", n, (long long)pool_rows);
+  if (row_elems < 16 || row_elems % 16) return fail(CP_ERR_UNSUPPORTED, "row_elems=%d is not a positive multiple of 16", row_elems);
+  if ((v_new == nullptr) != (v_pool == nullptr))
+    return fail(CP_ERR_INVALID_ARG, "v_new and v_pool must both be given or both NULL");
+  if ((pool_dtype == CP_FP8_E4M3) != (scale_pool != nullptr))
+    return fail(CP_ERR_INVALID_ARG, "scale_pool is required for an E4M3 pool and only for it");
+  if ((src_dtype == CP_FP8_E4M3) != (new_scale != nullptr))
+    return fail(CP_ERR_INVALID_ARG, "new_scale is required for E4M3 rows and only for them");
+  if (n == 0) return ok();
+  if (!slots || !k_new || !k_pool) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  const int64_t es = (int64_t)elem_size(src_dtype);
+  for (int64_t st : {k_stride, v_new ? v_stride : k_stride})
+    if (st < row_elems || st > kMaxRowStride || (st * es) % 16)
+      return fail(CP_ERR_INVALID_ARG, "row stride %lld: need >= row_elems=%d and a multiple of 16 bytes", (long long)st, row_elems);
+  if (!aligned16(k_new) || !aligned16(k_pool) || (v_new && (!aligned16(v_new) || !aligned16(v_pool))))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  const AppendArgs a = {slots, n, row_elems, k_new, v_new, (long long)k_stride, (long long)v_stride,
+                        k_pool, v_pool, new_scale, scale_pool, (long long)pool_rows};
+  const cudaError_t e = launch_cache_append(a, src_dtype, pool_dtype, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache append kernel");
+  return ok();
 }
 
 }  // extern "C"

@@ -29,7 +29,9 @@ enum KernelId : unsigned {
   kKernDecodeMlaFp8 = 3,
   kKernDecodeGqaTc = 4,
   kKernDecodeGqaF8 = 5,
-  kKernTf32 = 6
+  kKernTf32 = 6,
+  kKernMlaPrefill = 7,
+  kKernMlaProduct = 8
 };
 
 struct ShardPtrs {
@@ -191,6 +193,45 @@ cudaError_t launch_decode_simt(const int32_t* dev_plan, const cp_plan_header& h,
                                int Dv, float sm_scale, float* o_part, float* lse_part,
                                float* ws_o, float* ws_lse, const int32_t* pair_count,
                                cudaStream_t s);
+
+// ---- latent attention in its expanded form (mla_prefill_tc.cu) and the
+// per-head products with the up-projection (mla_product_tc.cu)
+cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan, const cp_plan_header& h,
+                               int rank, const void* q, const void* kv, const void* k_rope,
+                               long long rope_stride, int H, float sm_scale, void* o, float* lse,
+                               cudaStream_t s);
+cudaError_t launch_mla_expand(const void* latent, long long stride, const void* w, int T, int H, void* kv,
+                              cudaStream_t s);
+cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s);
+cudaError_t launch_mla_project(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s);
+
+// ---- pages, slots and new tokens of a paged cache (cache_kernels.cu)
+struct PageSlotsArgs {
+  int C, B;
+  const int32_t *ctx_len, *new_len;  // [B]
+  int32_t* table;                    // [C * B][max_pages]
+  int max_pages, page_size, num_pages;
+  const int32_t* free_ids;           // [n_free]
+  int n_free;
+  const int32_t* free_pos;           // [1]
+  int32_t* slots;                    // [max_tokens]
+  int max_tokens;
+  int32_t *cu_new, *info;            // [B + 1], [4]
+};
+cudaError_t launch_page_slots(const PageSlotsArgs& a, cudaStream_t s);
+struct AppendArgs {
+  const int32_t* slots;              // [n]
+  int n, row_elems;                  // row_elems of K, and of V where there is one
+  const void *k, *v;                 // new rows; v NULL for one row a token
+  long long k_stride, v_stride;      // elements
+  void *k_pool, *v_pool;
+  const float* new_scale;            // [n] with E4M3 rows
+  float* scale_pool;
+  long long pool_rows;
+};
+// src == pool: the rows as they are; bf16 or fp32 rows to an E4M3 pool: codes
+// and one scale a token.
+cudaError_t launch_cache_append(const AppendArgs& a, cp_dtype src, cp_dtype pool, cudaStream_t s);
 
 // ---- sparse decode: exact sharded top-k and the owners' gather (sparse_kernels.cu)
 // Decode kernels given a pair_count (device, one per (shard, request) pair)

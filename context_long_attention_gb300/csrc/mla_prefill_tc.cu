@@ -1,0 +1,510 @@
+// Causal prefill of multi-head latent attention in its expanded form, on the
+// tcgen05 tensor cores (bf16 in, fp32 accumulate).
+//
+// For a query at position p of its request and head h
+//   s_t = sm_scale (q_h[0:128] . k_nope_{t,h} + q_h[128:192] . k_rope_t), t = 0..p
+//   LSE = ln sum_t exp(s_t);  O_h = sum_t exp(s_t - LSE) v_{t,h}
+// k_nope and v are the two halves of a token's 256-wide row for the head (the
+// product of its latent vector with the up-projection, cp_mla_expand); the
+// 64 rotated key dims are one vector per token that all heads read ("How GPUs
+// Share a Long Context During LLM Inference" §1.2, §1.3: one 576-wide cache
+// entry, the latent part and the shared positional part).
+//
+// One CTA = one plan tile (up to 256 consecutive queries of one segment) x one
+// head, as two 128-row M tiles that share every K/V tile.
+//   warps 0-15  softmax: two warps per 32 rows of an M tile, each with half of
+//               a row's 128 scores and half of its 128 output dims
+//   warp 16     TMA producer; clears the last V tile's rows past the CTA's
+//               last key (another request's rows: a zero weight times a NaN
+//               there would be NaN)
+//   warp 17     MMA issuer and TMEM owner
+// TMEM (512 columns): tile t holds S_t in columns [256t, 256t + 128), O_t in
+// [256t + 128, 256t + 256); P (bf16 pairs) goes over the first 32 of a half's
+// 64 score columns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace cpattn {
+namespace {
+using namespace tc;
+
+constexpr int BM = 128;     // query rows per M tile
+constexpr int BN = 128;     // keys per K/V tile
+constexpr int kNope = 128;  // per-head key dims
+constexpr int kRope = 64;   // key dims shared by the heads
+constexpr int kDqk = kNope + kRope;
+constexpr int kDv = 128;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kWarpTma = kSoftmaxWarps;
+constexpr int kWarpMma = kSoftmaxWarps + 1;
+constexpr int kLaunchBoundThreads = 640;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.0f;      // move the running max when it grows by > 2^8
+constexpr float kSpecSum = 64.f * 256.f;  // a half row's P sum that may hide a P above 2^8
+
+constexpr int kQBytes = BM * kDqk * 2;
+constexpr int kKBytes = BN * kDqk * 2;
+constexpr int kVBytes = BN * kDv * 2;
+constexpr int kKSlots = 2;
+constexpr int kSmem = 2 * kQBytes + kKSlots * kKBytes + kVBytes + 1024;
+
+struct Params {
+  const int32_t* plan;
+  int off_seg;
+  int tile_list;
+  int n_tiles;
+  int row_sub;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  int H;
+  float sm_scale, scale_log2;
+  unsigned* status;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ void report_timeout(unsigned* status, unsigned site, volatile int* abort) {
+  *abort = 1;
+  if (atomicCAS(status, 0u, 1u) == 0u) {
+    status[1] = kKernMlaPrefill;
+    status[2] = site;
+    status[3] = blockIdx.x;
+    __threadfence();
+  }
+}
+
+__global__ void __launch_bounds__(kLaunchBoundThreads, 1)
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap kvmap,
+                       const __grid_constant__ CUtensorMap ropemap, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + 2 * kQBytes;
+  uint8_t* sV = sK + kKSlots * kKBytes;
+  // bar_k: K_j landed in slot j % 2; bar_krel: K_j read (the last S_j is
+  // complete, a softmax thread saw it); load j + 2 waits for release j, and
+  // release j + 2 needs load j + 2, so no phase completes unobserved.  V has
+  // one slot: V_j is loaded once the last P_(j-1) V_(j-1) is complete.
+  __shared__ __align__(8) uint64_t bar_k[kKSlots], bar_krel[kKSlots], bar_v, bar_tail;
+  __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2], bar_drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ volatile int zero_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x / p.n_tiles, tile_i = blockIdx.x - h * p.n_tiles;
+  const cp_tile_desc td = reinterpret_cast<const cp_tile_desc*>(p.plan + p.tile_list)[tile_i];
+  const cp_seg_desc sg = reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg)[td.seg];
+
+  const int rows0 = min(BM, max(0, sg.count - td.q_off));
+  const int rows1 = min(BM, max(0, sg.count - td.q_off - BM));
+  const int nkv0 = rows0 > 0 ? (sg.first_pos + (td.q_off + rows0 - 1) * sg.stride + BN) / BN : 0;
+  const int nkv1 = rows1 > 0 ? (sg.first_pos + (td.q_off + BM + rows1 - 1) * sg.stride + BN) / BN : 0;
+  const int nK = max(nkv0, nkv1);
+  const int last_t = nkv1 > 0 ? 1 : 0;  // the tile whose products come last in every step
+  const int n_keys = sg.first_pos + (td.q_off + rows0 + rows1 - 1) * sg.stride + 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKSlots; ++s) {
+      mbar_init(smem_u32(&bar_k[s]), 1);
+      mbar_init(smem_u32(&bar_krel[s]), 1);
+    }
+    mbar_init(smem_u32(&bar_v), 1);
+    mbar_init(smem_u32(&bar_tail), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&bar_q[t]), 2 * BM);
+      mbar_init(smem_u32(&bar_s[t]), 1);
+      mbar_init(smem_u32(&bar_p[t]), 2 * BM);
+      mbar_init(smem_u32(&bar_o[t]), 1);
+    }
+    mbar_init(smem_u32(&bar_drain), 1);
+    abort_flag = 0;
+    zero_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kWarpMma) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (warp == kWarpTma && lane == 0) {
+    prefetch_tmap(&kvmap);
+    prefetch_tmap(&ropemap);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------ softmax
+    const int quarter = warp & 3;
+    const int t = (warp >> 2) & 1;
+    const int half = warp >> 3;
+    const int i = quarter * 32 + lane;
+    const int pbar = 2 + t * 4 + quarter;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t colS = t * 256 + 64 * half, colO = t * 256 + 128 + (kDv / 2) * half;
+    const int rows_t = t ? rows1 : rows0;
+    const bool valid = i < rows_t;
+    const bool releaser = t == last_t && quarter == 0 && half == 0;
+    // value of the other half of this row, through column 63 of each half's
+    // scores (P never covers it, and the scores are in registers by then)
+    auto exchange = [&](float v) -> float {
+      tmem_st1(lane_addr + t * 256 + 64 * half + 63, __float_as_uint(v));
+      tmem_st_wait();
+      tc_fence_before();
+      named_bar_sync(pbar, 64);
+      tc_fence_after();
+      const uint32_t o = tmem_ld1(lane_addr + t * 256 + 64 * (half ^ 1) + 63);
+      tmem_ld_wait();
+      return __uint_as_float(o);
+    };
+    // Q row -> shared memory, 128-byte-swizzled K-major (half of its 24 pieces)
+    {
+      const long long f = (long long)sg.first_f + (long long)(td.q_off + t * BM + i) * sg.stride;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (f * p.H + h) * kDqk);
+      uint8_t* dst = sQ + t * kQBytes + i * 128;
+#pragma unroll
+      for (int c = half * (kDqk / 16); c < (half + 1) * (kDqk / 16); ++c) {
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (valid) val = __ldg(src + c);
+        const int a = c >> 3, cc = c & 7;
+        *reinterpret_cast<uint4*>(dst + a * (BM * 128) + ((cc ^ (i & 7)) << 4)) = val;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&bar_q[t]));
+    }
+    const int n_t = t ? nkv1 : nkv0;
+    if (n_t > 0) {
+      const int my_row = valid ? i : rows_t - 1;
+      const int pos = sg.first_pos + (td.q_off + t * BM + my_row) * sg.stride;
+      const float sl2 = p.scale_log2;
+      const float thr = kRescaleLog2 / sl2;
+      float m_used = -INFINITY, l = 0.f;
+      bool ok = true;
+      auto load_s = [&](int j, uint32_t (&sr)[64]) {
+        const int kbase = j * BN + 64 * half;
+        tmem_ld32(lane_addr + colS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(lane_addr + colS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_ld_wait();
+        if (kbase + 63 > pos) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (kbase + e > pos) sr[e] = __float_as_uint(-INFINITY);
+        }
+      };
+      auto exps = [&](const uint32_t (&sr)[64], uint32_t (&pk)[32]) -> float {
+        const float neg = -m_used * sl2;
+        float s0sum = 0.f, s1sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float s0 = __uint_as_float(sr[2 * e]), s1 = __uint_as_float(sr[2 * e + 1]);
+          float u0, u1;
+          fma2(u0, u1, s0, s1, sl2, sl2, neg, neg);
+          const float p0 = ex2(u0), p1 = ex2(u1);
+          add2(s0sum, s1sum, s0sum, s1sum, p0, p1);
+          pk[e] = pack_bf16x2(p0, p1);
+        }
+        return s0sum + s1sum;
+      };
+      for (int j = 0; j < n_t && ok; ++j) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_s[t]), j & 1, p.wait_ns,
+                                                           &abort_flag));
+        if (got && releaser && lane == 0) mbar_arrive(smem_u32(&bar_krel[j % kKSlots]));
+        tc_fence_after();
+        uint32_t sr[64], pk[32];
+        float part = 0.f;
+        bool slow = j == 0;
+        if (j > 0) {
+          // P with the running max as it stands; a half whose sum passes
+          // 64 x 2^8 may hold a P above 2^8 and sends the row down the exact
+          // path (NaN too).  The result is exact for any max in use.
+          load_s(j, sr);
+          part = exps(sr, pk);
+          slow = bar_red_or(pbar, 64, !got || !(part <= kSpecSum));
+        }
+        if (slow) {
+          if (bar_red_or(pbar, 64, !got)) {
+            if (!got) report_timeout(p.status, 1, &abort_flag);
+            ok = false;
+            break;
+          }
+          load_s(j, sr);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            mx = fmax3(mx, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+          const float mrow = fmaxf(mx, exchange(mx));
+          if (j == 0) {
+            m_used = mrow;
+          } else {
+            const bool need = mrow > m_used + thr;
+            const float alpha = need ? ex2((m_used - mrow) * sl2) : 1.f;
+            if (need) {
+              l *= alpha;
+              m_used = mrow;
+            }
+            const bool landed = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_o[t]), (j - 1) & 1,
+                                                                  p.wait_ns, &abort_flag));
+            if (bar_red_or(pbar, 64, !landed)) {
+              if (!landed) report_timeout(p.status, 2, &abort_flag);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kDv / 32; ++c) {
+              uint32_t r[16];
+              tmem_ld16(lane_addr + colO + c * 16, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              tmem_st16(lane_addr + colO + c * 16, r);
+            }
+          }
+          part = exps(sr, pk);
+        }
+        l += part;
+        tmem_st32(lane_addr + colS, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bar_p[t]));
+      }
+      const bool landed =
+          ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_o[t]), (n_t - 1) & 1, p.wait_ns,
+                                                  &abort_flag));
+      if (!bar_red_or(pbar, 64, !landed)) {
+        tc_fence_after();
+        const float lt = l + exchange(l);
+        const float inv = 1.f / lt;
+        const long long out_row =
+            (long long)sg.local_start + td.q_off + t * BM + i - p.row_sub;
+        __nv_bfloat16* dst = p.o + (out_row * p.H + h) * kDv + (kDv / 2) * half;
+#pragma unroll
+        for (int c = 0; c < kDv / 64; ++c) {
+          uint32_t r[32];
+          tmem_ld32(lane_addr + colO + c * 32, r);
+          tmem_ld_wait();
+          if (valid) {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+              uint4 w;
+              w.x = pack_bf16x2(__uint_as_float(r[8 * v4 + 0]) * inv, __uint_as_float(r[8 * v4 + 1]) * inv);
+              w.y = pack_bf16x2(__uint_as_float(r[8 * v4 + 2]) * inv, __uint_as_float(r[8 * v4 + 3]) * inv);
+              w.z = pack_bf16x2(__uint_as_float(r[8 * v4 + 4]) * inv, __uint_as_float(r[8 * v4 + 5]) * inv);
+              w.w = pack_bf16x2(__uint_as_float(r[8 * v4 + 6]) * inv, __uint_as_float(r[8 * v4 + 7]) * inv);
+              reinterpret_cast<uint4*>(dst + c * 32)[v4] = w;
+            }
+          }
+        }
+        if (valid && half == 0) p.lse[out_row * p.H + h] = m_used * p.sm_scale + logf(lt);
+      } else if (ok) {
+        report_timeout(p.status, 3, &abort_flag);
+      }
+    }
+  } else if (warp == kWarpTma) {
+    // ------------------------------------------------------------ TMA producer
+    int last_k = -1, last_v = -1;
+    bool ok = true;
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_ns, &abort_flag));
+    };
+    for (int j = 0; j <= nK && nK > 0 && ok; ++j) {
+      if (j < nK) {  // K_j
+        if (j >= kKSlots) ok = wait_all(smem_u32(&bar_krel[j % kKSlots]), (j / kKSlots - 1) & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t full = smem_u32(&bar_k[j % kKSlots]);
+          const uint32_t dst = smem_u32(sK + (j % kKSlots) * kKBytes);
+          const int row = sg.kv_base + j * BN;
+          mbar_expect_tx(full, kKBytes);
+          tma_load_3d(dst, &kvmap, 0, h, row, full);
+          tma_load_3d(dst + BN * 128, &kvmap, 64, h, row, full);
+          tma_load_2d(dst + 2 * BN * 128, &ropemap, 0, row, full);
+        }
+        __syncwarp();
+        last_k = j;
+      }
+      if (j > 0) {  // V_(j-1)
+        const int v = j - 1;
+        if (v > 0) ok = wait_all(smem_u32(&bar_o[last_t]), (v - 1) & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t full = smem_u32(&bar_v), dst = smem_u32(sV);
+          const int row = sg.kv_base + v * BN;
+          mbar_expect_tx(full, kVBytes);
+          tma_load_3d(dst, &kvmap, kNope, h, row, full);
+          tma_load_3d(dst + BN * 128, &kvmap, kNope + 64, h, row, full);
+        }
+        __syncwarp();
+        last_v = v;
+      }
+    }
+    if (ok && nK > 0) {  // the last V tile's rows past the last key
+      ok = wait_all(smem_u32(&bar_v), (nK - 1) & 1);
+      if (ok) {
+        for (int r = n_keys - (nK - 1) * BN + lane; r < BN; r += 32)
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(sV + (c >> 3) * (BN * 128) + r * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_tail));
+      }
+    }
+    if (!ok && lane == 0) report_timeout(p.status, 4, &abort_flag);
+    // Never leave with a copy in flight.
+    for (int k = max(0, last_k - kKSlots + 1); k <= last_k; ++k)
+      mbar_wait(smem_u32(&bar_k[k % kKSlots]), (k / kKSlots) & 1, 1000000000ull, &zero_flag);
+    if (last_v >= 0) mbar_wait(smem_u32(&bar_v), last_v & 1, 1000000000ull, &zero_flag);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t idS = idesc_bf16_f32(BM, BN, 0, 0);
+    const uint32_t idPV = idesc_bf16_f32(BM, kDv, 0, 1);
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_ns, &abort_flag));
+    };
+    const uint64_t dQ0 = smem_desc(smem_u32(sQ), 16, 1024);
+    const uint64_t dK0 = smem_desc(smem_u32(sK), 16, 1024);
+    const uint64_t dV0 = smem_desc(smem_u32(sV), BN * 128, 1024);
+    auto issue_s = [&](int t, int j) {
+      const uint64_t a0 = dQ0 + (uint64_t)((t * kQBytes) >> 4);
+      const uint64_t b0 = dK0 + (uint64_t)(((j % kKSlots) * kKBytes) >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kDqk / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + t * 256, a0 + off, b0 + off, idS, kk > 0);
+        }
+        mma_commit(smem_u32(&bar_s[t]));
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int t, bool acc) {
+      const uint32_t pa = tmem + t * 256, d = tmem + t * 256 + 128;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(d, pa + (kk >> 2) * 64 + (kk & 3) * 8, dV0 + (uint64_t)((kk * 16 * 128) >> 4),
+                 idPV, (acc || kk > 0) ? 1u : 0u);
+        mma_commit(smem_u32(&bar_o[t]));
+      }
+      __syncwarp();
+    };
+    unsigned bad = 0;
+    for (int t = 0; t < 2 && !bad; ++t)
+      if ((t ? nkv1 : nkv0) > 0 && !wait_all(smem_u32(&bar_q[t]), 0)) bad = 11;
+    if (!bad && nK > 0) {
+      if (!wait_all(smem_u32(&bar_k[0]), 0)) bad = 12;
+      tc_fence_after();
+      for (int t = 0; t < 2 && !bad; ++t)
+        if ((t ? nkv1 : nkv0) > 0) issue_s(t, 0);
+    }
+    for (int j = 0; j < nK && !bad; ++j) {
+      if (!wait_all(smem_u32(&bar_v), j & 1)) bad = 13;
+      if (!bad && j == nK - 1 && !wait_all(smem_u32(&bar_tail), 0)) bad = 16;
+      if (!bad && j + 1 < nK && !wait_all(smem_u32(&bar_k[(j + 1) % kKSlots]), ((j + 1) / kKSlots) & 1)) bad = 17;
+      for (int t = 0; t < 2 && !bad; ++t) {
+        const int nt = t ? nkv1 : nkv0;
+        if (j >= nt) continue;
+        if (!wait_all(smem_u32(&bar_p[t]), j & 1)) {
+          bad = 14 + t;
+          break;
+        }
+        tc_fence_after();
+        issue_pv(t, j > 0);
+        if (j + 1 < nt) issue_s(t, j + 1);
+      }
+    }
+    if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
+    // Never free TMEM under a running MMA: wait for everything issued.
+    if (elect_one()) mma_commit(smem_u32(&bar_drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan, const cp_plan_header& h,
+                               int rank, const void* q, const void* kv, const void* k_rope,
+                               long long rope_stride, int H, float sm_scale, void* o, float* lse,
+                               cudaStream_t s) {
+  Params p;
+  p.plan = dev_plan;
+  p.off_seg = h.off_seg;
+  if (rank < 0) {
+    p.tile_list = h.off_tiles;
+    p.n_tiles = h.n_tiles;
+    p.row_sub = 0;
+  } else {
+    const int32_t* rto = host_plan + h.off_rtile;
+    p.tile_list = h.off_rtile + h.C + 1 + 2 * rto[rank];
+    p.n_tiles = rto[rank + 1] - rto[rank];
+    p.row_sub = host_plan[h.off_rank + rank];
+  }
+  if (p.n_tiles == 0) return cudaSuccess;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.H = H;
+  p.sm_scale = sm_scale;
+  p.scale_log2 = sm_scale * kLog2e;
+  p.status = device_status_ptr();
+  if (!p.status) return cudaErrorInvalidDevice;
+  p.wait_ns = wait_limit_ns();
+  CUtensorMap kvm, rm;
+  {
+    const uint64_t dims[3] = {kNope + kDv, (uint64_t)H, (uint64_t)h.KV};
+    const uint64_t strides[2] = {(kNope + kDv) * 2, (uint64_t)H * (kNope + kDv) * 2};
+    const uint32_t box[3] = {64, 1, BN};
+    if (!encode_tensor_map_bf16(&kvm, kv, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[2] = {kRope, (uint64_t)h.KV};
+    const uint64_t strides[1] = {(uint64_t)rope_stride * 2};
+    const uint32_t box[2] = {64, BN};
+    if (!encode_tensor_map_bf16(&rm, k_rope, 2, dims, strides, box, false)) return cudaErrorInvalidValue;
+  }
+  cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)p.n_tiles * H;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  mla_prefill_kernel<<<(unsigned)blocks, kThreads, kSmem, s>>>(kvm, rm, p);
+  return cudaGetLastError();
+}
+
+}  // namespace cpattn

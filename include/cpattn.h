@@ -12,6 +12,10 @@
  *   cp_decode_attn     one decode query per request against each shard,
  *                      emitting per-shard partial (O, LSE)
  *   cp_lse_merge       exact log-sum-exp combine of partial results
+ *   cp_mla_*           latent attention around the MLA decode: the expanded
+ *                      form's prefill and the per-head products of both forms
+ *   cp_page_slots, cp_cache_append
+ *                      pages, slots and rows of a step's new tokens
  *
  * Sources (page title, section):
  *   [CTX] "How GPUs Share a Long Context During LLM Inference"
@@ -501,6 +505,119 @@ cp_status cp_decode_attn_paged(const void* host_plan, const void* dev_plan, cp_d
                                int max_pages, int page_size, int num_pages, int Hq, int Hkv,
                                int Dqk, int Dv, float sm_scale, float* o_part, float* lse_part,
                                void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Latent attention around the MLA decode ([CTX] §1.2, §1.3; [DCP] §5.3).
+ *
+ * A token's cache entry is one 576-wide vector for all heads: 512 latent
+ * dims c and 64 rotated key dims.  With the up-projection w_kv [H, 256, 512]
+ * (per head: 128 rows of the key part, then 128 rows of the value) head h has
+ *   k_nope = w_kv[h, 0:128] c,  v = w_kv[h, 128:256] c,
+ * and a query of 128 + 64 dims scores sm_scale (q_nope . k_nope + q_rope .
+ * k_rope).  Two forms of the same attention:
+ *   expanded (prompts): cp_mla_expand makes k_nope and v of every token and
+ *     cp_mla_prefill_attn attends over them;
+ *   absorbed (single tokens): cp_mla_absorb takes q_nope into the latent space
+ *     (q_nope . (W c) = (W^T q_nope) . c), cp_decode_attn (mode MLA) attends
+ *     over the cache entries as they are, and cp_mla_project takes its latent
+ *     output to the head's 128 value dims.
+ * All tensors bf16; sums in fp32, rounded once.  H >= 1.
+ *
+ * cp_mla_expand   latent [T, 512] with a row stride of latent_stride elements
+ *   (>= 512, a multiple of 8: 576 for the entries of a bf16 cache) ->
+ *   kv [T, H, 256] (128 key dims, then 128 value dims).
+ * cp_mla_absorb   q [N, H, 192] -> q_lat [N, H, 576]: 512 latent dims, then
+ *   q's last 64 (rotated) dims as they are.
+ * cp_mla_project  o_lat [N, H, 512] -> o [N, H, 128].
+ * T, N >= 0 (0: nothing is launched).  Outputs overlap no input.
+ * ------------------------------------------------------------------------- */
+cp_status cp_mla_expand(const void* latent, int64_t latent_stride, const void* w_kv, int T, int H, void* kv,
+                        void* stream);
+cp_status cp_mla_absorb(const void* q, const void* w_kv, int N, int H, void* q_lat, void* stream);
+cp_status cp_mla_project(const void* o_lat, const void* w_kv, int N, int H, void* o, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cp_mla_prefill_attn — cp_prefill_attn for latent attention in its expanded
+ * form: causal attention of every query a rank owns, over a zigzag or
+ * interleave plan of cp_shard_plan.
+ *
+ * q      [T, H, 192] bf16, flattened new-token order (128 dims, then 64 rotated)
+ * kv     [KV, H, 256] bf16, per request prefix rows then new-token rows
+ *        (cp_mla_expand's output)
+ * k_rope [KV, 64] bf16 with a row stride of rope_stride elements (>= 64, a
+ *        multiple of 8: the last 64 columns of the latent cache at stride 576)
+ * o      [rows, H, 128] bf16, lse [rows, H] fp32; rows and their order as in
+ *        cp_prefill_attn.
+ * A request's rows must be finite (a non-finite value row can reach the
+ * outputs of up to 255 queries of its segment before it); rows of other
+ * requests and past the last one are never mixed in.
+ * ------------------------------------------------------------------------- */
+cp_status cp_mla_prefill_attn(const void* host_plan, const void* dev_plan, int rank, const void* q,
+                              const void* kv, const void* k_rope, int64_t rope_stride, int H, float sm_scale,
+                              void* o, float* lse, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cp_page_slots — pages and slots of a step's new tokens, from lengths on the
+ * GPU ([CTX] §3.1: a slot is a shard and a row; [V4] §9.2: pages).
+ *
+ * Request b holds ctx_len[b] cached tokens and gets new_len[b] more (both
+ * [B] int32 device, >= 0).  Token p lives on shard p mod C at row p / C
+ * (CP_DCP_ROUND_ROBIN; contiguous chunks move when a request grows, so that
+ * layout has no append), and the rows of pair r * B + b in the pages of
+ * page_table [C * B][max_pages] (device, the table of cp_decode_attn_paged).
+ * Pages that the longer pair needs beyond those of ctx_len are taken from
+ * free_ids [n_free] (device) at position *free_pos on, in the order of
+ * requests, then shards, then pages, and written into the table; entries
+ * before them are read, all others stay as they are.
+ *   slots  [max_tokens] int32: the pool row of every new token, requests back
+ *          to back; -1 past the last one.  16-byte aligned.
+ *   cu_new [B + 1] int32: new tokens before request b.
+ *   info   [4] int32: {status, the next free_pos, pages taken, new tokens}.
+ * The lengths are known to the GPU only, so a step that does not fit is
+ * reported in info[0] as a sum of the flags below; nothing is taken then:
+ * the table stays, every slot is -1, cu_new is 0 and info[1] is *free_pos.
+ * A page id outside [0, num_pages) (in free_ids or the table) gives slots of
+ * -1 and, from free_ids, a table entry of -1.  The free list must name each
+ * page once.  free_pos may be info + 1 of an earlier call, not of this one.
+ * The call can be captured into a graph and replayed with new lengths.
+ * Errors: C outside [1, CP_MAX_SHARDS]; B outside [1, CP_SLOTS_MAX_B];
+ * page_size not a positive multiple of 64 (CP_ERR_UNSUPPORTED), max_pages,
+ * num_pages < 1, a pool of 2^31 rows or more; n_free, max_tokens < 0.
+ * ------------------------------------------------------------------------- */
+#define CP_SLOTS_MAX_B 8192
+enum {
+  CP_SLOTS_BAD_LENGTH = 1, /* a negative length, or a sum past 2^31 - 1 */
+  CP_SLOTS_TABLE_FULL = 2, /* a pair needs more than max_pages pages */
+  CP_SLOTS_NO_PAGES = 4,   /* the free list ends first, or free_pos is outside it */
+  CP_SLOTS_TOO_MANY = 8    /* more than max_tokens new tokens */
+};
+cp_status cp_page_slots(int C, int B, const int32_t* ctx_len, const int32_t* new_len, int32_t* page_table,
+                        int max_pages, int page_size, int num_pages, const int32_t* free_ids, int n_free,
+                        const int32_t* free_pos, int32_t* slots, int max_tokens, int32_t* cu_new,
+                        int32_t* info, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cp_cache_append — new tokens' rows into a paged pool (what
+ * cp_kv_shard_pack_paged does for a whole cache).
+ *
+ * Row i goes to pool row slots[i]; a slot outside [0, pool_rows) (the -1 of
+ * padding) is skipped.  Slots that are used must differ: two rows of one slot
+ * leave a mixture.  Rows of the pool that no slot names stay as they are.
+ * The decode reads whole tiles of a page, so a new pool must hold finite
+ * values (zeros) before its first use.
+ * k_new, v_new: [n, row_elems] of src_dtype with row strides in elements
+ *   (views of a larger projection output); v_new/v_pool NULL for an MLA cache.
+ * pool_dtype == src_dtype: rows are copied (with CP_FP8_E4M3 also their
+ *   scales new_scale [n] to scale_pool).
+ * src_dtype CP_BF16 or CP_FP32 into CP_FP8_E4M3: scale_pool[slot] = amax / 448
+ *   over the token's K and V row (1 for a row of zeros), code =
+ *   round-to-nearest-even(x / scale); new_scale NULL.  Rows must be finite.
+ * row_elems a multiple of 16; row bytes and strides in bytes multiples of 16.
+ * ------------------------------------------------------------------------- */
+cp_status cp_cache_append(const int32_t* slots, int n, cp_dtype src_dtype, const void* k_new, int64_t k_stride,
+                          const void* v_new, int64_t v_stride, const float* new_scale, int row_elems,
+                          cp_dtype pool_dtype, void* k_pool, void* v_pool, float* scale_pool,
+                          int64_t pool_rows, void* stream);
 
 /* ---------------------------------------------------------------------------
  * cp_lse_merge — exact combine of P partial results ([CTX] §3.3; [V4] §5).

@@ -551,3 +551,81 @@ def designated_partials(q: np.ndarray, kmain: np.ndarray, vmain: np.ndarray, kwi
         lses.append(lse)
     return np.stack(outs), np.stack(lses)
 
+
+# --------------------------------------------------------------------------
+# Latent attention's two forms and a paged cache's slots
+# --------------------------------------------------------------------------
+
+def mla_expand(latent: np.ndarray, w_kv: np.ndarray) -> np.ndarray:
+    """kv [T, H, 256] of latent rows [T, 512]: every head's 128 key and 128
+    value dims are its 256 rows of w_kv [H, 256, 512] times the row."""
+    return np.einsum("tc,hdc->thd", latent, w_kv, optimize=True)
+
+
+def mla_absorb(q: np.ndarray, w_kv: np.ndarray) -> np.ndarray:
+    """[N, H, 192] queries in the latent space: q_nope . (W c) = (W^T q_nope) . c,
+    the rotated dims unchanged."""
+    lat = np.einsum("nhd,hdc->nhc", q[..., :128], w_kv[:, :128], optimize=True)
+    return np.concatenate([lat, q[..., 128:]], axis=-1)
+
+
+def mla_project(o_lat: np.ndarray, w_kv: np.ndarray) -> np.ndarray:
+    """Latent outputs [N, H, 512] to the heads' 128 value dims."""
+    return np.einsum("nhc,hdc->nhd", o_lat, w_kv[:, 128:], optimize=True)
+
+
+def mla_expanded_qkv(kv: np.ndarray, k_rope: np.ndarray):
+    """(K [KV, H, 192], V [KV, H, 128]) of the expanded form: each head's own
+    128 key dims beside the 64 rotated dims that all heads share."""
+    H = kv.shape[1]
+    rope = np.repeat(k_rope[:, None, :], H, axis=1)
+    return np.concatenate([kv[..., :128], rope], axis=-1), kv[..., 128:]
+
+
+def page_slots(C: int, ctx_len, new_len, table, page_size: int, num_pages: int, free_ids, free_pos: int,
+               max_tokens: int):
+    """Pages and slots of a step, token by token: token p of request b goes
+    to shard p mod C, row p // C; a row on a page that its pair does not hold
+    yet takes the next free page, in the order of requests, shards, pages.
+    Returns (slots, cu_new, info, table), or the unchanged table with slots
+    of -1 and the reasons' sum in info[0]: 1 a bad length, 2 more pages than
+    the table holds, 4 too few free pages, 8 too many tokens."""
+    table = np.array(table, dtype=np.int64)
+    B, max_pages = len(ctx_len), table.shape[1]
+
+    def pages(L, r):
+        rows = len(range(r, L, C))
+        return -(-rows // page_size)
+
+    why = 0
+    if any(L < 0 or n < 0 or L + n > 2**31 - 1 for L, n in zip(ctx_len, new_len)):
+        why |= 1
+    good = [(b, L, n) for b, (L, n) in enumerate(zip(ctx_len, new_len)) if L >= 0 and n >= 0 and L + n <= 2**31 - 1]
+    if any(pages(L + n, 0) > max_pages for _, L, n in good):
+        why |= 2
+    need = sum(pages(L + n, r) - pages(L, r) for _, L, n in good for r in range(C))
+    if not 0 <= free_pos <= len(free_ids) or need > len(free_ids) - free_pos:
+        why |= 4
+    total = sum(n for _, _, n in good)
+    if total > max_tokens:
+        why |= 8
+    slots = np.full(max_tokens, -1, dtype=np.int64)
+    if why:
+        return slots, np.zeros(B + 1, np.int64), np.array([why, free_pos, 0, 0]), table
+    pos = free_pos
+    for b, L, n in good:
+        for r in range(C):
+            for i in range(pages(L, r), pages(L + n, r)):
+                page = int(free_ids[pos])
+                table[r * B + b, i] = page if 0 <= page < num_pages else -1
+                pos += 1
+    t = 0
+    for b, L, n in good:
+        for p in range(L, L + n):
+            r, row = p % C, p // C
+            page = int(table[r * B + b, row // page_size])
+            if 0 <= page < num_pages:
+                slots[t] = page * page_size + row % page_size
+            t += 1
+    cu = np.concatenate([[0], np.cumsum(new_len)])
+    return slots, cu, np.array([0, pos, pos - free_pos, total]), table

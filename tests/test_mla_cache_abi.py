@@ -1,0 +1,146 @@
+"""Refusals of the latent-attention and cache-append entry points: every bad
+argument is answered before a launch (no GPU needed), with a message."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+
+@pytest.fixture(scope="module")
+def cp():
+    import __graft_entry__
+    __graft_entry__.ensure_built()
+    import context_long_attention_gb300 as cp
+    return cp
+
+
+P = ctypes.c_void_p(256)  # never dereferenced: every case is answered before a launch
+ODD = ctypes.c_void_p(264)
+INVALID, UNSUPPORTED = -1, -2
+
+
+def refuse(lib, status, words, got):
+    assert got == status and words in lib.cp_last_error(), (got, lib.cp_last_error())
+
+
+def test_products(cp):
+    lib = cp.lib
+    refuse(lib, INVALID, b"H >= 1", lib.cp_mla_expand(P, 512, P, 4, 0, P, None))
+    refuse(lib, INVALID, b"T >= 0", lib.cp_mla_expand(P, 512, P, -1, 2, P, None))
+    for stride in (504, 516, 0, -512, 1 << 40):
+        refuse(lib, INVALID, b"latent_stride", lib.cp_mla_expand(P, stride, P, 4, 2, P, None))
+    refuse(lib, INVALID, b"NULL", lib.cp_mla_expand(None, 512, P, 4, 2, P, None))
+    refuse(lib, INVALID, b"aligned", lib.cp_mla_expand(P, 512, ODD, 4, 2, P, None))
+    for fn in (lib.cp_mla_absorb, lib.cp_mla_project):
+        refuse(lib, INVALID, b"N >= 0", fn(P, P, -1, 2, P, None))
+        refuse(lib, INVALID, b"H >= 1", fn(P, P, 1, 0, P, None))
+        refuse(lib, INVALID, b"NULL", fn(P, P, 1, 2, None, None))
+        refuse(lib, INVALID, b"aligned", fn(ODD, P, 1, 2, P, None))
+        assert fn(None, None, 0, 2, None, None) == 0
+    assert lib.cp_mla_expand(None, 0, None, 0, 2, None, None) == 0
+
+
+def test_prefill(cp):
+    lib = cp.lib
+    plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [5], [3], device=None)
+    h = plan.host.ctypes.data_as(ctypes.c_void_p)
+
+    def call(host=h, dev=P, rank=-1, q=P, rope=P, stride=576, H=2, scale=0.1, lse=P):
+        return lib.cp_mla_prefill_attn(host, dev, rank, q, P, rope, stride, H, scale, P, lse, None)
+
+    refuse(lib, INVALID, b"host_plan is NULL", call(host=None))
+    bogus = np.zeros(64, np.int32)
+    refuse(lib, INVALID, b"magic", call(host=bogus.ctypes.data_as(ctypes.c_void_p)))
+    decode = cp.cp_decode_plan(2, [5], n_workers=2)
+    refuse(lib, INVALID, b"expected a prefill plan", call(host=decode.host.ctypes.data_as(ctypes.c_void_p)))
+    for rank in (-2, 2):
+        refuse(lib, INVALID, b"rank", call(rank=rank))
+    refuse(lib, INVALID, b"H=0", call(H=0))
+    for scale in (0.0, -1.0, float("nan")):
+        refuse(lib, INVALID, b"sm_scale", call(scale=scale))
+    refuse(lib, INVALID, b"NULL", call(dev=None))
+    refuse(lib, INVALID, b"NULL", call(lse=None))
+    refuse(lib, INVALID, b"aligned", call(rope=ODD))
+    for stride in (56, 68, -64, 1 << 40):
+        refuse(lib, INVALID, b"rope_stride", call(stride=stride))
+    empty = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [0], [3], device=None)
+    assert call(host=empty.host.ctypes.data_as(ctypes.c_void_p), dev=None, q=None) == 0  # no query: nothing to do
+
+
+def test_page_slots(cp):
+    lib = cp.lib
+    pos, info = ctypes.c_void_p(512), ctypes.c_void_p(1024)
+
+    def call(C=2, B=3, ctx=P, max_pages=4, page=64, num=10, free=P, n_free=5, pos=pos, slots=P, most=8, info=info):
+        return lib.cp_page_slots(C, B, ctx, P, P, max_pages, page, num, free, n_free, pos, slots, most, P, info, None)
+
+    for C in (0, 65, -1):
+        refuse(lib, INVALID, b"C=", call(C=C))
+    for B in (0, -1, 8193):
+        refuse(lib, INVALID, b"B=", call(B=B))
+    for page in (0, 32, 96, -64):
+        refuse(lib, UNSUPPORTED, b"multiple of 64", call(page=page))
+    refuse(lib, INVALID, b"max_pages", call(max_pages=0))
+    refuse(lib, INVALID, b"num_pages", call(num=0))
+    refuse(lib, UNSUPPORTED, b"too large", call(num=1 << 25))
+    refuse(lib, INVALID, b"n_free", call(n_free=-1))
+    refuse(lib, INVALID, b"max_tokens", call(most=-1))
+    refuse(lib, INVALID, b"NULL", call(ctx=None))
+    refuse(lib, INVALID, b"NULL", call(free=None))
+    refuse(lib, INVALID, b"NULL", call(slots=None))
+    refuse(lib, INVALID, b"aligned", call(slots=ODD))
+    for k in range(4):
+        refuse(lib, INVALID, b"earlier call", call(pos=ctypes.c_void_p(1024 + 4 * k)))
+
+
+def test_cache_append(cp):
+    lib = cp.lib
+    BF16, FP32, FP8 = cp.CP_BF16, cp.CP_FP32, cp.CP_FP8_E4M3
+
+    def call(slots=P, n=4, src=BF16, k=P, ks=576, v=None, vs=0, ns=None, row=576, pool=BF16, kp=P, vp=None, sp=None, rows=64):
+        return lib.cp_cache_append(slots, n, src, k, ks, v, vs, ns, row, pool, kp, vp, sp, rows, None)
+
+    refuse(lib, INVALID, b"bad dtype", call(src=7))
+    for src, pool, sp in ((BF16, FP32, None), (FP32, BF16, None), (FP8, BF16, None)):
+        refuse(lib, UNSUPPORTED, b"own dtype", call(src=src, pool=pool, sp=sp))
+    for row in (0, 8, 24, -16):
+        refuse(lib, UNSUPPORTED, b"row_elems", call(row=row))
+    refuse(lib, INVALID, b"n=-1", call(n=-1))
+    for rows in (0, 1 << 31):
+        refuse(lib, INVALID, b"pool_rows", call(rows=rows))
+    refuse(lib, INVALID, b"v_new and v_pool", call(v=P))
+    refuse(lib, INVALID, b"v_new and v_pool", call(vp=P))
+    refuse(lib, INVALID, b"scale_pool", call(pool=FP8))
+    refuse(lib, INVALID, b"scale_pool", call(sp=P))
+    refuse(lib, INVALID, b"new_scale", call(src=FP8, pool=FP8, sp=P))
+    refuse(lib, INVALID, b"new_scale", call(ns=P))
+    for ks in (568, 580, 0, -576):
+        refuse(lib, INVALID, b"row stride", call(ks=ks))
+    refuse(lib, INVALID, b"row stride", call(v=P, vp=P, vs=8))
+    refuse(lib, INVALID, b"NULL", call(k=None))
+    refuse(lib, INVALID, b"aligned", call(kp=ODD))
+    refuse(lib, INVALID, b"aligned", call(v=ODD, vp=P, vs=576))
+    assert call(n=0, slots=None, k=None, kp=None) == 0
+
+
+def test_binding_checks(cp):
+    """The binding answers host tensors, wrong dtypes and shapes itself."""
+    import torch
+    w = torch.zeros(2, 256, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        cp.cp_mla_expand(torch.zeros(3, 512, dtype=torch.bfloat16), w)
+    with pytest.raises(TypeError, match="latent"):
+        cp.cp_mla_expand(torch.zeros(3, 512), w)
+    with pytest.raises(ValueError, match="CUDA"):
+        cp.cp_mla_absorb(torch.zeros(3, 2, 192, dtype=torch.bfloat16), w)
+    with pytest.raises(TypeError, match="w_kv"):
+        cp.cp_mla_project(torch.zeros(3, 2, 512, dtype=torch.bfloat16), w.float())
+    pages = cp.PageTable(np.zeros((4, 2)), 64, 8)
+    i32 = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device copy"):
+        cp.cp_page_slots(pages, 2, i32, i32, i32, i32[:1], 4)
+    with pytest.raises(ValueError, match="int32 CUDA"):
+        cp.PageTable.on_device(torch.zeros(4, 2, dtype=torch.int32), 64, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        cp.cp_cache_append(i32, torch.zeros(2, 576), torch.zeros(64, 576))
