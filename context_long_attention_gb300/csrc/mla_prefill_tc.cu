@@ -10,14 +10,22 @@
 // Share a Long Context During LLM Inference" §1.2, §1.3: one 576-wide cache
 // entry, the latent part and the shared positional part).
 //
-// One CTA = one plan tile (up to 256 consecutive queries of one segment) x one
-// head, as two 128-row M tiles that share every K/V tile.
+// The work of one CTA, or of a pair of CTAs, is up to 256 (512) consecutive
+// queries of one segment for one head, as two M tiles of 128 (256) rows that
+// share every K/V tile of 128 keys; CTA c of a pair has rows 128 c ..
+// 128 c + 127 of each M tile, half of each K tile's keys and half of each V
+// tile's dims.  The products of a pair are issued by its even CTA
+// (cta_group::2).
 //   warps 0-15  softmax: two warps per 32 rows of an M tile, each with half of
 //               a row's 128 scores and half of its 128 output dims
-//   warp 16     TMA producer; clears the last V tile's rows past the CTA's
-//               last key (another request's rows: a zero weight times a NaN
-//               there would be NaN)
-//   warp 17     MMA issuer and TMEM owner
+//   warp 16     TMA producer
+//   warp 17     MMA issuer (of a pair: the even CTA's) and TMEM owner
+//   warp 18     relay: adds an arrival to the P barrier of a step once the
+//               step's K/V tiles have landed in this CTA, so that the issuer's
+//               one wait covers them (a wait costs the issuing thread ~140 clk
+//               while the tensor pipe runs dry); clears the last V tile's rows
+//               past the last key (another request's rows: a zero weight
+//               times a NaN there would be NaN)
 // TMEM (512 columns): tile t holds S_t in columns [256t, 256t + 128), O_t in
 // [256t + 128, 256t + 256); P (bf16 pairs) goes over the first 32 of a half's
 // 64 score columns.
@@ -26,32 +34,44 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
-#include "tc_ptx.cuh"
+#include "tc_pair.cuh"
 
 namespace cpattn {
 namespace {
 using namespace tc;
 
-constexpr int BM = 128;     // query rows per M tile
+constexpr int BM = 128;     // query rows of an M tile in one CTA
 constexpr int BN = 128;     // keys per K/V tile
 constexpr int kNope = 128;  // per-head key dims
 constexpr int kRope = 64;   // key dims shared by the heads
 constexpr int kDqk = kNope + kRope;
 constexpr int kDv = 128;
 constexpr int kSoftmaxWarps = 16;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
 constexpr int kWarpTma = kSoftmaxWarps;
 constexpr int kWarpMma = kSoftmaxWarps + 1;
+constexpr int kWarpRelay = kSoftmaxWarps + 2;
 constexpr int kLaunchBoundThreads = 640;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;      // move the running max when it grows by > 2^8
 constexpr float kSpecSum = 64.f * 256.f;  // a half row's P sum that may hide a P above 2^8
 
 constexpr int kQBytes = BM * kDqk * 2;
-constexpr int kKBytes = BN * kDqk * 2;
-constexpr int kVBytes = BN * kDv * 2;
-constexpr int kKSlots = 2;
-constexpr int kSmem = 2 * kQBytes + kKSlots * kKBytes + kVBytes + 1024;
+constexpr long long kTileMajorBytes = 64ll << 20;  // keys and values that the L2 holds with room to spare
+
+template <bool PAIR>
+struct Cfg {
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kRows = BM * kCtas;                 // rows of an M tile
+  static constexpr int kKeys = BN / kCtas;                 // keys of a K tile in one CTA
+  static constexpr int kDims = kDv / kCtas;                // dims of a V tile in one CTA
+  static constexpr int kKBytes = kKeys * kDqk * 2;
+  static constexpr int kVBytes = BN * kDims * 2;
+  // a pair's halves fit three times beside Q, whole tiles twice (K) and once (V)
+  static constexpr int kKSlots = PAIR ? 3 : 2;
+  static constexpr int kVSlots = PAIR ? 3 : 1;
+  static constexpr int kSmem = 2 * kQBytes + kKSlots * kKBytes + kVSlots * kVBytes + 1024;
+};
 
 struct Params {
   const int32_t* plan;
@@ -63,6 +83,7 @@ struct Params {
   __nv_bfloat16* o;
   float* lse;
   int H;
+  int head_major;  // units head by head, else tile by tile (every head of the longest tiles first)
   float sm_scale, scale_log2;
   unsigned* status;
   unsigned long long wait_ns;
@@ -102,49 +123,62 @@ __device__ void report_timeout(unsigned* status, unsigned site, volatile int* ab
   }
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
-    mla_prefill_kernel(const __grid_constant__ CUtensorMap kvmap,
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ CUtensorMap ropemap, const Params p) {
+  using C = Cfg<PAIR>;
+  constexpr int KS = C::kKSlots, VS = C::kVSlots, MT = C::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + 2 * kQBytes;
-  uint8_t* sV = sK + kKSlots * kKBytes;
-  // bar_k: K_j landed in slot j % 2; bar_krel: K_j read (the last S_j is
-  // complete, a softmax thread saw it); load j + 2 waits for release j, and
-  // release j + 2 needs load j + 2, so no phase completes unobserved.  V has
-  // one slot: V_j is loaded once the last P_(j-1) V_(j-1) is complete.
-  __shared__ __align__(8) uint64_t bar_k[kKSlots], bar_krel[kKSlots], bar_v, bar_tail;
+  uint8_t* sV = sK + KS * C::kKBytes;
+  // bar_k, bar_v: this CTA's part of K_j (V_j) has landed; only the relay warp
+  // waits for them, tile after tile.  bar_rel[j % KS]: a softmax thread saw
+  // S_j of the step's last tile complete, so K_j and V_(j-1) are read (products
+  // complete in order).  K_(j+KS) is loaded after release j, and release j + KS
+  // needs that load, so no phase of bar_rel completes unobserved; nor one of
+  // bar_k or bar_v, since S_j needs P_(j-1), which the relay completes after
+  // it has waited for K_j and V_(j-1).
+  // bar_q, bar_k0, bar_p are waited for by the issuer and live in its CTA;
+  // warps arrive there from both CTAs.
+  __shared__ __align__(8) uint64_t bar_k[KS], bar_v[VS], bar_rel[KS], bar_k0;
   __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2], bar_drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int zero_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x / p.n_tiles, tile_i = blockIdx.x - h * p.n_tiles;
+  const int cta = PAIR ? (int)cluster_ctarank() : 0;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int h = p.head_major ? unit / p.n_tiles : unit % p.H;
+  const int tile_i = p.head_major ? unit - h * p.n_tiles : unit / p.H;
   const cp_tile_desc td = reinterpret_cast<const cp_tile_desc*>(p.plan + p.tile_list)[tile_i];
+  // a pair takes two plan tiles, from every even one of a segment
+  if (PAIR && (td.q_off & (2 * MT - 1))) return;
   const cp_seg_desc sg = reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg)[td.seg];
 
-  const int rows0 = min(BM, max(0, sg.count - td.q_off));
-  const int rows1 = min(BM, max(0, sg.count - td.q_off - BM));
+  const int rows0 = min(MT, max(0, sg.count - td.q_off));
+  const int rows1 = min(MT, max(0, sg.count - td.q_off - MT));
   const int nkv0 = rows0 > 0 ? (sg.first_pos + (td.q_off + rows0 - 1) * sg.stride + BN) / BN : 0;
-  const int nkv1 = rows1 > 0 ? (sg.first_pos + (td.q_off + BM + rows1 - 1) * sg.stride + BN) / BN : 0;
+  const int nkv1 = rows1 > 0 ? (sg.first_pos + (td.q_off + MT + rows1 - 1) * sg.stride + BN) / BN : 0;
   const int nK = max(nkv0, nkv1);
   const int last_t = nkv1 > 0 ? 1 : 0;  // the tile whose products come last in every step
   const int n_keys = sg.first_pos + (td.q_off + rows0 + rows1 - 1) * sg.stride + 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kKSlots; ++s) {
+    for (int s = 0; s < KS; ++s) {
       mbar_init(smem_u32(&bar_k[s]), 1);
-      mbar_init(smem_u32(&bar_krel[s]), 1);
+      mbar_init(smem_u32(&bar_rel[s]), 1);
     }
-    mbar_init(smem_u32(&bar_v), 1);
-    mbar_init(smem_u32(&bar_tail), 1);
+    for (int s = 0; s < VS; ++s) mbar_init(smem_u32(&bar_v[s]), 1);
+    mbar_init(smem_u32(&bar_k0), C::kCtas);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&bar_q[t]), 2 * BM);
+      mbar_init(smem_u32(&bar_q[t]), 8 * C::kCtas);        // a tile's eight softmax warps
+      mbar_init(smem_u32(&bar_p[t]), (8 + 1) * C::kCtas);  // and the relay
       mbar_init(smem_u32(&bar_s[t]), 1);
-      mbar_init(smem_u32(&bar_p[t]), 2 * BM);
       mbar_init(smem_u32(&bar_o[t]), 1);
     }
     mbar_init(smem_u32(&bar_drain), 1);
@@ -152,27 +186,45 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     zero_flag = 0;
     mbar_init_fence();
   }
-  if (warp == kWarpMma) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (warp == kWarpMma) {
+    if constexpr (PAIR) tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+    else tmem_alloc(smem_u32(&tmem_slot), 512);
+  }
   if (warp == kWarpTma && lane == 0) {
-    prefetch_tmap(&kvmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
     prefetch_tmap(&ropemap);
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+
+  // One arrival of a whole warp at a barrier of the issuer's CTA.
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (PAIR) mbar_arrive_cluster(map_to_rank(smem_u32(bar), 0));
+      else mbar_arrive(smem_u32(bar));
+    }
+  };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag)) != 0;
+  };
 
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax
     const int quarter = warp & 3;
     const int t = (warp >> 2) & 1;
     const int half = warp >> 3;
-    const int i = quarter * 32 + lane;
+    const int i = quarter * 32 + lane;  // row within the CTA's part of the M tile = TMEM lane
+    const int row = cta * BM + i;       // row within the M tile
     const int pbar = 2 + t * 4 + quarter;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t colS = t * 256 + 64 * half, colO = t * 256 + 128 + (kDv / 2) * half;
     const int rows_t = t ? rows1 : rows0;
-    const bool valid = i < rows_t;
+    const bool valid = row < rows_t;
     const bool releaser = t == last_t && quarter == 0 && half == 0;
     // value of the other half of this row, through column 63 of each half's
     // scores (P never covers it, and the scores are in registers by then)
@@ -188,7 +240,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     };
     // Q row -> shared memory, 128-byte-swizzled K-major (half of its 24 pieces)
     {
-      const long long f = (long long)sg.first_f + (long long)(td.q_off + t * BM + i) * sg.stride;
+      const long long f = (long long)sg.first_f + (long long)(td.q_off + t * MT + row) * sg.stride;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + (f * p.H + h) * kDqk);
       uint8_t* dst = sQ + t * kQBytes + i * 128;
 #pragma unroll
@@ -199,12 +251,12 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         *reinterpret_cast<uint4*>(dst + a * (BM * 128) + ((cc ^ (i & 7)) << 4)) = val;
       }
       fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&bar_q[t]));
+      warp_arrive(&bar_q[t]);
     }
     const int n_t = t ? nkv1 : nkv0;
     if (n_t > 0) {
-      const int my_row = valid ? i : rows_t - 1;
-      const int pos = sg.first_pos + (td.q_off + t * BM + my_row) * sg.stride;
+      const int my_row = min(row, rows_t - 1);  // rows past the segment run along with its last one's mask
+      const int pos = sg.first_pos + (td.q_off + t * MT + my_row) * sg.stride;
       const float sl2 = p.scale_log2;
       const float thr = kRescaleLog2 / sl2;
       float m_used = -INFINITY, l = 0.f;
@@ -235,9 +287,8 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         return s0sum + s1sum;
       };
       for (int j = 0; j < n_t && ok; ++j) {
-        const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_s[t]), j & 1, p.wait_ns,
-                                                           &abort_flag));
-        if (got && releaser && lane == 0) mbar_arrive(smem_u32(&bar_krel[j % kKSlots]));
+        const bool got = wait_all(&bar_s[t], j & 1);
+        if (got && releaser && lane == 0) mbar_arrive(smem_u32(&bar_rel[j % KS]));
         tc_fence_after();
         uint32_t sr[64], pk[32];
         float part = 0.f;
@@ -271,8 +322,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
               l *= alpha;
               m_used = mrow;
             }
-            const bool landed = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_o[t]), (j - 1) & 1,
-                                                                  p.wait_ns, &abort_flag));
+            const bool landed = wait_all(&bar_o[t], (j - 1) & 1);
             if (bar_red_or(pbar, 64, !landed)) {
               if (!landed) report_timeout(p.status, 2, &abort_flag);
               ok = false;
@@ -295,17 +345,14 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         tmem_st32(lane_addr + colS, pk);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&bar_p[t]));
+        warp_arrive(&bar_p[t]);
       }
-      const bool landed =
-          ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_o[t]), (n_t - 1) & 1, p.wait_ns,
-                                                  &abort_flag));
+      const bool landed = ok && wait_all(&bar_o[t], (n_t - 1) & 1);
       if (!bar_red_or(pbar, 64, !landed)) {
         tc_fence_after();
         const float lt = l + exchange(l);
         const float inv = 1.f / lt;
-        const long long out_row =
-            (long long)sg.local_start + td.q_off + t * BM + i - p.row_sub;
+        const long long out_row = (long long)sg.local_start + td.q_off + t * MT + row - p.row_sub;
         __nv_bfloat16* dst = p.o + (out_row * p.H + h) * kDv + (kDv / 2) * half;
 #pragma unroll
         for (int c = 0; c < kDv / 64; ++c) {
@@ -333,128 +380,195 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     // ------------------------------------------------------------ TMA producer
     int last_k = -1, last_v = -1;
     bool ok = true;
-    auto wait_all = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_ns, &abort_flag));
-    };
     for (int j = 0; j <= nK && nK > 0 && ok; ++j) {
       if (j < nK) {  // K_j
-        if (j >= kKSlots) ok = wait_all(smem_u32(&bar_krel[j % kKSlots]), (j / kKSlots - 1) & 1);
+        if (j >= KS) ok = wait_all(&bar_rel[j % KS], (j / KS - 1) & 1);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t full = smem_u32(&bar_k[j % kKSlots]);
-          const uint32_t dst = smem_u32(sK + (j % kKSlots) * kKBytes);
-          const int row = sg.kv_base + j * BN;
-          mbar_expect_tx(full, kKBytes);
-          tma_load_3d(dst, &kvmap, 0, h, row, full);
-          tma_load_3d(dst + BN * 128, &kvmap, 64, h, row, full);
-          tma_load_2d(dst + 2 * BN * 128, &ropemap, 0, row, full);
+          const uint32_t full = smem_u32(&bar_k[j % KS]);
+          const uint32_t dst = smem_u32(sK + (j % KS) * C::kKBytes);
+          const int row = sg.kv_base + j * BN + cta * C::kKeys;
+          mbar_expect_tx(full, C::kKBytes);
+          tma_load_3d(dst, &kmap, 0, h, row, full);
+          tma_load_3d(dst + C::kKeys * 128, &kmap, 64, h, row, full);
+          tma_load_2d(dst + 2 * C::kKeys * 128, &ropemap, 0, row, full);
         }
         __syncwarp();
         last_k = j;
       }
       if (j > 0) {  // V_(j-1)
         const int v = j - 1;
-        if (v > 0) ok = wait_all(smem_u32(&bar_o[last_t]), (v - 1) & 1);
+        if constexpr (PAIR) {
+          // its slot held V_(v-3), which release v - 2 frees; K_j has waited
+          // for that one (j - KS), the last V, without a K beside it, does here
+          if (j == nK && v >= VS) ok = wait_all(&bar_rel[j % KS], (j / KS - 1) & 1);
+        } else {
+          // one slot: the last product of step v - 1 (the next phase needs V_v)
+          if (v > 0) ok = wait_all(&bar_o[last_t], (v - 1) & 1);
+        }
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t full = smem_u32(&bar_v), dst = smem_u32(sV);
+          const uint32_t full = smem_u32(&bar_v[v % VS]), dst = smem_u32(sV + (v % VS) * C::kVBytes);
           const int row = sg.kv_base + v * BN;
-          mbar_expect_tx(full, kVBytes);
-          tma_load_3d(dst, &kvmap, kNope, h, row, full);
-          tma_load_3d(dst + BN * 128, &kvmap, kNope + 64, h, row, full);
+          mbar_expect_tx(full, C::kVBytes);
+#pragma unroll
+          for (int c = 0; c < C::kDims / 64; ++c)
+            tma_load_3d(dst + c * BN * 128, &vmap, kNope + cta * C::kDims + c * 64, h, row, full);
         }
         __syncwarp();
         last_v = v;
       }
     }
-    if (ok && nK > 0) {  // the last V tile's rows past the last key
-      ok = wait_all(smem_u32(&bar_v), (nK - 1) & 1);
-      if (ok) {
-        for (int r = n_keys - (nK - 1) * BN + lane; r < BN; r += 32)
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(sV + (c >> 3) * (BN * 128) + r * 128 + (c & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bar_tail));
-      }
-    }
     if (!ok && lane == 0) report_timeout(p.status, 4, &abort_flag);
     // Never leave with a copy in flight.
-    for (int k = max(0, last_k - kKSlots + 1); k <= last_k; ++k)
-      mbar_wait(smem_u32(&bar_k[k % kKSlots]), (k / kKSlots) & 1, 1000000000ull, &zero_flag);
-    if (last_v >= 0) mbar_wait(smem_u32(&bar_v), last_v & 1, 1000000000ull, &zero_flag);
+    for (int k = max(0, last_k - KS + 1); k <= last_k; ++k)
+      mbar_wait(smem_u32(&bar_k[k % KS]), (k / KS) & 1, 1000000000ull, &zero_flag);
+    for (int k = max(0, last_v - VS + 1); k <= last_v; ++k)
+      mbar_wait(smem_u32(&bar_v[k % VS]), (k / VS) & 1, 1000000000ull, &zero_flag);
     __syncwarp();
-  } else {
+  } else if (warp == kWarpRelay) {
+    // ------------------------------------------------------------ relay
+    bool ok = true;
+    if (nK > 0) {
+      ok = wait_all(&bar_k[0], 0);
+      if (ok) warp_arrive(&bar_k0);
+    }
+    for (int j = 0; j < nK && ok; ++j) {
+      ok = wait_all(&bar_v[j % VS], (j / VS) & 1);
+      if (ok && j + 1 < nK) ok = wait_all(&bar_k[(j + 1) % KS], ((j + 1) / KS) & 1);
+      if (ok && j == nK - 1) {  // rows past the last key
+        uint8_t* v = sV + (j % VS) * C::kVBytes;
+        for (int r = n_keys - j * BN + lane; r < BN; r += 32)
+#pragma unroll
+          for (int c = 0; c < C::kDims / 8; ++c)
+            *reinterpret_cast<uint4*>(v + (c >> 3) * (BN * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      // Phase j of a tile's P barrier has begun once S_j, issued after phase
+      // j - 1 was waited for, is complete; phase j + 1 of bar_s needs this
+      // arrival, so none is missed.
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (j >= (t ? nkv1 : nkv0)) continue;
+        ok = wait_all(&bar_s[t], j & 1);
+        if (ok) warp_arrive(&bar_p[t]);
+      }
+    }
+    if (!ok && lane == 0) report_timeout(p.status, 5, &abort_flag);
+  } else if (cta == 0) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t idS = idesc_bf16_f32(BM, BN, 0, 0);
-    const uint32_t idPV = idesc_bf16_f32(BM, kDv, 0, 1);
-    auto wait_all = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_ns, &abort_flag));
-    };
+    constexpr uint32_t idS = idesc_bf16_f32(MT, BN, 0, 0);
+    constexpr uint32_t idPV = idesc_bf16_f32(MT, kDv, 0, 1);
     const uint64_t dQ0 = smem_desc(smem_u32(sQ), 16, 1024);
     const uint64_t dK0 = smem_desc(smem_u32(sK), 16, 1024);
     const uint64_t dV0 = smem_desc(smem_u32(sV), BN * 128, 1024);
+    auto commit = [&](uint64_t* bar) {
+      if constexpr (PAIR) mma_commit_pair(smem_u32(bar));
+      else mma_commit(smem_u32(bar));
+    };
     auto issue_s = [&](int t, int j) {
       const uint64_t a0 = dQ0 + (uint64_t)((t * kQBytes) >> 4);
-      const uint64_t b0 = dK0 + (uint64_t)(((j % kKSlots) * kKBytes) >> 4);
+      const uint64_t b0 = dK0 + (uint64_t)(((j % KS) * C::kKBytes) >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kDqk / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + t * 256, a0 + off, b0 + off, idS, kk > 0);
+          const uint32_t oa = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+          const uint32_t ob = ((kk >> 2) * (C::kKeys * 128) + (kk & 3) * 32) >> 4;
+          if constexpr (PAIR) mma_ss_pair(tmem + t * 256, a0 + oa, b0 + ob, idS, kk > 0);
+          else mma_ss(tmem + t * 256, a0 + oa, b0 + ob, idS, kk > 0);
         }
-        mma_commit(smem_u32(&bar_s[t]));
+        commit(&bar_s[t]);
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int t, bool acc) {
+    auto issue_pv = [&](int t, int j) {
       const uint32_t pa = tmem + t * 256, d = tmem + t * 256 + 128;
+      const uint64_t v0 = dV0 + (uint64_t)(((j % VS) * C::kVBytes) >> 4);
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(d, pa + (kk >> 2) * 64 + (kk & 3) * 8, dV0 + (uint64_t)((kk * 16 * 128) >> 4),
-                 idPV, (acc || kk > 0) ? 1u : 0u);
-        mma_commit(smem_u32(&bar_o[t]));
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          const uint32_t a = pa + (kk >> 2) * 64 + (kk & 3) * 8;
+          const uint64_t b = v0 + (uint64_t)((kk * 16 * 128) >> 4);
+          if constexpr (PAIR) mma_ts_pair(d, a, b, idPV, (j > 0 || kk > 0) ? 1u : 0u);
+          else mma_ts(d, a, b, idPV, (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        commit(&bar_o[t]);
       }
       __syncwarp();
     };
     unsigned bad = 0;
     for (int t = 0; t < 2 && !bad; ++t)
-      if ((t ? nkv1 : nkv0) > 0 && !wait_all(smem_u32(&bar_q[t]), 0)) bad = 11;
+      if ((t ? nkv1 : nkv0) > 0 && !wait_all(&bar_q[t], 0)) bad = 11;
     if (!bad && nK > 0) {
-      if (!wait_all(smem_u32(&bar_k[0]), 0)) bad = 12;
+      if (!wait_all(&bar_k0, 0)) bad = 12;
       tc_fence_after();
       for (int t = 0; t < 2 && !bad; ++t)
         if ((t ? nkv1 : nkv0) > 0) issue_s(t, 0);
     }
     for (int j = 0; j < nK && !bad; ++j) {
-      if (!wait_all(smem_u32(&bar_v), j & 1)) bad = 13;
-      if (!bad && j == nK - 1 && !wait_all(smem_u32(&bar_tail), 0)) bad = 16;
-      if (!bad && j + 1 < nK && !wait_all(smem_u32(&bar_k[(j + 1) % kKSlots]), ((j + 1) / kKSlots) & 1)) bad = 17;
       for (int t = 0; t < 2 && !bad; ++t) {
         const int nt = t ? nkv1 : nkv0;
         if (j >= nt) continue;
-        if (!wait_all(smem_u32(&bar_p[t]), j & 1)) {
+        if (!wait_all(&bar_p[t], j & 1)) {  // P_j is written, V_j and K_(j+1) are in place
           bad = 14 + t;
           break;
         }
         tc_fence_after();
-        issue_pv(t, j > 0);
+        issue_pv(t, j);
         if (j + 1 < nt) issue_s(t, j + 1);
       }
     }
     if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
     // Never free TMEM under a running MMA: wait for everything issued.
-    if (elect_one()) mma_commit(smem_u32(&bar_drain));
+    if (elect_one()) commit(&bar_drain);
     __syncwarp();
     mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // neither CTA leaves while products read its memory
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (warp == kWarpMma) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
+}
+
+// Rows of the head's keys or values as 3-d (256 dims, heads, rows).
+bool kv_map(CUtensorMap* m, const void* kv, int H, int rows, int box_rows) {
+  const uint64_t dims[3] = {kNope + kDv, (uint64_t)H, (uint64_t)rows};
+  const uint64_t strides[2] = {(kNope + kDv) * 2, (uint64_t)H * (kNope + kDv) * 2};
+  const uint32_t box[3] = {64, 1, (uint32_t)box_rows};
+  return encode_tensor_map_bf16(m, kv, 3, dims, strides, box);
+}
+
+template <bool PAIR>
+cudaError_t launch(const Params& p, const void* kv, const void* k_rope, long long rope_stride, int rows,
+                   cudaStream_t s) {
+  using C = Cfg<PAIR>;
+  CUtensorMap km, vm, rm;
+  const uint64_t dims[2] = {kRope, (uint64_t)rows};
+  const uint64_t strides[1] = {(uint64_t)rope_stride * 2};
+  const uint32_t box[2] = {64, C::kKeys};
+  if (!kv_map(&km, kv, p.H, rows, C::kKeys) || !kv_map(&vm, kv, p.H, rows, BN) ||
+      !encode_tensor_map_bf16(&rm, k_rope, 2, dims, strides, box, false))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)p.n_tiles * p.H * C::kCtas;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C::kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mla_prefill_kernel<PAIR>, km, vm, rm, p);
 }
 
 }  // namespace
@@ -486,25 +600,17 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInvalidDevice;
   p.wait_ns = wait_limit_ns();
-  CUtensorMap kvm, rm;
-  {
-    const uint64_t dims[3] = {kNope + kDv, (uint64_t)H, (uint64_t)h.KV};
-    const uint64_t strides[2] = {(kNope + kDv) * 2, (uint64_t)H * (kNope + kDv) * 2};
-    const uint32_t box[3] = {64, 1, BN};
-    if (!encode_tensor_map_bf16(&kvm, kv, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  p.head_major = (long long)h.KV * H * (kNope + kDv) * 2 > kTileMajorBytes;
+  // how much of a pair's 4 x 128 rows the segments fill
+  const cp_seg_desc* seg = reinterpret_cast<const cp_seg_desc*>(host_plan + h.off_seg);
+  long long n128 = 0, n512 = 0;
+  for (int i = 0; i < h.n_seg; ++i) {
+    if (rank >= 0 && seg[i].rank != rank) continue;
+    n128 += (seg[i].count + 127) / 128;
+    n512 += (seg[i].count + 511) / 512;
   }
-  {
-    const uint64_t dims[2] = {kRope, (uint64_t)h.KV};
-    const uint64_t strides[1] = {(uint64_t)rope_stride * 2};
-    const uint32_t box[2] = {64, BN};
-    if (!encode_tensor_map_bf16(&rm, k_rope, 2, dims, strides, box, false)) return cudaErrorInvalidValue;
-  }
-  cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  const long long blocks = (long long)p.n_tiles * H;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  mla_prefill_kernel<<<(unsigned)blocks, kThreads, kSmem, s>>>(kvm, rm, p);
-  return cudaGetLastError();
+  const bool pair = n128 >= 3 * n512;
+  return pair ? launch<true>(p, kv, k_rope, rope_stride, h.KV, s) : launch<false>(p, kv, k_rope, rope_stride, h.KV, s);
 }
 
 }  // namespace cpattn
