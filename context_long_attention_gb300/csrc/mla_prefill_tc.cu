@@ -33,6 +33,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "tc_pair.cuh"
 
@@ -57,7 +59,8 @@ constexpr float kRescaleLog2 = 8.0f;      // move the running max when it grows 
 constexpr float kSpecSum = 64.f * 256.f;  // a half row's P sum that may hide a P above 2^8
 
 constexpr int kQBytes = BM * kDqk * 2;
-constexpr long long kTileMajorBytes = 64ll << 20;  // keys and values that the L2 holds with room to spare
+constexpr int kPiece = BN * 128;  // bytes of 64 dims of a tile's keys
+constexpr long long kGroupBytes = 80ll << 20;  // keys and values of a head group: the L2 (129 MB) holds them beside Q and O
 
 template <bool PAIR>
 struct Cfg {
@@ -67,10 +70,12 @@ struct Cfg {
   static constexpr int kDims = kDv / kCtas;                // dims of a V tile in one CTA
   static constexpr int kKBytes = kKeys * kDqk * 2;
   static constexpr int kVBytes = BN * kDims * 2;
-  // a pair's halves fit three times beside Q, whole tiles twice (K) and once (V)
-  static constexpr int kKSlots = PAIR ? 3 : 2;
-  static constexpr int kVSlots = PAIR ? 3 : 1;
-  static constexpr int kSmem = 2 * kQBytes + kKSlots * kKBytes + kVSlots * kVBytes + 1024;
+  // Beside Q a pair's halves fit three times.  Whole tiles do not fit twice:
+  // one CTA keeps a ring of eight pieces of [128 keys x 64 dims], a step's V_j
+  // (two) and K_(j+1) (three) and three of the next step.
+  static constexpr int kSlots = PAIR ? 3 : 2;  // barriers in turn; for a pair also tiles
+  static constexpr int kRing = PAIR ? kSlots * (kKBytes + kVBytes) : 8 * kPiece;
+  static constexpr int kSmem = 2 * kQBytes + kRing + 1024;
 };
 
 struct Params {
@@ -83,7 +88,7 @@ struct Params {
   __nv_bfloat16* o;
   float* lse;
   int H;
-  int head_major;  // units head by head, else tile by tile (every head of the longest tiles first)
+  int head_group;  // heads whose units run together, tile by tile
   float sm_scale, scale_log2;
   unsigned* status;
   unsigned long long wait_ns;
@@ -128,24 +133,30 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ CUtensorMap ropemap, const Params p) {
   using C = Cfg<PAIR>;
-  constexpr int KS = C::kKSlots, VS = C::kVSlots, MT = C::kRows;
+  constexpr int KS = C::kSlots, MT = C::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + 2 * kQBytes;
-  uint8_t* sV = sK + KS * C::kKBytes;
-  // bar_k, bar_v: this CTA's part of K_j (V_j) has landed; only the relay warp
-  // waits for them, tile after tile.  bar_rel[j % KS]: a softmax thread saw
-  // S_j of the step's last tile complete, so K_j and V_(j-1) are read (products
-  // complete in order).  K_(j+KS) is loaded after release j, and release j + KS
-  // needs that load, so no phase of bar_rel completes unobserved; nor one of
-  // bar_k or bar_v, since S_j needs P_(j-1), which the relay completes after
-  // it has waited for K_j and V_(j-1).
+  uint8_t* sV = sK + KS * C::kKBytes;  // (pair)
+  // one CTA: piece g of the order K_0, V_0, K_1, V_1, ... (K_j: 5j .. 5j + 2, V_j: 5j + 3, 5j + 4)
+  auto piece = [&](int g) { return sK + (g & 7) * kPiece; };
+  // bar_k, bar_v [j % KS]: this CTA's part of K_j (V_j) has landed; waited for
+  // tile after tile by the relay (V, and a pair's K) and by the issuer (K of
+  // one CTA).  bar_rel[j % KS]: a softmax thread saw S_j of the step's last
+  // tile complete, so K_j and V_(j-1) are read (products complete in order).
+  // A pair loads K_(j+3) and V_(j+2) after release j.  One CTA loads V_j and
+  // the first piece of K_(j+1), which take the pieces of K_(j-1), after release
+  // j - 1, and K_(j+1)'s other pieces, which take V_(j-1)'s, after the last
+  // P_(j-1) V_(j-1) (bar_o).  Every barrier that the producer waits for comes
+  // round again only after products that need the load it is waiting to make,
+  // and every landing barrier after products that its waiter lets through: no
+  // phase completes unobserved.  (bar_o alternates between two for that.)
   // bar_q, bar_k0, bar_p are waited for by the issuer and live in its CTA;
   // warps arrive there from both CTAs.
-  __shared__ __align__(8) uint64_t bar_k[KS], bar_v[VS], bar_rel[KS], bar_k0;
-  __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2], bar_drain;
+  __shared__ __align__(8) uint64_t bar_k[KS], bar_v[KS], bar_rel[KS], bar_k0;
+  __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2][2], bar_drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int zero_flag;
@@ -153,8 +164,12 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = PAIR ? (int)cluster_ctarank() : 0;
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  const int h = p.head_major ? unit / p.n_tiles : unit % p.H;
-  const int tile_i = p.head_major ? unit - h * p.n_tiles : unit / p.H;
+  // Units go head group by head group, in a group tile by tile (longest
+  // first) over its heads: the keys and values in use stay in the L2, and the
+  // long tiles of no head come last.
+  const int per_group = p.n_tiles * p.head_group, g0 = unit / per_group, rem = unit - g0 * per_group;
+  const int group = min(p.head_group, p.H - g0 * p.head_group);
+  const int tile_i = rem / group, h = g0 * p.head_group + rem - tile_i * group;
   const cp_tile_desc td = reinterpret_cast<const cp_tile_desc*>(p.plan + p.tile_list)[tile_i];
   // a pair takes two plan tiles, from every even one of a segment
   if (PAIR && (td.q_off & (2 * MT - 1))) return;
@@ -171,15 +186,15 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
       mbar_init(smem_u32(&bar_k[s]), 1);
+      mbar_init(smem_u32(&bar_v[s]), 1);
       mbar_init(smem_u32(&bar_rel[s]), 1);
     }
-    for (int s = 0; s < VS; ++s) mbar_init(smem_u32(&bar_v[s]), 1);
     mbar_init(smem_u32(&bar_k0), C::kCtas);
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&bar_q[t]), 8 * C::kCtas);        // a tile's eight softmax warps
       mbar_init(smem_u32(&bar_p[t]), (8 + 1) * C::kCtas);  // and the relay
       mbar_init(smem_u32(&bar_s[t]), 1);
-      mbar_init(smem_u32(&bar_o[t]), 1);
+      for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&bar_o[t][k]), 1);
     }
     mbar_init(smem_u32(&bar_drain), 1);
     abort_flag = 0;
@@ -322,7 +337,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
               l *= alpha;
               m_used = mrow;
             }
-            const bool landed = wait_all(&bar_o[t], (j - 1) & 1);
+            const bool landed = wait_all(&bar_o[t][(j - 1) & 1], ((j - 1) >> 1) & 1);
             if (bar_red_or(pbar, 64, !landed)) {
               if (!landed) report_timeout(p.status, 2, &abort_flag);
               ok = false;
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         tc_fence_before();
         warp_arrive(&bar_p[t]);
       }
-      const bool landed = ok && wait_all(&bar_o[t], (n_t - 1) & 1);
+      const bool landed = ok && wait_all(&bar_o[t][(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
       if (!bar_red_or(pbar, 64, !landed)) {
         tc_fence_after();
         const float lt = l + exchange(l);
@@ -380,68 +395,78 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     // ------------------------------------------------------------ TMA producer
     int last_k = -1, last_v = -1;
     bool ok = true;
-    for (int j = 0; j <= nK && nK > 0 && ok; ++j) {
-      if (j < nK) {  // K_j
-        if (j >= KS) ok = wait_all(&bar_rel[j % KS], (j / KS - 1) & 1);
-        if (!ok) break;
-        if (elect_one()) {
-          const uint32_t full = smem_u32(&bar_k[j % KS]);
-          const uint32_t dst = smem_u32(sK + (j % KS) * C::kKBytes);
-          const int row = sg.kv_base + j * BN + cta * C::kKeys;
-          mbar_expect_tx(full, C::kKBytes);
-          tma_load_3d(dst, &kmap, 0, h, row, full);
-          tma_load_3d(dst + C::kKeys * 128, &kmap, 64, h, row, full);
-          tma_load_2d(dst + 2 * C::kKeys * 128, &ropemap, 0, row, full);
-        }
-        __syncwarp();
-        last_k = j;
-      }
-      if (j > 0) {  // V_(j-1)
-        const int v = j - 1;
-        if constexpr (PAIR) {
-          // its slot held V_(v-3), which release v - 2 frees; K_j has waited
-          // for that one (j - KS), the last V, without a K beside it, does here
-          if (j == nK && v >= VS) ok = wait_all(&bar_rel[j % KS], (j / KS - 1) & 1);
-        } else {
-          // one slot: the last product of step v - 1 (the next phase needs V_v)
-          if (v > 0) ok = wait_all(&bar_o[last_t], (v - 1) & 1);
-        }
-        if (!ok) break;
-        if (elect_one()) {
-          const uint32_t full = smem_u32(&bar_v[v % VS]), dst = smem_u32(sV + (v % VS) * C::kVBytes);
-          const int row = sg.kv_base + v * BN;
-          mbar_expect_tx(full, C::kVBytes);
+    auto load_v = [&](int j) {
+      if (elect_one()) {
+        const uint32_t full = smem_u32(&bar_v[j % KS]);
+        mbar_expect_tx(full, C::kVBytes);
 #pragma unroll
-          for (int c = 0; c < C::kDims / 64; ++c)
-            tma_load_3d(dst + c * BN * 128, &vmap, kNope + cta * C::kDims + c * 64, h, row, full);
+        for (int c = 0; c < C::kDims / 64; ++c)
+          tma_load_3d(smem_u32(PAIR ? sV + (j % KS) * C::kVBytes : piece(5 * j + 3 + c)), &vmap,
+                      kNope + cta * C::kDims + c * 64, h, sg.kv_base + j * BN, full);
+      }
+      __syncwarp();
+      last_v = j;
+    };
+    auto load_k = [&](int j, int c0, int c1) {  // its 64-dim pieces c0 .. c1 - 1 (from 0 first)
+      if (elect_one()) {
+        const uint32_t full = smem_u32(&bar_k[j % KS]);
+        if (c0 == 0) mbar_expect_tx(full, C::kKBytes);
+        for (int c = c0; c < c1; ++c) {
+          const uint32_t dst = smem_u32(PAIR ? sK + (j % KS) * C::kKBytes + c * C::kKeys * 128 : piece(5 * j + c));
+          const int row = sg.kv_base + j * BN + cta * C::kKeys;
+          if (c < 2) tma_load_3d(dst, &kmap, c * 64, h, row, full);
+          else tma_load_2d(dst, &ropemap, 0, row, full);
         }
-        __syncwarp();
-        last_v = v;
+      }
+      __syncwarp();
+      last_k = j;
+    };
+    if (nK > 0) load_k(0, 0, 3);
+    for (int j = 0; j < nK && ok; ++j) {  // V_j and K_(j+1)
+      if constexpr (PAIR) {
+        if (j >= KS - 1) ok = wait_all(&bar_rel[(j + 1) % KS], ((j + 1) / KS - 1) & 1);
+        if (!ok) break;
+        load_v(j);
+        if (j + 1 < nK) load_k(j + 1, 0, 3);
+      } else {
+        if (j > 0) ok = wait_all(&bar_rel[(j - 1) & 1], ((j - 1) >> 1) & 1);
+        if (!ok) break;
+        load_v(j);
+        if (j + 1 < nK) {
+          load_k(j + 1, 0, 1);
+          if (j > 0) ok = wait_all(&bar_o[last_t][(j - 1) & 1], ((j - 1) >> 1) & 1);
+          if (!ok) {  // give the barrier what it waits for: nobody uses the pieces any more
+            load_k(j + 1, 1, 3);
+            break;
+          }
+          load_k(j + 1, 1, 3);
+        }
       }
     }
     if (!ok && lane == 0) report_timeout(p.status, 4, &abort_flag);
     // Never leave with a copy in flight.
     for (int k = max(0, last_k - KS + 1); k <= last_k; ++k)
       mbar_wait(smem_u32(&bar_k[k % KS]), (k / KS) & 1, 1000000000ull, &zero_flag);
-    for (int k = max(0, last_v - VS + 1); k <= last_v; ++k)
-      mbar_wait(smem_u32(&bar_v[k % VS]), (k / VS) & 1, 1000000000ull, &zero_flag);
+    for (int k = max(0, last_v - KS + 1); k <= last_v; ++k)
+      mbar_wait(smem_u32(&bar_v[k % KS]), (k / KS) & 1, 1000000000ull, &zero_flag);
     __syncwarp();
   } else if (warp == kWarpRelay) {
     // ------------------------------------------------------------ relay
     bool ok = true;
-    if (nK > 0) {
+    if (PAIR && nK > 0) {
       ok = wait_all(&bar_k[0], 0);
       if (ok) warp_arrive(&bar_k0);
     }
     for (int j = 0; j < nK && ok; ++j) {
-      ok = wait_all(&bar_v[j % VS], (j / VS) & 1);
-      if (ok && j + 1 < nK) ok = wait_all(&bar_k[(j + 1) % KS], ((j + 1) / KS) & 1);
+      ok = wait_all(&bar_v[j % KS], (j / KS) & 1);
+      if (PAIR && ok && j + 1 < nK) ok = wait_all(&bar_k[(j + 1) % KS], ((j + 1) / KS) & 1);
       if (ok && j == nK - 1) {  // rows past the last key
-        uint8_t* v = sV + (j % VS) * C::kVBytes;
         for (int r = n_keys - j * BN + lane; r < BN; r += 32)
 #pragma unroll
-          for (int c = 0; c < C::kDims / 8; ++c)
-            *reinterpret_cast<uint4*>(v + (c >> 3) * (BN * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < C::kDims / 8; ++c) {
+            uint8_t* v = PAIR ? sV + (j % KS) * C::kVBytes : piece(5 * j + 3 + (c >> 3));
+            *reinterpret_cast<uint4*>(v + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
         fence_proxy_async_smem();
       }
       // Phase j of a tile's P barrier has begun once S_j, issued after phase
@@ -460,21 +485,24 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     constexpr uint32_t idPV = idesc_bf16_f32(MT, kDv, 0, 1);
     const uint64_t dQ0 = smem_desc(smem_u32(sQ), 16, 1024);
     const uint64_t dK0 = smem_desc(smem_u32(sK), 16, 1024);
-    const uint64_t dV0 = smem_desc(smem_u32(sV), BN * 128, 1024);
+    const uint64_t dV0 = smem_desc(smem_u32(PAIR ? sV : sK), BN * 128, 1024);
     auto commit = [&](uint64_t* bar) {
       if constexpr (PAIR) mma_commit_pair(smem_u32(bar));
       else mma_commit(smem_u32(bar));
     };
     auto issue_s = [&](int t, int j) {
       const uint64_t a0 = dQ0 + (uint64_t)((t * kQBytes) >> 4);
-      const uint64_t b0 = dK0 + (uint64_t)(((j % KS) * C::kKBytes) >> 4);
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kDqk / 16; ++kk) {
-          const uint32_t oa = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          const uint32_t ob = ((kk >> 2) * (C::kKeys * 128) + (kk & 3) * 32) >> 4;
-          if constexpr (PAIR) mma_ss_pair(tmem + t * 256, a0 + oa, b0 + ob, idS, kk > 0);
-          else mma_ss(tmem + t * 256, a0 + oa, b0 + ob, idS, kk > 0);
+        for (int c = 0; c < 3; ++c) {
+          const uint64_t b0 = dK0 + (uint64_t)((PAIR ? (j % KS) * C::kKBytes + c * C::kKeys * 128
+                                                     : ((5 * j + c) & 7) * kPiece) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t a = a0 + ((c * (BM * 128) + kk * 32) >> 4), b = b0 + ((kk * 32) >> 4);
+            if constexpr (PAIR) mma_ss_pair(tmem + t * 256, a, b, idS, c + kk > 0);
+            else mma_ss(tmem + t * 256, a, b, idS, c + kk > 0);
+          }
         }
         commit(&bar_s[t]);
       }
@@ -482,16 +510,28 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     };
     auto issue_pv = [&](int t, int j) {
       const uint32_t pa = tmem + t * 256, d = tmem + t * 256 + 128;
-      const uint64_t v0 = dV0 + (uint64_t)(((j % VS) * C::kVBytes) >> 4);
+      const int g = (5 * j + 3) & 7;  // one CTA: V's first piece
+      const uint64_t v0 = dV0 + (uint64_t)((PAIR ? (j % KS) * C::kVBytes : g * kPiece) >> 4);
       if (elect_one()) {
+        if (!PAIR && g == 7) {
+          // the second piece is the ring's first: each 64 dims a product of their own
+          constexpr uint32_t idHalf = idesc_bf16_f32(MT, kDv / 2, 0, 1);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk) {
-          const uint32_t a = pa + (kk >> 2) * 64 + (kk & 3) * 8;
-          const uint64_t b = v0 + (uint64_t)((kk * 16 * 128) >> 4);
-          if constexpr (PAIR) mma_ts_pair(d, a, b, idPV, (j > 0 || kk > 0) ? 1u : 0u);
-          else mma_ts(d, a, b, idPV, (j > 0 || kk > 0) ? 1u : 0u);
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              mma_ts(d + c * 64, pa + (kk >> 2) * 64 + (kk & 3) * 8,
+                     (c ? dV0 : v0) + (uint64_t)((kk * 16 * 128) >> 4), idHalf, (j > 0 || kk > 0) ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk) {
+            const uint32_t a = pa + (kk >> 2) * 64 + (kk & 3) * 8;
+            const uint64_t b = v0 + (uint64_t)((kk * 16 * 128) >> 4);
+            if constexpr (PAIR) mma_ts_pair(d, a, b, idPV, (j > 0 || kk > 0) ? 1u : 0u);
+            else mma_ts(d, a, b, idPV, (j > 0 || kk > 0) ? 1u : 0u);
+          }
         }
-        commit(&bar_o[t]);
+        commit(&bar_o[t][j & 1]);
       }
       __syncwarp();
     };
@@ -499,22 +539,32 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     for (int t = 0; t < 2 && !bad; ++t)
       if ((t ? nkv1 : nkv0) > 0 && !wait_all(&bar_q[t], 0)) bad = 11;
     if (!bad && nK > 0) {
-      if (!wait_all(&bar_k0, 0)) bad = 12;
+      if (!wait_all(PAIR ? &bar_k0 : &bar_k[0], 0)) bad = 12;
       tc_fence_after();
       for (int t = 0; t < 2 && !bad; ++t)
         if ((t ? nkv1 : nkv0) > 0) issue_s(t, 0);
     }
     for (int j = 0; j < nK && !bad; ++j) {
+      bool k_in = PAIR;  // K_(j+1) is in place: a pair's P barrier says so
       for (int t = 0; t < 2 && !bad; ++t) {
         const int nt = t ? nkv1 : nkv0;
         if (j >= nt) continue;
-        if (!wait_all(&bar_p[t], j & 1)) {  // P_j is written, V_j and K_(j+1) are in place
+        if (!wait_all(&bar_p[t], j & 1)) {  // P_j is written, V_j is in place
           bad = 14 + t;
           break;
         }
         tc_fence_after();
         issue_pv(t, j);
-        if (j + 1 < nt) issue_s(t, j + 1);
+        if (j + 1 >= nt) continue;
+        if (!k_in) {  // while P V runs
+          k_in = wait_all(&bar_k[(j + 1) % KS], ((j + 1) / KS) & 1);
+          if (!k_in) {
+            bad = 17;
+            break;
+          }
+          tc_fence_after();
+        }
+        issue_s(t, j + 1);
       }
     }
     if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
@@ -600,8 +650,16 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInvalidDevice;
   p.wait_ns = wait_limit_ns();
-  p.head_major = (long long)h.KV * H * (kNope + kDv) * 2 > kTileMajorBytes;
-  // how much of a pair's 4 x 128 rows the segments fill
+  const long long head_bytes = (long long)h.KV * (kNope + kDv) * 2;
+  const int most = (int)std::min<long long>(H, std::max<long long>(1, kGroupBytes / head_bytes));
+  const int groups = (H + most - 1) / most;
+  p.head_group = (H + groups - 1) / groups;
+  // A pair where segments fill three quarters of its 512 rows or more.  Both
+  // forms take about as long for a tile step (3,000 clk for a pair's 512
+  // rows, 3,440 for one CTA's 256), so a pair whose second M tile is empty
+  // wastes an SM: 16,384 + 4,096 tokens in blocks of 1,024 queries, 32 heads:
+  // pairs 2,541 us, single CTAs 2,704; nine ragged requests interleaved over
+  // four ranks (63 quarters filled of 140), 16 heads: 196 and 129.
   const cp_seg_desc* seg = reinterpret_cast<const cp_seg_desc*>(host_plan + h.off_seg);
   long long n128 = 0, n512 = 0;
   for (int i = 0; i < h.n_seg; ++i) {
