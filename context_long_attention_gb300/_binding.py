@@ -738,59 +738,60 @@ def cp_sparse_decode_attn_merged(plan: DecodePlan, pair_count, mode: int, q, sel
 
 
 # ---------------------------------------------------------------- latent attention
+#
+# These calls are as short as a decode step's kernels (a few us), so their
+# checks are one comparison chain a tensor, and a message is only put together
+# once one of them fails.
 
 LATENT_DIM, MLA_NOPE_DIM, MLA_ROPE_DIM, MLA_V_DIM = 512, 128, 64, 128
+_bf16, _i32t = torch.bfloat16, torch.int32
 
 
-def _need(name, t, dtype, shape, device=None):
-    """A contiguous CUDA tensor of this dtype and shape (None: any extent),
-    on `device` if given."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: need {dtype}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: need shape {shape}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
-
-
-def _rows(name, t, cols, dtype, device=None):
-    """(pointer, row stride) of a CUDA tensor [n, >= cols] whose rows are
-    dense and may lie apart (a view of a wider tensor)."""
+def _complain(name, t, dtype, shape, device):
     if t.dtype != dtype:
         raise TypeError(f"{name}: need {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: need shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need(name, t, dtype, shape, device):
+    """A contiguous CUDA tensor of this dtype and shape on `device`."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
+        return t
+    return _complain(name, t, dtype, shape, device)
+
+
+def _rows(name, t, cols, dtype, device):
+    """(pointer, row stride) of a CUDA tensor [n, >= cols] whose rows are
+    dense and may lie apart (a view of a wider tensor)."""
+    if t.dtype is not dtype or not t.is_cuda or t.device != device:
+        _complain(name, t, dtype, t.shape, device)
     if t.dim() != 2 or t.shape[1] < cols or t.stride(1) != 1:
         raise ValueError(f"{name}: need [n, {cols}] with dense rows, got {tuple(t.shape)}, strides {t.stride()}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
 
 
 def _call(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device
     current (kernels launch on the current device)."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st != 0:
         _check(st)
 
 
-def _w_kv(w_kv, device):
-    _need("w_kv", w_kv, torch.bfloat16, (None, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), device)
-    return w_kv.shape[0]
-
-
-def _out(name, out, dtype, shape, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(name, out, dtype, shape, device)
-    return out
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def cp_mla_expand(latent, w_kv, out=None):
@@ -798,19 +799,23 @@ def cp_mla_expand(latent, w_kv, out=None):
     columns; rows may be a view of the 576-wide cache), w_kv [H, 256, 512]
     -> kv [T, H, 256] (128 key dims, then 128 value dims of each head)."""
     dev = latent.device
-    ptr, stride = _rows("latent", latent, LATENT_DIM, torch.bfloat16)
-    H = _w_kv(w_kv, dev)
-    out = _out("out", out, torch.bfloat16, (latent.shape[0], H, MLA_NOPE_DIM + MLA_V_DIM), dev)
-    _call(dev, lib.cp_mla_expand, ptr, stride, w_kv.data_ptr(), latent.shape[0], H, out.data_ptr())
+    ptr, stride = _rows("latent", latent, LATENT_DIM, _bf16, dev)
+    T, H = latent.shape[0], w_kv.shape[0]
+    _need("w_kv", w_kv, _bf16, (H, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), dev)
+    shape = (T, H, MLA_NOPE_DIM + MLA_V_DIM)
+    out = torch.empty(shape, dtype=_bf16, device=dev) if out is None else _need("out", out, _bf16, shape, dev)
+    _call(dev, lib.cp_mla_expand, ptr, stride, w_kv.data_ptr(), T, H, out.data_ptr())
     return out
 
 
 def _per_head(name, x, w_kv, cols, out_cols, out, fn):
     dev = x.device
-    H = _w_kv(w_kv, dev)
-    _need(name, x, torch.bfloat16, (None,) * (x.dim() - 2) + (H, cols))
+    H = w_kv.shape[0]
     lead = x.shape[:-2]
-    out = _out("out", out, torch.bfloat16, (*lead, H, out_cols), dev)
+    _need("w_kv", w_kv, _bf16, (H, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), dev)
+    _need(name, x, _bf16, (*lead, H, cols), dev)
+    shape = (*lead, H, out_cols)
+    out = torch.empty(shape, dtype=_bf16, device=dev) if out is None else _need("out", out, _bf16, shape, dev)
     _call(dev, fn, x.data_ptr(), w_kv.data_ptr(), lead.numel(), H, out.data_ptr())
     return out
 
@@ -834,19 +839,21 @@ def cp_mla_prefill_attn(plan: PrefillPlan, q, kv, k_rope, sm_scale=None, rank: i
     (cp_mla_expand); k_rope [KV, 64], a view of the latent cache's last
     columns or a tensor of its own; returns (o [rows, H, 128], lse [rows, H])."""
     dev = q.device
-    _need("q", q, torch.bfloat16, (plan.T, None, MLA_NOPE_DIM + MLA_ROPE_DIM))
-    H = q.shape[1]
-    _need("kv", kv, torch.bfloat16, (plan.KV, H, MLA_NOPE_DIM + MLA_V_DIM), dev)
-    rope, stride = _rows("k_rope", k_rope, MLA_ROPE_DIM, torch.bfloat16, dev)
-    if k_rope.shape[0] != plan.KV:
-        raise ValueError(f"k_rope has {k_rope.shape[0]} rows, the plan {plan.KV}")
+    T, KV, H = plan.header["T"], plan.header["KV"], q.shape[1]
+    _need("q", q, _bf16, (T, H, MLA_NOPE_DIM + MLA_ROPE_DIM), dev)
+    _need("kv", kv, _bf16, (KV, H, MLA_NOPE_DIM + MLA_V_DIM), dev)
+    rope, stride = _rows("k_rope", k_rope, MLA_ROPE_DIM, _bf16, dev)
+    if k_rope.shape[0] != KV:
+        raise ValueError(f"k_rope has {k_rope.shape[0]} rows, the plan {KV}")
     if plan.dev is None or plan.dev.device != dev:
         raise ValueError(f"the plan has no device part on {dev}")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(MLA_NOPE_DIM + MLA_ROPE_DIM)
-    rows = plan.rank_rows(rank)
-    out = _out("out", out, torch.bfloat16, (rows, H, MLA_V_DIM), dev)
-    lse = _out("lse", lse, torch.float32, (rows, H), dev)
+    rows = T if rank < 0 else plan.rank_rows(rank)
+    out = torch.empty((rows, H, MLA_V_DIM), dtype=_bf16, device=dev) if out is None else \
+        _need("out", out, _bf16, (rows, H, MLA_V_DIM), dev)
+    lse = torch.empty((rows, H), dtype=torch.float32, device=dev) if lse is None else \
+        _need("lse", lse, torch.float32, (rows, H), dev)
     _call(dev, lib.cp_mla_prefill_attn, plan.host.ctypes.data, plan.dev.data_ptr(), rank, q.data_ptr(), kv.data_ptr(),
           rope, stride, H, sm_scale, out.data_ptr(), lse.data_ptr())
     return out, lse
@@ -868,44 +875,44 @@ def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos
     ``pages.sync_host()`` where a decode call needs it).  Returns (slots
     [max_tokens], cu_new [B + 1], info [4] = status, next free_pos, pages
     taken, new tokens), all int32 on the GPU; see cpattn.h for the status."""
-    i32, table = torch.int32, pages.dev
+    i32, table = _i32t, pages.dev
     if table is None:
         raise ValueError("the page table has no device copy")
     dev = table.device
-    B = ctx_len.shape[0]
-    _need("page table", table, i32, (C * B, pages.max_pages))
+    B, n_free = ctx_len.shape[0], free_ids.shape[0]
+    _need("page table", table, i32, (C * B, pages.max_pages), dev)
     _need("ctx_len", ctx_len, i32, (B,), dev)
     _need("new_len", new_len, i32, (B,), dev)
-    _need("free_ids", free_ids, i32, (None,), dev)
+    _need("free_ids", free_ids, i32, (n_free,), dev)
     _need("free_pos", free_pos, i32, (1,), dev)
-    slots = _out("slots", slots, i32, (max_tokens,), dev)
-    if cu_new is None and info is None:
-        both = torch.empty(B + 5, dtype=i32, device=dev)  # one allocation for the two small outputs
-        info, cu_new = both[:4], both[4:]
-    cu_new = _out("cu_new", cu_new, i32, (B + 1,), dev)
-    info = _out("info", info, i32, (4,), dev)
+    slots = torch.empty(max_tokens, dtype=i32, device=dev) if slots is None else \
+        _need("slots", slots, i32, (max_tokens,), dev)
+    cu_new = torch.empty(B + 1, dtype=i32, device=dev) if cu_new is None else \
+        _need("cu_new", cu_new, i32, (B + 1,), dev)
+    info = torch.empty(4, dtype=i32, device=dev) if info is None else _need("info", info, i32, (4,), dev)
     _call(dev, lib.cp_page_slots, C, B, ctx_len.data_ptr(), new_len.data_ptr(), table.data_ptr(), pages.max_pages,
-          pages.page_size, pages.num_pages, free_ids.data_ptr(), free_ids.shape[0], free_pos.data_ptr(),
+          pages.page_size, pages.num_pages, free_ids.data_ptr(), n_free, free_pos.data_ptr(),
           slots.data_ptr(), max_tokens, cu_new.data_ptr(), info.data_ptr())
     return slots, cu_new, info
 
 
 def _new_rows(name, t, n, pool, dev):
-    """(pointer, row stride) of new tokens' rows [n, ...] shaped like the
-    pool's; only the first dimension may be strided."""
+    """(pointer, row stride, row elements) of new tokens' rows [n, ...] shaped
+    like the pool's; only the first dimension may be strided."""
+    shape, row = t.shape, pool.shape[1:]
     if not t.is_cuda or t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    if t.shape[0] != n or t.shape[1:] != pool.shape[1:]:
-        raise ValueError(f"{name}: need {(n, *pool.shape[1:])}, got {tuple(t.shape)}")
-    row = pool.shape[1:].numel()
+    if shape[0] != n or shape[1:] != row:
+        raise ValueError(f"{name}: need {(n, *row)}, got {tuple(shape)}")
+    elems = row.numel()
     if t.is_contiguous():
-        return t.data_ptr(), row
+        return t.data_ptr(), elems, elems
     inner = 1
-    for size, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+    for size, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
         if st != inner and size != 1:
             raise ValueError(f"{name}: a row must be dense, got strides {t.stride()}")
         inner *= size
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), t.stride(0), elems
 
 
 def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=None, new_scale=None):
@@ -918,14 +925,14 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
     an E4M3 pool (uint8 or float8_e4m3fn) are quantised with one scale a
     token, amax / 448 over its K and V, written to scale_pool [pool_rows]."""
     dev = k_pool.device
-    n = slots.shape[0]
+    n, rows = slots.shape[0], k_pool.shape[0]
     if not k_pool.is_cuda or not k_pool.is_contiguous():
         raise ValueError("k_pool must be a contiguous CUDA tensor")
-    _need("slots", slots, torch.int32, (None,), dev)
-    rows = k_pool.shape[0]
-    kp, ks = _new_rows("k_new", k_new, n, k_pool, dev)
+    _need("slots", slots, _i32t, (n,), dev)
+    kp, ks, elems = _new_rows("k_new", k_new, n, k_pool, dev)
     src, pool = _dtype_code(k_new), _dtype_code(k_pool)
-    vp = vs = vpool = 0
+    vp = vpool = None
+    vs = 0
     if (v_new is None) != (v_pool is None):
         raise ValueError("v_new and v_pool must both be given or both None")
     if v_new is not None:
@@ -933,15 +940,12 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
             raise TypeError("V must have K's dtypes")
         if v_pool.shape != k_pool.shape or v_pool.device != dev or not v_pool.is_contiguous():
             raise ValueError("v_pool must be a contiguous tensor like k_pool")
-        vp, vs = _new_rows("v_new", v_new, n, v_pool, dev)
+        vp, vs, _ = _new_rows("v_new", v_new, n, v_pool, dev)
         vpool = v_pool.data_ptr()
-    if scale_pool is not None:
-        _need("scale_pool", scale_pool, torch.float32, (rows,), dev)
-    if new_scale is not None:
-        _need("new_scale", new_scale, torch.float32, (n,), dev)
-    _call(dev, lib.cp_cache_append, slots.data_ptr(), n, src, kp, ks, vp or None, vs,
-          None if new_scale is None else new_scale.data_ptr(), k_pool.shape[1:].numel(), pool, k_pool.data_ptr(),
-          vpool or None, None if scale_pool is None else scale_pool.data_ptr(), rows)
+    _call(dev, lib.cp_cache_append, slots.data_ptr(), n, src, kp, ks, vp, vs,
+          None if new_scale is None else _need("new_scale", new_scale, torch.float32, (n,), dev).data_ptr(), elems,
+          pool, k_pool.data_ptr(), vpool,
+          None if scale_pool is None else _need("scale_pool", scale_pool, torch.float32, (rows,), dev).data_ptr(), rows)
 
 
 # ---------------------------------------------------------------- NVTX ranges

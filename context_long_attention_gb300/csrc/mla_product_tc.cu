@@ -16,13 +16,18 @@
 //              stage; its weight is read as an MN-major operand, so one
 //              layout of W serves all three)
 //   warp 1     MMA issuer and TMEM owner, two accumulators of NB columns
-//   warps 4-7  epilogue: a thread per token row
+//   warps 4-7  epilogue: a thread per token row, 64 columns at a time through
+//              shared memory to a TMA store (rows written straight from the
+//              registers, 16 bytes a lane and row, took absorb over 512
+//              tokens x 64 heads 22.1 us)
+//
+// A prompt's expansion runs on CTA pairs (expand_pair_kernel, below).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
-#include "tc_ptx.cuh"
+#include "tc_pair.cuh"
 
 namespace cpattn {
 namespace {
@@ -34,6 +39,8 @@ constexpr int kHeadRows = 256;  // W rows per head
 constexpr int kKeyDims = 128;   // W rows of the key part; the value part follows
 constexpr int kRope = 64;
 constexpr int kThreads = 256;
+
+constexpr int kOutBytes = BM * 128;  // an output piece: 128 tokens x 64 columns
 
 enum Mode { kExpand = 0, kAbsorb = 1, kProject = 2 };
 
@@ -48,7 +55,7 @@ struct Cfg {
   static constexpr int kBBytes = NB * kStageK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes > 6 ? 6 : 196608 / kStageBytes;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static constexpr int kSmem = kStages * kStageBytes + 2 * kOutBytes + 1024;
   static constexpr int kTmemCols = 2 * NB < 32 ? 32 : 2 * NB;
 };
 
@@ -72,6 +79,40 @@ __device__ void report_timeout(unsigned* status, unsigned site, volatile int* ab
   }
 }
 
+// NB columns of an accumulator to the output by the four epilogue warps:
+// 64 columns at a time, bf16, through two staging pieces in turn to a TMA
+// store at columns col0 on (rows past the last token fall outside the map).
+template <int NB>
+__device__ __forceinline__ void store_columns(uint32_t acc, uint8_t* stage, int row, int& pieces, const CUtensorMap* map,
+                                              int col0, int h, int tok0, int n_tokens) {
+#pragma unroll 1
+  for (int c = 0; c < NB / 64; ++c, ++pieces) {
+    uint8_t* buf = stage + (pieces & 1) * kOutBytes;
+    uint32_t r[2][32];
+    tmem_ld32(acc + c * 64, r[0]);
+    tmem_ld32(acc + c * 64 + 32, r[1]);
+    if (row == 0) tma_store_wait_read<1>();  // the store that used this piece before has read it
+    named_bar_sync(1, 128);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t* x = r[k >> 2] + 8 * (k & 3);
+      uint4 w;
+      w.x = pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+      w.y = pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+      w.z = pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5]));
+      w.w = pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7]));
+      *reinterpret_cast<uint4*>(buf + row * 128 + ((k ^ (row & 7)) << 4)) = w;
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(2, 128);
+    if (row == 0) {
+      if (tok0 < n_tokens) tma_store_3d(map, smem_u32(buf), col0 + c * 64, h, tok0);
+      tma_store_commit();
+    }
+  }
+}
+
 struct Item {
   int tile, h, nb;
 };
@@ -88,7 +129,7 @@ __device__ __forceinline__ Item item_of(int i, int H) {
 template <int MODE, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
-                       const Params p) {
+                       const __grid_constant__ CUtensorMap omap, const Params p) {
   using C = Cfg<MODE, NB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -116,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&amap);
     prefetch_tmap(&wmap);
+    prefetch_tmap(&omap);
   }
   tc_fence_before();
   __syncthreads();
@@ -203,45 +245,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
-    int n = 0;
+    uint8_t* stage = smem + C::kStages * C::kStageBytes;
+    int n = 0, pieces = 0;
     for (int i = blockIdx.x; i < p.n_items; i += gridDim.x, ++n) {
       const Item it = item_of<C>(i, p.H);
       const int acc = n & 1;
       const long long tok = (long long)it.tile * BM + row;
-      const bool valid = tok < p.n_tokens;
-      constexpr int ld = MODE == kExpand ? kHeadRows : MODE == kAbsorb ? kLatent + kRope : kKeyDims;
-      __nv_bfloat16* dst = p.out + (tok * p.H + it.h) * ld + it.nb * NB;
-      if (MODE == kAbsorb && it.nb == 0 && valid) {
+      if (MODE == kAbsorb && it.nb == 0 && tok < p.n_tokens) {  // the rotated part
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (tok * p.H + it.h) * (kKeyDims + kRope) + kKeyDims);
-        uint4* d = reinterpret_cast<uint4*>(dst + kLatent);
+        uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * p.H + it.h) * (kLatent + kRope) + kLatent);
 #pragma unroll
-        for (int c = 0; c < kRope / 8; ++c) d[c] = __ldg(src + c);
+        for (int c = 0; c < kRope / 8; ++c) dst[c] = __ldg(src + c);
       }
-      if (!wait_all(smem_u32(&bar_acc[acc]), (n / 2) & 1)) {
-        if (lane == 0) report_timeout(p.status, 4, &abort_flag);
+      // the four warps leave together: one that gave up meets the others here
+      const bool got = wait_all(smem_u32(&bar_acc[acc]), (n / 2) & 1);
+      if (bar_red_or(3, 128, !got)) {
+        if (!got && lane == 0) report_timeout(p.status, 4, &abort_flag);
         break;
       }
       tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < NB / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(lane_addr + acc * NB + c * 32, r);
-        tmem_ld_wait();
-        if (valid) {
-#pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(r[8 * v4 + 0]), __uint_as_float(r[8 * v4 + 1]));
-            w.y = pack_bf16x2(__uint_as_float(r[8 * v4 + 2]), __uint_as_float(r[8 * v4 + 3]));
-            w.z = pack_bf16x2(__uint_as_float(r[8 * v4 + 4]), __uint_as_float(r[8 * v4 + 5]));
-            w.w = pack_bf16x2(__uint_as_float(r[8 * v4 + 6]), __uint_as_float(r[8 * v4 + 7]));
-            reinterpret_cast<uint4*>(dst + c * 32)[v4] = w;
-          }
-        }
-      }
+      store_columns<NB>(lane_addr + acc * NB, stage, row, pieces, &omap, it.nb * NB, it.h, it.tile * BM,
+                        p.n_tokens);
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_free[acc]));
     }
+    if (row == 0) tma_store_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -249,8 +277,193 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// ---------------------------------------------------------------- expansion of a prompt
+//
+// A pair of CTAs holds 256 tokens' latent rows in shared memory (128 x 512
+// each) and takes heads one after another: M = 256 tokens, N = 256 columns of
+// the head, K = 512 streamed as eight [256 x 64] pieces of W, half of each in
+// either CTA.  So a CTA reads 16 KB of W for 512 clk of products (32 B/clk
+// through its L2 port; a single CTA's 128 x 256 tile reads 96).  Pairs take
+// contiguous runs of (token tile, head) items; a new tile's rows are loaded
+// piece by piece as the last head's products release the old ones.
+constexpr int kPieces = kLatent / 64;
+constexpr int kPieceBytes = BM * 128;  // 128 rows x 64 columns, of tokens or of W
+constexpr int kWStages = 4;
+constexpr int kExpandSmem = (kPieces + kWStages) * kPieceBytes + 2 * kOutBytes + 1024;
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expand_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap omap, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sW = smem + kPieces * kPieceBytes;
+  // bar_a[k], bar_w[s]: piece k of the tokens, the W piece in stage s landed in
+  // both CTAs (both halves' bytes count in the even CTA, which issues the
+  // products).  bar_afree, bar_wfree: read by the products (in both CTAs).
+  __shared__ __align__(8) uint64_t bar_a[kPieces], bar_afree[kPieces], bar_w[kWStages], bar_wfree[kWStages];
+  __shared__ __align__(8) uint64_t bar_acc[2], bar_free[2], bar_drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag, zero_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = (int)cluster_ctarank();
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  const int first = (int)((long long)p.n_items * pair / pairs), last = (int)((long long)p.n_items * (pair + 1) / pairs);
+
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kPieces; ++k) {
+      mbar_init(smem_u32(&bar_a[k]), 1);
+      mbar_init(smem_u32(&bar_afree[k]), 1);
+    }
+    for (int s = 0; s < kWStages; ++s) {
+      mbar_init(smem_u32(&bar_w[s]), 1);
+      mbar_init(smem_u32(&bar_wfree[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&bar_acc[a]), 1);
+      mbar_init(smem_u32(&bar_free[a]), 2 * 4);  // the epilogue warps of both CTAs
+    }
+    mbar_init(smem_u32(&bar_drain), 1);
+    abort_flag = 0;
+    zero_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&amap);
+    prefetch_tmap(&wmap);
+    prefetch_tmap(&omap);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag)) != 0;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    int g = 0, tiles = 0, tile = -1;
+    bool ok = true;
+    for (int i = first; i < last && ok; ++i) {
+      const int h = i % p.H;
+      const bool fresh = i / p.H != tile;
+      tile = i / p.H;
+      for (int k = 0; k < kPieces && ok; ++k, ++g) {
+        if (fresh) {
+          if (tiles > 0) ok = wait_all(&bar_afree[k], (tiles - 1) & 1);
+          if (!ok) break;
+          if (elect_one()) {
+            if (cta == 0) mbar_expect_tx(smem_u32(&bar_a[k]), 2 * kPieceBytes);
+            tma_load_2d_pair(smem_u32(sA + k * kPieceBytes), &amap, k * 64, tile * 2 * BM + cta * BM,
+                             map_to_rank(smem_u32(&bar_a[k]), 0));
+          }
+          __syncwarp();
+        }
+        const int s = g % kWStages;
+        if (g >= kWStages) ok = wait_all(&bar_wfree[s], (g / kWStages - 1) & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          if (cta == 0) mbar_expect_tx(smem_u32(&bar_w[s]), 2 * kPieceBytes);
+          tma_load_2d_pair(smem_u32(sW + s * kPieceBytes), &wmap, k * 64, h * kHeadRows + cta * 128,
+                           map_to_rank(smem_u32(&bar_w[s]), 0));
+        }
+        __syncwarp();
+      }
+      if (fresh) ++tiles;
+    }
+    if (!ok && lane == 0) report_timeout(p.status, 11, &abort_flag);
+    // Never leave with a copy in flight: the products of the last stages waited
+    // for both halves, and the CTAs leave together (a barrier of the cluster
+    // after the issuer has drained).  Where a wait ran out, wait here too.
+    if (!ok && cta == 0) {
+      for (int k = max(0, g - kWStages); k < g; ++k)
+        mbar_wait(smem_u32(&bar_w[k % kWStages]), (k / kWStages) & 1, 100000000ull, &zero_flag);
+      __syncwarp();
+    }
+  } else if (warp == 1 && cta == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id = idesc_bf16_f32(2 * BM, kHeadRows, 0, 0);
+    const uint64_t dA = smem_desc(smem_u32(sA), 16, 1024), dW = smem_desc(smem_u32(sW), 16, 1024);
+    int g = 0, n = 0, tiles = 0, tile = -1;
+    unsigned bad = 0;
+    for (int i = first; i < last && !bad; ++i, ++n) {
+      const int acc = n & 1;
+      const bool fresh = i / p.H != tile;
+      tile = i / p.H;
+      const bool leave = i + 1 < last && (i + 1) / p.H != tile;  // this tile's last head here
+      if (n >= 2 && !wait_all(&bar_free[acc], (n / 2 - 1) & 1)) bad = 12;
+      for (int k = 0; k < kPieces && !bad; ++k, ++g) {
+        const int s = g % kWStages;
+        if (fresh && !wait_all(&bar_a[k], tiles & 1)) bad = 13;
+        if (!bad && !wait_all(&bar_w[s], (g / kWStages) & 1)) bad = 14;
+        if (bad) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_pair(tmem + acc * kHeadRows, dA + (uint64_t)((k * kPieceBytes + kk * 32) >> 4),
+                        dW + (uint64_t)((s * kPieceBytes + kk * 32) >> 4), id, (k > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_pair(smem_u32(&bar_wfree[s]));
+          if (leave) mma_commit_pair(smem_u32(&bar_afree[k]));
+          if (k == kPieces - 1) mma_commit_pair(smem_u32(&bar_acc[acc]));
+        }
+        __syncwarp();
+      }
+      if (fresh) ++tiles;
+    }
+    if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
+    if (elect_one()) mma_commit_pair(smem_u32(&bar_drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+    uint8_t* stage = sW + kWStages * kPieceBytes;
+    int n = 0, pieces = 0;
+    for (int i = first; i < last; ++i, ++n) {
+      const int acc = n & 1, tile = i / p.H;
+      const bool got = wait_all(&bar_acc[acc], (n / 2) & 1);
+      if (bar_red_or(3, 128, !got)) {
+        if (!got && lane == 0) report_timeout(p.status, 15, &abort_flag);
+        break;
+      }
+      tc_fence_after();
+      store_columns<kHeadRows>(lane_addr + acc * kHeadRows, stage, row, pieces, &omap, 0, i - tile * p.H,
+                               tile * 2 * BM + cta * BM, p.n_tokens);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&bar_free[acc]), 0));
+    }
+    if (row == 0) tma_store_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while products read its memory
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+cudaError_t launch_expand_pair(const CUtensorMap& am, const CUtensorMap& wm, const CUtensorMap& om, Params p, int sms,
+                               cudaStream_t s) {
+  const long long items = (long long)((p.n_tokens + 2 * BM - 1) / (2 * BM)) * p.H;
+  if (items > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  p.n_items = (int)items;
+  cudaError_t e = cudaFuncSetAttribute(expand_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = (int)(items < sms / 2 ? items : sms / 2);
+  expand_pair_kernel<<<2 * pairs, kThreads, kExpandSmem, s>>>(am, wm, om, p);
+  return cudaGetLastError();
+}
+
 template <int MODE, int NB>
-cudaError_t launch(const CUtensorMap& am, const CUtensorMap& wm, Params p, int sms, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& am, const CUtensorMap& wm, const CUtensorMap& om, Params p, int sms,
+                   cudaStream_t s) {
   using C = Cfg<MODE, NB>;
   const long long items = (long long)((p.n_tokens + BM - 1) / BM) * p.H * C::kNBlocks;
   if (items > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
@@ -259,7 +472,7 @@ cudaError_t launch(const CUtensorMap& am, const CUtensorMap& wm, Params p, int s
                                        C::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = (int)(items < sms ? items : sms);
-  mla_product_kernel<MODE, NB><<<grid, kThreads, C::kSmem, s>>>(am, wm, p);
+  mla_product_kernel<MODE, NB><<<grid, kThreads, C::kSmem, s>>>(am, wm, om, p);
   return cudaGetLastError();
 }
 
@@ -291,13 +504,16 @@ cudaError_t launch_mla_expand(const void* latent, long long stride, const void* 
   Params p = {H, 0, T, static_cast<__nv_bfloat16*>(kv), nullptr, device_status_ptr(), wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
-  CUtensorMap am, wm;
+  CUtensorMap am, wm, om;
   const uint64_t dims[2] = {kLatent, (uint64_t)T};
   const uint64_t strides[1] = {(uint64_t)stride * 2};
   const uint32_t box[2] = {64, BM};
   if (!encode_tensor_map_bf16(&am, latent, 2, dims, strides, box)) return cudaErrorInvalidValue;
-  if (!weight_map(&wm, w, H, 256)) return cudaErrorInvalidValue;
-  return launch<kExpand, 256>(am, wm, p, sms, s);
+  if (!weight_map(&wm, w, H, 128) || !token_map(&om, kv, T, H, kHeadRows)) return cudaErrorInvalidValue;
+  // Pairs where every one of them has a few (256 tokens, head) items.
+  const long long items = (long long)((T + 2 * BM - 1) / (2 * BM)) * H;
+  if (items >= 2 * (sms / 2)) return launch_expand_pair(am, wm, om, p, sms, s);
+  return launch<kExpand, 128>(am, wm, om, p, sms, s);
 }
 
 cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s) {
@@ -305,18 +521,21 @@ cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* 
               wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
-  CUtensorMap am, wm;
-  if (!token_map(&am, q, n, H, kKeyDims + kRope) || !weight_map(&wm, w, H, kKeyDims)) return cudaErrorInvalidValue;
-  return launch<kAbsorb, 256>(am, wm, p, sms, s);
+  CUtensorMap am, wm, om;
+  if (!token_map(&am, q, n, H, kKeyDims + kRope) || !weight_map(&wm, w, H, kKeyDims) ||
+      !token_map(&om, ql, n, H, kLatent + kRope))
+    return cudaErrorInvalidValue;
+  return launch<kAbsorb, 256>(am, wm, om, p, sms, s);
 }
 
 cudaError_t launch_mla_project(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s) {
   Params p = {H, 0, n, static_cast<__nv_bfloat16*>(o), nullptr, device_status_ptr(), wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
-  CUtensorMap am, wm;
-  if (!token_map(&am, ol, n, H, kLatent) || !weight_map(&wm, w, H, 128)) return cudaErrorInvalidValue;
-  return launch<kProject, 128>(am, wm, p, sms, s);
+  CUtensorMap am, wm, om;
+  if (!token_map(&am, ol, n, H, kLatent) || !weight_map(&wm, w, H, 128) || !token_map(&om, o, n, H, kKeyDims))
+    return cudaErrorInvalidValue;
+  return launch<kProject, 128>(am, wm, om, p, sms, s);
 }
 
 }  // namespace cpattn
