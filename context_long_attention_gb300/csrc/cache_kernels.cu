@@ -22,40 +22,70 @@ namespace {
 //   F(L, r) = min(r, m) ceil((q + 1) / page) + max(0, r - m) ceil(q / page)
 // New pages are taken in the order of requests, then shards, then pages.
 // Every block runs the sum over the requests for itself (a few loads a
-// thread) and writes its own part of the table and the slots, so the step is
-// one launch without a barrier between blocks.
-constexpr int kSlotThreads = 512;
-constexpr int kSlotTokens = 4;  // consecutive tokens a thread
+// thread) and writes its own part, so the step is one launch without a barrier
+// between blocks; the first blocks write slots, the others table entries, so
+// neither waits for the other's loads.  The step of a decode batch is a chain of
+// latencies (launch, lengths, sum, page id, store): lengths are divided by C
+// and the page size with a multiplication.
+constexpr int kSlotThreads = 256;
+constexpr int kSlotWarps = kSlotThreads / 32;
+
+// n / d for 0 <= n < 2^31: with 2^s >= d > 2^(s-1) and m = ceil(2^(31+s) / d),
+// m d - 2^(31+s) < d <= 2^s, so n m / 2^(31+s) passes n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t m;
+  int shift, d;
+  explicit FastDiv(int div) : d(div) {
+    int s = 0;
+    while ((1ll << s) < div) ++s;
+    shift = 31 + s;
+    m = (uint32_t)(((1ull << shift) + div - 1) / div);
+  }
+  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+
+struct SlotsParams {
+  PageSlotsArgs a;
+  FastDiv by_c, by_page;
+  int tok_blocks;  // blocks that write slots; the others write table entries
+  int wide;        // a warp a pair (many pages each) instead of a thread
+};
 
 struct PageCount {
-  int q, m, small, big;  // rows and pages of a shard: q (small pages), or q + 1 (big) for the first m
+  int m, small, big;  // the first m shards hold `big` pages, the others `small`
 };
-__device__ __forceinline__ PageCount page_count(int L, int C, int page) {
+__device__ __forceinline__ PageCount page_count(const SlotsParams& p, int L) {
   PageCount c;
-  c.q = L / C;
-  c.m = L - c.q * C;
-  c.small = c.q / page + (c.q % page != 0);
-  c.big = c.q / page + 1;
+  const int q = p.by_c(L), qp = p.by_page(q);
+  c.m = L - q * p.by_c.d;
+  c.small = qp + (q != qp * p.by_page.d);
+  c.big = qp + 1;
   return c;
 }
-__device__ __forceinline__ long long pages_before(const PageCount& c, int r) {
-  return (long long)min(r, c.m) * c.big + (long long)max(0, r - c.m) * c.small;
+__device__ __forceinline__ int pages_before(const PageCount& c, int r) {
+  return min(r, c.m) * c.big + max(0, r - c.m) * c.small;
 }
 __device__ __forceinline__ int pages_of(const PageCount& c, int r) { return r < c.m ? c.big : c.small; }
+// Sums that stop at 2^31 - 1 (past every limit that they are compared with).
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, 0x7FFFFFFFu); }
 
-__global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageSlotsArgs a) {
+// VEC consecutive tokens a thread.
+template <int VEC>
+__global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const SlotsParams p) {
   extern __shared__ int32_t sm[];
+  const PageSlotsArgs& a = p.a;
   int32_t* s_cu = sm;              // [B + 1] new tokens before request b
   int32_t* s_take = sm + a.B + 1;  // [B] pages taken before request b
-  __shared__ long long w_tok[kSlotThreads / 32], w_take[kSlotThreads / 32];
-  __shared__ int w_bad[kSlotThreads / 32];
+  __shared__ uint32_t w_tok[kSlotWarps], w_take[kSlotWarps];
+  __shared__ int w_bad[kSlotWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.B, C = a.C, page = a.page_size;
+  const int pos = *a.free_pos;
 
   // running sums over the requests: a thread takes `per` consecutive ones
   const int per = (B + kSlotThreads - 1) / kSlotThreads;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-  long long tok = 0, take = 0;
+  uint32_t tok = 0, take = 0;
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
     const int L = a.ctx_len[b], n = a.new_len[b];
@@ -63,18 +93,18 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageSlot
       bad |= CP_SLOTS_BAD_LENGTH;
       continue;
     }
-    const PageCount want = page_count(L + n, C, page), have = page_count(L, C, page);
+    const PageCount want = page_count(p, L + n), have = page_count(p, L);
     if (pages_of(want, 0) > a.max_pages) bad |= CP_SLOTS_TABLE_FULL;
-    tok += n;
-    take += pages_before(want, C) - pages_before(have, C);
+    tok = sat_add(tok, n);
+    take = sat_add(take, pages_before(want, C) - pages_before(have, C));  // at most C + 2^31 / 64 pages each
   }
-  long long tok_in = tok, take_in = take;
+  uint32_t tok_in = tok, take_in = take;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, tok_in, d), y = __shfl_up_sync(0xffffffffu, take_in, d);
+    const uint32_t x = __shfl_up_sync(0xffffffffu, tok_in, d), y = __shfl_up_sync(0xffffffffu, take_in, d);
     if (lane >= d) {
-      tok_in += x;
-      take_in += y;
+      tok_in = sat_add(tok_in, x);
+      take_in = sat_add(take_in, y);
     }
   }
   bad = __reduce_or_sync(0xffffffffu, bad);
@@ -84,73 +114,72 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageSlot
     w_bad[warp] = bad;
   }
   __syncthreads();
-  long long tok0 = tok_in - tok, take0 = take_in - take, total = 0, taken = 0;
+  uint32_t before_tok = 0, before_take = 0, total = 0, taken = 0;
 #pragma unroll
-  for (int w = 0; w < kSlotThreads / 32; ++w) {
-    if (w < warp) {
-      tok0 += w_tok[w];
-      take0 += w_take[w];
+  for (int w = 0; w < kSlotWarps; ++w) {
+    if (w == warp) {
+      before_tok = total;
+      before_take = taken;
     }
-    total += w_tok[w];
-    taken += w_take[w];
+    total = sat_add(total, w_tok[w]);
+    taken = sat_add(taken, w_take[w]);
     bad |= w_bad[w];
   }
-  const int pos = *a.free_pos;
-  if (pos < 0 || pos > a.n_free || taken > a.n_free - pos) bad |= CP_SLOTS_NO_PAGES;
-  if (total > a.max_tokens) bad |= CP_SLOTS_TOO_MANY;
-  if (blockIdx.x == 0 && tid == 0) {
-    a.info[0] = bad;
-    a.info[1] = bad ? pos : pos + (int)taken;
-    a.info[2] = bad ? 0 : (int)taken;
-    a.info[3] = bad ? 0 : (int)total;
-  }
+  if (pos < 0 || pos > a.n_free || taken > (uint32_t)(a.n_free - pos)) bad |= CP_SLOTS_NO_PAGES;
+  if (total > (uint32_t)a.max_tokens) bad |= CP_SLOTS_TOO_MANY;
+  if (blockIdx.x == 0 && tid == 0)
+    *reinterpret_cast<int4*>(a.info) =
+        bad ? make_int4(bad, pos, 0, 0) : make_int4(0, pos + (int)taken, (int)taken, (int)total);
+  const bool tokens = blockIdx.x < (unsigned)p.tok_blocks;
   if (bad) {  // nothing is taken: no table entry changes, no token has a slot
     for (int b = tid; b <= B && blockIdx.x == 0; b += kSlotThreads) a.cu_new[b] = 0;
-    for (long long t = (long long)blockIdx.x * kSlotThreads + tid; t < a.max_tokens;
-         t += (long long)gridDim.x * kSlotThreads)
+    for (long long t = (long long)blockIdx.x * kSlotThreads + tid; tokens && t < a.max_tokens;
+         t += (long long)p.tok_blocks * kSlotThreads)
       a.slots[t] = -1;
     return;
   }
+  // nothing saturated: every sum is at most n_free or max_tokens
+  int tok0 = (int)(before_tok + tok_in - tok), take0 = (int)(before_take + take_in - take);
   for (int b = b0; b < b1; ++b) {
     const int L = a.ctx_len[b], n = a.new_len[b];
-    s_cu[b] = (int)tok0;
-    s_take[b] = (int)take0;
+    s_cu[b] = tok0;
+    s_take[b] = take0;
+    if (blockIdx.x == 0) a.cu_new[b] = tok0;
+    if (b + 1 == b1) break;
     tok0 += n;
-    take0 += pages_before(page_count(L + n, C, page), C) - pages_before(page_count(L, C, page), C);
+    take0 += pages_before(page_count(p, L + n), C) - pages_before(page_count(p, L), C);
   }
-  if (tid == 0) s_cu[B] = (int)total;
+  if (tid == 0) {
+    s_cu[B] = (int)total;
+    if (blockIdx.x == 0) a.cu_new[B] = (int)total;
+  }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= B; b += kSlotThreads) a.cu_new[b] = s_cu[b];
 
-  auto id_of = [&](long long i) {  // a page id of the free list, -1 if it names no page
+  auto id_of = [&](int i) {  // a page id of the free list, -1 if it names no page
     const int id = a.free_ids[i];
     return id >= 0 && id < a.num_pages ? id : -1;
   };
-  // new table entries: a warp per (request, shard) pair where the grid has
-  // warps enough (few pairs with many pages each), else a thread per pair
-  {
-    const int pairs = B * C;
-    const int warps = gridDim.x * (kSlotThreads / 32);
-    const bool wide = pairs <= warps;
-    const int step = wide ? 32 : 1, off = wide ? lane : 0;
-    const int first = wide ? warp * gridDim.x + blockIdx.x : blockIdx.x * kSlotThreads + tid;
-    const int stride = wide ? warps : gridDim.x * kSlotThreads;
+  if (!tokens) {
+    // new table entries of the (request, shard) pairs
+    const int pairs = B * C, block = blockIdx.x - p.tok_blocks, blocks = gridDim.x - p.tok_blocks;
+    const int step = p.wide ? 32 : 1, off = p.wide ? lane : 0;
+    const int first = p.wide ? warp * blocks + block : block * kSlotThreads + tid;
+    const int stride = p.wide ? blocks * kSlotWarps : blocks * kSlotThreads;
     for (int u = first; u < pairs; u += stride) {
-      const int b = u / C, r = u - b * C;
+      const int b = p.by_c(u), r = u - b * C;
       const int L = a.ctx_len[b], n = a.new_len[b];
       if (n == 0) continue;
-      const PageCount want = page_count(L + n, C, page), have = page_count(L, C, page);
+      const PageCount want = page_count(p, L + n), have = page_count(p, L);
       const int h0 = pages_of(have, r), h1 = pages_of(want, r);
-      const long long src = (long long)pos + s_take[b] + pages_before(want, r) - pages_before(have, r) - h0;
+      const int src = pos + s_take[b] + pages_before(want, r) - pages_before(have, r) - h0;
       int32_t* row = a.table + ((long long)r * B + b) * a.max_pages;
       for (int i = h0 + off; i < h1; i += step) row[i] = id_of(src + i);
     }
+    return;
   }
-  // slots: four consecutive tokens a thread
-  const long long stride = (long long)gridDim.x * kSlotThreads * kSlotTokens;
-  for (long long t0 = ((long long)blockIdx.x * kSlotThreads + tid) * kSlotTokens; t0 < a.max_tokens; t0 += stride) {
-    int out[kSlotTokens];
+  const long long stride = (long long)p.tok_blocks * kSlotThreads * VEC;
+  for (long long t0 = ((long long)blockIdx.x * kSlotThreads + tid) * VEC; t0 < a.max_tokens; t0 += stride) {
+    int out[VEC];
     int lo = 0, hi = B - 1;  // the last request starting at or before t0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -160,7 +189,7 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageSlot
     PageCount want, have;
     bool fresh = true;
 #pragma unroll
-    for (int k = 0; k < kSlotTokens; ++k) {
+    for (int k = 0; k < VEC; ++k) {
       const long long t = t0 + k;
       out[k] = -1;
       if (t >= total) continue;
@@ -170,27 +199,27 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageSlot
       }
       if (fresh) {
         L = a.ctx_len[b];
-        want = page_count(s_cu[b + 1] - s_cu[b] + L, C, page);
-        have = page_count(L, C, page);
+        want = page_count(p, s_cu[b + 1] - s_cu[b] + L);
+        have = page_count(p, L);
         fresh = false;
       }
-      const int p = L + (int)(t - s_cu[b]);
-      const int i = p / C, r = p - i * C, pg = i / page;
+      const int q = L + (int)(t - s_cu[b]);
+      const int i = p.by_c(q), r = q - i * C, pg = p.by_page(i);
       const int h0 = pages_of(have, r);
       int id;
       if (pg < h0) {
         id = a.table[((long long)r * B + b) * a.max_pages + pg];
         if (id < 0 || id >= a.num_pages) id = -1;
       } else {
-        id = id_of((long long)pos + s_take[b] + pages_before(want, r) - pages_before(have, r) + pg - h0);
+        id = id_of(pos + s_take[b] + pages_before(want, r) - pages_before(have, r) + pg - h0);
       }
       if (id >= 0) out[k] = id * page + (i - pg * page);
     }
-    if (t0 + kSlotTokens <= a.max_tokens) {
-      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(out[0], out[1], out[2], out[3]);
+    if (VEC == 4 && t0 + VEC <= a.max_tokens) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(out[0], out[VEC > 1 ? 1 : 0], out[VEC > 2 ? 2 : 0], out[VEC > 3 ? 3 : 0]);
     } else {
 #pragma unroll
-      for (int k = 0; k < kSlotTokens; ++k)
+      for (int k = 0; k < VEC; ++k)
         if (t0 + k < a.max_tokens) a.slots[t0 + k] = out[k];
     }
   }
@@ -235,6 +264,13 @@ struct Piece<__nv_bfloat16> {
     const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
     return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
   }
+  // The largest magnitude, as fp32 bits, of this and `top`: magnitudes are
+  // ordered like their bits, two bf16 at a time here.
+  __device__ uint32_t top_of(uint32_t top) const {
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(x.x & k, x.y & k), __vmaxu2(x.z & k, x.w & k));
+    return max(top, max(m & 0xffff0000u, m << 16));
+  }
 };
 template <>
 struct Piece<float> {
@@ -249,6 +285,10 @@ struct Piece<float> {
     const int k = i & 3;
     return __uint_as_float(k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
   }
+  __device__ uint32_t top_of(uint32_t top) const {
+    const uint32_t k = 0x7fffffffu;
+    return max(top, max(max(max(x.x & k, x.y & k), max(x.z & k, x.w & k)), max(max(y.x & k, y.y & k), max(y.z & k, y.w & k))));
+  }
 };
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -259,12 +299,25 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // Codes of eight elements: rn_E4M3(x / scale), the quotient rounded to fp32
-// first as a division gives it.
+// first as a division gives it.  With y = 1 / scale rounded once, q = x y is
+// within two units of the quotient, x - q scale is exact in one FMA, and adding
+// it times y rounds to the quotient (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990): three operations
+// where a division is some ten (57 us instead of 35 for 32,768 tokens of 2,048 elements).
+// `plain` for scales whose products could leave the normal range.
 template <typename T>
-__device__ __forceinline__ uint2 codes_of(const Piece<T>& x, float scale) {
+__device__ __forceinline__ uint2 codes_of(const Piece<T>& x, float scale, float inv, bool plain) {
   float q[8];
+  if (plain) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x.at(i), scale);
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x.at(i), scale);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = x.at(i), q0 = v * inv;
+      q[i] = __fmaf_rn(__fmaf_rn(-q0, scale, v), inv, q0);
+    }
+  }
   return make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
@@ -286,7 +339,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const Appen
   uint2* vd = a.v ? reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_pool) + (long long)slot * a.row_elems) : nullptr;
   auto src = [&](int c) { return static_cast<const void*>(c < vec ? k + 8 * c : v + 8 * (c - vec)); };
   auto dst = [&](int c) { return c < vec ? kd + c : vd + (c - vec); };
-  float amax = 0.f;
+  uint32_t top = 0;
   Piece<T> x[PIECES ? PIECES : 1];
   if (PIECES) {
 #pragma unroll
@@ -295,30 +348,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const Appen
       if (c < all) x[i].load(src(c)); else x[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[i].at(e)));
+    for (int i = 0; i < PIECES; ++i) top = x[i].top_of(top);
   } else {
     for (int c = lane; c < all; c += 32) {
       x[0].load(src(c));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[0].at(e)));
+      top = x[0].top_of(top);
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
   const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
   if (lane == 0) a.scale_pool[slot] = scale;
+  const float inv = __frcp_rn(scale);
+  const bool plain = !(scale >= 0x1p-80f && scale <= 0x1p100f);
   if (PIECES) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int c = lane + 32 * i;
-      if (c < all) *dst(c) = codes_of(x[i], scale);
+      if (c < all) *dst(c) = codes_of(x[i], scale, inv, plain);
     }
   } else {
     for (int c = lane; c < all; c += 32) {
       x[0].load(src(c));
-      *dst(c) = codes_of(x[0], scale);
+      *dst(c) = codes_of(x[0], scale, inv, plain);
     }
   }
 }
@@ -329,6 +380,7 @@ void append_e4m3(const AppendArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)((a.n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
   if (per_lane <= 3) append_e4m3_kernel<T, 3><<<grid, kAppendThreads, 0, s>>>(a);
   else if (per_lane <= 8) append_e4m3_kernel<T, 8><<<grid, kAppendThreads, 0, s>>>(a);
+  else if (per_lane <= 16 && sizeof(T) == 2) append_e4m3_kernel<T, sizeof(T) == 2 ? 16 : 0><<<grid, kAppendThreads, 0, s>>>(a);
   else append_e4m3_kernel<T, 0><<<grid, kAppendThreads, 0, s>>>(a);
 }
 
@@ -341,16 +393,23 @@ void append_copy(const AppendArgs& a, int elem, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_page_slots(const PageSlotsArgs& a, cudaStream_t s) {
+  SlotsParams p = {a, FastDiv(a.C), FastDiv(a.page_size), 0, 0};
+  // one token a thread until the blocks fill the SMs twice, then four
+  const bool vec = a.max_tokens > 304 * kSlotThreads;
+  const long long per_block = (long long)kSlotThreads * (vec ? 4 : 1);
+  const long long tok = (a.max_tokens + per_block - 1) / per_block;
+  p.tok_blocks = (int)(tok < 1 ? 1 : tok > 608 ? 608 : tok);
+  const long long pairs = (long long)a.B * a.C;
+  p.wide = a.max_tokens > 4 * pairs * a.page_size;  // some four new pages a pair or more
+  const long long pb = p.wide ? (pairs + kSlotWarps - 1) / kSlotWarps : (pairs + kSlotThreads - 1) / kSlotThreads;
+  const unsigned grid = (unsigned)(p.tok_blocks + (pb > 152 ? 152 : pb));
   const size_t smem = (size_t)(2 * a.B + 1) * sizeof(int32_t);
+  auto kern = vec ? page_slots_kernel<4> : page_slots_kernel<1>;
   if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(page_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  const long long by_tok = ((long long)a.max_tokens + kSlotThreads * kSlotTokens - 1) / (kSlotThreads * kSlotTokens);
-  const long long by_pair = ((long long)a.B * a.C + 4 * kSlotThreads - 1) / (4 * kSlotThreads);
-  long long grid = by_tok > by_pair ? by_tok : by_pair;
-  if (grid > 304) grid = 304;
-  page_slots_kernel<<<(unsigned)grid, kSlotThreads, smem, s>>>(a);
+  kern<<<grid, kSlotThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 

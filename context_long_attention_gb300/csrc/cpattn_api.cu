@@ -1374,7 +1374,8 @@ cp_status cp_page_slots(int C, int B, const int32_t* ctx_len, const int32_t* new
   if (!ctx_len || !new_len || !page_table || !free_pos || !cu_new || !info || (n_free && !free_ids) ||
       (max_tokens && !slots))
     return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
-  if (slots && !aligned16(slots)) return fail(CP_ERR_INVALID_ARG, "slots is not 16-byte aligned");
+  if ((slots && !aligned16(slots)) || !aligned16(info))
+    return fail(CP_ERR_INVALID_ARG, "slots or info is not 16-byte aligned");
   if (free_pos >= info && free_pos < info + 4)
     return fail(CP_ERR_INVALID_ARG, "free_pos lies in this call's info: pass an earlier call's");
   const PageSlotsArgs a = {C, B, ctx_len, new_len, page_table, max_pages, page_size, num_pages,

@@ -573,6 +573,7 @@ cp_status cp_mla_prefill_attn(const void* host_plan, const void* dev_plan, int r
  *          to back; -1 past the last one.  16-byte aligned.
  *   cu_new [B + 1] int32: new tokens before request b.
  *   info   [4] int32: {status, the next free_pos, pages taken, new tokens}.
+ *          16-byte aligned.
  * The lengths are known to the GPU only, so a step that does not fit is
  * reported in info[0] as a sum of the flags below; nothing is taken then:
  * the table stays, every slot is -1, cu_new is 0 and info[1] is *free_pos.
