@@ -175,13 +175,20 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   if (PAIR && (td.q_off & (2 * MT - 1))) return;
   const cp_seg_desc sg = reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg)[td.seg];
 
-  const int rows0 = min(MT, max(0, sg.count - td.q_off));
-  const int rows1 = min(MT, max(0, sg.count - td.q_off - MT));
-  const int nkv0 = rows0 > 0 ? (sg.first_pos + (td.q_off + rows0 - 1) * sg.stride + BN) / BN : 0;
-  const int nkv1 = rows1 > 0 ? (sg.first_pos + (td.q_off + MT + rows1 - 1) * sg.stride + BN) / BN : 0;
+  // Query (from the unit's first) of row i of M tile t.  A block's queries are
+  // neighbours and the second tile reads a tile or two of keys more; an
+  // interleave run's lie C apart and it would read C / 2 tiles more all alone
+  // (a step takes as long for one M tile as for two), so the tiles take every
+  // other query.
+  const bool split = sg.stride > 1;
+  auto query = [&](int t, int i) { return split ? 2 * i + t : t * MT + i; };
+  const int n_q = min(2 * MT, sg.count - td.q_off);
+  const int rows0 = split ? (n_q + 1) / 2 : min(MT, n_q), rows1 = n_q - rows0;
+  const int nkv0 = (sg.first_pos + (td.q_off + query(0, rows0 - 1)) * sg.stride + BN) / BN;
+  const int nkv1 = rows1 > 0 ? (sg.first_pos + (td.q_off + query(1, rows1 - 1)) * sg.stride + BN) / BN : 0;
   const int nK = max(nkv0, nkv1);
   const int last_t = nkv1 > 0 ? 1 : 0;  // the tile whose products come last in every step
-  const int n_keys = sg.first_pos + (td.q_off + rows0 + rows1 - 1) * sg.stride + 1;
+  const int n_keys = sg.first_pos + (td.q_off + n_q - 1) * sg.stride + 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
@@ -253,17 +260,23 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
       tmem_ld_wait();
       return __uint_as_float(o);
     };
-    // Q row -> shared memory, 128-byte-swizzled K-major (half of its 24 pieces)
+    // this warp's 32 rows of Q, its half of their 24 16-byte pieces, to shared
+    // memory (128-byte-swizzled, K-major): neighbouring lanes read neighbouring
+    // pieces, so a row's 192 bytes come at once
     {
-      const long long f = (long long)sg.first_f + (long long)(td.q_off + t * MT + row) * sg.stride;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (f * p.H + h) * kDqk);
-      uint8_t* dst = sQ + t * kQBytes + i * 128;
+      constexpr int kHalf = kDqk / 16;
+      uint4 val[kHalf];
 #pragma unroll
-      for (int c = half * (kDqk / 16); c < (half + 1) * (kDqk / 16); ++c) {
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (valid) val = __ldg(src + c);
-        const int a = c >> 3, cc = c & 7;
-        *reinterpret_cast<uint4*>(dst + a * (BM * 128) + ((cc ^ (i & 7)) << 4)) = val;
+      for (int k = 0; k < kHalf; ++k) {
+        const int e = k * 32 + lane, r = quarter * 32 + e / kHalf, c = half * kHalf + e % kHalf;
+        const long long f = (long long)sg.first_f + (long long)(td.q_off + query(t, cta * BM + r)) * sg.stride;
+        val[k] = make_uint4(0, 0, 0, 0);
+        if (cta * BM + r < rows_t) val[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (f * p.H + h) * kDqk) + c);
+      }
+#pragma unroll
+      for (int k = 0; k < kHalf; ++k) {
+        const int e = k * 32 + lane, r = quarter * 32 + e / kHalf, c = half * kHalf + e % kHalf;
+        *reinterpret_cast<uint4*>(sQ + t * kQBytes + (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = val[k];
       }
       fence_proxy_async_smem();
       warp_arrive(&bar_q[t]);
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     const int n_t = t ? nkv1 : nkv0;
     if (n_t > 0) {
       const int my_row = min(row, rows_t - 1);  // rows past the segment run along with its last one's mask
-      const int pos = sg.first_pos + (td.q_off + t * MT + my_row) * sg.stride;
+      const int pos = sg.first_pos + (td.q_off + query(t, my_row)) * sg.stride;
       const float sl2 = p.scale_log2;
       const float thr = kRescaleLog2 / sl2;
       float m_used = -INFINITY, l = 0.f;
@@ -367,26 +380,34 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         tc_fence_after();
         const float lt = l + exchange(l);
         const float inv = 1.f / lt;
-        const long long out_row = (long long)sg.local_start + td.q_off + t * MT + row - p.row_sub;
-        __nv_bfloat16* dst = p.o + (out_row * p.H + h) * kDv + (kDv / 2) * half;
+        const long long out_row = (long long)sg.local_start + td.q_off - p.row_sub;  // the unit's first
+        // O through this tile's Q (no product reads it any more), each warp in
+        // 4 KB of its own, so that eight lanes write a row's 128 bytes together
+        uint8_t* stage = sQ + t * kQBytes + (half * 4 + quarter) * 4096;
 #pragma unroll
         for (int c = 0; c < kDv / 64; ++c) {
           uint32_t r[32];
           tmem_ld32(lane_addr + colO + c * 32, r);
           tmem_ld_wait();
-          if (valid) {
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(r[8 * v4 + 0]) * inv, __uint_as_float(r[8 * v4 + 1]) * inv);
-              w.y = pack_bf16x2(__uint_as_float(r[8 * v4 + 2]) * inv, __uint_as_float(r[8 * v4 + 3]) * inv);
-              w.z = pack_bf16x2(__uint_as_float(r[8 * v4 + 4]) * inv, __uint_as_float(r[8 * v4 + 5]) * inv);
-              w.w = pack_bf16x2(__uint_as_float(r[8 * v4 + 6]) * inv, __uint_as_float(r[8 * v4 + 7]) * inv);
-              reinterpret_cast<uint4*>(dst + c * 32)[v4] = w;
-            }
+          for (int v4 = 0; v4 < 4; ++v4) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(r[8 * v4 + 0]) * inv, __uint_as_float(r[8 * v4 + 1]) * inv);
+            w.y = pack_bf16x2(__uint_as_float(r[8 * v4 + 2]) * inv, __uint_as_float(r[8 * v4 + 3]) * inv);
+            w.z = pack_bf16x2(__uint_as_float(r[8 * v4 + 4]) * inv, __uint_as_float(r[8 * v4 + 5]) * inv);
+            w.w = pack_bf16x2(__uint_as_float(r[8 * v4 + 6]) * inv, __uint_as_float(r[8 * v4 + 7]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + v4) ^ (lane & 7)) << 4)) = w;
           }
         }
-        if (valid && half == 0) p.lse[out_row * p.H + h] = m_used * p.sm_scale + logf(lt);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3), c = lane & 7, g = cta * BM + quarter * 32 + r;
+          if (g < rows_t)
+            reinterpret_cast<uint4*>(p.o + ((out_row + query(t, g)) * p.H + h) * kDv + (kDv / 2) * half)[c] =
+                *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+        }
+        if (valid && half == 0) p.lse[(out_row + query(t, row)) * p.H + h] = m_used * p.sm_scale + logf(lt);
       } else if (ok) {
         report_timeout(p.status, 3, &abort_flag);
       }
