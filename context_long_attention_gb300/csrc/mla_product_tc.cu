@@ -11,11 +11,12 @@
 // One work item = 128 tokens (the products' M) x one head x NB of its output
 // columns (N); rows of a tile past the last token read as zeros and are never
 // written.  Persistent CTAs take items in turn:
-//   warp 0     TMA producer: stages of the tokens' [128 x 64] and the
-//              weight's [NB x 64] pieces (absorb: the whole K = 128 in one
-//              stage; its weight is read as an MN-major operand, so one
-//              layout of W serves all three)
+//   warp 0     TMA producer: stages of 64 of K, the tokens' [128 x 64] and the
+//              weight's NB x 64 (absorb reads it as an MN-major operand, so
+//              one layout of W serves all three; after a head's first columns
+//              it also loads the query's rotated part as a stage)
 //   warp 1     MMA issuer and TMEM owner, two accumulators of NB columns
+//   warp 2     absorb: the rotated part's TMA store, straight from its stage
 //   warps 4-7  epilogue: a thread per token row, 64 columns at a time through
 //              shared memory to a TMA store (rows written straight from the
 //              registers, 16 bytes a lane and row, took absorb over 512
@@ -49,10 +50,9 @@ struct Cfg {
   static constexpr int kN = MODE == kExpand ? kHeadRows : MODE == kAbsorb ? kLatent : kKeyDims;  // columns per head
   static constexpr int kK = MODE == kAbsorb ? kKeyDims : kLatent;
   static constexpr int kNBlocks = kN / NB;
-  static constexpr int kStageK = MODE == kAbsorb ? kKeyDims : 64;
-  static constexpr int kIters = kK / kStageK;
-  static constexpr int kABytes = BM * kStageK * 2;
-  static constexpr int kBBytes = NB * kStageK * 2;
+  static constexpr int kIters = kK / 64;
+  static constexpr int kABytes = BM * 128;
+  static constexpr int kBBytes = NB * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes > 6 ? 6 : 196608 / kStageBytes;
   static constexpr int kSmem = kStages * kStageBytes + 2 * kOutBytes + 1024;
@@ -63,8 +63,6 @@ struct Params {
   int H;
   int n_items;  // token tiles x heads x column blocks
   int n_tokens;
-  __nv_bfloat16* out;
-  const __nv_bfloat16* q;  // absorb: the rotated part's source
   unsigned* status;
   unsigned long long wait_ns;
 };
@@ -125,6 +123,11 @@ __device__ __forceinline__ Item item_of(int i, int H) {
   it.tile = r / H;
   return it;
 }
+// Whether an item also carries the query's rotated part (64 columns as they are).
+template <int MODE>
+__device__ __forceinline__ bool rotated(const Item& it) {
+  return MODE == kAbsorb && it.nb == 0;
+}
 
 template <int MODE, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -142,7 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&bar_full[s]), 1);
-      mbar_init(smem_u32(&bar_empty[s]), 1);
+      // absorb: the issuer and warp 2 each wait for every stage and release it,
+      // so that neither misses a phase of a stage that the other one uses
+      mbar_init(smem_u32(&bar_empty[s]), MODE == kAbsorb ? 2 : 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&bar_acc[a]), 1);
@@ -173,25 +178,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
       const Item it = item_of<C>(i, p.H);
-      for (int k = 0; k < C::kIters && ok; ++k, ++g) {
+      const int stages = C::kIters + rotated<MODE>(it);
+      for (int k = 0; k < stages && ok; ++k, ++g) {
         const int s = g % C::kStages;
         if (g >= C::kStages) ok = wait_all(smem_u32(&bar_empty[s]), (g / C::kStages - 1) & 1);
         if (!ok) break;
         if (elect_one()) {
           const uint32_t full = smem_u32(&bar_full[s]);
           const uint32_t a = smem_u32(smem + s * C::kStageBytes), b = a + C::kABytes;
-          mbar_expect_tx(full, C::kStageBytes);
-          if (MODE == kExpand) {
-            tma_load_2d(a, &amap, k * 64, it.tile * BM, full);
-          } else {
+          mbar_expect_tx(full, k < C::kIters ? C::kStageBytes : C::kABytes);
+          if (MODE == kExpand) tma_load_2d(a, &amap, k * 64, it.tile * BM, full);
+          else tma_load_3d(a, &amap, k * 64, it.h, it.tile * BM, full);
+          if (MODE == kAbsorb) {  // [64 key dims x 64 latent columns] pieces
+            if (k < C::kIters) {
 #pragma unroll
-            for (int c = 0; c < C::kStageK / 64; ++c)
-              tma_load_3d(a + c * (BM * 128), &amap, k * C::kStageK + c * 64, it.h, it.tile * BM, full);
-          }
-          if (MODE == kAbsorb) {  // [128 key dims x 64 latent columns] pieces
-#pragma unroll
-            for (int c = 0; c < NB / 64; ++c)
-              tma_load_2d(b + c * (kKeyDims * 128), &wmap, it.nb * NB + c * 64, it.h * kHeadRows, full);
+              for (int c = 0; c < NB / 64; ++c)
+                tma_load_2d(b + c * 64 * 128, &wmap, it.nb * NB + c * 64, it.h * kHeadRows + k * 64, full);
+            }
           } else {  // [NB rows x 64 latent columns]
             const int row = it.h * kHeadRows + (MODE == kProject ? kKeyDims : 0) + it.nb * NB;
             tma_load_2d(b, &wmap, k * 64, row, full);
@@ -222,12 +225,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t a = smem_u32(smem + s * C::kStageBytes), b = a + C::kABytes;
         const uint64_t da = smem_desc(a, 16, 1024);
-        const uint64_t db = MODE == kAbsorb ? smem_desc(b, kKeyDims * 128, 1024) : smem_desc(b, 16, 1024);
+        const uint64_t db = MODE == kAbsorb ? smem_desc(b, 64 * 128, 1024) : smem_desc(b, 16, 1024);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < C::kStageK / 16; ++kk) {
-            const uint32_t oa = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-            const uint32_t ob = MODE == kAbsorb ? (kk * 16 * 128) >> 4 : ((kk & 3) * 32) >> 4;
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t oa = (kk * 32) >> 4;
+            const uint32_t ob = MODE == kAbsorb ? (kk * 16 * 128) >> 4 : (kk * 32) >> 4;
             mma_ss(tmem + acc * NB, da + oa, db + ob, id, (k > 0 || kk > 0) ? 1u : 0u);
           }
           mma_commit(smem_u32(&bar_empty[s]));
@@ -235,11 +238,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      if (!bad && rotated<MODE>(item_of<C>(i, p.H))) {  // warp 2's stage
+        const int s = g % C::kStages;
+        if (!wait_all(smem_u32(&bar_full[s]), (g / C::kStages) & 1)) bad = 6;
+        else if (lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));
+        __syncwarp();
+        ++g;
+      }
     }
     if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
     if (elect_one()) mma_commit(smem_u32(&bar_drain));
     __syncwarp();
     mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
+  } else if (MODE == kAbsorb && warp == 2) {
+    // ------------------------------------------------------------ rotated part
+    int g = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < p.n_items && ok; i += gridDim.x) {
+      const Item it = item_of<C>(i, p.H);
+      const int stages = C::kIters + rotated<MODE>(it);
+      for (int k = 0; k < stages && ok; ++k, ++g) {
+        const int s = g % C::kStages;
+        ok = wait_all(smem_u32(&bar_full[s]), (g / C::kStages) & 1);
+        if (ok && lane == 0) {
+          if (k == C::kIters) {
+            tma_store_3d(&omap, smem_u32(smem + s * C::kStageBytes), kLatent, it.h, it.tile * BM);
+            tma_store_commit();
+            tma_store_wait_read<0>();
+          }
+          mbar_arrive(smem_u32(&bar_empty[s]));
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) report_timeout(p.status, 5, &abort_flag);
+    if (lane == 0) tma_store_wait_all();
+    __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;
@@ -250,13 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = blockIdx.x; i < p.n_items; i += gridDim.x, ++n) {
       const Item it = item_of<C>(i, p.H);
       const int acc = n & 1;
-      const long long tok = (long long)it.tile * BM + row;
-      if (MODE == kAbsorb && it.nb == 0 && tok < p.n_tokens) {  // the rotated part
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (tok * p.H + it.h) * (kKeyDims + kRope) + kKeyDims);
-        uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * p.H + it.h) * (kLatent + kRope) + kLatent);
-#pragma unroll
-        for (int c = 0; c < kRope / 8; ++c) dst[c] = __ldg(src + c);
-      }
       // the four warps leave together: one that gave up meets the others here
       const bool got = wait_all(smem_u32(&bar_acc[acc]), (n / 2) & 1);
       if (bar_red_or(3, 128, !got)) {
@@ -501,7 +528,7 @@ int sm_count() {
 
 cudaError_t launch_mla_expand(const void* latent, long long stride, const void* w, int T, int H, void* kv,
                               cudaStream_t s) {
-  Params p = {H, 0, T, static_cast<__nv_bfloat16*>(kv), nullptr, device_status_ptr(), wait_limit_ns()};
+  Params p = {H, 0, T, device_status_ptr(), wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
   CUtensorMap am, wm, om;
@@ -517,19 +544,18 @@ cudaError_t launch_mla_expand(const void* latent, long long stride, const void* 
 }
 
 cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s) {
-  Params p = {H, 0, n, static_cast<__nv_bfloat16*>(ql), static_cast<const __nv_bfloat16*>(q), device_status_ptr(),
-              wait_limit_ns()};
+  Params p = {H, 0, n, device_status_ptr(), wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
   CUtensorMap am, wm, om;
-  if (!token_map(&am, q, n, H, kKeyDims + kRope) || !weight_map(&wm, w, H, kKeyDims) ||
+  if (!token_map(&am, q, n, H, kKeyDims + kRope) || !weight_map(&wm, w, H, 64) ||
       !token_map(&om, ql, n, H, kLatent + kRope))
     return cudaErrorInvalidValue;
-  return launch<kAbsorb, 256>(am, wm, om, p, sms, s);
+  return launch<kAbsorb, 128>(am, wm, om, p, sms, s);
 }
 
 cudaError_t launch_mla_project(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s) {
-  Params p = {H, 0, n, static_cast<__nv_bfloat16*>(o), nullptr, device_status_ptr(), wait_limit_ns()};
+  Params p = {H, 0, n, device_status_ptr(), wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
   CUtensorMap am, wm, om;
