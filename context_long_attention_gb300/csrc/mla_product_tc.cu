@@ -78,18 +78,18 @@ __device__ void report_timeout(unsigned* status, unsigned site, volatile int* ab
 }
 
 // NB columns of an accumulator to the output by the four epilogue warps:
-// 64 columns at a time, bf16, through two staging pieces in turn to a TMA
+// 64 columns at a time, bf16, through BUFS staging pieces in turn to a TMA
 // store at columns col0 on (rows past the last token fall outside the map).
-template <int NB>
+template <int NB, int BUFS>
 __device__ __forceinline__ void store_columns(uint32_t acc, uint8_t* stage, int row, int& pieces, const CUtensorMap* map,
                                               int col0, int h, int tok0, int n_tokens) {
 #pragma unroll 1
   for (int c = 0; c < NB / 64; ++c, ++pieces) {
-    uint8_t* buf = stage + (pieces & 1) * kOutBytes;
+    uint8_t* buf = stage + (pieces % BUFS) * kOutBytes;
     uint32_t r[2][32];
     tmem_ld32(acc + c * 64, r[0]);
     tmem_ld32(acc + c * 64 + 32, r[1]);
-    if (row == 0) tma_store_wait_read<1>();  // the store that used this piece before has read it
+    if (row == 0) tma_store_wait_read<BUFS - 1>();  // the store that used this piece before has read it
     named_bar_sync(1, 128);
     tmem_ld_wait();
 #pragma unroll
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      store_columns<NB>(lane_addr + acc * NB, stage, row, pieces, &omap, it.nb * NB, it.h, it.tile * BM,
+      store_columns<NB, 2>(lane_addr + acc * NB, stage, row, pieces, &omap, it.nb * NB, it.h, it.tile * BM,
                         p.n_tokens);
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_free[acc]));
@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // piece by piece as the last head's products release the old ones.
 constexpr int kPieces = kLatent / 64;
 constexpr int kPieceBytes = BM * 128;  // 128 rows x 64 columns, of tokens or of W
-constexpr int kWStages = 4;
-constexpr int kExpandSmem = (kPieces + kWStages) * kPieceBytes + 2 * kOutBytes + 1024;
+constexpr int kWStages = 5;
+constexpr int kExpandSmem = (kPieces + kWStages) * kPieceBytes + kOutBytes + 1024;
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expand_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
@@ -415,35 +415,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t id = idesc_bf16_f32(2 * BM, kHeadRows, 0, 0);
     const uint64_t dA = smem_desc(smem_u32(sA), 16, 1024), dW = smem_desc(smem_u32(sW), 16, 1024);
-    int g = 0, n = 0, tiles = 0, tile = -1;
-    unsigned bad = 0;
-    for (int i = first; i < last && !bad; ++i, ++n) {
-      const int acc = n & 1;
-      const bool fresh = i / p.H != tile;
-      tile = i / p.H;
-      const bool leave = i + 1 < last && (i + 1) / p.H != tile;  // this tile's last head here
-      if (n >= 2 && !wait_all(&bar_free[acc], (n / 2 - 1) & 1)) bad = 12;
-      for (int k = 0; k < kPieces && !bad; ++k, ++g) {
-        const int s = g % kWStages;
-        if (fresh && !wait_all(&bar_a[k], tiles & 1)) bad = 13;
-        if (!bad && !wait_all(&bar_w[s], (g / kWStages) & 1)) bad = 14;
-        if (bad) break;
-        tc_fence_after();
-        if (elect_one()) {
+    // One thread runs the loop: with four products between two waits, a wait of
+    // the whole warp is too long for the tensor pipe's queue.
+    if (lane == 0) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag);
+      };
+      unsigned bad = 0;
+      int s = 0, tiles = 0, head = first % p.H;
+      uint32_t phase = 0;  // of the W stages
+      bool fresh = true;
+      for (int n = 0; n < last - first && !bad; ++n) {
+        const int acc = n & 1;
+        const bool leave = head + 1 == p.H;  // this tile's last head
+        const uint32_t d = tmem + acc * kHeadRows;
+        if (n >= 2 && !wait(&bar_free[acc], (n / 2 - 1) & 1)) bad = 12;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          if (fresh && !bad && !wait(&bar_a[k], tiles & 1)) bad = 13;
+          if (!bad && !wait(&bar_w[s], phase)) bad = 14;
+          if (bad) break;
+          tc_fence_after();
+          const uint64_t a = dA + (uint64_t)((k * kPieceBytes) >> 4), b = dW + (uint64_t)((s * kPieceBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss_pair(tmem + acc * kHeadRows, dA + (uint64_t)((k * kPieceBytes + kk * 32) >> 4),
-                        dW + (uint64_t)((s * kPieceBytes + kk * 32) >> 4), id, (k > 0 || kk > 0) ? 1u : 0u);
+            mma_ss_pair(d, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), id, (k > 0 || kk > 0) ? 1u : 0u);
           mma_commit_pair(smem_u32(&bar_wfree[s]));
           if (leave) mma_commit_pair(smem_u32(&bar_afree[k]));
-          if (k == kPieces - 1) mma_commit_pair(smem_u32(&bar_acc[acc]));
+          if (++s == kWStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        __syncwarp();
+        if (!bad) mma_commit_pair(smem_u32(&bar_acc[acc]));
+        tiles += fresh;
+        fresh = leave;
+        head = leave ? 0 : head + 1;
       }
-      if (fresh) ++tiles;
+      if (bad) report_timeout(p.status, bad, &abort_flag);
+      mma_commit_pair(smem_u32(&bar_drain));
     }
-    if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
-    if (elect_one()) mma_commit_pair(smem_u32(&bar_drain));
     __syncwarp();
     mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
   } else if (warp >= 4) {
@@ -461,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      store_columns<kHeadRows>(lane_addr + acc * kHeadRows, stage, row, pieces, &omap, 0, i - tile * p.H,
+      store_columns<kHeadRows, 1>(lane_addr + acc * kHeadRows, stage, row, pieces, &omap, 0, i - tile * p.H,
                                tile * 2 * BM + cta * BM, p.n_tokens);
       tc_fence_before();
       __syncwarp();
