@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) report_timeout(p.status, 5, &abort_flag);
-    if (lane == 0) tma_store_wait_all();
+    if (lane == 0) tma_store_wait_read<0>();
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_free[acc]));
     }
-    if (row == 0) tma_store_wait_all();
+    if (row == 0) tma_store_wait_read<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -415,46 +415,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t id = idesc_bf16_f32(2 * BM, kHeadRows, 0, 0);
     const uint64_t dA = smem_desc(smem_u32(sA), 16, 1024), dW = smem_desc(smem_u32(sW), 16, 1024);
-    // One thread runs the loop: with four products between two waits, a wait of
-    // the whole warp is too long for the tensor pipe's queue.
-    if (lane == 0) {
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag);
-      };
-      unsigned bad = 0;
-      int s = 0, tiles = 0, head = first % p.H;
-      uint32_t phase = 0;  // of the W stages
-      bool fresh = true;
-      for (int n = 0; n < last - first && !bad; ++n) {
-        const int acc = n & 1;
-        const bool leave = head + 1 == p.H;  // this tile's last head
-        const uint32_t d = tmem + acc * kHeadRows;
-        if (n >= 2 && !wait(&bar_free[acc], (n / 2 - 1) & 1)) bad = 12;
+    unsigned bad = 0;
+    int s = 0, tiles = 0, head = first % p.H;
+    uint32_t phase = 0;  // of the W stages
+    bool fresh = true;
+    for (int n = 0; n < last - first && !bad; ++n) {
+      const int acc = n & 1;
+      const bool leave = head + 1 == p.H;  // this tile's last head
+      const uint32_t d = tmem + acc * kHeadRows;
+      if (n >= 2 && !wait_all(&bar_free[acc], (n / 2 - 1) & 1)) bad = 12;
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-          if (fresh && !bad && !wait(&bar_a[k], tiles & 1)) bad = 13;
-          if (!bad && !wait(&bar_w[s], phase)) bad = 14;
-          if (bad) break;
-          tc_fence_after();
-          const uint64_t a = dA + (uint64_t)((k * kPieceBytes) >> 4), b = dW + (uint64_t)((s * kPieceBytes) >> 4);
+      for (int k = 0; k < kPieces; ++k) {
+        if (fresh && !bad && !wait_all(&bar_a[k], tiles & 1)) bad = 13;
+        if (!bad && !wait_all(&bar_w[s], phase)) bad = 14;
+        if (bad) break;
+        tc_fence_after();
+        const uint64_t a = dA + (uint64_t)((k * kPieceBytes) >> 4), b = dW + (uint64_t)((s * kPieceBytes) >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_ss_pair(d, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), id, (k > 0 || kk > 0) ? 1u : 0u);
           mma_commit_pair(smem_u32(&bar_wfree[s]));
           if (leave) mma_commit_pair(smem_u32(&bar_afree[k]));
-          if (++s == kWStages) {
-            s = 0;
-            phase ^= 1;
-          }
+          if (k == kPieces - 1) mma_commit_pair(smem_u32(&bar_acc[acc]));
         }
-        if (!bad) mma_commit_pair(smem_u32(&bar_acc[acc]));
-        tiles += fresh;
-        fresh = leave;
-        head = leave ? 0 : head + 1;
+        __syncwarp();
+        if (++s == kWStages) {
+          s = 0;
+          phase ^= 1;
+        }
       }
-      if (bad) report_timeout(p.status, bad, &abort_flag);
-      mma_commit_pair(smem_u32(&bar_drain));
+      tiles += fresh;
+      fresh = leave;
+      head = leave ? 0 : head + 1;
     }
+    if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
+    if (elect_one()) mma_commit_pair(smem_u32(&bar_drain));
     __syncwarp();
     mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
   } else if (warp >= 4) {
@@ -478,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&bar_free[acc]), 0));
     }
-    if (row == 0) tma_store_wait_all();
+    if (row == 0) tma_store_wait_read<0>();
   }
   tc_fence_before();
   __syncthreads();
