@@ -204,6 +204,10 @@ cudaError_t launch_mla_expand(const void* latent, long long stride, const void* 
                               cudaStream_t s);
 cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s);
 cudaError_t launch_mla_project(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s);
+// The same for one to kMlaSmall tokens, on the CUDA cores (mla_product_small.cu).
+constexpr int kMlaSmall = 4;
+cudaError_t launch_mla_absorb_small(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s);
+cudaError_t launch_mla_project_small(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s);
 
 // ---- pages, slots and new tokens of a paged cache (cache_kernels.cu)
 struct PageSlotsArgs {

@@ -551,6 +551,7 @@ cudaError_t launch_mla_expand(const void* latent, long long stride, const void* 
 }
 
 cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s) {
+  if (n <= kMlaSmall) return launch_mla_absorb_small(q, w, n, H, ql, s);
   Params p = {H, 0, n, device_status_ptr(), wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
@@ -562,6 +563,7 @@ cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* 
 }
 
 cudaError_t launch_mla_project(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s) {
+  if (n <= kMlaSmall) return launch_mla_project_small(ol, w, n, H, o, s);
   Params p = {H, 0, n, device_status_ptr(), wait_limit_ns()};
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
