@@ -17,10 +17,14 @@
 //              it also loads the query's rotated part as a stage)
 //   warp 1     MMA issuer and TMEM owner, two accumulators of NB columns
 //   warp 2     absorb: the rotated part's TMA store, straight from its stage
-//   warps 4-7  epilogue: a thread per token row, 64 columns at a time through
-//              shared memory to a TMA store (rows written straight from the
-//              registers, 16 bytes a lane and row, took absorb over 512
-//              tokens x 64 heads 22.1 us)
+//   warps 4-11 epilogue, two groups of four warps with every other item: a
+//              thread per token row, 64 columns at a time through shared
+//              memory to a TMA store (rows written straight from the registers,
+//              16 bytes a lane and row, took absorb over 512 tokens x 64 heads
+//              twice as long)
+// Tiles of 256 tokens (a third less weight read from the L2) are no faster:
+// project over 1,000 tokens x 64 heads 18.6 us either way, over 300 of 16 heads
+// 8.4 instead of 6.6.
 //
 // A prompt's expansion runs on CTA pairs (expand_pair_kernel, below).
 #include <cuda.h>
@@ -39,7 +43,7 @@ constexpr int kLatent = 512;
 constexpr int kHeadRows = 256;  // W rows per head
 constexpr int kKeyDims = 128;   // W rows of the key part; the value part follows
 constexpr int kRope = 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 
 constexpr int kOutBytes = BM * 128;  // an output piece: 128 tokens x 64 columns
 
@@ -56,7 +60,7 @@ struct Cfg {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes > 6 ? 6 : 196608 / kStageBytes;
   static constexpr int kSmem = kStages * kStageBytes + 2 * kOutBytes + 1024;
-  static constexpr int kTmemCols = 2 * NB < 32 ? 32 : 2 * NB;
+  static constexpr int kTmemCols = 2 * NB;
 };
 
 struct Params {
@@ -77,20 +81,20 @@ __device__ void report_timeout(unsigned* status, unsigned site, volatile int* ab
   }
 }
 
-// NB columns of an accumulator to the output by the four epilogue warps:
-// 64 columns at a time, bf16, through BUFS staging pieces in turn to a TMA
-// store at columns col0 on (rows past the last token fall outside the map).
-template <int NB, int BUFS>
-__device__ __forceinline__ void store_columns(uint32_t acc, uint8_t* stage, int row, int& pieces, const CUtensorMap* map,
-                                              int col0, int h, int tok0, int n_tokens) {
+// NB columns of an accumulator to the output by four epilogue warps: 64
+// columns at a time, bf16, through the group's staging piece to a TMA store at
+// columns col0 on (rows past the last token fall outside the map).  Named
+// barriers bar, bar + 1 are the group's.
+template <int NB>
+__device__ __forceinline__ void store_columns(uint32_t acc, uint8_t* stage, int row, const CUtensorMap* map, int col0,
+                                              int h, int tok0, int n_tokens, int bar) {
 #pragma unroll 1
-  for (int c = 0; c < NB / 64; ++c, ++pieces) {
-    uint8_t* buf = stage + (pieces % BUFS) * kOutBytes;
+  for (int c = 0; c < NB / 64; ++c) {
     uint32_t r[2][32];
     tmem_ld32(acc + c * 64, r[0]);
     tmem_ld32(acc + c * 64 + 32, r[1]);
-    if (row == 0) tma_store_wait_read<BUFS - 1>();  // the store that used this piece before has read it
-    named_bar_sync(1, 128);
+    if (row == 0) tma_store_wait_read();  // the store before this one has read the piece
+    named_bar_sync(bar, 128);
     tmem_ld_wait();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -100,12 +104,12 @@ __device__ __forceinline__ void store_columns(uint32_t acc, uint8_t* stage, int 
       w.y = pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3]));
       w.z = pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5]));
       w.w = pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7]));
-      *reinterpret_cast<uint4*>(buf + row * 128 + ((k ^ (row & 7)) << 4)) = w;
+      *reinterpret_cast<uint4*>(stage + row * 128 + ((k ^ (row & 7)) << 4)) = w;
     }
     fence_proxy_async_smem();
-    named_bar_sync(2, 128);
+    named_bar_sync(bar + 1, 128);
     if (row == 0) {
-      if (tok0 < n_tokens) tma_store_3d(map, smem_u32(buf), col0 + c * 64, h, tok0);
+      if (tok0 < n_tokens) tma_store_3d(map, smem_u32(stage), col0 + c * 64, h, tok0);
       tma_store_commit();
     }
   }
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k == C::kIters) {
             tma_store_3d(&omap, smem_u32(smem + s * C::kStageBytes), kLatent, it.h, it.tile * BM);
             tma_store_commit();
-            tma_store_wait_read<0>();
+            tma_store_wait_read();
           }
           mbar_arrive(smem_u32(&bar_empty[s]));
         }
@@ -272,31 +276,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) report_timeout(p.status, 5, &abort_flag);
-    if (lane == 0) tma_store_wait_read<0>();
+    if (lane == 0) tma_store_wait_read();
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, group = (warp >> 2) - 1;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
-    uint8_t* stage = smem + C::kStages * C::kStageBytes;
-    int n = 0, pieces = 0;
+    uint8_t* stage = smem + C::kStages * C::kStageBytes + group * kOutBytes;
+    int n = 0;
     for (int i = blockIdx.x; i < p.n_items; i += gridDim.x, ++n) {
-      const Item it = item_of<C>(i, p.H);
       const int acc = n & 1;
+      if (acc != group) continue;
+      const Item it = item_of<C>(i, p.H);
       // the four warps leave together: one that gave up meets the others here
       const bool got = wait_all(smem_u32(&bar_acc[acc]), (n / 2) & 1);
-      if (bar_red_or(3, 128, !got)) {
+      if (bar_red_or(3 + 4 * group, 128, !got)) {
         if (!got && lane == 0) report_timeout(p.status, 4, &abort_flag);
         break;
       }
       tc_fence_after();
-      store_columns<NB, 2>(lane_addr + acc * NB, stage, row, pieces, &omap, it.nb * NB, it.h, it.tile * BM,
-                        p.n_tokens);
+      store_columns<NB>(lane_addr + acc * NB, stage, row, &omap, it.nb * NB, it.h, it.tile * BM,
+                           p.n_tokens, 1 + 4 * group);
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_free[acc]));
     }
-    if (row == 0) tma_store_wait_read<0>();
+    if (row == 0) tma_store_wait_read();
   }
   tc_fence_before();
   __syncthreads();
@@ -312,13 +317,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // either CTA.  So a CTA reads 16 KB of W for 512 clk of products (32 B/clk
 // through its L2 port; a single CTA's 128 x 256 tile reads 96).  Pairs take
 // contiguous runs of (token tile, head) items; a new tile's rows are loaded
-// piece by piece as the last head's products release the old ones.
+// piece by piece as the last head's products release the old ones.  20,480
+// tokens x 32 heads: 103 us = 1,670 TFLOP/s (the library's product of this
+// shape: 99.5; single CTAs with tiles of 128 x 256: 117 to 162); bound by power
+// (0.98 of the sustained bf16 rate) and the first rows' read.
 constexpr int kPieces = kLatent / 64;
 constexpr int kPieceBytes = BM * 128;  // 128 rows x 64 columns, of tokens or of W
+constexpr int kPairThreads = 256;  // four epilogue warps: 2,800 clk an item of 4,096 clk of products
 constexpr int kWStages = 5;
 constexpr int kExpandSmem = (kPieces + kWStages) * kPieceBytes + kOutBytes + 1024;
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     expand_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap omap, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -459,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     uint8_t* stage = sW + kWStages * kPieceBytes;
-    int n = 0, pieces = 0;
+    int n = 0;
     for (int i = first; i < last; ++i, ++n) {
       const int acc = n & 1, tile = i / p.H;
       const bool got = wait_all(&bar_acc[acc], (n / 2) & 1);
@@ -468,13 +477,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      store_columns<kHeadRows, 1>(lane_addr + acc * kHeadRows, stage, row, pieces, &omap, 0, i - tile * p.H,
-                               tile * 2 * BM + cta * BM, p.n_tokens);
+      store_columns<kHeadRows>(lane_addr + acc * kHeadRows, stage, row, &omap, 0, i - tile * p.H,
+                               tile * 2 * BM + cta * BM, p.n_tokens, 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&bar_free[acc]), 0));
     }
-    if (row == 0) tma_store_wait_read<0>();
+    if (row == 0) tma_store_wait_read();
   }
   tc_fence_before();
   __syncthreads();
@@ -491,7 +500,7 @@ cudaError_t launch_expand_pair(const CUtensorMap& am, const CUtensorMap& wm, con
   cudaError_t e = cudaFuncSetAttribute(expand_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
   if (e != cudaSuccess) return e;
   const int pairs = (int)(items < sms / 2 ? items : sms / 2);
-  expand_pair_kernel<<<2 * pairs, kThreads, kExpandSmem, s>>>(am, wm, om, p);
+  expand_pair_kernel<<<2 * pairs, kPairThreads, kExpandSmem, s>>>(am, wm, om, p);
   return cudaGetLastError();
 }
 
@@ -544,9 +553,12 @@ cudaError_t launch_mla_expand(const void* latent, long long stride, const void* 
   const uint32_t box[2] = {64, BM};
   if (!encode_tensor_map_bf16(&am, latent, 2, dims, strides, box)) return cudaErrorInvalidValue;
   if (!weight_map(&wm, w, H, 128) || !token_map(&om, kv, T, H, kHeadRows)) return cudaErrorInvalidValue;
-  // Pairs where every one of them has a few (256 tokens, head) items.
+  // Pairs where some have more than one (256 tokens, head) item.  Measured (us,
+  // pairs / single CTAs of 128 x 128 tiles, any split of the items into tokens
+  // and heads): 32 items 8.2 / 6.3, 64 8.5 / 8.7, 96 11.4 / 11.4, 128 11.4 / 13.6,
+  // 456 23.2 / 32.3.
   const long long items = (long long)((T + 2 * BM - 1) / (2 * BM)) * H;
-  if (items >= 2 * (sms / 2)) return launch_expand_pair(am, wm, om, p, sms, s);
+  if (items > sms / 2) return launch_expand_pair(am, wm, om, p, sms, s);
   return launch<kExpand, 128>(am, wm, om, p, sms, s);
 }
 

@@ -88,11 +88,11 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// At most N of this thread's store groups still read their shared memory (0
-// before the block ends; the stored bytes are in place when the kernel is).
-template <int N>
+// This thread's stores have read their shared memory (needed before it is
+// written again or the block ends; the stored bytes are in place when the
+// kernel is over).
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 }  // namespace tc
