@@ -170,6 +170,15 @@ cp_status build_prefill_plan(cp_strategy strategy, int C, int R, const int32_t* 
   std::stable_sort(by_rank.begin(), by_rank.end(), [](const TileKey& a, const TileKey& b) {
     return a.rank != b.rank ? a.rank < b.rank : a.work > b.work;
   });
+  // The requests' own tiles (a call over all ranks need not keep to their
+  // segments), in the same order.
+  std::vector<TileKey> by_req;
+  for (int j = 0; j < R; ++j)
+    for (int off = 0; off < new_len[j]; off += kPrefillTileRows) {
+      const int nrow = std::min(kPrefillTileRows, new_len[j] - off);
+      by_req.push_back({{j, off}, ((long long)prefix_len[j] + off + nrow) * nrow, 0});
+    }
+  std::stable_sort(by_req.begin(), by_req.end(), [](const TileKey& a, const TileKey& b) { return a.work > b.work; });
   std::vector<int32_t> rank_tile_off(C + 1, 0);
   for (const TileKey& t : by_rank) rank_tile_off[t.rank + 1]++;
   for (int r = 0; r < C; ++r) rank_tile_off[r + 1] += rank_tile_off[r];
@@ -196,6 +205,9 @@ cp_status build_prefill_plan(cp_strategy strategy, int C, int R, const int32_t* 
   w = align4(w + 2 * n_tiles);
   h.off_rtile = w;
   w = align4(w + (C + 1) + 2 * n_tiles);
+  h.off_run = w;
+  h.n_parts = (int32_t)by_req.size();
+  w = align4(w + 2 * h.n_parts);
   h.host_words = w;
   h.off_idx = w;
   w = align4(w + (int)T);
@@ -220,6 +232,10 @@ cp_status build_prefill_plan(cp_strategy strategy, int C, int R, const int32_t* 
   for (int i = 0; i < n_tiles; ++i) {
     W[h.off_rtile + C + 1 + 2 * i] = by_rank[i].t.seg;
     W[h.off_rtile + C + 1 + 2 * i + 1] = by_rank[i].t.q_off;
+  }
+  for (int i = 0; i < h.n_parts; ++i) {
+    W[h.off_run + 2 * i] = by_req[i].t.seg;
+    W[h.off_run + 2 * i + 1] = by_req[i].t.q_off;
   }
   out->dev_words = h.dev_words;
   return CP_OK;
@@ -1346,6 +1362,7 @@ cp_status cp_mla_prefill_attn(const void* host_plan, const void* dev_plan, int r
   const int32_t* W = (const int32_t*)host_plan;
   const int n_rows = rank < 0 ? h.T : W[h.off_rank + rank + 1] - W[h.off_rank + rank];
   if (n_rows == 0) return ok();
+  if (rank < 0 && (h.off_run <= 0 || h.n_parts <= 0)) return fail(CP_ERR_INVALID_ARG, "the plan has no request tiles");
   if (!dev_plan || !q || !kv || !k_rope || !o || !lse) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
   if (!aligned16(dev_plan) || !aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o) ||
       !aligned16(lse))

@@ -11,8 +11,11 @@
 // entry, the latent part and the shared positional part).
 //
 // The work of one CTA, or of a pair of CTAs, is up to 256 (512) consecutive
-// queries of one segment for one head, as two M tiles of 128 (256) rows that
-// share every K/V tile of 128 keys; CTA c of a pair has rows 128 c ..
+// queries for one head, as two M tiles of 128 (256) rows that share every K/V
+// tile of 128 keys.  For one rank they are a segment's; a call over all ranks
+// takes the requests' tokens as they come (a short request cut into 2 C blocks,
+// or a rank's every C-th token, would leave most of a tile empty or masked) and
+// writes each row where its rank's order has it.  CTA c of a pair has rows 128 c ..
 // 128 c + 127 of each M tile, half of each K tile's keys and half of each V
 // tile's dims.  The products of a pair are issued by its even CTA
 // (cta_group::2).
@@ -81,6 +84,10 @@ struct Cfg {
 struct Params {
   const int32_t* plan;
   int off_seg;
+  int off_req, off_rank;  // all ranks: the requests, the ranks' first rows
+  int C, R;
+  int zigzag;
+  int all;        // all ranks: the tile list holds {request, first query}
   int tile_list;
   int n_tiles;
   int row_sub;
@@ -173,7 +180,17 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   const cp_tile_desc td = reinterpret_cast<const cp_tile_desc*>(p.plan + p.tile_list)[tile_i];
   // a pair takes two plan tiles, from every even one of a segment
   if (PAIR && (td.q_off & (2 * MT - 1))) return;
-  const cp_seg_desc sg = reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg)[td.seg];
+  cp_seg_desc sg;
+  if (p.all) {
+    const cp_req_desc rq = reinterpret_cast<const cp_req_desc*>(p.plan + p.off_req)[td.seg];
+    sg.count = rq.new_len;
+    sg.first_f = rq.q_base;
+    sg.stride = 1;
+    sg.first_pos = rq.prefix_len;
+    sg.kv_base = rq.kv_base;
+  } else {
+    sg = reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg)[td.seg];
+  }
 
   // Query (from the unit's first) of row i of M tile t.  A block's queries are
   // neighbours and the second tile reads a tile or two of keys more; an
@@ -285,6 +302,25 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     if (n_t > 0) {
       const int my_row = min(row, rows_t - 1);  // rows past the segment run along with its last one's mask
       const int pos = sg.first_pos + (td.q_off + query(t, my_row)) * sg.stride;
+      // the output row of this lane's query
+      int out_row;
+      {
+        const int q = td.q_off + query(t, my_row);
+        if (!p.all) {
+          out_row = sg.local_start + q - p.row_sub;
+        } else if (p.zigzag) {  // block b of 2 C, the first n mod 2 C one longer; rank b or 2 C - 1 - b
+          const int blocks = 2 * p.C, base = sg.count / blocks, rem = sg.count - base * blocks;
+          const int big = rem * (base + 1);
+          const int b = q < big ? q / (base + 1) : rem + (q - big) / base;
+          const int r = b < p.C ? b : blocks - 1 - b;
+          const cp_seg_desc* s =
+              reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg) + (r * p.R + td.seg) * 2 + (b >= p.C);
+          out_row = s->local_start + q - s->q_start;
+        } else {  // flattened token f: rank f mod C, its f / C-th row
+          const int f = sg.first_f + q;
+          out_row = p.plan[p.off_rank + f % p.C] + f / p.C;
+        }
+      }
       const float sl2 = p.scale_log2;
       const float thr = kRescaleLog2 / sl2;
       float m_used = -INFINITY, l = 0.f;
@@ -380,7 +416,6 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         tc_fence_after();
         const float lt = l + exchange(l);
         const float inv = 1.f / lt;
-        const long long out_row = (long long)sg.local_start + td.q_off - p.row_sub;  // the unit's first
         // O through this tile's Q (no product reads it any more), each warp in
         // 4 KB of its own, so that eight lanes write a row's 128 bytes together
         uint8_t* stage = sQ + t * kQBytes + (half * 4 + quarter) * 4096;
@@ -403,11 +438,12 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int r = 4 * k + (lane >> 3), c = lane & 7, g = cta * BM + quarter * 32 + r;
+          const long long to = __shfl_sync(0xffffffffu, out_row, r);
           if (g < rows_t)
-            reinterpret_cast<uint4*>(p.o + ((out_row + query(t, g)) * p.H + h) * kDv + (kDv / 2) * half)[c] =
+            reinterpret_cast<uint4*>(p.o + (to * p.H + h) * kDv + (kDv / 2) * half)[c] =
                 *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
         }
-        if (valid && half == 0) p.lse[(out_row + query(t, row)) * p.H + h] = m_used * p.sm_scale + logf(lt);
+        if (valid && half == 0) p.lse[(long long)out_row * p.H + h] = m_used * p.sm_scale + logf(lt);
       } else if (ok) {
         report_timeout(p.status, 3, &abort_flag);
       }
@@ -651,9 +687,15 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
   Params p;
   p.plan = dev_plan;
   p.off_seg = h.off_seg;
+  p.off_req = h.off_req;
+  p.off_rank = h.off_rank;
+  p.C = h.C;
+  p.R = h.R;
+  p.zigzag = h.kind == 0;
+  p.all = rank < 0;
   if (rank < 0) {
-    p.tile_list = h.off_tiles;
-    p.n_tiles = h.n_tiles;
+    p.tile_list = h.off_run;
+    p.n_tiles = h.n_parts;
     p.row_sub = 0;
   } else {
     const int32_t* rto = host_plan + h.off_rtile;
@@ -682,11 +724,12 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
   // pairs 2,541 us, single CTAs 2,704; nine ragged requests interleaved over
   // four ranks (63 quarters filled of 140), 16 heads: 196 and 129.
   const cp_seg_desc* seg = reinterpret_cast<const cp_seg_desc*>(host_plan + h.off_seg);
+  const cp_req_desc* req = reinterpret_cast<const cp_req_desc*>(host_plan + h.off_req);
   long long n128 = 0, n512 = 0;
-  for (int i = 0; i < h.n_seg; ++i) {
-    if (rank >= 0 && seg[i].rank != rank) continue;
-    n128 += (seg[i].count + 127) / 128;
-    n512 += (seg[i].count + 511) / 512;
+  for (int i = 0; i < (rank < 0 ? h.R : h.n_seg); ++i) {
+    const int count = rank < 0 ? req[i].new_len : seg[i].rank == rank ? seg[i].count : 0;
+    n128 += (count + 127) / 128;
+    n512 += (count + 511) / 512;
   }
   const bool pair = n128 >= 3 * n512;
   return pair ? launch<true>(p, kv, k_rope, rope_stride, h.KV, s) : launch<false>(p, kv, k_rope, rope_stride, h.KV, s);

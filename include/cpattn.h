@@ -101,12 +101,14 @@ typedef struct {
   int32_t off_qreq;   /* prefill, device only: int32 qreq[T] (request of the query) */
   int32_t host_words; /* words in the host part */
   int32_t dev_words;  /* words in the device plan */
-  int32_t n_parts;    /* decode: partial slots in the workspace (split pairs) */
+  int32_t n_parts;    /* prefill: number of request tiles; decode: partial slots in the workspace (split pairs) */
   int32_t tile_rows;  /* decode: KV rows per scheduling tile (work boundaries) */
   int32_t n_split;    /* decode: pairs covered by more than one work item */
   int32_t layout;     /* decode: cp_dcp_layout of the token shards */
   int32_t s_q;        /* decode: query rows per request (1, or more for MTP) */
-  int32_t off_run;    /* decode: the merged-output run table (cp_decode_attn_merged) */
+  int32_t off_run;    /* prefill: {request, first query}[n_parts], 256-query tiles of the requests
+                         (whatever their ranks), longest first; decode: the merged-output run
+                         table (cp_decode_attn_merged) */
 } cp_plan_header;
 /* Decode plans reuse the table offsets: off_tiles -> int32 [R][2]
  * {ctx_len, first token of the request in the token-ordered cache};
@@ -549,8 +551,8 @@ cp_status cp_mla_project(const void* o_lat, const void* w_kv, int N, int H, void
  * o      [rows, H, 128] bf16, lse [rows, H] fp32; rows and their order as in
  *        cp_prefill_attn.
  * A request's rows must be finite (a non-finite value row can reach the
- * outputs of up to 255 queries of its segment before it); rows of other
- * requests and past the last one are never mixed in.
+ * outputs of up to 511 queries of its request or segment before it); rows of
+ * other requests and past the last one are never mixed in.
  * ------------------------------------------------------------------------- */
 cp_status cp_mla_prefill_attn(const void* host_plan, const void* dev_plan, int rank, const void* q,
                               const void* kv, const void* k_rope, int64_t rope_stride, int H, float sm_scale,

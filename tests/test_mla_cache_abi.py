@@ -64,8 +64,23 @@ def test_prefill(cp):
     refuse(lib, INVALID, b"aligned", call(rope=ODD))
     for stride in (56, 68, -64, 1 << 40):
         refuse(lib, INVALID, b"rope_stride", call(stride=stride))
+    old = plan.host.copy()
+    old[cp._binding.HEADER_FIELDS.index("off_run")] = 0
+    refuse(lib, INVALID, b"no request tiles", call(host=old.ctypes.data_as(ctypes.c_void_p)))
     empty = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [0], [3], device=None)
     assert call(host=empty.host.ctypes.data_as(ctypes.c_void_p), dev=None, q=None) == 0  # no query: nothing to do
+
+
+@pytest.mark.parametrize("strategy,C", [(0, 1), (0, 8), (1, 3)])
+def test_request_tiles_of_a_plan(cp, strategy, C):
+    """The request tiles cover every request's new tokens once, 256 at a time,
+    most work (queries x keys of the last one) first."""
+    new, prefix = [700, 0, 1, 256, 513, 90], [5, 3, 4000, 0, 77, 0]
+    plan = cp.cp_shard_plan(strategy, C, new, prefix, device=None)
+    tiles = plan.words(plan.off_run, 2 * plan.n_parts).reshape(-1, 2)
+    assert sorted(map(tuple, tiles.tolist())) == [(j, o) for j, n in enumerate(new) for o in range(0, n, 256)]
+    work = [(prefix[j] + min(o + 256, new[j])) * min(256, new[j] - o) for j, o in tiles.tolist()]
+    assert work == sorted(work, reverse=True)
 
 
 def test_page_slots(cp):
