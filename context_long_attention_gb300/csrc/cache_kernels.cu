@@ -323,65 +323,76 @@ __device__ __forceinline__ uint2 codes_of(const Piece<T>& x, float scale, float 
 
 // Rows to E4M3 codes with one scale a token, amax / 448 (1 for a row of
 // zeros) over its K row and, where there is one, its V row: a warp a token,
-// PIECES pieces of eight elements a lane kept in registers between the
-// maximum and the codes (PIECES = 0: any row length, read twice).
-template <typename T, int PIECES>
+// PIECES pieces of eight elements of each row a lane, kept in registers between
+// the maximum and the codes (PIECES = 0: any row length, read twice).
+template <typename T, int PIECES, bool HAS_V>
 __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const AppendArgs a) {
   const long long row = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= a.n) return;
   const int slot = a.slots[row];
   if (slot < 0 || slot >= a.pool_rows) return;
-  const int vec = a.row_elems / 8, all = a.v ? 2 * vec : vec;
-  const T* k = static_cast<const T*>(a.k) + row * a.k_stride;
-  const T* v = a.v ? static_cast<const T*>(a.v) + row * a.v_stride : nullptr;
-  uint2* kd = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_pool) + (long long)slot * a.row_elems);
-  uint2* vd = a.v ? reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_pool) + (long long)slot * a.row_elems) : nullptr;
-  auto src = [&](int c) { return static_cast<const void*>(c < vec ? k + 8 * c : v + 8 * (c - vec)); };
-  auto dst = [&](int c) { return c < vec ? kd + c : vd + (c - vec); };
+  constexpr int N = PIECES ? PIECES : 1, R = HAS_V ? 2 : 1;
+  const int vec = a.row_elems / 8;
+  const T* src[R];
+  uint2* dst[R];
+  src[0] = static_cast<const T*>(a.k) + row * a.k_stride + 8 * lane;
+  dst[0] = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_pool) + (long long)slot * a.row_elems) + lane;
+  if (HAS_V) {
+    src[R - 1] = static_cast<const T*>(a.v) + row * a.v_stride + 8 * lane;
+    dst[R - 1] = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_pool) + (long long)slot * a.row_elems) + lane;
+  }
   uint32_t top = 0;
-  Piece<T> x[PIECES ? PIECES : 1];
+  Piece<T> x[R][N];
   if (PIECES) {
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int c = lane + 32 * i;
-      if (c < all) x[i].load(src(c)); else x[i].zero();
-    }
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) top = x[i].top_of(top);
+      for (int i = 0; i < N; ++i)
+        if (lane + 32 * i < vec) x[r][i].load(src[r] + 256 * i); else x[r][i].zero();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < N; ++i) top = x[r][i].top_of(top);
   } else {
-    for (int c = lane; c < all; c += 32) {
-      x[0].load(src(c));
-      top = x[0].top_of(top);
-    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      for (int c = 0; c < vec - lane; c += 32) {
+        x[r][0].load(src[r] + 8 * c);
+        top = x[r][0].top_of(top);
+      }
   }
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
   const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
   if (lane == 0) a.scale_pool[slot] = scale;
   const float inv = __frcp_rn(scale);
   const bool plain = !(scale >= 0x1p-80f && scale <= 0x1p100f);
-  if (PIECES) {
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int c = lane + 32 * i;
-      if (c < all) *dst(c) = codes_of(x[i], scale, inv, plain);
-    }
-  } else {
-    for (int c = lane; c < all; c += 32) {
-      x[0].load(src(c));
-      *dst(c) = codes_of(x[0], scale, inv, plain);
+  for (int r = 0; r < R; ++r) {
+    if (PIECES) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (lane + 32 * i < vec) dst[r][32 * i] = codes_of(x[r][i], scale, inv, plain);
+    } else {
+      for (int c = 0; c < vec - lane; c += 32) {
+        x[r][0].load(src[r] + 8 * c);
+        dst[r][c] = codes_of(x[r][0], scale, inv, plain);
+      }
     }
   }
 }
 
-template <typename T>
+template <typename T, bool HAS_V>
 void append_e4m3(const AppendArgs& a, cudaStream_t s) {
-  const int per_lane = ((a.v ? 2 : 1) * a.row_elems / 8 + 31) / 32;
+  const int per_lane = (a.row_elems / 8 + 31) / 32;
   const unsigned grid = (unsigned)((a.n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
-  if (per_lane <= 3) append_e4m3_kernel<T, 3><<<grid, kAppendThreads, 0, s>>>(a);
-  else if (per_lane <= 8) append_e4m3_kernel<T, 8><<<grid, kAppendThreads, 0, s>>>(a);
-  else if (per_lane <= 16 && sizeof(T) == 2) append_e4m3_kernel<T, sizeof(T) == 2 ? 16 : 0><<<grid, kAppendThreads, 0, s>>>(a);
-  else append_e4m3_kernel<T, 0><<<grid, kAppendThreads, 0, s>>>(a);
+  auto kern = append_e4m3_kernel<T, 0, HAS_V>;
+  if (per_lane == 1) kern = append_e4m3_kernel<T, 1, HAS_V>;
+  else if (per_lane == 2) kern = append_e4m3_kernel<T, 2, HAS_V>;
+  else if (per_lane == 3) kern = append_e4m3_kernel<T, 3, HAS_V>;
+  else if (per_lane == 4) kern = append_e4m3_kernel<T, 4, HAS_V>;
+  else if (per_lane <= 8 && sizeof(T) == 2) kern = append_e4m3_kernel<T, sizeof(T) == 2 ? 8 : 0, HAS_V>;
+  kern<<<grid, kAppendThreads, 0, s>>>(a);
 }
 
 template <int LPR>
@@ -421,9 +432,9 @@ cudaError_t launch_cache_append(const AppendArgs& a, cp_dtype src, cp_dtype pool
     else if (vec <= 16) append_copy<16>(a, elem, s);
     else append_copy<32>(a, elem, s);
   } else if (src == CP_BF16) {
-    append_e4m3<__nv_bfloat16>(a, s);
+    a.v ? append_e4m3<__nv_bfloat16, true>(a, s) : append_e4m3<__nv_bfloat16, false>(a, s);
   } else {
-    append_e4m3<float>(a, s);
+    a.v ? append_e4m3<float, true>(a, s) : append_e4m3<float, false>(a, s);
   }
   return cudaGetLastError();
 }
