@@ -229,7 +229,9 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const SlotsPar
 
 constexpr int kAppendThreads = 128;
 
-// Rows as they are: LPR lanes a row, 16-byte pieces of K then of V.
+// Rows as they are: LPR lanes a row, 16-byte pieces of K, then of V.  A
+// long row's are loaded four a lane before the first store (which may alias the
+// next load for all the compiler knows).
 template <int LPR>
 __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const AppendArgs a, int elem) {
   const int per_block = kAppendThreads / LPR;
@@ -238,17 +240,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const Appen
   if (row >= a.n) return;
   const int slot = a.slots[row];
   if (slot < 0 || slot >= a.pool_rows) return;
+  constexpr int U = LPR == 32 ? 4 : 1;  // shorter rows have a piece a lane
   const int vec = a.row_elems * elem / 16;
-  const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k) + row * a.k_stride * elem);
-  uint4* kd = static_cast<uint4*>(a.k_pool) + (long long)slot * vec;
-#pragma unroll 4
-  for (int c = lane; c < vec; c += LPR) kd[c] = k[c];
-  if (a.v) {
-    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.v) + row * a.v_stride * elem);
-    uint4* vd = static_cast<uint4*>(a.v_pool) + (long long)slot * vec;
-#pragma unroll 4
-    for (int c = lane; c < vec; c += LPR) vd[c] = v[c];
-  }
+  auto copy = [&](const void* from, long long stride, void* pool) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + row * stride * elem);
+    uint4* dst = static_cast<uint4*>(pool) + (long long)slot * vec;
+    for (int c0 = lane; c0 < vec; c0 += U * LPR) {
+      uint4 x[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c0 + i * LPR < vec) x[i] = __ldg(src + c0 + i * LPR);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c0 + i * LPR < vec) dst[c0 + i * LPR] = x[i];
+    }
+  };
+  copy(a.k, a.k_stride, a.k_pool);
+  if (a.v) copy(a.v, a.v_stride, a.v_pool);
   if (a.scale_pool && lane == 0) a.scale_pool[slot] = a.new_scale[row];
 }
 
