@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const SlotsPar
 
 constexpr int kAppendThreads = 128;
 
-// Rows as they are: LPR lanes a row, 16-byte pieces of K, then of V.  A
-// long row's are loaded four a lane before the first store (which may alias the
-// next load for all the compiler knows).
+// Rows as they are: LPR lanes a row, 16-byte pieces of K and V, loaded before
+// the first store (which may alias the next load for all the compiler knows):
+// both rows' one piece a lane where they are short, else four of K, then of V.
 template <int LPR>
 __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const AppendArgs a, int elem) {
   const int per_block = kAppendThreads / LPR;
@@ -240,24 +240,34 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const Appen
   if (row >= a.n) return;
   const int slot = a.slots[row];
   if (slot < 0 || slot >= a.pool_rows) return;
-  constexpr int U = LPR == 32 ? 4 : 1;  // shorter rows have a piece a lane
   const int vec = a.row_elems * elem / 16;
-  auto copy = [&](const void* from, long long stride, void* pool) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + row * stride * elem);
-    uint4* dst = static_cast<uint4*>(pool) + (long long)slot * vec;
-    for (int c0 = lane; c0 < vec; c0 += U * LPR) {
-      uint4 x[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (c0 + i * LPR < vec) x[i] = __ldg(src + c0 + i * LPR);
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (c0 + i * LPR < vec) dst[c0 + i * LPR] = x[i];
+  const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k) + row * a.k_stride * elem);
+  const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.v) + (a.v ? row * a.v_stride * elem : 0));
+  uint4* kd = static_cast<uint4*>(a.k_pool) + (long long)slot * vec;
+  uint4* vd = static_cast<uint4*>(a.v_pool) + (a.v ? (long long)slot * vec : 0);
+  const float scale = a.scale_pool && lane == 0 ? a.new_scale[row] : 0.f;
+  if constexpr (LPR < 32) {
+    if (lane < vec) {
+      const uint4 x = __ldg(k + lane), y = a.v ? __ldg(v + lane) : make_uint4(0, 0, 0, 0);
+      kd[lane] = x;
+      if (a.v) vd[lane] = y;
     }
-  };
-  copy(a.k, a.k_stride, a.k_pool);
-  if (a.v) copy(a.v, a.v_stride, a.v_pool);
-  if (a.scale_pool && lane == 0) a.scale_pool[slot] = a.new_scale[row];
+  } else {
+    auto copy = [&](const uint4* src, uint4* dst) {
+      for (int c0 = lane; c0 < vec; c0 += 4 * LPR) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + i * LPR < vec) x[i] = __ldg(src + c0 + i * LPR);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + i * LPR < vec) dst[c0 + i * LPR] = x[i];
+      }
+    };
+    copy(k, kd);
+    if (a.v) copy(v, vd);
+  }
+  if (a.scale_pool && lane == 0) a.scale_pool[slot] = scale;
 }
 
 // Eight elements of a row as floats.
