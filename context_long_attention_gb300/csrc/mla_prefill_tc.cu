@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   // warps arrive there from both CTAs.
   __shared__ __align__(8) uint64_t bar_k[KS], bar_v[KS], bar_rel[KS], bar_k0;
   __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2][2], bar_drain;
+  __shared__ int s_row[2][BM];  // output row of each query, -1 past the unit's last (kept here: the loop has no register to spare)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int zero_flag;
@@ -302,12 +303,11 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     if (n_t > 0) {
       const int my_row = min(row, rows_t - 1);  // rows past the segment run along with its last one's mask
       const int pos = sg.first_pos + (td.q_off + query(t, my_row)) * sg.stride;
-      // the output row of this lane's query
-      int out_row;
-      {
+      if (half == 0) {
         const int q = td.q_off + query(t, my_row);
+        int to;
         if (!p.all) {
-          out_row = sg.local_start + q - p.row_sub;
+          to = sg.local_start + q - p.row_sub;
         } else if (p.zigzag) {  // block b of 2 C, the first n mod 2 C one longer; rank b or 2 C - 1 - b
           const int blocks = 2 * p.C, base = sg.count / blocks, rem = sg.count - base * blocks;
           const int big = rem * (base + 1);
@@ -315,11 +315,12 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
           const int r = b < p.C ? b : blocks - 1 - b;
           const cp_seg_desc* s =
               reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg) + (r * p.R + td.seg) * 2 + (b >= p.C);
-          out_row = s->local_start + q - s->q_start;
+          to = s->local_start + q - s->q_start;
         } else {  // flattened token f: rank f mod C, its f / C-th row
           const int f = sg.first_f + q;
-          out_row = p.plan[p.off_rank + f % p.C] + f / p.C;
+          to = p.plan[p.off_rank + f % p.C] + f / p.C;
         }
+        s_row[t][i] = valid ? to : -1;  // read after the pair's first named barrier
       }
       const float sl2 = p.scale_log2;
       const float thr = kRescaleLog2 / sl2;
@@ -437,13 +438,14 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int r = 4 * k + (lane >> 3), c = lane & 7, g = cta * BM + quarter * 32 + r;
-          const long long to = __shfl_sync(0xffffffffu, out_row, r);
-          if (g < rows_t)
+          const int r = 4 * k + (lane >> 3), c = lane & 7;
+          const long long to = s_row[t][quarter * 32 + r];
+          if (to >= 0)
             reinterpret_cast<uint4*>(p.o + (to * p.H + h) * kDv + (kDv / 2) * half)[c] =
                 *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
         }
-        if (valid && half == 0) p.lse[(long long)out_row * p.H + h] = m_used * p.sm_scale + logf(lt);
+        const long long to = s_row[t][i];
+        if (to >= 0 && half == 0) p.lse[to * p.H + h] = m_used * p.sm_scale + logf(lt);
       } else if (ok) {
         report_timeout(p.status, 3, &abort_flag);
       }
