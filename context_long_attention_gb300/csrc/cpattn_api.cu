@@ -1369,8 +1369,9 @@ cp_status cp_mla_prefill_attn(const void* host_plan, const void* dev_plan, int r
     return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
   if (rope_stride < 64 || rope_stride % 8 || rope_stride > kMaxRowStride)
     return fail(CP_ERR_INVALID_ARG, "rope_stride=%lld: need a multiple of 8 from 64 on", (long long)rope_stride);
+  const char* stall = getenv("CPATTN_TEST_STALL");  // the test hook of cp_prefill_attn
   const cudaError_t e = launch_mla_prefill((const int32_t*)dev_plan, W, h, rank, q, kv, k_rope, rope_stride, H,
-                                           sm_scale, o, lse, (cudaStream_t)stream);
+                                           sm_scale, o, lse, stall && stall[0] == '1', (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "latent prefill kernel");
   return ok();
 }

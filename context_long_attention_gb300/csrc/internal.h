@@ -199,7 +199,7 @@ cudaError_t launch_decode_simt(const int32_t* dev_plan, const cp_plan_header& h,
 cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan, const cp_plan_header& h,
                                int rank, const void* q, const void* kv, const void* k_rope,
                                long long rope_stride, int H, float sm_scale, void* o, float* lse,
-                               cudaStream_t s);
+                               bool stall_test, cudaStream_t s);
 cudaError_t launch_mla_expand(const void* latent, long long stride, const void* w, int T, int H, void* kv,
                               cudaStream_t s);
 cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s);

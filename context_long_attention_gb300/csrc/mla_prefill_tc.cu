@@ -99,6 +99,7 @@ struct Params {
   float sm_scale, scale_log2;
   unsigned* status;
   unsigned long long wait_ns;
+  int stall_test;  // test hook: the issuer waits on a barrier that nobody arrives at yet
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
       __syncwarp();
     };
     unsigned bad = 0;
+    if (p.stall_test && !wait_all(&bar_drain, 0)) bad = 10;
     for (int t = 0; t < 2 && !bad; ++t)
       if ((t ? nkv1 : nkv0) > 0 && !wait_all(&bar_q[t], 0)) bad = 11;
     if (!bad && nK > 0) {
@@ -685,7 +687,7 @@ cudaError_t launch(const Params& p, const void* kv, const void* k_rope, long lon
 cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan, const cp_plan_header& h,
                                int rank, const void* q, const void* kv, const void* k_rope,
                                long long rope_stride, int H, float sm_scale, void* o, float* lse,
-                               cudaStream_t s) {
+                               bool stall_test, cudaStream_t s) {
   Params p;
   p.plan = dev_plan;
   p.off_seg = h.off_seg;
@@ -714,7 +716,8 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
   p.scale_log2 = sm_scale * kLog2e;
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInvalidDevice;
-  p.wait_ns = wait_limit_ns();
+  p.wait_ns = stall_test ? 50000000ull : wait_limit_ns();
+  p.stall_test = stall_test;
   const long long head_bytes = (long long)h.KV * (kNope + kDv) * 2;
   const int most = (int)std::min<long long>(H, std::max<long long>(1, kGroupBytes / head_bytes));
   const int groups = (H + most - 1) / most;

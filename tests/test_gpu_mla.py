@@ -168,9 +168,9 @@ def test_prefill(cp, strategy, C, new, prefix, H):
     check_prefill(plan, ref, new, prefix, q, kv, rope, o, lse, strategy)
 
 
-@pytest.mark.parametrize("strategy,C", [("zigzag", 3), ("interleave", 4)])
-def test_prefill_rank_by_rank(cp, strategy, C):
-    new, prefix, H = [2400, 3, 129], [65, 0, 1], 2
+@pytest.mark.parametrize("strategy,C,n", [("zigzag", 3, 2400), ("interleave", 4, 2400), ("zigzag", 1, 1050), ("interleave", 2, 2048)])
+def test_prefill_rank_by_rank(cp, strategy, C, n):
+    new, prefix, H = [n, 3, 129], [65, 0, 1], 2
     q, kv, rope = prefill_inputs(new, prefix, H, 21)
     plan, _ = make_plan(cp, strategy, C, new, prefix)
     o, lse = cp.cp_mla_prefill_attn(plan, q, kv, rope)
@@ -243,6 +243,57 @@ def test_prefill_large_sampled(cp):
         at = int(plan.rank_off[r]) + local
         close(o[at], ro, (2.0 ** -8 + 2 * e) * mean[r][1] * 1.01 + 2.0 ** -8 * np.abs(ro), f"rank {r} O")
         close(lse[at], rl, e + 8100 * 2.0 ** -24 + 2.0 ** -22 * (np.abs(rl) + 1), f"rank {r} LSE")
+
+
+@pytest.mark.parametrize("n", [300, 1100])
+def test_prefill_reports_a_wait_that_runs_out(cp, monkeypatch, n):
+    """A wait of the issuer that nothing ends (single CTAs, pairs): every wait
+    gives up in turn, the status says so and the next call is right."""
+    new, prefix, H = [n], [40], 3
+    q, kv, rope = prefill_inputs(new, prefix, H, 61)
+    plan, ref = make_plan(cp, "zigzag", 1, new, prefix)
+    cp.cp_device_error_check()
+    monkeypatch.setenv("CPATTN_TEST_STALL", "1")
+    cp.cp_mla_prefill_attn(plan, q, kv, rope)
+    with pytest.raises(cp.CpError) as e:
+        cp.cp_device_error_check()
+    assert e.value.status == -4 and "kernel 7" in str(e.value)
+    monkeypatch.delenv("CPATTN_TEST_STALL")
+    cp.cp_device_error_check()
+    o, lse = cp.cp_mla_prefill_attn(plan, q, kv, rope)
+    cp.cp_device_error_check()
+    check_prefill(plan, ref, new, prefix, q, kv, rope, o, lse, "after the timeout")
+
+
+def test_calls_on_two_streams_at_once(cp):
+    """Prefill, expansion and products of two batches side by side give what
+    they give alone."""
+    H = 8
+    w = weights(H, 3)
+    jobs = []
+    for k, (new, prefix) in enumerate((([1500, 20], [100, 0]), ([900], [333]))):
+        q, _, _ = prefill_inputs(new, prefix, H, 70 + k)
+        jobs.append((make_plan(cp, "zigzag", 2, new, prefix)[0], q, randn((sum(new) + sum(prefix), 576), 80 + k),
+                     randn((150, H, 512), 90 + k)))
+
+    def work(plan, q, lat, ol):
+        out = []
+        for _ in range(6):
+            kv = cp.cp_mla_expand(lat[:, :512], w)
+            out = [kv, *cp.cp_mla_prefill_attn(plan, q, kv, lat[:, 512:]), cp.cp_mla_absorb(q, w), cp.cp_mla_project(ol, w)]
+        return out
+
+    alone = [work(*j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    both = []
+    for s, j in zip(streams, jobs):
+        with torch.cuda.stream(s):
+            both.append(work(*j))
+    torch.cuda.synchronize()
+    cp.cp_device_error_check()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_on_a_side_stream_and_in_a_graph(cp):

@@ -311,6 +311,9 @@ def test_latent_attention_step(cp, fp8):
         ctx = [c + 1 for c in ctx]
         dplan = cp.cp_decode_plan(C, ctx, device=DEV)
         ql = cp.cp_mla_absorb(qd, w)
+        if t == 0:  # the decode checks the table's host copy, which this one does not have yet
+            with pytest.raises(ValueError, match="sync_host"):
+                cp.cp_decode_attn_paged(dplan, pages, cp.CP_DECODE_MLA, ql, pool, scale_pool=spool, sm_scale=scale)
         op, lp = cp.cp_decode_attn_paged(dplan, pages.sync_host(), cp.CP_DECODE_MLA, ql, pool, scale_pool=spool, sm_scale=scale)
         ol, _ = cp.cp_lse_merge(op, lp)
         out = cp.cp_mla_project(ol, w)
