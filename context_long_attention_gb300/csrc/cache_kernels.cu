@@ -9,6 +9,7 @@
 //   as E4M3 codes with one fp32 scale a token.
 #include <cuda_bf16.h>
 
+#include "early_launch.cuh"
 #include "internal.h"
 
 namespace cpattn {
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const SlotsPar
   __shared__ int w_bad[kSlotWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.B, C = a.C, page = a.page_size;
+  wait_for_earlier_kernels();
   const int pos = *a.free_pos;
 
   // running sums over the requests: a thread takes `per` consecutive ones
@@ -237,6 +239,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const Appen
   const int per_block = kAppendThreads / LPR;
   const long long row = (long long)blockIdx.x * per_block + threadIdx.x / LPR;
   const int lane = threadIdx.x % LPR;
+  wait_for_earlier_kernels();
   if (row >= a.n) return;
   const int slot = a.slots[row];
   if (slot < 0 || slot >= a.pool_rows) return;
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const Appen
   const float scale = a.scale_pool && lane == 0 ? a.new_scale[row] : 0.f;
   if constexpr (LPR < 32) {
     if (lane < vec) {
-      const uint4 x = __ldg(k + lane), y = a.v ? __ldg(v + lane) : make_uint4(0, 0, 0, 0);
+      const uint4 x = __ldcg(k + lane), y = a.v ? __ldcg(v + lane) : make_uint4(0, 0, 0, 0);
       kd[lane] = x;
       if (a.v) vd[lane] = y;
     }
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const Appen
         uint4 x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (c0 + i * LPR < vec) x[i] = __ldg(src + c0 + i * LPR);
+          if (c0 + i * LPR < vec) x[i] = __ldcg(src + c0 + i * LPR);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (c0 + i * LPR < vec) dst[c0 + i * LPR] = x[i];
@@ -276,7 +279,7 @@ struct Piece;
 template <>
 struct Piece<__nv_bfloat16> {
   uint4 x;
-  __device__ void load(const void* p) { x = __ldg(static_cast<const uint4*>(p)); }
+  __device__ void load(const void* p) { x = __ldcg(static_cast<const uint4*>(p)); }
   __device__ void zero() { x = make_uint4(0, 0, 0, 0); }
   __device__ float at(int i) const {
     const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
@@ -294,8 +297,8 @@ template <>
 struct Piece<float> {
   uint4 x, y;
   __device__ void load(const void* p) {
-    x = __ldg(static_cast<const uint4*>(p));
-    y = __ldg(static_cast<const uint4*>(p) + 1);
+    x = __ldcg(static_cast<const uint4*>(p));
+    y = __ldcg(static_cast<const uint4*>(p) + 1);
   }
   __device__ void zero() { x = y = make_uint4(0, 0, 0, 0); }
   __device__ float at(int i) const {
@@ -347,6 +350,7 @@ template <typename T, int PIECES, bool HAS_V>
 __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const AppendArgs a) {
   const long long row = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  wait_for_earlier_kernels();
   if (row >= a.n) return;
   const int slot = a.slots[row];
   if (slot < 0 || slot >= a.pool_rows) return;
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const Appen
 }
 
 template <typename T, bool HAS_V>
-void append_e4m3(const AppendArgs& a, cudaStream_t s) {
+cudaError_t append_e4m3(const AppendArgs& a, cudaStream_t s) {
   const int per_lane = (a.row_elems / 8 + 31) / 32;
   const unsigned grid = (unsigned)((a.n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
   auto kern = append_e4m3_kernel<T, 0, HAS_V>;
@@ -410,13 +414,14 @@ void append_e4m3(const AppendArgs& a, cudaStream_t s) {
   else if (per_lane == 3) kern = append_e4m3_kernel<T, 3, HAS_V>;
   else if (per_lane == 4) kern = append_e4m3_kernel<T, 4, HAS_V>;
   else if (per_lane <= 8 && sizeof(T) == 2) kern = append_e4m3_kernel<T, sizeof(T) == 2 ? 8 : 0, HAS_V>;
-  kern<<<grid, kAppendThreads, 0, s>>>(a);
+  return launch_early(kern, grid, kAppendThreads, 0, s, 1, a);
 }
 
 template <int LPR>
-void append_copy(const AppendArgs& a, int elem, cudaStream_t s) {
+cudaError_t append_copy(const AppendArgs& a, int elem, cudaStream_t s) {
   const int per_block = kAppendThreads / LPR;
-  append_copy_kernel<LPR><<<(unsigned)((a.n + per_block - 1) / per_block), kAppendThreads, 0, s>>>(a, elem);
+  return launch_early(append_copy_kernel<LPR>, (unsigned)((a.n + per_block - 1) / per_block), kAppendThreads, 0, s, 1, a,
+                      elem);
 }
 
 }  // namespace
@@ -438,23 +443,17 @@ cudaError_t launch_page_slots(const PageSlotsArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kern<<<grid, kSlotThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(kern, grid, kSlotThreads, smem, s, 1, p);
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a, cp_dtype src, cp_dtype pool, cudaStream_t s) {
   if (src == pool) {
     const int elem = src == CP_FP32 ? 4 : src == CP_BF16 ? 2 : 1;
     const int vec = a.row_elems * elem / 16;
-    if (vec <= 8) append_copy<8>(a, elem, s);
-    else if (vec <= 16) append_copy<16>(a, elem, s);
-    else append_copy<32>(a, elem, s);
-  } else if (src == CP_BF16) {
-    a.v ? append_e4m3<__nv_bfloat16, true>(a, s) : append_e4m3<__nv_bfloat16, false>(a, s);
-  } else {
-    a.v ? append_e4m3<float, true>(a, s) : append_e4m3<float, false>(a, s);
+    return vec <= 8 ? append_copy<8>(a, elem, s) : vec <= 16 ? append_copy<16>(a, elem, s) : append_copy<32>(a, elem, s);
   }
-  return cudaGetLastError();
+  if (src == CP_BF16) return a.v ? append_e4m3<__nv_bfloat16, true>(a, s) : append_e4m3<__nv_bfloat16, false>(a, s);
+  return a.v ? append_e4m3<float, true>(a, s) : append_e4m3<float, false>(a, s);
 }
 
 }  // namespace cpattn

@@ -1,0 +1,51 @@
+// Launches that overlap the end of the kernel before them in their stream
+// (programmatic dependent launch).
+//
+// A decode step is a chain of kernels of a few microseconds, and between two of
+// them the GPU drains one, starts the next and waits for its set-up.  A kernel
+// launched here may become resident while the one before it finishes;
+// wait_for_earlier_kernels(), before its first access to global memory, holds
+// every thread until all earlier work of the stream is complete and visible, so
+// the order of reads and writes is the ordinary one.  After any other operation
+// the launch is an ordinary one.  Measured per call, calls back to back: absorb
+// of 512 tokens x 64 heads 16.4 -> 13.8 us, project of 1,000 20.5 -> 18.4, of 37
+// 5.8 -> 5.1.
+//
+// Global reads after the wait go through the L2 (TMA, __ldcg) or are plain
+// loads: never the read-only path, which promises that nobody writes during the
+// kernel's life.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace cpattn {
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_earlier_kernels() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the next such kernel may take its place once every block has come this far
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                         unsigned cluster, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#endif
+
+}  // namespace cpattn

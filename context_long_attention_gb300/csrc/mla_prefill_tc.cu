@@ -38,6 +38,7 @@
 
 #include <algorithm>
 
+#include "early_launch.cuh"
 #include "internal.h"
 #include "tc_pair.cuh"
 
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   __shared__ volatile int abort_flag;
   __shared__ volatile int zero_flag;
 
+  wait_for_earlier_kernels();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = PAIR ? (int)cluster_ctarank() : 0;
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         const int e = k * 32 + lane, r = quarter * 32 + e / kHalf, c = half * kHalf + e % kHalf;
         const long long f = (long long)sg.first_f + (long long)(td.q_off + query(t, cta * BM + r)) * sg.stride;
         val[k] = make_uint4(0, 0, 0, 0);
-        if (cta * BM + r < rows_t) val[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (f * p.H + h) * kDqk) + c);
+        if (cta * BM + r < rows_t) val[k] = __ldcg(reinterpret_cast<const uint4*>(p.q + (f * p.H + h) * kDqk) + c);
       }
 #pragma unroll
       for (int k = 0; k < kHalf; ++k) {
@@ -667,19 +669,7 @@ cudaError_t launch(const Params& p, const void* kv, const void* k_rope, long lon
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)p.n_tiles * p.H * C::kCtas;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C::kCtas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_prefill_kernel<PAIR>, km, vm, rm, p);
+  return launch_early(mla_prefill_kernel<PAIR>, (unsigned)blocks, kThreads, C::kSmem, s, C::kCtas, km, vm, rm, p);
 }
 
 }  // namespace

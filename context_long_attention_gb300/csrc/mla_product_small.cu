@@ -13,6 +13,7 @@
 // so they take up to four (one token over 64 heads reads its 8.4 MB of weight at 3.3 TB/s, launch included).
 #include <cuda_bf16.h>
 
+#include "early_launch.cuh"
 #include "internal.h"
 
 namespace cpattn {
@@ -34,18 +35,18 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
 // a row's 128 columns (8 each), so a thread has 8 columns of 8 rows; the rows
 // are summed over the two halves of a warp and then over the warps.
 template <int NT>
-__global__ void __launch_bounds__(kThreads) absorb_small_kernel(const __nv_bfloat16* __restrict__ q,
-                                                                const __nv_bfloat16* __restrict__ w,
-                                                                __nv_bfloat16* __restrict__ out, int n, int H) {
+__global__ void __launch_bounds__(kThreads) absorb_small_kernel(const __nv_bfloat16* q, const __nv_bfloat16* w,
+                                                                __nv_bfloat16* out, int n, int H) {
   __shared__ float sq[NT][kKeyDims];
   __shared__ float red[kThreads / 32][NT][kCols];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x / (kLatent / kCols), col0 = blockIdx.x % (kLatent / kCols) * kCols;
   const int cl = tid & 15, row0 = (tid >> 4) * 8;
   const __nv_bfloat16* src = w + ((long long)h * kHeadRows + row0) * kLatent + col0 + cl * 8;
+  wait_for_earlier_kernels();
   uint4 wv[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) wv[j] = __ldg(reinterpret_cast<const uint4*>(src + j * kLatent));
+  for (int j = 0; j < 8; ++j) wv[j] = __ldcg(reinterpret_cast<const uint4*>(src + j * kLatent));
   for (int i = tid; i < NT * kKeyDims; i += kThreads) {
     const int t = i / kKeyDims, d = i % kKeyDims;
     sq[t][d] = t < n ? __bfloat162float(q[((long long)t * H + h) * (kKeyDims + kRope) + d]) : 0.f;
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) absorb_small_kernel(const __nv_bfloa
   if (col0 == 0 && tid < n * (kRope / 8)) {  // the rotated part
     const int t = tid / (kRope / 8), c = tid % (kRope / 8);
     reinterpret_cast<uint4*>(out + ((long long)t * H + h) * (kLatent + kRope) + kLatent)[c] =
-        __ldg(reinterpret_cast<const uint4*>(q + ((long long)t * H + h) * (kKeyDims + kRope) + kKeyDims) + c);
+        __ldcg(reinterpret_cast<const uint4*>(q + ((long long)t * H + h) * (kKeyDims + kRope) + kKeyDims) + c);
   }
   __syncthreads();
   float acc[NT][8];
@@ -97,24 +98,24 @@ __global__ void __launch_bounds__(kThreads) absorb_small_kernel(const __nv_bfloa
 // A block: one head's 32 value dims, four a warp; a lane has 16 of a row's 512
 // latent columns.
 template <int NT>
-__global__ void __launch_bounds__(kThreads) project_small_kernel(const __nv_bfloat16* __restrict__ ol,
-                                                                 const __nv_bfloat16* __restrict__ w,
-                                                                 __nv_bfloat16* __restrict__ out, int n, int H) {
+__global__ void __launch_bounds__(kThreads) project_small_kernel(const __nv_bfloat16* ol, const __nv_bfloat16* w,
+                                                                 __nv_bfloat16* out, int n, int H) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x / (kKeyDims / kRows), row0 = blockIdx.x % (kKeyDims / kRows) * kRows + warp * 4;
   const __nv_bfloat16* src = w + ((long long)h * kHeadRows + kKeyDims + row0) * kLatent + lane * 8;
+  wait_for_earlier_kernels();
   uint4 wv[4][2];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) wv[j][k] = __ldg(reinterpret_cast<const uint4*>(src + j * kLatent + k * 256));
+    for (int k = 0; k < 2; ++k) wv[j][k] = __ldcg(reinterpret_cast<const uint4*>(src + j * kLatent + k * 256));
   float acc[NT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     uint4 xv[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      xv[k] = t < n ? __ldg(reinterpret_cast<const uint4*>(ol + ((long long)t * H + h) * kLatent + lane * 8 + k * 256))
+      xv[k] = t < n ? __ldcg(reinterpret_cast<const uint4*>(ol + ((long long)t * H + h) * kLatent + lane * 8 + k * 256))
                     : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
@@ -150,17 +151,15 @@ __global__ void __launch_bounds__(kThreads) project_small_kernel(const __nv_bflo
 cudaError_t launch_mla_absorb_small(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s) {
   const unsigned grid = (unsigned)H * (kLatent / kCols);
   auto kern = n == 1 ? absorb_small_kernel<1> : n == 2 ? absorb_small_kernel<2> : absorb_small_kernel<kMlaSmall>;
-  kern<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(w),
-                                 static_cast<__nv_bfloat16*>(ql), n, H);
-  return cudaGetLastError();
+  return launch_early(kern, grid, kThreads, 0, s, 1, static_cast<const __nv_bfloat16*>(q),
+                      static_cast<const __nv_bfloat16*>(w), static_cast<__nv_bfloat16*>(ql), n, H);
 }
 
 cudaError_t launch_mla_project_small(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s) {
   const unsigned grid = (unsigned)H * (kKeyDims / kRows);
   auto kern = n == 1 ? project_small_kernel<1> : n == 2 ? project_small_kernel<2> : project_small_kernel<kMlaSmall>;
-  kern<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(ol), static_cast<const __nv_bfloat16*>(w),
-                                 static_cast<__nv_bfloat16*>(o), n, H);
-  return cudaGetLastError();
+  return launch_early(kern, grid, kThreads, 0, s, 1, static_cast<const __nv_bfloat16*>(ol),
+                      static_cast<const __nv_bfloat16*>(w), static_cast<__nv_bfloat16*>(o), n, H);
 }
 
 }  // namespace cpattn

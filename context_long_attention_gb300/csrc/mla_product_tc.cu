@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "early_launch.cuh"
 #include "internal.h"
 #include "tc_pair.cuh"
 
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  wait_for_earlier_kernels();
   auto wait_all = [&](uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_ns, &abort_flag));
   };
@@ -334,7 +336,7 @@ constexpr int kPairThreads = 256;  // four epilogue warps: 2,800 clk an item of 
 constexpr int kWStages = 5;
 constexpr int kExpandSmem = (kPieces + kWStages) * kPieceBytes + kOutBytes + 1024;
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     expand_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap omap, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -383,6 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  wait_for_earlier_kernels();
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag)) != 0;
   };
@@ -507,8 +510,7 @@ cudaError_t launch_expand_pair(const CUtensorMap& am, const CUtensorMap& wm, con
   cudaError_t e = cudaFuncSetAttribute(expand_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
   if (e != cudaSuccess) return e;
   const int pairs = (int)(items < sms / 2 ? items : sms / 2);
-  expand_pair_kernel<<<2 * pairs, kPairThreads, kExpandSmem, s>>>(am, wm, om, p);
-  return cudaGetLastError();
+  return launch_early(expand_pair_kernel, 2 * pairs, kPairThreads, kExpandSmem, s, 2, am, wm, om, p);
 }
 
 template <int MODE, int NB>
@@ -522,8 +524,7 @@ cudaError_t launch(const CUtensorMap& am, const CUtensorMap& wm, const CUtensorM
                                        C::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = (int)(items < sms ? items : sms);
-  mla_product_kernel<MODE, NB><<<grid, kThreads, C::kSmem, s>>>(am, wm, om, p);
-  return cudaGetLastError();
+  return launch_early(mla_product_kernel<MODE, NB>, grid, kThreads, C::kSmem, s, 1, am, wm, om, p);
 }
 
 bool weight_map(CUtensorMap* m, const void* w, int H, int box_rows) {
