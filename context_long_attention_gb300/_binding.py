@@ -143,6 +143,14 @@ class _Plan:
         self.dev = dev    # int32 device words, or None for a host-only plan
         self.header = {k: int(v) for k, v in zip(HEADER_FIELDS, host[:len(HEADER_FIELDS)])}
 
+    @property
+    def host_ptr(self) -> int:
+        """Address of the host part (looked up once for each array)."""
+        known = self.__dict__.get("_host_ptr")
+        if known is None or known[0] is not self.host:
+            known = self.__dict__["_host_ptr"] = (self.host, self.host.ctypes.data)
+        return known[1]
+
     def __getattr__(self, k):
         h = self.__dict__.get("header", {})
         if k in h:
@@ -873,7 +881,7 @@ def cp_mla_prefill_attn(plan: PrefillPlan, q, kv, k_rope, sm_scale=None, rank: i
         _need("out", out, _bf16, (rows, H, MLA_V_DIM), dev)
     lse = _new((rows, H), torch.float32, dev) if lse is None else \
         _need("lse", lse, torch.float32, (rows, H), dev)
-    _call(dev, lib.cp_mla_prefill_attn, plan.host.ctypes.data, plan.dev.data_ptr(), rank, q.data_ptr(), kv.data_ptr(),
+    _call(dev, lib.cp_mla_prefill_attn, plan.host_ptr, plan.dev.data_ptr(), rank, q.data_ptr(), kv.data_ptr(),
           rope, stride, H, sm_scale, out.data_ptr(), lse.data_ptr())
     return out, lse
 
