@@ -296,6 +296,32 @@ def test_calls_on_two_streams_at_once(cp):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_offsets_past_32_bits(cp):
+    """Tensors of more than 2^31 elements: the last request's rows are, bit for
+    bit, those of a call with that request alone."""
+    H, n, R = 128, 1000, 90
+    w = weights(H, 1)
+    lat = randn((n * R, 576), 2)
+    kv = cp.cp_mla_expand(lat[:, :512], w)
+    tail = lat[-n:]
+    assert kv.numel() > 2**31 and torch.equal(kv[-n:], cp.cp_mla_expand(tail[:, :512], w))
+    q = torch.empty((n * R, H, 192), dtype=torch.bfloat16, device=DEV)
+    for r in range(R):
+        q[r * n:(r + 1) * n] = randn((n, H, 192), 100 + r)
+    assert q.numel() > 2**31
+    plan, _ = make_plan(cp, "zigzag", 1, [n] * R, [0] * R)
+    o, lse = cp.cp_mla_prefill_attn(plan, q, kv, lat[:, 512:])
+    alone, _ = make_plan(cp, "zigzag", 1, [n], [0])
+    oa, la = cp.cp_mla_prefill_attn(alone, q[-n:], kv[-n:], tail[:, 512:])
+    cp.cp_device_error_check()
+    assert torch.equal(o[-n:], oa) and torch.equal(lse[-n:], la)
+    ql = cp.cp_mla_absorb(q[-30000:], w)
+    assert ql.numel() > 2**31 and torch.equal(ql[-n:], cp.cp_mla_absorb(q[-n:], w))
+    ol = ql[..., :512].contiguous()
+    assert torch.equal(cp.cp_mla_project(ol, w)[-n:], cp.cp_mla_project(ol[-n:], w))
+    cp.cp_device_error_check()
+
+
 def test_on_a_side_stream_and_in_a_graph(cp):
     """The calls run on the current stream, and a captured step follows its
     inputs when it is replayed."""

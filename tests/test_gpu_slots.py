@@ -247,6 +247,23 @@ def test_append_copies(cp, dtype, n, heads, dim):
         assert torch.equal(sp[at], ns[keep])
 
 
+def test_append_past_32_bits(cp):
+    """Slots whose rows lie past 2^32 bytes of the pool."""
+    rows = 8_000_000
+    pool, scales = torch.zeros((rows, 576), dtype=torch.uint8, device=DEV), torch.zeros(rows, device=DEV)
+    k = randn((5, 576), 1)
+    slots = dev([rows - 1, 0, rows - 64, rows // 2, 4_000_001])
+    cp.cp_cache_append(slots, k, pool, scale_pool=scales)
+    kc, _, sc = quantised(k, None)
+    at = slots.long()
+    assert torch.equal(pool[at], kc) and torch.equal(scales[at], sc)
+    assert int((scales != 0).sum()) == 5
+    pool16 = pool.view(torch.bfloat16)[:, :288]
+    pool16.zero_()
+    cp.cp_cache_append(slots, k[:, :288], pool16)  # a view of a wider row as the source
+    assert torch.equal(pool16[at], k[:, :288])
+
+
 def test_append_nothing(cp):
     pool = torch.ones((64, 576), dtype=torch.bfloat16, device=DEV)
     cp.cp_cache_append(torch.empty(0, **I32), torch.empty((0, 576), dtype=torch.bfloat16, device=DEV), pool)
