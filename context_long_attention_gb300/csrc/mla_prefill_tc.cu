@@ -139,8 +139,9 @@ __device__ void report_timeout(unsigned* status, unsigned site, volatile int* ab
 
 template <bool PAIR>
 __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
-    mla_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const __grid_constant__ CUtensorMap ropemap, const Params p) {
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ropemap,
+                       const Params p) {
   using C = Cfg<PAIR>;
   constexpr int KS = C::kSlots, MT = C::kRows;
   extern __shared__ uint8_t smem_raw[];
@@ -165,7 +166,9 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   // bar_q, bar_k0, bar_p are waited for by the issuer and live in its CTA;
   // warps arrive there from both CTAs.
   __shared__ __align__(8) uint64_t bar_k[KS], bar_v[KS], bar_rel[KS], bar_k0;
-  __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2][2], bar_drain;
+  // bar_ql: a tile's Q rows are in this CTA's shared memory (by TMA, or
+  // written by its eight warps); the relay passes that on to bar_q.
+  __shared__ __align__(8) uint64_t bar_ql[2], bar_q[2], bar_s[2], bar_p[2], bar_o[2][2], bar_drain;
   __shared__ int s_row[2][BM];  // output row of each query, -1 past the unit's last (kept here: the loop has no register to spare)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
@@ -219,7 +222,8 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     }
     mbar_init(smem_u32(&bar_k0), C::kCtas);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&bar_q[t]), 8 * C::kCtas);        // a tile's eight softmax warps
+      mbar_init(smem_u32(&bar_ql[t]), split ? 8 : 1);
+      mbar_init(smem_u32(&bar_q[t]), C::kCtas);
       mbar_init(smem_u32(&bar_p[t]), (8 + 1) * C::kCtas);  // and the relay
       mbar_init(smem_u32(&bar_s[t]), 1);
       for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&bar_o[t][k]), 1);
@@ -234,6 +238,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     else tmem_alloc(smem_u32(&tmem_slot), 512);
   }
   if (warp == kWarpTma && lane == 0) {
+    prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
     prefetch_tmap(&ropemap);
@@ -281,10 +286,11 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
       tmem_ld_wait();
       return __uint_as_float(o);
     };
-    // this warp's 32 rows of Q, its half of their 24 16-byte pieces, to shared
-    // memory (128-byte-swizzled, K-major): neighbouring lanes read neighbouring
-    // pieces, so a row's 192 bytes come at once
-    {
+    // An interleave run's queries lie C rows apart and come by ordinary loads
+    // (others by TMA): this warp's 32 rows of Q, its half of their 24 16-byte
+    // pieces, to shared memory (128-byte-swizzled, K-major), neighbouring lanes
+    // reading neighbouring pieces, so that a row's 192 bytes come at once.
+    if (split) {
       constexpr int kHalf = kDqk / 16;
       uint4 val[kHalf];
 #pragma unroll
@@ -300,12 +306,15 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
         *reinterpret_cast<uint4*>(sQ + t * kQBytes + (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = val[k];
       }
       fence_proxy_async_smem();
-      warp_arrive(&bar_q[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_ql[t]));
     }
     const int n_t = t ? nkv1 : nkv0;
     if (n_t > 0) {
-      const int my_row = min(row, rows_t - 1);  // rows past the segment run along with its last one's mask
-      const int pos = sg.first_pos + (td.q_off + query(t, my_row)) * sg.stride;
+      // Rows past the unit's last query see no key: what Q holds there (the
+      // next request's queries) must not choose this unit's path.
+      const int my_row = min(row, rows_t - 1);
+      const int pos = row < rows_t ? sg.first_pos + (td.q_off + query(t, row)) * sg.stride : -1;
       if (half == 0) {
         const int q = td.q_off + query(t, my_row);
         int to;
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
             mx = fmax3(mx, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
           const float mrow = fmaxf(mx, exchange(mx));
           if (j == 0) {
-            m_used = mrow;
+            m_used = pos < 0 ? 0.f : mrow;
           } else {
             const bool need = mrow > m_used + thr;
             const float alpha = need ? ex2((m_used - mrow) * sl2) : 1.f;
@@ -483,6 +492,18 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
       __syncwarp();
       last_k = j;
     };
+    if (!split && elect_one()) {
+      // rows past the unit's last query are other requests' (or zeros); their
+      // results are not written
+      for (int t = 0; t < (rows1 > 0 ? 2 : 1); ++t) {
+        const uint32_t full = smem_u32(&bar_ql[t]);
+        mbar_expect_tx(full, kQBytes);
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d(smem_u32(sQ + t * kQBytes + c * BM * 128), &qmap, c * 64, h,
+                      sg.first_f + td.q_off + t * MT + cta * BM, full);
+      }
+    }
+    __syncwarp();
     if (nK > 0) load_k(0, 0, 3);
     for (int j = 0; j < nK && ok; ++j) {  // V_j and K_(j+1)
       if constexpr (PAIR) {
@@ -507,6 +528,8 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     }
     if (!ok && lane == 0) report_timeout(p.status, 4, &abort_flag);
     // Never leave with a copy in flight.
+    if (!split)
+      for (int t = 0; t < (rows1 > 0 ? 2 : 1); ++t) mbar_wait(smem_u32(&bar_ql[t]), 0, 1000000000ull, &zero_flag);
     for (int k = max(0, last_k - KS + 1); k <= last_k; ++k)
       mbar_wait(smem_u32(&bar_k[k % KS]), (k / KS) & 1, 1000000000ull, &zero_flag);
     for (int k = max(0, last_v - KS + 1); k <= last_v; ++k)
@@ -515,7 +538,11 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   } else if (warp == kWarpRelay) {
     // ------------------------------------------------------------ relay
     bool ok = true;
-    if (PAIR && nK > 0) {
+    for (int t = 0; t < (rows1 > 0 ? 2 : 1) && ok; ++t) {
+      ok = wait_all(&bar_ql[t], 0);
+      if (ok) warp_arrive(&bar_q[t]);
+    }
+    if (PAIR && ok && nK > 0) {
       ok = wait_all(&bar_k[0], 0);
       if (ok) warp_arrive(&bar_k0);
     }
@@ -655,21 +682,25 @@ bool kv_map(CUtensorMap* m, const void* kv, int H, int rows, int box_rows) {
 }
 
 template <bool PAIR>
-cudaError_t launch(const Params& p, const void* kv, const void* k_rope, long long rope_stride, int rows,
+cudaError_t launch(const Params& p, const void* kv, const void* k_rope, long long rope_stride, int n_q, int rows,
                    cudaStream_t s) {
   using C = Cfg<PAIR>;
-  CUtensorMap km, vm, rm;
+  CUtensorMap qm, km, vm, rm;
+  const uint64_t qdims[3] = {kDqk, (uint64_t)p.H, (uint64_t)n_q};
+  const uint64_t qstrides[2] = {kDqk * 2, (uint64_t)p.H * kDqk * 2};
+  const uint32_t qbox[3] = {64, 1, BM};
   const uint64_t dims[2] = {kRope, (uint64_t)rows};
   const uint64_t strides[1] = {(uint64_t)rope_stride * 2};
   const uint32_t box[2] = {64, C::kKeys};
-  if (!kv_map(&km, kv, p.H, rows, C::kKeys) || !kv_map(&vm, kv, p.H, rows, BN) ||
+  if (!encode_tensor_map_bf16(&qm, p.q, 3, qdims, qstrides, qbox) || !kv_map(&km, kv, p.H, rows, C::kKeys) ||
+      !kv_map(&vm, kv, p.H, rows, BN) ||
       !encode_tensor_map_bf16(&rm, k_rope, 2, dims, strides, box, false))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)p.n_tiles * p.H * C::kCtas;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  return launch_early(mla_prefill_kernel<PAIR>, (unsigned)blocks, kThreads, C::kSmem, s, C::kCtas, km, vm, rm, p);
+  return launch_early(mla_prefill_kernel<PAIR>, (unsigned)blocks, kThreads, C::kSmem, s, C::kCtas, qm, km, vm, rm, p);
 }
 
 }  // namespace
@@ -727,7 +758,8 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
     n512 += (count + 511) / 512;
   }
   const bool pair = n128 >= 3 * n512;
-  return pair ? launch<true>(p, kv, k_rope, rope_stride, h.KV, s) : launch<false>(p, kv, k_rope, rope_stride, h.KV, s);
+  return pair ? launch<true>(p, kv, k_rope, rope_stride, h.T, h.KV, s)
+              : launch<false>(p, kv, k_rope, rope_stride, h.T, h.KV, s);
 }
 
 }  // namespace cpattn

@@ -218,6 +218,33 @@ def test_prefill_other_requests_rows_do_not_matter(cp):
         assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2[keep], lse[keep])
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38, 1000.0])
+@pytest.mark.parametrize("C,H", [(1, 2), (2, 3)])
+def test_prefill_other_requests_queries_do_not_matter(cp, value, C, H):
+    """Nor do its queries: a tile's rows past a request's last query hold the
+    next one's."""
+    new, prefix = [300, 65, 1100, 70], [200, 0, 77, 400]
+    q, kv, rope = prefill_inputs(new, prefix, H, 61)
+    q[300:365] = value
+    q[1465:] = value
+    other = q.clone()
+    other[300:365] = 0
+    other[1465:] = 0
+    plan, ref = make_plan(cp, "zigzag", C, new, prefix)
+    got = cp.cp_mla_prefill_attn(plan, q, kv, rope)
+    want = cp.cp_mla_prefill_attn(plan, other, kv, rope)
+    cp.cp_device_error_check()
+    req = np.concatenate([np.asarray(x) for x in ref["req"]])
+    keep = torch.as_tensor(req % 2 == 0, device=DEV)
+    for a, b in zip(got, want):
+        assert torch.equal(a[keep], b[keep])
+    for r in range(C):
+        one = cp.cp_mla_prefill_attn(plan, q, kv, rope, rank=r)
+        at = slice(int(plan.rank_off[r]), int(plan.rank_off[r + 1]))
+        for a, b in zip(one, want):
+            assert torch.equal(a[keep[at]], b[at][keep[at]])
+
+
 def test_prefill_large_sampled(cp):
     """Several waves of CTAs, long rows: every segment's first and last query
     and random ones."""
