@@ -761,16 +761,17 @@ def _complain(name, t, dtype, shape, device):
         raise TypeError(f"{name}: need {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {f'cuda:{device}' if device >= 0 else 'no GPU'}")
     if t.shape != shape:
         raise ValueError(f"{name}: need shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
 def _need(name, t, dtype, shape, device):
-    """A contiguous CUDA tensor of this dtype and shape on `device`."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
+    """A contiguous CUDA tensor of this dtype and shape on `device`, the index
+    of a CUDA device (a tensor of another kind has index -1)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0 and t.is_contiguous():
         return t
     return _complain(name, t, dtype, shape, device)
 
@@ -778,7 +779,7 @@ def _need(name, t, dtype, shape, device):
 def _rows(name, t, cols, dtype, device):
     """(pointer, row stride) of a CUDA tensor [n, >= cols] whose rows are
     dense and may lie apart (a view of a wider tensor)."""
-    if t.dtype is not dtype or not t.is_cuda or t.device != device:
+    if t.dtype is not dtype or not t.is_cuda or t.get_device() != device:
         _complain(name, t, dtype, t.shape, device)
     if t.dim() != 2 or t.shape[1] < cols or t.stride(1) != 1:
         raise ValueError(f"{name}: need [n, {cols}] with dense rows, got {tuple(t.shape)}, strides {t.stride()}")
@@ -795,9 +796,9 @@ except AttributeError:
 
 
 def _new(shape, dtype, device):
-    """torch.empty(shape) on the CUDA device of a tensor at hand."""
-    if _empty_cuda is None or device.index != _device_index():
-        return torch.empty(shape, dtype=dtype, device=device)
+    """torch.empty(shape) on the CUDA device with this index."""
+    if _empty_cuda is None or device != _device_index():
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
     n = len(shape)
     if n == 1:
         return _empty_cuda(shape, (1,), dtype)
@@ -805,18 +806,17 @@ def _new(shape, dtype, device):
         return _empty_cuda(shape, (shape[1], 1), dtype)
     if n == 3:
         return _empty_cuda(shape, (shape[1] * shape[2], shape[2], 1), dtype)
-    return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
 
 
 def _call(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device
     current (kernels launch on the current device)."""
-    index = device.index
-    if index == _device_index():
-        st = fn(*args, _raw_stream(index))
+    if device == _device_index():
+        st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, _raw_stream(index))
+            st = fn(*args, _raw_stream(device))
     if st != 0:
         _check(st)
 
@@ -825,7 +825,7 @@ def cp_mla_expand(latent, w_kv, out=None):
     """Keys and values of latent rows: latent [T, >= 512] bf16 (its first 512
     columns; rows may be a view of the 576-wide cache), w_kv [H, 256, 512]
     -> kv [T, H, 256] (128 key dims, then 128 value dims of each head)."""
-    dev = latent.device
+    dev = latent.get_device()
     ptr, stride = _rows("latent", latent, LATENT_DIM, _bf16, dev)
     T, H = latent.shape[0], w_kv.shape[0]
     _need("w_kv", w_kv, _bf16, (H, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), dev)
@@ -836,7 +836,7 @@ def cp_mla_expand(latent, w_kv, out=None):
 
 
 def _per_head(name, x, w_kv, cols, out_cols, out, fn):
-    dev = x.device
+    dev = x.get_device()
     H = w_kv.shape[0]
     lead = x.shape[:-2]
     _need("w_kv", w_kv, _bf16, (H, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), dev)
@@ -865,15 +865,15 @@ def cp_mla_prefill_attn(plan: PrefillPlan, q, kv, k_rope, sm_scale=None, rank: i
     ``rank`` (-1: all ranks, rank-major).  q [T, H, 192]; kv [KV, H, 256]
     (cp_mla_expand); k_rope [KV, 64], a view of the latent cache's last
     columns or a tensor of its own; returns (o [rows, H, 128], lse [rows, H])."""
-    dev = q.device
+    dev = q.get_device()
     T, KV, H = plan.header["T"], plan.header["KV"], q.shape[1]
     _need("q", q, _bf16, (T, H, MLA_NOPE_DIM + MLA_ROPE_DIM), dev)
     _need("kv", kv, _bf16, (KV, H, MLA_NOPE_DIM + MLA_V_DIM), dev)
     rope, stride = _rows("k_rope", k_rope, MLA_ROPE_DIM, _bf16, dev)
     if k_rope.shape[0] != KV:
         raise ValueError(f"k_rope has {k_rope.shape[0]} rows, the plan {KV}")
-    if plan.dev is None or plan.dev.device != dev:
-        raise ValueError(f"the plan has no device part on {dev}")
+    if plan.dev is None or plan.dev.get_device() != dev:
+        raise ValueError(f"the plan has no device part on {q.device}")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(MLA_NOPE_DIM + MLA_ROPE_DIM)
     rows = T if rank < 0 else plan.rank_rows(rank)
@@ -905,7 +905,7 @@ def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos
     i32, table = _i32t, pages.dev
     if table is None:
         raise ValueError("the page table has no device copy")
-    dev = table.device
+    dev = table.get_device()
     B, n_free = ctx_len.shape[0], free_ids.shape[0]
     _need("page table", table, i32, (C * B, pages.max_pages), dev)
     _need("ctx_len", ctx_len, i32, (B,), dev)
@@ -927,8 +927,8 @@ def _new_rows(name, t, n, pool, dev):
     """(pointer, row stride, row elements) of new tokens' rows [n, ...] shaped
     like the pool's; only the first dimension may be strided."""
     shape, row = t.shape, pool.shape[1:]
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, not {t.device}")
     if shape[0] != n or shape[1:] != row:
         raise ValueError(f"{name}: need {(n, *row)}, got {tuple(shape)}")
     elems = row.numel()
@@ -951,7 +951,7 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
     them as they are (E4M3 codes with new_scale [n]); bf16 or fp32 rows into
     an E4M3 pool (uint8 or float8_e4m3fn) are quantised with one scale a
     token, amax / 448 over its K and V, written to scale_pool [pool_rows]."""
-    dev = k_pool.device
+    dev = k_pool.get_device()
     n, rows = slots.shape[0], k_pool.shape[0]
     if not k_pool.is_cuda or not k_pool.is_contiguous():
         raise ValueError("k_pool must be a contiguous CUDA tensor")
@@ -965,7 +965,7 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
     if v_new is not None:
         if _dtype_code(v_new) != src or _dtype_code(v_pool) != pool:
             raise TypeError("V must have K's dtypes")
-        if v_pool.shape != k_pool.shape or v_pool.device != dev or not v_pool.is_contiguous():
+        if v_pool.shape != k_pool.shape or v_pool.get_device() != dev or not v_pool.is_contiguous():
             raise ValueError("v_pool must be a contiguous tensor like k_pool")
         vp, vs, _ = _new_rows("v_new", v_new, n, v_pool, dev)
         vpool = v_pool.data_ptr()
