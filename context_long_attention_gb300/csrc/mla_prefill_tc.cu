@@ -743,12 +743,12 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
   const int most = (int)std::min<long long>(H, std::max<long long>(1, kGroupBytes / head_bytes));
   const int groups = (H + most - 1) / most;
   p.head_group = (H + groups - 1) / groups;
-  // A pair where segments fill three quarters of its 512 rows or more.  Both
-  // forms take about as long for a tile step (3,000 clk for a pair's 512
-  // rows, 3,440 for one CTA's 256), so a pair whose second M tile is empty
-  // wastes an SM: 16,384 + 4,096 tokens in blocks of 1,024 queries, 32 heads:
-  // pairs 2,541 us, single CTAs 2,704; nine ragged requests interleaved over
-  // four ranks (63 quarters filled of 140), 16 heads: 196 and 129.
+  // A pair where requests (one rank: segments) fill three quarters of its 512
+  // rows or more.  Both forms take about as long for a tile step (3,000 clk for
+  // a pair's 512 rows, 3,440 for one CTA's 256), so a pair whose second M tile
+  // is empty wastes an SM.  16,384 tokens behind 4,096, 32 heads: pairs
+  // 2,380 us, single CTAs 2,540; nine ragged requests of 1 to 2,500 tokens (48
+  // quarters filled of 68), 16 heads: 96 and 77.
   const cp_seg_desc* seg = reinterpret_cast<const cp_seg_desc*>(host_plan + h.off_seg);
   const cp_req_desc* req = reinterpret_cast<const cp_req_desc*>(host_plan + h.off_req);
   long long n128 = 0, n512 = 0;

@@ -8,9 +8,9 @@
 // a chain of latencies, which these kernels keep short: no tensor maps, no
 // tensor memory, every weight load in flight at once, one barrier.  In a
 // replayed graph, against the tensor-core kernels (us, absorb / project):
-//   64 heads   1 token 2.5 / 2.2 and 5.6 / 5.4   4 tokens 4.2 / 3.3 and 5.7 / 5.4   8 tokens 6.4 / 5.9 and 4.7 / 5.4
-//   8 heads    1 token 1.8 / 1.7 and 3.5 / 5.1   4 tokens 3.0 / 2.5 and 3.7 / 5.3   8 tokens 4.3 / 3.3 and 3.7 / 5.3
-// so they take up to four (one token over 64 heads reads its 8.4 MB of weight at 3.3 TB/s, launch included).
+//   64 heads   1 token 2.2 / 1.9 and 5.1 / 4.7   4 tokens 4.9 / 3.3 and 4.5 / 4.8   8 tokens 7.3 / 4.6 and 3.9 / 4.8
+//   8 heads    1 token 1.5 / 1.5 and 3.1 / 4.5   4 tokens 2.6 / 2.2 and 3.1 / 4.5   8 tokens 3.9 / 2.9 and 3.1 / 4.5
+// so they take up to four (one token over 64 heads reads its 8.4 MB of weight at 3.8 TB/s, launch included).
 #include <cuda_bf16.h>
 
 #include "early_launch.cuh"

@@ -22,9 +22,9 @@
 //              memory to a TMA store (rows written straight from the registers,
 //              16 bytes a lane and row, took absorb over 512 tokens x 64 heads
 //              twice as long)
-// Tiles of 256 tokens (a third less weight read from the L2) are no faster:
-// project over 1,000 tokens x 64 heads 18.6 us either way, over 300 of 16 heads
-// 8.4 instead of 6.6.
+// Tiles of 256 tokens (a third less weight read from the L2) were no faster:
+// a pass of project over 1,000 tokens x 64 heads took 18.6 us either way, one
+// over 300 tokens x 16 heads 8.4 instead of 6.6.
 //
 // A prompt's expansion runs on CTA pairs (expand_pair_kernel, below).
 #include <cuda.h>
@@ -61,7 +61,7 @@ struct Cfg {
   static constexpr int kStageBytes = kABytes + kBBytes;
   // staging pieces of an epilogue group: two, so that an item's stores do not
   // wait for each other, except where the call is bound by its writes (absorb
-  // over 512 tokens x 64 heads 14.5 us with one, 15.2 with two)
+  // over 512 tokens x 64 heads 10.7 us with one, 11.2 with two)
   static constexpr int kBufs = MODE == kAbsorb ? 1 : NB / 64;
   static constexpr int kStages = (229376 - 2 * kBufs * kOutBytes) / kStageBytes;
   static constexpr int kSmem = kStages * kStageBytes + 2 * kBufs * kOutBytes + 1024;
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // through its L2 port; a single CTA's 128 x 256 tile reads 96).  Pairs take
 // contiguous runs of (token tile, head) items; a new tile's rows are loaded
 // piece by piece as the last head's products release the old ones.  20,480
-// tokens x 32 heads: 103 us = 1,670 TFLOP/s (the library's product of this
+// tokens x 32 heads: 103 to 105 us = 1,650 TFLOP/s (the library's product of this
 // shape: 99.5; single CTAs with tiles of 128 x 256: 117 to 162); bound by power
 // (0.98 of the sustained bf16 rate) and the first rows' read.
 constexpr int kPieces = kLatent / 64;
@@ -561,12 +561,14 @@ cudaError_t launch_mla_expand(const void* latent, long long stride, const void* 
   const uint32_t box[2] = {64, BM};
   if (!encode_tensor_map_bf16(&am, latent, 2, dims, strides, box)) return cudaErrorInvalidValue;
   if (!weight_map(&wm, w, H, 128) || !token_map(&om, kv, T, H, kHeadRows)) return cudaErrorInvalidValue;
-  // Pairs where some have more than one (256 tokens, head) item.  Measured (us,
-  // pairs / single CTAs of 128 x 128 tiles, any split of the items into tokens
-  // and heads): 32 items 8.2 / 6.3, 64 8.5 / 8.7, 96 11.4 / 11.4, 128 11.4 / 13.6,
-  // 456 23.2 / 32.3.
-  const long long items = (long long)((T + 2 * BM - 1) / (2 * BM)) * H;
-  if (items > sms / 2) return launch_expand_pair(am, wm, om, p, sms, s);
+  // Measured in a replayed graph (us): r rounds of 128 x 128 tiles on single
+  // CTAs take 2.7 + 2.4 r (1 round 5.2, 2 7.6, 3 10.0, 4 12.2, 12 31.5, 68 167),
+  // r rounds of (256 tokens, head) items on pairs 4.6 + 3 r (1 round 7.6,
+  // 2 10.6, 3 13.5, 6 21.7, 34 105).  Twice the single rounds as a rule, fewer
+  // where the last 256 tokens are half empty or the last round is.
+  const long long singles = ((long long)((T + BM - 1) / BM) * 2 * H + sms - 1) / sms;
+  const long long pairs = ((long long)((T + 2 * BM - 1) / (2 * BM)) * H + sms / 2 - 1) / (sms / 2);
+  if (10 + 15 * pairs < 12 * singles) return launch_expand_pair(am, wm, om, p, sms, s);
   return launch<kExpand, 128>(am, wm, om, p, sms, s);
 }
 

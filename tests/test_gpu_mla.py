@@ -51,7 +51,8 @@ def product_tol(ref, terms, K):
 # ------------------------------------------------------------------ products
 
 @pytest.mark.parametrize("T,H,stride", [(1, 1, 512), (127, 3, 576), (128, 2, 512), (129, 16, 640), (700, 5, 576),
-                                        (5000, 8, 576), (2500, 33, 512), (257, 80, 576)])
+                                        (5000, 8, 576), (2500, 33, 512), (257, 80, 576), (700, 150, 576),
+                                        (513, 150, 512)])
 def test_expand(cp, T, H, stride):
     lat, w = randn((T, stride), T)[:, :512], weights(H, H)
     out, buf, keep = guarded((T, H, 256), torch.bfloat16, 3)
