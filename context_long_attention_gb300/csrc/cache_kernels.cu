@@ -336,7 +336,7 @@ __device__ __forceinline__ uint2 codes_of(const Piece<T>& x, float scale, float 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float v = x.at(i), q0 = v * inv;
-      q[i] = __fmaf_rn(__fmaf_rn(-q0, scale, v), inv, q0);
+      q[i] = __fmaf_rn(-__fmaf_rn(q0, scale, -v), inv, q0);  // these signs keep that of a zero
     }
   }
   return make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const Appen
 template <typename T, bool HAS_V>
 cudaError_t append_e4m3(const AppendArgs& a, cudaStream_t s) {
   const int per_lane = (a.row_elems / 8 + 31) / 32;
-  const unsigned grid = (unsigned)((a.n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+  const unsigned grid = (unsigned)(((long long)a.n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
   auto kern = append_e4m3_kernel<T, 0, HAS_V>;
   if (per_lane == 1) kern = append_e4m3_kernel<T, 1, HAS_V>;
   else if (per_lane == 2) kern = append_e4m3_kernel<T, 2, HAS_V>;
@@ -420,7 +420,7 @@ cudaError_t append_e4m3(const AppendArgs& a, cudaStream_t s) {
 template <int LPR>
 cudaError_t append_copy(const AppendArgs& a, int elem, cudaStream_t s) {
   const int per_block = kAppendThreads / LPR;
-  return launch_early(append_copy_kernel<LPR>, (unsigned)((a.n + per_block - 1) / per_block), kAppendThreads, 0, s, 1, a,
+  return launch_early(append_copy_kernel<LPR>, (unsigned)(((long long)a.n + per_block - 1) / per_block), kAppendThreads, 0, s, 1, a,
                       elem);
 }
 

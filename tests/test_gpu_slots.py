@@ -219,6 +219,20 @@ def test_append_quantises_any_scale(cp):
     assert torch.equal(sp, sc) and torch.equal(kp, kc)
 
 
+@pytest.mark.parametrize("src", [torch.bfloat16, torch.float32])
+def test_append_keeps_the_sign_of_zero(cp, src):
+    """Zeros of either sign, in rows of any scale and in a row of zeros."""
+    k = torch.tensor([[0.0, -0.0, 1.0, -1.0, 0.0, -1e-30, 1e-30, -0.0] * 8] * 4, device=DEV)
+    k[1] *= 1e-4
+    k[2] *= 1e30
+    k[3] = torch.where(k[3].signbit(), -0.0, 0.0)
+    k = k.to(src)
+    kp, sp = torch.full((4, 64), 77, dtype=torch.uint8, device=DEV), torch.zeros(4, device=DEV)
+    cp.cp_cache_append(torch.arange(4, **I32), k, kp, scale_pool=sp)
+    kc, _, sc = quantised(k, None)
+    assert torch.equal(sp, sc) and torch.equal(kp, kc)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.uint8])
 @pytest.mark.parametrize("n,heads,dim", [(1, 1, 64), (40, 8, 128), (19, 3, 48), (9, 1, 576), (3000, 2, 64)])
 def test_append_copies(cp, dtype, n, heads, dim):
