@@ -171,14 +171,21 @@ cp_status build_prefill_plan(cp_strategy strategy, int C, int R, const int32_t* 
     return a.rank != b.rank ? a.rank < b.rank : a.work > b.work;
   });
   // The requests' own tiles (a call over all ranks need not keep to their
-  // segments), in the same order.
-  std::vector<TileKey> by_req;
-  for (int j = 0; j < R; ++j)
-    for (int off = 0; off < new_len[j]; off += kPrefillTileRows) {
-      const int nrow = std::min(kPrefillTileRows, new_len[j] - off);
-      by_req.push_back({{j, off}, ((long long)prefix_len[j] + off + nrow) * nrow, 0});
-    }
-  std::stable_sort(by_req.begin(), by_req.end(), [](const TileKey& a, const TileKey& b) { return a.work > b.work; });
+  // segments), of 256 and of 512 queries: most keys first, since a step of the
+  // kernel takes as long for one query as for a full tile.
+  std::vector<cp_req_tile> req_tiles;
+  int n_req_tiles = 0;
+  for (int size : {kPrefillTileRows, 2 * kPrefillTileRows}) {
+    const size_t first = req_tiles.size();
+    for (int j = 0; j < R; ++j)
+      for (long long off = 0; off < new_len[j]; off += size) req_tiles.push_back({j, (int32_t)off, req[j], {0, 0}});
+    auto keys = [&](const cp_req_tile& t) {
+      return t.r.prefix_len + std::min((long long)t.r.new_len, (long long)t.q_off + size);
+    };
+    std::stable_sort(req_tiles.begin() + first, req_tiles.end(),
+                     [&](const cp_req_tile& a, const cp_req_tile& b) { return keys(a) > keys(b); });
+    if (!first) n_req_tiles = (int)req_tiles.size();
+  }
   std::vector<int32_t> rank_tile_off(C + 1, 0);
   for (const TileKey& t : by_rank) rank_tile_off[t.rank + 1]++;
   for (int r = 0; r < C; ++r) rank_tile_off[r + 1] += rank_tile_off[r];
@@ -206,8 +213,8 @@ cp_status build_prefill_plan(cp_strategy strategy, int C, int R, const int32_t* 
   h.off_rtile = w;
   w = align4(w + (C + 1) + 2 * n_tiles);
   h.off_run = w;
-  h.n_parts = (int32_t)by_req.size();
-  w = align4(w + 2 * h.n_parts);
+  h.n_parts = n_req_tiles;
+  w = align4(w + kReqTileWords * (int)req_tiles.size());
   h.host_words = w;
   h.off_idx = w;
   w = align4(w + (int)T);
@@ -233,10 +240,7 @@ cp_status build_prefill_plan(cp_strategy strategy, int C, int R, const int32_t* 
     W[h.off_rtile + C + 1 + 2 * i] = by_rank[i].t.seg;
     W[h.off_rtile + C + 1 + 2 * i + 1] = by_rank[i].t.q_off;
   }
-  for (int i = 0; i < h.n_parts; ++i) {
-    W[h.off_run + 2 * i] = by_req[i].t.seg;
-    W[h.off_run + 2 * i + 1] = by_req[i].t.q_off;
-  }
+  if (!req_tiles.empty()) memcpy(W + h.off_run, req_tiles.data(), sizeof(cp_req_tile) * req_tiles.size());
   out->dev_words = h.dev_words;
   return CP_OK;
 }

@@ -11,6 +11,7 @@ namespace cpattn {
 
 constexpr int kHeaderWords = (int)(sizeof(cp_plan_header) / 4);
 constexpr int kSegWords = (int)(sizeof(cp_seg_desc) / 4);
+constexpr int kReqTileWords = (int)(sizeof(cp_req_tile) / 4);
 constexpr int kPairWords = (int)(sizeof(cp_pair_desc) / 4);
 constexpr int kWorkWords = (int)(sizeof(cp_work_desc) / 4);
 constexpr int kPrefillTileRows = 256;  // queries per prefill tile (two 128-row MMA tiles)

@@ -85,10 +85,11 @@ struct Cfg {
 struct Params {
   const int32_t* plan;
   int off_seg;
-  int off_req, off_rank;  // all ranks: the requests, the ranks' first rows
+  int off_rank;  // all ranks: the ranks' first rows
   int C, R;
   int zigzag;
-  int all;        // all ranks: the tile list holds {request, first query}
+  int all;        // all ranks: the tile list holds cp_req_tile
+  int split;      // one rank of an interleave plan (below)
   int tile_list;
   int n_tiles;
   int row_sub;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   // warps arrive there from both CTAs.
   __shared__ __align__(8) uint64_t bar_k[KS], bar_v[KS], bar_rel[KS], bar_k0;
   // bar_ql: a tile's Q rows are in this CTA's shared memory (by TMA, or
-  // written by its eight warps); the relay passes that on to bar_q.
+  // written by its eight warps); in pairs the relays pass that on to bar_q.
   __shared__ __align__(8) uint64_t bar_ql[2], bar_q[2], bar_s[2], bar_p[2], bar_o[2][2], bar_drain;
   __shared__ int s_row[2][BM];  // output row of each query, -1 past the unit's last (kept here: the loop has no register to spare)
   __shared__ uint32_t tmem_slot;
@@ -184,35 +185,25 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   const int per_group = p.n_tiles * p.head_group, g0 = unit / per_group, rem = unit - g0 * per_group;
   const int group = min(p.head_group, p.H - g0 * p.head_group);
   const int tile_i = rem / group, h = g0 * p.head_group + rem - tile_i * group;
-  const cp_tile_desc td = reinterpret_cast<const cp_tile_desc*>(p.plan + p.tile_list)[tile_i];
-  // a pair takes two plan tiles, from every even one of a segment
-  if (PAIR && (td.q_off & (2 * MT - 1))) return;
+  cp_tile_desc td;
   cp_seg_desc sg;
   if (p.all) {
-    const cp_req_desc rq = reinterpret_cast<const cp_req_desc*>(p.plan + p.off_req)[td.seg];
-    sg.count = rq.new_len;
-    sg.first_f = rq.q_base;
+    const int4* tile = reinterpret_cast<const int4*>(p.plan + p.tile_list) + 2 * tile_i;  // a cp_req_tile
+    const int4 a = tile[0], b = tile[1];
+    td.seg = a.x;
+    td.q_off = a.y;
+    sg.count = a.z;
+    sg.first_pos = a.w;
+    sg.first_f = b.x;
+    sg.kv_base = b.y;
     sg.stride = 1;
-    sg.first_pos = rq.prefix_len;
-    sg.kv_base = rq.kv_base;
   } else {
+    td = reinterpret_cast<const cp_tile_desc*>(p.plan + p.tile_list)[tile_i];
+    // a pair takes two plan tiles, from every even one of a segment
+    if (PAIR && (td.q_off & (2 * MT - 1))) return;
     sg = reinterpret_cast<const cp_seg_desc*>(p.plan + p.off_seg)[td.seg];
   }
-
-  // Query (from the unit's first) of row i of M tile t.  A block's queries are
-  // neighbours and the second tile reads a tile or two of keys more; an
-  // interleave run's lie C apart and it would read C / 2 tiles more all alone
-  // (a step takes as long for one M tile as for two), so the tiles take every
-  // other query.
-  const bool split = sg.stride > 1;
-  auto query = [&](int t, int i) { return split ? 2 * i + t : t * MT + i; };
-  const int n_q = min(2 * MT, sg.count - td.q_off);
-  const int rows0 = split ? (n_q + 1) / 2 : min(MT, n_q), rows1 = n_q - rows0;
-  const int nkv0 = (sg.first_pos + (td.q_off + query(0, rows0 - 1)) * sg.stride + BN) / BN;
-  const int nkv1 = rows1 > 0 ? (sg.first_pos + (td.q_off + query(1, rows1 - 1)) * sg.stride + BN) / BN : 0;
-  const int nK = max(nkv0, nkv1);
-  const int last_t = nkv1 > 0 ? 1 : 0;  // the tile whose products come last in every step
-  const int n_keys = sg.first_pos + (td.q_off + n_q - 1) * sg.stride + 1;
+  const bool split = p.split;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
@@ -243,6 +234,21 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     prefetch_tmap(&vmap);
     prefetch_tmap(&ropemap);
   }
+
+  // Query (from the unit's first) of row i of M tile t.  A block's queries are
+  // neighbours and the second tile reads a tile or two of keys more; an
+  // interleave run's lie C apart and it would read C / 2 tiles more all alone
+  // (a step takes as long for one M tile as for two), so the tiles take every
+  // other query.
+  auto query = [&](int t, int i) { return split ? 2 * i + t : t * MT + i; };
+  const int n_q = min(2 * MT, sg.count - td.q_off);
+  const int rows0 = split ? (n_q + 1) / 2 : min(MT, n_q), rows1 = n_q - rows0;
+  const int nkv0 = (sg.first_pos + (td.q_off + query(0, rows0 - 1)) * sg.stride + BN) / BN;
+  const int nkv1 = rows1 > 0 ? (sg.first_pos + (td.q_off + query(1, rows1 - 1)) * sg.stride + BN) / BN : 0;
+  const int nK = max(nkv0, nkv1);
+  const int last_t = nkv1 > 0 ? 1 : 0;  // the tile whose products come last in every step
+  // rows of V from here on are not the unit's request's (one rank: not its last query's)
+  const int n_keys = sg.first_pos + (p.all ? sg.count : (td.q_off + n_q - 1) * sg.stride + 1);
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // both CTAs' barriers are set up
@@ -492,19 +498,21 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
       __syncwarp();
       last_k = j;
     };
-    if (!split && elect_one()) {
-      // rows past the unit's last query are other requests' (or zeros); their
-      // results are not written
-      for (int t = 0; t < (rows1 > 0 ? 2 : 1); ++t) {
+    auto load_q = [&](int t) {
+      if (!split && elect_one()) {
+        // rows past the unit's last query are other requests' (or zeros); their
+        // results are not written
         const uint32_t full = smem_u32(&bar_ql[t]);
         mbar_expect_tx(full, kQBytes);
         for (int c = 0; c < 3; ++c)
           tma_load_3d(smem_u32(sQ + t * kQBytes + c * BM * 128), &qmap, c * 64, h,
                       sg.first_f + td.q_off + t * MT + cta * BM, full);
       }
-    }
-    __syncwarp();
+      __syncwarp();
+    };
+    load_q(0);
     if (nK > 0) load_k(0, 0, 3);
+    if (rows1 > 0) load_q(1);  // the first tile's scores need not wait for it
     for (int j = 0; j < nK && ok; ++j) {  // V_j and K_(j+1)
       if constexpr (PAIR) {
         if (j >= KS - 1) ok = wait_all(&bar_rel[(j + 1) % KS], ((j + 1) / KS - 1) & 1);
@@ -538,23 +546,27 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   } else if (warp == kWarpRelay) {
     // ------------------------------------------------------------ relay
     bool ok = true;
-    for (int t = 0; t < (rows1 > 0 ? 2 : 1) && ok; ++t) {
-      ok = wait_all(&bar_ql[t], 0);
-      if (ok) warp_arrive(&bar_q[t]);
-    }
-    if (PAIR && ok && nK > 0) {
-      ok = wait_all(&bar_k[0], 0);
-      if (ok) warp_arrive(&bar_k0);
+    if constexpr (PAIR) {
+      ok = wait_all(&bar_ql[0], 0);
+      if (ok) warp_arrive(&bar_q[0]);
+      if (ok && nK > 0) {
+        ok = wait_all(&bar_k[0], 0);
+        if (ok) warp_arrive(&bar_k0);
+      }
+      if (ok && rows1 > 0) {
+        ok = wait_all(&bar_ql[1], 0);
+        if (ok) warp_arrive(&bar_q[1]);
+      }
     }
     for (int j = 0; j < nK && ok; ++j) {
       ok = wait_all(&bar_v[j % KS], (j / KS) & 1);
       if (PAIR && ok && j + 1 < nK) ok = wait_all(&bar_k[(j + 1) % KS], ((j + 1) / KS) & 1);
-      if (ok && j == nK - 1) {  // rows past the last key
-        for (int r = n_keys - j * BN + lane; r < BN; r += 32)
+      if (ok && j == nK - 1) {  // rows past the last key, four rows' 128 bytes at a time
+        for (int r = n_keys - j * BN + (lane >> 3); r < BN; r += 4)
 #pragma unroll
-          for (int c = 0; c < C::kDims / 8; ++c) {
-            uint8_t* v = PAIR ? sV + (j % KS) * C::kVBytes : piece(5 * j + 3 + (c >> 3));
-            *reinterpret_cast<uint4*>(v + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < C::kDims / 64; ++c) {
+            uint8_t* v = PAIR ? sV + (j % KS) * C::kVBytes : piece(5 * j + 3 + c);
+            *reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
         fence_proxy_async_smem();
       }
@@ -626,13 +638,15 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     };
     unsigned bad = 0;
     if (p.stall_test && !wait_all(&bar_drain, 0)) bad = 10;
-    for (int t = 0; t < 2 && !bad; ++t)
-      if ((t ? nkv1 : nkv0) > 0 && !wait_all(&bar_q[t], 0)) bad = 11;
-    if (!bad && nK > 0) {
-      if (!wait_all(PAIR ? &bar_k0 : &bar_k[0], 0)) bad = 12;
+    if (nK > 0 && !bad && !wait_all(PAIR ? &bar_k0 : &bar_k[0], 0)) bad = 12;
+    for (int t = 0; t < 2 && !bad; ++t) {
+      if ((t ? nkv1 : nkv0) == 0) continue;
+      if (!wait_all(PAIR ? &bar_q[t] : &bar_ql[t], 0)) {
+        bad = 11;
+        break;
+      }
       tc_fence_after();
-      for (int t = 0; t < 2 && !bad; ++t)
-        if ((t ? nkv1 : nkv0) > 0) issue_s(t, 0);
+      issue_s(t, 0);
     }
     for (int j = 0; j < nK && !bad; ++j) {
       bool k_in = PAIR;  // K_(j+1) is in place: a pair's P barrier says so
@@ -712,23 +726,12 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
   Params p;
   p.plan = dev_plan;
   p.off_seg = h.off_seg;
-  p.off_req = h.off_req;
   p.off_rank = h.off_rank;
   p.C = h.C;
   p.R = h.R;
   p.zigzag = h.kind == 0;
   p.all = rank < 0;
-  if (rank < 0) {
-    p.tile_list = h.off_run;
-    p.n_tiles = h.n_parts;
-    p.row_sub = 0;
-  } else {
-    const int32_t* rto = host_plan + h.off_rtile;
-    p.tile_list = h.off_rtile + h.C + 1 + 2 * rto[rank];
-    p.n_tiles = rto[rank + 1] - rto[rank];
-    p.row_sub = host_plan[h.off_rank + rank];
-  }
-  if (p.n_tiles == 0) return cudaSuccess;
+  p.split = rank >= 0 && h.kind == 1 && h.C > 1;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -758,6 +761,17 @@ cudaError_t launch_mla_prefill(const int32_t* dev_plan, const int32_t* host_plan
     n512 += (count + 511) / 512;
   }
   const bool pair = n128 >= 3 * n512;
+  if (rank < 0) {
+    p.tile_list = h.off_run + (pair ? kReqTileWords * h.n_parts : 0);
+    p.n_tiles = pair ? (int)n512 : h.n_parts;
+    p.row_sub = 0;
+  } else {
+    const int32_t* rto = host_plan + h.off_rtile;
+    p.tile_list = h.off_rtile + h.C + 1 + 2 * rto[rank];
+    p.n_tiles = rto[rank + 1] - rto[rank];
+    p.row_sub = host_plan[h.off_rank + rank];
+  }
+  if (p.n_tiles == 0) return cudaSuccess;
   return pair ? launch<true>(p, kv, k_rope, rope_stride, h.T, h.KV, s)
               : launch<false>(p, kv, k_rope, rope_stride, h.T, h.KV, s);
 }

@@ -101,14 +101,14 @@ typedef struct {
   int32_t off_qreq;   /* prefill, device only: int32 qreq[T] (request of the query) */
   int32_t host_words; /* words in the host part */
   int32_t dev_words;  /* words in the device plan */
-  int32_t n_parts;    /* prefill: number of request tiles; decode: partial slots in the workspace (split pairs) */
+  int32_t n_parts;    /* prefill: number of 256-query request tiles; decode: partial slots in the workspace (split pairs) */
   int32_t tile_rows;  /* decode: KV rows per scheduling tile (work boundaries) */
   int32_t n_split;    /* decode: pairs covered by more than one work item */
   int32_t layout;     /* decode: cp_dcp_layout of the token shards */
   int32_t s_q;        /* decode: query rows per request (1, or more for MTP) */
-  int32_t off_run;    /* prefill: {request, first query}[n_parts], 256-query tiles of the requests
-                         (whatever their ranks), longest first; decode: the merged-output run
-                         table (cp_decode_attn_merged) */
+  int32_t off_run;    /* prefill: cp_req_tile[n_parts], 256-query tiles of the requests (whatever
+                         their ranks), longest first, then their 512-query tiles likewise;
+                         decode: the merged-output run table (cp_decode_attn_merged) */
 } cp_plan_header;
 /* Decode plans reuse the table offsets: off_tiles -> int32 [R][2]
  * {ctx_len, first token of the request in the token-ordered cache};
@@ -139,6 +139,14 @@ typedef struct {
                           0 for an empty interleave run */
   int32_t kv_base;     /* first K/V row of the request */
 } cp_seg_desc;
+
+/* A tile of up to 256 or 512 consecutive queries of one request. */
+typedef struct {
+  int32_t req;   /* request index */
+  int32_t q_off; /* the tile's first query within the request */
+  cp_req_desc r; /* the request itself: one read gives a kernel its tile */
+  int32_t pad[2];
+} cp_req_tile;
 
 /* A tile of up to 256 consecutive queries of one segment. */
 typedef struct {

@@ -73,14 +73,21 @@ def test_prefill(cp):
 
 @pytest.mark.parametrize("strategy,C", [(0, 1), (0, 8), (1, 3)])
 def test_request_tiles_of_a_plan(cp, strategy, C):
-    """The request tiles cover every request's new tokens once, 256 at a time,
-    most work (queries x keys of the last one) first."""
+    """The request tiles cover every request's new tokens once, 256 and 512 at a
+    time, those whose last query has most keys first; each holds its request."""
     new, prefix = [700, 0, 1, 256, 513, 90], [5, 3, 4000, 0, 77, 0]
     plan = cp.cp_shard_plan(strategy, C, new, prefix, device=None)
-    tiles = plan.words(plan.off_run, 2 * plan.n_parts).reshape(-1, 2)
-    assert sorted(map(tuple, tiles.tolist())) == [(j, o) for j, n in enumerate(new) for o in range(0, n, 256)]
-    work = [(prefix[j] + min(o + 256, new[j])) * min(256, new[j] - o) for j, o in tiles.tolist()]
-    assert work == sorted(work, reverse=True)
+    at = plan.off_run
+    for size in (256, 512):
+        want = [(j, o) for j, n in enumerate(new) for o in range(0, n, size)]
+        tiles = plan.words(at, 8 * len(want)).reshape(-1, 8).tolist()
+        at += 8 * len(want)
+        assert size == 512 or plan.n_parts == len(want)
+        assert sorted((t[0], t[1]) for t in tiles) == want
+        for j, _, n, pre, q_base, kv_base, *_ in tiles:
+            assert (n, pre, q_base, kv_base) == (new[j], prefix[j], sum(new[:j]), sum(new[:j]) + sum(prefix[:j]))
+        keys = [prefix[j] + min(o + size, new[j]) for j, o, *_ in tiles]
+        assert keys == sorted(keys, reverse=True)
 
 
 def test_page_slots(cp):
