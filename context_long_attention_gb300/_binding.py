@@ -790,35 +790,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 try:
-    _empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+    _empty = torch._C._dynamo.guards._empty_strided_cuda
 except AttributeError:
-    _empty_cuda = None
+    def _empty(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
 
-def _new(shape, dtype, device):
-    """torch.empty(shape) on the CUDA device with this index."""
-    if _empty_cuda is None or device != _device_index():
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
-    n = len(shape)
-    if n == 1:
-        return _empty_cuda(shape, (1,), dtype)
-    if n == 2:
-        return _empty_cuda(shape, (shape[1], 1), dtype)
-    if n == 3:
-        return _empty_cuda(shape, (shape[1] * shape[2], shape[2], 1), dtype)
-    return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
-
-
-def _call(device, fn, *args):
-    """fn(*args, stream) on the device's current stream, with the device
-    current (kernels launch on the current device)."""
-    if device == _device_index():
-        st = fn(*args, _raw_stream(device))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _raw_stream(device))
-    if st != 0:
-        _check(st)
+def _on(device, fn, *args):
+    """fn with the arguments' device current (outputs are made and kernels
+    launched on the current device)."""
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def cp_mla_expand(latent, w_kv, out=None):
@@ -829,9 +811,13 @@ def cp_mla_expand(latent, w_kv, out=None):
     ptr, stride = _rows("latent", latent, LATENT_DIM, _bf16, dev)
     T, H = latent.shape[0], w_kv.shape[0]
     _need("w_kv", w_kv, _bf16, (H, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), dev)
-    shape = (T, H, MLA_NOPE_DIM + MLA_V_DIM)
-    out = _new(shape, _bf16, dev) if out is None else _need("out", out, _bf16, shape, dev)
-    _call(dev, lib.cp_mla_expand, ptr, stride, w_kv.data_ptr(), T, H, out.data_ptr())
+    if dev != _device_index():
+        return _on(dev, cp_mla_expand, latent, w_kv, out)
+    cols = MLA_NOPE_DIM + MLA_V_DIM
+    out = _empty((T, H, cols), (H * cols, cols, 1), _bf16) if out is None else _need("out", out, _bf16, (T, H, cols), dev)
+    st = lib.cp_mla_expand(ptr, stride, w_kv.data_ptr(), T, H, out.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -841,9 +827,18 @@ def _per_head(name, x, w_kv, cols, out_cols, out, fn):
     lead = x.shape[:-2]
     _need("w_kv", w_kv, _bf16, (H, MLA_NOPE_DIM + MLA_V_DIM, LATENT_DIM), dev)
     _need(name, x, _bf16, (*lead, H, cols), dev)
+    if dev != _device_index():
+        return _on(dev, _per_head, name, x, w_kv, cols, out_cols, out, fn)
     shape = (*lead, H, out_cols)
-    out = _new(shape, _bf16, dev) if out is None else _need("out", out, _bf16, shape, dev)
-    _call(dev, fn, x.data_ptr(), w_kv.data_ptr(), lead.numel(), H, out.data_ptr())
+    if out is not None:
+        _need("out", out, _bf16, shape, dev)
+    elif len(lead) == 1:
+        out = _empty(shape, (H * out_cols, out_cols, 1), _bf16)
+    else:
+        out = torch.empty(shape, dtype=_bf16, device=x.device)
+    st = fn(x.data_ptr(), w_kv.data_ptr(), lead.numel(), H, out.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -876,13 +871,17 @@ def cp_mla_prefill_attn(plan: PrefillPlan, q, kv, k_rope, sm_scale=None, rank: i
         raise ValueError(f"the plan has no device part on {q.device}")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(MLA_NOPE_DIM + MLA_ROPE_DIM)
+    if dev != _device_index():
+        return _on(dev, cp_mla_prefill_attn, plan, q, kv, k_rope, sm_scale, rank, out, lse)
     rows = T if rank < 0 else plan.rank_rows(rank)
-    out = _new((rows, H, MLA_V_DIM), _bf16, dev) if out is None else \
+    out = _empty((rows, H, MLA_V_DIM), (H * MLA_V_DIM, MLA_V_DIM, 1), _bf16) if out is None else \
         _need("out", out, _bf16, (rows, H, MLA_V_DIM), dev)
-    lse = _new((rows, H), torch.float32, dev) if lse is None else \
+    lse = _empty((rows, H), (H, 1), torch.float32) if lse is None else \
         _need("lse", lse, torch.float32, (rows, H), dev)
-    _call(dev, lib.cp_mla_prefill_attn, plan.host_ptr, plan.dev.data_ptr(), rank, q.data_ptr(), kv.data_ptr(),
-          rope, stride, H, sm_scale, out.data_ptr(), lse.data_ptr())
+    st = lib.cp_mla_prefill_attn(plan.host_ptr, plan.dev.data_ptr(), rank, q.data_ptr(), kv.data_ptr(), rope, stride,
+                                 H, sm_scale, out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
     return out, lse
 
 
@@ -912,21 +911,23 @@ def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos
     _need("new_len", new_len, i32, (B,), dev)
     _need("free_ids", free_ids, i32, (n_free,), dev)
     _need("free_pos", free_pos, i32, (1,), dev)
-    slots = _new((max_tokens,), i32, dev) if slots is None else \
-        _need("slots", slots, i32, (max_tokens,), dev)
-    cu_new = _new((B + 1,), i32, dev) if cu_new is None else \
-        _need("cu_new", cu_new, i32, (B + 1,), dev)
-    info = _new((4,), i32, dev) if info is None else _need("info", info, i32, (4,), dev)
-    _call(dev, lib.cp_page_slots, C, B, ctx_len.data_ptr(), new_len.data_ptr(), table.data_ptr(), pages.max_pages,
-          pages.page_size, pages.num_pages, free_ids.data_ptr(), n_free, free_pos.data_ptr(),
-          slots.data_ptr(), max_tokens, cu_new.data_ptr(), info.data_ptr())
+    if dev != _device_index():
+        return _on(dev, cp_page_slots, pages, C, ctx_len, new_len, free_ids, free_pos, max_tokens, slots, cu_new, info)
+    slots = _empty((max_tokens,), (1,), i32) if slots is None else _need("slots", slots, i32, (max_tokens,), dev)
+    cu_new = _empty((B + 1,), (1,), i32) if cu_new is None else _need("cu_new", cu_new, i32, (B + 1,), dev)
+    info = _empty((4,), (1,), i32) if info is None else _need("info", info, i32, (4,), dev)
+    st = lib.cp_page_slots(C, B, ctx_len.data_ptr(), new_len.data_ptr(), table.data_ptr(), pages.max_pages,
+                           pages.page_size, pages.num_pages, free_ids.data_ptr(), n_free, free_pos.data_ptr(),
+                           slots.data_ptr(), max_tokens, cu_new.data_ptr(), info.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
     return slots, cu_new, info
 
 
-def _new_rows(name, t, n, pool, dev):
-    """(pointer, row stride, row elements) of new tokens' rows [n, ...] shaped
-    like the pool's; only the first dimension may be strided."""
-    shape, row = t.shape, pool.shape[1:]
+def _new_rows(name, t, n, row, dev):
+    """(pointer, row stride, row elements) of new tokens' rows [n, *row]; only
+    the first dimension may be strided."""
+    shape = t.shape
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, not {t.device}")
     if shape[0] != n or shape[1:] != row:
@@ -956,7 +957,7 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
     if not k_pool.is_cuda or not k_pool.is_contiguous():
         raise ValueError("k_pool must be a contiguous CUDA tensor")
     _need("slots", slots, _i32t, (n,), dev)
-    kp, ks, elems = _new_rows("k_new", k_new, n, k_pool, dev)
+    kp, ks, elems = _new_rows("k_new", k_new, n, k_pool.shape[1:], dev)
     src, pool = _dtype_code(k_new), _dtype_code(k_pool)
     vp = vpool = None
     vs = 0
@@ -967,12 +968,19 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
             raise TypeError("V must have K's dtypes")
         if v_pool.shape != k_pool.shape or v_pool.get_device() != dev or not v_pool.is_contiguous():
             raise ValueError("v_pool must be a contiguous tensor like k_pool")
-        vp, vs, _ = _new_rows("v_new", v_new, n, v_pool, dev)
+        vp, vs, _ = _new_rows("v_new", v_new, n, v_pool.shape[1:], dev)
         vpool = v_pool.data_ptr()
-    _call(dev, lib.cp_cache_append, slots.data_ptr(), n, src, kp, ks, vp, vs,
-          None if new_scale is None else _need("new_scale", new_scale, torch.float32, (n,), dev).data_ptr(), elems,
-          pool, k_pool.data_ptr(), vpool,
-          None if scale_pool is None else _need("scale_pool", scale_pool, torch.float32, (rows,), dev).data_ptr(), rows)
+    scale = pool_scale = None
+    if new_scale is not None:
+        scale = _need("new_scale", new_scale, torch.float32, (n,), dev).data_ptr()
+    if scale_pool is not None:
+        pool_scale = _need("scale_pool", scale_pool, torch.float32, (rows,), dev).data_ptr()
+    if dev != _device_index():
+        return _on(dev, cp_cache_append, slots, k_new, k_pool, v_new, v_pool, scale_pool, new_scale)
+    st = lib.cp_cache_append(slots.data_ptr(), n, src, kp, ks, vp, vs, scale, elems, pool, k_pool.data_ptr(), vpool,
+                             pool_scale, rows, _raw_stream(dev))
+    if st:
+        _check(st)
 
 
 # ---------------------------------------------------------------- NVTX ranges
