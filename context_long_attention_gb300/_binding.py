@@ -368,7 +368,13 @@ def cp_kv_shard_pack(plan: DecodePlan, kv, kv_scale=None, shards=None, shard_sca
 class PageTable:
     """A paged decode cache's page table: int32 [C * R][max_pages] page ids
     (row i of pair (shard r, request b) is row i % page_size of page
-    table[r * R + b][i // page_size]), kept as a host array and a device copy."""
+    table[r * R + b][i // page_size]), kept as a host array and a device copy.
+
+    The paged pack and decode check the host copy and read the device one, so
+    both must hold the same ids.  cp_page_slots changes the device copy and
+    drops the host one (``host`` is None); sync_host() reads it back.  So does
+    a caller who changes ``dev`` in another way, as by replaying a captured
+    cp_page_slots: sync_host() after it."""
 
     def __init__(self, table, page_size: int, num_pages: int, device=None):
         self.host = np.ascontiguousarray(np.asarray(table, dtype=np.int32))
@@ -403,7 +409,7 @@ class PageTable:
 
 def _host_table(pages: PageTable):
     if pages.host is None:
-        raise ValueError("the page table has no host copy: call sync_host() first")
+        raise ValueError("the page table has no host copy of its present ids: call sync_host() first")
     return _np_ptr(pages.host)
 
 
@@ -897,8 +903,9 @@ def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos
     ctx_len, new_len [B] int32: cached and new tokens of every request; the
     pages that the new ones need are taken from free_ids at free_pos ([1]
     int32, or an earlier call's info[1:2]) on and written into
-    ``pages.dev`` (its host copy is brought up to date by
-    ``pages.sync_host()`` where a decode call needs it).  Returns (slots
+    ``pages.dev``.  The table's host copy is dropped, since the paged pack and
+    decode check it: they need ``pages.sync_host()`` after this call, and
+    after every replay of a graph that holds it.  Returns (slots
     [max_tokens], cu_new [B + 1], info [4] = status, next free_pos, pages
     taken, new tokens), all int32 on the GPU; see cpattn.h for the status."""
     i32, table = _i32t, pages.dev
@@ -921,6 +928,7 @@ def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos
                            slots.data_ptr(), max_tokens, cu_new.data_ptr(), info.data_ptr(), _raw_stream(dev))
     if st:
         _check(st)
+    pages.host = None
     return slots, cu_new, info
 
 

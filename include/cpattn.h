@@ -591,6 +591,8 @@ cp_status cp_mla_prefill_attn(const void* host_plan, const void* dev_plan, int r
  * -1 and, from free_ids, a table entry of -1.  The free list must name each
  * page once.  free_pos may be info + 1 of an earlier call, not of this one.
  * The call can be captured into a graph and replayed with new lengths.
+ * Only the device table changes: a host copy given to cp_decode_attn_paged or
+ * cp_kv_shard_pack_paged later has to be read back after this call (or replay).
  * Errors: C outside [1, CP_MAX_SHARDS]; B outside [1, CP_SLOTS_MAX_B];
  * page_size not a positive multiple of 64 (CP_ERR_UNSUPPORTED), max_pages,
  * num_pages < 1, a pool of 2^31 rows or more; n_free, max_tokens < 0.

@@ -166,3 +166,50 @@ def test_binding_checks(cp):
         cp.PageTable.on_device(torch.zeros(4, 2, dtype=torch.int32), 64, 8)
     with pytest.raises(ValueError, match="CUDA"):
         cp.cp_cache_append(i32, torch.zeros(2, 576), torch.zeros(64, 576))
+
+
+def host_only(monkeypatch, cp, **calls):
+    """The binding's own steps around calls that only record their arguments."""
+    b = cp._binding
+    monkeypatch.setattr(b, "_need", lambda name, t, *rest: t)
+    monkeypatch.setattr(b, "_device_index", lambda: -1)
+    monkeypatch.setattr(b, "_raw_stream", lambda index: None)
+    for name, status in calls.items():
+        monkeypatch.setattr(b.lib, name, lambda *a, status=status: status)
+
+
+@pytest.mark.parametrize("synced", [False, True])
+def test_page_slots_drops_the_host_copy(cp, monkeypatch, synced):
+    """The paged pack and decode check the host copy of a table: after a
+    slots call it no longer holds the table's ids, and both ask for sync_host()."""
+    import torch
+    host_only(monkeypatch, cp, cp_page_slots=0)
+    i32 = dict(dtype=torch.int32)
+    pages = cp.PageTable(np.zeros((4, 2)), 64, 8, device="cpu")
+    if synced:
+        pages.dev.fill_(3)
+        assert (pages.sync_host().host == 3).all()
+    out = dict(slots=torch.zeros(4, **i32), cu_new=torch.zeros(3, **i32), info=torch.zeros(4, **i32))
+    two = torch.zeros(2, **i32)
+    cp.cp_page_slots(pages, 2, two, two, two, two[:1], 4, **out)
+    plan = cp.cp_decode_plan(2, [5, 5], n_workers=2)
+    x = torch.zeros(10, 576, dtype=torch.bfloat16)
+    monkeypatch.setattr(cp._binding, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(cp._binding, "_stream", lambda d: None)
+    with pytest.raises(ValueError, match="sync_host"):
+        cp.cp_kv_shard_pack_paged(plan, pages, x, pool=x)
+    o = dict(o_part=torch.zeros(1), lse_part=torch.zeros(1), ws=torch.zeros(1))
+    with pytest.raises(ValueError, match="sync_host"):
+        cp.cp_decode_attn_paged(plan, pages, cp.CP_DECODE_MLA, torch.zeros(2, 1, 576, dtype=torch.bfloat16), x, sm_scale=1.0, **o)
+    pages.dev.fill_(5)
+    assert (pages.sync_host().host == 5).all()  # and have it from then on
+
+
+def test_page_slots_that_fails_keeps_the_host_copy(cp, monkeypatch):
+    import torch
+    host_only(monkeypatch, cp, cp_page_slots=INVALID)
+    pages = cp.PageTable(np.zeros((4, 2)), 64, 8, device="cpu")
+    two = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(cp.CpError):
+        cp.cp_page_slots(pages, 2, two, two, two, two[:1], 4, slots=two, cu_new=two, info=two)
+    assert (pages.host == 0).all()
