@@ -959,7 +959,7 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
     [pool_rows, ...] of the same row shape.  Pools of the rows' own dtype take
     them as they are (E4M3 codes with new_scale [n]); bf16 or fp32 rows into
     an E4M3 pool (uint8 or float8_e4m3fn) are quantised with one scale a
-    token, amax / 448 over its K and V, written to scale_pool [pool_rows]."""
+    token, amax / 448 over its K and V (at least 2^-149), written to scale_pool [pool_rows]."""
     dev = k_pool.get_device()
     n, rows = slots.shape[0], k_pool.shape[0]
     if not k_pool.is_cuda or not k_pool.is_contiguous():

@@ -342,8 +342,8 @@ __device__ __forceinline__ uint2 codes_of(const Piece<T>& x, float scale, float 
   return make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
-// Rows to E4M3 codes with one scale a token, amax / 448 (1 for a row of
-// zeros) over its K row and, where there is one, its V row: a warp a token,
+// Rows to E4M3 codes with one scale a token, amax / 448 (at least 2^-149; 1 for
+// a row of zeros) over its K row and, where there is one, its V row: a warp a token,
 // PIECES pieces of eight elements of each row a lane, kept in registers between
 // the maximum and the codes (PIECES = 0: any row length, read twice).
 template <typename T, int PIECES, bool HAS_V>
@@ -385,7 +385,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const Appen
       }
   }
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
-  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  // the quotient of an fp32 row below 224 x 2^-149 is 0, which would make codes
+  // of NaN out of its zeros: the least positive scale stands for such rows
+  const float scale = amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), 0x1p-149f) : 1.f;
   if (lane == 0) a.scale_pool[slot] = scale;
   const float inv = __frcp_rn(scale);
   const bool plain = !(scale >= 0x1p-80f && scale <= 0x1p100f);

@@ -623,7 +623,8 @@ cp_status cp_page_slots(int C, int B, const int32_t* ctx_len, const int32_t* new
  * pool_dtype == src_dtype: rows are copied (with CP_FP8_E4M3 also their
  *   scales new_scale [n] to scale_pool).
  * src_dtype CP_BF16 or CP_FP32 into CP_FP8_E4M3: scale_pool[slot] = amax / 448
- *   over the token's K and V row (1 for a row of zeros), code =
+ *   over the token's K and V row (at least 2^-149, where the quotient is below
+ *   fp32's least number; 1 for a row of zeros), code =
  *   round-to-nearest-even(x / scale); new_scale NULL.  Rows must be finite.
  * row_elems a multiple of 16; row bytes and strides in bytes multiples of 16.
  * ------------------------------------------------------------------------- */

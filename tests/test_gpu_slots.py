@@ -219,6 +219,27 @@ def test_append_quantises_any_scale(cp):
     assert torch.equal(sp, sc) and torch.equal(kp, kc)
 
 
+@pytest.mark.parametrize("row,with_v", [((64,), False), ((576,), False), ((8, 128), True), ((2048,), True)])
+def test_append_of_the_smallest_rows(cp, row, with_v):
+    """fp32 rows whose amax / 448 is no fp32 number, or one of its smallest, with
+    zeros of either sign among them: the scale is never 0 and a code never NaN."""
+    tiny = np.float32(2.0 ** -149)
+    sizes = np.asarray([1, 2, 7, 100, 223, 224, 225, 447, 448, 449, 900, 7000], np.float32) * tiny
+    n, m = len(sizes), int(np.prod(row))
+    base = np.resize(np.asarray([0.0, 1.0, -0.0, -1.0, 0.5, 0.0, -0.25], np.float32), (2, n, m))
+    k, v = (torch.from_numpy((x * sizes[:, None]).astype(np.float32).reshape(n, *row)) for x in base)
+    both = torch.cat([k.flatten(1), v.flatten(1)], 1).numpy() if with_v else k.flatten(1).numpy()
+    assert (np.abs(both).max(1) == sizes).all()
+    scale = np.maximum(sizes / np.float32(448), tiny)
+    want = torch.from_numpy(np.clip(both / scale[:, None], -448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    kp, sp = torch.full((n, *row), 77, dtype=torch.uint8, device=DEV), torch.zeros(n, device=DEV)
+    vp = torch.full_like(kp, 77) if with_v else None
+    cp.cp_cache_append(torch.arange(n, **I32), k.to(DEV), kp, v.to(DEV) if with_v else None, vp, sp)
+    got = torch.cat([kp.flatten(1), vp.flatten(1)], 1) if with_v else kp.flatten(1)
+    assert np.array_equal(sp.cpu().numpy(), scale) and torch.equal(got.cpu(), want)
+    assert not bool(((got & 127) == 127).any())
+
+
 @pytest.mark.parametrize("src", [torch.bfloat16, torch.float32])
 def test_append_keeps_the_sign_of_zero(cp, src):
     """Zeros of either sign, in rows of any scale and in a row of zeros."""
