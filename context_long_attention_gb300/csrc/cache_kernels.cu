@@ -67,8 +67,12 @@ __device__ __forceinline__ int pages_before(const PageCount& c, int r) {
   return min(r, c.m) * c.big + max(0, r - c.m) * c.small;
 }
 __device__ __forceinline__ int pages_of(const PageCount& c, int r) { return r < c.m ? c.big : c.small; }
-// Sums that stop at 2^31 - 1 (past every limit that they are compared with).
-__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, 0x7FFFFFFFu); }
+// Sums that stop at 2^32 - 1, past every limit that they are compared with
+// (limits are at most 2^31 - 1).
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
+  const uint32_t sum = a + b;
+  return sum < a ? 0xFFFFFFFFu : sum;
+}
 
 // VEC consecutive tokens a thread.
 template <int VEC>

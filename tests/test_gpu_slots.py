@@ -110,6 +110,22 @@ def test_slots_of_a_step_that_does_not_fit(cp, case):
     assert want[2][0] != 0 and info[0].item() == want[2][0]
 
 
+def test_slots_of_sums_past_31_bits(cp):
+    """Sums of tokens and of pages past 2^31 - 1 are over the largest limits,
+    too (the other reasons keep the step from taking anything either way)."""
+    table, most = torch.full((128, 2), -1, **I32), 2**31 - 1
+    slots, cu, info = cp.cp_page_slots(cp.PageTable.on_device(table[:3], 64, 100), 1, dev([0] * 3), dev([2**30] * 3),
+                                       dev(range(50)), dev([0]), most)
+    assert info.tolist() == [2 + 4 + 8, 0, 0, 0] and not cu.any()
+    assert all(bool((part == -1).all()) for part in slots.split(1 << 28))
+    del slots
+    free = torch.empty(most, **I32)  # never read
+    slots, cu, info = cp.cp_page_slots(cp.PageTable.on_device(table, 64, 100), 1, dev([0] * 128), dev([most] * 128),
+                                       free, dev([0]), 5)
+    assert info.tolist() == [2 + 4 + 8, 0, 0, 0] and not cu.any() and bool((slots == -1).all())
+    assert bool((table == -1).all())
+
+
 def test_slots_of_bad_page_ids(cp):
     """An id outside the pool gives no row in it."""
     step(cp, 2, [0, 10], [200, 300], 64, max_pages=8, num_pages=20, max_tokens=500, free=[3, 20, -5, 2**31 - 1, 19, 0, 1, 2, 4, 5])
