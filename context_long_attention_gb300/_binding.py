@@ -871,8 +871,8 @@ def cp_mla_prefill_attn(plan: PrefillPlan, q, kv, k_rope, sm_scale=None, rank: i
     _need("q", q, _bf16, (T, H, MLA_NOPE_DIM + MLA_ROPE_DIM), dev)
     _need("kv", kv, _bf16, (KV, H, MLA_NOPE_DIM + MLA_V_DIM), dev)
     rope, stride = _rows("k_rope", k_rope, MLA_ROPE_DIM, _bf16, dev)
-    if k_rope.shape[0] != KV:
-        raise ValueError(f"k_rope has {k_rope.shape[0]} rows, the plan {KV}")
+    if k_rope.shape != (KV, MLA_ROPE_DIM):  # a whole cache entry's first columns are its latent part
+        raise ValueError(f"k_rope: need {(KV, MLA_ROPE_DIM)}, got {tuple(k_rope.shape)}")
     if plan.dev is None or plan.dev.get_device() != dev:
         raise ValueError(f"the plan has no device part on {q.device}")
     if sm_scale is None:

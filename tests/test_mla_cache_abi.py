@@ -213,3 +213,20 @@ def test_page_slots_that_fails_keeps_the_host_copy(cp, monkeypatch):
     with pytest.raises(cp.CpError):
         cp.cp_page_slots(pages, 2, two, two, two, two[:1], 4, slots=two, cu_new=two, info=two)
     assert (pages.host == 0).all()
+
+
+def test_prefill_takes_the_rotated_columns_only(cp, monkeypatch):
+    """A k_rope of other columns or rows than the plan's [KV, 64], such as the
+    whole cache entries, is refused."""
+    import torch
+    host_only(monkeypatch, cp, cp_mla_prefill_attn=0)
+    monkeypatch.setattr(cp._binding, "_rows", lambda name, t, cols, dtype, dev: (t.data_ptr(), t.stride(0)))
+    plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [5], [3], device=None)
+    plan.dev = torch.from_numpy(plan.host)
+    bf = dict(dtype=torch.bfloat16)
+    q, kv, lat = torch.zeros(5, 2, 192, **bf), torch.zeros(8, 2, 256, **bf), torch.zeros(9, 576, **bf)
+    out = dict(out=torch.zeros(5, 2, 128, **bf), lse=torch.zeros(5, 2))
+    cp.cp_mla_prefill_attn(plan, q, kv, lat[:8, 512:], **out)
+    for rope in (lat[:8], lat[:8, 448:], lat[:8, 520:], lat[:, 512:], lat[:7, 512:]):
+        with pytest.raises(ValueError, match="k_rope"):
+            cp.cp_mla_prefill_attn(plan, q, kv, rope, **out)
