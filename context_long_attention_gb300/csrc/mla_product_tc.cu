@@ -30,6 +30,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <stdlib.h>
 
 #include "early_launch.cuh"
 #include "internal.h"
@@ -74,6 +75,7 @@ struct Params {
   int n_tokens;
   unsigned* status;
   unsigned long long wait_ns;
+  int stall_test;  // test hook: the issuer waits on a barrier that nobody arrives at yet
 };
 
 __device__ void report_timeout(unsigned* status, unsigned site, volatile int* abort) {
@@ -226,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id = idesc_bf16_f32(BM, NB, 0, MODE == kAbsorb ? 1 : 0);
     int g = 0, n = 0;
     unsigned bad = 0;
+    if (p.stall_test && !wait_all(smem_u32(&bar_drain), 0)) bad = 7;
     for (int i = blockIdx.x; i < p.n_items && !bad; i += gridDim.x, ++n) {
       const int acc = n & 1;
       if (n >= 2 && !wait_all(smem_u32(&bar_free[acc]), (n / 2 - 1) & 1)) bad = 2;
@@ -351,6 +354,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __shared__ __align__(8) uint64_t bar_acc[2], bar_free[2], bar_drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag, zero_flag;
+  __shared__ int issued[2];  // pieces of W and of the tokens that this CTA's producer has asked for
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = (int)cluster_ctarank();
   const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
@@ -389,10 +393,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag)) != 0;
   };
+  auto give_up = [&](unsigned site) {  // both CTAs stop, and both know it when they meet
+    report_timeout(p.status, site, &abort_flag);
+    st_cluster(map_to_rank(smem_u32(const_cast<int*>(&abort_flag)), cta ^ 1), 1);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    int g = 0, tiles = 0, tile = -1;
+    int g = 0, pieces = 0, tiles = 0, tile = -1;
     bool ok = true;
     for (int i = first; i < last && ok; ++i) {
       const int h = i % p.H;
@@ -408,6 +416,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                              map_to_rank(smem_u32(&bar_a[k]), 0));
           }
           __syncwarp();
+          ++pieces;
         }
         const int s = g % kWStages;
         if (g >= kWStages) ok = wait_all(&bar_wfree[s], (g / kWStages - 1) & 1);
@@ -421,15 +430,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       if (fresh) ++tiles;
     }
-    if (!ok && lane == 0) report_timeout(p.status, 11, &abort_flag);
-    // Never leave with a copy in flight: the products of the last stages waited
-    // for both halves, and the CTAs leave together (a barrier of the cluster
-    // after the issuer has drained).  Where a wait ran out, wait here too.
-    if (!ok && cta == 0) {
-      for (int k = max(0, g - kWStages); k < g; ++k)
-        mbar_wait(smem_u32(&bar_w[k % kWStages]), (k / kWStages) & 1, 100000000ull, &zero_flag);
-      __syncwarp();
+    if (!ok && lane == 0) give_up(11);
+    if (lane == 0) {
+      issued[0] = g;
+      issued[1] = pieces;
     }
+    __syncwarp();
   } else if (warp == 1 && cta == 0) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t id = idesc_bf16_f32(2 * BM, kHeadRows, 0, 0);
@@ -438,6 +444,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     int s = 0, tiles = 0, head = first % p.H;
     uint32_t phase = 0;  // of the W stages
     bool fresh = true;
+    if (p.stall_test && !wait_all(&bar_drain, 0)) bad = 16;
     for (int n = 0; n < last - first && !bad; ++n) {
       const int acc = n & 1;
       const bool leave = head + 1 == p.H;  // this tile's last head
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       fresh = leave;
       head = leave ? 0 : head + 1;
     }
-    if (bad && lane == 0) report_timeout(p.status, bad, &abort_flag);
+    if (bad && lane == 0) give_up(bad);
     if (elect_one()) mma_commit_pair(smem_u32(&bar_drain));
     __syncwarp();
     mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
@@ -483,7 +490,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int acc = n & 1, tile = i / p.H;
       const bool got = wait_all(&bar_acc[acc], (n / 2) & 1);
       if (bar_red_or(3, 128, !got)) {
-        if (!got && lane == 0) report_timeout(p.status, 15, &abort_flag);
+        if (!got && lane == 0) give_up(15);
         break;
       }
       tc_fence_after();
@@ -499,6 +506,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();  // neither CTA leaves while products read its memory
   tc_fence_after();
+  // Nor with a copy in flight: products waited for every piece, unless a wait ran
+  // out in either CTA.  Then both stay until the last pieces that either asked for
+  // have landed (the barriers of the even CTA count both halves; where only one
+  // half was asked for, until it has had far more time than a copy takes).
+  if (__any_sync(0xffffffffu, abort_flag)) {
+    if (cta == 0 && warp == 0) {
+      const uint32_t other = map_to_rank(smem_u32(issued), 1);
+      const int w = max(issued[0], (int)ld_cluster(other)), a = max(issued[1], (int)ld_cluster(other + 4));
+      for (int k = max(0, w - kWStages); k < w; ++k)
+        mbar_wait(smem_u32(&bar_w[k % kWStages]), (k / kWStages) & 1, 10000000ull, &zero_flag);
+      for (int k = max(0, a - kPieces); k < a; ++k)
+        mbar_wait(smem_u32(&bar_a[k % kPieces]), (k / kPieces) & 1, 10000000ull, &zero_flag);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
@@ -541,6 +564,12 @@ bool token_map(CUtensorMap* m, const void* x, int n, int H, int row) {
   return encode_tensor_map_bf16(m, x, 3, dims, strides, box);
 }
 
+Params params(int n, int H) {
+  const char* stall = getenv("CPATTN_TEST_STALL");  // the test hook of cp_prefill_attn
+  const bool stall_test = stall && stall[0] == '1';
+  return {H, 0, n, device_status_ptr(), stall_test ? 50000000ull : wait_limit_ns(), stall_test};
+}
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -552,7 +581,7 @@ int sm_count() {
 
 cudaError_t launch_mla_expand(const void* latent, long long stride, const void* w, int T, int H, void* kv,
                               cudaStream_t s) {
-  Params p = {H, 0, T, device_status_ptr(), wait_limit_ns()};
+  Params p = params(T, H);
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
   CUtensorMap am, wm, om;
@@ -574,7 +603,7 @@ cudaError_t launch_mla_expand(const void* latent, long long stride, const void* 
 
 cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* ql, cudaStream_t s) {
   if (n <= kMlaSmall) return launch_mla_absorb_small(q, w, n, H, ql, s);
-  Params p = {H, 0, n, device_status_ptr(), wait_limit_ns()};
+  Params p = params(n, H);
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
   CUtensorMap am, wm, om;
@@ -586,7 +615,7 @@ cudaError_t launch_mla_absorb(const void* q, const void* w, int n, int H, void* 
 
 cudaError_t launch_mla_project(const void* ol, const void* w, int n, int H, void* o, cudaStream_t s) {
   if (n <= kMlaSmall) return launch_mla_project_small(ol, w, n, H, o, s);
-  Params p = {H, 0, n, device_status_ptr(), wait_limit_ns()};
+  Params p = params(n, H);
   const int sms = sm_count();
   if (!p.status || !sms) return cudaErrorInvalidDevice;
   CUtensorMap am, wm, om;

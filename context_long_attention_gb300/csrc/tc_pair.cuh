@@ -21,6 +21,16 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// A word of shared memory of any CTA of the cluster (mapped addresses), ordered
+// by the cluster's barrier.
+__device__ __forceinline__ void st_cluster(uint32_t mapped, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapped), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t mapped) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapped) : "memory");
+  return v;
+}
 // Arrives at an mbarrier of any CTA of the cluster (a mapped address).  What
 // the arrival publishes here is tensor memory (ordered by the tcgen05 fences)
 // and shared memory for the async proxy (ordered by its proxy fence), so the

@@ -293,6 +293,33 @@ def test_prefill_reports_a_wait_that_runs_out(cp, monkeypatch, n):
     check_prefill(plan, ref, new, prefix, q, kv, rope, o, lse, "after the timeout")
 
 
+@pytest.mark.parametrize("op,n,H", [("expand", 300, 3), ("expand", 2560, 32), ("expand", 2400, 33), ("absorb", 5, 2), ("absorb", 700, 64),
+                                    ("project", 37, 3), ("project", 1000, 64)])
+def test_products_report_a_wait_that_runs_out(cp, monkeypatch, op, n, H):
+    """The same for the products: single CTAs with one item and with several,
+    and pairs (76 of them, whole and ragged runs of heads).  What a call that
+    gave up leaves is not looked at; the next one's result is the earlier one's."""
+    w = weights(H, 1)
+    x = randn((n, 576) if op == "expand" else (n, H, 192 if op == "absorb" else 512), 2)
+
+    def call():
+        return cp.cp_mla_expand(x[:, :512], w) if op == "expand" else getattr(cp, f"cp_mla_{op}")(x, w)
+
+    before = call()
+    cp.cp_device_error_check()
+    for _ in range(2):
+        monkeypatch.setenv("CPATTN_TEST_STALL", "1")
+        call()
+        with pytest.raises(cp.CpError) as e:
+            cp.cp_device_error_check()
+        assert e.value.status == -4 and "kernel 8" in str(e.value)
+        monkeypatch.delenv("CPATTN_TEST_STALL")
+        cp.cp_device_error_check()
+        after = call()
+        cp.cp_device_error_check()
+        assert torch.equal(before, after)
+
+
 def test_calls_on_two_streams_at_once(cp):
     """Prefill, expansion and products of two batches side by side give what
     they give alone."""
