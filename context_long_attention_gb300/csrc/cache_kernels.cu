@@ -446,7 +446,10 @@ cudaError_t launch_page_slots(const PageSlotsArgs& a, cudaStream_t s) {
   const size_t smem = (size_t)(2 * a.B + 1) * sizeof(int32_t);
   auto kern = vec ? page_slots_kernel<4> : page_slots_kernel<1>;
   if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the most that any call needs: a limit of this call's own would be another
+    // thread's for a moment, and refuse its launch
+    constexpr int kMost = (2 * CP_SLOTS_MAX_B + 1) * (int)sizeof(int32_t);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   return launch_early(kern, grid, kSlotThreads, smem, s, 1, p);

@@ -6,6 +6,7 @@ rule itself in fp32 (scale = amax / 448, code = rn(x / scale)), code by code.
 """
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -129,6 +130,36 @@ def test_slots_of_sums_past_31_bits(cp):
 def test_slots_of_bad_page_ids(cp):
     """An id outside the pool gives no row in it."""
     step(cp, 2, [0, 10], [200, 300], 64, max_pages=8, num_pages=20, max_tokens=500, free=[3, 20, -5, 2**31 - 1, 19, 0, 1, 2, 4, 5])
+
+
+def test_slots_of_batches_of_different_size_at_once(cp):
+    """Host threads whose batches need different amounts of shared memory: no
+    launch is refused, and each gets its own slots."""
+    bad = []
+
+    def work(B, n=4000):
+        pages = cp.PageTable.on_device(torch.full((B, 4), -1, **I32), 64, 4 * B)
+        ctx, new, free, pos = torch.zeros(B, **I32), torch.ones(B, **I32), torch.arange(4 * B, **I32), torch.zeros(1, **I32)
+        slots, cu, info = torch.empty(B, **I32), torch.empty(B + 1, **I32), torch.empty(4, **I32)
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        args = (1, B, ctx.data_ptr(), new.data_ptr(), pages.dev.data_ptr(), 4, 64, 4 * B, free.data_ptr(), 4 * B, pos.data_ptr(),
+                slots.data_ptr(), B, cu.data_ptr(), info.data_ptr(), stream.cuda_stream)
+        for _ in range(n):  # the library's call by itself: the threads meet in it
+            status = cp.lib.cp_page_slots(*args)
+            if status:
+                bad.append((B, status, cp.lib.cp_last_error()))
+                break
+        stream.synchronize()
+        if not torch.equal(slots, torch.arange(B, **I32) * 64):
+            bad.append((B, "slots"))
+
+    threads = [threading.Thread(target=work, args=(B,)) for B in (8192, 5200, 8192, 5200, 8192, 100)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
 
 
 def test_slots_follow_their_lengths_in_a_graph(cp):
