@@ -737,9 +737,13 @@ cudaError_t launch_topk_local(const int32_t* dev_plan, const cp_plan_header& h, 
   const int pairs = h.C * h.R;
   // room to stage the longest pair's scores, up to kStageScores (longer pairs read from L2)
   const int cap = max_pair_rows < kStageScores ? max_pair_rows : kStageScores;
-  const int smem = (int)sizeof(SelectSmem) + 2 * kStageWords * (int)sizeof(uint32_t) +
-                   (cap + 3 + 127) / 128 * 128 * (int)sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(topk_local_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int kBase = (int)sizeof(SelectSmem) + 2 * kStageWords * (int)sizeof(uint32_t);
+  auto staged = [](int rows) { return (rows + 3 + 127) / 128 * 128 * (int)sizeof(float); };
+  const int smem = kBase + staged(cap);
+  // the most that any call needs: a limit of this call's own would be another
+  // thread's for a moment, and refuse its launch
+  cudaError_t e = cudaFuncSetAttribute(topk_local_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kBase + staged(kStageScores));
   if (e != cudaSuccess) return e;
   topk_local_kernel<<<pairs, kThreads, smem, s>>>(dev_plan, h.R, h.off_rank, scores, k, cap, cand_keys,
                                                   cand_n, range);

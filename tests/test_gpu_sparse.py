@@ -4,7 +4,9 @@ against the oracle's local-lists-then-merge (and brute force), the owners'
 selection buffers bit-exact, and the sparse attention's partials and merged
 result against the oracle."""
 
+import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -282,3 +284,35 @@ def test_sparse_decode_full_size_sampled(cp):
         fo, fl = oracle.decode_attention(np64(data["q"][b]), K, V, scale, keys=np.asarray(want))
         check_o(o[b], fo, what=f"full-size sparse b{b}", **TOL_FP8)
         check_lse(lse[b], fl)
+
+
+def test_topk_of_contexts_of_different_length_at_once(cp):
+    """Host threads whose pairs need different amounts of shared memory: no
+    launch is refused, and each gets its own selection."""
+    bad, k = [], 64
+
+    def work(L, n=4000):
+        plan = cp.cp_decode_plan(1, [L], device=DEV)
+        scores = torch.arange(L, dtype=torch.float32, device=DEV)
+        sel, cnt = torch.empty((1, k), dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+        size = cp.cp_sparse_workspace_size(plan, k)
+        ws, ptr = torch.empty(size, dtype=torch.uint8, device=DEV), (ctypes.c_void_p * 1)(scores.data_ptr())
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        args = (plan.host.ctypes.data, plan.dev.data_ptr(), ptr, k, sel.data_ptr(), cnt.data_ptr(), ws.data_ptr(), size,
+                stream.cuda_stream)
+        for _ in range(n):  # the library's call by itself: the threads meet in it
+            status = cp.lib.cp_sparse_topk(*args)
+            if status:
+                bad.append((L, status, cp.lib.cp_last_error()))
+                break
+        stream.synchronize()
+        if sel[0].tolist() != list(range(L - k, L)):
+            bad.append((L, "selection"))
+
+    threads = [threading.Thread(target=work, args=(L,)) for L in (100, 20000, 33000, 300, 10000, 64)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
