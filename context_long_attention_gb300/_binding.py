@@ -755,8 +755,8 @@ def cp_sparse_decode_attn_merged(plan: DecodePlan, pair_count, mode: int, q, sel
 #
 # These calls are as short as a decode step's kernels (a few us), so their
 # checks are one comparison chain a tensor, a message is only put together once
-# one of them fails, and stream, device and outputs come from torch's own short
-# paths where it has them (an output costs 1.4 us instead of 3.7 beside a launch).
+# one of them fails, and stream and device come from torch's own short paths
+# where it has them.
 
 LATENT_DIM, MLA_NOPE_DIM, MLA_ROPE_DIM, MLA_V_DIM = 512, 128, 64, 128
 _bf16, _i32t = torch.bfloat16, torch.int32
@@ -795,11 +795,6 @@ def _rows(name, t, cols, dtype, device):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-try:
-    _empty = torch._C._dynamo.guards._empty_strided_cuda
-except AttributeError:
-    def _empty(shape, strides, dtype):
-        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
 
 def _on(device, fn, *args):
@@ -820,7 +815,7 @@ def cp_mla_expand(latent, w_kv, out=None):
     if dev != _device_index():
         return _on(dev, cp_mla_expand, latent, w_kv, out)
     cols = MLA_NOPE_DIM + MLA_V_DIM
-    out = _empty((T, H, cols), (H * cols, cols, 1), _bf16) if out is None else _need("out", out, _bf16, (T, H, cols), dev)
+    out = torch.empty((T, H, cols), dtype=_bf16, device=latent.device) if out is None else _need("out", out, _bf16, (T, H, cols), dev)
     st = lib.cp_mla_expand(ptr, stride, w_kv.data_ptr(), T, H, out.data_ptr(), _raw_stream(dev))
     if st:
         _check(st)
@@ -836,12 +831,7 @@ def _per_head(name, x, w_kv, cols, out_cols, out, fn):
     if dev != _device_index():
         return _on(dev, _per_head, name, x, w_kv, cols, out_cols, out, fn)
     shape = (*lead, H, out_cols)
-    if out is not None:
-        _need("out", out, _bf16, shape, dev)
-    elif len(lead) == 1:
-        out = _empty(shape, (H * out_cols, out_cols, 1), _bf16)
-    else:
-        out = torch.empty(shape, dtype=_bf16, device=x.device)
+    out = torch.empty(shape, dtype=_bf16, device=x.device) if out is None else _need("out", out, _bf16, shape, dev)
     st = fn(x.data_ptr(), w_kv.data_ptr(), lead.numel(), H, out.data_ptr(), _raw_stream(dev))
     if st:
         _check(st)
@@ -880,9 +870,9 @@ def cp_mla_prefill_attn(plan: PrefillPlan, q, kv, k_rope, sm_scale=None, rank: i
     if dev != _device_index():
         return _on(dev, cp_mla_prefill_attn, plan, q, kv, k_rope, sm_scale, rank, out, lse)
     rows = T if rank < 0 else plan.rank_rows(rank)
-    out = _empty((rows, H, MLA_V_DIM), (H * MLA_V_DIM, MLA_V_DIM, 1), _bf16) if out is None else \
+    out = torch.empty((rows, H, MLA_V_DIM), dtype=_bf16, device=q.device) if out is None else \
         _need("out", out, _bf16, (rows, H, MLA_V_DIM), dev)
-    lse = _empty((rows, H), (H, 1), torch.float32) if lse is None else \
+    lse = torch.empty((rows, H), dtype=torch.float32, device=q.device) if lse is None else \
         _need("lse", lse, torch.float32, (rows, H), dev)
     st = lib.cp_mla_prefill_attn(plan.host_ptr, plan.dev.data_ptr(), rank, q.data_ptr(), kv.data_ptr(), rope, stride,
                                  H, sm_scale, out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
@@ -920,9 +910,10 @@ def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos
     _need("free_pos", free_pos, i32, (1,), dev)
     if dev != _device_index():
         return _on(dev, cp_page_slots, pages, C, ctx_len, new_len, free_ids, free_pos, max_tokens, slots, cu_new, info)
-    slots = _empty((max_tokens,), (1,), i32) if slots is None else _need("slots", slots, i32, (max_tokens,), dev)
-    cu_new = _empty((B + 1,), (1,), i32) if cu_new is None else _need("cu_new", cu_new, i32, (B + 1,), dev)
-    info = _empty((4,), (1,), i32) if info is None else _need("info", info, i32, (4,), dev)
+    where = table.device
+    slots = torch.empty(max_tokens, dtype=i32, device=where) if slots is None else _need("slots", slots, i32, (max_tokens,), dev)
+    cu_new = torch.empty(B + 1, dtype=i32, device=where) if cu_new is None else _need("cu_new", cu_new, i32, (B + 1,), dev)
+    info = torch.empty(4, dtype=i32, device=where) if info is None else _need("info", info, i32, (4,), dev)
     st = lib.cp_page_slots(C, B, ctx_len.data_ptr(), new_len.data_ptr(), table.data_ptr(), pages.max_pages,
                            pages.page_size, pages.num_pages, free_ids.data_ptr(), n_free, free_pos.data_ptr(),
                            slots.data_ptr(), max_tokens, cu_new.data_ptr(), info.data_ptr(), _raw_stream(dev))

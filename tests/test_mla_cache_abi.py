@@ -230,3 +230,36 @@ def test_prefill_takes_the_rotated_columns_only(cp, monkeypatch):
     for rope in (lat[:8], lat[:8, 448:], lat[:8, 520:], lat[:, 512:], lat[:7, 512:]):
         with pytest.raises(ValueError, match="k_rope"):
             cp.cp_mla_prefill_attn(plan, q, kv, rope, **out)
+
+
+def test_outputs_come_from_torch(cp, monkeypatch):
+    """The calls' own outputs are made through torch's dispatcher, on their
+    inputs' device: a mode sees them."""
+    import torch
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Made(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            if func is torch.ops.aten.empty.memory_format:
+                self.made.append(out)
+            return out
+
+    host_only(monkeypatch, cp, cp_page_slots=0, cp_mla_expand=0, cp_mla_absorb=0, cp_mla_project=0, cp_mla_prefill_attn=0)
+    monkeypatch.setattr(cp._binding, "_rows", lambda name, t, cols, dtype, dev: (t.data_ptr(), t.stride(0)))
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [5], [3], device=None)
+    plan.dev = torch.from_numpy(plan.host)
+    pages, two = cp.PageTable(np.zeros((4, 2)), 64, 8, device="cpu"), torch.zeros(2, **i32)
+    w, lat = torch.zeros(2, 256, 512, **bf), torch.zeros(8, 576, **bf)
+    q, kv = torch.zeros(5, 2, 192, **bf), torch.zeros(8, 2, 256, **bf)
+    mode = Made()
+    mode.made = []
+    with mode:
+        got = [cp.cp_mla_expand(lat, w), cp.cp_mla_absorb(q, w), cp.cp_mla_absorb(q[None], w), cp.cp_mla_project(torch.zeros(2, 512, **bf), w),
+               *cp.cp_mla_prefill_attn(plan, q, kv, lat[:, 512:]), *cp.cp_mla_prefill_attn(plan, q, kv, lat[:, 512:], rank=1),
+               *cp.cp_page_slots(pages, 2, two, two, two, two[:1], 7)]
+    want = [((8, 2, 256), bf), ((5, 2, 576), bf), ((1, 5, 2, 576), bf), ((2, 128), bf), ((5, 2, 128), bf), ((5, 2), dict(dtype=torch.float32)),
+            ((plan.rank_rows(1), 2, 128), bf), ((plan.rank_rows(1), 2), dict(dtype=torch.float32)), ((7,), i32), ((3,), i32), ((4,), i32)]
+    assert [(tuple(t.shape), dict(dtype=t.dtype)) for t in got] == want
+    assert all(t.is_contiguous() and any(t.data_ptr() == m.data_ptr() for m in mode.made) for t in got)
