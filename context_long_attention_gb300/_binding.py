@@ -792,6 +792,8 @@ def _rows(name, t, cols, dtype, device):
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
 
 
+_MAX_COUNT = 2**31 - 1  # of the C interface; ctypes would pass a larger one's low 32 bits
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -903,6 +905,8 @@ def cp_page_slots(pages: PageTable, C: int, ctx_len, new_len, free_ids, free_pos
         raise ValueError("the page table has no device copy")
     dev = table.get_device()
     B, n_free = ctx_len.shape[0], free_ids.shape[0]
+    if max_tokens > _MAX_COUNT or n_free > _MAX_COUNT:
+        raise ValueError(f"max_tokens={max_tokens}, n_free={n_free}: at most 2^31 - 1")
     _need("page table", table, i32, (C * B, pages.max_pages), dev)
     _need("ctx_len", ctx_len, i32, (B,), dev)
     _need("new_len", new_len, i32, (B,), dev)
@@ -953,6 +957,8 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
     token, amax / 448 over its K and V (at least 2^-149), written to scale_pool [pool_rows]."""
     dev = k_pool.get_device()
     n, rows = slots.shape[0], k_pool.shape[0]
+    if n > _MAX_COUNT:
+        raise ValueError(f"{n} slots: at most 2^31 - 1")
     if not k_pool.is_cuda or not k_pool.is_contiguous():
         raise ValueError("k_pool must be a contiguous CUDA tensor")
     _need("slots", slots, _i32t, (n,), dev)

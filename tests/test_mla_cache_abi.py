@@ -263,3 +263,20 @@ def test_outputs_come_from_torch(cp, monkeypatch):
             ((plan.rank_rows(1), 2, 128), bf), ((plan.rank_rows(1), 2), dict(dtype=torch.float32)), ((7,), i32), ((3,), i32), ((4,), i32)]
     assert [(tuple(t.shape), dict(dtype=t.dtype)) for t in got] == want
     assert all(t.is_contiguous() and any(t.data_ptr() == m.data_ptr() for m in mode.made) for t in got)
+
+
+def test_counts_past_31_bits(cp, monkeypatch):
+    """Counts that the C interface cannot hold are refused, not cut to 32 bits."""
+    import torch
+    host_only(monkeypatch, cp, cp_page_slots=0, cp_cache_append=0)
+    pages, two = cp.PageTable(np.zeros((4, 2)), 64, 8, device="cpu"), torch.zeros(2, dtype=torch.int32)
+    out = dict(slots=two, cu_new=two, info=two)
+    for n in (2**31, 2**32 + 5):
+        many = two[:1].expand(n)
+        with pytest.raises(ValueError, match="max_tokens"):
+            cp.cp_page_slots(pages, 2, two, two, two, two[:1], n, **out)
+        with pytest.raises(ValueError, match="n_free"):
+            cp.cp_page_slots(pages, 2, two, two, many, two[:1], 4, **out)
+        assert pages.host is not None
+        with pytest.raises(ValueError, match="slots"):
+            cp.cp_cache_append(many, torch.zeros(1, 16).expand(n, 16), torch.zeros(64, 16))
