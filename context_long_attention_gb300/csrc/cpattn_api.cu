@@ -174,16 +174,19 @@ cp_status build_prefill_plan(cp_strategy strategy, int C, int R, const int32_t* 
   // segments), of 256 and of 512 queries: most keys first, since a step of the
   // kernel takes as long for one query as for a full tile.
   std::vector<cp_req_tile> req_tiles;
+  req_tiles.reserve(2 * tiles.size());
   int n_req_tiles = 0;
   for (int size : {kPrefillTileRows, 2 * kPrefillTileRows}) {
     const size_t first = req_tiles.size();
-    for (int j = 0; j < R; ++j)
-      for (long long off = 0; off < new_len[j]; off += size) req_tiles.push_back({j, (int32_t)off, req[j], {0, 0}});
+    for (int j = 0; j < R; ++j)  // a request's last tile first: one request's tiles need no sorting
+      for (int off = (new_len[j] - 1) / size * size; off >= 0 && new_len[j] > 0; off -= size)
+        req_tiles.push_back({j, off, req[j], {0, 0}});
     auto keys = [&](const cp_req_tile& t) {
       return t.r.prefix_len + std::min((long long)t.r.new_len, (long long)t.q_off + size);
     };
-    std::stable_sort(req_tiles.begin() + first, req_tiles.end(),
-                     [&](const cp_req_tile& a, const cp_req_tile& b) { return keys(a) > keys(b); });
+    auto before = [&](const cp_req_tile& a, const cp_req_tile& b) { return keys(a) > keys(b); };
+    if (!std::is_sorted(req_tiles.begin() + first, req_tiles.end(), before))
+      std::stable_sort(req_tiles.begin() + first, req_tiles.end(), before);
     if (!first) n_req_tiles = (int)req_tiles.size();
   }
   std::vector<int32_t> rank_tile_off(C + 1, 0);
