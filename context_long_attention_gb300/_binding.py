@@ -407,7 +407,9 @@ class PageTable:
         return self.num_pages * self.page_size
 
 
-def _host_table(pages: PageTable):
+def _host_table(pages: PageTable, plan):
+    if pages.host is not None and pages.host.shape[0] < plan.C * plan.R:
+        raise ValueError(f"the page table has {pages.host.shape[0]} rows, the plan C * R = {plan.C * plan.R} pairs")
     if pages.host is None:
         raise ValueError("the page table has no host copy of its present ids: call sync_host() first")
     return _np_ptr(pages.host)
@@ -428,7 +430,7 @@ def cp_kv_shard_pack_paged(plan: DecodePlan, pages: PageTable, kv, kv_scale=None
     _check(lib.cp_kv_shard_pack_paged(_np_ptr(plan.host), _ptr(plan.dev), _dtype_code(kv), _ptr(kv),
                                       _ptr(kv_scale), row_elems, _ptr(pool),
                                       _ptr(scale_pool) if kv_scale is not None else None,
-                                      _host_table(pages), _ptr(pages.dev), pages.max_pages,
+                                      _host_table(pages, plan), _ptr(pages.dev), pages.max_pages,
                                       pages.page_size, pages.num_pages, _stream(kv.device)))
     return pool, (scale_pool if kv_scale is not None else None)
 
@@ -457,7 +459,7 @@ def cp_decode_attn_paged(plan: DecodePlan, pages: PageTable, mode: int, q, k_poo
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.cp_decode_attn_paged(_np_ptr(plan.host), _ptr(plan.dev), mode, kv_dtype, _ptr(q),
-                                    _ptr(kp), _ptr(v_pool), _ptr(scale_pool), _host_table(pages),
+                                    _ptr(kp), _ptr(v_pool), _ptr(scale_pool), _host_table(pages, plan),
                                     _ptr(pages.dev), pages.max_pages, pages.page_size,
                                     pages.num_pages, H, Hkv, Dqk, Dv, float(sm_scale), _ptr(o_part),
                                     _ptr(lse_part), _ptr(ws), ws_bytes, _stream(q.device)))

@@ -280,3 +280,29 @@ def test_counts_past_31_bits(cp, monkeypatch):
         assert pages.host is not None
         with pytest.raises(ValueError, match="slots"):
             cp.cp_cache_append(many, torch.zeros(1, 16).expand(n, 16), torch.zeros(64, 16))
+
+
+def test_paged_calls_need_a_row_for_every_pair(cp, monkeypatch):
+    """A table of a smaller batch than the plan's is refused by the paged pack and
+    decode (the library reads a row of both copies for every pair)."""
+    import torch
+    b = cp._binding
+    monkeypatch.setattr(b, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(b, "_stream", lambda d: None)
+    monkeypatch.setattr(b, "_ptr", lambda t: None)
+    monkeypatch.setattr(b.lib, "cp_kv_shard_pack_paged", lambda *a: 0)
+    monkeypatch.setattr(b.lib, "cp_decode_attn_paged", lambda *a: 0)
+    plan = cp.cp_decode_plan(2, [5, 5, 9], n_workers=2)
+    x, q = torch.zeros(19, 576, dtype=torch.bfloat16), torch.zeros(3, 1, 576, dtype=torch.bfloat16)
+    pool = torch.zeros(8 * 64, 576, dtype=torch.bfloat16)
+    o = dict(o_part=torch.zeros(1), lse_part=torch.zeros(1), ws=torch.zeros(1))
+    for rows in (6, 8):
+        pages = cp.PageTable(np.zeros((rows, 2)), 64, 8, device="cpu")
+        cp.cp_kv_shard_pack_paged(plan, pages, x, pool=pool)
+        cp.cp_decode_attn_paged(plan, pages, cp.CP_DECODE_MLA, q, pool, sm_scale=1.0, **o)
+    for rows in (1, 4, 5):
+        pages = cp.PageTable(np.zeros((rows, 2)), 64, 8, device="cpu")
+        with pytest.raises(ValueError, match="6 pairs"):
+            cp.cp_kv_shard_pack_paged(plan, pages, x, pool=pool)
+        with pytest.raises(ValueError, match="6 pairs"):
+            cp.cp_decode_attn_paged(plan, pages, cp.CP_DECODE_MLA, q, pool, sm_scale=1.0, **o)
