@@ -407,11 +407,16 @@ class PageTable:
         return self.num_pages * self.page_size
 
 
-def _host_table(pages: PageTable, plan):
-    if pages.host is not None and pages.host.shape[0] < plan.C * plan.R:
-        raise ValueError(f"the page table has {pages.host.shape[0]} rows, the plan C * R = {plan.C * plan.R} pairs")
+def _host_table(pages: PageTable, plan, **pools):
+    """The host copy's address: what the library checks; it cannot check that
+    the table has a row for every pair and the pools one for every page's."""
     if pages.host is None:
         raise ValueError("the page table has no host copy of its present ids: call sync_host() first")
+    if pages.host.shape[0] < plan.C * plan.R:
+        raise ValueError(f"the page table has {pages.host.shape[0]} rows, the plan C * R = {plan.C * plan.R} pairs")
+    for name, t in pools.items():
+        if t is not None and t.shape[0] < pages.pool_rows:
+            raise ValueError(f"{name} has {t.shape[0]} rows, the page table's pool {pages.pool_rows}")
     return _np_ptr(pages.host)
 
 
@@ -427,10 +432,11 @@ def cp_kv_shard_pack_paged(plan: DecodePlan, pages: PageTable, kv, kv_scale=None
         pool = torch.empty((pages.pool_rows, *kv.shape[1:]), dtype=kv.dtype, device=kv.device)
     if kv_scale is not None and scale_pool is None:
         scale_pool = torch.empty((pages.pool_rows,), dtype=torch.float32, device=kv.device)
+    table = _host_table(pages, plan, pool=pool, scale_pool=scale_pool if kv_scale is not None else None)
     _check(lib.cp_kv_shard_pack_paged(_np_ptr(plan.host), _ptr(plan.dev), _dtype_code(kv), _ptr(kv),
                                       _ptr(kv_scale), row_elems, _ptr(pool),
                                       _ptr(scale_pool) if kv_scale is not None else None,
-                                      _host_table(pages, plan), _ptr(pages.dev), pages.max_pages,
+                                      table, _ptr(pages.dev), pages.max_pages,
                                       pages.page_size, pages.num_pages, _stream(kv.device)))
     return pool, (scale_pool if kv_scale is not None else None)
 
@@ -441,6 +447,7 @@ def cp_decode_attn_paged(plan: DecodePlan, pages: PageTable, mode: int, q, k_poo
     k_pool / v_pool [pool_rows, Hkv, D] for GQA)."""
     lead, H, Dqk = _decode_shapes(plan, q)
     _need_cuda(q, k_pool)
+    table = _host_table(pages, plan, k_pool=k_pool, v_pool=v_pool, scale_pool=scale_pool)
     kp = k_pool.view(torch.uint8) if k_pool.dtype == torch.float8_e4m3fn else k_pool
     kv_dtype = _dtype_code(kp)
     if mode == CP_DECODE_MLA:
@@ -459,7 +466,7 @@ def cp_decode_attn_paged(plan: DecodePlan, pages: PageTable, mode: int, q, k_poo
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.cp_decode_attn_paged(_np_ptr(plan.host), _ptr(plan.dev), mode, kv_dtype, _ptr(q),
-                                    _ptr(kp), _ptr(v_pool), _ptr(scale_pool), _host_table(pages, plan),
+                                    _ptr(kp), _ptr(v_pool), _ptr(scale_pool), table,
                                     _ptr(pages.dev), pages.max_pages, pages.page_size,
                                     pages.num_pages, H, Hkv, Dqk, Dv, float(sm_scale), _ptr(o_part),
                                     _ptr(lse_part), _ptr(ws), ws_bytes, _stream(q.device)))

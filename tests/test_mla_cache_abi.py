@@ -306,3 +306,31 @@ def test_paged_calls_need_a_row_for_every_pair(cp, monkeypatch):
             cp.cp_kv_shard_pack_paged(plan, pages, x, pool=pool)
         with pytest.raises(ValueError, match="6 pairs"):
             cp.cp_decode_attn_paged(plan, pages, cp.CP_DECODE_MLA, q, pool, sm_scale=1.0, **o)
+
+
+def test_paged_calls_need_the_pool_of_the_table(cp, monkeypatch):
+    """A pool, or a pool of scales, with fewer rows than the table's pages is
+    refused by the paged pack and decode."""
+    import torch
+    b = cp._binding
+    monkeypatch.setattr(b, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(b, "_stream", lambda d: None)
+    monkeypatch.setattr(b, "_ptr", lambda t: None)
+    monkeypatch.setattr(b.lib, "cp_kv_shard_pack_paged", lambda *a: 0)
+    monkeypatch.setattr(b.lib, "cp_decode_attn_paged", lambda *a: 0)
+    plan, pages = cp.cp_decode_plan(2, [5], n_workers=2), cp.PageTable(np.zeros((2, 1)), 64, 3, device="cpu")
+    x, q, sx = torch.zeros(5, 576, dtype=torch.uint8), torch.zeros(1, 1, 576, dtype=torch.bfloat16), torch.zeros(5)
+    g, qg = torch.zeros(192, 1, 64, dtype=torch.bfloat16), torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    o = dict(o_part=torch.zeros(1), lse_part=torch.zeros(1), ws=torch.zeros(1))
+    pool, scales = torch.zeros(192, 576, dtype=torch.uint8), torch.zeros(192)
+    for p, s, why in ((pool, scales, None), (pool[:191], scales, "pool has 191"), (pool, scales[:64], "scale_pool has 64")):
+        for fn, args, kw in ((cp.cp_kv_shard_pack_paged, (plan, pages, x, sx, p, s), {}),
+                             (cp.cp_decode_attn_paged, (plan, pages, cp.CP_DECODE_MLA, q, p), dict(scale_pool=s, sm_scale=1.0, **o))):
+            if why is None:
+                fn(*args, **kw)
+            else:
+                with pytest.raises(ValueError, match=why):
+                    fn(*args, **kw)
+    cp.cp_decode_attn_paged(plan, pages, cp.CP_DECODE_GQA, qg, g, g, sm_scale=1.0, **o)
+    with pytest.raises(ValueError, match="v_pool has 128"):
+        cp.cp_decode_attn_paged(plan, pages, cp.CP_DECODE_GQA, qg, g, g[:128], sm_scale=1.0, **o)
