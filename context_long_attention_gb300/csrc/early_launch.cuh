@@ -7,9 +7,9 @@
 // wait_for_earlier_kernels(), before its first access to global memory, holds
 // every thread until all earlier work of the stream is complete and visible, so
 // the order of reads and writes is the ordinary one.  After any other operation
-// the launch is an ordinary one.  Measured per call, calls back to back: absorb
-// of 512 tokens x 64 heads 16.4 -> 13.8 us, project of 1,000 20.5 -> 18.4, of 37
-// 5.8 -> 5.1.
+// the launch is an ordinary one.  Measured per call of the package,
+// calls back to back, where they outlast the host: absorb of 512 tokens x 64
+// heads 16.4 -> 13.8 us, project of 1,000 20.5 -> 18.4.
 //
 // Global reads after the wait go through the L2 (TMA, __ldcg) or are plain
 // loads: never the read-only path, which promises that nobody writes during the

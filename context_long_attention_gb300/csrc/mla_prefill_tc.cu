@@ -32,6 +32,11 @@
 // TMEM (512 columns): tile t holds S_t in columns [256t, 256t + 128), O_t in
 // [256t + 128, 256t + 256); P (bf16 pairs) goes over the first 32 of a half's
 // 64 score columns.
+//
+// P is rounded to bf16, the type of its product with V on the tensor cores; the
+// row's sum, in fp32, takes it before that.  A weight is then off by at most
+// 2^-8 of itself and O by 2^-8 of the weights' mean of |v| (relative error against
+// 64 bits on the long prompt 0.0023; with the output's rounding alone 0.0017).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

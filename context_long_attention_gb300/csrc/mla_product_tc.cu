@@ -330,9 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // through its L2 port; a single CTA's 128 x 256 tile reads 96).  Pairs take
 // contiguous runs of (token tile, head) items; a new tile's rows are loaded
 // piece by piece as the last head's products release the old ones.  20,480
-// tokens x 32 heads: 103 to 105 us = 1,650 TFLOP/s (the library's product of this
-// shape: 99.5; single CTAs with tiles of 128 x 256: 117 to 162); bound by power
-// (0.98 of the sustained bf16 rate) and the first rows' read.
+// tokens x 32 heads in a replayed graph: 103 to 105 us = 1,650 TFLOP/s (the
+// library's product of this shape: 99.5; single CTAs with tiles of 128 x 256: 117
+// to 162); bound by power (0.98 of the sustained bf16 rate) and the first rows'
+// read.  A call among others takes 116 to 120.
 constexpr int kPieces = kLatent / 64;
 constexpr int kPieceBytes = BM * 128;  // 128 rows x 64 columns, of tokens or of W
 constexpr int kPairThreads = 256;  // four epilogue warps: 2,800 clk an item of 4,096 clk of products

@@ -615,7 +615,8 @@ cp_status cp_page_slots(int C, int B, const int32_t* ctx_len, const int32_t* new
  *
  * Row i goes to pool row slots[i]; a slot outside [0, pool_rows) (the -1 of
  * padding) is skipped.  Slots that are used must differ: two rows of one slot
- * leave a mixture.  Rows of the pool that no slot names stay as they are.
+ * leave a mixture; so does a new row that is itself a pool row which a slot
+ * names (rows are read and written in no order).  Rows of the pool that no slot names stay as they are.
  * The decode reads whole tiles of a page, so a new pool must hold finite
  * values (zeros) before its first use.
  * k_new, v_new: [n, row_elems] of src_dtype with row strides in elements
