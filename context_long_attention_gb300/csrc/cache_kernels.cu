@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const Appen
       }
   }
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
-  // the quotient of an fp32 row below 224 x 2^-149 is 0, which would make codes
+  // the quotient of an fp32 row up to 224 x 2^-149 is 0, which would make codes
   // of NaN out of its zeros: the least positive scale stands for such rows
   const float scale = amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), 0x1p-149f) : 1.f;
   if (lane == 0) a.scale_pool[slot] = scale;
