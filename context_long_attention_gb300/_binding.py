@@ -89,6 +89,19 @@ _SIGS = {
     "cp_mla_prefill_attn": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i64, _i, _f, _vp, _vp, _vp]),
     "cp_page_slots": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp]),
     "cp_cache_append": (_i, [_vp, _i, _i, _vp, _i64, _vp, _i64, _vp, _i, _i, _vp, _vp, _vp, _i64, _vp]),
+    "cp_rope": (_i, [_i, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _i64, _i, _i, _vp, _i64, _vp, _i64, _i, _i, _vp, _i64, _vp]),
+    "cp_prefix_plan_size": (_i, [_i, _i, _vp, _vp, _i, _i, _i, _i, _szp, _szp]),
+    "cp_prefix_plan": (_i, [_i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp, _sz, _vp]),
+    "cp_prefix_workspace_size": (_i, [_vp, _i, _i, _szp]),
+    "cp_prefix_attn": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "cp_prefix_attn_paged": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp, _vp, _i,
+                                  _vp, _vp, _sz, _vp]),
+    "cp_prefill_weights_workspace_size": (_i, [_vp, _i, _i, _i, _i, _szp]),
+    "cp_prefill_weights": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _vp, _sz, _vp]),
+    "cp_decode_weights": (_i, [_vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp]),
+    "cp_evict_select": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp]),
+    "cp_cache_move": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i64, _vp]),
+    "cp_page_release": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -995,6 +1008,466 @@ def cp_cache_append(slots, k_new, k_pool, v_new=None, v_pool=None, scale_pool=No
                              pool_scale, rows, _raw_stream(dev))
     if st:
         _check(st)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+CP_ROPE_HALF, CP_ROPE_INTERLEAVED = 0, 1
+_f32 = torch.float32
+
+
+class RopeFreqs:
+    """Frequencies of cp_rope: ``turns`` [rot / 2] int64 on the device, the
+    angle that a pair turns by at each position in units of 2^-64 turn (modulo
+    one turn), and ``scale``, the factor on cos and sin.  ``inv_freq`` keeps the
+    radians a position in 64 bits."""
+
+    def __init__(self, inv_freq, scale: float = 1.0, device=None):
+        self.inv_freq = np.asarray(inv_freq, dtype=np.float64)
+        if self.inv_freq.ndim != 1 or not np.all(np.isfinite(self.inv_freq)):
+            raise ValueError("inv_freq: need a list of finite frequencies")
+        self.scale, self.rot = float(scale), 2 * self.inv_freq.size
+        turns = [int(round(math.fmod(float(f) / (2 * math.pi), 1.0) * 2.0**64)) % 2**64 for f in self.inv_freq]
+        self.turns = torch.from_numpy(np.array(turns, dtype=np.uint64).view(np.int64)).to(device)
+
+
+def cp_rope_freqs(rot: int, base: float = 10000.0, scaling=None, device=None) -> RopeFreqs:
+    """Frequencies base^(-2 i / rot) of rot / 2 pairs, as they are or scaled for
+    contexts longer than the trained one.  scaling: None, or a dict with "kind"
+      "linear"  factor: every frequency divided by it (position interpolation)
+      "ntk"     factor: base x factor^(rot / (rot - 2)), so that the slowest pair
+                is interpolated by about the factor and the fastest stays
+      "bands"   factor, original, low, high: by a pair's turns over the original
+                context, original f / (2 pi): divided up to `low` turns, as they are
+                from `high` on, a linear blend between
+      "yarn"    factor, original, beta_fast = 32, beta_slow = 1, mscale = 1: the blend is
+                linear in the pair's index between those of beta_fast and beta_slow turns,
+                and cos and sin carry 0.1 mscale ln(factor) + 1 (Peng et al., "YaRN", 2023)
+    """
+    if rot < 2 or rot % 2 or not base > 1:
+        raise ValueError(f"rot={rot}, base={base}: need an even rot >= 2 and a base above 1")
+    i = np.arange(rot // 2, dtype=np.float64) * 2 / rot
+    f, scale = base ** -i, 1.0
+    if scaling is not None:
+        c = dict(scaling)
+        kind, factor = c.pop("kind"), float(c.pop("factor"))
+        if not factor >= 1:
+            raise ValueError(f"factor={factor}: need at least 1")
+        want = {"linear": (), "ntk": (), "bands": ("original", "low", "high"),
+                "yarn": ("original", "beta_fast", "beta_slow", "mscale")}
+        if kind not in want:
+            raise ValueError(f"unknown scaling {kind!r}")
+        if kind == "yarn":
+            c = {"beta_fast": 32.0, "beta_slow": 1.0, "mscale": 1.0, **c}
+        if set(c) != set(want[kind]):
+            raise ValueError(f"scaling {kind!r}: need {want[kind]}, got {tuple(c)}")
+        if kind == "linear":
+            f = f / factor
+        elif kind == "ntk":
+            if rot < 4:
+                raise ValueError("scaling 'ntk' needs rot >= 4")
+            f = (base * factor ** (rot / (rot - 2))) ** -i
+        elif kind == "bands":
+            if not c["high"] > c["low"]:
+                raise ValueError("scaling 'bands': need high > low")
+            keep = np.clip((c["original"] * f / (2 * math.pi) - c["low"]) / (c["high"] - c["low"]), 0, 1)
+            f = f * keep + f / factor * (1 - keep)
+        else:
+            at = [rot * math.log(c["original"] / (2 * math.pi * b)) / (2 * math.log(base)) for b in (c["beta_fast"], c["beta_slow"])]
+            lo, hi = max(0, math.floor(at[0])), min(rot - 1, math.ceil(at[1]))
+            part = np.clip((np.arange(rot // 2) - lo) / max(hi - lo, 0.001), 0, 1)
+            f = f * (1 - part) + f / factor * part
+            scale = 0.1 * c["mscale"] * math.log(factor) + 1
+    return RopeFreqs(f, scale, device)
+
+
+def _tokens(name, t, T, dtype, dev):
+    """(pointer, token stride, heads, dim) of [T, heads, dim] with dense heads."""
+    if t.dtype is not dtype or not t.is_cuda or t.get_device() != dev:
+        _complain(name, t, dtype, t.shape, dev)
+    if t.dim() != 3 or t.shape[0] != T:
+        raise ValueError(f"{name}: need [{T}, heads, dim], got {tuple(t.shape)}")
+    heads, dim = t.shape[1], t.shape[2]
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim, heads, dim
+    st, sh, sd = t.stride()
+    if (sd != 1 and dim != 1) or (sh != dim and heads != 1):
+        raise ValueError(f"{name}: a token's heads must be dense, got strides {t.stride()}")
+    return t.data_ptr(), st if T > 1 else heads * dim, heads, dim
+
+
+def cp_rope(q, k, pos, freqs: RopeFreqs, layout: int = CP_ROPE_HALF, tail: bool = False, inverse: bool = False, q_out=None,
+            k_out=None):
+    """Rotary positions: q [T, Hq, Dq] and k [T, Hk, Dk] (or None), bf16 or fp32,
+    views whose tokens may lie apart; pos [T] int32 (cp_shard_plan's qpos for the
+    rows of a rank).  The first freqs.rot dims of every head turn, or with
+    ``tail`` the last ones.  Returns (q_out, k_out): new tensors, or the given ones;
+    q_out=q turns in place.  ``inverse`` turns back, the gradient's direction."""
+    dev, dtype = q.get_device(), q.dtype
+    if dtype is not _bf16 and dtype is not _f32:
+        raise TypeError(f"q: need bf16 or fp32, got {dtype}")
+    T = q.shape[0]
+    if T > _MAX_COUNT:
+        raise ValueError(f"{T} tokens: at most 2^31 - 1")
+    qp, qs, Hq, Dq = _tokens("q", q, T, dtype, dev)
+    _need("pos", pos, _i32t, (T,), dev)
+    turns = freqs.turns
+    if turns.get_device() != dev:
+        raise ValueError(f"the frequencies are on {turns.device}, q on {q.device}")
+    if dev != _device_index():
+        return _on(dev, cp_rope, q, k, pos, freqs, layout, tail, inverse, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, Dq), dtype=dtype, device=q.device)
+        op, os = q_out.data_ptr(), Hq * Dq
+    else:
+        op, os, Ho, Do = _tokens("q_out", q_out, T, dtype, dev)
+        if (Ho, Do) != (Hq, Dq):
+            raise ValueError(f"q_out: need {(T, Hq, Dq)}, got {tuple(q_out.shape)}")
+    kp = kop = None
+    ks = kos = Hk = Dk = 0
+    if k is not None:
+        kp, ks, Hk, Dk = _tokens("k", k, T, dtype, dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, Dk), dtype=dtype, device=q.device)
+            kop, kos = k_out.data_ptr(), Hk * Dk
+        else:
+            kop, kos, Ho, Do = _tokens("k_out", k_out, T, dtype, dev)
+            if (Ho, Do) != (Hk, Dk):
+                raise ValueError(f"k_out: need {(T, Hk, Dk)}, got {tuple(k_out.shape)}")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    st = lib.cp_rope(T, pos.data_ptr(), turns.data_ptr(), freqs.rot, layout, tail, inverse, freqs.scale,
+                     CP_BF16 if dtype is _bf16 else CP_FP32, qp, qs, Hq, Dq, op, os, kp, ks, Hk, Dk, kop, kos, _raw_stream(dev))
+    if st:
+        _check(st)
+    return q_out, k_out
+
+
+# ---------------------------------------------------------------- shared prefixes
+
+PREFIX_ITEM_FIELDS = ["group", "kv_head", "row0", "m0", "m_rows", "tile_begin", "tile_end", "part", "alone"]
+PREFIX_BLOCK_FIELDS = ["group", "kv_head", "row0", "m0", "m_rows", "first_part", "n_parts"]
+
+
+class PrefixPlan(_Plan):
+    """Work of cp_prefix_attn over R shared prefixes (cp_prefix_plan)."""
+
+    @property
+    def pairs(self):
+        P = self.C * self.R
+        return self.words(self.off_rank, PAIR_WORDS * P).reshape(P, PAIR_WORDS)
+
+    @property
+    def worker_off(self):
+        return self.words(self.off_req, self.n_tiles + 1)
+
+    @property
+    def items(self):
+        """[n, 12]: PREFIX_ITEM_FIELDS and padding."""
+        return self.words(self.off_seg, 12 * self.n_seg).reshape(-1, 12)
+
+    @property
+    def blocks(self):
+        """[n, 8]: PREFIX_BLOCK_FIELDS and padding, those that need a merge first."""
+        return self.words(self.off_run, 8 * self.n_split).reshape(-1, 8)
+
+    @property
+    def tile_off(self):
+        return self.words(self.off_tiles, self.R * (self.C + 1)).reshape(self.R, self.C + 1)
+
+    @property
+    def heads(self):
+        """(Hq, Hkv) that the plan was made for."""
+        return int(self.host[self.off_idx]), int(self.host[self.off_idx + 1])
+
+    @property
+    def n_merge(self):
+        return int(self.host[self.off_idx + 2])
+
+    def shard_rows(self):
+        p = self.pairs
+        return [int(p[r * self.R:(r + 1) * self.R, 0].sum()) for r in range(self.C)]
+
+
+def cp_prefix_plan(C: int, prefix_len, members, Hq: int, Hkv: int, layout: int = CP_DCP_ROUND_ROBIN, n_workers: int = 0,
+                   device=None) -> PrefixPlan:
+    """The plan of cp_prefix_attn: members[g] consecutive query rows read the
+    prefix of prefix_len[g] tokens, stored as request g of
+    cp_decode_plan_ex(C, prefix_len, layout)."""
+    pl, mb = _i32(prefix_len), _i32(members)
+    if pl.shape != mb.shape or pl.ndim != 1:
+        raise ValueError(f"prefix_len and members must be lists of one length, got {pl.shape} and {mb.shape}")
+    hb, db = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib.cp_prefix_plan_size(C, len(pl), _np_ptr(pl), _np_ptr(mb), layout, Hq, Hkv, n_workers, ctypes.byref(hb),
+                                   ctypes.byref(db)))
+    host = np.zeros(hb.value // 4, dtype=np.int32)
+    dev = torch.empty(db.value // 4, dtype=torch.int32, device=device) if device is not None else None
+    _check(lib.cp_prefix_plan(C, len(pl), _np_ptr(pl), _np_ptr(mb), layout, Hq, Hkv, n_workers, _np_ptr(host), hb.value,
+                              _ptr(dev), db.value, _stream(dev.device) if dev is not None else None))
+    return PrefixPlan(host, dev)
+
+
+def cp_prefix_workspace_size(plan: PrefixPlan, D: int, P: int = 0) -> int:
+    b = ctypes.c_size_t()
+    _check(lib.cp_prefix_workspace_size(plan.host_ptr, D, P, ctypes.byref(b)))
+    return b.value
+
+
+def _prefix_call(plan, q, Hkv, D, o_part, lse_part, out_dtype, o, lse, ws, dev):
+    """Checks what shards and pages share and makes the outputs."""
+    N, Hq = plan.header["T"], plan.heads[0]
+    if plan.heads != (Hq, Hkv):
+        raise ValueError(f"{Hkv} kv heads: the plan was made for {plan.heads[1]}")
+    if plan.dev is None or plan.dev.get_device() != dev:
+        raise ValueError(f"the plan has no device part on {q.device}")
+    P = 0
+    if (o_part is None) != (lse_part is None):
+        raise ValueError("o_part and lse_part must both be given or both None")
+    if o_part is not None:
+        P = o_part.shape[0]
+        if tuple(o_part.shape[1:]) != (N, Hq, D) and o_part.numel() != P * N * Hq * D:
+            raise ValueError(f"o_part: need [P, {N}, {Hq}, {D}], got {tuple(o_part.shape)}")
+        _need("o_part", o_part, _f32, o_part.shape, dev)
+        if lse_part.shape[0] != P or lse_part.numel() != P * N * Hq:
+            raise ValueError(f"lse_part: need [{P}, {N}, {Hq}], got {tuple(lse_part.shape)}")
+        _need("lse_part", lse_part, _f32, lse_part.shape, dev)
+    if out_dtype is not _bf16 and out_dtype is not _f32:
+        raise TypeError(f"out_dtype: need bf16 or fp32, got {out_dtype}")
+    o = torch.empty((N, Hq, D), dtype=out_dtype, device=q.device) if o is None else _need("o", o, out_dtype, (N, Hq, D), dev)
+    lse = torch.empty((N, Hq), dtype=_f32, device=q.device) if lse is None else _need("lse", lse, _f32, (N, Hq), dev)
+    need = cp_prefix_workspace_size(plan, D, P)
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {q.device}")
+    return P, o, lse, ws, 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _prefix_q(plan, q, kv_dtype):
+    dev = q.get_device()
+    if q.dim() != 3:
+        raise ValueError(f"q: need [{plan.header['T']}, Hq, D], got {tuple(q.shape)}")
+    return dev, _need("q", q, _f32 if kv_dtype == CP_FP32 else _bf16, (plan.header["T"], plan.heads[0], q.shape[2]), dev).shape[2]
+
+
+def cp_prefix_attn(plan: PrefixPlan, q, shard_k, shard_v, shard_scale=None, sm_scale=None, o_part=None, lse_part=None,
+                   out_dtype=torch.bfloat16, o=None, lse=None, ws=None):
+    """Attention of the groups' query rows q [N, Hq, D] over the prefix of their
+    group, in C shards shard_k[r], shard_v[r] [rows_r, Hkv, D] (and, for E4M3 codes,
+    shard_scale[r] [rows_r]), joined with P partial results of the rows' own
+    tokens (o_part [P, N, Hq, D], lse_part [P, N, Hq] fp32, as cp_decode_attn
+    returns them).  Returns (o [N, Hq, D] out_dtype, lse [N, Hq] fp32)."""
+    if len(shard_k) != plan.C or len(shard_v) != plan.C or (shard_scale is not None and len(shard_scale) != plan.C):
+        raise ValueError(f"need one tensor for each of {plan.C} shards")
+    kv_dtype = _dtype_code(shard_k[0])
+    dev, D = _prefix_q(plan, q, kv_dtype)
+    Hkv = plan.heads[1]
+    for r, rows in enumerate(plan.shard_rows()):
+        for name, t in (("shard_k", shard_k[r]), ("shard_v", shard_v[r])):
+            if _dtype_code(t) != kv_dtype:
+                raise TypeError(f"{name}[{r}]: all shards need one dtype")
+            _need(f"{name}[{r}]", t, t.dtype, (rows, Hkv, D), dev)
+        if shard_scale is not None:
+            _need(f"shard_scale[{r}]", shard_scale[r], _f32, (rows,), dev)
+    if dev != _device_index():
+        return _on(dev, cp_prefix_attn, plan, q, shard_k, shard_v, shard_scale, sm_scale, o_part, lse_part, out_dtype, o, lse, ws)
+    P, o, lse, ws, ws_bytes = _prefix_call(plan, q, Hkv, D, o_part, lse_part, out_dtype, o, lse, ws, dev)
+    _check(lib.cp_prefix_attn(plan.host_ptr, plan.dev.data_ptr(), kv_dtype, q.data_ptr(), _ptr_array(shard_k),
+                              _ptr_array(shard_v), _ptr_array(shard_scale) if shard_scale is not None else None,
+                              plan.heads[0], Hkv, D, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), P,
+                              _ptr(o_part), _ptr(lse_part), o.data_ptr(), _dtype_code(o), lse.data_ptr(), _ptr(ws), ws_bytes,
+                              _raw_stream(dev)))
+    return o, lse
+
+
+def cp_prefix_attn_paged(plan: PrefixPlan, pages: PageTable, q, k_pool, v_pool, scale_pool=None, sm_scale=None, o_part=None,
+                         lse_part=None, out_dtype=torch.bfloat16, o=None, lse=None, ws=None):
+    """cp_prefix_attn over prefixes in the pages of one pool (k_pool, v_pool
+    [pool_rows, Hkv, D]; ``pages`` has a row for every pair r * R + g)."""
+    kv_dtype = _dtype_code(k_pool)
+    dev, D = _prefix_q(plan, q, kv_dtype)
+    Hkv, rows = plan.heads[1], k_pool.shape[0]
+    table = _host_table(pages, plan, k_pool=k_pool, v_pool=v_pool, scale_pool=scale_pool)
+    if _dtype_code(v_pool) != kv_dtype:
+        raise TypeError("v_pool must have k_pool's dtype")
+    _need("k_pool", k_pool, k_pool.dtype, (rows, Hkv, D), dev)
+    _need("v_pool", v_pool, v_pool.dtype, (rows, Hkv, D), dev)
+    if scale_pool is not None:
+        _need("scale_pool", scale_pool, _f32, (rows,), dev)
+    if pages.dev is None or pages.dev.get_device() != dev:
+        raise ValueError(f"the page table has no device copy on {q.device}")
+    if dev != _device_index():
+        return _on(dev, cp_prefix_attn_paged, plan, pages, q, k_pool, v_pool, scale_pool, sm_scale, o_part, lse_part, out_dtype,
+                   o, lse, ws)
+    P, o, lse, ws, ws_bytes = _prefix_call(plan, q, Hkv, D, o_part, lse_part, out_dtype, o, lse, ws, dev)
+    _check(lib.cp_prefix_attn_paged(plan.host_ptr, plan.dev.data_ptr(), kv_dtype, q.data_ptr(), k_pool.data_ptr(),
+                                    v_pool.data_ptr(), _ptr(scale_pool), table, _ptr(pages.dev), pages.max_pages,
+                                    pages.page_size, pages.num_pages, plan.heads[0], Hkv, D,
+                                    1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), P, _ptr(o_part),
+                                    _ptr(lse_part), o.data_ptr(), _dtype_code(o), lse.data_ptr(), _ptr(ws), ws_bytes,
+                                    _raw_stream(dev)))
+    return o, lse
+
+
+# ---------------------------------------------------------------- accumulated weights, eviction
+
+def cp_prefill_weights(plan: PrefillPlan, q, k, lse, sm_scale=None, window: int = 0, out=None, ws=None):
+    """The attention weight of every key of a prompt batch: out [KV] fp32, the sum
+    over the queries that read it (``window``: over the last so many new tokens of
+    each request) and all heads of exp(score - lse).  q [T, Hq, D], k [KV, Hkv, D]
+    as given to cp_prefill_attn, lse [T, Hq] as it returned it for all ranks."""
+    dev, dtype = q.get_device(), q.dtype
+    T, KV = plan.header["T"], plan.header["KV"]
+    if dtype is not _bf16 and dtype is not _f32:
+        raise TypeError(f"q: need bf16 or fp32, got {dtype}")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"need q [{T}, Hq, D] and k [{KV}, Hkv, D], got {tuple(q.shape)} and {tuple(k.shape)}")
+    Hq, D, Hkv = q.shape[1], q.shape[2], k.shape[1]
+    _need("q", q, dtype, (T, Hq, D), dev)
+    _need("k", k, dtype, (KV, Hkv, D), dev)
+    _need("lse", lse, _f32, (T, Hq), dev)
+    if plan.dev is None or plan.dev.get_device() != dev:
+        raise ValueError(f"the plan has no device part on {q.device}")
+    if not 0 <= window <= _MAX_COUNT:
+        raise ValueError(f"window={window}: need 0 .. 2^31 - 1")
+    if dev != _device_index():
+        return _on(dev, cp_prefill_weights, plan, q, k, lse, sm_scale, window, out, ws)
+    out = torch.empty(KV, dtype=_f32, device=q.device) if out is None else _need("out", out, _f32, (KV,), dev)
+    code, b = _dtype_code(q), ctypes.c_size_t()
+    _check(lib.cp_prefill_weights_workspace_size(plan.host_ptr, code, Hq, D, window, ctypes.byref(b)))
+    if ws is None and b.value:
+        ws = torch.empty(b.value, dtype=torch.uint8, device=q.device)
+    elif ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {q.device}")
+    _check(lib.cp_prefill_weights(plan.host_ptr, plan.dev.data_ptr(), code, q.data_ptr(), k.data_ptr(), lse.data_ptr(), Hq,
+                                  Hkv, D, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, out.data_ptr(),
+                                  _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(dev)))
+    return out
+
+
+def cp_decode_weights(plan: DecodePlan, pages: PageTable, mode: int, q, k_pool, lse, weights, scale_pool=None, sm_scale=None):
+    """Adds a decode step's attention weights to ``weights`` [pool_rows] fp32, in
+    place: for every cached row of the plan's requests the sum over their query
+    rows and heads of exp(score - lse).  The plan, pages, q and k_pool as given to
+    cp_decode_attn_paged, lse [B, (s_q,) Hq] the merged one.  Returns weights."""
+    lead, H, Dqk = _decode_shapes(plan, q)
+    dev, rows = q.get_device(), k_pool.shape[0]
+    kv_dtype = _dtype_code(k_pool)
+    Hkv = 1 if mode == CP_DECODE_MLA else k_pool.shape[1]
+    _need("q", q, _f32 if kv_dtype == CP_FP32 else _bf16, (plan.R, *lead[1:], H, Dqk), dev)
+    _need("k_pool", k_pool, k_pool.dtype, (rows, Dqk) if mode == CP_DECODE_MLA else (rows, Hkv, Dqk), dev)
+    _need("lse", lse, _f32, (*lead, H), dev)
+    _need("weights", weights, _f32, (rows,), dev)
+    if scale_pool is not None:
+        _need("scale_pool", scale_pool, _f32, (rows,), dev)
+    table = _host_table(pages, plan, k_pool=k_pool)
+    for what, t in (("plan", plan.dev), ("page table", pages.dev)):
+        if t is None or t.get_device() != dev:
+            raise ValueError(f"the {what} has no device copy on {q.device}")
+    if dev != _device_index():
+        return _on(dev, cp_decode_weights, plan, pages, mode, q, k_pool, lse, weights, scale_pool, sm_scale)
+    _check(lib.cp_decode_weights(plan.host_ptr, plan.dev.data_ptr(), mode, kv_dtype, q.data_ptr(), k_pool.data_ptr(),
+                                 _ptr(scale_pool), table, pages.dev.data_ptr(), pages.max_pages, pages.page_size,
+                                 pages.num_pages, H, Hkv, Dqk, 1.0 / math.sqrt(Dqk) if sm_scale is None else float(sm_scale),
+                                 lse.data_ptr(), weights.data_ptr(), _raw_stream(dev)))
+    return weights
+
+
+def _evict_table(pages, C, ctx_len, keep_len):
+    table = pages.dev
+    if table is None:
+        raise ValueError("the page table has no device copy")
+    dev, B = table.get_device(), ctx_len.shape[0]
+    _need("page table", table, _i32t, (C * B, pages.max_pages), dev)
+    _need("ctx_len", ctx_len, _i32t, (B,), dev)
+    _need("keep_len", keep_len, _i32t, (B,), dev)
+    return table, dev, B
+
+
+def cp_evict_select(pages: PageTable, C: int, ctx_len, keep_len, weights, max_moves: int, pos=None, keep_below: int = 0,
+                    keep_from=None, src=None, dst=None, count=None):
+    """Which rows every pair (shard, request) keeps when its request goes from
+    ctx_len[b] to keep_len[b] cached tokens ([B] int32 on the GPU): rows of
+    position < keep_below or >= keep_from[b], then the heaviest by ``weights``
+    [pool_rows].  Returns the moves that bring the kept rows together, for
+    cp_cache_move: (src, dst [C B, max_moves] pool rows, -1 behind the last;
+    count [C B], -1 for a pair that does not fit: see cpattn.h)."""
+    table, dev, B = _evict_table(pages, C, ctx_len, keep_len)
+    rows = pages.pool_rows
+    _need("weights", weights, _f32, (rows,), dev)
+    if pos is not None:
+        _need("pos", pos, _i32t, (rows,), dev)
+    if keep_from is not None:
+        _need("keep_from", keep_from, _i32t, (B,), dev)
+    if not 1 <= max_moves <= _MAX_COUNT or not -_MAX_COUNT <= keep_below <= _MAX_COUNT:
+        raise ValueError(f"max_moves={max_moves}: need 1 .. 2^31 - 1; keep_below={keep_below}: need an int32")
+    if dev != _device_index():
+        return _on(dev, cp_evict_select, pages, C, ctx_len, keep_len, weights, max_moves, pos, keep_below, keep_from, src, dst, count)
+    shape, where = (C * B, max_moves), table.device
+    src = torch.empty(shape, dtype=_i32t, device=where) if src is None else _need("src", src, _i32t, shape, dev)
+    dst = torch.empty(shape, dtype=_i32t, device=where) if dst is None else _need("dst", dst, _i32t, shape, dev)
+    count = torch.empty(C * B, dtype=_i32t, device=where) if count is None else _need("count", count, _i32t, (C * B,), dev)
+    st = lib.cp_evict_select(C, B, ctx_len.data_ptr(), keep_len.data_ptr(), table.data_ptr(), pages.max_pages, pages.page_size,
+                             pages.num_pages, weights.data_ptr(), None if pos is None else pos.data_ptr(), keep_below,
+                             None if keep_from is None else keep_from.data_ptr(), max_moves, src.data_ptr(), dst.data_ptr(),
+                             count.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
+    return src, dst, count
+
+
+def cp_cache_move(src, dst, count, k_pool, v_pool=None, scale_pool=None, weights=None, pos=None):
+    """The moves of cp_evict_select on a pool's rows, in place: k_pool and v_pool
+    [pool_rows, ...], and scale_pool, weights (fp32) and pos (int32) [pool_rows]
+    where they are given."""
+    dev, rows = k_pool.get_device(), k_pool.shape[0]
+    pairs, most = src.shape
+    _need("src", src, _i32t, (pairs, most), dev)
+    _need("dst", dst, _i32t, (pairs, most), dev)
+    _need("count", count, _i32t, (pairs,), dev)
+    _need("k_pool", k_pool, k_pool.dtype, k_pool.shape, dev)
+    if v_pool is not None:
+        _need("v_pool", v_pool, k_pool.dtype, k_pool.shape, dev)
+    for name, t, dtype in (("scale_pool", scale_pool, _f32), ("weights", weights, _f32), ("pos", pos, _i32t)):
+        if t is not None:
+            _need(name, t, dtype, (rows,), dev)
+    if dev != _device_index():
+        return _on(dev, cp_cache_move, src, dst, count, k_pool, v_pool, scale_pool, weights, pos)
+    st = lib.cp_cache_move(pairs, most, src.data_ptr(), dst.data_ptr(), count.data_ptr(), k_pool.data_ptr(),
+                           None if v_pool is None else v_pool.data_ptr(), k_pool.shape[1:].numel() * k_pool.element_size(),
+                           None if scale_pool is None else scale_pool.data_ptr(), None if weights is None else weights.data_ptr(),
+                           None if pos is None else pos.data_ptr(), rows, _raw_stream(dev))
+    if st:
+        _check(st)
+
+
+def cp_page_release(pages: PageTable, C: int, ctx_len, keep_len, free_ids, free_pos, weights=None, pos=None, info=None):
+    """Hands the pages that shorter requests no longer need back to free_ids, below
+    free_pos ([1] int32, or an earlier call's info[1:2]), clears their table entries
+    and the weights and positions of the rows behind the new lengths.  Returns
+    info [4] = status, next free_pos, pages released, 0.  Like cp_page_slots it drops the
+    table's host copy (``pages.sync_host()``)."""
+    table, dev, B = _evict_table(pages, C, ctx_len, keep_len)
+    n_free, rows = free_ids.shape[0], pages.pool_rows
+    if n_free > _MAX_COUNT:
+        raise ValueError(f"n_free={n_free}: at most 2^31 - 1")
+    _need("free_ids", free_ids, _i32t, (n_free,), dev)
+    _need("free_pos", free_pos, _i32t, (1,), dev)
+    if weights is not None:
+        _need("weights", weights, _f32, (rows,), dev)
+    if pos is not None:
+        _need("pos", pos, _i32t, (rows,), dev)
+    if dev != _device_index():
+        return _on(dev, cp_page_release, pages, C, ctx_len, keep_len, free_ids, free_pos, weights, pos, info)
+    info = torch.empty(4, dtype=_i32t, device=table.device) if info is None else _need("info", info, _i32t, (4,), dev)
+    st = lib.cp_page_release(C, B, ctx_len.data_ptr(), keep_len.data_ptr(), table.data_ptr(), pages.max_pages, pages.page_size,
+                             pages.num_pages, free_ids.data_ptr(), n_free, free_pos.data_ptr(),
+                             None if weights is None else weights.data_ptr(), None if pos is None else pos.data_ptr(),
+                             info.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
+    pages.host = None
+    return info
 
 
 # ---------------------------------------------------------------- NVTX ranges

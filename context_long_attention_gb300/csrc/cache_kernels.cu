@@ -11,6 +11,7 @@
 
 #include "early_launch.cuh"
 #include "internal.h"
+#include "page_count.cuh"
 
 namespace cpattn {
 namespace {
@@ -31,20 +32,6 @@ namespace {
 constexpr int kSlotThreads = 256;
 constexpr int kSlotWarps = kSlotThreads / 32;
 
-// n / d for 0 <= n < 2^31: with 2^s >= d > 2^(s-1) and m = ceil(2^(31+s) / d),
-// m d - 2^(31+s) < d <= 2^s, so n m / 2^(31+s) passes n / d by less than 1 / d.
-struct FastDiv {
-  uint32_t m;
-  int shift, d;
-  explicit FastDiv(int div) : d(div) {
-    int s = 0;
-    while ((1ll << s) < div) ++s;
-    shift = 31 + s;
-    m = (uint32_t)(((1ull << shift) + div - 1) / div);
-  }
-  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
-};
-
 struct SlotsParams {
   PageSlotsArgs a;
   FastDiv by_c, by_page;
@@ -52,27 +39,7 @@ struct SlotsParams {
   int wide;        // a warp a pair (many pages each) instead of a thread
 };
 
-struct PageCount {
-  int m, small, big;  // the first m shards hold `big` pages, the others `small`
-};
-__device__ __forceinline__ PageCount page_count(const SlotsParams& p, int L) {
-  PageCount c;
-  const int q = p.by_c(L), qp = p.by_page(q);
-  c.m = L - q * p.by_c.d;
-  c.small = qp + (q != qp * p.by_page.d);
-  c.big = qp + 1;
-  return c;
-}
-__device__ __forceinline__ int pages_before(const PageCount& c, int r) {
-  return min(r, c.m) * c.big + max(0, r - c.m) * c.small;
-}
-__device__ __forceinline__ int pages_of(const PageCount& c, int r) { return r < c.m ? c.big : c.small; }
-// Sums that stop at 2^32 - 1, past every limit that they are compared with
-// (limits are at most 2^31 - 1).
-__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
-  const uint32_t sum = a + b;
-  return sum < a ? 0xFFFFFFFFu : sum;
-}
+__device__ __forceinline__ PageCount page_count(const SlotsParams& p, int L) { return page_count(p.by_c, p.by_page, L); }
 
 // VEC consecutive tokens a thread.
 template <int VEC>

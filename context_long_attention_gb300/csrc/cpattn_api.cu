@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "plan_rows.cuh"
 
 using namespace cpattn;
 
@@ -495,7 +496,8 @@ cp_status read_header(const void* host_plan, int want_kind, cp_plan_header* h) {
   memcpy(h, host_plan, sizeof(*h));
   if (h->magic != CP_PLAN_MAGIC) return fail(CP_ERR_INVALID_ARG, "host_plan is not a plan (bad magic)");
   if (want_kind == 2 && h->kind != 2) return fail(CP_ERR_INVALID_ARG, "expected a decode plan");
-  if (want_kind != 2 && h->kind == 2) return fail(CP_ERR_INVALID_ARG, "expected a prefill plan");
+  if (want_kind == 0 && h->kind != 0 && h->kind != 1) return fail(CP_ERR_INVALID_ARG, "expected a prefill plan");
+  if (want_kind == 3 && h->kind != 3) return fail(CP_ERR_INVALID_ARG, "expected a shared-prefix plan");
   return CP_OK;
 }
 
@@ -696,6 +698,232 @@ cp_status run_decode_merged(const cp_plan_header& h, const int32_t* W, const voi
   return ok();
 }
 
+
+// ------------------------------------------------------------------ shared prefixes
+
+// Work of one block's tile against its fixed work (query rows, the first tile's
+// fill, the result), in sixteenths of a tile of two 128-row M tiles.
+constexpr long long kPrefixItemCost = 32, kPrefixTile2 = 16, kPrefixTile1 = 10;
+
+cp_status build_prefix_plan(int C, int R, const int32_t* prefix_len, const int32_t* members, int layout, int Hq, int Hkv,
+                            int n_workers, std::vector<int32_t>* out) {
+  if (!members) return fail(CP_ERR_INVALID_ARG, "members is NULL");
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv) return fail(CP_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d", Hq, Hkv);
+  if (layout == CP_DCP_SELECTED) return fail(CP_ERR_INVALID_ARG, "layout=%d: a prefix lies round robin or in contiguous chunks", layout);
+  int G = n_workers;
+  if (G == 0) {
+    const cp_status st = sm_count(&G);
+    if (st != CP_OK) return st;
+  }
+  DecodeBuild d;  // the pairs of the prefixes as requests of a decode plan
+  cp_status st = build_decode_plan(C, R, prefix_len, layout, 1, G < 0 ? G : 1, &d);
+  if (st != CP_OK) return st;
+  cp_plan_header h;
+  memcpy(&h, d.words.data(), sizeof(h));
+  std::vector<cp_pair_desc> pair(C * R);
+  memcpy(pair.data(), d.words.data() + h.off_rank, sizeof(cp_pair_desc) * pair.size());
+  for (cp_pair_desc& p : pair) {
+    p.n_parts = 0;
+    p.first_part = -1;
+  }
+  const int group = Hq / Hkv;
+  long long N = 0;
+  std::vector<int32_t> row_off(R + 1, 0), tile_off((size_t)R * (C + 1), 0);
+  for (int g = 0; g < R; ++g) {
+    if (members[g] < 0) return fail(CP_ERR_INVALID_ARG, "members[%d] < 0", g);
+    N += members[g];
+    if (N * Hq > 0x7FFFFFFFLL) return fail(CP_ERR_INVALID_ARG, "query rows x heads past 2^31 - 1");
+    row_off[g + 1] = (int32_t)N;
+    for (int r = 0; r < C; ++r)
+      tile_off[(size_t)g * (C + 1) + r + 1] = tile_off[(size_t)g * (C + 1) + r] + (pair[r * R + g].rows + kDecodeTileRows - 1) / kDecodeTileRows;
+  }
+  if (N == 0) return fail(CP_ERR_INVALID_ARG, "no query rows");
+
+  // Blocks, kv head by kv head so that blocks of the same keys run side by side;
+  // the walk over all blocks' tiles is cut into equal costs.
+  std::vector<cp_prefix_block> block;
+  std::vector<long long> start(1, 0);
+  for (int g = 0; g < R; ++g)
+    for (int kh = 0; kh < Hkv; ++kh)
+      for (long long m0 = 0; m0 < (long long)members[g] * group; m0 += kPrefixRows) {
+        const int rows = (int)std::min<long long>(kPrefixRows, (long long)members[g] * group - m0);
+        block.push_back({g, kh, row_off[g], (int32_t)m0, rows, 0, 0, 0});
+        const long long nt = tile_off[(size_t)g * (C + 1) + C];
+        start.push_back(start.back() + (nt ? kPrefixItemCost + nt * (rows > 128 ? kPrefixTile2 : kPrefixTile1) : 0));
+      }
+  const int NB = (int)block.size();
+  std::vector<cp_prefix_item> item;
+  std::vector<int32_t> worker_off(G + 1, 0), item_block;
+  int i = 0, t = 0;  // the walk: block and its next tile
+  for (int w = 0; w < G; ++w) {
+    worker_off[w] = (int)item.size();
+    const long long end = start[NB] * (w + 1) / G;
+    while (i < NB) {
+      const cp_prefix_block& b = block[i];
+      const int nt = tile_off[(size_t)b.group * (C + 1) + C];
+      const long long per = b.m_rows > 128 ? kPrefixTile2 : kPrefixTile1;
+      // tiles of this block that end by the worker's share
+      long long upto = w + 1 == G || start[i + 1] <= end ? nt : (end - start[i] - kPrefixItemCost + per / 2) / per;
+      upto = std::min<long long>(upto, nt);
+      if (upto > t) {
+        cp_prefix_item x;
+        memset(&x, 0, sizeof(x));
+        x.group = b.group;
+        x.kv_head = b.kv_head;
+        x.row0 = b.row0;
+        x.m0 = b.m0;
+        x.m_rows = b.m_rows;
+        x.tile_begin = t;
+        x.tile_end = (int32_t)upto;
+        item.push_back(x);
+        item_block.push_back(i);
+        block[i].n_parts++;
+        t = (int)upto;
+      }
+      if (t < nt) break;
+      ++i;
+      t = 0;
+    }
+  }
+  worker_off[G] = (int)item.size();
+  // blocks that need a merge come first, and so do their parts
+  std::vector<int> order;
+  for (int pass = 0; pass < 2; ++pass)
+    for (int k = 0; k < NB; ++k)
+      if ((block[k].n_parts == 1) == (pass == 1)) order.push_back(k);
+  int n_parts = 0, merge_parts = 0, n_merge = 0;
+  for (int k : order) {
+    block[k].first_part = n_parts;
+    n_parts += block[k].n_parts;
+    if (block[k].n_parts != 1) {
+      ++n_merge;
+      merge_parts = n_parts;
+    }
+  }
+  std::vector<int> next(NB, 0);
+  for (size_t k = 0; k < item.size(); ++k) {
+    const cp_prefix_block& b = block[item_block[k]];
+    item[k].part = b.first_part + next[item_block[k]]++;
+    item[k].alone = b.n_parts == 1;
+  }
+  std::vector<cp_prefix_block> sorted;
+  for (int k : order) sorted.push_back(block[k]);
+
+  const int P = C * R, n_item = (int)item.size();
+  cp_plan_header o;
+  memset(&o, 0, sizeof(o));
+  o.magic = CP_PLAN_MAGIC;
+  o.kind = 3;
+  o.C = C;
+  o.R = R;
+  o.T = (int32_t)N;
+  o.KV = h.T;
+  o.n_seg = n_item;
+  o.n_tiles = G;
+  o.n_parts = n_parts;
+  o.n_split = NB;
+  o.tile_rows = kDecodeTileRows;
+  o.layout = layout;
+  o.s_q = 1;
+  long long w = align4(kHeaderWords);
+  auto table = [&](int32_t* off, long long words) {
+    *off = (int32_t)w;
+    w = (w + words + 3) & ~3LL;
+  };
+  table(&o.off_rank, (long long)kPairWords * P);
+  table(&o.off_req, G + 1);
+  table(&o.off_seg, (long long)(sizeof(cp_prefix_item) / 4) * n_item);
+  table(&o.off_tiles, (long long)R * (C + 1));
+  table(&o.off_rtile, R + 1);
+  table(&o.off_run, (long long)(sizeof(cp_prefix_block) / 4) * NB);
+  table(&o.off_idx, 4);
+  if (w > 0x7FFFFFFFLL) return fail(CP_ERR_UNSUPPORTED, "the plan is too large");
+  o.host_words = o.dev_words = (int32_t)w;
+  out->assign(w, 0);
+  int32_t* W = out->data();
+  memcpy(W, &o, sizeof(o));
+  memcpy(W + o.off_rank, pair.data(), sizeof(cp_pair_desc) * P);
+  memcpy(W + o.off_req, worker_off.data(), 4 * (G + 1));
+  if (n_item) memcpy(W + o.off_seg, item.data(), sizeof(cp_prefix_item) * n_item);
+  memcpy(W + o.off_tiles, tile_off.data(), 4 * tile_off.size());
+  memcpy(W + o.off_rtile, row_off.data(), 4 * (R + 1));
+  memcpy(W + o.off_run, sorted.data(), sizeof(cp_prefix_block) * NB);
+  const int32_t info[4] = {Hq, Hkv, n_merge, merge_parts};
+  memcpy(W + o.off_idx, info, sizeof(info));
+  return CP_OK;
+}
+
+// Part slots of a call: with the caller's own parts every block goes through them.
+size_t prefix_parts(const cp_plan_header& h, const int32_t* W, int P) { return P > 0 ? h.n_parts : W[h.off_idx + 3]; }
+
+// The checks and arguments that shards and pages share.
+cp_status prefix_args(const void* host_plan, const void* dev_plan, cp_dtype kv_dtype, const void* q, const void* k,
+                      const void* v, const void* scale, int Hq, int Hkv, int D, float sm_scale, int P,
+                      const float* own_o, const float* own_lse, void* o, cp_dtype o_dtype, float* lse, void* ws,
+                      size_t ws_bytes, cp_plan_header* h, PrefixArgs* a) {
+  cp_status st = read_header(host_plan, 3, h);
+  if (st != CP_OK) return st;
+  const int32_t* W = (const int32_t*)host_plan;
+  if (!dev_plan || !q || !k || !o || !lse) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(dev_plan) || !aligned16(q) || !aligned16(o) || !aligned16(lse))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  if (o_dtype != CP_BF16 && o_dtype != CP_FP32) return fail(CP_ERR_INVALID_ARG, "o_dtype must be bf16 or fp32");
+  st = check_decode_shapes(CP_DECODE_GQA, kv_dtype, v != nullptr, scale != nullptr, Hq, Hkv, D, D, sm_scale, 1);
+  if (st != CP_OK) return st;
+  if (Hq != W[h->off_idx] || Hkv != W[h->off_idx + 1])
+    return fail(CP_ERR_INVALID_ARG, "Hq=%d, Hkv=%d: the plan was made for %d and %d", Hq, Hkv, W[h->off_idx], W[h->off_idx + 1]);
+  if (P < 0 || P > CP_MAX_SHARDS) return fail(CP_ERR_INVALID_ARG, "P=%d outside [0, %d]", P, CP_MAX_SHARDS);
+  if (P > 0 && (!own_o || !own_lse || !aligned16(own_o))) return fail(CP_ERR_INVALID_ARG, "own_o or own_lse NULL or misaligned");
+  const size_t parts = prefix_parts(*h, W, P), need = parts * kPrefixRows * (D + 1) * sizeof(float);
+  if (ws_bytes < need || (need && !ws)) return fail(CP_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  if (need && !aligned16(ws)) return fail(CP_ERR_INVALID_ARG, "ws is not 16-byte aligned");
+  memset(a, 0, sizeof(*a));
+  a->plan = (const int32_t*)dev_plan;
+  a->off_pair = h->off_rank;
+  a->off_worker = h->off_req;
+  a->off_item = h->off_seg;
+  a->off_tiles = h->off_tiles;
+  a->off_block = h->off_run;
+  a->C = h->C;
+  a->R = h->R;
+  a->N = h->T;
+  a->q = q;
+  a->Hq = Hq;
+  a->Hkv = Hkv;
+  a->G = Hq / Hkv;
+  a->D = D;
+  a->sm_scale = sm_scale;
+  a->o = o;
+  a->o_bf16 = o_dtype == CP_BF16;
+  a->lse = lse;
+  a->ws_o = (float*)ws;
+  a->ws_lse = ws ? (float*)ws + parts * kPrefixRows * D : nullptr;
+  a->P = P;
+  a->own_o = own_o;
+  a->own_lse = own_lse;
+  return CP_OK;
+}
+
+cp_status run_prefix(const cp_plan_header& h, const int32_t* W, const PrefixArgs& a, cp_dtype kv_dtype,
+                     const long long* shard_rows, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (h.n_seg > 0) e = launch_prefix_simt(a, kv_dtype, h.n_tiles, s);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix attention kernel");
+  e = launch_prefix_merge(a, a.P > 0 ? h.n_split : W[h.off_idx + 2], s);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix merge kernel");
+  return ok();
+}
+
+// The shape of a paged pool of C x B pairs.
+cp_status check_pool_shape(int C, int B, int max_pages, int page_size, int num_pages) {
+  if (C < 1 || C > CP_MAX_SHARDS) return fail(CP_ERR_INVALID_ARG, "C=%d outside [1, %d]", C, CP_MAX_SHARDS);
+  if (B < 1 || B > CP_SLOTS_MAX_B) return fail(CP_ERR_INVALID_ARG, "B=%d outside [1, %d]", B, CP_SLOTS_MAX_B);
+  if (page_size < 64 || page_size % 64) return fail(CP_ERR_UNSUPPORTED, "page_size=%d is not a positive multiple of 64", page_size);
+  if (max_pages < 1 || num_pages < 1) return fail(CP_ERR_INVALID_ARG, "max_pages=%d, num_pages=%d must be >= 1", max_pages, num_pages);
+  if ((long long)num_pages * page_size > 0x7FFFFF00LL)
+    return fail(CP_ERR_UNSUPPORTED, "pool of %lld rows is too large", (long long)num_pages * page_size);
+  return CP_OK;
+}
 
 }  // namespace
 
@@ -1439,6 +1667,268 @@ cp_status cp_cache_append(const int32_t* slots, int n, cp_dtype src_dtype, const
                         k_pool, v_pool, new_scale, scale_pool, (long long)pool_rows};
   const cudaError_t e = launch_cache_append(a, src_dtype, pool_dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "cache append kernel");
+  return ok();
+}
+
+// ------------------------------------------------------------------ rotary positions
+
+cp_status cp_rope(int T, const int32_t* pos, const uint64_t* turns, int rot, int layout, int tail, int inverse,
+                  float scale, cp_dtype dtype, const void* q, int64_t q_stride, int q_heads, int q_dim,
+                  void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, int k_heads, int k_dim,
+                  void* k_out, int64_t k_out_stride, void* stream) {
+  if (T < 0) return fail(CP_ERR_INVALID_ARG, "T=%d must be >= 0", T);
+  if (layout != CP_ROPE_HALF && layout != CP_ROPE_INTERLEAVED) return fail(CP_ERR_INVALID_ARG, "unknown layout %d", layout);
+  if (dtype != CP_BF16 && dtype != CP_FP32) return fail(CP_ERR_UNSUPPORTED, "rope dtype must be bf16 or fp32");
+  if (rot < 16 || rot > 1024 || rot % 16) return fail(CP_ERR_UNSUPPORTED, "rot=%d: need a multiple of 16 in [16, 1024]", rot);
+  if (q_heads < 1 || k_heads < 0) return fail(CP_ERR_INVALID_ARG, "q_heads=%d must be >= 1, k_heads=%d >= 0", q_heads, k_heads);
+  if (!(scale > 0.f)) return fail(CP_ERR_INVALID_ARG, "scale must be > 0");
+  struct In {
+    const char* name;
+    const void* x;
+    const void* out;
+    int64_t stride, out_stride;
+    int heads, dim;
+  };
+  const In in[2] = {{"q", q, q_out, q_stride, q_out_stride, q_heads, q_dim}, {"k", k, k_out, k_stride, k_out_stride, k_heads, k_dim}};
+  int64_t elems = 0;
+  for (const In& t : in) {
+    if (t.heads == 0) continue;
+    if (t.dim < rot || t.dim % 8) return fail(CP_ERR_UNSUPPORTED, "%s: head dim %d: need a multiple of 8, at least rot=%d", t.name, t.dim, rot);
+    const int64_t row = (int64_t)t.heads * t.dim;
+    if (row > 262144) return fail(CP_ERR_UNSUPPORTED, "%s: %lld elements a token, at most 262,144", t.name, (long long)row);
+    elems += row;
+    for (int64_t st : {t.stride, t.out_stride})
+      if (T > 0 && (st < row || st > kMaxRowStride || st % 8))
+        return fail(CP_ERR_INVALID_ARG, "%s: stride %lld: need a multiple of 8, at least %lld", t.name, (long long)st, (long long)row);
+  }
+  if (elems > 262144) return fail(CP_ERR_UNSUPPORTED, "%lld elements a token, at most 262,144", (long long)elems);
+  if (T == 0) return ok();
+  if (!pos || !turns) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (reinterpret_cast<uintptr_t>(turns) & 7u) return fail(CP_ERR_INVALID_ARG, "turns is not 8-byte aligned");
+  for (const In& t : in) {
+    if (t.heads == 0) continue;
+    if (!t.x || !t.out) return fail(CP_ERR_INVALID_ARG, "%s: a pointer argument is NULL", t.name);
+    if (!aligned16(t.x) || !aligned16(t.out)) return fail(CP_ERR_INVALID_ARG, "%s: a device pointer is not 16-byte aligned", t.name);
+    if (t.x == t.out && t.stride != t.out_stride) return fail(CP_ERR_INVALID_ARG, "%s: in place with two strides", t.name);
+  }
+  RopeArgs a = {{q, q_out, (long long)q_stride, (long long)q_out_stride, q_heads, q_dim},
+                {k, k_out, (long long)k_stride, (long long)k_out_stride, k_heads, k_heads ? k_dim : rot},
+                pos, (const unsigned long long*)turns, T, rot, layout == CP_ROPE_HALF, tail != 0, inverse != 0, scale};
+  const cudaError_t e = launch_rope(a, dtype == CP_BF16, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rope kernel");
+  return ok();
+}
+
+// ------------------------------------------------------------------ shared prefixes
+
+cp_status cp_prefix_plan_size(int C, int R, const int32_t* prefix_len, const int32_t* members,
+                              cp_dcp_layout layout, int Hq, int Hkv, int n_workers, size_t* host_bytes,
+                              size_t* dev_bytes) {
+  if (!host_bytes || !dev_bytes) return fail(CP_ERR_INVALID_ARG, "a size pointer is NULL");
+  std::vector<int32_t> words;
+  const cp_status st = build_prefix_plan(C, R, prefix_len, members, layout, Hq, Hkv, n_workers, &words);
+  if (st != CP_OK) return st;
+  *host_bytes = *dev_bytes = words.size() * 4;
+  return ok();
+}
+
+cp_status cp_prefix_plan(int C, int R, const int32_t* prefix_len, const int32_t* members, cp_dcp_layout layout,
+                         int Hq, int Hkv, int n_workers, void* host_plan, size_t host_bytes, void* dev_plan,
+                         size_t dev_bytes, void* stream) {
+  std::vector<int32_t> words;
+  cp_status st = build_prefix_plan(C, R, prefix_len, members, layout, Hq, Hkv, n_workers, &words);
+  if (st != CP_OK) return st;
+  st = copy_plan(words, host_plan, host_bytes, dev_plan, dev_bytes, words.size() * 4, (cudaStream_t)stream);
+  return st == CP_OK ? ok() : st;
+}
+
+cp_status cp_prefix_workspace_size(const void* host_plan, int D, int P, size_t* bytes) {
+  cp_plan_header h;
+  const cp_status st = read_header(host_plan, 3, &h);
+  if (st != CP_OK) return st;
+  if (!bytes || D < 1 || P < 0) return fail(CP_ERR_INVALID_ARG, "bad arguments");
+  *bytes = prefix_parts(h, (const int32_t*)host_plan, P) * kPrefixRows * (D + 1) * sizeof(float);
+  return ok();
+}
+
+cp_status cp_prefix_attn(const void* host_plan, const void* dev_plan, cp_dtype kv_dtype, const void* q,
+                         const void* const* shard_k, const void* const* shard_v,
+                         const float* const* shard_scale, int Hq, int Hkv, int D, float sm_scale, int P,
+                         const float* own_o, const float* own_lse, void* o, cp_dtype o_dtype, float* lse,
+                         void* ws, size_t ws_bytes, void* stream) {
+  cp_plan_header h;
+  PrefixArgs a;
+  cp_status st = prefix_args(host_plan, dev_plan, kv_dtype, q, shard_k, shard_v, shard_scale, Hq, Hkv, D, sm_scale, P,
+                             own_o, own_lse, o, o_dtype, lse, ws, ws_bytes, &h, &a);
+  if (st != CP_OK) return st;
+  long long shard_rows[CP_MAX_SHARDS] = {0};
+  for (int r = 0; r < h.C; ++r) {
+    shard_rows[r] = pair_rows_of_shard(h, (const int32_t*)host_plan, r);
+    if (shard_rows[r] == 0) continue;
+    if (!shard_k[r] || !aligned16(shard_k[r]) || !shard_v[r] || !aligned16(shard_v[r]))
+      return fail(CP_ERR_INVALID_ARG, "shard_k[%d] or shard_v[%d] NULL or misaligned", r, r);
+    if (shard_scale && !shard_scale[r]) return fail(CP_ERR_INVALID_ARG, "shard_scale[%d] is NULL", r);
+    a.k.p[r] = shard_k[r];
+    a.v.p[r] = shard_v[r];
+    if (shard_scale) a.sc.p[r] = shard_scale[r];
+  }
+  return run_prefix(h, (const int32_t*)host_plan, a, kv_dtype, shard_rows, (cudaStream_t)stream);
+}
+
+cp_status cp_prefix_attn_paged(const void* host_plan, const void* dev_plan, cp_dtype kv_dtype, const void* q,
+                               const void* k_pool, const void* v_pool, const float* scale_pool,
+                               const int32_t* host_page_table, const int32_t* dev_page_table, int max_pages,
+                               int page_size, int num_pages, int Hq, int Hkv, int D, float sm_scale, int P,
+                               const float* own_o, const float* own_lse, void* o, cp_dtype o_dtype, float* lse,
+                               void* ws, size_t ws_bytes, void* stream) {
+  cp_plan_header h;
+  PrefixArgs a;
+  cp_status st = prefix_args(host_plan, dev_plan, kv_dtype, q, k_pool, v_pool, scale_pool, Hq, Hkv, D, sm_scale, P,
+                             own_o, own_lse, o, o_dtype, lse, ws, ws_bytes, &h, &a);
+  if (st != CP_OK) return st;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(CP_ERR_INVALID_ARG, "k_pool or v_pool is not 16-byte aligned");
+  st = check_pages(h, (const int32_t*)host_plan, host_page_table, max_pages, page_size, num_pages, false, &a.rm, dev_page_table);
+  if (st != CP_OK) return st;
+  long long shard_rows[CP_MAX_SHARDS] = {0};
+  for (int r = 0; r < h.C; ++r) {
+    a.k.p[r] = k_pool;
+    a.v.p[r] = v_pool;
+    a.sc.p[r] = scale_pool;
+    shard_rows[r] = pair_rows_of_shard(h, (const int32_t*)host_plan, r);
+  }
+  return run_prefix(h, (const int32_t*)host_plan, a, kv_dtype, shard_rows, (cudaStream_t)stream);
+}
+
+// ------------------------------------------------------------------ accumulated weights
+
+cp_status cp_prefill_weights_workspace_size(const void* host_plan, cp_dtype dtype, int Hq, int D, int window, size_t* bytes) {
+  cp_plan_header h;
+  const cp_status st = read_header(host_plan, 0, &h);
+  if (st != CP_OK) return st;
+  if (!bytes || Hq < 1 || D < 1 || window < 0) return fail(CP_ERR_INVALID_ARG, "bad arguments");
+  *bytes = 0;
+  return ok();
+}
+
+cp_status cp_prefill_weights(const void* host_plan, const void* dev_plan, cp_dtype dtype, const void* q,
+                             const void* k, const float* lse, int Hq, int Hkv, int D, float sm_scale, int window,
+                             float* out, void* ws, size_t ws_bytes, void* stream) {
+  cp_plan_header h;
+  cp_status st = read_header(host_plan, 0, &h);
+  if (st != CP_OK) return st;
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv) return fail(CP_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d", Hq, Hkv);
+  if (dtype != CP_BF16 && dtype != CP_FP32) return fail(CP_ERR_UNSUPPORTED, "dtype must be bf16 or fp32");
+  if (D < 32 || D > 128 || D % 32) return fail(CP_ERR_UNSUPPORTED, "head dim D=%d: need a multiple of 32 in [32, 128]", D);
+  if (dtype == CP_BF16 && D != 64 && D != 128) return fail(CP_ERR_UNSUPPORTED, "bf16 weights need D in {64, 128}, got %d", D);
+  if (!(sm_scale > 0.f)) return fail(CP_ERR_INVALID_ARG, "sm_scale must be > 0");
+  if (window < 0) return fail(CP_ERR_INVALID_ARG, "window=%d must be >= 0", window);
+  size_t need = 0;
+  st = cp_prefill_weights_workspace_size(host_plan, dtype, Hq, D, window, &need);
+  if (st != CP_OK) return st;
+  if (ws_bytes < need || (need && !ws)) return fail(CP_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  if (need && !aligned16(ws)) return fail(CP_ERR_INVALID_ARG, "ws is not 16-byte aligned");
+  if (h.KV == 0) return ok();
+  if (!dev_plan || !k || !out || (h.T > 0 && (!q || !lse))) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(dev_plan) || !aligned16(k) || !aligned16(out) || (h.T > 0 && (!aligned16(q) || !aligned16(lse))))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  const PrefillWeightsArgs a = {{(const int32_t*)dev_plan, h.off_req, h.off_seg, h.C, h.R, h.T, h.KV, h.kind == 0}, q, k,
+                                lse, out, Hq, Hkv, Hq / Hkv, window, sm_scale};
+  const cudaError_t e = launch_prefill_weights_simt(a, dtype == CP_BF16, D, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill weights kernel");
+  return ok();
+}
+
+cp_status cp_decode_weights(const void* host_plan, const void* dev_plan, cp_decode_mode mode, cp_dtype kv_dtype,
+                            const void* q, const void* k_pool, const float* scale_pool,
+                            const int32_t* host_page_table, const int32_t* dev_page_table, int max_pages,
+                            int page_size, int num_pages, int Hq, int Hkv, int Dqk, float sm_scale,
+                            const float* lse, float* weights, void* stream) {
+  cp_plan_header h;
+  cp_status st = read_header(host_plan, 2, &h);
+  if (st != CP_OK) return st;
+  if (h.layout == CP_DCP_SELECTED) return fail(CP_ERR_INVALID_ARG, "a selection plan has no pages");
+  if (!dev_plan || !q || !k_pool || !lse || !weights) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(dev_plan) || !aligned16(q) || !aligned16(k_pool) || !aligned16(lse) || !aligned16(weights))
+    return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
+  st = check_decode_shapes(mode, kv_dtype, mode == CP_DECODE_GQA, scale_pool != nullptr, Hq, Hkv, Dqk,
+                           mode == CP_DECODE_MLA ? 512 : Dqk, sm_scale, plan_s_q(h));
+  if (st != CP_OK) return st;
+  DecodeWeightsArgs a;
+  memset(&a, 0, sizeof(a));
+  st = check_pages(h, (const int32_t*)host_plan, host_page_table, max_pages, page_size, num_pages, true, &a.rm, dev_page_table);
+  if (st != CP_OK) return st;
+  if (h.T == 0) return ok();
+  a.plan = (const int32_t*)dev_plan;
+  a.off_pair = h.off_rank;
+  a.off_worker = h.off_req;
+  a.off_work = h.off_seg;
+  a.B = h.R;
+  a.q = q;
+  a.k = k_pool;
+  a.scale = scale_pool;
+  a.lse = lse;
+  a.weights = weights;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.s_q = plan_s_q(h);
+  a.sm_scale = sm_scale;
+  const cudaError_t e = launch_decode_weights_simt(a, kv_dtype, Dqk, h.n_tiles, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "decode weights kernel");
+  return ok();
+}
+
+// ------------------------------------------------------------------ eviction
+
+cp_status cp_evict_select(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, const int32_t* page_table,
+                          int max_pages, int page_size, int num_pages, const float* weights, const int32_t* pos,
+                          int keep_below, const int32_t* keep_from, int max_moves, int32_t* src, int32_t* dst,
+                          int32_t* count, void* stream) {
+  const cp_status st = check_pool_shape(C, B, max_pages, page_size, num_pages);
+  if (st != CP_OK) return st;
+  if (max_moves < 1 || (long long)C * B * max_moves > 0x7FFFFFFFLL)
+    return fail(CP_ERR_INVALID_ARG, "max_moves=%d: need >= 1 and C B max_moves < 2^31", max_moves);
+  if (!ctx_len || !keep_len || !page_table || !weights || !src || !dst || !count)
+    return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  const EvictArgs a = {C, B, ctx_len, keep_len, page_table, max_pages, page_size, num_pages, weights, pos,
+                       keep_below, keep_from, max_moves, src, dst, count};
+  const cudaError_t e = launch_evict_select(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "evict select kernel");
+  return ok();
+}
+
+cp_status cp_cache_move(int pairs, int max_moves, const int32_t* src, const int32_t* dst, const int32_t* count,
+                        void* k_pool, void* v_pool, int row_bytes, float* scale_pool, float* weights, int32_t* pos,
+                        int64_t pool_rows, void* stream) {
+  if (pairs < 0 || max_moves < 1 || (long long)pairs * max_moves > 0x7FFFFFFFLL)
+    return fail(CP_ERR_INVALID_ARG, "pairs=%d must be >= 0, max_moves=%d >= 1, their product < 2^31", pairs, max_moves);
+  if (pool_rows < 1 || pool_rows > 0x7FFFFF00LL) return fail(CP_ERR_INVALID_ARG, "pool_rows=%lld out of range", (long long)pool_rows);
+  if (row_bytes < 16 || row_bytes % 16) return fail(CP_ERR_UNSUPPORTED, "row_bytes=%d is not a positive multiple of 16", row_bytes);
+  if (pairs == 0) return ok();
+  if (!src || !dst || !count || !k_pool) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(CP_ERR_INVALID_ARG, "a pool is not 16-byte aligned");
+  const MoveArgs a = {src, dst, count, pairs, max_moves, k_pool, v_pool, row_bytes,
+                      {(uint32_t*)scale_pool, (uint32_t*)weights, (uint32_t*)pos}, (long long)pool_rows};
+  const cudaError_t e = launch_cache_move(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache move kernel");
+  return ok();
+}
+
+cp_status cp_page_release(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, int32_t* page_table,
+                          int max_pages, int page_size, int num_pages, int32_t* free_ids, int n_free,
+                          const int32_t* free_pos, float* weights, int32_t* pos, int32_t* info, void* stream) {
+  const cp_status st = check_pool_shape(C, B, max_pages, page_size, num_pages);
+  if (st != CP_OK) return st;
+  if (n_free < 0) return fail(CP_ERR_INVALID_ARG, "n_free=%d must be >= 0", n_free);
+  if (!ctx_len || !keep_len || !page_table || !free_pos || !info || (n_free && !free_ids))
+    return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(info)) return fail(CP_ERR_INVALID_ARG, "info is not 16-byte aligned");
+  if (free_pos >= info && free_pos < info + 4)
+    return fail(CP_ERR_INVALID_ARG, "free_pos lies in this call's info: pass an earlier call's");
+  const ReleaseArgs a = {C, B, ctx_len, keep_len, page_table, max_pages, page_size, num_pages, free_ids, n_free,
+                         free_pos, weights, pos, info};
+  const cudaError_t e = launch_page_release(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "page release kernel");
   return ok();
 }
 

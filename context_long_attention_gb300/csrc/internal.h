@@ -238,6 +238,97 @@ struct AppendArgs {
 // and one scale a token.
 cudaError_t launch_cache_append(const AppendArgs& a, cp_dtype src, cp_dtype pool, cudaStream_t s);
 
+// ---- rotary positions (rope.cu)
+struct RopeSide {
+  const void* x;
+  void* out;                         // x itself: in place
+  long long x_stride, out_stride;    // elements between tokens
+  int heads, dim;
+};
+struct RopeArgs {
+  RopeSide q, k;                     // k.heads == 0: none
+  const int32_t* pos;                // [T]
+  const unsigned long long* turns;   // [rot / 2] frequencies in 2^-64 turns a position
+  int T, rot;
+  bool half, tail, inverse;
+  float scale;
+};
+cudaError_t launch_rope(const RopeArgs& a, bool bf16, cudaStream_t s);
+
+// ---- attention over shared prefixes (prefix_attn.cu)
+constexpr int kPrefixRows = 256;  // query rows x heads of a kv head in one block of work
+struct PrefixArgs {
+  const int32_t* plan;
+  int off_pair, off_worker, off_item, off_tiles, off_block;
+  int C, R, N;
+  RowMap rm;
+  const void* q;
+  ShardPtrs k, v;
+  ScalePtrs sc;
+  int Hq, Hkv, G, D;
+  float sm_scale;
+  void* o;
+  bool o_bf16;
+  float* lse;
+  float *ws_o, *ws_lse;              // parts: [slot][kPrefixRows][D], [slot][kPrefixRows]
+  int P;                             // the caller's own partial results
+  const float *own_o, *own_lse;      // [P][N][Hq][D], [P][N][Hq]
+};
+cudaError_t launch_prefix_simt(const PrefixArgs& a, cp_dtype kv, int workers, cudaStream_t s);
+// The first `blocks` blocks of the plan's list, from parts to results.
+cudaError_t launch_prefix_merge(const PrefixArgs& a, int blocks, cudaStream_t s);
+
+// ---- accumulated attention weights (key_weights.cu)
+struct PrefillWeightsArgs;
+struct DecodeWeightsArgs {
+  const int32_t* plan;
+  int off_pair, off_worker, off_work, B;
+  RowMap rm;
+  const void *q, *k;
+  const float *scale, *lse;          // scale_pool (E4M3) or nullptr; [B s_q][Hq]
+  float* weights;                    // [pool_rows], added to
+  int Hq, Hkv, G, s_q;
+  float sm_scale;
+};
+cudaError_t launch_prefill_weights_simt(const PrefillWeightsArgs& a, bool bf16, int D, cudaStream_t s);
+cudaError_t launch_decode_weights_simt(const DecodeWeightsArgs& a, cp_dtype kv, int D, int workers, cudaStream_t s);
+
+// ---- eviction by weight from a paged cache (evict_kernels.cu)
+struct EvictArgs {
+  int C, B;
+  const int32_t *ctx_len, *keep_len;  // [B]
+  const int32_t* table;               // [C * B][max_pages]
+  int max_pages, page_size, num_pages;
+  const float* weights;               // [pool_rows]
+  const int32_t* pos;                 // [pool_rows], or nullptr: row i of shard r is token i C + r
+  int keep_below;
+  const int32_t* keep_from;           // [B] or nullptr
+  int max_moves;
+  int32_t *src, *dst, *count;         // [C * B][max_moves] twice, [C * B]
+};
+cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s);
+struct MoveArgs {
+  const int32_t *src, *dst, *count;
+  int pairs, max_moves;
+  void *k, *v;
+  int row_bytes;
+  uint32_t* words[3];                 // pools of one word a row (scales, weights, positions) or nullptr
+  long long pool_rows;
+};
+cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t s);
+struct ReleaseArgs {
+  int C, B;
+  const int32_t *ctx_len, *keep_len;
+  int32_t* table;
+  int max_pages, page_size, num_pages;
+  int32_t* free_ids;
+  int n_free;
+  const int32_t* free_pos;
+  float* weights;                     // [pool_rows] or nullptr
+  int32_t *pos, *info;                // [pool_rows] or nullptr; [4]
+};
+cudaError_t launch_page_release(const ReleaseArgs& a, cudaStream_t s);
+
 // ---- sparse decode: exact sharded top-k and the owners' gather (sparse_kernels.cu)
 // Decode kernels given a pair_count (device, one per (shard, request) pair)
 // read only the first pair_count[pair] rows of each pair.

@@ -1,0 +1,195 @@
+// Attention of groups of queries over the prefix that each group shares: the
+// CUDA-core form and the merge of the parts.  (bf16 and FP8 caches at the usual
+// head dims run on the tensor cores, prefix_tc.cu.)
+//
+// The query rows of a group and the G = Hq / Hkv heads of a kv head are the rows
+// m = n G + i of one attention over the group's keys, in blocks of 256.  The plan
+// cuts the (block, key tile) walk evenly over the workers; a block cut between
+// workers, or joined with the partial results of the queries' own tokens, goes
+// through parts in the workspace, combined exactly by log-sum-exp ("How GPUs
+// Share a Long Context During LLM Inference" §3.3).
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "early_launch.cuh"
+#include "internal.h"
+
+namespace cpattn {
+namespace {
+
+__device__ __forceinline__ float ld_elem(const float* p, long long i) { return p[i]; }
+__device__ __forceinline__ float ld_elem(const __nv_bfloat16* p, long long i) { return __bfloat162float(p[i]); }
+__device__ __forceinline__ float ld_elem(const __nv_fp8_e4m3* p, long long i) { return float(p[i]); }
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+
+// A warp a row m, lane l holding dims l, l + 32, ...: every shape that the tensor
+// cores do not take (fp32, other head dims, a paged FP8 pool).
+constexpr int kSimtWarps = 4;
+template <typename TQ, typename T, int ND>
+__global__ void __launch_bounds__(kSimtWarps * 32) prefix_simt_kernel(const PrefixArgs a) {
+  constexpr int D = ND * 32;
+  const int lane = threadIdx.x & 31, dm = blockIdx.y * kSimtWarps + (threadIdx.x >> 5);
+  const TQ* q = static_cast<const TQ*>(a.q);
+  for (int wi = a.plan[a.off_worker + blockIdx.x]; wi < a.plan[a.off_worker + blockIdx.x + 1]; ++wi) {
+    const cp_prefix_item it = reinterpret_cast<const cp_prefix_item*>(a.plan + a.off_item)[wi];
+    if (dm >= it.m_rows) continue;
+    const int m = it.m0 + dm, head = it.kv_head * a.G + m % a.G;
+    const long long n = it.row0 + m / a.G;
+    float qv[ND], acc[ND], mx = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < ND; ++e) {
+      qv[e] = ld_elem(q, (n * a.Hq + head) * D + lane + 32 * e);
+      acc[e] = 0.f;
+    }
+    const int32_t* tile_off = a.plan + a.off_tiles + it.group * (a.C + 1);
+    for (int r = 0; r < a.C; ++r) {
+      const int t0 = max(it.tile_begin, tile_off[r]) - tile_off[r], t1 = min(it.tile_end, tile_off[r + 1]) - tile_off[r];
+      const int pair = r * a.R + it.group;
+      const cp_pair_desc pd = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair)[pair];
+      const T* kb = static_cast<const T*>(a.k.p[r]);
+      const T* vb = static_cast<const T*>(a.v.p[r]);
+      const float* scr = a.sc.p[r];
+      for (int row = t0 * kDecodeTileRows; row < min(pd.rows, t1 * kDecodeTileRows); ++row) {
+        const long long cr = map_row(a.rm, pair, pd.row_off, row);
+        const long long kr = (cr * a.Hkv + it.kv_head) * D + lane;
+        const float rs = scr ? scr[cr] : 1.f;
+        float part = 0.f, vv[ND];
+#pragma unroll
+        for (int e = 0; e < ND; ++e) {
+          part += qv[e] * ld_elem(kb, kr + 32 * e);
+          vv[e] = ld_elem(vb, kr + 32 * e) * rs;
+        }
+        const float s = a.sm_scale * rs * warp_sum(part);
+        const float mn = fmaxf(mx, s), corr = expf(mx - mn), p = expf(s - mn);
+        l = l * corr + p;
+#pragma unroll
+        for (int e = 0; e < ND; ++e) acc[e] = acc[e] * corr + p * vv[e];
+        mx = mn;
+      }
+    }
+    const float inv = 1.f / l, lse = mx + logf(l);
+    if (it.alone && !a.P) {
+      const long long at = n * a.Hq + head;
+#pragma unroll
+      for (int e = 0; e < ND; ++e) {
+        const long long i = at * D + lane + 32 * e;
+        if (a.o_bf16) static_cast<__nv_bfloat16*>(a.o)[i] = __float2bfloat16_rn(acc[e] * inv);
+        else static_cast<float*>(a.o)[i] = acc[e] * inv;
+      }
+      if (lane == 0) a.lse[at] = lse;
+    } else {
+      const long long at = (long long)it.part * kPrefixRows + dm;
+#pragma unroll
+      for (int e = 0; e < ND; ++e) a.ws_o[at * D + lane + 32 * e] = acc[e] * inv;
+      if (lane == 0) a.ws_lse[at] = lse;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ merge
+
+// A warp an output row: the weights of its parts, two to a lane at a time, then
+// its dims over the lanes.  Two passes over the parts' LSE and one over their rows.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixArgs a) {
+  constexpr int kPer = kPrefixRows / kMergeWarps;
+  const int lane = threadIdx.x & 31, dm = (blockIdx.x % kPer) * kMergeWarps + (threadIdx.x >> 5);
+  // the plan is no output of an earlier kernel's, but it may be this stream's copy
+  wait_for_earlier_kernels();
+  const cp_prefix_block bl = reinterpret_cast<const cp_prefix_block*>(a.plan + a.off_block)[blockIdx.x / kPer];
+  if (dm >= bl.m_rows) return;
+  const int m = bl.m0 + dm, head = bl.kv_head * a.G + m % a.G;
+  const long long at = (long long)(bl.row0 + m / a.G) * a.Hq + head, NH = (long long)a.N * a.Hq;
+  const int parts = bl.n_parts + a.P;
+  // part i: the block's own parts, then the caller's
+  auto lse_at = [&](int i) {
+    return i < bl.n_parts ? __ldcg(a.ws_lse + (long long)(bl.first_part + i) * kPrefixRows + dm) : __ldcg(a.own_lse + (i - bl.n_parts) * NH + at);
+  };
+  float g = -INFINITY;
+  for (int i = lane; i < parts; i += 32) g = fmaxf(g, lse_at(i));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+  const float g0 = g == -INFINITY ? 0.f : g;
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  float z = 0.f;
+  const int vec = a.D / 4;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const float w = i0 + lane < parts ? expf(lse_at(i0 + lane) - g0) : 0.f;
+    const int n = min(32, parts - i0);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      z += wk;
+      if (wk == 0.f) continue;  // an empty part's row is not read
+      const int i = i0 + k;
+      const float4* row = reinterpret_cast<const float4*>(
+          i < bl.n_parts ? a.ws_o + ((long long)(bl.first_part + i) * kPrefixRows + dm) * a.D : a.own_o + ((i - bl.n_parts) * NH + at) * a.D);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (lane + 32 * c < vec) {
+          const float4 x = __ldcg(row + lane + 32 * c);
+          acc[c].x += wk * x.x;
+          acc[c].y += wk * x.y;
+          acc[c].z += wk * x.z;
+          acc[c].w += wk * x.w;
+        }
+    }
+  }
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int d = 4 * (lane + 32 * c);
+    if (d >= a.D) continue;
+    const float x = acc[c].x * inv, y = acc[c].y * inv, u = acc[c].z * inv, v = acc[c].w * inv;
+    if (a.o_bf16) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(x, y), hi = __floats2bfloat162_rn(u, v);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at * a.D + d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at * a.D + d) = make_float4(x, y, u, v);
+    }
+  }
+  if (lane == 0) a.lse[at] = z > 0.f ? g + logf(z) : -INFINITY;
+}
+
+template <typename TQ, typename T>
+cudaError_t simt_t(const PrefixArgs& a, int workers, cudaStream_t s) {
+  const dim3 grid(workers, kPrefixRows / kSimtWarps);
+  auto run = [&](auto kern) {
+    kern<<<grid, kSimtWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+  };
+  switch (a.D / 32) {
+    case 1: return run(prefix_simt_kernel<TQ, T, 1>);
+    case 2: return run(prefix_simt_kernel<TQ, T, 2>);
+    case 3: return run(prefix_simt_kernel<TQ, T, 3>);
+    case 4: return run(prefix_simt_kernel<TQ, T, 4>);
+    case 5: return run(prefix_simt_kernel<TQ, T, 5>);
+    case 6: return run(prefix_simt_kernel<TQ, T, 6>);
+    case 7: return run(prefix_simt_kernel<TQ, T, 7>);
+    case 8: return run(prefix_simt_kernel<TQ, T, 8>);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_simt(const PrefixArgs& a, cp_dtype kv, int workers, cudaStream_t s) {
+  switch (kv) {
+    case CP_BF16: return simt_t<__nv_bfloat16, __nv_bfloat16>(a, workers, s);
+    case CP_FP32: return simt_t<float, float>(a, workers, s);
+    default: return simt_t<__nv_bfloat16, __nv_fp8_e4m3>(a, workers, s);
+  }
+}
+
+cudaError_t launch_prefix_merge(const PrefixArgs& a, int blocks, cudaStream_t s) {
+  if (blocks == 0) return cudaSuccess;
+  return launch_early(prefix_merge_kernel, (unsigned)blocks * (kPrefixRows / kMergeWarps), kMergeWarps * 32, 0, s, 1, a);
+}
+
+}  // namespace cpattn

@@ -16,6 +16,12 @@
  *                      form's prefill and the per-head products of both forms
  *   cp_page_slots, cp_cache_append
  *                      pages, slots and rows of a step's new tokens
+ *   cp_rope            rotary positions of queries and keys
+ *   cp_prefix_attn     attention of groups of queries over a shared prefix
+ *   cp_prefill_weights, cp_decode_weights
+ *                      the attention weight that each cached token received
+ *   cp_evict_select, cp_cache_move, cp_page_release
+ *                      eviction by that weight from a paged cache
  *
  * Sources (page title, section):
  *   [CTX] "How GPUs Share a Long Context During LLM Inference"
@@ -84,7 +90,7 @@ typedef enum {
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t magic;      /* CP_PLAN_MAGIC */
-  int32_t kind;       /* 0 zigzag prefill, 1 interleave prefill, 2 decode */
+  int32_t kind;       /* 0 zigzag prefill, 1 interleave prefill, 2 decode, 3 shared prefixes */
   int32_t C;          /* number of virtual shards (ranks) */
   int32_t R;          /* number of requests */
   int32_t T;          /* prefill: total new tokens; decode: total cached tokens */
@@ -633,6 +639,189 @@ cp_status cp_cache_append(const int32_t* slots, int n, cp_dtype src_dtype, const
                           const void* v_new, int64_t v_stride, const float* new_scale, int row_elems,
                           cp_dtype pool_dtype, void* k_pool, void* v_pool, float* scale_pool,
                           int64_t pool_rows, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cp_rope — rotary positions of queries and keys.
+ *
+ * Pair i < rot / 2 of a head's rotated part turns by t_i = pos x f_i:
+ *   (a, b) -> scale (a cos t_i - b sin t_i, b cos t_i + a sin t_i)
+ * CP_ROPE_HALF: the pair is (x[i], x[i + rot / 2]); CP_ROPE_INTERLEAVED:
+ * (x[2 i], x[2 i + 1]).  The rotated part is the first rot dims of a head, or
+ * with tail != 0 the last ones (the 64 rotated dims of latent attention); the
+ * others are copied as they are.  inverse != 0 turns by -t_i: the gradient of the
+ * inputs from that of the outputs (the map is linear and this is its transpose).
+ *
+ * pos    [T] int32 device, any value (a position of a prompt: the plan's qpos)
+ * turns  [rot / 2] uint64 device: f_i / (2 pi) x 2^64, modulo 2^64, so that angles
+ *        of far positions lose nothing; scale multiplies cos and sin (1, or the
+ *        attention factor of a scaling for long contexts)
+ * q, k   [T][heads][dim] of `dtype` (CP_BF16 or CP_FP32) with dense heads and a
+ *        stride of *_stride elements between tokens (a view of the cache's
+ *        entries, say); k_heads = 0: no k.  q_out == q (with its stride) turns in
+ *        place and then touches the rotated part only; outputs overlap no input
+ *        otherwise.  Angles, sines and products in fp32, rounded once.
+ * rot in [16, 1024], a multiple of 16, at most dim; dim a multiple of 8; strides
+ * multiples of 8 elements; q_heads q_dim + k_heads k_dim <= 262,144.  T = 0
+ * launches nothing.
+ * ------------------------------------------------------------------------- */
+enum { CP_ROPE_HALF = 0, CP_ROPE_INTERLEAVED = 1 };
+cp_status cp_rope(int T, const int32_t* pos, const uint64_t* turns, int rot, int layout, int tail, int inverse,
+                  float scale, cp_dtype dtype, const void* q, int64_t q_stride, int q_heads, int q_dim,
+                  void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, int k_heads, int k_dim,
+                  void* k_out, int64_t k_out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cp_prefix_attn — attention of groups of queries over the cached prefix that
+ * each group shares (a batch behind one system prompt or document).
+ *
+ * Group g of R has prefix_len[g] cached tokens and members[g] consecutive query
+ * rows (a request's one row, or its s_q rows); every row of the group reads
+ * all of the prefix.  The prefix lies in the cache as R requests of
+ * prefix_len[g] tokens of a decode plan would (cp_decode_plan(_ex) of the same C
+ * and layout serves cp_kv_shard_pack(_paged)): in C shards, or in the pages of one
+ * pool.  Each key and value is then read once for a block of up to 256 query
+ * rows x heads of its kv head, instead of once a request.
+ *
+ * The results over all shards are combined ([CTX] §3.3), together with P >= 0
+ * partial results of the queries' own tokens, own_o [P, N, Hq, D] and own_lse
+ * [P, N, Hq] fp32 (N = sum of members; the o_part and lse_part of a
+ * cp_decode_attn call over the own tokens with P = its C): o [N, Hq, D] of
+ * o_dtype CP_BF16 or CP_FP32, lse [N, Hq] fp32.  A row without keys gets O = 0,
+ * LSE = -inf; a part of LSE = -inf is not read.
+ *
+ * q [N, Hq, D]; kv_dtype, shard_k, shard_v, shard_scale, head dims and pools as
+ * for CP_DECODE_GQA.  On the tensor cores: bf16 with D = 64 or 128 (shards or a
+ * pool), E4M3 with D = 128 (shards); every other shape on the CUDA cores.
+ * n_workers: CTAs that the work is cut for (0 = the SM count).
+ * ws: cp_prefix_workspace_size() bytes (NULL if that is 0).
+ * Errors: as for cp_decode_attn; CP_ERR_INVALID_ARG for members < 0, no query
+ * row at all, or a plan of other head counts.
+ * ------------------------------------------------------------------------- */
+/* Up to 256 query rows x heads of a group and kv head: row m is query row0 + m / (Hq/Hkv),
+ * head kv_head (Hq/Hkv) + m mod (Hq/Hkv). */
+typedef struct {
+  int32_t group, kv_head;
+  int32_t row0;        /* the group's first query row */
+  int32_t m0, m_rows;  /* rows m0 .. m0 + m_rows - 1 */
+  int32_t first_part, n_parts;  /* its parts in the workspace, consecutive */
+  int32_t reserved;
+} cp_prefix_block;
+/* A range of key tiles (128 rows of a shard; the group's tiles shard by shard) of one block. */
+typedef struct {
+  int32_t group, kv_head, row0, m0, m_rows;
+  int32_t tile_begin, tile_end;
+  int32_t part;        /* workspace slot */
+  int32_t alone;       /* the block's only item: its result needs no merge */
+  int32_t reserved[3];
+} cp_prefix_item;
+/* Plan tables of kind 3: off_rank cp_pair_desc[C * R], off_req worker_off[n_tiles + 1],
+ * off_seg cp_prefix_item[n_seg], off_tiles int32 [R][C + 1] first tile of every
+ * shard, off_rtile int32 [R + 1] first query row of every group, off_run
+ * cp_prefix_block[n_split], those that need a merge (no part or several) first;
+ * T = N query rows, KV = prefix tokens, off_idx -> int32 {Hq, Hkv, blocks that
+ * need a merge, their parts}. */
+cp_status cp_prefix_plan_size(int C, int R, const int32_t* prefix_len, const int32_t* members,
+                              cp_dcp_layout layout, int Hq, int Hkv, int n_workers, size_t* host_bytes,
+                              size_t* dev_bytes);
+cp_status cp_prefix_plan(int C, int R, const int32_t* prefix_len, const int32_t* members, cp_dcp_layout layout,
+                         int Hq, int Hkv, int n_workers, void* host_plan, size_t host_bytes, void* dev_plan,
+                         size_t dev_bytes, void* stream);
+cp_status cp_prefix_workspace_size(const void* host_plan, int D, int P, size_t* bytes);
+cp_status cp_prefix_attn(const void* host_plan, const void* dev_plan, cp_dtype kv_dtype, const void* q,
+                         const void* const* shard_k, const void* const* shard_v,
+                         const float* const* shard_scale, int Hq, int Hkv, int D, float sm_scale, int P,
+                         const float* own_o, const float* own_lse, void* o, cp_dtype o_dtype, float* lse,
+                         void* ws, size_t ws_bytes, void* stream);
+cp_status cp_prefix_attn_paged(const void* host_plan, const void* dev_plan, cp_dtype kv_dtype, const void* q,
+                               const void* k_pool, const void* v_pool, const float* scale_pool,
+                               const int32_t* host_page_table, const int32_t* dev_page_table, int max_pages,
+                               int page_size, int num_pages, int Hq, int Hkv, int D, float sm_scale, int P,
+                               const float* own_o, const float* own_lse, void* o, cp_dtype o_dtype, float* lse,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cp_prefill_weights, cp_decode_weights — the attention weight that cached
+ * tokens received, the measure that eviction goes by:
+ *   w_j = sum over queries i that read token j and query heads h of
+ *         exp(sm_scale <q_ih, k_jg> - LSE_ih)
+ * with the LSE that the attention itself returned.  A query row of LSE = -inf
+ * (no keys) weighs nothing.  Sums in fp32, always in the same order.
+ *
+ * cp_prefill_weights: the tokens of a prompt batch.  host_plan, dev_plan, q
+ *   [T, Hq, D], k [KV, Hkv, D] as given to cp_prefill_attn and lse [T, Hq] as it
+ *   returned it for all ranks (rank-major); out [KV] fp32 is written.  window = 0:
+ *   every query; else the last `window` new tokens of every request.  dtype
+ *   CP_BF16 (D = 64, 128: tensor cores) or CP_FP32 (D = 32, 64, 96, 128: CUDA cores).
+ *   ws: cp_prefill_weights_workspace_size() bytes (NULL if that is 0).
+ * cp_decode_weights: a decode step over a paged pool.  The plan, q and the page
+ *   table as given to cp_decode_attn_paged, lse [B, (s_q,) Hq] the merged one;
+ *   weights [pool_rows] fp32: the sums are added to the rows of the requests, all
+ *   other rows stay.  mode CP_DECODE_MLA: k_pool [pool_rows, 576], one kv head.
+ *   On the tensor cores: bf16 at D = 64 or 128 and at 576 (MLA), E4M3 at D = 128
+ *   and 576, with at most 64 query rows x heads a kv head and 96 KB of query
+ *   operands; every other shape on the CUDA cores.
+ *   No page may belong to two pairs.
+ * Errors: as for cp_prefill_attn and cp_decode_attn_paged; window < 0.
+ * ------------------------------------------------------------------------- */
+cp_status cp_prefill_weights_workspace_size(const void* host_plan, cp_dtype dtype, int Hq, int D, int window,
+                                            size_t* bytes);
+cp_status cp_prefill_weights(const void* host_plan, const void* dev_plan, cp_dtype dtype, const void* q,
+                             const void* k, const float* lse, int Hq, int Hkv, int D, float sm_scale, int window,
+                             float* out, void* ws, size_t ws_bytes, void* stream);
+cp_status cp_decode_weights(const void* host_plan, const void* dev_plan, cp_decode_mode mode, cp_dtype kv_dtype,
+                            const void* q, const void* k_pool, const float* scale_pool,
+                            const int32_t* host_page_table, const int32_t* dev_page_table, int max_pages,
+                            int page_size, int num_pages, int Hq, int Hkv, int Dqk, float sm_scale,
+                            const float* lse, float* weights, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Eviction by weight from a paged token-sharded cache.
+ *
+ * Request b holds ctx_len[b] tokens and shall hold keep_len[b] (both [B] int32
+ * device).  Its pair on shard r has n = ceil((ctx_len - r) / C) rows and keeps
+ * the m = min(n, ceil((keep_len - r) / C)) first of them in this order:
+ * protected rows, by rising row; then the others by falling weight, equal ones by
+ * rising row, a NaN weight last.  Protected: rows of position < keep_below or (keep_from [B] given)
+ * >= keep_from[b], where pos [pool_rows] int32 holds each row's position; pos
+ * NULL: row i of shard r is token i C + r, as before any eviction.
+ * Afterwards the pair's rows 0 .. m - 1 hold the kept tokens, in no order of
+ * position, and plans, tables and slots of keep_len tokens (CP_DCP_ROUND_ROBIN,
+ * one query row) describe the cache.
+ *
+ * cp_evict_select: weights [pool_rows] and page_table as elsewhere; writes, for
+ *   each pair r B + b, count moves and the pool rows src -> dst of each: the kept
+ *   rows at or behind m, in order, into the places of the evicted rows before m, in
+ *   order; -1 behind the last ([C B][max_moves], count [C B]).  A pair whose lengths
+ *   are negative or past its pages, which has a page id outside [0, num_pages) or
+ *   needs more than max_moves moves (min(m, n - m) is enough) gets count = -1 and
+ *   no move.  Nothing else is written.
+ * cp_cache_move: the moves, on the rows of k_pool and (or NULL) v_pool, of
+ *   row_bytes each (a multiple of 16), and the words of scale_pool, weights and
+ *   pos (each or NULL).  A pair of count <= 0 and a move of a row outside the pool
+ *   are skipped.  All sources must differ from all destinations.
+ * cp_page_release: what the shorter requests no longer need.  The pages behind
+ *   ceil(m / page_size) of every pair go back to free_ids, in the order of
+ *   requests, shards, pages, at positions info[1] .. *free_pos - 1 (a list that
+ *   cp_page_slots takes from at info[1]), their table entries become -1, and rows
+ *   m .. of the pages that a pair held get weight 0 and position -1 (weights,
+ *   pos: each or NULL), so that tokens appended there start at weight 0.
+ *   info [4] int32, 16-byte aligned: {status, the next free_pos, pages released, 0}.
+ *   A step that does not fit is reported as a sum of CP_SLOTS_BAD_LENGTH (a negative
+ *   length), CP_SLOTS_TABLE_FULL (a pair of more than max_pages pages) and
+ *   CP_SLOTS_NO_PAGES (*free_pos outside [0, n_free], or fewer than the released
+ *   pages); nothing else is written then.  keep_len >= ctx_len releases nothing.
+ * Errors: as for cp_page_slots; max_moves < 1; C B max_moves >= 2^31.
+ * ------------------------------------------------------------------------- */
+cp_status cp_evict_select(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, const int32_t* page_table,
+                          int max_pages, int page_size, int num_pages, const float* weights, const int32_t* pos,
+                          int keep_below, const int32_t* keep_from, int max_moves, int32_t* src, int32_t* dst,
+                          int32_t* count, void* stream);
+cp_status cp_cache_move(int pairs, int max_moves, const int32_t* src, const int32_t* dst, const int32_t* count,
+                        void* k_pool, void* v_pool, int row_bytes, float* scale_pool, float* weights, int32_t* pos,
+                        int64_t pool_rows, void* stream);
+cp_status cp_page_release(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, int32_t* page_table,
+                          int max_pages, int page_size, int num_pages, int32_t* free_ids, int n_free,
+                          const int32_t* free_pos, float* weights, int32_t* pos, int32_t* info, void* stream);
 
 /* ---------------------------------------------------------------------------
  * cp_lse_merge — exact combine of P partial results ([CTX] §3.3; [V4] §5).
