@@ -907,7 +907,14 @@ cp_status prefix_args(const void* host_plan, const void* dev_plan, cp_dtype kv_d
 cp_status run_prefix(const cp_plan_header& h, const int32_t* W, const PrefixArgs& a, cp_dtype kv_dtype,
                      const long long* shard_rows, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  if (h.n_seg > 0) e = launch_prefix_simt(a, kv_dtype, h.n_tiles, s);
+  if (h.n_seg > 0) {
+    if (prefix_tc_supported(kv_dtype, a.D)) {
+      const char* stall = getenv("CPATTN_TEST_STALL");  // test hook of the bounded waits
+      e = launch_prefix_tc(a, shard_rows, h.n_tiles, stall && stall[0] == '1', s);
+    } else {
+      e = launch_prefix_simt(a, kv_dtype, h.n_tiles, s);
+    }
+  }
   if (e != cudaSuccess) return cuda_fail(e, "prefix attention kernel");
   e = launch_prefix_merge(a, a.P > 0 ? h.n_split : W[h.off_idx + 2], s);
   if (e != cudaSuccess) return cuda_fail(e, "prefix merge kernel");

@@ -32,7 +32,10 @@ enum KernelId : unsigned {
   kKernDecodeGqaF8 = 5,
   kKernTf32 = 6,
   kKernMlaPrefill = 7,
-  kKernMlaProduct = 8
+  kKernMlaProduct = 8,
+  kKernPrefixTc = 9,
+  kKernPrefillWeights = 10,
+  kKernDecodeWeights = 11
 };
 
 struct ShardPtrs {
@@ -275,6 +278,8 @@ struct PrefixArgs {
   const float *own_o, *own_lse;      // [P][N][Hq][D], [P][N][Hq]
 };
 cudaError_t launch_prefix_simt(const PrefixArgs& a, cp_dtype kv, int workers, cudaStream_t s);
+bool prefix_tc_supported(cp_dtype kv, int D);
+cudaError_t launch_prefix_tc(const PrefixArgs& a, const long long* shard_rows, int workers, bool stall_test, cudaStream_t s);
 // The first `blocks` blocks of the plan's list, from parts to results.
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int blocks, cudaStream_t s);
 

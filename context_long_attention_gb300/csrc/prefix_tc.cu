@@ -1,0 +1,621 @@
+// Attention of groups of queries over a shared prefix on the tcgen05 tensor
+// cores (bf16 cache, head dim 64 or 128).
+//
+// With n requests behind one prefix the n G rows (query, head of the kv head's G)
+// are the M dimension of ordinary matrix products over the prefix, so each key and value
+// is read once for a block of 256 rows.  A worker (one CTA an SM) takes the
+// plan's items one after another, each a range of key tiles of one block:
+//   warps 0-15  softmax: warp w takes rows [32 (w % 4), +32) of chain t = (w / 4) % 2
+//               and, with h = w / 8, one half of its score columns and of O's dims
+//   warp 16     TMA producer: K_j and V_j [128 keys x D] into a ring of slots,
+//               V_(j-1) and K_j as one unit under one barrier
+//   warp 17     MMA issuer (one elected lane) and TMEM owner
+//   warp 18     relay: clears the rows of V behind a shard's last key and adds one
+//               arrival on each chain's P barrier once the step's unit has landed,
+//               so that the issuer's wait for P covers the unit
+// Two chains keep the tensor cores and the exponentials busy in turn.  A block
+// of more than 128 rows: chain t is M tile t, both share the step's K and V.  A
+// block of up to 128 rows (WIDE = false): chain t takes keys [64 t, 64 t + 64) of every
+// tile, and the two results combine in shared memory at the end: a single chain
+// would wait for its own exponentials in every step.
+// TMEM (512 columns): chain t holds S in columns [256 t, +128) (or 64) and O in
+// [256 t + 128, +D).  Each half of a row writes its P (bf16 pairs) over the first
+// half of its own S columns.  The running max moves only when a row's max grows by
+// more than 2^8; any running max gives the exact result (O = sum e^(s-m) v / sum e^(s-m)).
+// P is rounded to bf16 for its product, its sum is not.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace cpattn {
+namespace {
+using namespace tc;
+
+constexpr int BM = 128;  // rows of an M tile
+constexpr int BN = 128;  // keys of a K/V tile
+constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+constexpr int kWarpTma = kSoftmaxWarps, kWarpMma = kSoftmaxWarps + 1, kWarpRelay = kSoftmaxWarps + 2;
+constexpr int kLaunchBoundThreads = 640;  // registers as for five warps an SM sub-partition
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kQBytes = BM * D * 2;
+  static constexpr int kSlotBytes = BN * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kSmem = 2 * kQBytes + kSlots * kSlotBytes + 1024;
+};
+
+// K and V of up to MAXC shards; a pool has one map of each, with 64-row boxes.
+template <int MAXC>
+struct Maps {
+  CUtensorMap k[MAXC], v[MAXC];
+};
+
+struct Params {
+  PrefixArgs a;
+  float scale_log2;
+  unsigned* status;
+  unsigned long long wait_ns;
+  int stall_test;  // test hook: the MMA thread waits on a barrier nobody arrives at
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void mbar_inval(uint32_t bar) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
+
+__device__ void report_timeout(unsigned* status, unsigned site, volatile int* abort) {
+  *abort = 1;
+  if (atomicCAS(status, 0u, 1u) == 0u) {
+    status[1] = kKernPrefixTc;
+    status[2] = site;
+    status[3] = blockIdx.x;
+    __threadfence();
+  }
+}
+
+// The walk over an item's key tiles: shard, first row in the shard, keys in use.
+struct Walk {
+  const int32_t* off;  // [C + 1] first tile of every shard
+  int r, t;
+  __device__ __forceinline__ Walk(const int32_t* o, int first) : off(o), r(0), t(first) {
+    while (off[r + 1] <= t) ++r;
+  }
+  __device__ __forceinline__ void next() {
+    ++t;
+    while (off[r + 1] <= t) ++r;  // not past the last tile: the caller stops there
+  }
+};
+
+struct Shared {
+  uint64_t bar_unit[10], bar_rel[10], bar_q[2], bar_s[2], bar_p[2], bar_o[2], bar_never, bar_drain;
+  uint32_t tmem_slot;
+  volatile int abort_flag;
+  volatile int zero_flag;  // never set: drains ignore the abort flag
+  int32_t tile_off[CP_MAX_SHARDS + 2];
+  int32_t rows[CP_MAX_SHARDS];
+  float m[BM], l[BM];      // chain 1's running max and sum for the combination
+  cp_prefix_item item;
+};
+
+template <int D, bool WIDE, int MAXC>
+__device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Shared& sh, uint8_t* sQ,
+                                        uint8_t* sKV, uint32_t tmem) {
+  using C = Cfg<D>;
+  constexpr int kUnitBars = C::kSlots;
+  constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
+  constexpr int NC = NS / 2;           // of one half of a row
+  // a half row's P sum that can hide a P above 2^8
+  constexpr float kSpecSum = NC * 256.f;
+  const PrefixArgs& a = p.a;
+  const cp_prefix_item& it = sh.item;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nK = it.tile_end - it.tile_begin;
+  volatile int* abort = &sh.abort_flag;
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------ softmax
+    const int quarter = warp & 3, t = (warp >> 2) & 1, half = warp >> 3;
+    const int i = quarter * 32 + lane;  // row within the M tile = TMEM lane
+    const int pbar = 2 + t * 4 + quarter;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t colS = t * 256 + NC * half, colO = t * 256 + 128 + (D / 2) * half;
+    const int row = (WIDE ? t * BM : 0) + i;  // row of the block
+    auto query_row = [&]() -> long long {      // of the row's query and head in q and o (made twice: no register in the loop)
+      const int m = it.m0 + row, n = m / a.G;
+      return (long long)(it.row0 + n) * a.Hq + it.kv_head * a.G + m - n * a.G;
+    };
+    const bool releaser = t == 1 && quarter == 0 && half == 0;  // frees K/V slots
+    // value of the other half of this row, through the last of its S columns, which
+    // P never covers and which S no longer needs once a tile's values are in registers
+    auto exchange = [&](float v) -> float {
+      tmem_st1(lane_addr + t * 256 + NC * half + NC - 1, __float_as_uint(v));
+      tmem_st_wait();
+      tc_fence_before();
+      named_bar_sync(pbar, 64);
+      tc_fence_after();
+      const uint32_t o = tmem_ld1(lane_addr + t * 256 + NC * (half ^ 1) + NC - 1);
+      tmem_ld_wait();
+      return __uint_as_float(o);
+    };
+    {  // this row's query to shared memory (128-byte-swizzled K-major), its pieces over the threads of the row
+      const bool valid = row < it.m_rows;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (valid ? query_row() * D : 0));
+      uint8_t* dst = sQ + (WIDE ? t * C::kQBytes : 0) + i * 128;
+      constexpr int kPer = WIDE ? D / 16 : D / 32;
+      const int first = (WIDE ? half : 2 * t + half) * kPer;
+#pragma unroll
+      for (int c = first; c < first + kPer; ++c) {
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (valid) val = __ldg(src + c);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (BM * 128) + (((c & 7) ^ (i & 7)) << 4)) = val;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&sh.bar_q[t]));
+    }
+    const float sl2 = p.scale_log2;
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true, first = true;  // first: no key of this chain so far
+    int keys = 0;                  // of this half's columns, those in use in this tile
+    auto load_s = [&](uint32_t (&sr)[NC]) {
+      if constexpr (NC == 64) {
+        tmem_ld32(lane_addr + colS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(lane_addr + colS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+      } else {
+        tmem_ld32(lane_addr + colS, sr);
+      }
+      tmem_ld_wait();
+      if (keys < NC) {
+#pragma unroll
+        for (int e = 0; e < NC; ++e)
+          if (e >= keys) sr[e] = __float_as_uint(-INFINITY);
+      }
+    };
+    auto exps = [&](const uint32_t (&sr)[NC], uint32_t (&pk)[NC / 2]) -> float {
+      const float neg = -m_used * sl2;
+      float s0sum = 0.f, s1sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < NC / 2; ++e) {
+        float u0, u1;
+        fma2(u0, u1, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]), sl2, sl2, neg, neg);
+        const float p0 = ex2(u0), p1 = ex2(u1);
+        add2(s0sum, s1sum, s0sum, s1sum, p0, p1);
+        pk[e] = pack_bf16x2(p0, p1);
+      }
+      return s0sum + s1sum;
+    };
+    Walk w(sh.tile_off, it.tile_begin);
+    for (int j = 0; j < nK && ok; ++j) {
+      const int nv = min(BN, sh.rows[w.r] - (w.t - w.off[w.r]) * BN);  // keys of the tile
+      const int chain = WIDE ? nv : nv - 64 * t;                      // of the chain
+      keys = chain - NC * half;
+      if (j + 1 < nK) w.next();
+      const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_s[t]), j & 1, p.wait_ns, abort));
+      if (got && releaser && lane == 0) mbar_arrive(smem_u32(&sh.bar_rel[j % C::kSlots]));
+      tc_fence_after();
+      uint32_t sr[NC], pk[NC / 2];
+      float part = 0.f;
+      const bool fresh = WIDE ? j == 0 : first;
+      bool slow = WIDE ? fresh : fresh && chain > 0;
+      if (!fresh) {
+        // P with the running max as it stands: a half whose P sums past NC x 2^8
+        // holds a P above 2^8 (or a NaN), and the row takes the exact path
+        load_s(sr);
+        part = exps(sr, pk);
+        slow = bar_red_or(pbar, 64, !got || !(part <= kSpecSum));
+      } else if (!WIDE && chain <= 0) {  // nothing to weigh yet
+        if (bar_red_or(pbar, 64, !got)) slow = true;
+#pragma unroll
+        for (int e = 0; e < NC / 2; ++e) pk[e] = 0;
+      }
+      if (slow) {
+        // both warps of these rows leave together: one that gave up meets the other at this vote
+        if (bar_red_or(pbar, 64, !got)) {
+          if (!got) report_timeout(p.status, 1, abort);
+          ok = false;
+          break;
+        }
+        load_s(sr);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < NC / 2; ++e) mx = fmax3(mx, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        const float mrow = fmaxf(mx, exchange(mx));
+        if (fresh) {
+          m_used = mrow;
+          first = false;
+        } else {
+          // Each row moves its own max; the wait and the pair's barrier are taken by every lane
+          const bool need = (mrow - m_used) * sl2 > kRescaleLog2;
+          const float alpha = need ? ex2((m_used - mrow) * sl2) : 1.f;
+          if (need) {
+            l *= alpha;
+            m_used = mrow;
+          }
+          const bool landed = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_o[t]), (j - 1) & 1, p.wait_ns, abort));
+          if (bar_red_or(pbar, 64, !landed)) {
+            if (!landed) report_timeout(p.status, 2, abort);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[16];
+            tmem_ld16(lane_addr + colO + c * 16, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            tmem_st16(lane_addr + colO + c * 16, r);
+          }
+        }
+        part = exps(sr, pk);
+      }
+      l += part;
+      if constexpr (NC == 64) tmem_st32(lane_addr + colS, pk);
+      else tmem_st16(lane_addr + colS, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.bar_p[t]));
+    }
+    // ------------------------------------------------------------ epilogue
+    const bool landed = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_o[t]), (nK - 1) & 1, p.wait_ns, abort));
+    const bool failed = WIDE ? bar_red_or(pbar, 64, !landed) : bar_red_or(1, kSoftmaxWarps * 32, !landed);
+    if (failed) {
+      if (ok && !landed) report_timeout(p.status, 3, abort);
+    } else {
+      tc_fence_after();
+      const bool valid = row < it.m_rows;
+      const long long out_row = valid ? query_row() : 0;
+      float lt = l + exchange(l);
+      float w0 = 1.f;
+      // O of chain 1 [dim][row] in the K/V ring: every product of the item is complete, so it is free
+      float* other = reinterpret_cast<float*>(sKV);
+      if (!WIDE) {
+        if (t == 1) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t r[32];
+            tmem_ld32(lane_addr + colO + c * 32, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) other[((D / 2) * half + c * 32 + e) * BM + i] = __uint_as_float(r[e]);
+          }
+          if (half == 0) {
+            sh.m[i] = m_used;
+            sh.l[i] = lt;
+          }
+        }
+        named_bar_sync(1, kSoftmaxWarps * 32);
+      }
+      if (WIDE || t == 0) {
+        float w1 = 0.f;
+        if (!WIDE) {
+          // either chain may have had no key (max -inf, sum 0)
+          const float m1 = sh.m[i], mm = fmaxf(m_used, m1);
+          w0 = m_used == -INFINITY ? 0.f : ex2((m_used - mm) * sl2);
+          w1 = m1 == -INFINITY ? 0.f : ex2((m1 - mm) * sl2);
+          lt = lt * w0 + sh.l[i] * w1;
+          m_used = mm;
+        }
+        const float inv = 1.f / lt;
+        w0 *= inv;
+        w1 *= inv;
+        const bool direct = it.alone && a.P == 0;
+        const long long part_row = (long long)it.part * kPrefixRows + row;
+        const int d0 = (D / 2) * half;
+        float* f32 = (direct ? static_cast<float*>(a.o) + out_row * D : a.ws_o + part_row * D) + d0;
+        __nv_bfloat16* b16 = static_cast<__nv_bfloat16*>(a.o) + out_row * D + d0;
+        const bool bf16 = direct && a.o_bf16;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t r[32];
+          tmem_ld32(lane_addr + colO + c * 32, r);
+          tmem_ld_wait();
+          auto value = [&](int e) {
+            const float x = __uint_as_float(r[e]) * w0;
+            return WIDE ? x : x + other[(d0 + c * 32 + e) * BM + i] * w1;
+          };
+          if (valid && bf16) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              reinterpret_cast<uint4*>(b16 + c * 32)[v] =
+                  make_uint4(pack_bf16x2(value(8 * v), value(8 * v + 1)), pack_bf16x2(value(8 * v + 2), value(8 * v + 3)),
+                             pack_bf16x2(value(8 * v + 4), value(8 * v + 5)), pack_bf16x2(value(8 * v + 6), value(8 * v + 7)));
+          } else if (valid) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              reinterpret_cast<float4*>(f32 + c * 32)[v] = make_float4(value(4 * v), value(4 * v + 1), value(4 * v + 2), value(4 * v + 3));
+          }
+        }
+        if (valid && half == 0) (direct ? a.lse + out_row : a.ws_lse + part_row)[0] = m_used * a.sm_scale + logf(lt);
+      }
+    }
+  } else if (warp == kWarpTma) {
+    // ------------------------------------------------------------ TMA producer
+    int last_unit = -1;
+    bool ok = true;
+    Walk wk(sh.tile_off, it.tile_begin), wv(sh.tile_off, it.tile_begin);  // K runs one tile ahead of V
+    auto load = [&](bool is_v, const Walk& w, uint32_t dst, uint32_t full) {
+      const int row = (w.t - w.off[w.r]) * BN, pair = w.r * a.R + it.group;
+      if (!a.rm.table) {
+        const int y = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair)[pair].row_off + row;
+        const CUtensorMap* map = is_v ? &maps.v[w.r] : &maps.k[w.r];
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) tma_load_3d(dst + c * (BN * 128), map, c * 64, it.kv_head, y, full);
+      } else {
+        // two 64-row halves, each inside one page; a half behind the pair's rows lies past
+        // the pool and reads zeros
+        const CUtensorMap* map = is_v ? &maps.v[0] : &maps.k[0];
+        for (int hh = 0; hh < 2; ++hh) {
+          const int i0 = row + 64 * hh;
+          const int y = (int)(i0 < sh.rows[w.r] ? map_row(a.rm, pair, 0, i0) : a.rm.pool_rows);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(dst + c * (BN * 128) + hh * 64 * 128, map, c * 64, it.kv_head, y, full);
+        }
+      }
+    };
+    for (int k = 0; k <= nK && ok; ++k) {
+      // load u = 2j (K_j) or 2j + 1 (V_j) goes to slot u % kSlots; unit k = {V_(k-1), K_k}
+      const int u0 = k == 0 ? 0 : 2 * k - 1, u1 = k == nK ? 2 * k - 1 : 2 * k;
+      for (int u = u0; u <= u1 && ok; ++u) {
+        if (u < C::kSlots) continue;             // the slot's first load
+        const int r = (u - C::kSlots + 1) >> 1;  // the release of load u - kSlots
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_rel[r % C::kSlots]), (r / C::kSlots) & 1, p.wait_ns, abort))) {
+          if (lane == 0) report_timeout(p.status, 4, abort);
+          ok = false;
+        }
+      }
+      if (!ok) break;
+      const uint32_t full = smem_u32(&sh.bar_unit[k % kUnitBars]);
+      if (elect_one()) {
+        mbar_expect_tx(full, (u1 - u0 + 1) * C::kSlotBytes);
+        if (k > 0) load(true, wv, smem_u32(sKV + ((2 * k - 1) % C::kSlots) * C::kSlotBytes), full);
+        if (k < nK) load(false, wk, smem_u32(sKV + ((2 * k) % C::kSlots) * C::kSlotBytes), full);
+      }
+      __syncwarp();
+      if (k > 0 && k < nK) wv.next();
+      if (k + 1 < nK) wk.next();
+      last_unit = k;
+    }
+    // never leave with a copy in flight: the last unit of every barrier
+    for (int k = max(0, last_unit - kUnitBars + 1); k <= last_unit; ++k)
+      mbar_wait(smem_u32(&sh.bar_unit[k % kUnitBars]), (k / kUnitBars) & 1, 1000000000ull, &sh.zero_flag);
+    __syncwarp();
+  } else if (warp == kWarpRelay) {
+    // ------------------------------------------------------------ relay
+    bool ok = true;
+    Walk w(sh.tile_off, it.tile_begin);
+    for (int j = 0; j < nK && ok; ++j) {
+      const int nv = sh.rows[w.r] - (w.t - w.off[w.r]) * BN;
+      if (j + 1 < nK) w.next();
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait(smem_u32(&sh.bar_unit[(j + 1) % kUnitBars]), ((j + 1) / kUnitBars) & 1, p.wait_ns, abort));
+      if (ok && nv < BN) {
+        // rows of V behind the shard's last key: another group's, or a page's tail; they
+        // meet weights of 0 and must not be infinite or NaN
+        uint8_t* v = sKV + ((2 * j + 1) % C::kSlots) * C::kSlotBytes;
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          for (int x = nv * 8 + lane; x < BN * 8; x += 32)
+            reinterpret_cast<uint4*>(v + c * (BN * 128))[x] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_p[t]), (j - 1) & 1, p.wait_ns, abort));
+        if (ok && lane == 0) mbar_arrive(smem_u32(&sh.bar_p[t]));
+        __syncwarp();
+      }
+      if (!ok && lane == 0) report_timeout(p.status, 17, abort);
+    }
+  } else {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr unsigned kAll = 0xffffffffu;
+    const uint32_t idS = idesc_bf16_f32(BM, NS, 0, 0);
+    const uint32_t idPV = idesc_bf16_f32(BM, D, 0, 1);
+    auto fail = [&](unsigned site) {
+      if (lane == 0) report_timeout(p.status, site, abort);
+    };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(kAll, mbar_wait(smem_u32(bar), parity, p.wait_ns, abort));
+    };
+    const uint64_t dQ0 = smem_desc(smem_u32(sQ), 16, 1024);
+    const uint64_t dK0 = smem_desc(smem_u32(sKV), 16, 1024);
+    const uint64_t dV0 = smem_desc(smem_u32(sKV), BN * 128, 1024);
+    auto issue_s = [&](int t, int u) {
+      const uint64_t a0 = dQ0 + (uint64_t)((WIDE ? t * C::kQBytes : 0) >> 4);
+      // the chain's 64 keys are the tile's rows 64 t on: 8 KB into every 64-dim chunk
+      const uint64_t b0 = dK0 + (uint64_t)(((u % C::kSlots) * C::kSlotBytes + (WIDE ? 0 : t * 64 * 128)) >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + t * 256, a0 + off, b0 + off, idS, kk > 0);
+        }
+        mma_commit(smem_u32(&sh.bar_s[t]));
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int t, int u, bool acc) {
+      const uint64_t v0 = dV0 + (uint64_t)(((u % C::kSlots) * C::kSlotBytes + (WIDE ? 0 : t * 64 * 128)) >> 4);
+      const uint32_t pa = tmem + t * 256, d = tmem + t * 256 + 128;
+      if (elect_one()) {
+        // P of a half's NC keys sits over the first NC / 2 of its NC columns
+        constexpr int kHalf = NC / 16;
+#pragma unroll
+        for (int kk = 0; kk < NS / 16; ++kk)
+          mma_ts(d, pa + (kk / kHalf) * NC + (kk % kHalf) * 8, v0 + (uint64_t)((kk * 16 * 128) >> 4), idPV, (acc || kk > 0) ? 1u : 0u);
+        mma_commit(smem_u32(&sh.bar_o[t]));
+      }
+      __syncwarp();
+    };
+    bool ok = true;
+    if (p.stall_test && !wait_all(&sh.bar_never, 0)) {
+      fail(10);
+      ok = false;
+    }
+    for (int t = 0; t < 2 && ok; ++t)
+      if (!wait_all(&sh.bar_q[t], 0)) {
+        fail(11);
+        ok = false;
+      }
+    if (ok && !wait_all(&sh.bar_unit[0], 0)) {
+      fail(12);
+      ok = false;
+    }
+    if (ok) {
+      tc_fence_after();
+      issue_s(0, 0);
+      issue_s(1, 0);
+    }
+    for (int j = 0; j < nK && ok; ++j) {
+      const int uV = 2 * j + 1, uK = 2 * j + 2;
+      for (int t = 0; t < 2 && ok; ++t) {
+        // V_j and K_(j+1) are in place once the chain's P_j has completed (the relay's arrival)
+        if (!wait_all(&sh.bar_p[t], j & 1)) {
+          fail(14 + t);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_pv(t, uV, j > 0);
+        if (j + 1 < nK) issue_s(t, uK);
+      }
+    }
+    // never go on under a running product
+    if (elect_one()) mma_commit(smem_u32(&sh.bar_drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&sh.bar_drain), 0, 1000000000ull, &sh.zero_flag);
+  }
+}
+
+template <int D, int MAXC>
+__global__ void __launch_bounds__(kLaunchBoundThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ Maps<MAXC> maps, const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * C::kQBytes;
+  __shared__ __align__(8) Shared sh;
+  const PrefixArgs& a = p.a;
+  const int warp = threadIdx.x >> 5;
+  const int w0 = a.plan[a.off_worker + blockIdx.x], w1 = a.plan[a.off_worker + blockIdx.x + 1];
+  if (w0 == w1) return;
+  constexpr int kBars = (int)(offsetof(Shared, tmem_slot) / 8);
+  auto bars = [&](bool fresh) {
+    uint64_t* b = reinterpret_cast<uint64_t*>(&sh);
+    for (int i = 0; i < kBars; ++i) {
+      const uint32_t bar = smem_u32(b + i);
+      if (!fresh) mbar_inval(bar);
+      const bool q = b + i == &sh.bar_q[0] || b + i == &sh.bar_q[1], pp = b + i == &sh.bar_p[0] || b + i == &sh.bar_p[1];
+      mbar_init(bar, q ? 2 * BM : pp ? 2 * BM + 1 : 1);
+    }
+    mbar_init_fence();
+  };
+  if (warp == kWarpMma) tmem_alloc(smem_u32(&sh.tmem_slot), 512);
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    sh.zero_flag = 0;
+  }
+  for (int wi = w0; wi < w1; ++wi) {
+    const cp_prefix_item* it = reinterpret_cast<const cp_prefix_item*>(a.plan + a.off_item) + wi;
+    if (threadIdx.x == 0) {
+      sh.item = *it;
+      bars(wi == w0);
+    }
+    for (int r = threadIdx.x; r <= a.C; r += blockDim.x) {
+      sh.tile_off[r] = a.plan[a.off_tiles + it->group * (a.C + 1) + r];
+      if (r < a.C) sh.rows[r] = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair)[r * a.R + it->group].rows;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_slot;
+    if (sh.item.m_rows > BM) process<D, true, MAXC>(p, maps, sh, sQ, sKV, tmem);
+    else process<D, false, MAXC>(p, maps, sh, sQ, sKV, tmem);
+    fence_proxy_async_smem();  // the next item's copies come after this one's reads and writes
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (sh.abort_flag) break;
+  }
+  if (warp == kWarpMma) tmem_dealloc(sh.tmem_slot, 512);
+}
+
+// [rows, H, D] bf16 as 3-D (D, H, rows); box (64, 1, box_rows), 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, long long rows, int H, int D, int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)rows};
+  const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)H * D * 2};
+  const uint32_t box[3] = {64, 1, (uint32_t)box_rows};
+  return encode_tensor_map_bf16(m, base, 3, dims, strides, box, D == 128);
+}
+
+template <int D, int MAXC>
+cudaError_t launch_c(const Params& p, const long long* shard_rows, int workers, cudaStream_t s) {
+  const PrefixArgs& a = p.a;
+  Maps<MAXC> maps;
+  memset(&maps, 0, sizeof(maps));
+  if (a.rm.table) {
+    if (!make_map(&maps.k[0], a.k.p[0], a.rm.pool_rows, a.Hkv, D, 64) || !make_map(&maps.v[0], a.v.p[0], a.rm.pool_rows, a.Hkv, D, 64))
+      return cudaErrorInvalidValue;
+  } else {
+    for (int r = 0; r < a.C; ++r)
+      if (shard_rows[r] > 0 &&
+          (!make_map(&maps.k[r], a.k.p[r], shard_rows[r], a.Hkv, D, BN) || !make_map(&maps.v[r], a.v.p[r], shard_rows[r], a.Hkv, D, BN)))
+        return cudaErrorInvalidValue;
+  }
+  const cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D, MAXC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  prefix_tc_kernel<D, MAXC><<<workers, kThreads, Cfg<D>::kSmem, s>>>(maps, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool prefix_tc_supported(cp_dtype kv, int D) { return kv == CP_BF16 && (D == 64 || D == 128); }
+
+cudaError_t launch_prefix_tc(const PrefixArgs& a, const long long* shard_rows, int workers, bool stall_test, cudaStream_t s) {
+  Params p;
+  p.a = a;
+  p.scale_log2 = a.sm_scale * kLog2e;
+  p.status = device_status_ptr();
+  if (!p.status) return cudaErrorInvalidDevice;
+  p.wait_ns = stall_test ? 50000000ull : wait_limit_ns();
+  p.stall_test = stall_test ? 1 : 0;
+  // the maps travel as kernel arguments: 2 KB of them where eight shards are enough
+  const bool few = a.rm.table || a.C <= 8;
+  if (a.D == 128) return few ? launch_c<128, 8>(p, shard_rows, workers, s) : launch_c<128, CP_MAX_SHARDS>(p, shard_rows, workers, s);
+  return few ? launch_c<64, 8>(p, shard_rows, workers, s) : launch_c<64, CP_MAX_SHARDS>(p, shard_rows, workers, s);
+}
+
+}  // namespace cpattn
