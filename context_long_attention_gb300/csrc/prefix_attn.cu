@@ -93,15 +93,16 @@ __global__ void __launch_bounds__(kSimtWarps * 32) prefix_simt_kernel(const Pref
 
 // ------------------------------------------------------------------ merge
 
-// A warp an output row: the weights of its parts, two to a lane at a time, then
-// its dims over the lanes.  Two passes over the parts' LSE and one over their rows.
-constexpr int kMergeWarps = 8;
+// A warp an output row: the weights of its parts, one to a lane, then its dims over
+// the lanes, NV pieces of four to a lane.
+constexpr int kMergeWarps = 8, kBatch = 8;
+template <int NV>
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixArgs a) {
   constexpr int kPer = kPrefixRows / kMergeWarps;
   const int lane = threadIdx.x & 31, dm = (blockIdx.x % kPer) * kMergeWarps + (threadIdx.x >> 5);
-  // the plan is no output of an earlier kernel's, but it may be this stream's copy
-  wait_for_earlier_kernels();
+  // the plan comes by copies, never from a kernel: it is there before the kernel before this one ends
   const cp_prefix_block bl = reinterpret_cast<const cp_prefix_block*>(a.plan + a.off_block)[blockIdx.x / kPer];
+  wait_for_earlier_kernels();
   if (dm >= bl.m_rows) return;
   const int m = bl.m0 + dm, head = bl.kv_head * a.G + m % a.G;
   const long long at = (long long)(bl.row0 + m / a.G) * a.Hq + head, NH = (long long)a.N * a.Hq;
@@ -115,34 +116,45 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
   const float g0 = g == -INFINITY ? 0.f : g;
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  float4 acc[NV];
+#pragma unroll
+  for (int c = 0; c < NV; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f;
   const int vec = a.D / 4;
   for (int i0 = 0; i0 < parts; i0 += 32) {
     const float w = i0 + lane < parts ? expf(lse_at(i0 + lane) - g0) : 0.f;
     const int n = min(32, parts - i0);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      z += wk;
-      if (wk == 0.f) continue;  // an empty part's row is not read
-      const int i = i0 + k;
-      const float4* row = reinterpret_cast<const float4*>(
-          i < bl.n_parts ? a.ws_o + ((long long)(bl.first_part + i) * kPrefixRows + dm) * a.D : a.own_o + ((i - bl.n_parts) * NH + at) * a.D);
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+      // the rows of a batch of parts are loaded together
+      float wk[kBatch];
+      float4 x[kBatch][NV];
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (lane + 32 * c < vec) {
-          const float4 x = __ldcg(row + lane + 32 * c);
-          acc[c].x += wk * x.x;
-          acc[c].y += wk * x.y;
-          acc[c].z += wk * x.z;
-          acc[c].w += wk * x.w;
+      for (int k = 0; k < kBatch; ++k) {
+        wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        if (k0 + k >= n) wk[k] = 0.f;
+        const int i = i0 + k0 + k;
+        const float4* row = reinterpret_cast<const float4*>(
+            i < bl.n_parts ? a.ws_o + ((long long)(bl.first_part + i) * kPrefixRows + dm) * a.D : a.own_o + ((i - bl.n_parts) * NH + at) * a.D);
+#pragma unroll
+        for (int c = 0; c < NV; ++c)  // an empty part's row is not read
+          x[k][c] = wk[k] != 0.f && lane + 32 * c < vec ? __ldcg(row + lane + 32 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        z += wk[k];
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          acc[c].x += wk[k] * x[k][c].x;
+          acc[c].y += wk[k] * x[k][c].y;
+          acc[c].z += wk[k] * x[k][c].z;
+          acc[c].w += wk[k] * x[k][c].w;
         }
+      }
     }
   }
   const float inv = z > 0.f ? 1.f / z : 0.f;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < NV; ++c) {
     const int d = 4 * (lane + 32 * c);
     if (d >= a.D) continue;
     const float x = acc[c].x * inv, y = acc[c].y * inv, u = acc[c].z * inv, v = acc[c].w * inv;
@@ -189,7 +201,7 @@ cudaError_t launch_prefix_simt(const PrefixArgs& a, cp_dtype kv, int workers, cu
 
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int blocks, cudaStream_t s) {
   if (blocks == 0) return cudaSuccess;
-  return launch_early(prefix_merge_kernel, (unsigned)blocks * (kPrefixRows / kMergeWarps), kMergeWarps * 32, 0, s, 1, a);
+  return launch_early(a.D <= 128 ? prefix_merge_kernel<1> : prefix_merge_kernel<2>, (unsigned)blocks * (kPrefixRows / kMergeWarps), kMergeWarps * 32, 0, s, 1, a);
 }
 
 }  // namespace cpattn

@@ -121,8 +121,7 @@ struct Shared {
   volatile int abort_flag;
   volatile int zero_flag;  // never set: drains ignore the abort flag
   int32_t tile_off[CP_MAX_SHARDS + 2];
-  int32_t rows[CP_MAX_SHARDS];
-  float m[BM], l[BM];      // chain 1's running max and sum for the combination
+  int32_t rows[CP_MAX_SHARDS], row_off[CP_MAX_SHARDS];
   cp_prefix_item item;
 };
 
@@ -298,6 +297,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       float w0 = 1.f;
       // O of chain 1 [dim][row] in the K/V ring: every product of the item is complete, so it is free
       float* other = reinterpret_cast<float*>(sKV);
+      float *other_m = other + D * BM, *other_l = other_m + BM;  // its running max and sum
       if (!WIDE) {
         if (t == 1) {
 #pragma unroll
@@ -309,8 +309,8 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
             for (int e = 0; e < 32; ++e) other[((D / 2) * half + c * 32 + e) * BM + i] = __uint_as_float(r[e]);
           }
           if (half == 0) {
-            sh.m[i] = m_used;
-            sh.l[i] = lt;
+            other_m[i] = m_used;
+            other_l[i] = lt;
           }
         }
         named_bar_sync(1, kSoftmaxWarps * 32);
@@ -319,10 +319,10 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         float w1 = 0.f;
         if (!WIDE) {
           // either chain may have had no key (max -inf, sum 0)
-          const float m1 = sh.m[i], mm = fmaxf(m_used, m1);
+          const float m1 = other_m[i], mm = fmaxf(m_used, m1);
           w0 = m_used == -INFINITY ? 0.f : ex2((m_used - mm) * sl2);
           w1 = m1 == -INFINITY ? 0.f : ex2((m1 - mm) * sl2);
-          lt = lt * w0 + sh.l[i] * w1;
+          lt = lt * w0 + other_l[i] * w1;
           m_used = mm;
         }
         const float inv = 1.f / lt;
@@ -362,27 +362,34 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     // ------------------------------------------------------------ TMA producer
     int last_unit = -1;
     bool ok = true;
-    Walk wk(sh.tile_off, it.tile_begin), wv(sh.tile_off, it.tile_begin);  // K runs one tile ahead of V
-    auto load = [&](bool is_v, const Walk& w, uint32_t dst, uint32_t full) {
-      const int row = (w.t - w.off[w.r]) * BN, pair = w.r * a.R + it.group;
+    int v0 = 0, v1 = 0, vr = 0;  // V's: the K of the unit before
+    // The rows to load are known before the wait that frees their slots: a tile's
+    // coordinates come from shared memory or the page table while the one before it is
+    // on its way, and V's are K's of the step before.
+    Walk w(sh.tile_off, it.tile_begin);
+    int y0 = 0, y1 = 0, yr = 0;  // of tile w.t: its rows' coordinate (of both halves in a pool) and shard
+    auto locate = [&]() {
+      const int row = (w.t - w.off[w.r]) * BN;
+      yr = w.r;
       if (!a.rm.table) {
-        const int y = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair)[pair].row_off + row;
-        const CUtensorMap* map = is_v ? &maps.v[w.r] : &maps.k[w.r];
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) tma_load_3d(dst + c * (BN * 128), map, c * 64, it.kv_head, y, full);
+        y0 = sh.row_off[w.r] + row;
       } else {
         // two 64-row halves, each inside one page; a half behind the pair's rows lies past
         // the pool and reads zeros
-        const CUtensorMap* map = is_v ? &maps.v[0] : &maps.k[0];
-        for (int hh = 0; hh < 2; ++hh) {
-          const int i0 = row + 64 * hh;
-          const int y = (int)(i0 < sh.rows[w.r] ? map_row(a.rm, pair, 0, i0) : a.rm.pool_rows);
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(dst + c * (BN * 128) + hh * 64 * 128, map, c * 64, it.kv_head, y, full);
-        }
+        const int pair = w.r * a.R + it.group;
+        y0 = (int)map_row(a.rm, pair, 0, row);
+        y1 = row + 64 < sh.rows[w.r] ? (int)map_row(a.rm, pair, 0, row + 64) : (int)a.rm.pool_rows;
+        yr = 0;
       }
     };
+    auto load = [&](const CUtensorMap* map, int c0, int c1, uint32_t dst, uint32_t full) {
+#pragma unroll
+      for (int c = 0; c < C::kChunks; ++c) {
+        tma_load_3d(dst + c * (BN * 128), map, c * 64, it.kv_head, c0, full);
+        if (a.rm.table) tma_load_3d(dst + c * (BN * 128) + 64 * 128, map, c * 64, it.kv_head, c1, full);
+      }
+    };
+    locate();
     for (int k = 0; k <= nK && ok; ++k) {
       // load u = 2j (K_j) or 2j + 1 (V_j) goes to slot u % kSlots; unit k = {V_(k-1), K_k}
       const int u0 = k == 0 ? 0 : 2 * k - 1, u1 = k == nK ? 2 * k - 1 : 2 * k;
@@ -396,14 +403,21 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
       if (!ok) break;
       const uint32_t full = smem_u32(&sh.bar_unit[k % kUnitBars]);
+      const uint32_t v_slot = smem_u32(sKV + ((2 * k + C::kSlots - 1) % C::kSlots) * C::kSlotBytes);
+      const uint32_t k_slot = smem_u32(sKV + ((2 * k) % C::kSlots) * C::kSlotBytes);
       if (elect_one()) {
         mbar_expect_tx(full, (u1 - u0 + 1) * C::kSlotBytes);
-        if (k > 0) load(true, wv, smem_u32(sKV + ((2 * k - 1) % C::kSlots) * C::kSlotBytes), full);
-        if (k < nK) load(false, wk, smem_u32(sKV + ((2 * k) % C::kSlots) * C::kSlotBytes), full);
+        if (k > 0) load(&maps.v[vr], v0, v1, v_slot, full);
+        if (k < nK) load(&maps.k[yr], y0, y1, k_slot, full);
       }
       __syncwarp();
-      if (k > 0 && k < nK) wv.next();
-      if (k + 1 < nK) wk.next();
+      v0 = y0;
+      v1 = y1;
+      vr = yr;
+      if (k + 1 < nK) {
+        w.next();
+        locate();
+      }
       last_unit = k;
     }
     // never leave with a copy in flight: the last unit of every barrier
@@ -518,6 +532,9 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   }
 }
 
+// the static arrays and the dynamic ones together: at most 227 KB a block
+static_assert(Cfg<128>::kSmem + sizeof(Shared) <= 232448 && Cfg<64>::kSmem + sizeof(Shared) <= 232448, "shared memory");
+
 template <int D, int MAXC>
 __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     prefix_tc_kernel(const __grid_constant__ Maps<MAXC> maps, const __grid_constant__ Params p) {
@@ -555,7 +572,11 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     }
     for (int r = threadIdx.x; r <= a.C; r += blockDim.x) {
       sh.tile_off[r] = a.plan[a.off_tiles + it->group * (a.C + 1) + r];
-      if (r < a.C) sh.rows[r] = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair)[r * a.R + it->group].rows;
+      if (r < a.C) {
+        const cp_pair_desc* pd = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair) + r * a.R + it->group;
+        sh.rows[r] = pd->rows;
+        sh.row_off[r] = pd->row_off;
+      }
     }
     tc_fence_before();
     __syncthreads();
