@@ -1145,7 +1145,8 @@ def cp_rope(q, k, pos, freqs: RopeFreqs, layout: int = CP_ROPE_HALF, tail: bool 
 
 # ---------------------------------------------------------------- shared prefixes
 
-PREFIX_ITEM_FIELDS = ["group", "kv_head", "row0", "m0", "m_rows", "tile_begin", "tile_end", "part", "alone"]
+PREFIX_ITEM_FIELDS = ["group", "kv_head", "row0", "m0", "m_rows", "tile_begin", "tile_end", "part", "alone",
+                      "first_shard", "first_y", "first_row", "first_rows"]
 PREFIX_BLOCK_FIELDS = ["group", "kv_head", "row0", "m0", "m_rows", "first_part", "n_parts"]
 
 
@@ -1163,8 +1164,8 @@ class PrefixPlan(_Plan):
 
     @property
     def items(self):
-        """[n, 12]: PREFIX_ITEM_FIELDS and padding."""
-        return self.words(self.off_seg, 12 * self.n_seg).reshape(-1, 12)
+        """[n, 16]: PREFIX_ITEM_FIELDS and padding."""
+        return self.words(self.off_seg, 16 * self.n_seg).reshape(-1, 16)
 
     @property
     def blocks(self):

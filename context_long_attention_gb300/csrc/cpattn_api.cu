@@ -775,6 +775,14 @@ cp_status build_prefix_plan(int C, int R, const int32_t* prefix_len, const int32
         x.m_rows = b.m_rows;
         x.tile_begin = t;
         x.tile_end = (int32_t)upto;
+        const int32_t* off = &tile_off[(size_t)b.group * (C + 1)];
+        int r = 0;
+        while (off[r + 1] <= t) ++r;
+        const cp_pair_desc& pd = pair[r * R + b.group];
+        x.first_shard = r;
+        x.first_row = (t - off[r]) * kDecodeTileRows;
+        x.first_y = pd.row_off + x.first_row;
+        x.first_rows = pd.rows;
         item.push_back(x);
         item_block.push_back(i);
         block[i].n_parts++;
@@ -1880,7 +1888,11 @@ cp_status cp_decode_weights(const void* host_plan, const void* dev_plan, cp_deco
   a.G = Hq / Hkv;
   a.s_q = plan_s_q(h);
   a.sm_scale = sm_scale;
-  const cudaError_t e = launch_decode_weights_simt(a, kv_dtype, Dqk, h.n_tiles, (cudaStream_t)stream);
+  const char* stall = getenv("CPATTN_TEST_STALL");  // test hook of the bounded waits
+  const cudaError_t e =
+      decode_weights_tc_supported(kv_dtype, Hkv, a.G, a.s_q, Dqk)
+          ? launch_decode_weights_tc(a, kv_dtype, Dqk, h.n_tiles, stall && stall[0] == '1', (cudaStream_t)stream)
+          : launch_decode_weights_simt(a, kv_dtype, Dqk, h.n_tiles, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "decode weights kernel");
   return ok();
 }

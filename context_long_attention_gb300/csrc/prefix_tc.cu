@@ -29,7 +29,9 @@
 
 #include <cstring>
 
+#include "early_launch.cuh"
 #include "internal.h"
+#include "page_count.cuh"
 #include "tc_ptx.cuh"
 
 namespace cpattn {
@@ -62,6 +64,7 @@ struct Maps {
 
 struct Params {
   PrefixArgs a;
+  FastDiv by_g;  // rows of a block to query rows
   float scale_log2;
   unsigned* status;
   unsigned long long wait_ns;
@@ -116,7 +119,7 @@ struct Walk {
 };
 
 struct Shared {
-  uint64_t bar_unit[10], bar_rel[10], bar_q[2], bar_s[2], bar_p[2], bar_o[2], bar_never, bar_drain;
+  uint64_t bar_unit[10], bar_rel[10], bar_s[2], bar_p[2], bar_o[2], bar_never, bar_drain;
   uint32_t tmem_slot;
   volatile int abort_flag;
   volatile int zero_flag;  // never set: drains ignore the abort flag
@@ -148,10 +151,6 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t colS = t * 256 + NC * half, colO = t * 256 + 128 + (D / 2) * half;
     const int row = (WIDE ? t * BM : 0) + i;  // row of the block
-    auto query_row = [&]() -> long long {      // of the row's query and head in q and o (made twice: no register in the loop)
-      const int m = it.m0 + row, n = m / a.G;
-      return (long long)(it.row0 + n) * a.Hq + it.kv_head * a.G + m - n * a.G;
-    };
     const bool releaser = t == 1 && quarter == 0 && half == 0;  // frees K/V slots
     // value of the other half of this row, through the last of its S columns, which
     // P never covers and which S no longer needs once a tile's values are in registers
@@ -165,21 +164,6 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       tmem_ld_wait();
       return __uint_as_float(o);
     };
-    {  // this row's query to shared memory (128-byte-swizzled K-major), its pieces over the threads of the row
-      const bool valid = row < it.m_rows;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (valid ? query_row() * D : 0));
-      uint8_t* dst = sQ + (WIDE ? t * C::kQBytes : 0) + i * 128;
-      constexpr int kPer = WIDE ? D / 16 : D / 32;
-      const int first = (WIDE ? half : 2 * t + half) * kPer;
-#pragma unroll
-      for (int c = first; c < first + kPer; ++c) {
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (valid) val = __ldg(src + c);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (BM * 128) + (((c & 7) ^ (i & 7)) << 4)) = val;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&sh.bar_q[t]));
-    }
     const float sl2 = p.scale_log2;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true, first = true;  // first: no key of this chain so far
@@ -286,27 +270,29 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     }
     // ------------------------------------------------------------ epilogue
     const bool landed = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_o[t]), (nK - 1) & 1, p.wait_ns, abort));
-    const bool failed = WIDE ? bar_red_or(pbar, 64, !landed) : bar_red_or(1, kSoftmaxWarps * 32, !landed);
+    const bool failed = bar_red_or(1, kSoftmaxWarps * 32, !landed);
     if (failed) {
       if (ok && !landed) report_timeout(p.status, 3, abort);
     } else {
       tc_fence_after();
-      const bool valid = row < it.m_rows;
-      const long long out_row = valid ? query_row() : 0;
+
       float lt = l + exchange(l);
       float w0 = 1.f;
-      // O of chain 1 [dim][row] in the K/V ring: every product of the item is complete, so it is free
+      // Every product of the item is complete (both chains' last ones were waited for), so the
+      // K/V ring is free.  O of chain 1 [dim][row], its running max and sum; the block's results
       float* other = reinterpret_cast<float*>(sKV);
-      float *other_m = other + D * BM, *other_l = other_m + BM;  // its running max and sum
+      float *other_m = other + D * BM, *other_l = other_m + BM;
+      float4* out = reinterpret_cast<float4*>(sKV + (WIDE ? 0 : (D + 2) * BM * 4));
+      float* out_lse = reinterpret_cast<float*>(out + (WIDE ? 2 : 1) * BM * (D / 4));
       if (!WIDE) {
         if (t == 1) {
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t r[32];
-            tmem_ld32(lane_addr + colO + c * 32, r);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[16];
+            tmem_ld16(lane_addr + colO + c * 16, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) other[((D / 2) * half + c * 32 + e) * BM + i] = __uint_as_float(r[e]);
+            for (int e = 0; e < 16; ++e) other[((D / 2) * half + c * 16 + e) * BM + i] = __uint_as_float(r[e]);
           }
           if (half == 0) {
             other_m[i] = m_used;
@@ -328,39 +314,67 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         const float inv = 1.f / lt;
         w0 *= inv;
         w1 *= inv;
-        const bool direct = it.alone && a.P == 0;
-        const long long part_row = (long long)it.part * kPrefixRows + row;
-        const int d0 = (D / 2) * half;
-        float* f32 = (direct ? static_cast<float*>(a.o) + out_row * D : a.ws_o + part_row * D) + d0;
-        __nv_bfloat16* b16 = static_cast<__nv_bfloat16*>(a.o) + out_row * D + d0;
-        const bool bf16 = direct && a.o_bf16;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t r[32];
-          tmem_ld32(lane_addr + colO + c * 32, r);
+        // O and the LSE of this half of the row to shared memory, pieces of four dims
+        // rotated by the row (a column of pieces would share its banks).  This code runs
+        // once an item, out of the instruction cache: short loops.
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[16];
+          tmem_ld16(lane_addr + colO + c * 16, r);
           tmem_ld_wait();
-          auto value = [&](int e) {
-            const float x = __uint_as_float(r[e]) * w0;
-            return WIDE ? x : x + other[(d0 + c * 32 + e) * BM + i] * w1;
-          };
-          if (valid && bf16) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              reinterpret_cast<uint4*>(b16 + c * 32)[v] =
-                  make_uint4(pack_bf16x2(value(8 * v), value(8 * v + 1)), pack_bf16x2(value(8 * v + 2), value(8 * v + 3)),
-                             pack_bf16x2(value(8 * v + 4), value(8 * v + 5)), pack_bf16x2(value(8 * v + 6), value(8 * v + 7)));
-          } else if (valid) {
+          for (int v = 0; v < 4; ++v) {
+            float x[4];
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              reinterpret_cast<float4*>(f32 + c * 32)[v] = make_float4(value(4 * v), value(4 * v + 1), value(4 * v + 2), value(4 * v + 3));
+            for (int e = 0; e < 4; ++e) {
+              x[e] = __uint_as_float(r[4 * v + e]) * w0;
+              if (!WIDE) x[e] += other[((D / 2) * half + c * 16 + 4 * v + e) * BM + i] * w1;
+            }
+            const int piece = (D / 8) * half + c * 4 + v;
+            out[row * (D / 4) + (piece ^ (i & 7))] = make_float4(x[0], x[1], x[2], x[3]);
           }
         }
-        if (valid && half == 0) (direct ? a.lse + out_row : a.ws_lse + part_row)[0] = m_used * a.sm_scale + logf(lt);
+        if (half == 0) out_lse[row] = m_used * a.sm_scale + logf(lt);
+        // ... and from there whole rows at a time to global memory: the two warps of these
+        // 32 rows take every other one
+        named_bar_sync(pbar, 64);
+        constexpr int kLanes = D / 4, kRows = 32 / kLanes;  // lanes a row, rows a warp at a time
+        constexpr int kSteps = 16 / kRows, kBatch = 4;
+        const int piece = lane % kLanes, x0 = half * kRows + lane / kLanes;
+        const int base = row - i + quarter * 32, rows = min(32, it.m_rows - base);
+        const bool direct = it.alone && a.P == 0;
+#pragma unroll 1
+        for (int b = 0; b < kSteps; b += kBatch) {
+          float4 v[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int x = x0 + 2 * kRows * (b + k);
+            v[k] = out[(base + x) * (D / 4) + (piece ^ (x & 7))];
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int x = x0 + 2 * kRows * (b + k);
+            if (x >= rows) continue;
+            if (!direct) {
+              const long long at = (long long)it.part * kPrefixRows + base + x;
+              reinterpret_cast<float4*>(a.ws_o + at * D)[piece] = v[k];
+              if (piece == 0) a.ws_lse[at] = out_lse[base + x];
+            } else {
+              const int m = it.m0 + base + x, n = p.by_g(m);
+              const long long at = (long long)(it.row0 + n) * a.Hq + it.kv_head * a.G + m - n * a.G;
+              if (a.o_bf16)
+                reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at * D)[piece] = make_uint2(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w));
+              else
+                reinterpret_cast<float4*>(static_cast<float*>(a.o) + at * D)[piece] = v[k];
+              if (piece == 0) a.lse[at] = out_lse[base + x];
+            }
+          }
+        }
       }
     }
   } else if (warp == kWarpTma) {
     // ------------------------------------------------------------ TMA producer
-    int last_unit = -1;
+    int last_unit = 0;  // K_0: loaded before the block's barrier
     bool ok = true;
     int v0 = 0, v1 = 0, vr = 0;  // V's: the K of the unit before
     // The rows to load are known before the wait that frees their slots: a tile's
@@ -390,9 +404,16 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
     };
     locate();
-    for (int k = 0; k <= nK && ok; ++k) {
+    v0 = y0;
+    v1 = y1;
+    vr = yr;
+    if (nK > 1) {
+      w.next();
+      locate();
+    }
+    for (int k = 1; k <= nK && ok; ++k) {
       // load u = 2j (K_j) or 2j + 1 (V_j) goes to slot u % kSlots; unit k = {V_(k-1), K_k}
-      const int u0 = k == 0 ? 0 : 2 * k - 1, u1 = k == nK ? 2 * k - 1 : 2 * k;
+      const int u0 = 2 * k - 1, u1 = k == nK ? 2 * k - 1 : 2 * k;
       for (int u = u0; u <= u1 && ok; ++u) {
         if (u < C::kSlots) continue;             // the slot's first load
         const int r = (u - C::kSlots + 1) >> 1;  // the release of load u - kSlots
@@ -407,7 +428,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       const uint32_t k_slot = smem_u32(sKV + ((2 * k) % C::kSlots) * C::kSlotBytes);
       if (elect_one()) {
         mbar_expect_tx(full, (u1 - u0 + 1) * C::kSlotBytes);
-        if (k > 0) load(&maps.v[vr], v0, v1, v_slot, full);
+        load(&maps.v[vr], v0, v1, v_slot, full);
         if (k < nK) load(&maps.k[yr], y0, y1, k_slot, full);
       }
       __syncwarp();
@@ -497,11 +518,6 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       fail(10);
       ok = false;
     }
-    for (int t = 0; t < 2 && ok; ++t)
-      if (!wait_all(&sh.bar_q[t], 0)) {
-        fail(11);
-        ok = false;
-      }
     if (ok && !wait_all(&sh.bar_unit[0], 0)) {
       fail(12);
       ok = false;
@@ -546,36 +562,88 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   __shared__ __align__(8) Shared sh;
   const PrefixArgs& a = p.a;
   const int warp = threadIdx.x >> 5;
+  if (warp == kWarpTma)  // the descriptors' own latency, before the first load needs them
+    for (int r = threadIdx.x & 31; r < (a.rm.table ? 1 : a.C); r += 32) {
+      prefetch_tmap(&maps.k[r]);
+      prefetch_tmap(&maps.v[r]);
+    }
   const int w0 = a.plan[a.off_worker + blockIdx.x], w1 = a.plan[a.off_worker + blockIdx.x + 1];
   if (w0 == w1) return;
-  constexpr int kBars = (int)(offsetof(Shared, tmem_slot) / 8);
-  auto bars = [&](bool fresh) {
-    uint64_t* b = reinterpret_cast<uint64_t*>(&sh);
-    for (int i = 0; i < kBars; ++i) {
-      const uint32_t bar = smem_u32(b + i);
-      if (!fresh) mbar_inval(bar);
-      const bool q = b + i == &sh.bar_q[0] || b + i == &sh.bar_q[1], pp = b + i == &sh.bar_p[0] || b + i == &sh.bar_p[1];
-      mbar_init(bar, q ? 2 * BM : pp ? 2 * BM + 1 : 1);
-    }
-    mbar_init_fence();
-  };
+  constexpr int kBars = (int)(offsetof(Shared, tmem_slot) / 8);  // a lane each
+  static_assert(kBars <= 32, "barriers");
   if (warp == kWarpMma) tmem_alloc(smem_u32(&sh.tmem_slot), 512);
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
     sh.zero_flag = 0;
   }
+  // the plan comes by copies, never from a kernel: it may be read before the kernel
+  // before this one ends
+  cp_prefix_item it = reinterpret_cast<const cp_prefix_item*>(a.plan + a.off_item)[w0];
+  wait_for_earlier_kernels();
   for (int wi = w0; wi < w1; ++wi) {
-    const cp_prefix_item* it = reinterpret_cast<const cp_prefix_item*>(a.plan + a.off_item) + wi;
-    if (threadIdx.x == 0) {
-      sh.item = *it;
-      bars(wi == w0);
-    }
-    for (int r = threadIdx.x; r <= a.C; r += blockDim.x) {
-      sh.tile_off[r] = a.plan[a.off_tiles + it->group * (a.C + 1) + r];
-      if (r < a.C) {
-        const cp_pair_desc* pd = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair) + r * a.R + it->group;
-        sh.rows[r] = pd->rows;
-        sh.row_off[r] = pd->row_off;
+    // What an item's first product waits for comes in one step after the item itself:
+    // the first K tile, the block's queries and the group's tables.
+    if (wi > w0) it = reinterpret_cast<const cp_prefix_item*>(a.plan + a.off_item)[wi];
+    if (warp == kWarpTma) {
+      const int lane = threadIdx.x & 31;
+      if (lane < kBars) {
+        uint64_t* b = reinterpret_cast<uint64_t*>(&sh) + lane;
+        if (wi > w0) mbar_inval(smem_u32(b));
+        mbar_init(smem_u32(b), b == &sh.bar_p[0] || b == &sh.bar_p[1] ? 2 * BM + 1 : 1);
+        mbar_init_fence();
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        // K_0 (more of the ring here would hold up the block's barrier)
+        int y0 = it.first_y, y1 = 0;
+        if (a.rm.table) {
+          const int pair = it.first_shard * a.R + it.group;
+          y0 = (int)map_row(a.rm, pair, 0, it.first_row);
+          y1 = it.first_row + 64 < it.first_rows ? (int)map_row(a.rm, pair, 0, it.first_row + 64) : (int)a.rm.pool_rows;
+        }
+        const CUtensorMap* map = &maps.k[a.rm.table ? 0 : it.first_shard];
+        const uint32_t full = smem_u32(&sh.bar_unit[0]), dst = smem_u32(sKV);
+        mbar_expect_tx(full, C::kSlotBytes);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          tma_load_3d(dst + c * (BN * 128), map, c * 64, it.kv_head, y0, full);
+          if (a.rm.table) tma_load_3d(dst + c * (BN * 128) + 64 * 128, map, c * 64, it.kv_head, y1, full);
+        }
+        sh.item = it;
+      }
+    } else if (warp < kSoftmaxWarps) {
+      // queries to shared memory (128-byte-swizzled K-major): 16 bytes a thread, a row's
+      // pieces side by side, four loads before their stores
+      constexpr int kPieces = D / 8, kStep = kSoftmaxWarps * 32, kBatch = 4;
+      const int count = (it.m_rows > BM ? 2 * BM : BM) * kPieces;
+#pragma unroll 1
+      for (int e0 = threadIdx.x; e0 < count; e0 += kBatch * kStep) {
+        uint4 val[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int e = e0 + x * kStep, r = e / kPieces, m = it.m0 + r, n = p.by_g(m);
+          val[x] = make_uint4(0, 0, 0, 0);
+          if (r < it.m_rows)
+            val[x] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                           ((long long)(it.row0 + n) * a.Hq + it.kv_head * a.G + m - n * a.G) * D) + e % kPieces);
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int e = e0 + x * kStep, r = e / kPieces, c = e % kPieces;
+          if (e < count)
+            *reinterpret_cast<uint4*>(sQ + (r >> 7) * C::kQBytes + (c >> 3) * (BM * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = val[x];
+        }
+      }
+      fence_proxy_async_smem();
+    } else {
+      for (int r = threadIdx.x - kWarpMma * 32; r <= a.C; r += 64) {
+        sh.tile_off[r] = a.plan[a.off_tiles + it.group * (a.C + 1) + r];
+        if (r < a.C) {
+          const cp_pair_desc* pd = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair) + r * a.R + it.group;
+          sh.rows[r] = pd->rows;
+          sh.row_off[r] = pd->row_off;
+        }
       }
     }
     tc_fence_before();
@@ -617,8 +685,7 @@ cudaError_t launch_c(const Params& p, const long long* shard_rows, int workers, 
   }
   const cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D, MAXC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  prefix_tc_kernel<D, MAXC><<<workers, kThreads, Cfg<D>::kSmem, s>>>(maps, p);
-  return cudaGetLastError();
+  return launch_early(prefix_tc_kernel<D, MAXC>, (unsigned)workers, kThreads, Cfg<D>::kSmem, s, 1, maps, p);
 }
 
 }  // namespace
@@ -626,8 +693,7 @@ cudaError_t launch_c(const Params& p, const long long* shard_rows, int workers, 
 bool prefix_tc_supported(cp_dtype kv, int D) { return kv == CP_BF16 && (D == 64 || D == 128); }
 
 cudaError_t launch_prefix_tc(const PrefixArgs& a, const long long* shard_rows, int workers, bool stall_test, cudaStream_t s) {
-  Params p;
-  p.a = a;
+  Params p = {a, FastDiv(a.G), 0.f, nullptr, 0, 0};
   p.scale_log2 = a.sm_scale * kLog2e;
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInvalidDevice;

@@ -712,6 +712,10 @@ typedef struct {
   int32_t tile_begin, tile_end;
   int32_t part;        /* workspace slot */
   int32_t alone;       /* the block's only item: its result needs no merge */
+  int32_t first_shard; /* of tile_begin: its shard, ... */
+  int32_t first_y;     /* ... its first row, in the shard's buffer */
+  int32_t first_row;   /* ... or in the pair (a pool's rows go through the page table), */
+  int32_t first_rows;  /* ... and the pair's rows */
   int32_t reserved[3];
 } cp_prefix_item;
 /* Plan tables of kind 3: off_rank cp_pair_desc[C * R], off_req worker_off[n_tiles + 1],
