@@ -22,6 +22,7 @@
 
 #include <cstring>
 
+#include "early_launch.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
 
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  wait_for_earlier_kernels();
   const int w0 = a.plan[a.off_worker + blockIdx.x], w1 = a.plan[a.off_worker + blockIdx.x + 1];
 
   if (warp == kWarpTma) {
@@ -280,41 +282,71 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           sL[i] = l;
         }
-        // a warp a query row (kv head kh, column n)
-        for (int i = warp; i < a.Hkv * ncols; i += 4) {
-          const int kh = i / ncols, n = i % ncols;
-          const __nv_bfloat16* src = q + ((long long)(n / a.G) * a.Hq + kh * a.G + n % a.G) * p.D;
-          uint8_t* base = sQ + kh * p.chunks * NT * 128;
+        // a warp kBatch query rows (kv head, column) at a time: their loads overlap
+        constexpr int kBatch = 4, kPer = 5;  // E4M3: pieces of 4 dims a lane, up to 576
+        const int rows = a.Hkv * ncols;
+        for (int i0 = warp * kBatch; i0 < rows; i0 += 4 * kBatch) {
           if constexpr (!F8) {
-            for (int c = lane; c < p.D / 8; c += 32)
-              *reinterpret_cast<uint4*>(base + (c >> 3) * NT * 128 + n * 128 + (((c & 7) ^ (n & 7)) << 4)) =
-                  __ldg(reinterpret_cast<const uint4*>(src) + c);
-          } else {
-            float top = 0.f;
-            for (int e = 4 * lane; e < p.D; e += 128)
+            const int vec = p.D / 8;
+            uint4 x[kBatch][3];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(__bfloat162float(src[e + k])));
+            for (int k = 0; k < kBatch; ++k) {
+              const int i = min(i0 + k, rows - 1), kh = i / ncols, n = i - kh * ncols;
+              const uint4* src = reinterpret_cast<const uint4*>(q + ((long long)(n / a.G) * a.Hq + kh * a.G + n % a.G) * p.D);
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            // 2^(7 - x) brings a largest element of [2^x, 2^(x+1)) to [128, 256)
-            const int x = max(-100, (int)(__float_as_uint(top) >> 23) - 127);
-            const float f = __uint_as_float((uint32_t)(7 - x + 127) << 23);
-            if (lane == 0) sF[kh * NP + n] = __uint_as_float((uint32_t)(x - 7 + 127) << 23);
-            for (int e = 4 * lane; e < p.D; e += 128) {
-              uint32_t hi = 0, lo = 0;
+              for (int c = 0; c < 3; ++c)
+                if (lane + 32 * c < vec) x[k][c] = __ldcg(src + lane + 32 * c);
+            }
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float v0 = __bfloat162float(src[e + 2 * k]) * f, v1 = __bfloat162float(src[e + 2 * k + 1]) * f;
-                const uint32_t h = e4m3x2(v0, v1);
-                float h0, h1;
-                e4m3x2_value(h, h0, h1);
-                hi |= h << (16 * k);
-                lo |= e4m3x2((v0 - h0) * 16.f, (v1 - h1) * 16.f) << (16 * k);
+            for (int k = 0; k < kBatch; ++k) {
+              const int i = min(i0 + k, rows - 1), kh = i / ncols, n = i - kh * ncols;
+              uint8_t* base = sQ + kh * p.chunks * NT * 128 + n * 128;
+#pragma unroll
+              for (int c = 0; c < 3; ++c) {
+                const int e = lane + 32 * c;
+                if (e < vec) *reinterpret_cast<uint4*>(base + (e >> 3) * NT * 128 + (((e & 7) ^ (n & 7)) << 4)) = x[k][c];
               }
-              uint8_t* row = base + (e >> 7) * NT * 128 + ((e & 15));
-              const int piece = (e & 127) >> 4;
-              *reinterpret_cast<uint32_t*>(row + n * 128 + ((piece ^ (n & 7)) << 4)) = hi;
-              *reinterpret_cast<uint32_t*>(row + (NP + n) * 128 + ((piece ^ (n & 7)) << 4)) = lo;
+            }
+          } else {
+            uint2 x[kBatch][kPer];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int i = min(i0 + k, rows - 1), kh = i / ncols, n = i - kh * ncols;
+              const uint2* src = reinterpret_cast<const uint2*>(q + ((long long)(n / a.G) * a.Hq + kh * a.G + n % a.G) * p.D);
+#pragma unroll
+              for (int c = 0; c < kPer; ++c) x[k][c] = 4 * lane + 128 * c < p.D ? __ldcg(src + lane + 32 * c) : make_uint2(0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int i = min(i0 + k, rows - 1), kh = i / ncols, n = i - kh * ncols;
+              // magnitudes are ordered like their bits, two bf16 at a time
+              uint32_t m = 0;
+#pragma unroll
+              for (int c = 0; c < kPer; ++c) m = __vmaxu2(m, __vmaxu2(x[k][c].x & 0x7fff7fffu, x[k][c].y & 0x7fff7fffu));
+              const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffff0000u, m << 16));
+              // 2^(7 - e) brings a largest element of [2^e, 2^(e+1)) to [128, 256)
+              const int e = max(-100, (int)(top >> 23) - 127);
+              const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+              if (lane == 0) sF[kh * NP + n] = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+              uint8_t* base = sQ + kh * p.chunks * NT * 128 + 4 * (lane & 3);
+#pragma unroll
+              for (int c = 0; c < kPer; ++c) {
+                if (c >= p.chunks) break;
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                  const uint32_t b = w ? x[k][c].y : x[k][c].x;
+                  const float v0 = __uint_as_float(b << 16) * f, v1 = __uint_as_float(b & 0xffff0000u) * f;
+                  const uint32_t h = e4m3x2(v0, v1);
+                  float h0, h1;
+                  e4m3x2_value(h, h0, h1);
+                  hi |= h << (16 * w);
+                  lo |= e4m3x2((v0 - h0) * 16.f, (v1 - h1) * 16.f) << (16 * w);
+                }
+                uint8_t* row = base + c * NT * 128 + (((lane >> 2) ^ (n & 7)) << 4);
+                *reinterpret_cast<uint32_t*>(row + n * 128) = hi;
+                *reinterpret_cast<uint32_t*>(row + (NP + n) * 128) = lo;
+              }
             }
           }
         }
@@ -323,12 +355,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t == 0) mbar_arrive(smem_u32(&bar_q));
       }
       const int lim = it.pd.ctx_len - a.s_q;
+      // A tile's pool rows, weights and scales are loaded one tile ahead, their pages two:
+      // the chain of the three must not stand between the products and the sums.
+      auto page_of = [&](int j) {
+        const int i = min(it.row_begin + j * kRows + t, it.pd.rows - 1);
+        return j < it.ntiles ? __ldcg(a.rm.table + (long long)it.pair * a.rm.max_pages + i / a.rm.page_size) : 0;
+      };
+      int page = page_of(0), next_page = page_of(1);
+      long long row = 0;
+      float before = 0.f, scale = 0.f;
+      auto fetch = [&](int j, int pg) {
+        const int i = j * kRows + t;
+        if (i >= it.nrows) return;
+        row = (long long)pg * a.rm.page_size + (it.row_begin + i) % a.rm.page_size;
+        before = a.weights[row];
+        if (F8) scale = __ldcg(a.scale + row);
+      };
+      fetch(0, page);
       for (int j = 0; j < it.ntiles; ++j) {
         const int i = j * kRows + t;
         const bool valid = i < it.nrows;
-        const long long row = valid ? map_row(a.rm, it.pair, 0, it.row_begin + i) : 0;
-        const float before = valid ? a.weights[row] : 0.f;
-        const float c = F8 ? (valid ? p.scale_log2 * a.scale[row] : 0.f) : p.scale_log2;
+        const long long row_j = row;
+        const float before_j = before, c = F8 ? p.scale_log2 * scale : p.scale_log2;
+        fetch(j + 1, next_page);
+        next_page = page_of(j + 2);
         // several query rows: row qi reads tokens up to L - s_q + qi, so this cache row
         // weighs nothing for the columns n = qi G + i of qi < tok - lim
         const int first = max(0, it.pd.tok0 + (it.row_begin + i) * it.pd.tok_step - lim) * a.G;
@@ -369,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           w += (part[0] + part[1]) + (part[2] + part[3]);
         }
-        if (valid && ok) a.weights[row] = before + w;
+        if (valid && ok) a.weights[row_j] = before_j + w;
       }
     }
   }
@@ -390,8 +440,7 @@ cudaError_t launch_np(const CUtensorMap& map, Params p, int workers, cudaStream_
   // one limit for all calls: another thread's call may set it at the same time
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
-  kern<<<workers, kThreads, p.stages * kChunkBytes + q_bytes + cols + 1024, s>>>(map, p);
-  return cudaGetLastError();
+  return launch_early(kern, (unsigned)workers, kThreads, (size_t)p.stages * kChunkBytes + q_bytes + cols + 1024, s, 1, map, p);
 }
 
 }  // namespace
