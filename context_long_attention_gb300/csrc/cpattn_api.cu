@@ -1821,7 +1821,7 @@ cp_status cp_prefill_weights_workspace_size(const void* host_plan, cp_dtype dtyp
   const cp_status st = read_header(host_plan, 0, &h);
   if (st != CP_OK) return st;
   if (!bytes || Hq < 1 || D < 1 || window < 0) return fail(CP_ERR_INVALID_ARG, "bad arguments");
-  *bytes = 0;
+  *bytes = dtype == CP_BF16 && h.KV > 0 ? prefill_weights_tc_bytes((const int32_t*)host_plan, h, Hq, window) : 0;
   return ok();
 }
 
@@ -1848,7 +1848,10 @@ cp_status cp_prefill_weights(const void* host_plan, const void* dev_plan, cp_dty
     return fail(CP_ERR_INVALID_ARG, "a device pointer is not 16-byte aligned");
   const PrefillWeightsArgs a = {{(const int32_t*)dev_plan, h.off_req, h.off_seg, h.C, h.R, h.T, h.KV, h.kind == 0}, q, k,
                                 lse, out, Hq, Hkv, Hq / Hkv, window, sm_scale};
-  const cudaError_t e = launch_prefill_weights_simt(a, dtype == CP_BF16, D, (cudaStream_t)stream);
+  const char* stall = getenv("CPATTN_TEST_STALL");  // test hook of the bounded waits
+  const cudaError_t e = dtype == CP_BF16 ? launch_prefill_weights_tc(a, (const int32_t*)host_plan, h, D, ws,
+                                                                     stall && stall[0] == '1', (cudaStream_t)stream)
+                                         : launch_prefill_weights_simt(a, D, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefill weights kernel");
   return ok();
 }

@@ -295,7 +295,7 @@ struct DecodeWeightsArgs {
   int Hq, Hkv, G, s_q;
   float sm_scale;
 };
-cudaError_t launch_prefill_weights_simt(const PrefillWeightsArgs& a, bool bf16, int D, cudaStream_t s);
+cudaError_t launch_prefill_weights_simt(const PrefillWeightsArgs& a, int D, cudaStream_t s);
 cudaError_t launch_decode_weights_simt(const DecodeWeightsArgs& a, cp_dtype kv, int D, int workers, cudaStream_t s);
 bool decode_weights_tc_supported(cp_dtype kv, int Hkv, int G, int s_q, int D);
 cudaError_t launch_decode_weights_tc(const DecodeWeightsArgs& a, cp_dtype kv, int D, int workers, bool stall_test, cudaStream_t s);

@@ -140,9 +140,7 @@ cudaError_t prefill_t(const PrefillWeightsArgs& a, int D, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_prefill_weights_simt(const PrefillWeightsArgs& a, bool bf16, int D, cudaStream_t s) {
-  return bf16 ? prefill_t<__nv_bfloat16>(a, D, s) : prefill_t<float>(a, D, s);
-}
+cudaError_t launch_prefill_weights_simt(const PrefillWeightsArgs& a, int D, cudaStream_t s) { return prefill_t<float>(a, D, s); }
 
 cudaError_t launch_decode_weights_simt(const DecodeWeightsArgs& a, cp_dtype kv, int D, int workers, cudaStream_t s) {
   switch (kv) {

@@ -22,6 +22,11 @@ struct PrefillWeightsArgs {
   float sm_scale;
 };
 
+// On the tensor cores (prefill_weights_tc.cu): bf16, head dim 64 or 128.
+size_t prefill_weights_tc_bytes(const int32_t* host_plan, const cp_plan_header& h, int Hq, int window);
+cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t* host_plan, const cp_plan_header& h, int D,
+                                      void* ws, bool stall_test, cudaStream_t s);
+
 #ifdef __CUDACC__
 // Row of query i (of rq.new_len) of request j.  Segments go by rank, then
 // request; a zigzag rank has two blocks of every request (early, late).

@@ -1,0 +1,596 @@
+// The attention weights of a prompt batch on the tcgen05 tensor cores (bf16, head
+// dim 64 or 128).
+//
+// One pass: with the LSE at hand a weight is exp(score - LSE) at once, so there is
+// no second product and no running maximum.  Products are transposed: 256 keys of
+// a request (two M tiles of 128) against 128 queries of one head,
+//   S^T_t [128 keys x 128 queries] = K_t . Q^T,   t = 0, 1,
+// so a key's weight is a sum along its own TMEM lane and stays in a thread over all
+// queries and heads.  The work is the walk over (request, key block, head, query tile);
+// tiles before the block's first key are left out; workers (one CTA an SM) take equal
+// parts of it.  A block's sums end in a row of their own, or in one of two part
+// rows of each worker that shares the block with others, and a last kernel adds the parts in
+// the order of the workers: no atomics, the same order every time.
+//   warps 0-15  sums: warp w takes keys [32 (w % 4), +32) of M tile (w / 4) % 2 and
+//               the half w / 8 of the query columns
+//   warp 16     TMA producer (K blocks, Q tiles, the LSE of a tile)
+//   warp 17     MMA issuer and TMEM owner
+// TMEM (512 columns): S^T of tile t in columns [256 t, +256), two buffers of 128.
+// What bounds it: the products need 1,024 clk of the tensor cores a step, its 32,768
+// exponentials as much of the special function units.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "early_launch.cuh"
+#include "internal.h"
+#include "plan_rows.cuh"
+#include "tc_ptx.cuh"
+
+namespace cpattn {
+namespace {
+using namespace tc;
+
+constexpr int kBlock = 256;  // keys of a block
+constexpr int BQ = 128;      // queries of a tile
+constexpr int kSumWarps = 16, kThreads = 32 * (kSumWarps + 2);
+constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1;
+constexpr int kLseSlots = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTileBytes = 128 * D * 2;     // 128 keys or queries
+  static constexpr int kQSlots = D == 128 ? 3 : 6;
+  static constexpr int kSmem = 4 * kTileBytes + kQSlots * kTileBytes + kLseSlots * BQ * 4;
+};
+
+// One request's share of the walk.
+struct Req {
+  int n, pre, q_base, kv_base;
+  int w, off, nq;   // observed queries, the position of the first one, their tiles
+  int c, m0, nb;    // blocks 0 .. m0 - 1 are read by every tile, block k >= m0 from tile 2 k - c on
+};
+__host__ __device__ inline Req make_req(const cp_req_desc& d, int window) {
+  Req r;
+  r.n = d.new_len;
+  r.pre = d.prefix_len;
+  r.q_base = d.q_base;
+  r.kv_base = d.kv_base;
+  r.w = window > 0 && window < d.new_len ? window : d.new_len;
+  r.off = d.prefix_len + d.new_len - r.w;
+  r.nq = (int)(((long long)r.w + BQ - 1) / BQ);
+  r.c = (int)(((long long)r.off + BQ - 1) / BQ);
+  r.m0 = r.c / 2 + 1;
+  r.nb = r.nq ? (int)(((long long)d.prefix_len + d.new_len + kBlock - 1) / kBlock) : 0;
+  return r;
+}
+// The first tile that reads block k (its last query is at or behind the block's first key).
+__host__ __device__ inline int first_tile(const Req& r, int k) { return k < r.m0 ? 0 : 2 * k - r.c; }
+// Tiles of blocks 0 .. k - 1 (of one head).
+__host__ __device__ inline long long tiles_before(const Req& r, long long k) {
+  long long f = k * r.nq;
+  if (k > r.m0) f -= k * (k - 1) - (long long)r.m0 * (r.m0 - 1) - (long long)r.c * (k - r.m0);
+  return f;
+}
+
+struct Params {
+  PrefillWeightsArgs a;
+  int workers;
+  long long total;       // steps of the walk
+  int n_tiles;           // query tiles of all requests
+  long long* base;       // [R + 1] first step of every request
+  int32_t* tile_base;    // [R + 1] first query tile
+  int32_t* block_base;   // [R + 1] first key block (a request without queries has its blocks, too)
+  float* lse;            // [Hq][n_tiles][BQ] minus the LSE in log2 units, -inf where there is no query
+  float* full;           // [2][KV] sums of blocks of one worker, by half of the columns
+  float* part;           // [workers][2][2][kBlock]
+  float scale_log2;
+  unsigned* status;
+  unsigned long long wait_ns;
+  int stall_test;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ void report_timeout(unsigned* status, unsigned site, volatile int* abort) {
+  *abort = 1;
+  if (atomicCAS(status, 0u, 1u) == 0u) {
+    status[1] = kKernPrefillWeights;
+    status[2] = site;
+    status[3] = blockIdx.x;
+    __threadfence();
+  }
+}
+
+__device__ __forceinline__ cp_req_desc req_desc(const Params& p, int j) {
+  return reinterpret_cast<const cp_req_desc*>(p.a.rows.plan + p.a.rows.off_req)[j];
+}
+// The last j of [0, R) with first(j) <= x.
+template <typename F>
+__device__ __forceinline__ int find(int R, F first, long long x) {
+  int lo = 0, hi = R - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first(mid) <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ long long worker_start(const Params& p, long long w) { return p.total / p.workers * w + p.total % p.workers * w / p.workers; }
+
+// ------------------------------------------------------------------ tables and LSE tiles
+
+// Running sums over the requests: one block, a thread for consecutive requests.
+__global__ void __launch_bounds__(256) weights_table_kernel(const Params p) {
+  __shared__ long long s_step[256];
+  __shared__ int s_tile[256], s_block[256];
+  const int R = p.a.rows.R, per = (R + 255) / 256;
+  const int j0 = min(R, (int)threadIdx.x * per), j1 = min(R, j0 + per);
+  long long step = 0;
+  int tile = 0, block = 0;
+  auto each = [&](int j) {
+    const Req r = make_req(req_desc(p, j), p.a.window);
+    step += p.a.Hq * tiles_before(r, r.nb);
+    tile += r.nq;
+    block += (int)(((long long)r.pre + r.n + kBlock - 1) / kBlock);
+  };
+  for (int j = j0; j < j1; ++j) each(j);
+  s_step[threadIdx.x] = step;
+  s_tile[threadIdx.x] = tile;
+  s_block[threadIdx.x] = block;
+  wait_for_earlier_kernels();
+  __syncthreads();
+  step = tile = block = 0;
+  for (int t = 0; t < (int)threadIdx.x; ++t) {
+    step += s_step[t];
+    tile += s_tile[t];
+    block += s_block[t];
+  }
+  for (int j = j0; j < j1; ++j) {
+    p.base[j] = step;
+    p.tile_base[j] = tile;
+    p.block_base[j] = block;
+    each(j);
+    if (j + 1 == R) {
+      p.base[R] = step;
+      p.tile_base[R] = tile;
+      p.block_base[R] = block;
+    }
+  }
+}
+
+// A tile's LSE of every head: rank-major rows in, [head][tile][query] out.
+__global__ void __launch_bounds__(256) weights_lse_kernel(const Params p) {
+  wait_for_earlier_kernels();
+  const int tile = blockIdx.x, R = p.a.rows.R, Hq = p.a.Hq;
+  const int j = find(R, [&](int x) -> long long { return p.tile_base[x]; }, tile);
+  const cp_req_desc d = req_desc(p, j);
+  const Req r = make_req(d, p.a.window);
+  const int i0 = r.n - r.w + (tile - p.tile_base[j]) * BQ;  // the tile's first query
+  __shared__ int s_row[BQ];
+  for (int x = threadIdx.x; x < BQ; x += 256) s_row[x] = i0 + x < r.n ? plan_row(p.a.rows, j, d, i0 + x) : -1;
+  __syncthreads();
+  for (int h0 = 0; h0 < Hq; h0 += 8) {
+    // eight heads of a row side by side, so that whole sectors are read
+    for (int e = threadIdx.x; e < BQ * 8; e += 256) {
+      const int x = e >> 3, h = h0 + (e & 7);
+      if (h >= Hq) continue;
+      float v = -INFINITY;
+      if (s_row[x] >= 0) {
+        const float l = __ldcg(p.a.lse + (long long)s_row[x] * Hq + h);
+        if (l != -INFINITY) v = -l * kLog2e;  // a query without keys weighs nothing
+      }
+      p.lse[((long long)h * p.n_tiles + tile) * BQ + x] = v;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sums
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sK = smem;                                 // [2 buffers][2 tiles]
+  uint8_t* sQ = smem + 4 * C::kTileBytes;             // ring of query tiles
+  float* sL = reinterpret_cast<float*>(sQ + C::kQSlots * C::kTileBytes);  // ring of their LSE
+  __shared__ __align__(8) uint64_t bar_k[2], bar_kfree[2], bar_q[C::kQSlots], bar_qfree[C::kQSlots], bar_l[kLseSlots],
+      bar_lfree[kLseSlots], bar_s[4], bar_sfree[4], bar_drain, bar_never;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ volatile int zero_flag;
+  const PrefillWeightsArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bar_k[i]), 1);
+      mbar_init(smem_u32(&bar_kfree[i]), 1);
+    }
+    for (int i = 0; i < C::kQSlots; ++i) {
+      mbar_init(smem_u32(&bar_q[i]), 1);
+      mbar_init(smem_u32(&bar_qfree[i]), 1);
+    }
+    for (int i = 0; i < kLseSlots; ++i) {
+      mbar_init(smem_u32(&bar_l[i]), 1);
+      mbar_init(smem_u32(&bar_lfree[i]), kSumWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&bar_s[i]), 1);
+      mbar_init(smem_u32(&bar_sfree[i]), kSumWarps / 2);
+    }
+    mbar_init(smem_u32(&bar_drain), 1);
+    mbar_init(smem_u32(&bar_never), 1);
+    abort_flag = 0;
+    zero_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kWarpMma) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (warp == kWarpTma && lane == 0) {
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&qmap);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  wait_for_earlier_kernels();
+  const long long begin = worker_start(p, blockIdx.x), end = worker_start(p, blockIdx.x + 1);
+
+  // The blocks of this worker's part of the walk, in order: each(request index,
+  // request, block, first step of the worker in the block, one past its last, block's steps).
+  auto walk = [&](auto&& each) {
+    if (begin >= end) return;
+    int j = find(a.rows.R, [&](int x) { return p.base[x]; }, begin);
+    Req r = make_req(req_desc(p, j), a.window);
+    long long base = p.base[j], pos = begin;
+    // the block of step `begin`: binary search of the sums
+    int kb;
+    {
+      const long long t = (begin - base) / a.Hq;
+      int lo = 0, hi = r.nb - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tiles_before(r, mid) <= t) lo = mid; else hi = mid - 1;
+      }
+      kb = lo;
+    }
+    while (pos < end) {
+      while (kb >= r.nb) {  // the next request with steps
+        ++j;
+        r = make_req(req_desc(p, j), a.window);
+        base = p.base[j];
+        kb = 0;
+      }
+      const long long s0 = base + a.Hq * tiles_before(r, kb);
+      const int steps = a.Hq * (r.nq - first_tile(r, kb));
+      const int x0 = (int)(pos - s0), x1 = (int)min((long long)steps, end - s0);
+      if (!each(j, r, kb, x0, x1, steps)) return;
+      pos = s0 + x1;
+      ++kb;
+    }
+  };
+
+  if (warp == kWarpTma) {
+    // ------------------------------------------------------------ TMA
+    bool ok = true;
+    int nk = 0, nq = 0;  // K blocks and query tiles loaded so far
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+      if (__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag))) return true;
+      if (lane == 0) report_timeout(p.status, site, &abort_flag);
+      return ok = false;
+    };
+    walk([&](int j, const Req& r, int kb, int x0, int x1, int) {
+      const int first = first_tile(r, kb), cnt = r.nq - first;
+      int h = x0 / cnt, q = x0 - h * cnt, g_in = -1;
+      const int tile0 = p.tile_base[j];
+      for (int x = x0; x < x1; ++x) {
+        const int g = h / a.G;
+        if (g != g_in) {
+          g_in = g;
+          const int b = nk & 1;
+          if (nk >= 2 && !wait_all(&bar_kfree[b], (nk / 2 - 1) & 1, 1)) return false;
+          if (elect_one()) {
+            const uint32_t full = smem_u32(&bar_k[b]), dst = smem_u32(sK + b * 2 * C::kTileBytes);
+            mbar_expect_tx(full, 2 * C::kTileBytes);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(dst + t * C::kTileBytes + c * (128 * 128), &kmap, c * 64, g, r.kv_base + kb * kBlock + t * 128, full);
+          }
+          __syncwarp();
+          ++nk;
+        }
+        const int s = nq % C::kQSlots, l = nq % kLseSlots;
+        if (nq >= C::kQSlots && !wait_all(&bar_qfree[s], (nq / C::kQSlots - 1) & 1, 2)) return false;
+        if (nq >= kLseSlots && !wait_all(&bar_lfree[l], (nq / kLseSlots - 1) & 1, 3)) return false;
+        if (elect_one()) {
+          const uint32_t full = smem_u32(&bar_q[s]), dst = smem_u32(sQ + s * C::kTileBytes);
+          mbar_expect_tx(full, C::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(dst + c * (128 * 128), &qmap, c * 64, h, r.q_base + r.n - r.w + (first + q) * BQ, full);
+          const uint32_t lf = smem_u32(&bar_l[l]);
+          mbar_expect_tx(lf, BQ * 4);
+          bulk_load(smem_u32(sL + l * BQ), p.lse + ((long long)h * p.n_tiles + tile0 + first + q) * BQ, BQ * 4, lf);
+        }
+        __syncwarp();
+        ++nq;
+        if (++q == cnt) {
+          q = 0;
+          ++h;
+        }
+      }
+      return true;
+    });
+    if (!ok) {
+      // never leave with a copy in flight: the last fill of every place
+      auto drain = [&](uint64_t* bar, int n, int slots) {
+        for (int x = 0; x < slots; ++x) {
+          const int fills = n / slots + (x < n % slots);
+          if (fills > 0) mbar_wait(smem_u32(bar + x), (fills - 1) & 1, 1000000000ull, &zero_flag);
+        }
+      };
+      drain(bar_k, nk, 2);
+      drain(bar_q, nq, C::kQSlots);
+      drain(bar_l, nq, kLseSlots);
+      __syncwarp();
+    }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMA issue
+    const uint32_t id = idesc_bf16_f32(128, BQ, 0, 0);
+    const uint64_t dK = smem_desc(smem_u32(sK), 16, 1024), dQ = smem_desc(smem_u32(sQ), 16, 1024);
+    int nk = 0, nq = 0;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+      if (__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, &abort_flag))) return true;
+      if (lane == 0) report_timeout(p.status, site, &abort_flag);
+      return false;
+    };
+    if (!p.stall_test || wait_all(&bar_never, 0, 10))
+      walk([&](int, const Req& r, int kb, int x0, int x1, int) {
+        const int cnt = r.nq - first_tile(r, kb);
+        int h = x0 / cnt, q = x0 - h * cnt, g_in = -1;
+        for (int x = x0; x < x1; ++x, ++nq) {
+          if (h / a.G != g_in) {
+            g_in = h / a.G;
+            if (!wait_all(&bar_k[nk & 1], (nk >> 1) & 1, 4)) return false;
+            ++nk;
+          }
+          if (++q == cnt) {
+            q = 0;
+            ++h;
+          }
+          const bool last = x + 1 == x1 || h / a.G != g_in;  // of this K block
+          const int s = nq % C::kQSlots, buf = nq & 1;
+          if (!wait_all(&bar_q[s], (nq / C::kQSlots) & 1, 5)) return false;
+          for (int t = 0; t < 2; ++t) {
+            if (nq >= 2 && !wait_all(&bar_sfree[2 * t + buf], (nq / 2 - 1) & 1, 6)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t k = dK + ((uint32_t)((((nk - 1) & 1) * 2 + t) * C::kTileBytes) >> 4);
+              const uint64_t b = dQ + ((uint32_t)(s * C::kTileBytes) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + t * 256 + buf * 128, k + off, b + off, id, kk > 0);
+              }
+              mma_commit(smem_u32(&bar_s[2 * t + buf]));
+              if (t == 1) {
+                mma_commit(smem_u32(&bar_qfree[s]));
+                if (last) mma_commit(smem_u32(&bar_kfree[(nk - 1) & 1]));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        return true;
+      });
+    // never free TMEM under a running product
+    if (elect_one()) mma_commit(smem_u32(&bar_drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
+  } else {
+    // ------------------------------------------------------------ sums
+    const int quarter = warp & 3, t = (warp >> 2) & 1, half = warp >> 3;
+    const int i = t * 128 + quarter * 32 + lane;  // key of the block
+    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + t * 256 + 64 * half;
+    const float sl2 = p.scale_log2;
+    int nq = 0;
+    walk([&](int, const Req& r, int kb, int x0, int x1, int steps) {
+      const int first = first_tile(r, kb), cnt = r.nq - first;
+      int q = x0 % cnt;
+      // column c of tile q stands at position off + 128 q + c: it reads this key from c = lo - 128 q on
+      const int lo = kb * kBlock + i - r.off - 64 * half, warp_lo = lo - lane + 31;
+      float sum = 0.f;
+      for (int x = x0; x < x1; ++x, ++nq) {
+        const int buf = nq & 1, l = nq % kLseSlots;
+        bool got = mbar_wait(smem_u32(&bar_l[l]), (nq / kLseSlots) & 1, p.wait_ns, &abort_flag);
+        got = __all_sync(0xffffffffu, got && mbar_wait(smem_u32(&bar_s[2 * t + buf]), (nq >> 1) & 1, p.wait_ns, &abort_flag));
+        if (!got) {
+          if (lane == 0) report_timeout(p.status, 7, &abort_flag);
+          return false;
+        }
+        tc_fence_after();
+        uint32_t sr[64];
+        tmem_ld32(lane_addr + buf * 128, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(lane_addr + buf * 128 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_sfree[2 * t + buf]));
+        const int tile = first + q, cols = r.w - tile * BQ - 64 * half;  // queries of this half
+        const int from = lo - tile * BQ;
+        if (warp_lo - tile * BQ > 0 || cols < 64) {
+          // columns that do not read this key, or are no query of the request
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e < from || e >= cols) sr[e] = __float_as_uint(-INFINITY);
+        }
+        const float4* lse = reinterpret_cast<const float4*>(sL + l * BQ + 64 * half);
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 v = lse[e];
+          float u0, u1, u2, u3;
+          fma2(u0, u1, __uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1]), sl2, sl2, v.x, v.y);
+          fma2(u2, u3, __uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3]), sl2, sl2, v.z, v.w);
+          add2(s0, s1, s0, s1, ex2(u0), ex2(u1));
+          add2(s2, s3, s2, s3, ex2(u2), ex2(u3));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_lfree[l]));
+        sum += (s0 + s1) + (s2 + s3);
+        if (++q == cnt) q = 0;
+      }
+      // the whole block: its own row; else this worker's first part (the block began
+      // with another worker) or its second
+      if (x0 == 0 && x1 == steps) {
+        const long long row = (long long)kb * kBlock + i;
+        if (row < (long long)r.pre + r.n) p.full[(long long)half * a.rows.KV + r.kv_base + row] = sum;
+      } else {
+        p.part[(((long long)blockIdx.x * 2 + (x0 == 0)) * 2 + half) * kBlock + i] = sum;
+      }
+      return true;
+    });
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ parts
+
+// A block of keys: its row, or its workers' parts in order.
+__global__ void __launch_bounds__(kBlock) weights_join_kernel(const Params p) {
+  wait_for_earlier_kernels();
+  const int R = p.a.rows.R;
+  const int j = find(R, [&](int x) -> long long { return p.block_base[x]; }, blockIdx.x);
+  const Req r = make_req(req_desc(p, j), p.a.window);
+  const int kb = blockIdx.x - p.block_base[j];
+  const long long row = (long long)kb * kBlock + threadIdx.x;
+  if (row >= (long long)r.pre + r.n) return;
+  float sum = 0.f;
+  if (kb < r.nb) {
+    const long long s0 = p.base[j] + p.a.Hq * tiles_before(r, kb), s1 = p.base[j] + p.a.Hq * tiles_before(r, kb + 1);
+    // the last worker that starts at or before a step
+    auto worker = [&](long long s) { return find(p.workers, [&](int w) { return worker_start(p, w); }, s); };
+    const int w0 = worker(s0), w1 = worker(s1 - 1);
+    if (w0 == w1) {
+      const long long at = r.kv_base + row;
+      sum = __ldcg(p.full + at) + __ldcg(p.full + p.a.rows.KV + at);
+    } else {
+      for (int w = w0; w <= w1; ++w) {
+        if (worker_start(p, w) == worker_start(p, w + 1)) continue;  // a worker without steps
+        const float* x = p.part + (((long long)w * 2 + (worker_start(p, w) <= s0)) * 2) * kBlock + threadIdx.x;
+        sum += __ldcg(x) + __ldcg(x + kBlock);
+      }
+    }
+  }
+  p.a.out[r.kv_base + row] = sum;
+}
+
+struct Layout {
+  long long total = 0;
+  int n_tiles = 0, n_blocks = 0;
+  size_t base, tile_base, block_base, lse, full, part, bytes;
+};
+Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int workers) {
+  Layout l;
+  for (int j = 0; j < R; ++j) {
+    const Req r = make_req(reqs[j], window);
+    l.total += Hq * tiles_before(r, r.nb);
+    l.n_tiles += r.nq;
+    l.n_blocks += (int)(((long long)r.pre + r.n + kBlock - 1) / kBlock);
+  }
+  size_t at = 0;
+  auto place = [&](size_t n) {
+    const size_t here = at;
+    at = (at + n + 511) / 512 * 512;
+    return here;
+  };
+  l.base = place(8 * ((size_t)R + 1));
+  l.tile_base = place(4 * ((size_t)R + 1));
+  l.block_base = place(4 * ((size_t)R + 1));
+  l.lse = place((size_t)Hq * l.n_tiles * BQ * 4);
+  l.full = place((size_t)2 * KV * 4);
+  l.part = place((size_t)workers * 4 * kBlock * 4);
+  l.bytes = at;
+  return l;
+}
+
+constexpr int kWorkers = 152;  // one an SM
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& km, const CUtensorMap& qm, const Params& p, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_early(weights_tc_kernel<D>, (unsigned)p.workers, kThreads, Cfg<D>::kSmem, s, 1, km, qm, p);
+}
+
+}  // namespace
+
+size_t prefill_weights_tc_bytes(const int32_t* host_plan, const cp_plan_header& h, int Hq, int window) {
+  return layout(reinterpret_cast<const cp_req_desc*>(host_plan + h.off_req), h.R, h.KV, Hq, window, kWorkers).bytes;
+}
+
+cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t* host_plan, const cp_plan_header& h, int D,
+                                      void* ws, bool stall_test, cudaStream_t s) {
+  const Layout l = layout(reinterpret_cast<const cp_req_desc*>(host_plan + h.off_req), h.R, h.KV, a.Hq, a.window, kWorkers);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  Params p;
+  p.a = a;
+  p.workers = kWorkers;
+  p.total = l.total;
+  p.n_tiles = l.n_tiles;
+  p.base = reinterpret_cast<long long*>(w + l.base);
+  p.tile_base = reinterpret_cast<int32_t*>(w + l.tile_base);
+  p.block_base = reinterpret_cast<int32_t*>(w + l.block_base);
+  p.lse = reinterpret_cast<float*>(w + l.lse);
+  p.full = reinterpret_cast<float*>(w + l.full);
+  p.part = reinterpret_cast<float*>(w + l.part);
+  p.scale_log2 = a.sm_scale * kLog2e;
+  p.status = device_status_ptr();
+  if (!p.status) return cudaErrorInvalidDevice;
+  p.wait_ns = stall_test ? 50000000ull : wait_limit_ns();
+  p.stall_test = stall_test ? 1 : 0;
+  cudaError_t e = launch_early(weights_table_kernel, 1, 256, 0, s, 1, p);
+  if (e == cudaSuccess && l.n_tiles > 0) {
+    CUtensorMap km, qm;
+    const uint32_t box[3] = {64, 1, 128};
+    const uint64_t kd[3] = {(uint64_t)D, (uint64_t)a.Hkv, (uint64_t)a.rows.KV}, ks[2] = {(uint64_t)D * 2, (uint64_t)a.Hkv * D * 2};
+    const uint64_t qd[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.rows.T}, qs[2] = {(uint64_t)D * 2, (uint64_t)a.Hq * D * 2};
+    if (!encode_tensor_map_bf16(&km, a.k, 3, kd, ks, box) || !encode_tensor_map_bf16(&qm, a.q, 3, qd, qs, box))
+      return cudaErrorInvalidValue;
+    e = launch_early(weights_lse_kernel, (unsigned)l.n_tiles, 256, 0, s, 1, p);
+    if (e == cudaSuccess) e = D == 128 ? launch_d<128>(km, qm, p, s) : launch_d<64>(km, qm, p, s);
+  }
+  if (e == cudaSuccess) e = launch_early(weights_join_kernel, (unsigned)l.n_blocks, kBlock, 0, s, 1, p);
+  return e;
+}
+
+}  // namespace cpattn
