@@ -5,16 +5,26 @@
 // no second product and no running maximum.  Products are transposed: 256 keys of
 // a request (two M tiles of 128) against 128 queries of one head,
 //   S^T_t [128 keys x 128 queries] = K_t . Q^T,   t = 0, 1,
-// so a key's weight is a sum along its own TMEM lane and stays in a thread over all
-// queries and heads.  The work is the walk over (request, key block, head, query tile);
-// tiles before the block's first key are left out; workers (one CTA an SM) take equal
-// parts of it.  A block's sums end in a row of their own, or in one of two part
-// rows of each worker that shares the block with others, and a last kernel adds the parts in
-// the order of the workers: no atomics, the same order every time.
+// so a key's weight is a sum along its own TMEM lane and stays in a thread over its
+// queries.  The work of one head is the walk over (request, key block, query tile), tiles
+// before the block's first key left out; workers (one CTA an SM) take equal parts of
+// it.  Long prompts: each worker goes through its part once for every kv head (its
+// keys once, its queries head by head), so that all workers are at the same head
+// and the L2 holds its queries; every block's sums grow over the kv heads.  Short
+// ones (fewer than kLongSteps tiles a worker): the walk has the heads inside the key block
+// and is cut between heads, too.  A block's sums end in a row of their own, or in
+// one of two part rows of each worker that shares the block with others, and a last
+// kernel adds the parts in the order of the workers: no atomics, the same order every time.
 //   warps 0-15  sums: warp w takes keys [32 (w % 4), +32) of M tile (w / 4) % 2 and
 //               the half w / 8 of the query columns
 //   warp 16     TMA producer (K blocks, Q tiles, the LSE of a tile)
 //   warp 17     MMA issuer and TMEM owner
+//   warps 18-19 relays: one more arrival on the barrier that frees a score buffer once
+//               the step's queries and keys have landed, and one on the barrier of its
+//               scores once the LSE has: the issuer waits twice a step, the sums once
+//               (a wait costs some 140 clk even on a phase that is over)
+// A sum warp has half of its columns on their way from TMEM while it works on the
+// other half, across steps, too: the loads' latency is as long as the work.
 // TMEM (512 columns): S^T of tile t in columns [256 t, +256), two buffers of 128.
 // What bounds it: the products need 1,024 clk of the tensor cores a step, its 32,768
 // exponentials as much of the special function units.
@@ -34,17 +44,20 @@ using namespace tc;
 
 constexpr int kBlock = 256;  // keys of a block
 constexpr int BQ = 128;      // queries of a tile
-constexpr int kSumWarps = 16, kThreads = 32 * (kSumWarps + 2);
-constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1;
+constexpr int kSumWarps = 16, kThreads = 32 * (kSumWarps + 4);
+constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1, kWarpRelay = kSumWarps + 2;  // and the one after it
 constexpr int kLseSlots = 4;
+constexpr int kLongSteps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
+// KB buffers of a key block: two where a block meets few query tiles, one where it
+// meets many (the ring of queries is then deeper).
+template <int D, int KB>
 struct Cfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kTileBytes = 128 * D * 2;     // 128 keys or queries
-  static constexpr int kQSlots = D == 128 ? 3 : 6;
-  static constexpr int kSmem = 4 * kTileBytes + kQSlots * kTileBytes + kLseSlots * BQ * 4;
+  static constexpr int kQSlots = (D == 128 ? 7 : 10) - 2 * KB;
+  static constexpr int kSmem = 2 * KB * kTileBytes + kQSlots * kTileBytes + kLseSlots * BQ * 4;
 };
 
 // One request's share of the walk.
@@ -79,6 +92,7 @@ __host__ __device__ inline long long tiles_before(const Req& r, long long k) {
 struct Params {
   PrefillWeightsArgs a;
   int workers;
+  int inner;             // heads inside the walk's blocks: Hq, or 1 where each worker takes its part for every head
   long long total;       // steps of the walk
   int n_tiles;           // query tiles of all requests
   long long* base;       // [R + 1] first step of every request
@@ -114,6 +128,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
                : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
 }
 __device__ void report_timeout(unsigned* status, unsigned site, volatile int* abort) {
   *abort = 1;
@@ -152,7 +171,7 @@ __global__ void __launch_bounds__(256) weights_table_kernel(const Params p) {
   int tile = 0, block = 0;
   auto each = [&](int j) {
     const Req r = make_req(req_desc(p, j), p.a.window);
-    step += p.a.Hq * tiles_before(r, r.nb);
+    step += p.inner * tiles_before(r, r.nb);
     tile += r.nq;
     block += (int)(((long long)r.pre + r.n + kBlock - 1) / kBlock);
   };
@@ -209,24 +228,94 @@ __global__ void __launch_bounds__(256) weights_lse_kernel(const Params p) {
 
 // ------------------------------------------------------------------ sums
 
-template <int D>
+// The steps of a span for one sum warp: adds the weights of its 32 keys and 64 query
+// columns to *sum; false if a wait ran out.  A function of its own, so that the loop
+// has the registers that the walk's state would take.
+struct SumArgs {
+  uint32_t tmem;             // this warp's lanes, its tile's first buffer, its columns
+  uint32_t s, go, lfree;     // barriers: scores, free buffers (of the tile's first buffer), LSE slots
+  uint32_t lse;              // ring of LSE, from this warp's columns on
+  float scale;
+  int nq, steps;
+  int tile, first, last;     // query tile of the first step; tiles go round [first, last)
+  int lo, cols;              // keys are read from column lo - 128 tile on (of this half), columns end at cols - 128 tile
+  unsigned long long wait_ns;
+  volatile int* abort;
+};
+__device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
+  const int lane = threadIdx.x & 31;
+  const int warp_lo = a.lo - lane + 31;
+  uint32_t ra[32], rb[32];
+  float sum = 0.f;
+  int nq = a.nq, tile = a.tile;
+  auto wait_s = [&](int n) {
+    const bool got = __all_sync(0xffffffffu, mbar_wait(a.s + 8 * (n & 1), (n >> 1) & 1, a.wait_ns, a.abort));
+    if (got) tc_fence_after();
+    else *ok = false;
+    return got;
+  };
+  if (!wait_s(nq)) return sum;
+  tmem_ld32(a.tmem + (nq & 1) * 128, ra);
+  for (const int end = nq + a.steps; nq < end; ++nq) {
+    const uint32_t lse = a.lse + (nq % kLseSlots) * (BQ * 4);
+    const bool mask = warp_lo > tile * BQ || a.cols - tile * BQ < 64;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    auto add = [&](uint32_t (&sr)[32], int c0) {
+      if (mask) {  // some columns do not read this key, or are no query of the request: bits [from, to) stay
+        const int from = min(max(a.lo - tile * BQ - c0, 0), 32), to = min(max(a.cols - tile * BQ - c0, 0), 32);
+        const uint32_t keep = __funnelshift_lc(0xffffffffu, 0u, to) & ~__funnelshift_lc(0xffffffffu, 0u, from);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (!(keep >> e & 1)) sr[e] = 0xff800000u;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 v = lds4(lse + (c0 + 4 * e) * 4);
+        float u0, u1, u2, u3;
+        fma2(u0, u1, __uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1]), a.scale, a.scale, v.x, v.y);
+        fma2(u2, u3, __uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3]), a.scale, a.scale, v.z, v.w);
+        add2(s0, s1, s0, s1, ex2(u0), ex2(u1));
+        add2(s2, s3, s2, s3, ex2(u2), ex2(u3));
+      }
+    };
+    tmem_ld_wait();
+    tmem_ld32(a.tmem + (nq & 1) * 128 + 32, rb);
+    add(ra, 0);
+    tmem_ld_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(a.go + 8 * (nq & 1));
+    if (nq + 1 < end) {
+      if (!wait_s(nq + 1)) return sum;
+      tmem_ld32(a.tmem + ((nq + 1) & 1) * 128, ra);
+    }
+    add(rb, 32);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(a.lfree + 8 * (nq % kLseSlots));
+    sum += (s0 + s1) + (s2 + s3);
+    if (++tile == a.last) tile = a.first;
+  }
+  return sum;
+}
+
+template <int D, int KB>
 __global__ void __launch_bounds__(kThreads, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ Params p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, KB>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sK = smem;                                 // [2 buffers][2 tiles]
-  uint8_t* sQ = smem + 4 * C::kTileBytes;             // ring of query tiles
+  uint8_t* sK = smem;                                 // [KB buffers][2 tiles]
+  uint8_t* sQ = smem + 2 * KB * C::kTileBytes;             // ring of query tiles
   float* sL = reinterpret_cast<float*>(sQ + C::kQSlots * C::kTileBytes);  // ring of their LSE
-  __shared__ __align__(8) uint64_t bar_k[2], bar_kfree[2], bar_q[C::kQSlots], bar_qfree[C::kQSlots], bar_l[kLseSlots],
-      bar_lfree[kLseSlots], bar_s[4], bar_sfree[4], bar_drain, bar_never;
+  __shared__ __align__(8) uint64_t bar_k[KB], bar_kfree[KB], bar_q[C::kQSlots], bar_qfree[C::kQSlots], bar_l[kLseSlots],
+      bar_lfree[kLseSlots], bar_s[4], bar_go[4], bar_drain, bar_never;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int zero_flag;
   const PrefillWeightsArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < KB; ++i) {
       mbar_init(smem_u32(&bar_k[i]), 1);
       mbar_init(smem_u32(&bar_kfree[i]), 1);
     }
@@ -239,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bar_lfree[i]), kSumWarps);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&bar_s[i]), 1);
-      mbar_init(smem_u32(&bar_sfree[i]), kSumWarps / 2);
+      mbar_init(smem_u32(&bar_s[i]), 2);  // the products' commit and the relay
+      mbar_init(smem_u32(&bar_go[i]), kSumWarps / 2 + 1);  // a tile's sum warps and the relay
     }
     mbar_init(smem_u32(&bar_drain), 1);
     mbar_init(smem_u32(&bar_never), 1);
@@ -260,37 +349,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_earlier_kernels();
   const long long begin = worker_start(p, blockIdx.x), end = worker_start(p, blockIdx.x + 1);
 
-  // The blocks of this worker's part of the walk, in order: each(request index,
-  // request, block, first step of the worker in the block, one past its last, block's steps).
+  // The spans of this worker, in order: each(request, block, first tile, tiles, heads
+  // [h0, h1) of one kv head or of all, first step x0 and last x1 of them (head by head over
+  // the tiles), whether the span begins and ends the block's work of this pass, pass).
+  // With inner == 1 a pass is a kv head and the tiles are the worker's own.
+  struct Span {
+    int j, kb, first, cnt, h0, x0, x1, pass;
+    bool whole;    // the block is this worker's alone
+    bool begins;   // the block's first step is this worker's
+  };
+  // Heads of a span's first kv head from its first step on.
+  auto heads_left = [&](const Span& sp) { return a.G - (sp.h0 + sp.x0 / sp.cnt) % a.G; };
   auto walk = [&](auto&& each) {
     if (begin >= end) return;
-    int j = find(a.rows.R, [&](int x) { return p.base[x]; }, begin);
-    Req r = make_req(req_desc(p, j), a.window);
-    long long base = p.base[j], pos = begin;
-    // the block of step `begin`: binary search of the sums
-    int kb;
-    {
-      const long long t = (begin - base) / a.Hq;
-      int lo = 0, hi = r.nb - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tiles_before(r, mid) <= t) lo = mid; else hi = mid - 1;
+    const int passes = p.inner == 1 ? a.Hkv : 1;
+    for (int pass = 0; pass < passes; ++pass) {
+      int j = find(a.rows.R, [&](int x) { return p.base[x]; }, begin);
+      Req r = make_req(req_desc(p, j), a.window);
+      long long base = p.base[j], pos = begin;
+      int kb;  // the block of step `begin`: binary search of the sums
+      {
+        const long long t = (begin - base) / p.inner;
+        int lo = 0, hi = r.nb - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (tiles_before(r, mid) <= t) lo = mid; else hi = mid - 1;
+        }
+        kb = lo;
       }
-      kb = lo;
-    }
-    while (pos < end) {
-      while (kb >= r.nb) {  // the next request with steps
-        ++j;
-        r = make_req(req_desc(p, j), a.window);
-        base = p.base[j];
-        kb = 0;
+      while (pos < end) {
+        while (kb >= r.nb) {  // the next request with steps
+          ++j;
+          r = make_req(req_desc(p, j), a.window);
+          base = p.base[j];
+          kb = 0;
+        }
+        const long long s0 = base + p.inner * tiles_before(r, kb);
+        const int first = first_tile(r, kb), tiles = r.nq - first;
+        const int a0 = (int)(pos - s0), a1 = (int)min((long long)p.inner * tiles, end - s0);
+        Span sp = {j, kb, first, tiles, 0, a0, a1, pass, a0 == 0 && a1 == p.inner * tiles, a0 == 0};
+        if (p.inner == 1) {  // tiles [a0, a1) for each head of the pass
+          sp.first = first + a0;
+          sp.cnt = a1 - a0;
+          sp.h0 = pass * a.G;
+          sp.x0 = 0;
+          sp.x1 = a.G * sp.cnt;
+        }
+        if (!each(r, sp)) return;
+        pos = s0 + a1;
+        ++kb;
       }
-      const long long s0 = base + a.Hq * tiles_before(r, kb);
-      const int steps = a.Hq * (r.nq - first_tile(r, kb));
-      const int x0 = (int)(pos - s0), x1 = (int)min((long long)steps, end - s0);
-      if (!each(j, r, kb, x0, x1, steps)) return;
-      pos = s0 + x1;
-      ++kb;
     }
   };
 
@@ -303,28 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) report_timeout(p.status, site, &abort_flag);
       return ok = false;
     };
-    walk([&](int j, const Req& r, int kb, int x0, int x1, int) {
-      const int first = first_tile(r, kb), cnt = r.nq - first;
-      int h = x0 / cnt, q = x0 - h * cnt, g_in = -1;
-      const int tile0 = p.tile_base[j];
-      for (int x = x0; x < x1; ++x) {
-        const int g = h / a.G;
-        if (g != g_in) {
-          g_in = g;
-          const int b = nk & 1;
-          if (nk >= 2 && !wait_all(&bar_kfree[b], (nk / 2 - 1) & 1, 1)) return false;
-          if (elect_one()) {
-            const uint32_t full = smem_u32(&bar_k[b]), dst = smem_u32(sK + b * 2 * C::kTileBytes);
-            mbar_expect_tx(full, 2 * C::kTileBytes);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int c = 0; c < C::kChunks; ++c)
-                tma_load_3d(dst + t * C::kTileBytes + c * (128 * 128), &kmap, c * 64, g, r.kv_base + kb * kBlock + t * 128, full);
-          }
-          __syncwarp();
-          ++nk;
-        }
+    walk([&](const Req& r, const Span& sp) {
+      int h = sp.x0 / sp.cnt, q = sp.x0 - h * sp.cnt, g_in = -1;
+      h += sp.h0;
+      int g = h / a.G, hg = h - g * a.G;
+      const int tile0 = p.tile_base[sp.j];
+      for (int x = sp.x0; x < sp.x1; ++x) {
         const int s = nq % C::kQSlots, l = nq % kLseSlots;
         if (nq >= C::kQSlots && !wait_all(&bar_qfree[s], (nq / C::kQSlots - 1) & 1, 2)) return false;
         if (nq >= kLseSlots && !wait_all(&bar_lfree[l], (nq / kLseSlots - 1) & 1, 3)) return false;
@@ -333,16 +425,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_expect_tx(full, C::kTileBytes);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(dst + c * (128 * 128), &qmap, c * 64, h, r.q_base + r.n - r.w + (first + q) * BQ, full);
+            tma_load_3d(dst + c * (128 * 128), &qmap, c * 64, h, r.q_base + r.n - r.w + (sp.first + q) * BQ, full);
           const uint32_t lf = smem_u32(&bar_l[l]);
           mbar_expect_tx(lf, BQ * 4);
-          bulk_load(smem_u32(sL + l * BQ), p.lse + ((long long)h * p.n_tiles + tile0 + first + q) * BQ, BQ * 4, lf);
+          bulk_load(smem_u32(sL + l * BQ), p.lse + ((long long)h * p.n_tiles + tile0 + sp.first + q) * BQ, BQ * 4, lf);
         }
         __syncwarp();
         ++nq;
-        if (++q == cnt) {
+        if (g != g_in) {  // behind the first query tile that meets the block: that is on its way meanwhile
+          g_in = g;
+          const int b = nk % KB;
+          if (nk >= KB && !wait_all(&bar_kfree[b], (nk / KB - 1) & 1, 1)) return false;
+          if (elect_one()) {
+            const uint32_t full = smem_u32(&bar_k[b]), dst = smem_u32(sK + b * 2 * C::kTileBytes);
+            mbar_expect_tx(full, 2 * C::kTileBytes);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(dst + t * C::kTileBytes + c * (128 * 128), &kmap, c * 64, g, r.kv_base + sp.kb * kBlock + t * 128, full);
+          }
+          __syncwarp();
+          ++nk;
+        }
+        if (++q == sp.cnt) {
           q = 0;
           ++h;
+          if (++hg == a.G) {
+            hg = 0;
+            ++g;
+          }
         }
       }
       return true;
@@ -355,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (fills > 0) mbar_wait(smem_u32(bar + x), (fills - 1) & 1, 1000000000ull, &zero_flag);
         }
       };
-      drain(bar_k, nk, 2);
+      drain(bar_k, nk, KB);
       drain(bar_q, nq, C::kQSlots);
       drain(bar_l, nq, kLseSlots);
       __syncwarp();
@@ -371,27 +483,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       return false;
     };
     if (!p.stall_test || wait_all(&bar_never, 0, 10))
-      walk([&](int, const Req& r, int kb, int x0, int x1, int) {
-        const int cnt = r.nq - first_tile(r, kb);
-        int h = x0 / cnt, q = x0 - h * cnt, g_in = -1;
-        for (int x = x0; x < x1; ++x, ++nq) {
-          if (h / a.G != g_in) {
-            g_in = h / a.G;
-            if (!wait_all(&bar_k[nk & 1], (nk >> 1) & 1, 4)) return false;
+      walk([&](const Req&, const Span& sp) {
+        // steps until the kv head changes
+        int left = heads_left(sp) * sp.cnt - sp.x0 % sp.cnt;
+        ++nk;
+        for (int x = sp.x0; x < sp.x1; ++x, ++nq) {
+          if (left == 0) {
+            left = a.G * sp.cnt;
             ++nk;
           }
-          if (++q == cnt) {
-            q = 0;
-            ++h;
-          }
-          const bool last = x + 1 == x1 || h / a.G != g_in;  // of this K block
+          --left;
+          const bool last = x + 1 == sp.x1 || left == 0;  // of this K block
           const int s = nq % C::kQSlots, buf = nq & 1;
-          if (!wait_all(&bar_q[s], (nq / C::kQSlots) & 1, 5)) return false;
           for (int t = 0; t < 2; ++t) {
-            if (nq >= 2 && !wait_all(&bar_sfree[2 * t + buf], (nq / 2 - 1) & 1, 6)) return false;
+            // the buffer's scores of two steps ago are read, this step's queries and keys have landed
+            if (!wait_all(&bar_go[2 * t + buf], (nq >> 1) & 1, 6)) return false;
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t k = dK + ((uint32_t)((((nk - 1) & 1) * 2 + t) * C::kTileBytes) >> 4);
+              const uint64_t k = dK + ((uint32_t)((((nk - 1) % KB) * 2 + t) * C::kTileBytes) >> 4);
               const uint64_t b = dQ + ((uint32_t)(s * C::kTileBytes) >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
@@ -401,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_commit(smem_u32(&bar_s[2 * t + buf]));
               if (t == 1) {
                 mma_commit(smem_u32(&bar_qfree[s]));
-                if (last) mma_commit(smem_u32(&bar_kfree[(nk - 1) & 1]));
+                if (last) mma_commit(smem_u32(&bar_kfree[(nk - 1) % KB]));
               }
             }
             __syncwarp();
@@ -413,67 +522,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) mma_commit(smem_u32(&bar_drain));
     __syncwarp();
     mbar_wait(smem_u32(&bar_drain), 0, 1000000000ull, &zero_flag);
+  } else if (warp >= kWarpRelay) {
+    // ------------------------------------------------------------ relays
+    // The arrival for step n comes after the barrier's phase of step n - 2 is over, so
+    // no phase takes an arrival that is the next one's.
+    const bool operands = warp == kWarpRelay;  // else the LSE
+    int nq = 0, nk = 0;
+    walk([&](const Req&, const Span& sp) {
+      int left = heads_left(sp) * sp.cnt - sp.x0 % sp.cnt;
+      bool keys = true;  // the step's K block is a new one
+      for (int x = sp.x0; x < sp.x1; ++x, ++nq) {
+        bool got;
+        if (operands) {
+          got = mbar_wait(smem_u32(&bar_q[nq % C::kQSlots]), (nq / C::kQSlots) & 1, p.wait_ns, &abort_flag);
+          if (left == 0) {
+            left = a.G * sp.cnt;
+            keys = true;
+          }
+          --left;
+          if (keys) {
+            got = got && mbar_wait(smem_u32(&bar_k[nk % KB]), (nk / KB) & 1, p.wait_ns, &abort_flag);
+            ++nk;
+            keys = false;
+          }
+        } else {
+          got = mbar_wait(smem_u32(&bar_l[nq % kLseSlots]), (nq / kLseSlots) & 1, p.wait_ns, &abort_flag);
+        }
+        for (int t = 0; t < 2 && got; ++t) {
+          const uint32_t bar = smem_u32(operands ? &bar_go[2 * t + (nq & 1)] : &bar_s[2 * t + (nq & 1)]);
+          if (nq >= 2) got = mbar_wait(bar, (nq / 2 - 1) & 1, p.wait_ns, &abort_flag);
+          got = __all_sync(0xffffffffu, got);
+          if (got && lane == 0) mbar_arrive(bar);
+        }
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) report_timeout(p.status, 8, &abort_flag);
+          return false;
+        }
+      }
+      return true;
+    });
   } else {
     // ------------------------------------------------------------ sums
     const int quarter = warp & 3, t = (warp >> 2) & 1, half = warp >> 3;
     const int i = t * 128 + quarter * 32 + lane;  // key of the block
-    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + t * 256 + 64 * half;
-    const float sl2 = p.scale_log2;
-    int nq = 0;
-    walk([&](int, const Req& r, int kb, int x0, int x1, int steps) {
-      const int first = first_tile(r, kb), cnt = r.nq - first;
-      int q = x0 % cnt;
+    SumArgs sa;
+    sa.tmem = tmem + ((uint32_t)(quarter * 32) << 16) + t * 256 + 64 * half;
+    sa.s = smem_u32(&bar_s[2 * t]);
+    sa.go = smem_u32(&bar_go[2 * t]);
+    sa.lfree = smem_u32(&bar_lfree[0]);
+    sa.lse = smem_u32(sL + 64 * half);
+    sa.scale = p.scale_log2;
+    sa.nq = 0;
+    sa.wait_ns = p.wait_ns;
+    sa.abort = &abort_flag;
+    if (lane == 0) {  // both buffers are free
+      mbar_arrive(smem_u32(&bar_go[2 * t]));
+      mbar_arrive(smem_u32(&bar_go[2 * t + 1]));
+    }
+    walk([&](const Req& r, const Span& sp) {
+      sa.steps = sp.x1 - sp.x0;
+      sa.first = sp.first;
+      sa.last = sp.first + sp.cnt;
+      sa.tile = sp.first + sp.x0 % sp.cnt;
       // column c of tile q stands at position off + 128 q + c: it reads this key from c = lo - 128 q on
-      const int lo = kb * kBlock + i - r.off - 64 * half, warp_lo = lo - lane + 31;
-      float sum = 0.f;
-      for (int x = x0; x < x1; ++x, ++nq) {
-        const int buf = nq & 1, l = nq % kLseSlots;
-        bool got = mbar_wait(smem_u32(&bar_l[l]), (nq / kLseSlots) & 1, p.wait_ns, &abort_flag);
-        got = __all_sync(0xffffffffu, got && mbar_wait(smem_u32(&bar_s[2 * t + buf]), (nq >> 1) & 1, p.wait_ns, &abort_flag));
-        if (!got) {
-          if (lane == 0) report_timeout(p.status, 7, &abort_flag);
-          return false;
-        }
-        tc_fence_after();
-        uint32_t sr[64];
-        tmem_ld32(lane_addr + buf * 128, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld32(lane_addr + buf * 128 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bar_sfree[2 * t + buf]));
-        const int tile = first + q, cols = r.w - tile * BQ - 64 * half;  // queries of this half
-        const int from = lo - tile * BQ;
-        if (warp_lo - tile * BQ > 0 || cols < 64) {
-          // columns that do not read this key, or are no query of the request
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e < from || e >= cols) sr[e] = __float_as_uint(-INFINITY);
-        }
-        const float4* lse = reinterpret_cast<const float4*>(sL + l * BQ + 64 * half);
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 v = lse[e];
-          float u0, u1, u2, u3;
-          fma2(u0, u1, __uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1]), sl2, sl2, v.x, v.y);
-          fma2(u2, u3, __uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3]), sl2, sl2, v.z, v.w);
-          add2(s0, s1, s0, s1, ex2(u0), ex2(u1));
-          add2(s2, s3, s2, s3, ex2(u2), ex2(u3));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bar_lfree[l]));
-        sum += (s0 + s1) + (s2 + s3);
-        if (++q == cnt) q = 0;
+      sa.lo = sp.kb * kBlock + i - r.off - 64 * half;
+      sa.cols = r.w - 64 * half;
+      bool ok = true;
+      const float sum = sum_steps(sa, &ok);
+      if (!ok) {
+        if (lane == 0) report_timeout(p.status, 7, &abort_flag);
+        return false;
       }
+      sa.nq += sa.steps;
       // the whole block: its own row; else this worker's first part (the block began
-      // with another worker) or its second
-      if (x0 == 0 && x1 == steps) {
-        const long long row = (long long)kb * kBlock + i;
-        if (row < (long long)r.pre + r.n) p.full[(long long)half * a.rows.KV + r.kv_base + row] = sum;
+      // with another worker) or its second.  Later kv heads add to what this thread wrote.
+      float* to = nullptr;
+      if (!sp.whole) {
+        to = p.part + (((long long)blockIdx.x * 2 + sp.begins) * 2 + half) * kBlock + i;
       } else {
-        p.part[(((long long)blockIdx.x * 2 + (x0 == 0)) * 2 + half) * kBlock + i] = sum;
+        const long long row = (long long)sp.kb * kBlock + i;
+        if (row < (long long)r.pre + r.n) to = p.full + (long long)half * a.rows.KV + r.kv_base + row;
       }
+      if (to) *to = sp.pass ? *to + sum : sum;
       return true;
     });
   }
@@ -496,7 +626,7 @@ __global__ void __launch_bounds__(kBlock) weights_join_kernel(const Params p) {
   if (row >= (long long)r.pre + r.n) return;
   float sum = 0.f;
   if (kb < r.nb) {
-    const long long s0 = p.base[j] + p.a.Hq * tiles_before(r, kb), s1 = p.base[j] + p.a.Hq * tiles_before(r, kb + 1);
+    const long long s0 = p.base[j] + p.inner * tiles_before(r, kb), s1 = p.base[j] + p.inner * tiles_before(r, kb + 1);
     // the last worker that starts at or before a step
     auto worker = [&](long long s) { return find(p.workers, [&](int w) { return worker_start(p, w); }, s); };
     const int w0 = worker(s0), w1 = worker(s1 - 1);
@@ -516,16 +646,20 @@ __global__ void __launch_bounds__(kBlock) weights_join_kernel(const Params p) {
 
 struct Layout {
   long long total = 0;
-  int n_tiles = 0, n_blocks = 0;
+  int n_tiles = 0, n_blocks = 0, inner = 1;
   size_t base, tile_base, block_base, lse, full, part, bytes;
 };
 Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int workers) {
   Layout l;
   for (int j = 0; j < R; ++j) {
     const Req r = make_req(reqs[j], window);
-    l.total += Hq * tiles_before(r, r.nb);
+    l.total += tiles_before(r, r.nb);
     l.n_tiles += r.nq;
     l.n_blocks += (int)(((long long)r.pre + r.n + kBlock - 1) / kBlock);
+  }
+  if (l.total < (long long)kLongSteps * workers) {
+    l.inner = Hq;
+    l.total *= Hq;
   }
   size_t at = 0;
   auto place = [&](size_t n) {
@@ -545,11 +679,11 @@ Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int wo
 
 constexpr int kWorkers = 152;  // one an SM
 
-template <int D>
+template <int D, int KB>
 cudaError_t launch_d(const CUtensorMap& km, const CUtensorMap& qm, const Params& p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<D, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, KB>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_early(weights_tc_kernel<D>, (unsigned)p.workers, kThreads, Cfg<D>::kSmem, s, 1, km, qm, p);
+  return launch_early(weights_tc_kernel<D, KB>, (unsigned)p.workers, kThreads, Cfg<D, KB>::kSmem, s, 1, km, qm, p);
 }
 
 }  // namespace
@@ -565,6 +699,7 @@ cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t
   Params p;
   p.a = a;
   p.workers = kWorkers;
+  p.inner = l.inner;
   p.total = l.total;
   p.n_tiles = l.n_tiles;
   p.base = reinterpret_cast<long long*>(w + l.base);
@@ -587,7 +722,11 @@ cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t
     if (!encode_tensor_map_bf16(&km, a.k, 3, kd, ks, box) || !encode_tensor_map_bf16(&qm, a.q, 3, qd, qs, box))
       return cudaErrorInvalidValue;
     e = launch_early(weights_lse_kernel, (unsigned)l.n_tiles, 256, 0, s, 1, p);
-    if (e == cudaSuccess) e = D == 128 ? launch_d<128>(km, qm, p, s) : launch_d<64>(km, qm, p, s);
+    if (e == cudaSuccess) {
+      const bool many = l.inner == 1;
+      e = D == 128 ? (many ? launch_d<128, 1>(km, qm, p, s) : launch_d<128, 2>(km, qm, p, s))
+                   : (many ? launch_d<64, 1>(km, qm, p, s) : launch_d<64, 2>(km, qm, p, s));
+    }
   }
   if (e == cudaSuccess) e = launch_early(weights_join_kernel, (unsigned)l.n_blocks, kBlock, 0, s, 1, p);
   return e;
