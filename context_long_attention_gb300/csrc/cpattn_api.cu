@@ -918,7 +918,7 @@ cp_status run_prefix(const cp_plan_header& h, const int32_t* W, const PrefixArgs
   if (h.n_seg > 0) {
     if (prefix_tc_supported(kv_dtype, a.D)) {
       const char* stall = getenv("CPATTN_TEST_STALL");  // test hook of the bounded waits
-      e = launch_prefix_tc(a, shard_rows, h.n_tiles, stall && stall[0] == '1', s);
+      e = launch_prefix_tc(a, kv_dtype, shard_rows, h.n_tiles, stall && stall[0] == '1', s);
     } else {
       e = launch_prefix_simt(a, kv_dtype, h.n_tiles, s);
     }

@@ -279,7 +279,7 @@ struct PrefixArgs {
 };
 cudaError_t launch_prefix_simt(const PrefixArgs& a, cp_dtype kv, int workers, cudaStream_t s);
 bool prefix_tc_supported(cp_dtype kv, int D);
-cudaError_t launch_prefix_tc(const PrefixArgs& a, const long long* shard_rows, int workers, bool stall_test, cudaStream_t s);
+cudaError_t launch_prefix_tc(const PrefixArgs& a, cp_dtype kv, const long long* shard_rows, int workers, bool stall_test, cudaStream_t s);
 // The first `blocks` blocks of the plan's list, from parts to results.
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int blocks, cudaStream_t s);
 

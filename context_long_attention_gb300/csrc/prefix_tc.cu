@@ -1,5 +1,5 @@
 // Attention of groups of queries over a shared prefix on the tcgen05 tensor
-// cores (bf16 cache, head dim 64 or 128).
+// cores (bf16 cache at head dim 64 or 128, E4M3 cache at 128).
 //
 // With n requests behind one prefix the n G rows (query, head of the kv head's G)
 // are the M dimension of ordinary matrix products over the prefix, so each key and value
@@ -23,6 +23,9 @@
 // half of its own S columns.  The running max moves only when a row's max grows by
 // more than 2^8; any running max gives the exact result (O = sum e^(s-m) v / sum e^(s-m)).
 // P is rounded to bf16 for its product, its sum is not.
+// E4M3 (F8): the ring holds the codes as bf16 (exact), three slots behind a ring of four
+// code tiles; warps 18-21 convert and take the relay's part.  A token's scale multiplies its
+// column of S and, once P's sum is taken, of P.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,19 +44,20 @@ using namespace tc;
 constexpr int BM = 128;  // rows of an M tile
 constexpr int BN = 128;  // keys of a K/V tile
 constexpr int kSoftmaxWarps = 16;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
 constexpr int kWarpTma = kSoftmaxWarps, kWarpMma = kSoftmaxWarps + 1, kWarpRelay = kSoftmaxWarps + 2;
-constexpr int kLaunchBoundThreads = 640;  // registers as for five warps an SM sub-partition
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
 
-template <int D>
+template <int D, bool F8>
 struct Cfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kQBytes = BM * D * 2;
   static constexpr int kSlotBytes = BN * D * 2;
-  static constexpr int kSlots = D == 128 ? 5 : 10;
-  static constexpr int kSmem = 2 * kQBytes + kSlots * kSlotBytes + 1024;
+  static constexpr int kSlots = F8 ? 3 : D == 128 ? 5 : 10;
+  static constexpr int kCodeSlots = F8 ? 4 : 0, kCodeBytes = BN * D;
+  static constexpr int kTiles = 2 * kQBytes + kSlots * kSlotBytes + kCodeSlots * kCodeBytes;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + (F8 ? 6 : 3));
+  static constexpr int kRelays = F8 ? 4 : 1;  // arrivals of the relay's part
 };
 
 // K and V of up to MAXC shards; a pool has one map of each, with 64-row boxes.
@@ -93,6 +97,16 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// Four E4M3 codes as bf16, two words of two.  With the code's exponent and mantissa at
+// bf16's place a code is 2^-120 of its value (subnormal codes are subnormal bf16),
+// and the product with 2^120 is exact.
+__device__ __forceinline__ void bf16_of_codes(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);  // codes in the upper bytes of halves
+  const uint32_t x = (a & 0x80008000u) | ((a & 0x7f007f00u) >> 4), y = (b & 0x80008000u) | ((b & 0x7f007f00u) >> 4);
+  const uint32_t k = 0x7b807b80u;  // 2^120 twice
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(k));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(k));
+}
 __device__ __forceinline__ void mbar_inval(uint32_t bar) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
 
 __device__ void report_timeout(unsigned* status, unsigned site, volatile int* abort) {
@@ -119,6 +133,8 @@ struct Walk {
 };
 
 struct Shared {
+  // E4M3: unit[0..3] code tiles landed, unit[4..7] code tiles read, rel[4..5] a tile's scales
+  // written, rel[8] K_0 converted
   uint64_t bar_unit[10], bar_rel[10], bar_s[2], bar_p[2], bar_o[2], bar_never, bar_drain;
   uint32_t tmem_slot;
   volatile int abort_flag;
@@ -126,12 +142,13 @@ struct Shared {
   int32_t tile_off[CP_MAX_SHARDS + 2];
   int32_t rows[CP_MAX_SHARDS], row_off[CP_MAX_SHARDS];
   cp_prefix_item item;
+  alignas(16) float scale[2][BN];  // read in pieces of four; E4M3: the tokens' scales of the last two tiles
 };
 
-template <int D, bool WIDE, int MAXC>
+template <int D, bool WIDE, int MAXC, bool F8>
 __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Shared& sh, uint8_t* sQ,
                                         uint8_t* sKV, uint32_t tmem) {
-  using C = Cfg<D>;
+  using C = Cfg<D, F8>;
   constexpr int kUnitBars = C::kSlots;
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
@@ -168,6 +185,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     float m_used = -INFINITY, l = 0.f;
     bool ok = true, first = true;  // first: no key of this chain so far
     int keys = 0;                  // of this half's columns, those in use in this tile
+    const float* scales = nullptr;  // E4M3: of this half's columns
     auto load_s = [&](uint32_t (&sr)[NC]) {
       if constexpr (NC == 64) {
         tmem_ld32(lane_addr + colS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
@@ -176,6 +194,16 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         tmem_ld32(lane_addr + colS, sr);
       }
       tmem_ld_wait();
+      if constexpr (F8) {
+#pragma unroll
+        for (int e = 0; e < NC; e += 4) {
+          const float4 k = *reinterpret_cast<const float4*>(scales + e);
+          sr[e] = __float_as_uint(__uint_as_float(sr[e]) * k.x);
+          sr[e + 1] = __float_as_uint(__uint_as_float(sr[e + 1]) * k.y);
+          sr[e + 2] = __float_as_uint(__uint_as_float(sr[e + 2]) * k.z);
+          sr[e + 3] = __float_as_uint(__uint_as_float(sr[e + 3]) * k.w);
+        }
+      }
       if (keys < NC) {
 #pragma unroll
         for (int e = 0; e < NC; ++e)
@@ -191,7 +219,12 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         fma2(u0, u1, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]), sl2, sl2, neg, neg);
         const float p0 = ex2(u0), p1 = ex2(u1);
         add2(s0sum, s1sum, s0sum, s1sum, p0, p1);
-        pk[e] = pack_bf16x2(p0, p1);
+        if constexpr (F8) {
+          const float2 k = *reinterpret_cast<const float2*>(scales + 2 * e);
+          pk[e] = pack_bf16x2(p0 * k.x, p1 * k.y);
+        } else {
+          pk[e] = pack_bf16x2(p0, p1);
+        }
       }
       return s0sum + s1sum;
     };
@@ -201,7 +234,12 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       const int chain = WIDE ? nv : nv - 64 * t;                      // of the chain
       keys = chain - NC * half;
       if (j + 1 < nK) w.next();
-      const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_s[t]), j & 1, p.wait_ns, abort));
+      bool got = mbar_wait(smem_u32(&sh.bar_s[t]), j & 1, p.wait_ns, abort);
+      if constexpr (F8) {
+        got = got && mbar_wait(smem_u32(&sh.bar_rel[4 + (j & 1)]), (j >> 1) & 1, p.wait_ns, abort);
+        scales = sh.scale[j & 1] + (WIDE ? 0 : 64 * t) + NC * half;
+      }
+      got = __all_sync(0xffffffffu, got);
       if (got && releaser && lane == 0) mbar_arrive(smem_u32(&sh.bar_rel[j % C::kSlots]));
       tc_fence_after();
       uint32_t sr[NC], pk[NC / 2];
@@ -397,12 +435,41 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
     };
     auto load = [&](const CUtensorMap* map, int c0, int c1, uint32_t dst, uint32_t full) {
+      // a code row is one chunk of 128 bytes
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c) {
+      for (int c = 0; c < (F8 ? 1 : C::kChunks); ++c) {
         tma_load_3d(dst + c * (BN * 128), map, c * 64, it.kv_head, c0, full);
         if (a.rm.table) tma_load_3d(dst + c * (BN * 128) + 64 * 128, map, c * 64, it.kv_head, c1, full);
       }
     };
+    if constexpr (F8) {
+      // load u = 2j (K_j) or 2j + 1 (V_j) goes to code slot u % 4
+      uint8_t* codes = sKV + C::kSlots * C::kSlotBytes;
+      locate();
+      int last = 0;  // K_0: loaded before the block's barrier
+      for (int u = 1; u < 2 * nK; ++u) {
+        const int s = u & 3;
+        if (u >= 4 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_unit[4 + s]), ((u >> 2) - 1) & 1, p.wait_ns, abort))) {
+          if (lane == 0) report_timeout(p.status, 4, abort);
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t full = smem_u32(&sh.bar_unit[s]);
+          mbar_expect_tx(full, C::kCodeBytes);
+          load(u & 1 ? &maps.v[yr] : &maps.k[yr], y0, y1, smem_u32(codes + s * C::kCodeBytes), full);
+        }
+        __syncwarp();
+        last = u;
+        if ((u & 1) && u + 1 < 2 * nK) {
+          w.next();
+          locate();
+        }
+      }
+      // never leave with a copy in flight: the last fill of every slot
+      for (int u = max(0, last - 3); u <= last; ++u) mbar_wait(smem_u32(&sh.bar_unit[u & 3]), (u >> 2) & 1, 1000000000ull, &sh.zero_flag);
+      __syncwarp();
+      return;
+    }
     locate();
     v0 = y0;
     v1 = y1;
@@ -445,6 +512,68 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     for (int k = max(0, last_unit - kUnitBars + 1); k <= last_unit; ++k)
       mbar_wait(smem_u32(&sh.bar_unit[k % kUnitBars]), (k / kUnitBars) & 1, 1000000000ull, &sh.zero_flag);
     __syncwarp();
+  } else if (F8 && warp >= kWarpRelay) {
+    // ------------------------------------------------------------ E4M3 to bf16 (a thread a row)
+    bool ok = true;
+    const int row = (warp - kWarpRelay) * 32 + lane;
+    uint8_t* codes = sKV + C::kSlots * C::kSlotBytes;
+    Walk w(sh.tile_off, it.tile_begin);
+    for (int u = 0; u < 2 * nK && ok; ++u) {
+      const int j = u >> 1;
+      const bool is_v = u & 1;
+      const int nv = sh.rows[w.r] - (w.t - w.off[w.r]) * BN;  // keys of tile j from its first row on
+      float scale = 0.f;
+      if (!is_v && row < nv) {
+        const int in_pair = (w.t - w.off[w.r]) * BN + row, pair = w.r * a.R + it.group;
+        scale = __ldcg(a.sc.p[w.r] + (a.rm.table ? map_row(a.rm, pair, 0, in_pair) : (long long)sh.row_off[w.r] + in_pair));
+      }
+      if (is_v && j + 1 < nK) w.next();
+      ok = mbar_wait(smem_u32(&sh.bar_unit[u & 3]), (u >> 2) & 1, p.wait_ns, abort);
+      if (ok && u >= C::kSlots) {  // the slot's load u - 3 is read: release r frees V_(r-1) and K_r
+        const int r = (u - C::kSlots + 1) >> 1;
+        ok = mbar_wait(smem_u32(&sh.bar_rel[r % C::kSlots]), (r / C::kSlots) & 1, p.wait_ns, abort);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) report_timeout(p.status, 5, abort);
+        break;
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(codes + (u & 3) * C::kCodeBytes + row * 128);
+      uint8_t* dst = sKV + (u % C::kSlots) * C::kSlotBytes + row * 128;
+      // V's rows behind the shard's last key meet weights of 0: any finite value will do
+#pragma unroll 2
+      for (int c = 0; c < 8; ++c) {
+        const uint4 x = src[c ^ (row & 7)];
+        uint32_t o[8];
+        bf16_of_codes(x.x, o[0], o[1]);
+        bf16_of_codes(x.y, o[2], o[3]);
+        bf16_of_codes(x.z, o[4], o[5]);
+        bf16_of_codes(x.w, o[6], o[7]);
+        uint8_t* chunk = dst + (c >> 2) * (BN * 128);
+        const int unit = 2 * (c & 3);
+        *reinterpret_cast<uint4*>(chunk + ((unit ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(chunk + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      // K_j's slot was free: S_(j-1) is complete, so both chains are done with P_(j-2) and its scales
+      if (!is_v) sh.scale[j & 1][row] = scale;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sh.bar_unit[4 + (u & 3)]));
+        if (!is_v) mbar_arrive(smem_u32(&sh.bar_rel[4 + (j & 1)]));
+        if (u == 0) mbar_arrive(smem_u32(&sh.bar_rel[8]));
+      }
+      // V_j and K_(j+1) (if there is one) are in place: this warp's arrival on both chains' P_j
+      const int step = is_v ? j : j - 1;
+      if (is_v ? j + 1 == nK : j > 0) {
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (step > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_p[t]), (step - 1) & 1, p.wait_ns, abort));
+          if (ok && lane == 0) mbar_arrive(smem_u32(&sh.bar_p[t]));
+          __syncwarp();
+        }
+        if (!ok && lane == 0) report_timeout(p.status, 17, abort);
+      }
+    }
   } else if (warp == kWarpRelay) {
     // ------------------------------------------------------------ relay
     bool ok = true;
@@ -518,7 +647,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       fail(10);
       ok = false;
     }
-    if (ok && !wait_all(&sh.bar_unit[0], 0)) {
+    if (ok && !wait_all(F8 ? &sh.bar_rel[8] : &sh.bar_unit[0], 0)) {
       fail(12);
       ok = false;
     }
@@ -548,18 +677,19 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   }
 }
 
-// the static arrays and the dynamic ones together: at most 227 KB a block
-static_assert(Cfg<128>::kSmem + sizeof(Shared) <= 232448 && Cfg<64>::kSmem + sizeof(Shared) <= 232448, "shared memory");
+// the tiles and what stands behind them: at most 227 KB a block
+template <int D, bool F8>
+constexpr int kSmem = Cfg<D, F8>::kTiles + (int)sizeof(Shared);
+static_assert(kSmem<128, false> <= 232448 && kSmem<64, false> <= 232448 && kSmem<128, true> <= 232448, "shared memory");
 
-template <int D, int MAXC>
-__global__ void __launch_bounds__(kLaunchBoundThreads, 1)
+template <int D, int MAXC, bool F8>
+__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ Maps<MAXC> maps, const __grid_constant__ Params p) {
-  using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  using C = Cfg<D, F8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * C::kQBytes;
-  __shared__ __align__(8) Shared sh;
+  Shared& sh = *reinterpret_cast<Shared*>(smem + C::kTiles);
   const PrefixArgs& a = p.a;
   const int warp = threadIdx.x >> 5;
   if (warp == kWarpTma)  // the descriptors' own latency, before the first load needs them
@@ -589,7 +719,9 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
       if (lane < kBars) {
         uint64_t* b = reinterpret_cast<uint64_t*>(&sh) + lane;
         if (wi > w0) mbar_inval(smem_u32(b));
-        mbar_init(smem_u32(b), b == &sh.bar_p[0] || b == &sh.bar_p[1] ? 2 * BM + 1 : 1);
+        const bool is_p = b == &sh.bar_p[0] || b == &sh.bar_p[1];
+        const bool four = F8 && ((b >= &sh.bar_unit[4] && b <= &sh.bar_unit[7]) || (b >= &sh.bar_rel[4] && b <= &sh.bar_rel[8]));
+        mbar_init(smem_u32(b), is_p ? 2 * BM + C::kRelays : four ? 4 : 1);
         mbar_init_fence();
         fence_proxy_async_smem();
       }
@@ -603,10 +735,10 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
           y1 = it.first_row + 64 < it.first_rows ? (int)map_row(a.rm, pair, 0, it.first_row + 64) : (int)a.rm.pool_rows;
         }
         const CUtensorMap* map = &maps.k[a.rm.table ? 0 : it.first_shard];
-        const uint32_t full = smem_u32(&sh.bar_unit[0]), dst = smem_u32(sKV);
-        mbar_expect_tx(full, C::kSlotBytes);
+        const uint32_t full = smem_u32(&sh.bar_unit[0]), dst = smem_u32(F8 ? sKV + C::kSlots * C::kSlotBytes : sKV);
+        mbar_expect_tx(full, F8 ? C::kCodeBytes : C::kSlotBytes);
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
+        for (int c = 0; c < (F8 ? 1 : C::kChunks); ++c) {
           tma_load_3d(dst + c * (BN * 128), map, c * 64, it.kv_head, y0, full);
           if (a.rm.table) tma_load_3d(dst + c * (BN * 128) + 64 * 128, map, c * 64, it.kv_head, y1, full);
         }
@@ -637,7 +769,7 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
       }
       fence_proxy_async_smem();
     } else {
-      for (int r = threadIdx.x - kWarpMma * 32; r <= a.C; r += 64) {
+      for (int r = threadIdx.x - kWarpMma * 32; r <= a.C; r += C::kThreads - kWarpMma * 32) {
         sh.tile_off[r] = a.plan[a.off_tiles + it.group * (a.C + 1) + r];
         if (r < a.C) {
           const cp_pair_desc* pd = reinterpret_cast<const cp_pair_desc*>(a.plan + a.off_pair) + r * a.R + it.group;
@@ -650,8 +782,8 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_slot;
-    if (sh.item.m_rows > BM) process<D, true, MAXC>(p, maps, sh, sQ, sKV, tmem);
-    else process<D, false, MAXC>(p, maps, sh, sQ, sKV, tmem);
+    if (sh.item.m_rows > BM) process<D, true, MAXC, F8>(p, maps, sh, sQ, sKV, tmem);
+    else process<D, false, MAXC, F8>(p, maps, sh, sQ, sKV, tmem);
     fence_proxy_async_smem();  // the next item's copies come after this one's reads and writes
     tc_fence_before();
     __syncthreads();
@@ -661,38 +793,43 @@ __global__ void __launch_bounds__(kLaunchBoundThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(sh.tmem_slot, 512);
 }
 
-// [rows, H, D] bf16 as 3-D (D, H, rows); box (64, 1, box_rows), 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* base, long long rows, int H, int D, int box_rows) {
+// [rows, H, D] as 3-D (D, H, rows); boxes of 128-byte rows, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, long long rows, int H, int D, int box_rows, bool f8) {
+  if (f8) {
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)rows}, strides[2] = {(uint64_t)D, (uint64_t)H * D};
+    const uint32_t box[3] = {(uint32_t)D, 1, (uint32_t)box_rows};
+    return encode_tensor_map_u8_3d(m, base, dims, strides, box);
+  }
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)rows};
   const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)H * D * 2};
   const uint32_t box[3] = {64, 1, (uint32_t)box_rows};
   return encode_tensor_map_bf16(m, base, 3, dims, strides, box, D == 128);
 }
 
-template <int D, int MAXC>
+template <int D, int MAXC, bool F8>
 cudaError_t launch_c(const Params& p, const long long* shard_rows, int workers, cudaStream_t s) {
   const PrefixArgs& a = p.a;
   Maps<MAXC> maps;
   memset(&maps, 0, sizeof(maps));
   if (a.rm.table) {
-    if (!make_map(&maps.k[0], a.k.p[0], a.rm.pool_rows, a.Hkv, D, 64) || !make_map(&maps.v[0], a.v.p[0], a.rm.pool_rows, a.Hkv, D, 64))
+    if (!make_map(&maps.k[0], a.k.p[0], a.rm.pool_rows, a.Hkv, D, 64, F8) || !make_map(&maps.v[0], a.v.p[0], a.rm.pool_rows, a.Hkv, D, 64, F8))
       return cudaErrorInvalidValue;
   } else {
     for (int r = 0; r < a.C; ++r)
       if (shard_rows[r] > 0 &&
-          (!make_map(&maps.k[r], a.k.p[r], shard_rows[r], a.Hkv, D, BN) || !make_map(&maps.v[r], a.v.p[r], shard_rows[r], a.Hkv, D, BN)))
+          (!make_map(&maps.k[r], a.k.p[r], shard_rows[r], a.Hkv, D, BN, F8) || !make_map(&maps.v[r], a.v.p[r], shard_rows[r], a.Hkv, D, BN, F8)))
         return cudaErrorInvalidValue;
   }
-  const cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D, MAXC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D, MAXC, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, F8>);
   if (e != cudaSuccess) return e;
-  return launch_early(prefix_tc_kernel<D, MAXC>, (unsigned)workers, kThreads, Cfg<D>::kSmem, s, 1, maps, p);
+  return launch_early(prefix_tc_kernel<D, MAXC, F8>, (unsigned)workers, Cfg<D, F8>::kThreads, kSmem<D, F8>, s, 1, maps, p);
 }
 
 }  // namespace
 
-bool prefix_tc_supported(cp_dtype kv, int D) { return kv == CP_BF16 && (D == 64 || D == 128); }
+bool prefix_tc_supported(cp_dtype kv, int D) { return kv == CP_BF16 ? D == 64 || D == 128 : kv == CP_FP8_E4M3 && D == 128; }
 
-cudaError_t launch_prefix_tc(const PrefixArgs& a, const long long* shard_rows, int workers, bool stall_test, cudaStream_t s) {
+cudaError_t launch_prefix_tc(const PrefixArgs& a, cp_dtype kv, const long long* shard_rows, int workers, bool stall_test, cudaStream_t s) {
   Params p = {a, FastDiv(a.G), 0.f, nullptr, 0, 0};
   p.scale_log2 = a.sm_scale * kLog2e;
   p.status = device_status_ptr();
@@ -701,8 +838,11 @@ cudaError_t launch_prefix_tc(const PrefixArgs& a, const long long* shard_rows, i
   p.stall_test = stall_test ? 1 : 0;
   // the maps travel as kernel arguments: 2 KB of them where eight shards are enough
   const bool few = a.rm.table || a.C <= 8;
-  if (a.D == 128) return few ? launch_c<128, 8>(p, shard_rows, workers, s) : launch_c<128, CP_MAX_SHARDS>(p, shard_rows, workers, s);
-  return few ? launch_c<64, 8>(p, shard_rows, workers, s) : launch_c<64, CP_MAX_SHARDS>(p, shard_rows, workers, s);
+  if (kv == CP_FP8_E4M3)
+    return few ? launch_c<128, 8, true>(p, shard_rows, workers, s) : launch_c<128, CP_MAX_SHARDS, true>(p, shard_rows, workers, s);
+  if (a.D == 128)
+    return few ? launch_c<128, 8, false>(p, shard_rows, workers, s) : launch_c<128, CP_MAX_SHARDS, false>(p, shard_rows, workers, s);
+  return few ? launch_c<64, 8, false>(p, shard_rows, workers, s) : launch_c<64, CP_MAX_SHARDS, false>(p, shard_rows, workers, s);
 }
 
 }  // namespace cpattn
