@@ -703,7 +703,7 @@ cp_status run_decode_merged(const cp_plan_header& h, const int32_t* W, const voi
 
 // Work of one block's tile against its fixed work (query rows, the first tile's
 // fill, the result), in sixteenths of a tile of two 128-row M tiles.
-constexpr long long kPrefixItemCost = 32, kPrefixTile2 = 16, kPrefixTile1 = 10;
+constexpr long long kPrefixItemCost = 64, kPrefixTile2 = 16, kPrefixTile1 = 14;
 
 cp_status build_prefix_plan(int C, int R, const int32_t* prefix_len, const int32_t* members, int layout, int Hq, int Hkv,
                             int n_workers, std::vector<int32_t>* out) {

@@ -23,8 +23,8 @@
 // half of its own S columns.  The running max moves only when a row's max grows by
 // more than 2^8; any running max gives the exact result (O = sum e^(s-m) v / sum e^(s-m)).
 // P is rounded to bf16 for its product, its sum is not.
-// E4M3 (F8): the ring holds the codes as bf16 (exact), three slots behind a ring of four
-// code tiles; warps 18-21 convert and take the relay's part.  A token's scale multiplies its
+// E4M3 (F8): the ring holds the codes as bf16 (exact), three slots (four where one Q tile
+// leaves room, so that K is a step ahead) behind a ring of four code tiles; warps 18-21 convert and take the relay's part.  A token's scale multiplies its
 // column of S and, once P's sum is taken, of P.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -48,14 +48,16 @@ constexpr int kWarpTma = kSoftmaxWarps, kWarpMma = kSoftmaxWarps + 1, kWarpRelay
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
 
-template <int D, bool F8>
+template <int D, bool F8, bool WIDE = true>
 struct Cfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kQBytes = BM * D * 2;
   static constexpr int kSlotBytes = BN * D * 2;
-  static constexpr int kSlots = F8 ? 3 : D == 128 ? 5 : 10;
+  static constexpr int kSlots = F8 ? (WIDE ? 3 : 4) : D == 128 ? 5 : 10;
+  static constexpr int kRing = (F8 && !WIDE ? 1 : 2) * kQBytes;  // where the ring begins
   static constexpr int kCodeSlots = F8 ? 4 : 0, kCodeBytes = BN * D;
-  static constexpr int kTiles = 2 * kQBytes + kSlots * kSlotBytes + kCodeSlots * kCodeBytes;
+  static constexpr int kCodes = kRing + kSlots * kSlotBytes;
+  static constexpr int kTiles = kCodes + kCodeSlots * kCodeBytes;
   static constexpr int kThreads = 32 * (kSoftmaxWarps + (F8 ? 6 : 3));
   static constexpr int kRelays = F8 ? 4 : 1;  // arrivals of the relay's part
 };
@@ -133,7 +135,7 @@ struct Walk {
 };
 
 struct Shared {
-  // E4M3: unit[0..3] code tiles landed, unit[4..7] code tiles read, rel[4..5] a tile's scales
+  // E4M3: unit[0..3] code tiles landed, unit[4..7] code tiles read, rel[4..6] a tile's scales
   // written, rel[8] K_0 converted
   uint64_t bar_unit[10], bar_rel[10], bar_s[2], bar_p[2], bar_o[2], bar_never, bar_drain;
   uint32_t tmem_slot;
@@ -142,13 +144,15 @@ struct Shared {
   int32_t tile_off[CP_MAX_SHARDS + 2];
   int32_t rows[CP_MAX_SHARDS], row_off[CP_MAX_SHARDS];
   cp_prefix_item item;
-  alignas(16) float scale[2][BN];  // read in pieces of four; E4M3: the tokens' scales of the last two tiles
+  alignas(16) float scale[3][BN];  // read in pieces of four; E4M3: the tokens' scales of the last three tiles
 };
 
 template <int D, bool WIDE, int MAXC, bool F8>
 __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Shared& sh, uint8_t* sQ,
-                                        uint8_t* sKV, uint32_t tmem) {
-  using C = Cfg<D, F8>;
+                                        uint32_t tmem) {
+  using C = Cfg<D, F8, WIDE>;
+  static_assert(C::kCodes == Cfg<D, F8>::kCodes, "one place of the code tiles");
+  uint8_t* sKV = sQ + C::kRing;
   constexpr int kUnitBars = C::kSlots;
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
@@ -236,8 +240,8 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       if (j + 1 < nK) w.next();
       bool got = mbar_wait(smem_u32(&sh.bar_s[t]), j & 1, p.wait_ns, abort);
       if constexpr (F8) {
-        got = got && mbar_wait(smem_u32(&sh.bar_rel[4 + (j & 1)]), (j >> 1) & 1, p.wait_ns, abort);
-        scales = sh.scale[j & 1] + (WIDE ? 0 : 64 * t) + NC * half;
+        got = got && mbar_wait(smem_u32(&sh.bar_rel[4 + j % 3]), (j / 3) & 1, p.wait_ns, abort);
+        scales = sh.scale[j % 3] + (WIDE ? 0 : 64 * t) + NC * half;
       }
       got = __all_sync(0xffffffffu, got);
       if (got && releaser && lane == 0) mbar_arrive(smem_u32(&sh.bar_rel[j % C::kSlots]));
@@ -444,7 +448,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     };
     if constexpr (F8) {
       // load u = 2j (K_j) or 2j + 1 (V_j) goes to code slot u % 4
-      uint8_t* codes = sKV + C::kSlots * C::kSlotBytes;
+      uint8_t* codes = sQ + C::kCodes;
       locate();
       int last = 0;  // K_0: loaded before the block's barrier
       for (int u = 1; u < 2 * nK; ++u) {
@@ -516,7 +520,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     // ------------------------------------------------------------ E4M3 to bf16 (a thread a row)
     bool ok = true;
     const int row = (warp - kWarpRelay) * 32 + lane;
-    uint8_t* codes = sKV + C::kSlots * C::kSlotBytes;
+    uint8_t* codes = sQ + C::kCodes;
     Walk w(sh.tile_off, it.tile_begin);
     for (int u = 0; u < 2 * nK && ok; ++u) {
       const int j = u >> 1;
@@ -529,7 +533,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
       if (is_v && j + 1 < nK) w.next();
       ok = mbar_wait(smem_u32(&sh.bar_unit[u & 3]), (u >> 2) & 1, p.wait_ns, abort);
-      if (ok && u >= C::kSlots) {  // the slot's load u - 3 is read: release r frees V_(r-1) and K_r
+      if (ok && u >= C::kSlots) {  // the slot's load u - kSlots is read: release r frees V_(r-1) and K_r
         const int r = (u - C::kSlots + 1) >> 1;
         ok = mbar_wait(smem_u32(&sh.bar_rel[r % C::kSlots]), (r / C::kSlots) & 1, p.wait_ns, abort);
       }
@@ -541,7 +545,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       const uint4* src = reinterpret_cast<const uint4*>(codes + (u & 3) * C::kCodeBytes + row * 128);
       uint8_t* dst = sKV + (u % C::kSlots) * C::kSlotBytes + row * 128;
       // V's rows behind the shard's last key meet weights of 0: any finite value will do
-#pragma unroll 2
+#pragma unroll 4
       for (int c = 0; c < 8; ++c) {
         const uint4 x = src[c ^ (row & 7)];
         uint32_t o[8];
@@ -554,13 +558,13 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         *reinterpret_cast<uint4*>(chunk + ((unit ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(chunk + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      // K_j's slot was free: S_(j-1) is complete, so both chains are done with P_(j-2) and its scales
-      if (!is_v) sh.scale[j & 1][row] = scale;
+      // K_j's slot was free: S_(j-2) is complete, so both chains are done with P_(j-3) and its scales
+      if (!is_v) sh.scale[j % 3][row] = scale;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(smem_u32(&sh.bar_unit[4 + (u & 3)]));
-        if (!is_v) mbar_arrive(smem_u32(&sh.bar_rel[4 + (j & 1)]));
+        if (!is_v) mbar_arrive(smem_u32(&sh.bar_rel[4 + j % 3]));
         if (u == 0) mbar_arrive(smem_u32(&sh.bar_rel[8]));
       }
       // V_j and K_(j+1) (if there is one) are in place: this warp's arrival on both chains' P_j
@@ -688,7 +692,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   using C = Cfg<D, F8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * C::kQBytes;
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::kTiles);
   const PrefixArgs& a = p.a;
   const int warp = threadIdx.x >> 5;
@@ -735,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           y1 = it.first_row + 64 < it.first_rows ? (int)map_row(a.rm, pair, 0, it.first_row + 64) : (int)a.rm.pool_rows;
         }
         const CUtensorMap* map = &maps.k[a.rm.table ? 0 : it.first_shard];
-        const uint32_t full = smem_u32(&sh.bar_unit[0]), dst = smem_u32(F8 ? sKV + C::kSlots * C::kSlotBytes : sKV);
+        const uint32_t full = smem_u32(&sh.bar_unit[0]), dst = smem_u32(F8 ? sQ + C::kCodes : sQ + C::kRing);
         mbar_expect_tx(full, F8 ? C::kCodeBytes : C::kSlotBytes);
 #pragma unroll
         for (int c = 0; c < (F8 ? 1 : C::kChunks); ++c) {
@@ -782,8 +785,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_slot;
-    if (sh.item.m_rows > BM) process<D, true, MAXC, F8>(p, maps, sh, sQ, sKV, tmem);
-    else process<D, false, MAXC, F8>(p, maps, sh, sQ, sKV, tmem);
+    if (sh.item.m_rows > BM) process<D, true, MAXC, F8>(p, maps, sh, sQ, tmem);
+    else process<D, false, MAXC, F8>(p, maps, sh, sQ, tmem);
     fence_proxy_async_smem();  // the next item's copies come after this one's reads and writes
     tc_fence_before();
     __syncthreads();

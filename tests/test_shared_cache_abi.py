@@ -110,8 +110,8 @@ def test_prefix_plan(cp, C, lens, members, Hq, Hkv, workers, layout):
         assert len(seen[key]) == b[6] and [x for x, _ in seen[key]] + [total] == [0] * (total > 0) + [y for _, y in seen[key]] + [0] * (total == 0)
     assert sorted(int(i[7]) for i in p.items) == list(range(p.n_parts))
     assert [b[6] != 1 for b in p.blocks] == [True] * p.n_merge + [False] * (len(p.blocks) - p.n_merge)
-    cost = [sum((int(i[6]) - int(i[5])) * (16 if i[4] > 128 else 10) for i in p.items[p.worker_off[w]:p.worker_off[w + 1]]) for w in range(workers)]
-    whole = sum(cost) + 32 * sum(1 for b in p.blocks if b[6])
+    cost = [sum((int(i[6]) - int(i[5])) * (16 if i[4] > 128 else 14) for i in p.items[p.worker_off[w]:p.worker_off[w + 1]]) for w in range(workers)]
+    whole = sum(cost) + 64 * sum(1 for b in p.blocks if b[6])
     assert max(cost, default=0) <= whole / workers + 16 + 16
     need = [cp.cp_prefix_workspace_size(p, 128, n) for n in (0, 1)]
     assert need[1] == p.n_parts * 256 * 129 * 4 and need[0] == sum(int(b[6]) for b in p.blocks[:p.n_merge]) * 256 * 129 * 4
