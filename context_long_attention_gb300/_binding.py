@@ -1153,6 +1153,13 @@ PREFIX_BLOCK_FIELDS = ["group", "kv_head", "row0", "m0", "m_rows", "first_part",
 class PrefixPlan(_Plan):
     """Work of cp_prefix_attn over R shared prefixes (cp_prefix_plan)."""
 
+    def __init__(self, host: np.ndarray, dev: torch.Tensor | None):
+        super().__init__(host, dev)
+        p, R, at = self.pairs, self.R, self.off_idx
+        self.heads = int(host[at]), int(host[at + 1])  # (Hq, Hkv) that the plan was made for
+        self.n_merge, self.merge_parts = int(host[at + 2]), int(host[at + 3])
+        self._shard_rows = [int(p[r * R:(r + 1) * R, 0].sum()) for r in range(self.C)]
+
     @property
     def pairs(self):
         P = self.C * self.R
@@ -1176,18 +1183,12 @@ class PrefixPlan(_Plan):
     def tile_off(self):
         return self.words(self.off_tiles, self.R * (self.C + 1)).reshape(self.R, self.C + 1)
 
-    @property
-    def heads(self):
-        """(Hq, Hkv) that the plan was made for."""
-        return int(self.host[self.off_idx]), int(self.host[self.off_idx + 1])
-
-    @property
-    def n_merge(self):
-        return int(self.host[self.off_idx + 2])
-
     def shard_rows(self):
-        p = self.pairs
-        return [int(p[r * self.R:(r + 1) * self.R, 0].sum()) for r in range(self.C)]
+        return list(self._shard_rows)
+
+    def workspace_bytes(self, D: int, P: int) -> int:
+        """cp_prefix_workspace_size without the call."""
+        return (self.header["n_parts"] if P else self.merge_parts) * 256 * (D + 1) * 4
 
 
 def cp_prefix_plan(C: int, prefix_len, members, Hq: int, Hkv: int, layout: int = CP_DCP_ROUND_ROBIN, n_workers: int = 0,
@@ -1214,11 +1215,9 @@ def cp_prefix_workspace_size(plan: PrefixPlan, D: int, P: int = 0) -> int:
     return b.value
 
 
-def _prefix_call(plan, q, Hkv, D, o_part, lse_part, out_dtype, o, lse, ws, dev):
+def _prefix_call(plan, q, D, o_part, lse_part, out_dtype, o, lse, ws, dev):
     """Checks what shards and pages share and makes the outputs."""
     N, Hq = plan.header["T"], plan.heads[0]
-    if plan.heads != (Hq, Hkv):
-        raise ValueError(f"{Hkv} kv heads: the plan was made for {plan.heads[1]}")
     if plan.dev is None or plan.dev.get_device() != dev:
         raise ValueError(f"the plan has no device part on {q.device}")
     P = 0
@@ -1226,29 +1225,33 @@ def _prefix_call(plan, q, Hkv, D, o_part, lse_part, out_dtype, o, lse, ws, dev):
         raise ValueError("o_part and lse_part must both be given or both None")
     if o_part is not None:
         P = o_part.shape[0]
-        if tuple(o_part.shape[1:]) != (N, Hq, D) and o_part.numel() != P * N * Hq * D:
-            raise ValueError(f"o_part: need [P, {N}, {Hq}, {D}], got {tuple(o_part.shape)}")
+        if o_part.numel() != P * N * Hq * D or lse_part.shape[0] != P or lse_part.numel() != P * N * Hq:
+            raise ValueError(f"need o_part [P, {N}, {Hq}, {D}] and lse_part [P, {N}, {Hq}], got {tuple(o_part.shape)} and "
+                             f"{tuple(lse_part.shape)}")
         _need("o_part", o_part, _f32, o_part.shape, dev)
-        if lse_part.shape[0] != P or lse_part.numel() != P * N * Hq:
-            raise ValueError(f"lse_part: need [{P}, {N}, {Hq}], got {tuple(lse_part.shape)}")
         _need("lse_part", lse_part, _f32, lse_part.shape, dev)
     if out_dtype is not _bf16 and out_dtype is not _f32:
         raise TypeError(f"out_dtype: need bf16 or fp32, got {out_dtype}")
-    o = torch.empty((N, Hq, D), dtype=out_dtype, device=q.device) if o is None else _need("o", o, out_dtype, (N, Hq, D), dev)
-    lse = torch.empty((N, Hq), dtype=_f32, device=q.device) if lse is None else _need("lse", lse, _f32, (N, Hq), dev)
-    need = cp_prefix_workspace_size(plan, D, P)
-    if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
-        raise ValueError(f"ws must be a contiguous tensor on {q.device}")
-    return P, o, lse, ws, 0 if ws is None else ws.numel() * ws.element_size()
+    where = q.device
+    o = torch.empty((N, Hq, D), dtype=out_dtype, device=where) if o is None else _need("o", o, out_dtype, (N, Hq, D), dev)
+    lse = torch.empty((N, Hq), dtype=_f32, device=where) if lse is None else _need("lse", lse, _f32, (N, Hq), dev)
+    if ws is None:
+        ws_bytes = plan.workspace_bytes(D, P)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=where) if ws_bytes else None
+    else:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {where}")
+        ws_bytes = ws.numel() * ws.element_size()
+    return P, o, lse, ws, ws_bytes
 
 
 def _prefix_q(plan, q, kv_dtype):
     dev = q.get_device()
     if q.dim() != 3:
         raise ValueError(f"q: need [{plan.header['T']}, Hq, D], got {tuple(q.shape)}")
-    return dev, _need("q", q, _f32 if kv_dtype == CP_FP32 else _bf16, (plan.header["T"], plan.heads[0], q.shape[2]), dev).shape[2]
+    D = q.shape[2]
+    _need("q", q, _f32 if kv_dtype == CP_FP32 else _bf16, (plan.header["T"], plan.heads[0], D), dev)
+    return dev, D
 
 
 def cp_prefix_attn(plan: PrefixPlan, q, shard_k, shard_v, shard_scale=None, sm_scale=None, o_part=None, lse_part=None,
@@ -1258,26 +1261,30 @@ def cp_prefix_attn(plan: PrefixPlan, q, shard_k, shard_v, shard_scale=None, sm_s
     shard_scale[r] [rows_r]), joined with P partial results of the rows' own
     tokens (o_part [P, N, Hq, D], lse_part [P, N, Hq] fp32, as cp_decode_attn
     returns them).  Returns (o [N, Hq, D] out_dtype, lse [N, Hq] fp32)."""
-    if len(shard_k) != plan.C or len(shard_v) != plan.C or (shard_scale is not None and len(shard_scale) != plan.C):
-        raise ValueError(f"need one tensor for each of {plan.C} shards")
+    C, Hkv = plan.header["C"], plan.heads[1]
+    if len(shard_k) != C or len(shard_v) != C or (shard_scale is not None and len(shard_scale) != C):
+        raise ValueError(f"need one tensor for each of {C} shards")
+    dtype = shard_k[0].dtype
     kv_dtype = _dtype_code(shard_k[0])
     dev, D = _prefix_q(plan, q, kv_dtype)
-    Hkv = plan.heads[1]
-    for r, rows in enumerate(plan.shard_rows()):
-        for name, t in (("shard_k", shard_k[r]), ("shard_v", shard_v[r])):
-            if _dtype_code(t) != kv_dtype:
-                raise TypeError(f"{name}[{r}]: all shards need one dtype")
-            _need(f"{name}[{r}]", t, t.dtype, (rows, Hkv, D), dev)
-        if shard_scale is not None:
-            _need(f"shard_scale[{r}]", shard_scale[r], _f32, (rows,), dev)
+    rows, tail = plan._shard_rows, (Hkv, D)
+    kp, vp = (ctypes.c_void_p * C)(), (ctypes.c_void_p * C)()
+    sp = None if shard_scale is None else (ctypes.c_void_p * C)()
+    for r in range(C):
+        shape = (rows[r], *tail)
+        kp[r] = _need(f"shard_k[{r}]", shard_k[r], dtype, shape, dev).data_ptr()
+        vp[r] = _need(f"shard_v[{r}]", shard_v[r], dtype, shape, dev).data_ptr()
+        if sp is not None:
+            sp[r] = _need(f"shard_scale[{r}]", shard_scale[r], _f32, (rows[r],), dev).data_ptr()
     if dev != _device_index():
         return _on(dev, cp_prefix_attn, plan, q, shard_k, shard_v, shard_scale, sm_scale, o_part, lse_part, out_dtype, o, lse, ws)
-    P, o, lse, ws, ws_bytes = _prefix_call(plan, q, Hkv, D, o_part, lse_part, out_dtype, o, lse, ws, dev)
-    _check(lib.cp_prefix_attn(plan.host_ptr, plan.dev.data_ptr(), kv_dtype, q.data_ptr(), _ptr_array(shard_k),
-                              _ptr_array(shard_v), _ptr_array(shard_scale) if shard_scale is not None else None,
-                              plan.heads[0], Hkv, D, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), P,
-                              _ptr(o_part), _ptr(lse_part), o.data_ptr(), _dtype_code(o), lse.data_ptr(), _ptr(ws), ws_bytes,
-                              _raw_stream(dev)))
+    P, o, lse, ws, ws_bytes = _prefix_call(plan, q, D, o_part, lse_part, out_dtype, o, lse, ws, dev)
+    st = lib.cp_prefix_attn(plan.host_ptr, plan.dev.data_ptr(), kv_dtype, q.data_ptr(), kp, vp, sp, plan.heads[0], Hkv, D,
+                            1.0 / math.sqrt(D) if sm_scale is None else sm_scale, P, o_part.data_ptr() if P else None,
+                            lse_part.data_ptr() if P else None, o.data_ptr(), CP_BF16 if out_dtype is _bf16 else CP_FP32,
+                            lse.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st)
     return o, lse
 
 
@@ -1300,7 +1307,7 @@ def cp_prefix_attn_paged(plan: PrefixPlan, pages: PageTable, q, k_pool, v_pool, 
     if dev != _device_index():
         return _on(dev, cp_prefix_attn_paged, plan, pages, q, k_pool, v_pool, scale_pool, sm_scale, o_part, lse_part, out_dtype,
                    o, lse, ws)
-    P, o, lse, ws, ws_bytes = _prefix_call(plan, q, Hkv, D, o_part, lse_part, out_dtype, o, lse, ws, dev)
+    P, o, lse, ws, ws_bytes = _prefix_call(plan, q, D, o_part, lse_part, out_dtype, o, lse, ws, dev)
     _check(lib.cp_prefix_attn_paged(plan.host_ptr, plan.dev.data_ptr(), kv_dtype, q.data_ptr(), k_pool.data_ptr(),
                                     v_pool.data_ptr(), _ptr(scale_pool), table, _ptr(pages.dev), pages.max_pages,
                                     pages.page_size, pages.num_pages, plan.heads[0], Hkv, D,
