@@ -35,6 +35,77 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Pairs of up to kRankRows rows: a row's place is the number of rows before it, counted
+// by its thread over all keys in shared memory.  One barrier, where the radix select has some
+// twenty (a step of 512 pairs of 264 rows: 22.7 us with its moves by the radix select).
+constexpr int kRankRows = 512;
+__global__ void __launch_bounds__(kRankRows) evict_rank_kernel(const EvictArgs a, const FastDiv by_page) {
+  __shared__ __align__(16) uint32_t s_key[kRankRows];
+  __shared__ int s_holes[kRankRows / 32], s_movers[kRankRows / 32];
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  const int pair = blockIdx.x, b = pair % a.B, r = pair / a.B;
+  wait_for_earlier_kernels();
+  const int page = by_page(i);
+  // a row behind the pair's last reads its page's entry as far as the table goes, too
+  const int id = page < a.max_pages ? __ldcg(a.table + (long long)pair * a.max_pages + page) : -1;
+  const int L = a.ctx_len[b], K = a.keep_len[b], start = a.keep_from ? a.keep_from[b] : 0;
+  auto rows_of = [&](int len) { return len > r ? (len - r - 1) / a.C + 1 : 0; };
+  const bool bad_len = L < 0 || K < 0 || rows_of(L) > (long long)a.max_pages * a.page_size;
+  const int n = bad_len ? 0 : rows_of(L), m = bad_len ? 0 : min(n, rows_of(K));
+  const bool there = i < n, in = id >= 0 && id < a.num_pages;
+  const int row = id * a.page_size + (i - page * a.page_size);
+  uint32_t key = 0;
+  if (there && in) {
+    const float w = __ldcg(a.weights + row);
+    const int pos = a.pos ? __ldcg(a.pos + row) : i * a.C + r;
+    key = pos < a.keep_below || (a.keep_from && pos >= start) ? kProtected : weight_key(w);
+  }
+  s_key[i] = key;
+  const bool bad = __syncthreads_or(there && !in);
+  int32_t* src = a.src + (long long)pair * a.max_moves;
+  int32_t* dst = a.dst + (long long)pair * a.max_moves;
+  int moves = bad_len ? -1 : 0;
+  if (m > 0 && m < n) {
+    // rows before this one in the order: larger keys, and equal ones of lower rows
+    int before = 0;
+    for (int j = 0; j < warp * 32; j += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(s_key + j);
+      before += (k.x >= key) + (k.y >= key) + (k.z >= key) + (k.w >= key);
+    }
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t k = s_key[warp * 32 + j];
+      before += j < lane ? k >= key : k > key;
+    }
+    for (int j = warp * 32 + 32; j < n; j += 4) {  // rows behind the last one have key 0: not larger
+      const uint4 k = *reinterpret_cast<const uint4*>(s_key + j);
+      before += (k.x > key) + (k.y > key) + (k.z > key) + (k.w > key);
+    }
+    const bool stay = there && before < m;
+    const unsigned h = __ballot_sync(0xffffffffu, there && !stay && i < m), v = __ballot_sync(0xffffffffu, stay && i >= m);
+    if (lane == 0) {
+      s_holes[warp] = __popc(h);
+      s_movers[warp] = __popc(v);
+    }
+    __syncthreads();
+    int hole = __popc(h & ((1u << lane) - 1)), mover = __popc(v & ((1u << lane) - 1));
+    for (int w = 0; w < kRankRows / 32; ++w) {
+      if (w < warp) {
+        hole += s_holes[w];
+        mover += s_movers[w];
+      }
+      moves += s_holes[w];
+    }
+    if (bad || moves > a.max_moves) {
+      moves = -1;
+    } else {
+      if (h >> lane & 1) dst[hole] = row;
+      if (v >> lane & 1) src[mover] = row;
+    }
+  }
+  for (int x = max(moves, 0) + i; x < a.max_moves; x += kRankRows) src[x] = dst[x] = -1;
+  if (i == 0) a.count[pair] = moves;
+}
+
 struct SelectParams {
   EvictArgs a;
   FastDiv by_page;
@@ -52,7 +123,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const SelectParams p) 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pair = blockIdx.x, b = pair % a.B, r = pair / a.B;
   wait_for_earlier_kernels();
-  const int L = a.ctx_len[b], K = a.keep_len[b];
+  const int L = a.ctx_len[b], K = a.keep_len[b], start = a.keep_from ? a.keep_from[b] : 0;
   auto rows_of = [&](int len) { return len > r ? (len - r - 1) / a.C + 1 : 0; };
   int32_t* src = a.src + (long long)pair * a.max_moves;
   int32_t* dst = a.dst + (long long)pair * a.max_moves;
@@ -67,10 +138,36 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const SelectParams p) 
     const int row = pool_row(i);
     if (row < 0) return 0;
     const int pos = a.pos ? a.pos[row] : i * a.C + r;
-    if (pos < a.keep_below || (a.keep_from && pos >= a.keep_from[b])) return kProtected;
+    if (pos < a.keep_below || (a.keep_from && pos >= start)) return kProtected;
     return weight_key(a.weights[row]);
   };
   auto key_of = [&](int i) { return i < p.cached ? s_key[i] : read_key(i); };
+  // Keys of kBatch rows a thread: pages, then weights and positions are loaded together.
+  // False where a page is outside the pool.
+  constexpr int kBatch = 4;
+  auto load_keys = [&](int i0) {
+    int id[kBatch], pos[kBatch];
+    float w[kBatch];
+    bool good = true;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) id[k] = i0 + k * NT < n ? __ldcg(table + p.by_page(i0 + k * NT)) : 0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * NT;
+      const bool in = id[k] >= 0 && id[k] < a.num_pages;
+      const int row = id[k] * a.page_size + (i - p.by_page(i) * a.page_size);
+      good &= in || i >= n;
+      pos[k] = in && i < n && a.pos ? __ldcg(a.pos + row) : i * a.C + r;
+      w[k] = in && i < n ? __ldcg(a.weights + row) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * NT;
+      const bool safe = pos[k] < a.keep_below || (a.keep_from && pos[k] >= start);
+      if (i < n && i < p.cached) s_key[i] = safe ? kProtected : weight_key(w[k]);
+    }
+    return good;
+  };
   int moves = bad_len ? -1 : 0;
   if (m > 0 && m < n) {
     if (tid == 0) {
@@ -81,10 +178,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const SelectParams p) 
     for (int i = tid; i < 256; i += NT) s_hist[i] = 0;
     __syncthreads();
     bool bad = false;
-    for (int i = tid; i < n; i += NT) {
-      bad |= pool_row(i) < 0;
-      if (i < p.cached) s_key[i] = read_key(i);
-    }
+    for (int i = tid; i < n; i += kBatch * NT) bad |= !load_keys(i);
     if (bad) s_bad = 1;
     __syncthreads();
     for (int shift = 24; shift >= 0; shift -= 8) {
@@ -206,42 +300,50 @@ struct MoveParams {
   int splits;  // blocks that share a pair
 };
 
-// A warp a move: both rows' pieces are loaded before the first store.  Sources
-// are rows behind the new length and destinations before it, so no move reads
-// what another writes.
+// A warp a move: both rows' pieces are loaded before the first store, and the rows
+// of its next moves are known before (a lane reads those of one).  Sources are rows behind
+// the new length and destinations before it, so no move reads what another writes.
 __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveParams p) {
   const MoveArgs& a = p.a;
   const int pair = blockIdx.x / p.splits, part = blockIdx.x - pair * p.splits;
   const int lane = threadIdx.x & 31, warp = part * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const int step = p.splits * (kMoveThreads / 32);
   wait_for_earlier_kernels();
-  const int n = min(a.count[pair], a.max_moves);
+  const int n = min(__ldcg(a.count + pair), a.max_moves);
   const int vec = a.row_bytes / 16;
-  for (int j = warp; j < n; j += p.splits * (kMoveThreads / 32)) {
-    const long long at = (long long)pair * a.max_moves + j;
-    const int from = a.src[at], to = a.dst[at];
-    if (from < 0 || to < 0 || from >= a.pool_rows || to >= a.pool_rows) continue;
-    const uint4* k0 = static_cast<const uint4*>(a.k) + (long long)from * vec;
-    uint4* k1 = static_cast<uint4*>(a.k) + (long long)to * vec;
-    const uint4* v0 = a.v ? static_cast<const uint4*>(a.v) + (long long)from * vec : nullptr;
-    uint4* v1 = a.v ? static_cast<uint4*>(a.v) + (long long)to * vec : nullptr;
-    uint32_t word = 0;
-    if (lane < 3 && a.words[lane]) word = __ldcg(a.words[lane] + from);
-    for (int c0 = lane; c0 < vec; c0 += 128) {
-      uint4 x[4], y[4];
+  for (int j0 = warp; j0 < n; j0 += 32 * step) {
+    const int mine = j0 + lane * step;
+    const long long at = (long long)pair * a.max_moves + mine;
+    const int src = mine < n ? __ldcg(a.src + at) : -1, dst = mine < n ? __ldcg(a.dst + at) : -1;
+    const bool good = src >= 0 && dst >= 0 && src < a.pool_rows && dst < a.pool_rows;
+    if (good) {  // the words a row has beside its pieces
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c0 + 32 * i < vec) {
-          x[i] = __ldcg(k0 + c0 + 32 * i);
-          if (v0) y[i] = __ldcg(v0 + c0 + 32 * i);
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c0 + 32 * i < vec) {
-          k1[c0 + 32 * i] = x[i];
-          if (v0) v1[c0 + 32 * i] = y[i];
-        }
+      for (int k = 0; k < 3; ++k)
+        if (a.words[k]) a.words[k][dst] = __ldcg(a.words[k] + src);
     }
-    if (lane < 3 && a.words[lane]) a.words[lane][to] = word;
+    for (unsigned left = __ballot_sync(0xffffffffu, good); left; left &= left - 1) {
+      const int k = __ffs(left) - 1;
+      const long long from = __shfl_sync(0xffffffffu, src, k), to = __shfl_sync(0xffffffffu, dst, k);
+      const uint4* k0 = static_cast<const uint4*>(a.k) + from * vec;
+      uint4* k1 = static_cast<uint4*>(a.k) + to * vec;
+      const uint4* v0 = a.v ? static_cast<const uint4*>(a.v) + from * vec : nullptr;
+      uint4* v1 = a.v ? static_cast<uint4*>(a.v) + to * vec : nullptr;
+      for (int c0 = lane; c0 < vec; c0 += 128) {
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + 32 * i < vec) {
+            x[i] = __ldcg(k0 + c0 + 32 * i);
+            if (v0) y[i] = __ldcg(v0 + c0 + 32 * i);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + 32 * i < vec) {
+            k1[c0 + 32 * i] = x[i];
+            if (v0) v1[c0 + 32 * i] = y[i];
+          }
+      }
+    }
   }
 }
 
@@ -354,12 +456,13 @@ cudaError_t select_nt(const SelectParams& p, cudaStream_t s) {
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s) {
   const long long most = (long long)a.max_pages * a.page_size;  // rows of a pair
+  if (most <= kRankRows) return launch_early(evict_rank_kernel, (unsigned)(a.B * a.C), kRankRows, 0, s, 1, a, FastDiv(a.page_size));
   const SelectParams p = {a, FastDiv(a.page_size), (int)(most < 48 * 1024 ? most : 48 * 1024)};
   return most <= 2048 ? select_nt<256>(p, s) : select_nt<1024>(p, s);
 }
 
 cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t s) {
-  // some eight blocks an SM, as many as a pair has work for
+  // some eight blocks an SM, as many as a pair has work for (four: the same within 2 %)
   const int useful = (a.max_moves + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
   int splits = (152 * 8 + a.pairs - 1) / a.pairs;
   if (splits > useful) splits = useful;
