@@ -22,10 +22,9 @@ namespace {
 
 // ------------------------------------------------------------------ select
 
-// A pair's rows are ranked by a 32-bit key with the order of their weights; a
-// radix select over the key's four bytes finds the m-th largest, and a scan in
-// row order tells the rows equal to it apart and numbers the moves.  A block a
-// pair; the keys stay in shared memory (read from the pool again where they do not fit).
+// A pair's rows are ranked by a 32-bit key with the order of their weights: the
+// m-th largest key is found, and a scan in row order tells the rows equal to it
+// apart and numbers the moves.  A block a pair.
 constexpr uint32_t kProtected = 0xFFFFFFFFu;  // above +inf's key
 
 // Larger weight, larger key; equal weights (-0 and 0 too), equal keys; NaN below all.
@@ -35,77 +34,125 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Pairs of up to kRankRows rows: a row's place is the number of rows before it, counted
-// by its thread over all keys in shared memory.  One barrier, where the radix select has some
-// twenty (a step of 512 pairs of 264 rows: 22.7 us with its moves by the radix select).
-constexpr int kRankRows = 512;
-__global__ void __launch_bounds__(kRankRows) evict_rank_kernel(const EvictArgs a, const FastDiv by_page) {
-  __shared__ __align__(16) uint32_t s_key[kRankRows];
-  __shared__ int s_holes[kRankRows / 32], s_movers[kRankRows / 32];
-  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+// Pairs of up to R x 1,024 rows: the keys stay in registers, R of a thread (rows
+// tid, tid + NT, ...), and the m-th largest one is found bit by bit: it is the largest T
+// that at least m keys reach.  A bit is one count over the block and one barrier (512
+// pairs of 264 rows with their moves 22.7 -> 16.3 us against a radix select).
+constexpr int kBitThreads = 1024;
+template <int R>
+__global__ void __launch_bounds__(kBitThreads) evict_bits_kernel(const EvictArgs a, const FastDiv by_page) {
+  __shared__ int s_count[2][32], s_equal[R][32], s_holes[R][32], s_movers[R][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
   const int pair = blockIdx.x, b = pair % a.B, r = pair / a.B;
   wait_for_earlier_kernels();
-  const int page = by_page(i);
   // a row behind the pair's last reads its page's entry as far as the table goes, too
-  const int id = page < a.max_pages ? __ldcg(a.table + (long long)pair * a.max_pages + page) : -1;
+  int id[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int page = by_page(tid + k * nt);
+    id[k] = page < a.max_pages ? __ldcg(a.table + (long long)pair * a.max_pages + page) : -1;
+  }
   const int L = a.ctx_len[b], K = a.keep_len[b], start = a.keep_from ? a.keep_from[b] : 0;
   auto rows_of = [&](int len) { return len > r ? (len - r - 1) / a.C + 1 : 0; };
   const bool bad_len = L < 0 || K < 0 || rows_of(L) > (long long)a.max_pages * a.page_size;
   const int n = bad_len ? 0 : rows_of(L), m = bad_len ? 0 : min(n, rows_of(K));
-  const bool there = i < n, in = id >= 0 && id < a.num_pages;
-  const int row = id * a.page_size + (i - page * a.page_size);
-  uint32_t key = 0;
-  if (there && in) {
-    const float w = __ldcg(a.weights + row);
-    const int pos = a.pos ? __ldcg(a.pos + row) : i * a.C + r;
-    key = pos < a.keep_below || (a.keep_from && pos >= start) ? kProtected : weight_key(w);
+  uint32_t key[R];
+  int row[R];
+  bool outside = false;
+  {
+    float w[R];
+    int pos[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int i = tid + k * nt;
+      const bool in = id[k] >= 0 && id[k] < a.num_pages;
+      outside |= i < n && !in;
+      row[k] = id[k] * a.page_size + (i - by_page(i) * a.page_size);
+      pos[k] = in && i < n && a.pos ? __ldcg(a.pos + row[k]) : i * a.C + r;
+      w[k] = in && i < n ? __ldcg(a.weights + row[k]) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) key[k] = pos[k] < a.keep_below || (a.keep_from && pos[k] >= start) ? kProtected : weight_key(w[k]);
   }
-  s_key[i] = key;
-  const bool bad = __syncthreads_or(there && !in);
+  const bool bad = __syncthreads_or(outside);
   int32_t* src = a.src + (long long)pair * a.max_moves;
   int32_t* dst = a.dst + (long long)pair * a.max_moves;
   int moves = bad_len ? -1 : 0;
   if (m > 0 && m < n) {
-    // rows before this one in the order: larger keys, and equal ones of lower rows
-    int before = 0;
-    for (int j = 0; j < warp * 32; j += 4) {
-      const uint4 k = *reinterpret_cast<const uint4*>(s_key + j);
-      before += (k.x >= key) + (k.y >= key) + (k.z >= key) + (k.w >= key);
+    // keys that are at least t, of the whole block
+    int turn = 0;
+    auto reach = [&](uint32_t t) {
+      int c = 0;
+#pragma unroll
+      for (int k = 0; k < R; ++k) c += tid + k * nt < n && key[k] >= t;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) s_count[turn][warp] = c;
+      __syncthreads();
+      c = __reduce_add_sync(0xffffffffu, lane < warps ? s_count[turn][lane] : 0);
+      turn ^= 1;  // the next count writes where nobody reads any more after its barrier
+      return c;
+    };
+    uint32_t mth = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t t = mth | (1u << bit);
+      if (reach(t) >= m) mth = t;
     }
-    for (int j = 0; j < 32; ++j) {
-      const uint32_t k = s_key[warp * 32 + j];
-      before += j < lane ? k >= key : k > key;
-    }
-    for (int j = warp * 32 + 32; j < n; j += 4) {  // rows behind the last one have key 0: not larger
-      const uint4 k = *reinterpret_cast<const uint4*>(s_key + j);
-      before += (k.x > key) + (k.y > key) + (k.z > key) + (k.w > key);
-    }
-    const bool stay = there && before < m;
-    const unsigned h = __ballot_sync(0xffffffffu, there && !stay && i < m), v = __ballot_sync(0xffffffffu, stay && i >= m);
-    if (lane == 0) {
-      s_holes[warp] = __popc(h);
-      s_movers[warp] = __popc(v);
+    // of the rows equal to the m-th, the first `need` stay
+    const int need = m - (mth == 0xFFFFFFFFu ? 0 : reach(mth + 1));
+    const unsigned below = (1u << lane) - 1;
+    unsigned eq[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      eq[k] = __ballot_sync(0xffffffffu, tid + k * nt < n && key[k] == mth);
+      if (lane == 0) s_equal[k][warp] = __popc(eq[k]);
     }
     __syncthreads();
-    int hole = __popc(h & ((1u << lane) - 1)), mover = __popc(v & ((1u << lane) - 1));
-    for (int w = 0; w < kRankRows / 32; ++w) {
-      if (w < warp) {
-        hole += s_holes[w];
-        mover += s_movers[w];
+    // a count's running sum over the rows before this warp's of slice k, and its total
+    auto before = [&](int (&count)[R][32], int (&first)[R]) {
+      int total = 0;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const int c = lane < warps ? count[k][lane] : 0;
+        first[k] = total + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+        total += __reduce_add_sync(0xffffffffu, c);
       }
-      moves += s_holes[w];
+      return total;
+    };
+    int first[R];
+    before(s_equal, first);
+    unsigned holes[R], movers[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int i = tid + k * nt;
+      const bool equal = i < n && key[k] == mth;
+      const bool stay = i < n && (equal ? first[k] + __popc(eq[k] & below) < need : key[k] > mth);
+      holes[k] = __ballot_sync(0xffffffffu, i < n && !stay && i < m);
+      movers[k] = __ballot_sync(0xffffffffu, stay && i >= m);
+      if (lane == 0) {
+        s_holes[k][warp] = __popc(holes[k]);
+        s_movers[k][warp] = __popc(movers[k]);
+      }
     }
+    __syncthreads();
+    int hole[R], mover[R];
+    moves = before(s_holes, hole);
+    before(s_movers, mover);
     if (bad || moves > a.max_moves) {
       moves = -1;
     } else {
-      if (h >> lane & 1) dst[hole] = row;
-      if (v >> lane & 1) src[mover] = row;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (holes[k] >> lane & 1) dst[hole[k] + __popc(holes[k] & below)] = row[k];
+        if (movers[k] >> lane & 1) src[mover[k] + __popc(movers[k] & below)] = row[k];
+      }
     }
   }
-  for (int x = max(moves, 0) + i; x < a.max_moves; x += kRankRows) src[x] = dst[x] = -1;
-  if (i == 0) a.count[pair] = moves;
+  for (int x = max(moves, 0) + tid; x < a.max_moves; x += nt) src[x] = dst[x] = -1;
+  if (tid == 0) a.count[pair] = moves;
 }
 
+// Longer pairs: a radix select over the key's four bytes, the keys in shared memory (read
+// from the pool again where they do not fit).
 struct SelectParams {
   EvictArgs a;
   FastDiv by_page;
@@ -456,9 +503,14 @@ cudaError_t select_nt(const SelectParams& p, cudaStream_t s) {
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s) {
   const long long most = (long long)a.max_pages * a.page_size;  // rows of a pair
-  if (most <= kRankRows) return launch_early(evict_rank_kernel, (unsigned)(a.B * a.C), kRankRows, 0, s, 1, a, FastDiv(a.page_size));
-  const SelectParams p = {a, FastDiv(a.page_size), (int)(most < 48 * 1024 ? most : 48 * 1024)};
-  return most <= 2048 ? select_nt<256>(p, s) : select_nt<1024>(p, s);
+  const unsigned pairs = (unsigned)(a.B * a.C);
+  const FastDiv by_page(a.page_size);
+  if (most <= kBitThreads) return launch_early(evict_bits_kernel<1>, pairs, (unsigned)(most + 31) / 32 * 32, 0, s, 1, a, by_page);
+  if (most <= 4 * kBitThreads) return launch_early(evict_bits_kernel<4>, pairs, kBitThreads, 0, s, 1, a, by_page);
+  // longer ones: a radix select over shared memory (at 4,096 rows the bits are faster: eight
+  // prompts with their moves 44 us against 58)
+  const SelectParams p = {a, by_page, (int)(most < 48 * 1024 ? most : 48 * 1024)};
+  return select_nt<1024>(p, s);
 }
 
 cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t s) {

@@ -228,7 +228,8 @@ def chosen(p, keep, w, pos, below, start, most):
 @pytest.mark.parametrize("kind", ["spread", "ties", "zeros", "special", "negative"])
 @pytest.mark.parametrize("C,ctx,keep,page", [
     (1, [1, 2, 70], [1, 1, 64], 64), (2, [300, 0, 129, 64], [100, 5, 200, 0], 64), (3, [2112] * 5, [2048] * 5, 192),
-    (8, [5000, 700], [512, 699], 64), (1, [70000], [333], 64)])
+    (8, [5000, 700], [512, 699], 64), (1, [70000], [333], 64), (1, [3000, 1025, 4000], [1000, 1024, 3999], 64),
+    (2, [9000, 130], [100, 129], 128)])
 def test_evict_select(cp, kind, C, ctx, keep, page):
     p = Pool(cp, C, ctx, (64,), page, seed=C + len(ctx))
     rng = np.random.default_rng(4)
@@ -454,3 +455,129 @@ def test_rotate_attend_weigh_evict(cp, C):
                 m[key] = [m[key][new_rows[i]] for i in range(keep[b])]
             have[b] = keep[b]
     assert max(have) <= room + 1
+
+
+# ------------------------------------------------------------------ streams, graphs, waits
+
+def replay(fn, *reset):
+    """fn captured and replayed once, after `reset` is put back."""
+    keep = [x.clone() for x in reset]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fn()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            out = fn()
+        for x, y in zip(reset, keep):
+            x.copy_(y)
+        g.replay()
+    side.synchronize()
+    return out
+
+
+def test_weights_and_eviction_replayed(cp):
+    """Captured calls give the eager ones' results bit for bit."""
+    ctx, C, Hq, Hkv, D = [700, 300], 2, 8, 2, 128
+    p = Pool(cp, C, ctx, (Hkv, D))
+    q, lse = randn(gen(2), (2, Hq, D)), torch.full((2, Hq), 5.0, device=DEV)
+    w0 = p.w.clone()
+    run = lambda: cp.cp_decode_weights(p.plan, p.pages, cp.CP_DECODE_GQA, q, p.k, lse, p.w)  # noqa: E731
+    want = run().clone()
+    p.w.copy_(w0)
+    assert torch.equal(replay(run, p.w), want)
+    new, pre = [300, 5], [40, 0]
+    plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, new, pre, device=DEV)
+    qq, kk = randn(gen(3), (305, Hq, D)), randn(gen(4), (345, Hkv, D))
+    ll = cp.cp_prefill_attn(plan, qq, kk, kk)[1]
+    want = cp.cp_prefill_weights(plan, qq, kk, ll)
+    assert torch.equal(replay(lambda: cp.cp_prefill_weights(plan, qq, kk, ll)), want)
+    old, keep = i32(ctx), i32([100, 300])
+    at, free = i32([20]), torch.full((30,), -5, **I32)
+    k0, t0 = p.k.clone(), p.pages.dev.clone()
+
+    def step():
+        src, dst, count = cp.cp_evict_select(p.pages, C, old, keep, p.w, 60)
+        cp.cp_cache_move(src, dst, count, p.k, p.v)
+        return src, dst, count, cp.cp_page_release(p.pages, C, old, keep, free, at)
+
+    v0 = p.v.clone()
+    want = [x.clone() for x in step()] + [p.k.clone(), p.v.clone(), p.pages.dev.clone(), free.clone()]
+    for x, y in ((p.k, k0), (p.v, v0), (p.pages.dev, t0)):
+        x.copy_(y)
+    free.fill_(-5)
+    got = list(replay(step, p.k, p.v, p.pages.dev, free)) + [p.k, p.v, p.pages.dev, free]
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
+def test_weights_on_two_streams(cp):
+    """Two prompts' weights at once, each with a workspace of its own."""
+    jobs = []
+    for seed, new in ((1, [900, 70]), (2, [33, 500, 1])):
+        plan = cp.cp_shard_plan(cp.CP_INTERLEAVE, 3, new, device=DEV)
+        q, k = randn(gen(seed), (sum(new), 8, 64)), randn(gen(seed + 5), (sum(new), 2, 64))
+        lse = cp.cp_prefill_attn(plan, q, k, k)[1]
+        jobs.append((plan, q, k, lse, cp.cp_prefill_weights(plan, q, k, lse)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        got = []
+        for s, (plan, q, k, lse, _) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                got.append(cp.cp_prefill_weights(plan, q, k, lse))
+        torch.cuda.synchronize()
+        for g, j in zip(got, jobs):
+            assert torch.equal(g, j[4])
+
+
+@pytest.mark.parametrize("kind", ["prompt", "short", "step", "latent"])
+def test_weights_wait_that_runs_out(cp, monkeypatch, kind):
+    """The issuer waits for a barrier that nothing arrives at: the kernel gives up,
+    drains and returns, and the next call is right."""
+    if kind in ("prompt", "short"):
+        new = [6000 if kind == "prompt" else 90]
+        plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, new, device=DEV)
+        q, k = randn(gen(1), (new[0], 4, 64)), randn(gen(2), (new[0], 2, 64))
+        lse = cp.cp_prefill_attn(plan, q, k, k)[1]
+        run = lambda: cp.cp_prefill_weights(plan, q, k, lse)  # noqa: E731
+    else:
+        p = Pool(cp, 2, [700, 300], (576,) if kind == "latent" else (2, 64), dtype=torch.float8_e4m3fn if kind == "latent" else torch.bfloat16)
+        q, lse = randn(gen(2), (2, 8, 576 if kind == "latent" else 64)), torch.full((2, 8), 9.0, device=DEV)
+        mode = cp.CP_DECODE_MLA if kind == "latent" else cp.CP_DECODE_GQA
+        run = lambda: cp.cp_decode_weights(p.plan, p.pages, mode, q, p.k, lse, torch.zeros_like(p.w), scale_pool=p.scale, sm_scale=0.05)  # noqa: E731
+    cp.cp_device_error_check()
+    want = run()
+    monkeypatch.setenv("CPATTN_TEST_STALL", "1")
+    run()
+    with pytest.raises(cp.CpError) as ei:
+        cp.cp_device_error_check()
+    assert ei.value.status == -4
+    monkeypatch.delenv("CPATTN_TEST_STALL")
+    assert torch.equal(run(), want)
+    cp.cp_device_error_check()
+
+
+def test_weights_and_moves_past_31_bits(cp):
+    """A pool whose last rows lie behind 2^31 elements."""
+    page, row = 64, (8, 128)
+    num = 2**31 // (1024 * page) + 2
+    k = torch.zeros((num * page, *row), dtype=torch.bfloat16, device=DEV)
+    table = np.array([[0, num - 1]], np.int32)
+    pages = cp.PageTable(table, page, num, device=DEV)
+    k[-page:] = randn(gen(1), (page, *row))
+    last = k[-page:].clone()
+    q, lse, w = randn(gen(2), (1, 8, 128)), torch.full((1, 8), 3.0, device=DEV), torch.zeros(num * page, device=DEV)
+    plan = cp.cp_decode_plan(1, [100], device=DEV)
+    cp.cp_decode_weights(plan, pages, cp.CP_DECODE_GQA, q, k, lse, w)
+    cp.cp_device_error_check()
+    x = torch.einsum("hd,khd->kh", q[0].double(), last.double()) / math.sqrt(128) - 3
+    want = x.exp().sum(1)[:36]
+    size = float(torch.einsum("hd,khd->kh", q[0].double().abs(), last.double().abs()).max()) / math.sqrt(128)
+    assert ((w[-page:-page + 36].double() - want).abs() <= (2.0**-18 + 2.0**-20 * size) * want).all()
+    w[:] = 0
+    w[-page:-page + 36] = 1
+    src, dst, count = cp.cp_evict_select(pages, 1, i32([100]), i32([36]), w, 36)
+    assert count.item() == 36 and src[0, 0].item() == (num - 1) * page and dst[0, 35].item() == 35
+    cp.cp_cache_move(src, dst, count, k, weights=w)
+    assert torch.equal(k[:36], last[:36]) and bool((w[:36] == 1).all())

@@ -234,3 +234,37 @@ def test_prefix_refusals(cp):
         cp.cp_prefix_attn(host_only, c.q, c.sk, c.sv)
     with pytest.raises(cp.CpError, match="scale"):
         cp.cp_prefix_attn(c.plan, c.q, c.sk, c.sv, sm_scale=0.0)
+
+
+@pytest.mark.parametrize("kv,D,members", [("bf16", 128, 70), ("bf16", 64, 9), ("fp8", 128, 9), ("fp8", 128, 70)])
+def test_prefix_wait_that_runs_out(cp, monkeypatch, kv, D, members):
+    """The issuer waits for a barrier that nothing arrives at: the kernel gives up,
+    drains and returns, and the next call is right."""
+    c = Case(cp, 2, [700], [members], 16, 4, D, kv, workers=6)
+    cp.cp_device_error_check()
+    monkeypatch.setenv("CPATTN_TEST_STALL", "1")
+    c.run()
+    with pytest.raises(cp.CpError) as ei:
+        cp.cp_device_error_check()
+    assert ei.value.status == -4
+    monkeypatch.delenv("CPATTN_TEST_STALL")
+    o, lse = c.run()
+    cp.cp_device_error_check()
+    c.check(o, lse)
+
+
+def test_prefix_of_a_long_cache(cp):
+    """K and V past 2^31 elements: the last rows are the ones that are read last."""
+    P, Hq, Hkv, D = 2**31 // (8 * 128) + 300, 8, 8, 128
+    g = gen(1)
+    k, v = torch.zeros((P, Hkv, D), dtype=torch.bfloat16, device=DEV), torch.zeros((P, Hkv, D), dtype=torch.bfloat16, device=DEV)
+    q = torch.ones((2, Hq, D), dtype=torch.bfloat16, device=DEV)
+    k[-200:] = 4.0  # these take all of the weight
+    v[-200:] = randn(g, (200, Hkv, D))
+    plan = cp.cp_prefix_plan(1, [P], [2], Hq, Hkv, device=DEV)
+    o, lse = cp.cp_prefix_attn(plan, q, [k], [v], sm_scale=0.1, out_dtype=torch.float32)
+    cp.cp_device_error_check()
+    want = v[-200:].double().mean(0)
+    # the other rows' weight: 2^21 e^-51.2, under 2^-52; P = 1 is exact, V's sums are fp32
+    assert ((o.double() - want).abs() <= 2.0**-20 * v[-200:].double().abs().mean(0) + 2.0**-22).all()
+    assert ((lse.double() - (51.2 + math.log(200))).abs() <= 2.0**-20 * 60).all()
