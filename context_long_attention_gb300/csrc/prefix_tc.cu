@@ -23,9 +23,12 @@
 // half of its own S columns.  The running max moves only when a row's max grows by
 // more than 2^8; any running max gives the exact result (O = sum e^(s-m) v / sum e^(s-m)).
 // P is rounded to bf16 for its product, its sum is not.
-// E4M3 (F8): the ring holds the codes as bf16 (exact), three slots (four where one Q tile
-// leaves room, so that K is a step ahead) behind a ring of four code tiles; warps 18-21 convert and take the relay's part.  A token's scale multiplies its
-// column of S and, once P's sum is taken, of P.
+// E4M3 (F8): S multiplies K's codes as they are stored, with the queries as two E4M3
+// numbers each, hi + lo of the row times a power of two that brings its largest element
+// to [128, 256) (4 + 4 significant bits hold bf16's 8, down to 2^-17 of the largest); warps
+// 18-21 turn V's codes into bf16 (exact) and take the relay's part, since P needs the
+// range that bf16 has.  A token's scale multiplies its column of S and, once P's sum is
+// taken, of P.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,16 +51,17 @@ constexpr int kWarpTma = kSoftmaxWarps, kWarpMma = kSoftmaxWarps + 1, kWarpRelay
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
 
-template <int D, bool F8, bool WIDE = true>
+template <int D, bool F8>
 struct Cfg {
   static constexpr int kChunks = D / 64;
-  static constexpr int kQBytes = BM * D * 2;
+  static constexpr int kQBytes = BM * D * 2;    // (E4M3: hi, then lo)
   static constexpr int kSlotBytes = BN * D * 2;
-  static constexpr int kSlots = F8 ? (WIDE ? 3 : 4) : D == 128 ? 5 : 10;
-  static constexpr int kRing = (F8 && !WIDE ? 1 : 2) * kQBytes;  // where the ring begins
-  static constexpr int kCodeSlots = F8 ? 4 : 0, kCodeBytes = BN * D;
+  static constexpr int kSlots = F8 ? 2 : D == 128 ? 5 : 10;  // of the K/V ring (E4M3: of V as bf16)
+  static constexpr int kRing = 2 * kQBytes;
+  // E4M3: rings of code tiles behind it
+  static constexpr int kKSlots = 3, kVSlots = 2, kCodeBytes = BN * D;
   static constexpr int kCodes = kRing + kSlots * kSlotBytes;
-  static constexpr int kTiles = kCodes + kCodeSlots * kCodeBytes;
+  static constexpr int kTiles = kCodes + (F8 ? (kKSlots + kVSlots) * kCodeBytes : 0);
   static constexpr int kThreads = 32 * (kSoftmaxWarps + (F8 ? 6 : 3));
   static constexpr int kRelays = F8 ? 4 : 1;  // arrivals of the relay's part
 };
@@ -109,6 +113,36 @@ __device__ __forceinline__ void bf16_of_codes(uint32_t codes, uint32_t& lo, uint
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(k));
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(k));
 }
+// Eight elements of a query row, whose 16 lanes stand side by side, as E4M3 hi and lo of
+// the row times 2^(7 - e), its largest magnitude in [2^e, 2^(e+1)); *inv = 2^(e - 7).
+__device__ __forceinline__ void put_codes(const uint4& x, uint8_t* row, int swizzle, int piece, float* inv) {
+  const uint32_t k = 0x7fff7fffu;  // magnitudes are ordered like their bits, two bf16 at a time
+  uint32_t m = __vmaxu2(__vmaxu2(x.x & k, x.y & k), __vmaxu2(x.z & k, x.w & k));
+  m = max(m & 0xffff0000u, m << 16);
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const int e = max(-100, (int)(m >> 23) - 127);
+  const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+  if (piece == 0) *inv = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float v0 = __uint_as_float(in[i] << 16) * f, v1 = __uint_as_float(in[i] & 0xffff0000u) * f;
+    uint16_t h, l;
+    uint32_t b;
+    float h0, h1;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(v1), "f"(v0));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
+    asm("{\n .reg .f16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}" : "=f"(h0), "=f"(h1) : "r"(b));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(v1 - h1), "f"(v0 - h0));
+    hi[i >> 1] |= (uint32_t)h << (16 * (i & 1));
+    lo[i >> 1] |= (uint32_t)l << (16 * (i & 1));
+  }
+  uint8_t* at = row + (((piece >> 1) ^ swizzle) << 4) + 8 * (piece & 1);
+  *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2*>(at + BM * 128) = make_uint2(lo[0], lo[1]);
+}
 __device__ __forceinline__ void mbar_inval(uint32_t bar) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
 
 __device__ void report_timeout(unsigned* status, unsigned site, volatile int* abort) {
@@ -134,9 +168,9 @@ struct Walk {
   }
 };
 
-struct Shared {
-  // E4M3: unit[0..3] code tiles landed, unit[4..7] code tiles read, rel[4..6] a tile's scales
-  // written, rel[8] K_0 converted
+struct alignas(16) Shared {
+  // E4M3: unit[0..2] K tiles landed, unit[3..4] V tiles landed, unit[5..6] V tiles converted,
+  // rel[4..6] a tile's scales written
   uint64_t bar_unit[10], bar_rel[10], bar_s[2], bar_p[2], bar_o[2], bar_never, bar_drain;
   uint32_t tmem_slot;
   volatile int abort_flag;
@@ -144,22 +178,26 @@ struct Shared {
   int32_t tile_off[CP_MAX_SHARDS + 2];
   int32_t rows[CP_MAX_SHARDS], row_off[CP_MAX_SHARDS];
   cp_prefix_item item;
-  alignas(16) float scale[3][BN];  // read in pieces of four; E4M3: the tokens' scales of the last three tiles
+};
+struct alignas(16) Scales {  // behind Shared, for an E4M3 cache only
+  float scale[3][BN];  // the tokens' of the last three tiles, read in pieces of four
+  float inv[2 * BM];   // what undoes the rows' powers of two
 };
 
 template <int D, bool WIDE, int MAXC, bool F8>
 __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Shared& sh, uint8_t* sQ,
                                         uint32_t tmem) {
-  using C = Cfg<D, F8, WIDE>;
-  static_assert(C::kCodes == Cfg<D, F8>::kCodes, "one place of the code tiles");
+  using C = Cfg<D, F8>;
   uint8_t* sKV = sQ + C::kRing;
   constexpr int kUnitBars = C::kSlots;
+  constexpr int kRels = F8 ? 3 : C::kSlots;  // barriers of the releases
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
   // a half row's P sum that can hide a P above 2^8
   constexpr float kSpecSum = NC * 256.f;
   const PrefixArgs& a = p.a;
   const cp_prefix_item& it = sh.item;
+  Scales& sc = *reinterpret_cast<Scales*>(&sh + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nK = it.tile_end - it.tile_begin;
   volatile int* abort = &sh.abort_flag;
@@ -185,7 +223,10 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       tmem_ld_wait();
       return __uint_as_float(o);
     };
-    const float sl2 = p.scale_log2;
+    // rows of the block in use by this warp (a single chain's block may leave quarters empty)
+    const bool idle = !WIDE && quarter * 32 >= it.m_rows;
+    const float inv_row = F8 ? sc.inv[row] : 1.f;
+    const float sl2 = p.scale_log2 * inv_row;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true, first = true;  // first: no key of this chain so far
     int keys = 0;                  // of this half's columns, those in use in this tile
@@ -241,10 +282,19 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       bool got = mbar_wait(smem_u32(&sh.bar_s[t]), j & 1, p.wait_ns, abort);
       if constexpr (F8) {
         got = got && mbar_wait(smem_u32(&sh.bar_rel[4 + j % 3]), (j / 3) & 1, p.wait_ns, abort);
-        scales = sh.scale[j % 3] + (WIDE ? 0 : 64 * t) + NC * half;
+        scales = sc.scale[j % 3] + (WIDE ? 0 : 64 * t) + NC * half;
       }
       got = __all_sync(0xffffffffu, got);
-      if (got && releaser && lane == 0) mbar_arrive(smem_u32(&sh.bar_rel[j % C::kSlots]));
+      if (idle) {  // no row of the block: O of these lanes is never read; no votes
+        if (!got) {
+          if (lane == 0) report_timeout(p.status, 1, abort);
+          ok = false;
+          break;
+        }
+        mbar_arrive(smem_u32(&sh.bar_p[t]));
+        continue;
+      }
+      if (got && releaser && lane == 0) mbar_arrive(smem_u32(&sh.bar_rel[j % kRels]));
       tc_fence_after();
       uint32_t sr[NC], pk[NC / 2];
       float part = 0.f;
@@ -376,7 +426,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
             out[row * (D / 4) + (piece ^ (i & 7))] = make_float4(x[0], x[1], x[2], x[3]);
           }
         }
-        if (half == 0) out_lse[row] = m_used * a.sm_scale + logf(lt);
+        if (half == 0) out_lse[row] = m_used * (a.sm_scale * inv_row) + logf(lt);
         // ... and from there whole rows at a time to global memory: the two warps of these
         // 32 rows take every other one
         named_bar_sync(pbar, 64);
@@ -447,30 +497,45 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
     };
     if constexpr (F8) {
-      // load u = 2j (K_j) or 2j + 1 (V_j) goes to code slot u % 4
       uint8_t* codes = sQ + C::kCodes;
       locate();
-      int last = 0;  // K_0: loaded before the block's barrier
-      for (int u = 1; u < 2 * nK; ++u) {
-        const int s = u & 3;
-        if (u >= 4 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_unit[4 + s]), ((u >> 2) - 1) & 1, p.wait_ns, abort))) {
-          if (lane == 0) report_timeout(p.status, 4, abort);
-          break;
-        }
+      int nk = 1, nv = 0;  // tiles loaded (K_0 before the block's barrier)
+      int v0 = y0, v1 = y1, vr = yr;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, abort))) return true;
+        if (lane == 0) report_timeout(p.status, 4, abort);
+        return false;
+      };
+      for (int j = 0; j < nK; ++j) {  // V_j, then K_(j+1)
+        if (nv >= C::kVSlots && !wait_all(&sh.bar_unit[5 + nv % C::kVSlots], (nv / C::kVSlots - 1) & 1)) break;
         if (elect_one()) {
-          const uint32_t full = smem_u32(&sh.bar_unit[s]);
+          const uint32_t full = smem_u32(&sh.bar_unit[3 + nv % C::kVSlots]);
           mbar_expect_tx(full, C::kCodeBytes);
-          load(u & 1 ? &maps.v[yr] : &maps.k[yr], y0, y1, smem_u32(codes + s * C::kCodeBytes), full);
+          load(&maps.v[vr], v0, v1, smem_u32(codes + (C::kKSlots + nv % C::kVSlots) * C::kCodeBytes), full);
         }
         __syncwarp();
-        last = u;
-        if ((u & 1) && u + 1 < 2 * nK) {
-          w.next();
-          locate();
+        ++nv;
+        if (nk == nK) continue;
+        w.next();
+        locate();
+        v0 = y0;
+        v1 = y1;
+        vr = yr;
+        // K_(nk - 3) is read once S_(nk - 3) is complete
+        if (nk >= C::kKSlots && !wait_all(&sh.bar_rel[(nk - C::kKSlots) % 3], ((nk - C::kKSlots) / 3) & 1)) break;
+        if (elect_one()) {
+          const uint32_t full = smem_u32(&sh.bar_unit[nk % C::kKSlots]);
+          mbar_expect_tx(full, C::kCodeBytes);
+          load(&maps.k[yr], y0, y1, smem_u32(codes + nk % C::kKSlots * C::kCodeBytes), full);
         }
+        __syncwarp();
+        ++nk;
       }
       // never leave with a copy in flight: the last fill of every slot
-      for (int u = max(0, last - 3); u <= last; ++u) mbar_wait(smem_u32(&sh.bar_unit[u & 3]), (u >> 2) & 1, 1000000000ull, &sh.zero_flag);
+      for (int u = max(0, nk - C::kKSlots); u < nk; ++u)
+        mbar_wait(smem_u32(&sh.bar_unit[u % C::kKSlots]), (u / C::kKSlots) & 1, 1000000000ull, &sh.zero_flag);
+      for (int u = max(0, nv - C::kVSlots); u < nv; ++u)
+        mbar_wait(smem_u32(&sh.bar_unit[3 + u % C::kVSlots]), (u / C::kVSlots) & 1, 1000000000ull, &sh.zero_flag);
       __syncwarp();
       return;
     }
@@ -517,34 +582,39 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       mbar_wait(smem_u32(&sh.bar_unit[k % kUnitBars]), (k / kUnitBars) & 1, 1000000000ull, &sh.zero_flag);
     __syncwarp();
   } else if (F8 && warp >= kWarpRelay) {
-    // ------------------------------------------------------------ E4M3 to bf16 (a thread a row)
+    // ------------------------------------------------------------ V's codes to bf16 (a thread a row)
     bool ok = true;
     const int row = (warp - kWarpRelay) * 32 + lane;
-    uint8_t* codes = sQ + C::kCodes;
+    uint8_t* codes = sQ + C::kCodes + C::kKSlots * C::kCodeBytes;
     Walk w(sh.tile_off, it.tile_begin);
-    for (int u = 0; u < 2 * nK && ok; ++u) {
-      const int j = u >> 1;
-      const bool is_v = u & 1;
-      const int nv = sh.rows[w.r] - (w.t - w.off[w.r]) * BN;  // keys of tile j from its first row on
+    auto scale_of = [&]() -> float {  // of this row of tile w.t; 0 behind the shard's last key
+      const int in_pair = (w.t - w.off[w.r]) * BN + row, pair = w.r * a.R + it.group;
+      if (in_pair >= sh.rows[w.r]) return 0.f;
+      return __ldcg(a.sc.p[w.r] + (a.rm.table ? map_row(a.rm, pair, 0, in_pair) : (long long)sh.row_off[w.r] + in_pair));
+    };
+    auto put_scale = [&](int j, float x) {
+      sc.scale[j % 3][row] = x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.bar_rel[4 + j % 3]));
+    };
+    put_scale(0, scale_of());
+    for (int j = 0; j < nK && ok; ++j) {
       float scale = 0.f;
-      if (!is_v && row < nv) {
-        const int in_pair = (w.t - w.off[w.r]) * BN + row, pair = w.r * a.R + it.group;
-        scale = __ldcg(a.sc.p[w.r] + (a.rm.table ? map_row(a.rm, pair, 0, in_pair) : (long long)sh.row_off[w.r] + in_pair));
+      if (j + 1 < nK) {
+        w.next();
+        scale = scale_of();
       }
-      if (is_v && j + 1 < nK) w.next();
-      ok = mbar_wait(smem_u32(&sh.bar_unit[u & 3]), (u >> 2) & 1, p.wait_ns, abort);
-      if (ok && u >= C::kSlots) {  // the slot's load u - kSlots is read: release r frees V_(r-1) and K_r
-        const int r = (u - C::kSlots + 1) >> 1;
-        ok = mbar_wait(smem_u32(&sh.bar_rel[r % C::kSlots]), (r / C::kSlots) & 1, p.wait_ns, abort);
-      }
+      // V_j has landed; its bf16 slot's V_(j-2) is read (release j - 1: S_(j-1) is complete)
+      ok = mbar_wait(smem_u32(&sh.bar_unit[3 + j % C::kVSlots]), (j / C::kVSlots) & 1, p.wait_ns, abort);
+      if (ok && j >= C::kSlots) ok = mbar_wait(smem_u32(&sh.bar_rel[(j - 1) % kRels]), ((j - 1) / kRels) & 1, p.wait_ns, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         if (lane == 0) report_timeout(p.status, 5, abort);
         break;
       }
-      const uint4* src = reinterpret_cast<const uint4*>(codes + (u & 3) * C::kCodeBytes + row * 128);
-      uint8_t* dst = sKV + (u % C::kSlots) * C::kSlotBytes + row * 128;
-      // V's rows behind the shard's last key meet weights of 0: any finite value will do
+      const uint4* src = reinterpret_cast<const uint4*>(codes + j % C::kVSlots * C::kCodeBytes + row * 128);
+      uint8_t* dst = sKV + (j % C::kSlots) * C::kSlotBytes + row * 128;
+      // rows behind the shard's last key meet weights of 0: any finite value will do
 #pragma unroll 4
       for (int c = 0; c < 8; ++c) {
         const uint4 x = src[c ^ (row & 7)];
@@ -558,25 +628,21 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         *reinterpret_cast<uint4*>(chunk + ((unit ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(chunk + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      // K_j's slot was free: S_(j-2) is complete, so both chains are done with P_(j-3) and its scales
-      if (!is_v) sh.scale[j % 3][row] = scale;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&sh.bar_unit[4 + (u & 3)]));
-        if (!is_v) mbar_arrive(smem_u32(&sh.bar_rel[4 + j % 3]));
-        if (u == 0) mbar_arrive(smem_u32(&sh.bar_rel[8]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[5 + j % C::kVSlots]));
+      if (j + 1 < nK) {
+        // V_(j-2) was free: both chains are done with P_(j-2), whose scales these replace
+        put_scale(j + 1, scale);
+        ok = mbar_wait(smem_u32(&sh.bar_unit[(j + 1) % C::kKSlots]), ((j + 1) / C::kKSlots) & 1, p.wait_ns, abort);
       }
-      // V_j and K_(j+1) (if there is one) are in place: this warp's arrival on both chains' P_j
-      const int step = is_v ? j : j - 1;
-      if (is_v ? j + 1 == nK : j > 0) {
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (step > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_p[t]), (step - 1) & 1, p.wait_ns, abort));
-          if (ok && lane == 0) mbar_arrive(smem_u32(&sh.bar_p[t]));
-          __syncwarp();
-        }
-        if (!ok && lane == 0) report_timeout(p.status, 17, abort);
+      // V_j and K_(j+1) are in place: this warp's arrival on both chains' P_j
+      for (int t = 0; t < 2; ++t) {
+        if (j > 0) ok = ok && mbar_wait(smem_u32(&sh.bar_p[t]), (j - 1) & 1, p.wait_ns, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && lane == 0) mbar_arrive(smem_u32(&sh.bar_p[t]));
       }
+      if (!ok && lane == 0) report_timeout(p.status, 17, abort);
     }
   } else if (warp == kWarpRelay) {
     // ------------------------------------------------------------ relay
@@ -608,7 +674,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   } else {
     // ------------------------------------------------------------ MMA issuer
     constexpr unsigned kAll = 0xffffffffu;
-    const uint32_t idS = idesc_bf16_f32(BM, NS, 0, 0);
+    const uint32_t idS = F8 ? idesc_e4m3_f32(BM, NS, 0, 0) : idesc_bf16_f32(BM, NS, 0, 0);
     const uint32_t idPV = idesc_bf16_f32(BM, D, 0, 1);
     auto fail = [&](unsigned site) {
       if (lane == 0) report_timeout(p.status, site, abort);
@@ -619,22 +685,31 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     const uint64_t dQ0 = smem_desc(smem_u32(sQ), 16, 1024);
     const uint64_t dK0 = smem_desc(smem_u32(sKV), 16, 1024);
     const uint64_t dV0 = smem_desc(smem_u32(sKV), BN * 128, 1024);
-    auto issue_s = [&](int t, int u) {
+    auto issue_s = [&](int t, int j) {
       const uint64_t a0 = dQ0 + (uint64_t)((WIDE ? t * C::kQBytes : 0) >> 4);
-      // the chain's 64 keys are the tile's rows 64 t on: 8 KB into every 64-dim chunk
-      const uint64_t b0 = dK0 + (uint64_t)(((u % C::kSlots) * C::kSlotBytes + (WIDE ? 0 : t * 64 * 128)) >> 4);
+      // the chain's 64 keys are the tile's rows 64 t on: 8 KB into every chunk
+      const int chain = WIDE ? 0 : t * 64 * 128;
       if (elect_one()) {
+        if constexpr (F8) {  // hi, then lo, which stands behind it
+          const uint64_t b0 = dQ0 + (uint64_t)((C::kCodes + j % C::kKSlots * C::kCodeBytes + chain) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + t * 256, a0 + off, b0 + off, idS, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_f8(tmem + t * 256, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4), b0 + (((kk & 3) * 32) >> 4), idS, kk > 0);
+        } else {
+          const uint64_t b0 = dK0 + (uint64_t)((((2 * j) % C::kSlots) * C::kSlotBytes + chain) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + t * 256, a0 + off, b0 + off, idS, kk > 0);
+          }
         }
         mma_commit(smem_u32(&sh.bar_s[t]));
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int t, int u, bool acc) {
-      const uint64_t v0 = dV0 + (uint64_t)(((u % C::kSlots) * C::kSlotBytes + (WIDE ? 0 : t * 64 * 128)) >> 4);
+    auto issue_pv = [&](int t, int j, bool acc) {
+      const int slot = (F8 ? j : 2 * j + 1) % C::kSlots;
+      const uint64_t v0 = dV0 + (uint64_t)((slot * C::kSlotBytes + (WIDE ? 0 : t * 64 * 128)) >> 4);
       const uint32_t pa = tmem + t * 256, d = tmem + t * 256 + 128;
       if (elect_one()) {
         // P of a half's NC keys sits over the first NC / 2 of its NC columns
@@ -651,7 +726,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       fail(10);
       ok = false;
     }
-    if (ok && !wait_all(F8 ? &sh.bar_rel[8] : &sh.bar_unit[0], 0)) {
+    if (ok && !wait_all(&sh.bar_unit[0], 0)) {
       fail(12);
       ok = false;
     }
@@ -661,7 +736,6 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       issue_s(1, 0);
     }
     for (int j = 0; j < nK && ok; ++j) {
-      const int uV = 2 * j + 1, uK = 2 * j + 2;
       for (int t = 0; t < 2 && ok; ++t) {
         // V_j and K_(j+1) are in place once the chain's P_j has completed (the relay's arrival)
         if (!wait_all(&sh.bar_p[t], j & 1)) {
@@ -670,8 +744,8 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
           break;
         }
         tc_fence_after();
-        issue_pv(t, uV, j > 0);
-        if (j + 1 < nK) issue_s(t, uK);
+        issue_pv(t, j, j > 0);
+        if (j + 1 < nK) issue_s(t, j + 1);
       }
     }
     // never go on under a running product
@@ -683,7 +757,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
 
 // the tiles and what stands behind them: at most 227 KB a block
 template <int D, bool F8>
-constexpr int kSmem = Cfg<D, F8>::kTiles + (int)sizeof(Shared);
+constexpr int kSmem = Cfg<D, F8>::kTiles + (int)sizeof(Shared) + (F8 ? (int)sizeof(Scales) : 0);
 static_assert(kSmem<128, false> <= 232448 && kSmem<64, false> <= 232448 && kSmem<128, true> <= 232448, "shared memory");
 
 template <int D, int MAXC, bool F8>
@@ -723,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         uint64_t* b = reinterpret_cast<uint64_t*>(&sh) + lane;
         if (wi > w0) mbar_inval(smem_u32(b));
         const bool is_p = b == &sh.bar_p[0] || b == &sh.bar_p[1];
-        const bool four = F8 && ((b >= &sh.bar_unit[4] && b <= &sh.bar_unit[7]) || (b >= &sh.bar_rel[4] && b <= &sh.bar_rel[8]));
+        const bool four = F8 && (b == &sh.bar_unit[5] || b == &sh.bar_unit[6] || (b >= &sh.bar_rel[4] && b <= &sh.bar_rel[6]));
         mbar_init(smem_u32(b), is_p ? 2 * BM + C::kRelays : four ? 4 : 1);
         mbar_init_fence();
         fence_proxy_async_smem();
@@ -766,8 +840,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
           const int e = e0 + x * kStep, r = e / kPieces, c = e % kPieces;
-          if (e < count)
+          if (e >= count) continue;
+          if constexpr (F8) {
+            put_codes(val[x], sQ + (r >> 7) * C::kQBytes + (r & 127) * 128, r & 7, c, &reinterpret_cast<Scales*>(&sh + 1)->inv[r]);
+          } else {
             *reinterpret_cast<uint4*>(sQ + (r >> 7) * C::kQBytes + (c >> 3) * (BM * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = val[x];
+          }
         }
       }
       fence_proxy_async_smem();
