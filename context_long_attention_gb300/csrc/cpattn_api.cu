@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstdio>
 #include <cstring>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -703,6 +704,7 @@ cp_status run_decode_merged(const cp_plan_header& h, const int32_t* W, const voi
 
 // Work of one block's tile against its fixed work (query rows, the first tile's
 // fill, the result), in sixteenths of a tile of two 128-row M tiles.
+constexpr int kMaxPrefixWorkers = 65536;
 constexpr long long kPrefixItemCost = 64, kPrefixTile2 = 16, kPrefixTile1 = 14;
 
 cp_status build_prefix_plan(int C, int R, const int32_t* prefix_len, const int32_t* members, int layout, int Hq, int Hkv,
@@ -710,6 +712,7 @@ cp_status build_prefix_plan(int C, int R, const int32_t* prefix_len, const int32
   if (!members) return fail(CP_ERR_INVALID_ARG, "members is NULL");
   if (Hq < 1 || Hkv < 1 || Hq % Hkv) return fail(CP_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d", Hq, Hkv);
   if (layout == CP_DCP_SELECTED) return fail(CP_ERR_INVALID_ARG, "layout=%d: a prefix lies round robin or in contiguous chunks", layout);
+  if (n_workers > kMaxPrefixWorkers) return fail(CP_ERR_INVALID_ARG, "n_workers=%d, at most %d", n_workers, kMaxPrefixWorkers);
   int G = n_workers;
   if (G == 0) {
     const cp_status st = sm_count(&G);
@@ -757,7 +760,7 @@ cp_status build_prefix_plan(int C, int R, const int32_t* prefix_len, const int32
   int i = 0, t = 0;  // the walk: block and its next tile
   for (int w = 0; w < G; ++w) {
     worker_off[w] = (int)item.size();
-    const long long end = start[NB] * (w + 1) / G;
+    const long long end = (long long)((__int128)start[NB] * (w + 1) / G);  // costs x workers may pass 2^63
     while (i < NB) {
       const cp_prefix_block& b = block[i];
       const int nt = tile_off[(size_t)b.group * (C + 1) + C];
@@ -859,6 +862,16 @@ cp_status build_prefix_plan(int C, int R, const int32_t* prefix_len, const int32
   const int32_t info[4] = {Hq, Hkv, n_merge, merge_parts};
   memcpy(W + o.off_idx, info, sizeof(info));
   return CP_OK;
+}
+
+// No exception leaves the C interface.
+cp_status try_prefix_plan(int C, int R, const int32_t* prefix_len, const int32_t* members, int layout, int Hq, int Hkv,
+                          int n_workers, std::vector<int32_t>* out) {
+  try {
+    return build_prefix_plan(C, R, prefix_len, members, layout, Hq, Hkv, n_workers, out);
+  } catch (const std::bad_alloc&) {
+    return fail(CP_ERR_UNSUPPORTED, "the plan of %d groups does not fit the host's memory", R);
+  }
 }
 
 // Part slots of a call: with the caller's own parts every block goes through them.
@@ -1741,7 +1754,7 @@ cp_status cp_prefix_plan_size(int C, int R, const int32_t* prefix_len, const int
                               size_t* dev_bytes) {
   if (!host_bytes || !dev_bytes) return fail(CP_ERR_INVALID_ARG, "a size pointer is NULL");
   std::vector<int32_t> words;
-  const cp_status st = build_prefix_plan(C, R, prefix_len, members, layout, Hq, Hkv, n_workers, &words);
+  const cp_status st = try_prefix_plan(C, R, prefix_len, members, layout, Hq, Hkv, n_workers, &words);
   if (st != CP_OK) return st;
   *host_bytes = *dev_bytes = words.size() * 4;
   return ok();
@@ -1751,7 +1764,7 @@ cp_status cp_prefix_plan(int C, int R, const int32_t* prefix_len, const int32_t*
                          int Hq, int Hkv, int n_workers, void* host_plan, size_t host_bytes, void* dev_plan,
                          size_t dev_bytes, void* stream) {
   std::vector<int32_t> words;
-  cp_status st = build_prefix_plan(C, R, prefix_len, members, layout, Hq, Hkv, n_workers, &words);
+  cp_status st = try_prefix_plan(C, R, prefix_len, members, layout, Hq, Hkv, n_workers, &words);
   if (st != CP_OK) return st;
   st = copy_plan(words, host_plan, host_bytes, dev_plan, dev_bytes, words.size() * 4, (cudaStream_t)stream);
   return st == CP_OK ? ok() : st;

@@ -692,7 +692,7 @@ cp_status cp_rope(int T, const int32_t* pos, const uint64_t* turns, int rot, int
  * q [N, Hq, D]; kv_dtype, shard_k, shard_v, shard_scale, head dims and pools as
  * for CP_DECODE_GQA.  On the tensor cores: bf16 with D = 64 or 128 and E4M3 with
  * D = 128, in shards or a pool; every other shape on the CUDA cores.
- * n_workers: CTAs that the work is cut for (0 = the SM count).
+ * n_workers: CTAs that the work is cut for (0 = the SM count), at most 65,536.
  * ws: cp_prefix_workspace_size() bytes (NULL if that is 0).
  * Errors: as for cp_decode_attn; CP_ERR_INVALID_ARG for members < 0, no query
  * row at all, or a plan of other head counts.

@@ -127,6 +127,8 @@ def test_prefix_plan_refusals(cp):
         cp.cp_prefix_plan(1, [1], [1], 4, 2, layout=2, n_workers=4)
     with pytest.raises(cp.CpError, match="n_workers"):
         cp.cp_prefix_plan(1, [1], [1], 4, 2, n_workers=-1)
+    with pytest.raises(cp.CpError, match="n_workers"):
+        cp.cp_prefix_plan(1, [1], [1], 4, 2, n_workers=2**31 - 1)
     with pytest.raises(ValueError, match="one length"):
         cp.cp_prefix_plan(1, [1, 2], [1], 4, 2, n_workers=4)
 
