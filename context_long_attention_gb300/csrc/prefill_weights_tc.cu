@@ -228,23 +228,25 @@ __global__ void __launch_bounds__(256) weights_lse_kernel(const Params p) {
 
 // ------------------------------------------------------------------ sums
 
-// The steps of a span for one sum warp: adds the weights of its 32 keys and 64 query
-// columns to *sum; false if a wait ran out.  A function of its own, so that the loop
-// has the registers that the walk's state would take.
+// A run of steps for one sum warp: the sum of the weights of its 32 keys and 64 query
+// columns; *ok = false if a wait ran out.  MASK: some columns do not read a key, or are
+// no query of the request.  Functions of their own, so that the loops have the registers
+// that the walk's state would take, and the common one no masks (with both in one loop
+// 1.50 ms for 16,384 queries x 32 heads over 20,480 keys).
 struct SumArgs {
   uint32_t tmem;             // this warp's lanes, its tile's first buffer, its columns
   uint32_t s, go, lfree;     // barriers: scores, free buffers (of the tile's first buffer), LSE slots
   uint32_t lse;              // ring of LSE, from this warp's columns on
   float scale;
-  int nq, steps;
-  int tile, first, last;     // query tile of the first step; tiles go round [first, last)
+  int nq, steps, tile;       // first step, number of steps, query tile of the first one
+  int first, last;           // tiles go round [first, last), head after head
   int lo, cols;              // keys are read from column lo - 128 tile on (of this half), columns end at cols - 128 tile
   unsigned long long wait_ns;
   volatile int* abort;
 };
+template <bool MASK>
 __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
   const int lane = threadIdx.x & 31;
-  const int warp_lo = a.lo - lane + 31;
   uint32_t ra[32], rb[32];
   float sum = 0.f;
   int nq = a.nq, tile = a.tile;
@@ -258,10 +260,9 @@ __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
   tmem_ld32(a.tmem + (nq & 1) * 128, ra);
   for (const int end = nq + a.steps; nq < end; ++nq) {
     const uint32_t lse = a.lse + (nq % kLseSlots) * (BQ * 4);
-    const bool mask = warp_lo > tile * BQ || a.cols - tile * BQ < 64;
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
     auto add = [&](uint32_t (&sr)[32], int c0) {
-      if (mask) {  // some columns do not read this key, or are no query of the request: bits [from, to) stay
+      if constexpr (MASK) {  // bits [from, to) stay
         const int from = min(max(a.lo - tile * BQ - c0, 0), 32), to = min(max(a.cols - tile * BQ - c0, 0), 32);
         const uint32_t keep = __funnelshift_lc(0xffffffffu, 0u, to) & ~__funnelshift_lc(0xffffffffu, 0u, from);
 #pragma unroll
@@ -580,20 +581,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(smem_u32(&bar_go[2 * t + 1]));
     }
     walk([&](const Req& r, const Span& sp) {
-      sa.steps = sp.x1 - sp.x0;
-      sa.first = sp.first;
-      sa.last = sp.first + sp.cnt;
-      sa.tile = sp.first + sp.x0 % sp.cnt;
       // column c of tile q stands at position off + 128 q + c: it reads this key from c = lo - 128 q on
       sa.lo = sp.kb * kBlock + i - r.off - 64 * half;
       sa.cols = r.w - 64 * half;
+      // tiles [mask0, mask1) have all of this warp's columns for all of its keys
+      const int warp_lo = max(0, sa.lo - lane + 31), last = sp.first + sp.cnt;
+      const int mask0 = (warp_lo + BQ - 1) / BQ, mask1 = sa.cols < 64 ? 0 : (sa.cols - 64) / BQ + 1;
+      sa.tile = sp.first + sp.x0 % sp.cnt;
+      sa.first = sp.first;
+      sa.last = last;
+      const bool none = max(mask0, sp.first) >= min(mask1, last);  // no such tile here
+      float sum = 0.f;
       bool ok = true;
-      const float sum = sum_steps(sa, &ok);
+      for (int left = sp.x1 - sp.x0; left > 0 && ok; left -= sa.steps) {
+        const bool whole = sa.tile >= mask0 && sa.tile < mask1;
+        sa.steps = none ? left : min(left, (whole ? min(mask1, last) : sa.tile < mask0 ? min(mask0, last) : last) - sa.tile);
+        sum += whole ? sum_steps<false>(sa, &ok) : sum_steps<true>(sa, &ok);
+        sa.nq += sa.steps;
+        sa.tile += sa.steps;
+        if (sa.tile == last) sa.tile = sp.first;
+      }
       if (!ok) {
         if (lane == 0) report_timeout(p.status, 7, &abort_flag);
         return false;
       }
-      sa.nq += sa.steps;
       // the whole block: its own row; else this worker's first part (the block began
       // with another worker) or its second.  Later kv heads add to what this thread wrote.
       float* to = nullptr;
