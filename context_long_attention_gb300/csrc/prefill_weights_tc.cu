@@ -43,7 +43,7 @@ namespace {
 using namespace tc;
 
 constexpr int kBlock = 256;  // keys of a block
-constexpr int BQ = 128;      // queries of a tile
+constexpr int kBuf = 128;    // TMEM columns of a score buffer
 constexpr int kSumWarps = 16, kThreads = 32 * (kSumWarps + 4);
 constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1, kWarpRelay = kSumWarps + 2;  // and the one after it
 constexpr int kLseSlots = 4;
@@ -52,21 +52,23 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // KB buffers of a key block: two where a block meets few query tiles, one where it
 // meets many (the ring of queries is then deeper).
-template <int D, int KB>
+// BQ queries a tile: 128, or 64 where no request has more (a window of its last queries).
+template <int D, int KB, int BQ>
 struct Cfg {
   static constexpr int kChunks = D / 64;
-  static constexpr int kTileBytes = 128 * D * 2;     // 128 keys or queries
-  static constexpr int kQSlots = (D == 128 ? 7 : 10) - 2 * KB;
-  static constexpr int kSmem = 2 * KB * kTileBytes + kQSlots * kTileBytes + kLseSlots * BQ * 4;
+  static constexpr int kTileBytes = 128 * D * 2;     // 128 keys
+  static constexpr int kQBytes = BQ * D * 2;
+  static constexpr int kQSlots = ((D == 128 ? 7 : 10) - 2 * KB) * 128 / BQ;
+  static constexpr int kSmem = 2 * KB * kTileBytes + kQSlots * kQBytes + kLseSlots * BQ * 4;
 };
 
 // One request's share of the walk.
 struct Req {
   int n, pre, q_base, kv_base;
   int w, off, nq;   // observed queries, the position of the first one, their tiles
-  int c, m0, nb;    // blocks 0 .. m0 - 1 are read by every tile, block k >= m0 from tile 2 k - c on
+  int m, c, m0, nb; // blocks 0 .. m0 - 1 are read by every tile, block k >= m0 from tile m k - c on
 };
-__host__ __device__ inline Req make_req(const cp_req_desc& d, int window) {
+__host__ __device__ inline Req make_req(const cp_req_desc& d, int window, int bq) {
   Req r;
   r.n = d.new_len;
   r.pre = d.prefix_len;
@@ -74,18 +76,19 @@ __host__ __device__ inline Req make_req(const cp_req_desc& d, int window) {
   r.kv_base = d.kv_base;
   r.w = window > 0 && window < d.new_len ? window : d.new_len;
   r.off = d.prefix_len + d.new_len - r.w;
-  r.nq = (int)(((long long)r.w + BQ - 1) / BQ);
-  r.c = (int)(((long long)r.off + BQ - 1) / BQ);
-  r.m0 = r.c / 2 + 1;
+  r.nq = (int)(((long long)r.w + bq - 1) / bq);
+  r.c = (int)(((long long)r.off + bq - 1) / bq);
+  r.m = kBlock / bq;
+  r.m0 = r.c / r.m + 1;
   r.nb = r.nq ? (int)(((long long)d.prefix_len + d.new_len + kBlock - 1) / kBlock) : 0;
   return r;
 }
 // The first tile that reads block k (its last query is at or behind the block's first key).
-__host__ __device__ inline int first_tile(const Req& r, int k) { return k < r.m0 ? 0 : 2 * k - r.c; }
+__host__ __device__ inline int first_tile(const Req& r, int k) { return k < r.m0 ? 0 : r.m * k - r.c; }
 // Tiles of blocks 0 .. k - 1 (of one head).
 __host__ __device__ inline long long tiles_before(const Req& r, long long k) {
   long long f = k * r.nq;
-  if (k > r.m0) f -= k * (k - 1) - (long long)r.m0 * (r.m0 - 1) - (long long)r.c * (k - r.m0);
+  if (k > r.m0) f -= r.m * (k * (k - 1) - (long long)r.m0 * (r.m0 - 1)) / 2 - (long long)r.c * (k - r.m0);
   return f;
 }
 
@@ -94,11 +97,12 @@ struct Params {
   int workers;
   int inner;             // heads inside the walk's blocks: Hq, or 1 where each worker takes its part for every head
   long long total;       // steps of the walk
+  int bq;                // queries of a tile
   int n_tiles;           // query tiles of all requests
   long long* base;       // [R + 1] first step of every request
   int32_t* tile_base;    // [R + 1] first query tile
   int32_t* block_base;   // [R + 1] first key block (a request without queries has its blocks, too)
-  float* lse;            // [Hq][n_tiles][BQ] minus the LSE in log2 units, -inf where there is no query
+  float* lse;            // [Hq][n_tiles][bq] minus the LSE in log2 units, -inf where there is no query
   float* full;           // [2][KV] sums of blocks of one worker, by half of the columns
   float* part;           // [workers][2][2][kBlock]
   float scale_log2;
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(256) weights_table_kernel(const Params p) {
   long long step = 0;
   int tile = 0, block = 0;
   auto each = [&](int j) {
-    const Req r = make_req(req_desc(p, j), p.a.window);
+    const Req r = make_req(req_desc(p, j), p.a.window, p.bq);
     step += p.inner * tiles_before(r, r.nb);
     tile += r.nq;
     block += (int)(((long long)r.pre + r.n + kBlock - 1) / kBlock);
@@ -206,14 +210,14 @@ __global__ void __launch_bounds__(256) weights_lse_kernel(const Params p) {
   const int tile = blockIdx.x, R = p.a.rows.R, Hq = p.a.Hq;
   const int j = find(R, [&](int x) -> long long { return p.tile_base[x]; }, tile);
   const cp_req_desc d = req_desc(p, j);
-  const Req r = make_req(d, p.a.window);
-  const int i0 = r.n - r.w + (tile - p.tile_base[j]) * BQ;  // the tile's first query
-  __shared__ int s_row[BQ];
-  for (int x = threadIdx.x; x < BQ; x += 256) s_row[x] = i0 + x < r.n ? plan_row(p.a.rows, j, d, i0 + x) : -1;
+  const Req r = make_req(d, p.a.window, p.bq);
+  const int i0 = r.n - r.w + (tile - p.tile_base[j]) * p.bq;  // the tile's first query
+  __shared__ int s_row[128];
+  for (int x = threadIdx.x; x < p.bq; x += 256) s_row[x] = i0 + x < r.n ? plan_row(p.a.rows, j, d, i0 + x) : -1;
   __syncthreads();
   for (int h0 = 0; h0 < Hq; h0 += 8) {
     // eight heads of a row side by side, so that whole sectors are read
-    for (int e = threadIdx.x; e < BQ * 8; e += 256) {
+    for (int e = threadIdx.x; e < p.bq * 8; e += 256) {
       const int x = e >> 3, h = h0 + (e & 7);
       if (h >= Hq) continue;
       float v = -INFINITY;
@@ -221,15 +225,15 @@ __global__ void __launch_bounds__(256) weights_lse_kernel(const Params p) {
         const float l = __ldcg(p.a.lse + (long long)s_row[x] * Hq + h);
         if (l != -INFINITY) v = -l * kLog2e;  // a query without keys weighs nothing
       }
-      p.lse[((long long)h * p.n_tiles + tile) * BQ + x] = v;
+      p.lse[((long long)h * p.n_tiles + tile) * p.bq + x] = v;
     }
   }
 }
 
 // ------------------------------------------------------------------ sums
 
-// A run of steps for one sum warp: the sum of the weights of its 32 keys and 64 query
-// columns; *ok = false if a wait ran out.  MASK: some columns do not read a key, or are
+// A run of steps for one sum warp: the sum of the weights of its 32 keys and half of the
+// query columns; *ok = false if a wait ran out.  MASK: some columns do not read a key, or are
 // no query of the request.  Functions of their own, so that the loops have the registers
 // that the walk's state would take, and the common one no masks (with both in one loop
 // 1.50 ms for 16,384 queries x 32 heads over 20,480 keys).
@@ -240,11 +244,11 @@ struct SumArgs {
   float scale;
   int nq, steps, tile;       // first step, number of steps, query tile of the first one
   int first, last;           // tiles go round [first, last), head after head
-  int lo, cols;              // keys are read from column lo - 128 tile on (of this half), columns end at cols - 128 tile
+  int lo, cols;              // keys are read from column lo - BQ tile on (of this half), columns end at cols - BQ tile
   unsigned long long wait_ns;
   volatile int* abort;
 };
-template <bool MASK>
+template <bool MASK, int BQ>
 __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
   const int lane = threadIdx.x & 31;
   uint32_t ra[32], rb[32];
@@ -257,7 +261,7 @@ __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
     return got;
   };
   if (!wait_s(nq)) return sum;
-  tmem_ld32(a.tmem + (nq & 1) * 128, ra);
+  tmem_ld32(a.tmem + (nq & 1) * kBuf, ra);
   for (const int end = nq + a.steps; nq < end; ++nq) {
     const uint32_t lse = a.lse + (nq % kLseSlots) * (BQ * 4);
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
@@ -280,17 +284,22 @@ __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
       }
     };
     tmem_ld_wait();
-    tmem_ld32(a.tmem + (nq & 1) * 128 + 32, rb);
-    add(ra, 0);
-    tmem_ld_wait();
+    if constexpr (BQ == 128) {
+      tmem_ld32(a.tmem + (nq & 1) * kBuf + 32, rb);
+      add(ra, 0);
+      tmem_ld_wait();
+    } else {  // 32 columns: the other array takes the next step's
+#pragma unroll
+      for (int e = 0; e < 32; ++e) rb[e] = ra[e];
+    }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(a.go + 8 * (nq & 1));
     if (nq + 1 < end) {
       if (!wait_s(nq + 1)) return sum;
-      tmem_ld32(a.tmem + ((nq + 1) & 1) * 128, ra);
+      tmem_ld32(a.tmem + ((nq + 1) & 1) * kBuf, ra);
     }
-    add(rb, 32);
+    add(rb, BQ / 2 - 32);
     __syncwarp();
     if (lane == 0) mbar_arrive(a.lfree + 8 * (nq % kLseSlots));
     sum += (s0 + s1) + (s2 + s3);
@@ -299,15 +308,15 @@ __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
   return sum;
 }
 
-template <int D, int KB>
+template <int D, int KB, int BQ>
 __global__ void __launch_bounds__(kThreads, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ Params p) {
-  using C = Cfg<D, KB>;
+  using C = Cfg<D, KB, BQ>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem;                                 // [KB buffers][2 tiles]
   uint8_t* sQ = smem + 2 * KB * C::kTileBytes;             // ring of query tiles
-  float* sL = reinterpret_cast<float*>(sQ + C::kQSlots * C::kTileBytes);  // ring of their LSE
+  float* sL = reinterpret_cast<float*>(sQ + C::kQSlots * C::kQBytes);  // ring of their LSE
   __shared__ __align__(8) uint64_t bar_k[KB], bar_kfree[KB], bar_q[C::kQSlots], bar_qfree[C::kQSlots], bar_l[kLseSlots],
       bar_lfree[kLseSlots], bar_s[4], bar_go[4], bar_drain, bar_never;
   __shared__ uint32_t tmem_slot;
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int passes = p.inner == 1 ? a.Hkv : 1;
     for (int pass = 0; pass < passes; ++pass) {
       int j = find(a.rows.R, [&](int x) { return p.base[x]; }, begin);
-      Req r = make_req(req_desc(p, j), a.window);
+      Req r = make_req(req_desc(p, j), a.window, BQ);
       long long base = p.base[j], pos = begin;
       int kb;  // the block of step `begin`: binary search of the sums
       {
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (pos < end) {
         while (kb >= r.nb) {  // the next request with steps
           ++j;
-          r = make_req(req_desc(p, j), a.window);
+          r = make_req(req_desc(p, j), a.window, BQ);
           base = p.base[j];
           kb = 0;
         }
@@ -422,11 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nq >= C::kQSlots && !wait_all(&bar_qfree[s], (nq / C::kQSlots - 1) & 1, 2)) return false;
         if (nq >= kLseSlots && !wait_all(&bar_lfree[l], (nq / kLseSlots - 1) & 1, 3)) return false;
         if (elect_one()) {
-          const uint32_t full = smem_u32(&bar_q[s]), dst = smem_u32(sQ + s * C::kTileBytes);
-          mbar_expect_tx(full, C::kTileBytes);
+          const uint32_t full = smem_u32(&bar_q[s]), dst = smem_u32(sQ + s * C::kQBytes);
+          mbar_expect_tx(full, C::kQBytes);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(dst + c * (128 * 128), &qmap, c * 64, h, r.q_base + r.n - r.w + (sp.first + q) * BQ, full);
+            tma_load_3d(dst + c * (BQ * 128), &qmap, c * 64, h, r.q_base + r.n - r.w + (sp.first + q) * BQ, full);
           const uint32_t lf = smem_u32(&bar_l[l]);
           mbar_expect_tx(lf, BQ * 4);
           bulk_load(smem_u32(sL + l * BQ), p.lse + ((long long)h * p.n_tiles + tile0 + sp.first + q) * BQ, BQ * 4, lf);
@@ -502,11 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (elect_one()) {
               const uint64_t k = dK + ((uint32_t)((((nk - 1) % KB) * 2 + t) * C::kTileBytes) >> 4);
-              const uint64_t b = dQ + ((uint32_t)(s * C::kTileBytes) >> 4);
+              const uint64_t b = dQ + ((uint32_t)(s * C::kQBytes) >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
-                mma_ss(tmem + t * 256 + buf * 128, k + off, b + off, id, kk > 0);
+                const uint32_t ko = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4, qo = ((kk >> 2) * (BQ * 128) + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + t * 256 + buf * kBuf, k + ko, b + qo, id, kk > 0);
               }
               mma_commit(smem_u32(&bar_s[2 * t + buf]));
               if (t == 1) {
@@ -567,11 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, t = (warp >> 2) & 1, half = warp >> 3;
     const int i = t * 128 + quarter * 32 + lane;  // key of the block
     SumArgs sa;
-    sa.tmem = tmem + ((uint32_t)(quarter * 32) << 16) + t * 256 + 64 * half;
+    sa.tmem = tmem + ((uint32_t)(quarter * 32) << 16) + t * 256 + BQ / 2 * half;
     sa.s = smem_u32(&bar_s[2 * t]);
     sa.go = smem_u32(&bar_go[2 * t]);
     sa.lfree = smem_u32(&bar_lfree[0]);
-    sa.lse = smem_u32(sL + 64 * half);
+    sa.lse = smem_u32(sL + BQ / 2 * half);
     sa.scale = p.scale_log2;
     sa.nq = 0;
     sa.wait_ns = p.wait_ns;
@@ -581,12 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(smem_u32(&bar_go[2 * t + 1]));
     }
     walk([&](const Req& r, const Span& sp) {
-      // column c of tile q stands at position off + 128 q + c: it reads this key from c = lo - 128 q on
-      sa.lo = sp.kb * kBlock + i - r.off - 64 * half;
-      sa.cols = r.w - 64 * half;
+      // column c of tile q stands at position off + BQ q + c: it reads this key from c = lo - BQ q on
+      sa.lo = sp.kb * kBlock + i - r.off - BQ / 2 * half;
+      sa.cols = r.w - BQ / 2 * half;
       // tiles [mask0, mask1) have all of this warp's columns for all of its keys
       const int warp_lo = max(0, sa.lo - lane + 31), last = sp.first + sp.cnt;
-      const int mask0 = (warp_lo + BQ - 1) / BQ, mask1 = sa.cols < 64 ? 0 : (sa.cols - 64) / BQ + 1;
+      const int mask0 = (warp_lo + BQ - 1) / BQ, mask1 = sa.cols < BQ / 2 ? 0 : (sa.cols - BQ / 2) / BQ + 1;
       sa.tile = sp.first + sp.x0 % sp.cnt;
       sa.first = sp.first;
       sa.last = last;
@@ -596,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int left = sp.x1 - sp.x0; left > 0 && ok; left -= sa.steps) {
         const bool whole = sa.tile >= mask0 && sa.tile < mask1;
         sa.steps = none ? left : min(left, (whole ? min(mask1, last) : sa.tile < mask0 ? min(mask0, last) : last) - sa.tile);
-        sum += whole ? sum_steps<false>(sa, &ok) : sum_steps<true>(sa, &ok);
+        sum += whole ? sum_steps<false, BQ>(sa, &ok) : sum_steps<true, BQ>(sa, &ok);
         sa.nq += sa.steps;
         sa.tile += sa.steps;
         if (sa.tile == last) sa.tile = sp.first;
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(kBlock) weights_join_kernel(const Params p) {
   wait_for_earlier_kernels();
   const int R = p.a.rows.R;
   const int j = find(R, [&](int x) -> long long { return p.block_base[x]; }, blockIdx.x);
-  const Req r = make_req(req_desc(p, j), p.a.window);
+  const Req r = make_req(req_desc(p, j), p.a.window, p.bq);
   const int kb = blockIdx.x - p.block_base[j];
   const long long row = (long long)kb * kBlock + threadIdx.x;
   if (row >= (long long)r.pre + r.n) return;
@@ -657,18 +666,20 @@ __global__ void __launch_bounds__(kBlock) weights_join_kernel(const Params p) {
 
 struct Layout {
   long long total = 0;
-  int n_tiles = 0, n_blocks = 0, inner = 1;
+  int n_tiles = 0, n_blocks = 0, inner = 1, bq = 64;
   size_t base, tile_base, block_base, lse, full, part, bytes;
 };
 Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int workers) {
   Layout l;
+  for (int j = 0; j < R && l.bq == 64; ++j)
+    if ((window > 0 && window < reqs[j].new_len ? window : reqs[j].new_len) > 64) l.bq = 128;
   for (int j = 0; j < R; ++j) {
-    const Req r = make_req(reqs[j], window);
+    const Req r = make_req(reqs[j], window, l.bq);
     l.total += tiles_before(r, r.nb);
     l.n_tiles += r.nq;
     l.n_blocks += (int)(((long long)r.pre + r.n + kBlock - 1) / kBlock);
   }
-  if (l.total < (long long)kLongSteps * workers) {
+  if (l.bq == 64 || l.total < (long long)kLongSteps * workers) {
     l.inner = Hq;
     l.total *= Hq;
   }
@@ -681,7 +692,7 @@ Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int wo
   l.base = place(8 * ((size_t)R + 1));
   l.tile_base = place(4 * ((size_t)R + 1));
   l.block_base = place(4 * ((size_t)R + 1));
-  l.lse = place((size_t)Hq * l.n_tiles * BQ * 4);
+  l.lse = place((size_t)Hq * l.n_tiles * l.bq * 4);
   l.full = place((size_t)2 * KV * 4);
   l.part = place((size_t)workers * 4 * kBlock * 4);
   l.bytes = at;
@@ -690,11 +701,11 @@ Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int wo
 
 constexpr int kWorkers = 152;  // one an SM
 
-template <int D, int KB>
+template <int D, int KB, int BQ>
 cudaError_t launch_d(const CUtensorMap& km, const CUtensorMap& qm, const Params& p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<D, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, KB>::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<D, KB, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, KB, BQ>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_early(weights_tc_kernel<D, KB>, (unsigned)p.workers, kThreads, Cfg<D, KB>::kSmem, s, 1, km, qm, p);
+  return launch_early(weights_tc_kernel<D, KB, BQ>, (unsigned)p.workers, kThreads, Cfg<D, KB, BQ>::kSmem, s, 1, km, qm, p);
 }
 
 }  // namespace
@@ -712,6 +723,7 @@ cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t
   p.workers = kWorkers;
   p.inner = l.inner;
   p.total = l.total;
+  p.bq = l.bq;
   p.n_tiles = l.n_tiles;
   p.base = reinterpret_cast<long long*>(w + l.base);
   p.tile_base = reinterpret_cast<int32_t*>(w + l.tile_base);
@@ -727,16 +739,18 @@ cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t
   cudaError_t e = launch_early(weights_table_kernel, 1, 256, 0, s, 1, p);
   if (e == cudaSuccess && l.n_tiles > 0) {
     CUtensorMap km, qm;
-    const uint32_t box[3] = {64, 1, 128};
+    const uint32_t box[3] = {64, 1, 128}, qbox[3] = {64, 1, (uint32_t)l.bq};
     const uint64_t kd[3] = {(uint64_t)D, (uint64_t)a.Hkv, (uint64_t)a.rows.KV}, ks[2] = {(uint64_t)D * 2, (uint64_t)a.Hkv * D * 2};
     const uint64_t qd[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.rows.T}, qs[2] = {(uint64_t)D * 2, (uint64_t)a.Hq * D * 2};
-    if (!encode_tensor_map_bf16(&km, a.k, 3, kd, ks, box) || !encode_tensor_map_bf16(&qm, a.q, 3, qd, qs, box))
+    if (!encode_tensor_map_bf16(&km, a.k, 3, kd, ks, box) || !encode_tensor_map_bf16(&qm, a.q, 3, qd, qs, qbox))
       return cudaErrorInvalidValue;
     e = launch_early(weights_lse_kernel, (unsigned)l.n_tiles, 256, 0, s, 1, p);
     if (e == cudaSuccess) {
-      const bool many = l.inner == 1;
-      e = D == 128 ? (many ? launch_d<128, 1>(km, qm, p, s) : launch_d<128, 2>(km, qm, p, s))
-                   : (many ? launch_d<64, 1>(km, qm, p, s) : launch_d<64, 2>(km, qm, p, s));
+      const bool many = l.inner == 1 && l.bq == 128;  // (one head alone has inner == 1, too)
+      if (D == 128)
+        e = many ? launch_d<128, 1, 128>(km, qm, p, s) : l.bq == 64 ? launch_d<128, 2, 64>(km, qm, p, s) : launch_d<128, 2, 128>(km, qm, p, s);
+      else
+        e = many ? launch_d<64, 1, 128>(km, qm, p, s) : l.bq == 64 ? launch_d<64, 2, 64>(km, qm, p, s) : launch_d<64, 2, 128>(km, qm, p, s);
     }
   }
   if (e == cudaSuccess) e = launch_early(weights_join_kernel, (unsigned)l.n_blocks, kBlock, 0, s, 1, p);
