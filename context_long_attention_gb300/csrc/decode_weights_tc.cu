@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sL[i] = l;
         }
         // a warp kBatch query rows (kv head, column) at a time: their loads overlap
-        constexpr int kBatch = 4, kPer = 5;  // E4M3: pieces of 4 dims a lane, up to 576
+        constexpr int kBatch = 8, kPer = 5;  // E4M3: pieces of 4 dims a lane, up to 576
         const int rows = a.Hkv * ncols;
         for (int i0 = warp * kBatch; i0 < rows; i0 += 4 * kBatch) {
           if constexpr (!F8) {
