@@ -1083,11 +1083,12 @@ def cp_rope_freqs(rot: int, base: float = 10000.0, scaling=None, device=None) ->
 
 def _tokens(name, t, T, dtype, dev):
     """(pointer, token stride, heads, dim) of [T, heads, dim] with dense heads."""
-    if t.dtype is not dtype or not t.is_cuda or t.get_device() != dev:
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0:
         _complain(name, t, dtype, t.shape, dev)
-    if t.dim() != 3 or t.shape[0] != T:
-        raise ValueError(f"{name}: need [{T}, heads, dim], got {tuple(t.shape)}")
-    heads, dim = t.shape[1], t.shape[2]
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T:
+        raise ValueError(f"{name}: need [{T}, heads, dim], got {tuple(shape)}")
+    _, heads, dim = shape
     if t.is_contiguous():
         return t.data_ptr(), heads * dim, heads, dim
     st, sh, sd = t.stride()
@@ -1103,15 +1104,15 @@ def cp_rope(q, k, pos, freqs: RopeFreqs, layout: int = CP_ROPE_HALF, tail: bool 
     rows of a rank).  The first freqs.rot dims of every head turn, or with
     ``tail`` the last ones.  Returns (q_out, k_out): new tensors, or the given ones;
     q_out=q turns in place.  ``inverse`` turns back, the gradient's direction."""
-    dev, dtype = q.get_device(), q.dtype
+    dev, dtype, turns = q.get_device(), q.dtype, freqs.turns
     if dtype is not _bf16 and dtype is not _f32:
         raise TypeError(f"q: need bf16 or fp32, got {dtype}")
     T = q.shape[0]
     if T > _MAX_COUNT:
         raise ValueError(f"{T} tokens: at most 2^31 - 1")
     qp, qs, Hq, Dq = _tokens("q", q, T, dtype, dev)
-    _need("pos", pos, _i32t, (T,), dev)
-    turns = freqs.turns
+    if pos.dtype is not _i32t or pos.get_device() != dev or pos.shape != (T,) or not pos.is_contiguous():
+        _need("pos", pos, _i32t, (T,), dev)
     if turns.get_device() != dev:
         raise ValueError(f"the frequencies are on {turns.device}, q on {q.device}")
     if dev != _device_index():
@@ -1123,9 +1124,12 @@ def cp_rope(q, k, pos, freqs: RopeFreqs, layout: int = CP_ROPE_HALF, tail: bool 
         op, os, Ho, Do = _tokens("q_out", q_out, T, dtype, dev)
         if (Ho, Do) != (Hq, Dq):
             raise ValueError(f"q_out: need {(T, Hq, Dq)}, got {tuple(q_out.shape)}")
-    kp = kop = None
-    ks = kos = Hk = Dk = 0
-    if k is not None:
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        st = lib.cp_rope(T, pos.data_ptr(), turns.data_ptr(), freqs.rot, layout, tail, inverse, freqs.scale,
+                         CP_BF16 if dtype is _bf16 else CP_FP32, qp, qs, Hq, Dq, op, os, None, 0, 0, 0, None, 0, _raw_stream(dev))
+    else:
         kp, ks, Hk, Dk = _tokens("k", k, T, dtype, dev)
         if k_out is None:
             k_out = torch.empty((T, Hk, Dk), dtype=dtype, device=q.device)
@@ -1134,10 +1138,8 @@ def cp_rope(q, k, pos, freqs: RopeFreqs, layout: int = CP_ROPE_HALF, tail: bool 
             kop, kos, Ho, Do = _tokens("k_out", k_out, T, dtype, dev)
             if (Ho, Do) != (Hk, Dk):
                 raise ValueError(f"k_out: need {(T, Hk, Dk)}, got {tuple(k_out.shape)}")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    st = lib.cp_rope(T, pos.data_ptr(), turns.data_ptr(), freqs.rot, layout, tail, inverse, freqs.scale,
-                     CP_BF16 if dtype is _bf16 else CP_FP32, qp, qs, Hq, Dq, op, os, kp, ks, Hk, Dk, kop, kos, _raw_stream(dev))
+        st = lib.cp_rope(T, pos.data_ptr(), turns.data_ptr(), freqs.rot, layout, tail, inverse, freqs.scale,
+                         CP_BF16 if dtype is _bf16 else CP_FP32, qp, qs, Hq, Dq, op, os, kp, ks, Hk, Dk, kop, kos, _raw_stream(dev))
     if st:
         _check(st)
     return q_out, k_out
