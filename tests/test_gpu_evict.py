@@ -95,6 +95,19 @@ def test_prefill_weights_of_a_long_prompt(cp):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("window", [0, 40])
+def test_prefill_weights_of_a_request_beside_nan(cp, window):
+    """Queries and keys of other requests are not mixed in."""
+    g, new, pre = gen(4), [150, 77, 300], [30, 0, 11]
+    q, k = randn(g, (sum(new), 8, 64)), randn(g, (sum(new) + sum(pre), 2, 64))
+    plan = cp.cp_shard_plan(cp.CP_INTERLEAVE, 3, new, pre, device=DEV)
+    lse = cp.cp_prefill_attn(plan, q, k, k)[1]
+    want = cp.cp_prefill_weights(plan, q, k, lse, window=window)
+    q[150:227], k[180:257] = math.nan, math.nan
+    got = cp.cp_prefill_weights(plan, q, k, lse, window=window)
+    assert torch.equal(got[:180], want[:180]) and torch.equal(got[257:], want[257:]) and got[180:257].isnan().any()
+
+
 def test_prefill_weights_of_nothing(cp):
     plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [0, 0], [70, 0], device=DEV)
     k = randn(gen(1), (70, 2, 64))
@@ -175,6 +188,11 @@ def test_decode_weights(cp, C, ctx, Hq, Hkv, D, kv, s_q, page):
                     if l[h] > -math.inf:
                         want[at] += torch.where(seen, (kk @ qq[h] * scale - l[h]).exp(), 0.0)
     before = p.w.clone()
+    if kv == "fp8":  # rows that are no request's may hold NaN
+        p.k.view(torch.uint8)[~named] = 0x7F
+        p.scale[~named] = math.nan
+    else:
+        p.k[~named] = math.nan
     mode = cp.CP_DECODE_MLA if mla else cp.CP_DECODE_GQA
     got = cp.cp_decode_weights(p.plan, p.pages, mode, q, p.k, lse, p.w, scale_pool=p.scale, sm_scale=scale)
     cp.cp_device_error_check()

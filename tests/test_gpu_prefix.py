@@ -154,16 +154,52 @@ def test_prefix_of_rising_and_large_scores(cp, D):
         c.check(o, lse)
 
 
-def test_prefix_reads_its_group_only(cp):
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp32"])
+@pytest.mark.parametrize("members", [9, 70])
+def test_prefix_reads_its_group_only(cp, kv, members):
     """Rows of other groups next to a group's, and rows of the pool that no pair
-    names, may hold anything that is finite; LSE -inf parts may hold NaN."""
-    c = Case(cp, 2, [100, 130], [9, 9], 8, 2, 128, page=64)
+    names, are not mixed in: they may even be NaN."""
+    bad = 0x7F if kv == "fp8" else math.nan  # E4M3's NaN
+    c = Case(cp, 2, [100, 130], [members, members], 8, 2, 128, kv, page=64)
     o, lse = c.run()
     used = {(int(c.pages.host[p, i // 64]) * 64 + i % 64) for p in range(4) for i in range(int(c.plan.pairs[p, 0]))}
     rest = torch.tensor(sorted(set(range(c.pages.pool_rows)) - used), device=DEV)
     for x in c.pool[:2]:
-        x[rest] = 1e4
+        x[rest] = bad
+    if c.pool[2] is not None:
+        c.pool[2][rest] = math.nan
     o2, lse2 = c.run()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # shards: the second group's rows follow the first one's inside a tile
+    c = Case(cp, 2, [100, 130], [members, members], 8, 2, 128, kv)
+    o, lse = c.run()
+    for r in range(2):
+        n = int(c.plan.pairs[r * 2, 0])
+        c.sk[r][n:], c.sv[r][n:] = bad, bad
+        if c.sc is not None:
+            c.sc[r][n:] = math.nan
+    o2, lse2 = c.run()
+    assert torch.equal(o[:members], o2[:members]) and torch.equal(lse[:members], lse2[:members])
+
+
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("bf16", 64), ("fp8", 128)])
+def test_prefix_of_many_shards(cp, kv, D):
+    """More shards than the short list of tensor maps holds, most of them with few rows."""
+    c = Case(cp, 40, [700, 30, 5000], [5, 1, 40], 8, 2, D, kv, workers=20, P=1)
+    o, lse = c.run()
+    cp.cp_device_error_check()
+    c.check(o, lse)
+
+
+def test_prefix_of_a_query_that_is_nan(cp):
+    """A NaN query row spoils its own results only."""
+    c = Case(cp, 1, [600], [20], 8, 2, 128, workers=3)
+    o, lse = c.run()
+    c.q[3, 5, 7] = math.nan
+    o2, lse2 = c.run()
+    cp.cp_device_error_check()
+    assert o2[3, 5].isnan().all() and lse2[3, 5].isnan()
+    o2[3, 5], lse2[3, 5] = o[3, 5], lse[3, 5]
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
