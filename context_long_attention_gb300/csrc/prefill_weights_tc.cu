@@ -269,12 +269,10 @@ __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
     const uint32_t lse = a.lse + (nq % kLseSlots) * (BQ * 4);
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
     auto add = [&](uint32_t (&sr)[32], int c0) {
+      uint32_t keep = 0xffffffffu;
       if constexpr (MASK) {  // bits [from, to) stay
         const int from = min(max(a.lo - tile * BQ - c0, 0), 32), to = min(max(a.cols - tile * BQ - c0, 0), 32);
-        const uint32_t keep = __funnelshift_lc(0xffffffffu, 0u, to) & ~__funnelshift_lc(0xffffffffu, 0u, from);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (!(keep >> e & 1)) sr[e] = 0xff800000u;
+        keep = __funnelshift_lc(0xffffffffu, 0u, to) & ~__funnelshift_lc(0xffffffffu, 0u, from);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -282,6 +280,12 @@ __device__ __noinline__ float sum_steps(const SumArgs a, bool* ok) {
         float u0, u1, u2, u3;
         fma2(u0, u1, __uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1]), a.scale, a.scale, v.x, v.y);
         fma2(u2, u3, __uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3]), a.scale, a.scale, v.z, v.w);
+        if constexpr (MASK) {  // behind the LSE, which may be NaN
+          if (!(keep >> (4 * e) & 1)) u0 = -INFINITY;
+          if (!(keep >> (4 * e + 1) & 1)) u1 = -INFINITY;
+          if (!(keep >> (4 * e + 2) & 1)) u2 = -INFINITY;
+          if (!(keep >> (4 * e + 3) & 1)) u3 = -INFINITY;
+        }
         add2(s0, s1, s0, s1, ex2(u0), ex2(u1));
         add2(s2, s3, s2, s3, ex2(u2), ex2(u3));
       }

@@ -108,6 +108,25 @@ def test_prefill_weights_of_a_request_beside_nan(cp, window):
     assert torch.equal(got[:180], want[:180]) and torch.equal(got[257:], want[257:]) and got[180:257].isnan().any()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("window,at", [(0, 200), (0, 128), (50, 280)])
+def test_prefill_weights_of_a_query_that_is_nan(cp, window, at, dtype):
+    """A NaN query spoils the keys that it reads (unless the attention itself gave it LSE
+    -inf, as its fp32 form does: then it weighs nothing), not the later ones."""
+    g, new, pre = gen(5), 300, 20
+    q, k = randn(g, (new, 8, 64)).to(dtype), randn(g, (new + pre, 2, 64)).to(dtype)
+    plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [new], [pre], device=DEV)
+    lse = cp.cp_prefill_attn(plan, q, k, k)[1]
+    want = cp.cp_prefill_weights(plan, q, k, lse, window=window)
+    q[at] = math.nan
+    lse = cp.cp_prefill_attn(plan, q, k, k)[1]
+    got = cp.cp_prefill_weights(plan, q, k, lse, window=window)
+    assert lse.isnan().any() or (lse == -math.inf).any()
+    reads = got[:pre + at + 1].isnan()
+    assert reads.all() if lse.isnan().any() else not reads.any()
+    assert torch.equal(got[pre + at + 1:], want[pre + at + 1:])
+
+
 def test_prefill_weights_of_nothing(cp):
     plan = cp.cp_shard_plan(cp.CP_ZIGZAG, 2, [0, 0], [70, 0], device=DEV)
     k = randn(gen(1), (70, 2, 64))
