@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
       *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at * a.D + d) = make_float4(x, y, u, v);
     }
   }
-  if (lane == 0) a.lse[at] = z > 0.f ? g + logf(z) : -INFINITY;
+  if (lane == 0) a.lse[at] = z == 0.f ? -INFINITY : g + logf(z);  // NaN stays NaN
 }
 
 template <typename TQ, typename T>

@@ -191,9 +191,11 @@ def test_prefix_of_many_shards(cp, kv, D):
     c.check(o, lse)
 
 
-def test_prefix_of_a_query_that_is_nan(cp):
-    """A NaN query row spoils its own results only."""
-    c = Case(cp, 1, [600], [20], 8, 2, 128, workers=3)
+@pytest.mark.parametrize("workers", [2, 3, 9])
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp32"])
+def test_prefix_of_a_query_that_is_nan(cp, kv, workers):
+    """A NaN query row spoils its own results only, in parts or alone."""
+    c = Case(cp, 1, [600], [20], 8, 2, 128, kv, workers=workers)
     o, lse = c.run()
     c.q[3, 5, 7] = math.nan
     o2, lse2 = c.run()
