@@ -1921,6 +1921,9 @@ cp_status cp_evict_select(int C, int B, const int32_t* ctx_len, const int32_t* k
                           int32_t* count, void* stream) {
   const cp_status st = check_pool_shape(C, B, max_pages, page_size, num_pages);
   if (st != CP_OK) return st;
+  // the kernels' row indices stay below 2^31 with what they add to them
+  if ((long long)max_pages * page_size > 1 << 30)
+    return fail(CP_ERR_UNSUPPORTED, "max_pages=%d x page_size=%d: more than 2^30 rows a pair", max_pages, page_size);
   if (max_moves < 1 || (long long)C * B * max_moves > 0x7FFFFFFFLL)
     return fail(CP_ERR_INVALID_ARG, "max_moves=%d: need >= 1 and C B max_moves < 2^31", max_moves);
   if (!ctx_len || !keep_len || !page_table || !weights || !src || !dst || !count)

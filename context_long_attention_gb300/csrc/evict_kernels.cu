@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kBitThreads) evict_bits_kernel(const EvictArgs
       }
     }
   }
-  for (int x = max(moves, 0) + tid; x < a.max_moves; x += nt) src[x] = dst[x] = -1;
+  for (long long x = max(moves, 0) + tid; x < a.max_moves; x += nt) src[x] = dst[x] = -1;
   if (tid == 0) a.count[pair] = moves;
 }
 
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const SelectParams p) 
       });
     }
   }
-  for (int i = max(moves, 0) + tid; i < a.max_moves; i += NT) src[i] = dst[i] = -1;
+  for (long long i = max(moves, 0) + tid; i < a.max_moves; i += NT) src[i] = dst[i] = -1;
   if (tid == 0) a.count[pair] = moves;
 }
 
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MovePara
   wait_for_earlier_kernels();
   const int n = min(__ldcg(a.count + pair), a.max_moves);
   const int vec = a.row_bytes / 16;
-  for (int j0 = warp; j0 < n; j0 += 32 * step) {
-    const int mine = j0 + lane * step;
+  for (long long j0 = warp; j0 < n; j0 += 32 * step) {
+    const long long mine = j0 + lane * step;
     const long long at = (long long)pair * a.max_moves + mine;
     const int src = mine < n ? __ldcg(a.src + at) : -1, dst = mine < n ? __ldcg(a.dst + at) : -1;
     const bool good = src >= 0 && dst >= 0 && src < a.pool_rows && dst < a.pool_rows;
@@ -515,8 +515,8 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t s) {
   // some eight blocks an SM, as many as a pair has work for (four: the same within 2 %)
-  const int useful = (a.max_moves + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
-  int splits = (152 * 8 + a.pairs - 1) / a.pairs;
+  const int useful = (a.max_moves - 1) / (kMoveThreads / 32) + 1;
+  int splits = (152 * 8 - 1) / a.pairs + 1;
   if (splits > useful) splits = useful;
   return launch_early(cache_move_kernel, (unsigned)a.pairs * splits, kMoveThreads, 0, s, 1, MoveParams{a, splits});
 }

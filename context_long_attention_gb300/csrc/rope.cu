@@ -230,7 +230,7 @@ cudaError_t launch_rope(const RopeArgs& a, bool bf16, cudaStream_t stream) {
   const int most = kMaxAngles / (a.rot / 2);
   p.tokens = (4 * kThreads + p.token_units - 1) / p.token_units;
   if (p.tokens > most) p.tokens = most;
-  while (p.tokens > 1 && (a.T + p.tokens - 1) / p.tokens < 152) p.tokens /= 2;
+  while (p.tokens > 1 && (a.T - 1) / p.tokens < 151) p.tokens /= 2;
   p.by_token = SmallDiv((uint32_t)p.token_units);
   if (bf16) return a.half ? launch_t<__nv_bfloat16, true>(p, stream) : launch_t<__nv_bfloat16, false>(p, stream);
   return a.half ? launch_t<float, true>(p, stream) : launch_t<float, false>(p, stream);

@@ -814,7 +814,12 @@ cp_status cp_decode_weights(const void* host_plan, const void* dev_plan, cp_deco
  *   length), CP_SLOTS_TABLE_FULL (a pair of more than max_pages pages) and
  *   CP_SLOTS_NO_PAGES (*free_pos outside [0, n_free], or fewer than the released
  *   pages); nothing else is written then.  keep_len >= ctx_len releases nothing.
- * Errors: as for cp_page_slots; max_moves < 1; C B max_moves >= 2^31.
+ *   Ids go back as they stand in the table, and a pair that cp_evict_select gave
+ *   count -1 loses its last pages with whatever they hold: give such a request
+ *   keep_len = ctx_len first.
+ * No page may belong to two pairs in any of the three.
+ * Errors: as for cp_page_slots; max_moves < 1; C B max_moves >= 2^31; max_pages
+ * x page_size > 2^30 for cp_evict_select (CP_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 cp_status cp_evict_select(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, const int32_t* page_table,
                           int max_pages, int page_size, int num_pages, const float* weights, const int32_t* pos,

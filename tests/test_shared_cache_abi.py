@@ -243,6 +243,7 @@ def test_eviction(cp):
     refuse(lib, UNSUPPORTED, b"page_size", select(page=100))
     refuse(lib, UNSUPPORTED, b"too large", select(num=1 << 26))
     refuse(lib, INVALID, b"max_pages", select(most=0))
+    refuse(lib, UNSUPPORTED, b"rows a pair", select(most=1 << 25))
     for moves in (0, -1, 1 << 30):
         refuse(lib, INVALID, b"max_moves", select(moves=moves))
     for kw in (dict(ctx=None), dict(keep=None), dict(t=None), dict(w=None), dict(src=None), dict(dst=None), dict(count=None)):
