@@ -30,7 +30,7 @@
 // shared memory at 128 B a clk, as both operands come from there; its 32,768 exponentials
 // take the special function units as long as the products.  16,384 queries x 32 heads over 20,480 keys:
 // 1.44 ms, 1,140 TFLOP/s (1.28 ms with the sums' work left out); the last 64 queries of
-// nine prompts of up to 30,000 tokens: 147 us, a chain of short steps.
+// nine prompts of up to 30,000 tokens: 138-147 us, a chain of short steps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
