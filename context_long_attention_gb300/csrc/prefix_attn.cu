@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kSimtWarps * 32) prefix_simt_kernel(const Pref
 // ------------------------------------------------------------------ merge
 
 // A warp an output row: the weights of its parts, one to a lane, then its dims over
-// the lanes, NV pieces of four to a lane.
-constexpr int kMergeWarps = 8, kBatch = 8;
-template <int NV>
+// the lanes, NV pieces of four to a lane; kBatch parts' rows are loaded together.
+constexpr int kMergeWarps = 8;
+template <int NV, int kBatch>
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixArgs a) {
   constexpr int kPer = kPrefixRows / kMergeWarps;
   const int lane = threadIdx.x & 31, dm = (blockIdx.x % kPer) * kMergeWarps + (threadIdx.x >> 5);
@@ -125,7 +125,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
     const float w = i0 + lane < parts ? expf(lse_at(i0 + lane) - g0) : 0.f;
     const int n = min(32, parts - i0);
     for (int k0 = 0; k0 < n; k0 += kBatch) {
-      // the rows of a batch of parts are loaded together
       float wk[kBatch];
       float4 x[kBatch][NV];
 #pragma unroll
@@ -201,7 +200,12 @@ cudaError_t launch_prefix_simt(const PrefixArgs& a, cp_dtype kv, int workers, cu
 
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int blocks, cudaStream_t s) {
   if (blocks == 0) return cudaSuccess;
-  return launch_early(a.D <= 128 ? prefix_merge_kernel<1> : prefix_merge_kernel<2>, (unsigned)blocks * (kPrefixRows / kMergeWarps), kMergeWarps * 32, 0, s, 1, a);
+  const unsigned grid = (unsigned)blocks * (kPrefixRows / kMergeWarps);
+  // Few blocks: all the parts that a block of 152 workers usually has at once (4 requests
+  // behind 4,096 tokens 20.1 -> 18.5 us, 64 behind 32,768 53.1 -> 51.4); in several waves
+  // the registers of 20 would cost the warps that hide the latency (124 -> 130 us for 300 x 64 heads).
+  auto kern = a.D > 128 ? prefix_merge_kernel<2, 8> : grid <= 2 * 152 ? prefix_merge_kernel<1, 20> : prefix_merge_kernel<1, 12>;
+  return launch_early(kern, grid, kMergeWarps * 32, 0, s, 1, a);
 }
 
 }  // namespace cpattn
