@@ -55,6 +55,8 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kWarpTma = kSoftmaxWarps, kWarpMma = kSoftmaxWarps + 1, kWarpRelay = kSoftmaxWarps + 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
+// E4M3: in a block of up to so many rows half of the softmax warps have none, and convert V.
+constexpr int kHelpRows = 64;
 
 template <int D, bool F8>
 struct Cfg {
@@ -147,6 +149,25 @@ __device__ __forceinline__ void put_codes(const uint4& x, uint8_t* row, int swiz
   uint8_t* at = row + (((piece >> 1) ^ swizzle) << 4) + 8 * (piece & 1);
   *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
   *reinterpret_cast<uint2*>(at + BM * 128) = make_uint2(lo[0], lo[1]);
+}
+// Chunks [c0, c0 + N) of 16 codes of a V tile's row as bf16, both 128-byte-swizzled; `to`
+// is the row in the first of the bf16 tile's two 64-dim chunks of BN rows.
+template <int N>
+__device__ __forceinline__ void convert_row(const uint8_t* from, uint8_t* to, int row, int c0) {
+  const uint4* src = reinterpret_cast<const uint4*>(from);
+#pragma unroll 4
+  for (int c = c0; c < c0 + N; ++c) {
+    const uint4 x = src[c ^ (row & 7)];
+    uint32_t o[8];
+    bf16_of_codes(x.x, o[0], o[1]);
+    bf16_of_codes(x.y, o[2], o[3]);
+    bf16_of_codes(x.z, o[4], o[5]);
+    bf16_of_codes(x.w, o[6], o[7]);
+    uint8_t* chunk = to + (c >> 2) * (BN * 128);
+    const int unit = 2 * (c & 3);
+    *reinterpret_cast<uint4*>(chunk + ((unit ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(chunk + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
 }
 __device__ __forceinline__ void mbar_inval(uint32_t bar) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
 
@@ -278,8 +299,33 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
       return s0sum + s1sum;
     };
+    const bool helps = F8 && !WIDE && it.m_rows <= kHelpRows && quarter >= 2;
+    if (helps) {
+      // 32 of the chain's 64 rows of V, one half of the dims.  V_(j+1) goes where V_(j-1) was, and
+      // the chain's product with that one is complete when its S_j is; this warp's arrival on
+      // P_(j+1) covers it.
+      const int vrow = 64 * t + (quarter - 2) * 32 + lane;
+      uint8_t* codes = sQ + C::kCodes + C::kKSlots * C::kCodeBytes + vrow * 128;
+      for (int j = -1; j < nK; ++j) {
+        bool got = j < 0 || mbar_wait(smem_u32(&sh.bar_s[t]), j & 1, p.wait_ns, abort);
+        if (got && j >= 0) mbar_arrive(smem_u32(&sh.bar_p[t]));
+        const int v = j + 1;
+        if (got && v < nK) got = mbar_wait(smem_u32(&sh.bar_unit[3 + v % C::kVSlots]), (v / C::kVSlots) & 1, p.wait_ns, abort);
+        got = __all_sync(0xffffffffu, got);
+        if (!got) {
+          if (lane == 0) report_timeout(p.status, 6, abort);
+          ok = false;
+          break;
+        }
+        if (v == nK) break;
+        convert_row<4>(codes + v % C::kVSlots * C::kCodeBytes, sKV + (v % C::kSlots) * C::kSlotBytes + vrow * 128, vrow, 4 * half);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[5 + v % C::kVSlots]));
+      }
+    }
     Walk w(sh.tile_off, it.tile_begin);
-    for (int j = 0; j < nK && ok; ++j) {
+    for (int j = helps ? nK : 0; j < nK && ok; ++j) {
       const int nv = min(BN, sh.rows[w.r] - (w.t - w.off[w.r]) * BN);  // keys of the tile
       const int chain = WIDE ? nv : nv - 64 * t;                      // of the chain
       keys = chain - NC * half;
@@ -617,23 +663,11 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         if (lane == 0) report_timeout(p.status, 5, abort);
         break;
       }
-      const uint4* src = reinterpret_cast<const uint4*>(codes + j % C::kVSlots * C::kCodeBytes + row * 128);
-      uint8_t* dst = sKV + (j % C::kSlots) * C::kSlotBytes + row * 128;
       // rows behind the shard's last key meet weights of 0: any finite value will do
-#pragma unroll 4
-      for (int c = 0; c < 8; ++c) {
-        const uint4 x = src[c ^ (row & 7)];
-        uint32_t o[8];
-        bf16_of_codes(x.x, o[0], o[1]);
-        bf16_of_codes(x.y, o[2], o[3]);
-        bf16_of_codes(x.z, o[4], o[5]);
-        bf16_of_codes(x.w, o[6], o[7]);
-        uint8_t* chunk = dst + (c >> 2) * (BN * 128);
-        const int unit = 2 * (c & 3);
-        *reinterpret_cast<uint4*>(chunk + ((unit ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(chunk + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      if (it.m_rows > kHelpRows) {
+        convert_row<8>(codes + j % C::kVSlots * C::kCodeBytes + row * 128, sKV + (j % C::kSlots) * C::kSlotBytes + row * 128, row, 0);
+        fence_proxy_async_smem();
       }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[5 + j % C::kVSlots]));
       if (j + 1 < nK) {
@@ -803,7 +837,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (wi > w0) mbar_inval(smem_u32(b));
         const bool is_p = b == &sh.bar_p[0] || b == &sh.bar_p[1];
         const bool four = F8 && (b == &sh.bar_unit[5] || b == &sh.bar_unit[6] || (b >= &sh.bar_rel[4] && b <= &sh.bar_rel[6]));
-        mbar_init(smem_u32(b), is_p ? 2 * BM + C::kRelays : four ? 4 : 1);
+        const bool converted = b == &sh.bar_unit[5] || b == &sh.bar_unit[6];
+        mbar_init(smem_u32(b), is_p ? 2 * BM + C::kRelays : four ? (converted && it.m_rows <= kHelpRows ? 12 : 4) : 1);
         mbar_init_fence();
         fence_proxy_async_smem();
       }
