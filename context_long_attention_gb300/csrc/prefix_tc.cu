@@ -66,9 +66,9 @@ struct Cfg {
   static constexpr int kSlots = F8 ? 2 : D == 128 ? 5 : 10;  // of the K/V ring (E4M3: of V as bf16)
   static constexpr int kRing = 2 * kQBytes;
   // E4M3: rings of code tiles behind it
-  static constexpr int kKSlots = 3, kVSlots = 2, kCodeBytes = BN * D;
+  static constexpr int kKSlots = 3, kCodeTiles = kKSlots + 2, kCodeBytes = BN * D;
   static constexpr int kCodes = kRing + kSlots * kSlotBytes;
-  static constexpr int kTiles = kCodes + (F8 ? (kKSlots + kVSlots) * kCodeBytes : 0);
+  static constexpr int kTiles = kCodes + (F8 ? kCodeTiles * kCodeBytes : 0);
   static constexpr int kThreads = 32 * (kSoftmaxWarps + (F8 ? 6 : 3));
   static constexpr int kRelays = F8 ? 4 : 1;  // arrivals of the relay's part
 };
@@ -195,7 +195,7 @@ struct Walk {
 };
 
 struct alignas(16) Shared {
-  // E4M3: unit[0..2] K tiles landed, unit[3..4] V tiles landed, unit[5..6] V tiles converted,
+  // E4M3: unit[0..2] K tiles landed, unit[3..5] V tiles landed, unit[6..8] V tiles converted,
   // rel[4..6] a tile's scales written
   uint64_t bar_unit[10], bar_rel[10], bar_s[2], bar_p[2], bar_o[2], bar_never, bar_drain;
   uint32_t tmem_slot;
@@ -216,6 +216,12 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   using C = Cfg<D, F8>;
   uint8_t* sKV = sQ + C::kRing;
   constexpr int kUnitBars = C::kSlots;
+  // E4M3: V's code tiles, the third one where a second M tile of queries would be
+  constexpr int kVSlots = WIDE ? 2 : 3;
+  auto v_codes = [&](int j) {
+    const int slot = j % kVSlots;
+    return sQ + (slot < 2 ? C::kCodes + (C::kKSlots + slot) * C::kCodeBytes : C::kQBytes);
+  };
   constexpr int kRels = F8 ? 3 : C::kSlots;  // barriers of the releases
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
@@ -305,12 +311,11 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       // the chain's product with that one is complete when its S_j is; this warp's arrival on
       // P_(j+1) covers it.
       const int vrow = 64 * t + (quarter - 2) * 32 + lane;
-      uint8_t* codes = sQ + C::kCodes + C::kKSlots * C::kCodeBytes + vrow * 128;
       for (int j = -1; j < nK; ++j) {
         bool got = j < 0 || mbar_wait(smem_u32(&sh.bar_s[t]), j & 1, p.wait_ns, abort);
         if (got && j >= 0) mbar_arrive(smem_u32(&sh.bar_p[t]));
         const int v = j + 1;
-        if (got && v < nK) got = mbar_wait(smem_u32(&sh.bar_unit[3 + v % C::kVSlots]), (v / C::kVSlots) & 1, p.wait_ns, abort);
+        if (got && v < nK) got = mbar_wait(smem_u32(&sh.bar_unit[3 + v % kVSlots]), (v / kVSlots) & 1, p.wait_ns, abort);
         got = __all_sync(0xffffffffu, got);
         if (!got) {
           if (lane == 0) report_timeout(p.status, 6, abort);
@@ -318,10 +323,10 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
           break;
         }
         if (v == nK) break;
-        convert_row<4>(codes + v % C::kVSlots * C::kCodeBytes, sKV + (v % C::kSlots) * C::kSlotBytes + vrow * 128, vrow, 4 * half);
+        convert_row<4>(v_codes(v) + vrow * 128, sKV + (v % C::kSlots) * C::kSlotBytes + vrow * 128, vrow, 4 * half);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[5 + v % C::kVSlots]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[6 + v % kVSlots]));
       }
     }
     Walk w(sh.tile_off, it.tile_begin);
@@ -558,11 +563,11 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         return false;
       };
       for (int j = 0; j < nK; ++j) {  // V_j, then K_(j+1)
-        if (nv >= C::kVSlots && !wait_all(&sh.bar_unit[5 + nv % C::kVSlots], (nv / C::kVSlots - 1) & 1)) break;
+        if (nv >= kVSlots && !wait_all(&sh.bar_unit[6 + nv % kVSlots], (nv / kVSlots - 1) & 1)) break;
         if (elect_one()) {
-          const uint32_t full = smem_u32(&sh.bar_unit[3 + nv % C::kVSlots]);
+          const uint32_t full = smem_u32(&sh.bar_unit[3 + nv % kVSlots]);
           mbar_expect_tx(full, C::kCodeBytes);
-          load(&maps.v[vr], v0, v1, smem_u32(codes + (C::kKSlots + nv % C::kVSlots) * C::kCodeBytes), full);
+          load(&maps.v[vr], v0, v1, smem_u32(v_codes(nv)), full);
         }
         __syncwarp();
         ++nv;
@@ -585,8 +590,8 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       // never leave with a copy in flight: the last fill of every slot
       for (int u = max(0, nk - C::kKSlots); u < nk; ++u)
         mbar_wait(smem_u32(&sh.bar_unit[u % C::kKSlots]), (u / C::kKSlots) & 1, 1000000000ull, &sh.zero_flag);
-      for (int u = max(0, nv - C::kVSlots); u < nv; ++u)
-        mbar_wait(smem_u32(&sh.bar_unit[3 + u % C::kVSlots]), (u / C::kVSlots) & 1, 1000000000ull, &sh.zero_flag);
+      for (int u = max(0, nv - kVSlots); u < nv; ++u)
+        mbar_wait(smem_u32(&sh.bar_unit[3 + u % kVSlots]), (u / kVSlots) & 1, 1000000000ull, &sh.zero_flag);
       __syncwarp();
       return;
     }
@@ -636,7 +641,6 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     // ------------------------------------------------------------ V's codes to bf16 (a thread a row)
     bool ok = true;
     const int row = (warp - kWarpRelay) * 32 + lane;
-    uint8_t* codes = sQ + C::kCodes + C::kKSlots * C::kCodeBytes;
     Walk w(sh.tile_off, it.tile_begin);
     auto scale_of = [&]() -> float {  // of this row of tile w.t; 0 behind the shard's last key
       const int in_pair = (w.t - w.off[w.r]) * BN + row, pair = w.r * a.R + it.group;
@@ -656,7 +660,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         scale = scale_of();
       }
       // V_j has landed; its bf16 slot's V_(j-2) is read (release j - 1: S_(j-1) is complete)
-      ok = mbar_wait(smem_u32(&sh.bar_unit[3 + j % C::kVSlots]), (j / C::kVSlots) & 1, p.wait_ns, abort);
+      ok = mbar_wait(smem_u32(&sh.bar_unit[3 + j % kVSlots]), (j / kVSlots) & 1, p.wait_ns, abort);
       if (ok && j >= C::kSlots) ok = mbar_wait(smem_u32(&sh.bar_rel[(j - 1) % kRels]), ((j - 1) / kRels) & 1, p.wait_ns, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
@@ -665,11 +669,11 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
       // rows behind the shard's last key meet weights of 0: any finite value will do
       if (it.m_rows > kHelpRows) {
-        convert_row<8>(codes + j % C::kVSlots * C::kCodeBytes + row * 128, sKV + (j % C::kSlots) * C::kSlotBytes + row * 128, row, 0);
+        convert_row<8>(v_codes(j) + row * 128, sKV + (j % C::kSlots) * C::kSlotBytes + row * 128, row, 0);
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[5 + j % C::kVSlots]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[6 + j % kVSlots]));
       if (j + 1 < nK) {
         // V_(j-2) was free: both chains are done with P_(j-2), whose scales these replace
         put_scale(j + 1, scale);
@@ -836,9 +840,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         uint64_t* b = reinterpret_cast<uint64_t*>(&sh) + lane;
         if (wi > w0) mbar_inval(smem_u32(b));
         const bool is_p = b == &sh.bar_p[0] || b == &sh.bar_p[1];
-        const bool four = F8 && (b == &sh.bar_unit[5] || b == &sh.bar_unit[6] || (b >= &sh.bar_rel[4] && b <= &sh.bar_rel[6]));
-        const bool converted = b == &sh.bar_unit[5] || b == &sh.bar_unit[6];
-        mbar_init(smem_u32(b), is_p ? 2 * BM + C::kRelays : four ? (converted && it.m_rows <= kHelpRows ? 12 : 4) : 1);
+        const bool converted = F8 && b >= &sh.bar_unit[6] && b <= &sh.bar_unit[8], scaled = F8 && b >= &sh.bar_rel[4] && b <= &sh.bar_rel[6];
+        mbar_init(smem_u32(b), is_p ? 2 * BM + C::kRelays : converted ? (it.m_rows <= kHelpRows ? 12 : 4) : scaled ? 4 : 1);
         mbar_init_fence();
         fence_proxy_async_smem();
       }
