@@ -225,6 +225,9 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   constexpr int kRels = F8 ? 3 : C::kSlots;  // barriers of the releases
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
+  // Columns in registers at a time: E4M3's further warps leave 80 registers a thread, which
+  // do not hold 64 scores and their P (64 x 32 heads behind 131,072 tokens: 516 us)
+  constexpr int NB = F8 && NC == 64 ? 32 : NC;
   // a half row's P sum that can hide a P above 2^8
   constexpr float kSpecSum = NC * 256.f;
   const PrefixArgs& a = p.a;
@@ -263,44 +266,44 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     bool ok = true, first = true;  // first: no key of this chain so far
     int keys = 0;                  // of this half's columns, those in use in this tile
     const float* scales = nullptr;  // E4M3: of this half's columns
-    auto load_s = [&](uint32_t (&sr)[NC]) {
-      if constexpr (NC == 64) {
+    auto load_s = [&](int c0, uint32_t (&sr)[NB]) {  // columns [c0, c0 + NB) of the half
+      if constexpr (NB == 64) {
         tmem_ld32(lane_addr + colS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tmem_ld32(lane_addr + colS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       } else {
-        tmem_ld32(lane_addr + colS, sr);
+        tmem_ld32(lane_addr + colS + c0, sr);
       }
       tmem_ld_wait();
       if constexpr (F8) {
 #pragma unroll
-        for (int e = 0; e < NC; e += 4) {
-          const float4 k = *reinterpret_cast<const float4*>(scales + e);
+        for (int e = 0; e < NB; e += 4) {
+          const float4 k = *reinterpret_cast<const float4*>(scales + c0 + e);
           sr[e] = __float_as_uint(__uint_as_float(sr[e]) * k.x);
           sr[e + 1] = __float_as_uint(__uint_as_float(sr[e + 1]) * k.y);
           sr[e + 2] = __float_as_uint(__uint_as_float(sr[e + 2]) * k.z);
           sr[e + 3] = __float_as_uint(__uint_as_float(sr[e + 3]) * k.w);
         }
       }
-      if (keys < NC) {
+      if (keys < c0 + NB) {
 #pragma unroll
-        for (int e = 0; e < NC; ++e)
-          if (e >= keys) sr[e] = __float_as_uint(-INFINITY);
+        for (int e = 0; e < NB; ++e)
+          if (c0 + e >= keys) sr[e] = __float_as_uint(-INFINITY);
       }
     };
-    auto exps = [&](const uint32_t (&sr)[NC], uint32_t (&pk)[NC / 2]) -> float {
+    auto exps = [&](int c0, const uint32_t (&sr)[NB], uint32_t (&pk)[NC / 2]) -> float {
       const float neg = -m_used * sl2;
       float s0sum = 0.f, s1sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < NC / 2; ++e) {
+      for (int e = 0; e < NB / 2; ++e) {
         float u0, u1;
         fma2(u0, u1, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]), sl2, sl2, neg, neg);
         const float p0 = ex2(u0), p1 = ex2(u1);
         add2(s0sum, s1sum, s0sum, s1sum, p0, p1);
         if constexpr (F8) {
-          const float2 k = *reinterpret_cast<const float2*>(scales + 2 * e);
-          pk[e] = pack_bf16x2(p0 * k.x, p1 * k.y);
+          const float2 k = *reinterpret_cast<const float2*>(scales + c0 + 2 * e);
+          pk[c0 / 2 + e] = pack_bf16x2(p0 * k.x, p1 * k.y);
         } else {
-          pk[e] = pack_bf16x2(p0, p1);
+          pk[c0 / 2 + e] = pack_bf16x2(p0, p1);
         }
       }
       return s0sum + s1sum;
@@ -352,15 +355,18 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       }
       if (got && releaser && lane == 0) mbar_arrive(smem_u32(&sh.bar_rel[j % kRels]));
       tc_fence_after();
-      uint32_t sr[NC], pk[NC / 2];
+      uint32_t sr[NB], pk[NC / 2];
       float part = 0.f;
       const bool fresh = WIDE ? j == 0 : first;
       bool slow = WIDE ? fresh : fresh && chain > 0;
       if (!fresh) {
         // P with the running max as it stands: a half whose P sums past NC x 2^8
         // holds a P above 2^8 (or a NaN), and the row takes the exact path
-        load_s(sr);
-        part = exps(sr, pk);
+#pragma unroll
+        for (int c0 = 0; c0 < NC; c0 += NB) {
+          load_s(c0, sr);
+          part += exps(c0, sr, pk);
+        }
         slow = bar_red_or(pbar, 64, !got || !(part <= kSpecSum));
       } else if (!WIDE && chain <= 0) {  // nothing to weigh yet
         if (bar_red_or(pbar, 64, !got)) slow = true;
@@ -374,10 +380,13 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
           ok = false;
           break;
         }
-        load_s(sr);
         float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < NC / 2; ++e) mx = fmax3(mx, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        for (int c0 = 0; c0 < NC; c0 += NB) {
+          load_s(c0, sr);
+#pragma unroll
+          for (int e = 0; e < NB / 2; ++e) mx = fmax3(mx, __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        }
         const float mrow = fmaxf(mx, exchange(mx));
         if (fresh) {
           m_used = mrow;
@@ -407,7 +416,13 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
             tmem_st16(lane_addr + colO + c * 16, r);
           }
         }
-        part = exps(sr, pk);
+        // the last columns, whose place in TMEM the exchange took, are still in registers
+        part = exps(NC - NB, sr, pk);
+#pragma unroll
+        for (int c0 = 0; c0 < NC - NB; c0 += NB) {
+          load_s(c0, sr);
+          part += exps(c0, sr, pk);
+        }
       }
       l += part;
       if constexpr (NC == 64) tmem_st32(lane_addr + colS, pk);
