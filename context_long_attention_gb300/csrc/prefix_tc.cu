@@ -226,8 +226,9 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
   // Columns in registers at a time: E4M3's further warps leave 80 registers a thread, which
-  // do not hold 64 scores and their P (64 x 32 heads behind 131,072 tokens: 516 us)
-  constexpr int NB = F8 && NC == 64 ? 32 : NC;
+  // do not hold 64 scores and their P (64 x 32 heads behind 131,072 tokens: 516 us with all 64
+  // of them, 204 with 32, 191 with 16)
+  constexpr int NB = F8 && NC == 64 ? 16 : NC;
   // a half row's P sum that can hide a P above 2^8
   constexpr float kSpecSum = NC * 256.f;
   const PrefixArgs& a = p.a;
@@ -270,6 +271,8 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
       if constexpr (NB == 64) {
         tmem_ld32(lane_addr + colS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tmem_ld32(lane_addr + colS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+      } else if constexpr (NB == 16) {
+        tmem_ld16(lane_addr + colS + c0, sr);
       } else {
         tmem_ld32(lane_addr + colS + c0, sr);
       }
