@@ -226,9 +226,9 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
   // Columns in registers at a time: E4M3's further warps leave 80 registers a thread, which
-  // do not hold 64 scores and their P (64 x 32 heads behind 131,072 tokens: 516 us with all 64
-  // of them, 204 with 32, 191 with 16)
-  constexpr int NB = F8 && NC == 64 ? 16 : NC;
+  // do not hold a half's scores and their P (64 x 32 heads behind 131,072 tokens: 516 us with
+  // all 64 of them, 190 with 16; blocks of 64 rows, 16 x 32 heads: 117 us with 32, 99 with 16)
+  constexpr int NB = F8 ? 16 : NC;
   // a half row's P sum that can hide a P above 2^8
   constexpr float kSpecSum = NC * 256.f;
   const PrefixArgs& a = p.a;
