@@ -225,10 +225,10 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   constexpr int kRels = F8 ? 3 : C::kSlots;  // barriers of the releases
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
   constexpr int NC = NS / 2;           // of one half of a row
-  // Columns in registers at a time: E4M3's further warps leave 80 registers a thread, which
-  // do not hold a half's scores and their P (64 x 32 heads behind 131,072 tokens: 516 us with
-  // all 64 of them, 190 with 16; blocks of 64 rows, 16 x 32 heads: 117 us with 32, 99 with 16)
-  constexpr int NB = F8 ? 16 : NC;
+  // Score columns in registers at a time: all of a half's and their P need more registers than
+  // a thread has (80 over E4M3, with its further warps: 64 x 32 heads behind 131,072 tokens took
+  // 516 us and take 190, 16 x 32 heads 117 and 96; bf16, 96 registers: 300 x 64 heads 124 and 119)
+  constexpr int NB = 16;
   // a half row's P sum that can hide a P above 2^8
   constexpr float kSpecSum = NC * 256.f;
   const PrefixArgs& a = p.a;
@@ -268,14 +268,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     int keys = 0;                  // of this half's columns, those in use in this tile
     const float* scales = nullptr;  // E4M3: of this half's columns
     auto load_s = [&](int c0, uint32_t (&sr)[NB]) {  // columns [c0, c0 + NB) of the half
-      if constexpr (NB == 64) {
-        tmem_ld32(lane_addr + colS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld32(lane_addr + colS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-      } else if constexpr (NB == 16) {
-        tmem_ld16(lane_addr + colS + c0, sr);
-      } else {
-        tmem_ld32(lane_addr + colS + c0, sr);
-      }
+      tmem_ld16(lane_addr + colS + c0, sr);
       tmem_ld_wait();
       if constexpr (F8) {
 #pragma unroll
