@@ -28,7 +28,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // A warp a row m, lane l holding dims l, l + 32, ...: every shape that the tensor
-// cores do not take (fp32, other head dims, a paged FP8 pool).
+// cores do not take (fp32, other head dims).
 constexpr int kSimtWarps = 4;
 template <typename TQ, typename T, int ND>
 __global__ void __launch_bounds__(kSimtWarps * 32) prefix_simt_kernel(const PrefixArgs a) {

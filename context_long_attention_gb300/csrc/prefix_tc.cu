@@ -25,15 +25,15 @@
 // P is rounded to bf16 for its product, its sum is not.
 // E4M3 (F8): S multiplies K's codes as they are stored, with the queries as two E4M3
 // numbers each, hi + lo of the row times a power of two that brings its largest element
-// to [128, 256) (4 + 4 significant bits hold bf16's 8, down to 2^-17 of the largest); warps
-// 18-21 turn V's codes into bf16 (exact) and take the relay's part, since P needs the
-// range that bf16 has.  A token's scale multiplies its column of S and, once P's sum is
-// taken, of P.
+// to [128, 256) (4 + 4 significant bits hold bf16's 8, down to 2^-17 of the largest); V's
+// codes become bf16 (exact), since P needs the range that bf16 has: warps 18-21 convert them
+// and take the relay's part, but in blocks of up to 64 rows the softmax warps without rows
+// convert.  A token's scale multiplies its column of S and, once P's sum is taken, of P.
 // What bounds it: 64 requests x 32 heads behind 32,768 keys of 8 kv heads (134 MB) take
-// 48 us with the merge, 0.42 of HBM: 14 tiles of 1.5 us, at HBM's rate, and some 20 us of
+// 48-50 us with the merge, 0.4 of HBM: 14 tiles of 1.5 us, at HBM's rate, and some 20 us of
 // plan and first loads, the last product, fp32 parts and merge.  300 x 64 heads behind
-// 85,000 keys in five groups: 124 us.  16 x 64 heads behind 131,072 E4M3 keys: 137 us, bound by
-// V's conversion (2.5 us a tile, 99 us in all if an eighth is converted).
+// 85,000 keys in five groups: 119 us.  131,072 E4M3 keys: 16 x 32 heads 95 us, a chain of
+// 54 tiles of 1.4 us; 32 x 32 heads 134 us and 64 x 32 heads 190, bound by V's conversion (four warps).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -55,7 +55,8 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kWarpTma = kSoftmaxWarps, kWarpMma = kSoftmaxWarps + 1, kWarpRelay = kSoftmaxWarps + 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
-// E4M3: in a block of up to so many rows half of the softmax warps have none, and convert V.
+// E4M3: in a block of up to so many rows half of the softmax warps have none, and convert V
+// (16 x 32 heads behind 131,072 tokens 135 -> 128 us).
 constexpr int kHelpRows = 64;
 
 template <int D, bool F8>
