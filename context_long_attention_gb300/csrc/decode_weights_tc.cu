@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // pair's rows lies past the pool and reads zeros), found one tile ahead
       auto locate = [&](int j, int half) {
         const int i = it.row_begin + j * kRows + 64 * half;
-        return (int)(i < it.pd.rows ? map_row(a.rm, it.pair, 0, i) : a.rm.pool_rows);
+        return (int)(i < it.pd.rows ? map_row_early(a.rm, it.pair, 0, i) : a.rm.pool_rows);
       };
       int y0 = 0, y1 = 0;
       if (it.ntiles > 0) {

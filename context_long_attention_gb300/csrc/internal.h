@@ -69,6 +69,14 @@ __device__ __forceinline__ long long map_row(const RowMap& m, int pair, long lon
   const int page = __ldg(m.table + (long long)pair * m.max_pages + i / m.page_size);
   return (long long)page * m.page_size + i % m.page_size;
 }
+// The same in a kernel that may start before the one before it ends (early_launch.cuh):
+// that one may be cp_page_slots, so the table's entry comes from the L2, never
+// through the read-only path, which may hold the line as it was.
+__device__ __forceinline__ long long map_row_early(const RowMap& m, int pair, long long row_off, int i) {
+  if (!m.table) return row_off + i;
+  const int page = __ldcg(m.table + (long long)pair * m.max_pages + i / m.page_size);
+  return (long long)page * m.page_size + i % m.page_size;
+}
 #endif
 
 // Returns the device address of this device's status words (set up once per device).

@@ -551,8 +551,8 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         // two 64-row halves, each inside one page; a half behind the pair's rows lies past
         // the pool and reads zeros
         const int pair = w.r * a.R + it.group;
-        y0 = (int)map_row(a.rm, pair, 0, row);
-        y1 = row + 64 < sh.rows[w.r] ? (int)map_row(a.rm, pair, 0, row + 64) : (int)a.rm.pool_rows;
+        y0 = (int)map_row_early(a.rm, pair, 0, row);
+        y1 = row + 64 < sh.rows[w.r] ? (int)map_row_early(a.rm, pair, 0, row + 64) : (int)a.rm.pool_rows;
         yr = 0;
       }
     };
@@ -657,7 +657,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
     auto scale_of = [&]() -> float {  // of this row of tile w.t; 0 behind the shard's last key
       const int in_pair = (w.t - w.off[w.r]) * BN + row, pair = w.r * a.R + it.group;
       if (in_pair >= sh.rows[w.r]) return 0.f;
-      return __ldcg(a.sc.p[w.r] + (a.rm.table ? map_row(a.rm, pair, 0, in_pair) : (long long)sh.row_off[w.r] + in_pair));
+      return __ldcg(a.sc.p[w.r] + (a.rm.table ? map_row_early(a.rm, pair, 0, in_pair) : (long long)sh.row_off[w.r] + in_pair));
     };
     auto put_scale = [&](int j, float x) {
       sc.scale[j % 3][row] = x;
@@ -863,8 +863,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         int y0 = it.first_y, y1 = 0;
         if (a.rm.table) {
           const int pair = it.first_shard * a.R + it.group;
-          y0 = (int)map_row(a.rm, pair, 0, it.first_row);
-          y1 = it.first_row + 64 < it.first_rows ? (int)map_row(a.rm, pair, 0, it.first_row + 64) : (int)a.rm.pool_rows;
+          y0 = (int)map_row_early(a.rm, pair, 0, it.first_row);
+          y1 = it.first_row + 64 < it.first_rows ? (int)map_row_early(a.rm, pair, 0, it.first_row + 64) : (int)a.rm.pool_rows;
         }
         const CUtensorMap* map = &maps.k[a.rm.table ? 0 : it.first_shard];
         const uint32_t full = smem_u32(&sh.bar_unit[0]), dst = smem_u32(F8 ? sQ + C::kCodes : sQ + C::kRing);
