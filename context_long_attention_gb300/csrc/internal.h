@@ -70,11 +70,13 @@ __device__ __forceinline__ long long map_row(const RowMap& m, int pair, long lon
   return (long long)page * m.page_size + i % m.page_size;
 }
 // The same in a kernel that may start before the one before it ends (early_launch.cuh):
-// that one may be cp_page_slots, so the table's entry comes from the L2, never
-// through the read-only path, which may hold the line as it was.
+// that one may be cp_page_slots, so the table's entry is an ordinary load behind
+// wait_for_earlier_kernels(), never one of the read-only path, which may hold the line as
+// it was.  (Around the L1, by __ldcg, it is as right and slower: 300 queries x 64 heads over
+// five prefixes in pages 118 -> 122 us, weights of 64 x 20,000 latent entries 94 -> 97.)
 __device__ __forceinline__ long long map_row_early(const RowMap& m, int pair, long long row_off, int i) {
   if (!m.table) return row_off + i;
-  const int page = __ldcg(m.table + (long long)pair * m.max_pages + i / m.page_size);
+  const int page = m.table[(long long)pair * m.max_pages + i / m.page_size];
   return (long long)page * m.page_size + i % m.page_size;
 }
 #endif
