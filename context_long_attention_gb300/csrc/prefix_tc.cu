@@ -26,7 +26,7 @@
 // E4M3 (F8): S multiplies K's codes as they are stored, with the queries as two E4M3
 // numbers each, hi + lo of the row times a power of two that brings its largest element
 // to [128, 256) (4 + 4 significant bits hold bf16's 8, down to 2^-17 of the largest); V's
-// codes become bf16 (exact), since P needs the range that bf16 has: warps 18-21 convert them
+// codes become bf16 (exact; a NaN code NaN), since P needs the range that bf16 has: warps 18-21 convert them
 // and take the relay's part, but in blocks of up to 64 rows the softmax warps without rows
 // convert.  A token's scale multiplies its column of S and, once P's sum is taken, of P.
 // What bounds it: 64 requests x 32 heads behind 32,768 keys of 8 kv heads (134 MB) take
@@ -114,12 +114,15 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // Four E4M3 codes as bf16, two words of two.  With the code's exponent and mantissa at
 // bf16's place a code is 2^-120 of its value (subnormal codes are subnormal bf16),
 // and the product with 2^120 is exact.
-__device__ __forceinline__ void bf16_of_codes(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+// *top: the largest magnitude so far, two at a time in the upper bytes of halves.
+__device__ __forceinline__ void bf16_of_codes(uint32_t codes, uint32_t& lo, uint32_t& hi, uint32_t& top) {
   const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);  // codes in the upper bytes of halves
-  const uint32_t x = (a & 0x80008000u) | ((a & 0x7f007f00u) >> 4), y = (b & 0x80008000u) | ((b & 0x7f007f00u) >> 4);
+  const uint32_t m = a & 0x7f007f00u, n = b & 0x7f007f00u;
+  const uint32_t x = (a & 0x80008000u) | (m >> 4), y = (b & 0x80008000u) | (n >> 4);
   const uint32_t k = 0x7b807b80u;  // 2^120 twice
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(k));
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(k));
+  top = __vimax3_u16x2(top, m, n);
 }
 // Eight elements of a query row, whose 16 lanes stand side by side, as E4M3 hi and lo of
 // the row times 2^(7 - e), its largest magnitude in [2^e, 2^(e+1)); *inv = 2^(e - 7).
@@ -152,22 +155,34 @@ __device__ __forceinline__ void put_codes(const uint4& x, uint8_t* row, int swiz
   *reinterpret_cast<uint2*>(at + BM * 128) = make_uint2(lo[0], lo[1]);
 }
 // Chunks [c0, c0 + N) of 16 codes of a V tile's row as bf16, both 128-byte-swizzled; `to`
-// is the row in the first of the bf16 tile's two 64-dim chunks of BN rows.
+// is the row in the first of the bf16 tile's two 64-dim chunks of BN rows.  A NaN code
+// (0x7F, 0xFF) becomes +-480 here; true if there is one (nan_codes puts it right).
 template <int N>
-__device__ __forceinline__ void convert_row(const uint8_t* from, uint8_t* to, int row, int c0) {
+__device__ __forceinline__ bool convert_row(const uint8_t* from, uint8_t* to, int row, int c0) {
   const uint4* src = reinterpret_cast<const uint4*>(from);
+  uint32_t top = 0;
 #pragma unroll 4
   for (int c = c0; c < c0 + N; ++c) {
     const uint4 x = src[c ^ (row & 7)];
     uint32_t o[8];
-    bf16_of_codes(x.x, o[0], o[1]);
-    bf16_of_codes(x.y, o[2], o[3]);
-    bf16_of_codes(x.z, o[4], o[5]);
-    bf16_of_codes(x.w, o[6], o[7]);
+    bf16_of_codes(x.x, o[0], o[1], top);
+    bf16_of_codes(x.y, o[2], o[3], top);
+    bf16_of_codes(x.z, o[4], o[5], top);
+    bf16_of_codes(x.w, o[6], o[7], top);
     uint8_t* chunk = to + (c >> 2) * (BN * 128);
     const int unit = 2 * (c & 3);
     *reinterpret_cast<uint4*>(chunk + ((unit ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(chunk + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  return (top & 0xffffu) == 0x7f00u || top >> 16 == 0x7f00u;
+}
+// The NaN codes of those chunks as bf16 NaN: hardly ever called.
+__device__ __noinline__ void nan_codes(const uint8_t* from, uint8_t* to, int row, int c0, int n) {
+#pragma unroll 1
+  for (int d = 16 * c0; d < 16 * (c0 + n); ++d) {
+    if ((from[((d >> 4 ^ (row & 7)) << 4) + (d & 15)] & 0x7f) != 0x7f) continue;
+    const int at = (((d >> 3 & 7) ^ (row & 7)) << 4) + 2 * (d & 7);
+    *reinterpret_cast<uint16_t*>(to + (d >> 6) * (BN * 128) + at) = 0x7fff;
   }
 }
 __device__ __forceinline__ void mbar_inval(uint32_t bar) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
@@ -222,6 +237,12 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   auto v_codes = [&](int j) {
     const int slot = j % kVSlots;
     return sQ + (slot < 2 ? C::kCodes + (C::kKSlots + slot) * C::kCodeBytes : C::kQBytes);
+  };
+  // keys of the item's tile j, where a row of it has a NaN code (rows behind them may have
+  // any, and meet weights of 0: they stay finite)
+  auto keys_of = [&](int j) {
+    const Walk w(sh.tile_off, sh.item.tile_begin + j);
+    return sh.rows[w.r] - (w.t - w.off[w.r]) * BN;
   };
   constexpr int kRels = F8 ? 3 : C::kSlots;  // barriers of the releases
   constexpr int NS = WIDE ? 128 : 64;  // score columns of a chain
@@ -323,7 +344,8 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
           break;
         }
         if (v == nK) break;
-        convert_row<4>(v_codes(v) + vrow * 128, sKV + (v % C::kSlots) * C::kSlotBytes + vrow * 128, vrow, 4 * half);
+        uint8_t* to = sKV + (v % C::kSlots) * C::kSlotBytes + vrow * 128;
+        if (convert_row<4>(v_codes(v) + vrow * 128, to, vrow, 4 * half) && vrow < keys_of(v)) nan_codes(v_codes(v) + vrow * 128, to, vrow, 4 * half, 4);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.bar_unit[6 + v % kVSlots]));
@@ -679,9 +701,10 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
         if (lane == 0) report_timeout(p.status, 5, abort);
         break;
       }
-      // rows behind the shard's last key meet weights of 0: any finite value will do
+      // rows behind the shard's last key meet weights of 0: any finite value will do (a NaN code's, too)
       if (it.m_rows > kHelpRows) {
-        convert_row<8>(v_codes(j) + row * 128, sKV + (j % C::kSlots) * C::kSlotBytes + row * 128, row, 0);
+        uint8_t* to = sKV + (j % C::kSlots) * C::kSlotBytes + row * 128;
+        if (convert_row<8>(v_codes(j) + row * 128, to, row, 0) && row < keys_of(j)) nan_codes(v_codes(j) + row * 128, to, row, 0, 8);
         fence_proxy_async_smem();
       }
       __syncwarp();
