@@ -73,10 +73,13 @@ __device__ __forceinline__ long long map_row(const RowMap& m, int pair, long lon
 // that one may be cp_page_slots, so the table's entry is an ordinary load behind
 // wait_for_earlier_kernels(), never one of the read-only path, which may hold the line as
 // it was.  (Around the L1, by __ldcg, it is as right and slower: 300 queries x 64 heads over
-// five prefixes in pages 118 -> 122 us, weights of 64 x 20,000 latent entries 94 -> 97.)
+// five prefixes in pages 118 -> 122 us, weights of 64 x 20,000 latent entries 94 -> 97.
+// Written as m.table[...] the compiler joins both branches' loads and waits for them: 16 x 32
+// heads behind 131,072 E4M3 tokens in shards 94 -> 121 us.)
 __device__ __forceinline__ long long map_row_early(const RowMap& m, int pair, long long row_off, int i) {
   if (!m.table) return row_off + i;
-  const int page = m.table[(long long)pair * m.max_pages + i / m.page_size];
+  int page;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(page) : "l"(m.table + (long long)pair * m.max_pages + i / m.page_size) : "memory");
   return (long long)page * m.page_size + i % m.page_size;
 }
 #endif
