@@ -435,13 +435,17 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
             tmem_st16(lane_addr + colO + c * 16, r);
           }
         }
-        // the last columns, whose place in TMEM the exchange took, are still in registers
-        part = exps(NC - NB, sr, pk);
+        // the last columns, whose place in TMEM the exchange took, are still in registers; the
+        // sum goes by rising column as above, so that a row's bits do not depend on whether
+        // another row of the warp takes this path
+        const float last = exps(NC - NB, sr, pk);
+        part = 0.f;
 #pragma unroll
         for (int c0 = 0; c0 < NC - NB; c0 += NB) {
           load_s(c0, sr);
           part += exps(c0, sr, pk);
         }
+        part += last;
       }
       l += part;
       if constexpr (NC == 64) tmem_st32(lane_addr + colS, pk);
