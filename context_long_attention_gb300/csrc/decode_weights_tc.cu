@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               // 2^(7 - e) brings a largest element of [2^e, 2^(e+1)) to [128, 256)
               const int e = max(-100, (int)(top >> 23) - 127);
               const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
-              if (lane == 0) sF[kh * NP + n] = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+              // an infinite element would become 448: the row's scores are NaN instead
+              if (lane == 0) sF[kh * NP + n] = __uint_as_float(e < 128 ? (uint32_t)(e - 7 + 127) << 23 : 0x7fffffffu);
               uint8_t* base = sQ + kh * p.chunks * NT * 128 + 4 * (lane & 3);
 #pragma unroll
               for (int c = 0; c < kPer; ++c) {

@@ -134,7 +134,8 @@ __device__ __forceinline__ void put_codes(const uint4& x, uint8_t* row, int swiz
   for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   const int e = max(-100, (int)(m >> 23) - 127);
   const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
-  if (piece == 0) *inv = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+  // an infinite element would become 448: the row's scores are NaN instead
+  if (piece == 0) *inv = __uint_as_float(e < 128 ? (uint32_t)(e - 7 + 127) << 23 : 0x7fffffffu);
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
   uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
