@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kBitThreads) evict_bits_kernel(const EvictArgs
   const bool bad = __syncthreads_or(outside);
   int32_t* src = a.src + (long long)pair * a.max_moves;
   int32_t* dst = a.dst + (long long)pair * a.max_moves;
-  int moves = bad_len ? -1 : 0;
-  if (m > 0 && m < n) {
+  int moves = bad_len || bad ? -1 : 0;
+  if (m > 0 && m < n && !bad) {
     // keys that are at least t, of the whole block
     int turn = 0;
     auto reach = [&](uint32_t t) {
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kBitThreads) evict_bits_kernel(const EvictArgs
     int hole[R], mover[R];
     moves = before(s_holes, hole);
     before(s_movers, mover);
-    if (bad || moves > a.max_moves) {
+    if (moves > a.max_moves) {
       moves = -1;
     } else {
 #pragma unroll
@@ -216,6 +216,14 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const SelectParams p) 
     return good;
   };
   int moves = bad_len ? -1 : 0;
+  if (n > 0 && !(m > 0 && m < n)) {  // all rows stay or none: of the pages nothing is asked but that they are there
+    bool bad = false;
+    for (int pg = tid; pg <= p.by_page(n - 1); pg += NT) {
+      const int id = __ldcg(table + pg);
+      bad |= id < 0 || id >= a.num_pages;
+    }
+    if (__syncthreads_or(bad)) moves = -1;
+  }
   if (m > 0 && m < n) {
     if (tid == 0) {
       s_prefix = 0;

@@ -796,9 +796,9 @@ cp_status cp_decode_weights(const void* host_plan, const void* dev_plan, cp_deco
  *   each pair r B + b, count moves and the pool rows src -> dst of each: the kept
  *   rows at or behind m, in order, into the places of the evicted rows before m, in
  *   order; -1 behind the last ([C B][max_moves], count [C B]).  A pair whose lengths
- *   are negative or past its pages, which has a page id outside [0, num_pages) or
- *   needs more than max_moves moves (min(m, n - m) is enough) gets count = -1 and
- *   no move.  Nothing else is written.
+ *   are negative or past its pages, which has a page id outside [0, num_pages) among
+ *   the pages of its n rows (whatever it keeps) or needs more than max_moves moves
+ *   (min(m, n - m) is enough) gets count = -1 and no move.  Nothing else is written.
  * cp_cache_move: the moves, on the rows of k_pool and (or NULL) v_pool, of
  *   row_bytes each (a multiple of 16), and the words of scale_pool, weights and
  *   pos (each or NULL).  A pair of count <= 0 and a move of a row outside the pool
