@@ -1398,8 +1398,9 @@ def cp_evict_select(pages: PageTable, C: int, ctx_len, keep_len, weights, max_mo
                     keep_from=None, src=None, dst=None, count=None):
     """Which rows every pair (shard, request) keeps when its request goes from
     ctx_len[b] to keep_len[b] cached tokens ([B] int32 on the GPU): rows of
-    position < keep_below or >= keep_from[b], then the heaviest by ``weights``
-    [pool_rows].  Returns the moves that bring the kept rows together, for
+    position in [0, keep_below) or >= keep_from[b], then the heaviest by ``weights``
+    [pool_rows].  ``pos`` [pool_rows] is the caller's: appended tokens' positions go to
+    their slots; a negative one protects nothing.  Returns the moves that bring the kept rows together, for
     cp_cache_move: (src, dst [C B, max_moves] pool rows, -1 behind the last;
     count [C B], -1 for a pair that does not fit: see cpattn.h)."""
     table, dev, B = _evict_table(pages, C, ctx_len, keep_len)

@@ -34,6 +34,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Protected by its position: below keep_below, or from `start`, its request's keep_from, on.  A negative
+// position, which nobody has written, protects nothing.
+__device__ __forceinline__ bool protects(const EvictArgs& a, int pos, int start) {
+  return pos >= 0 && (pos < a.keep_below || (a.keep_from && pos >= start));
+}
+
 // Pairs of up to R x 1,024 rows: the keys stay in registers, R of a thread (rows
 // tid, tid + NT, ...), and the m-th largest one is found bit by bit: it is the largest T
 // that at least m keys reach.  A bit is one count over the block and one barrier (512
@@ -72,7 +78,7 @@ __global__ void __launch_bounds__(kBitThreads) evict_bits_kernel(const EvictArgs
       w[k] = in && i < n ? __ldcg(a.weights + row[k]) : 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < R; ++k) key[k] = pos[k] < a.keep_below || (a.keep_from && pos[k] >= start) ? kProtected : weight_key(w[k]);
+    for (int k = 0; k < R; ++k) key[k] = protects(a, pos[k], start) ? kProtected : weight_key(w[k]);
   }
   const bool bad = __syncthreads_or(outside);
   int32_t* src = a.src + (long long)pair * a.max_moves;
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const SelectParams p) 
     const int row = pool_row(i);
     if (row < 0) return 0;
     const int pos = a.pos ? a.pos[row] : i * a.C + r;
-    if (pos < a.keep_below || (a.keep_from && pos >= start)) return kProtected;
+    if (protects(a, pos, start)) return kProtected;
     return weight_key(a.weights[row]);
   };
   auto key_of = [&](int i) { return i < p.cached ? s_key[i] : read_key(i); };
@@ -210,8 +216,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const SelectParams p) 
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * NT;
-      const bool safe = pos[k] < a.keep_below || (a.keep_from && pos[k] >= start);
-      if (i < n && i < p.cached) s_key[i] = safe ? kProtected : weight_key(w[k]);
+      if (i < n && i < p.cached) s_key[i] = protects(a, pos[k], start) ? kProtected : weight_key(w[k]);
     }
     return good;
   };

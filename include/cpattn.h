@@ -785,9 +785,12 @@ cp_status cp_decode_weights(const void* host_plan, const void* dev_plan, cp_deco
  * device).  Its pair on shard r has n = ceil((ctx_len - r) / C) rows and keeps
  * the m = min(n, ceil((keep_len - r) / C)) first of them in this order:
  * protected rows, by rising row; then the others by falling weight, equal ones by
- * rising row, a NaN weight last.  Protected: rows of position < keep_below or (keep_from [B] given)
- * >= keep_from[b], where pos [pool_rows] int32 holds each row's position; pos
- * NULL: row i of shard r is token i C + r, as before any eviction.
+ * rising row, a NaN weight last.  Protected: rows of position in [0, keep_below) or
+ * (keep_from [B] given) >= max(0, keep_from[b]), where pos [pool_rows] int32 holds each
+ * row's position; pos NULL: row i of shard r is token i C + r, as before any eviction.
+ * pos belongs to the caller: the positions of appended tokens go to their slots
+ * (cp_page_slots) as the tokens' rows do.  A negative entry, as cp_page_release
+ * leaves it where rows are free, is a position that nobody has written and protects nothing.
  * Afterwards the pair's rows 0 .. m - 1 hold the kept tokens, in no order of
  * position, and plans, tables and slots of keep_len tokens (CP_DCP_ROUND_ROBIN,
  * one query row) describe the cache.

@@ -1,11 +1,12 @@
 """Eviction where its inputs are at their edges: pages that are not there in pairs
-that keep all or nothing."""
+that keep all or nothing, and positions that nobody has written."""
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_evict import Pool, i32, shard_rows
-from test_gpu_parity import cp  # noqa: F401
+from test_gpu_evict import I32, Pool, i32, shard_rows
+from test_gpu_parity import DEV, cp  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,44 @@ def test_a_page_that_is_not_there(cp, L, bad):
     # a request without tokens has no page
     p.pages.dev.fill_(ident)
     assert (cp.cp_evict_select(p.pages, 2, i32([0] * 3), i32([0, 1, 5]), p.w, 3)[2] == 0).all()
+
+
+@pytest.mark.parametrize("C,ctx,keep", [(2, 300, 200), (1, 3000, 100), (1, 9000, 8999), (8, 5000, 512)])
+@pytest.mark.parametrize("below", [0, 4])
+def test_a_position_that_nobody_has_written(cp, C, ctx, keep, below):
+    """Rows of a negative position are protected by neither bound: they stay by their weight."""
+    p = Pool(cp, C, [ctx], (16,), seed=ctx)
+    rng = np.random.default_rng(3)
+    w = rng.random(p.w.numel()).astype(np.float32)
+    pos = np.full(w.size, -1, np.int32)
+    for r in range(C):
+        at = p.rows(0, r)
+        known = rng.random(at.size) < 0.5
+        pos[at[known]] = (np.arange(at.size) * C + r)[known]
+        pos[at[~known]] = rng.choice([-1, -2, -2**31], int((~known).sum()))
+    start = ctx - 20
+    most = max(1, min(shard_rows(ctx, C, 0), shard_rows(keep, C, 0)))
+    src, dst, count = cp.cp_evict_select(p.pages, C, i32([ctx]), i32([keep]), torch.from_numpy(w).to(DEV), most, pos=torch.from_numpy(pos).to(DEV),
+                                         keep_below=below, keep_from=i32([start]))
+    src, dst, count = (x.cpu().numpy() for x in (src, dst, count))
+    for r in range(C):
+        at, m = p.rows(0, r), shard_rows(keep, C, r)
+        where = pos[at]
+        safe = ((where >= 0) & (where < below)) | (where >= start)
+        rank = sorted(range(at.size), key=lambda i: (not safe[i], 0.0 if safe[i] else -float(w[at[i]]), i))
+        stay = sorted(rank[:m])
+        late, holes = [i for i in stay if i >= m], sorted(set(range(m)) - set(stay))
+        assert count[r] == len(late)
+        assert src[r, :len(late)].tolist() == at[late].tolist() and dst[r, :len(late)].tolist() == at[holes].tolist()
+
+
+def test_tokens_appended_without_positions(cp):
+    """A released row's position is -1: tokens put there compete by weight."""
+    p = Pool(cp, 1, [128], (16,))
+    pos = torch.full((p.w.numel(),), -1, **I32)
+    at = torch.from_numpy(p.rows(0, 0)).to(DEV)
+    pos[at[:64]] = torch.arange(64, **I32)
+    w = torch.ones_like(p.w)
+    w[at[64:]] = 0.5  # new tokens, lighter
+    src, dst, count = cp.cp_evict_select(p.pages, 1, i32([128]), i32([64]), w, 64, pos=pos, keep_from=i32([1000]))
+    assert count.item() == 0
