@@ -101,7 +101,9 @@ _SIGS = {
     "cp_decode_weights": (_i, [_vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp]),
     "cp_evict_select": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp]),
     "cp_cache_move": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i64, _vp]),
+    "cp_cache_move_ex": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i64, _vp]),
     "cp_page_release": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp]),
+    "cp_page_release_ex": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -1427,10 +1429,12 @@ def cp_evict_select(pages: PageTable, C: int, ctx_len, keep_len, weights, max_mo
     return src, dst, count
 
 
-def cp_cache_move(src, dst, count, k_pool, v_pool=None, scale_pool=None, weights=None, pos=None):
+def cp_cache_move(src, dst, count, k_pool, v_pool=None, scale_pool=None, weights=None, pos=None, C: int = 0):
     """The moves of cp_evict_select on a pool's rows, in place: k_pool and v_pool
     [pool_rows, ...], and scale_pool, weights (fp32) and pos (int32) [pool_rows]
-    where they are given."""
+    where they are given.  With the number of shards ``C`` requests move whole: where a
+    pair's choice did not fit (count -1) its request stays as it is on all
+    shards; without it such pairs alone are skipped."""
     dev, rows = k_pool.get_device(), k_pool.shape[0]
     pairs, most = src.shape
     _need("src", src, _i32t, (pairs, most), dev)
@@ -1443,8 +1447,14 @@ def cp_cache_move(src, dst, count, k_pool, v_pool=None, scale_pool=None, weights
         if t is not None:
             _need(name, t, dtype, (rows,), dev)
     if dev != _device_index():
-        return _on(dev, cp_cache_move, src, dst, count, k_pool, v_pool, scale_pool, weights, pos)
-    st = lib.cp_cache_move(pairs, most, src.data_ptr(), dst.data_ptr(), count.data_ptr(), k_pool.data_ptr(),
+        return _on(dev, cp_cache_move, src, dst, count, k_pool, v_pool, scale_pool, weights, pos, C)
+    if C:
+        if C < 0 or pairs % C:
+            raise ValueError(f"{pairs} pairs are no multiple of C={C}")
+        shape, call = (C, pairs // C), lib.cp_cache_move_ex
+    else:
+        shape, call = (pairs,), lib.cp_cache_move
+    st = call(*shape, most, src.data_ptr(), dst.data_ptr(), count.data_ptr(), k_pool.data_ptr(),
                            None if v_pool is None else v_pool.data_ptr(), k_pool.shape[1:].numel() * k_pool.element_size(),
                            None if scale_pool is None else scale_pool.data_ptr(), None if weights is None else weights.data_ptr(),
                            None if pos is None else pos.data_ptr(), rows, _raw_stream(dev))
@@ -1452,12 +1462,15 @@ def cp_cache_move(src, dst, count, k_pool, v_pool=None, scale_pool=None, weights
         _check(st)
 
 
-def cp_page_release(pages: PageTable, C: int, ctx_len, keep_len, free_ids, free_pos, weights=None, pos=None, info=None):
+def cp_page_release(pages: PageTable, C: int, ctx_len, keep_len, free_ids, free_pos, weights=None, pos=None, info=None,
+                    count=None):
     """Hands the pages that shorter requests no longer need back to free_ids, below
     free_pos ([1] int32, or an earlier call's info[1:2]), clears their table entries
-    and the weights and positions of the rows behind the new lengths.  Returns
-    info [4] = status, next free_pos, pages released, 0.  Like cp_page_slots it drops the
-    table's host copy (``pages.sync_host()``)."""
+    and the weights and positions of the rows behind the new lengths.  With the
+    ``count`` of cp_evict_select a request one of whose pairs did not fit (count -1)
+    stays as it is.  Returns info [4] = status, next free_pos, pages released, requests
+    that stay as they are.  Like cp_page_slots it drops the table's host copy
+    (``pages.sync_host()``)."""
     table, dev, B = _evict_table(pages, C, ctx_len, keep_len)
     n_free, rows = free_ids.shape[0], pages.pool_rows
     if n_free > _MAX_COUNT:
@@ -1466,15 +1479,17 @@ def cp_page_release(pages: PageTable, C: int, ctx_len, keep_len, free_ids, free_
     _need("free_pos", free_pos, _i32t, (1,), dev)
     if weights is not None:
         _need("weights", weights, _f32, (rows,), dev)
+    if count is not None:
+        _need("count", count, _i32t, (C * B,), dev)
     if pos is not None:
         _need("pos", pos, _i32t, (rows,), dev)
     if dev != _device_index():
-        return _on(dev, cp_page_release, pages, C, ctx_len, keep_len, free_ids, free_pos, weights, pos, info)
+        return _on(dev, cp_page_release, pages, C, ctx_len, keep_len, free_ids, free_pos, weights, pos, info, count)
     info = torch.empty(4, dtype=_i32t, device=table.device) if info is None else _need("info", info, _i32t, (4,), dev)
-    st = lib.cp_page_release(C, B, ctx_len.data_ptr(), keep_len.data_ptr(), table.data_ptr(), pages.max_pages, pages.page_size,
-                             pages.num_pages, free_ids.data_ptr(), n_free, free_pos.data_ptr(),
-                             None if weights is None else weights.data_ptr(), None if pos is None else pos.data_ptr(),
-                             info.data_ptr(), _raw_stream(dev))
+    st = lib.cp_page_release_ex(C, B, ctx_len.data_ptr(), keep_len.data_ptr(), table.data_ptr(), pages.max_pages, pages.page_size,
+                                pages.num_pages, free_ids.data_ptr(), n_free, free_pos.data_ptr(),
+                                None if count is None else count.data_ptr(), None if weights is None else weights.data_ptr(),
+                                None if pos is None else pos.data_ptr(), info.data_ptr(), _raw_stream(dev))
     if st:
         _check(st)
     pages.host = None

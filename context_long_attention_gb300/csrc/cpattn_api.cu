@@ -953,6 +953,24 @@ cp_status check_pool_shape(int C, int B, int max_pages, int page_size, int num_p
   return CP_OK;
 }
 
+// C = B = 0: every pair on its own.
+cp_status run_cache_move(int pairs, int C, int B, int max_moves, const int32_t* src, const int32_t* dst, const int32_t* count,
+                         void* k_pool, void* v_pool, int row_bytes, float* scale_pool, float* weights, int32_t* pos,
+                         int64_t pool_rows, void* stream) {
+  if (pairs < 0 || max_moves < 1 || (long long)pairs * max_moves > 0x7FFFFFFFLL)
+    return fail(CP_ERR_INVALID_ARG, "pairs=%d must be >= 0, max_moves=%d >= 1, their product < 2^31", pairs, max_moves);
+  if (pool_rows < 1 || pool_rows > 0x7FFFFF00LL) return fail(CP_ERR_INVALID_ARG, "pool_rows=%lld out of range", (long long)pool_rows);
+  if (row_bytes < 16 || row_bytes % 16) return fail(CP_ERR_UNSUPPORTED, "row_bytes=%d is not a positive multiple of 16", row_bytes);
+  if (pairs == 0) return ok();
+  if (!src || !dst || !count || !k_pool) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(CP_ERR_INVALID_ARG, "a pool is not 16-byte aligned");
+  const MoveArgs a = {src, dst, count, pairs, max_moves, C, B, k_pool, v_pool, row_bytes,
+                      {(uint32_t*)scale_pool, (uint32_t*)weights, (uint32_t*)pos}, (long long)pool_rows};
+  const cudaError_t e = launch_cache_move(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache move kernel");
+  return ok();
+}
+
 }  // namespace
 
 // ====================================================================== C ABI
@@ -1938,23 +1956,28 @@ cp_status cp_evict_select(int C, int B, const int32_t* ctx_len, const int32_t* k
 cp_status cp_cache_move(int pairs, int max_moves, const int32_t* src, const int32_t* dst, const int32_t* count,
                         void* k_pool, void* v_pool, int row_bytes, float* scale_pool, float* weights, int32_t* pos,
                         int64_t pool_rows, void* stream) {
-  if (pairs < 0 || max_moves < 1 || (long long)pairs * max_moves > 0x7FFFFFFFLL)
-    return fail(CP_ERR_INVALID_ARG, "pairs=%d must be >= 0, max_moves=%d >= 1, their product < 2^31", pairs, max_moves);
-  if (pool_rows < 1 || pool_rows > 0x7FFFFF00LL) return fail(CP_ERR_INVALID_ARG, "pool_rows=%lld out of range", (long long)pool_rows);
-  if (row_bytes < 16 || row_bytes % 16) return fail(CP_ERR_UNSUPPORTED, "row_bytes=%d is not a positive multiple of 16", row_bytes);
-  if (pairs == 0) return ok();
-  if (!src || !dst || !count || !k_pool) return fail(CP_ERR_INVALID_ARG, "a pointer argument is NULL");
-  if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(CP_ERR_INVALID_ARG, "a pool is not 16-byte aligned");
-  const MoveArgs a = {src, dst, count, pairs, max_moves, k_pool, v_pool, row_bytes,
-                      {(uint32_t*)scale_pool, (uint32_t*)weights, (uint32_t*)pos}, (long long)pool_rows};
-  const cudaError_t e = launch_cache_move(a, (cudaStream_t)stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cache move kernel");
-  return ok();
+  return run_cache_move(pairs, 0, 0, max_moves, src, dst, count, k_pool, v_pool, row_bytes, scale_pool, weights, pos, pool_rows, stream);
+}
+
+cp_status cp_cache_move_ex(int C, int B, int max_moves, const int32_t* src, const int32_t* dst, const int32_t* count,
+                           void* k_pool, void* v_pool, int row_bytes, float* scale_pool, float* weights, int32_t* pos,
+                           int64_t pool_rows, void* stream) {
+  if (C < 1 || C > CP_MAX_SHARDS) return fail(CP_ERR_INVALID_ARG, "C=%d outside [1, %d]", C, CP_MAX_SHARDS);
+  if (B < 1 || B > CP_SLOTS_MAX_B) return fail(CP_ERR_INVALID_ARG, "B=%d outside [1, %d]", B, CP_SLOTS_MAX_B);
+  return run_cache_move(C * B, C, B, max_moves, src, dst, count, k_pool, v_pool, row_bytes, scale_pool, weights, pos, pool_rows, stream);
 }
 
 cp_status cp_page_release(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, int32_t* page_table,
                           int max_pages, int page_size, int num_pages, int32_t* free_ids, int n_free,
                           const int32_t* free_pos, float* weights, int32_t* pos, int32_t* info, void* stream) {
+  return cp_page_release_ex(C, B, ctx_len, keep_len, page_table, max_pages, page_size, num_pages, free_ids, n_free, free_pos,
+                            nullptr, weights, pos, info, stream);
+}
+
+cp_status cp_page_release_ex(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, int32_t* page_table,
+                             int max_pages, int page_size, int num_pages, int32_t* free_ids, int n_free,
+                             const int32_t* free_pos, const int32_t* count, float* weights, int32_t* pos, int32_t* info,
+                             void* stream) {
   const cp_status st = check_pool_shape(C, B, max_pages, page_size, num_pages);
   if (st != CP_OK) return st;
   if (n_free < 0) return fail(CP_ERR_INVALID_ARG, "n_free=%d must be >= 0", n_free);
@@ -1964,7 +1987,7 @@ cp_status cp_page_release(int C, int B, const int32_t* ctx_len, const int32_t* k
   if (free_pos >= info && free_pos < info + 4)
     return fail(CP_ERR_INVALID_ARG, "free_pos lies in this call's info: pass an earlier call's");
   const ReleaseArgs a = {C, B, ctx_len, keep_len, page_table, max_pages, page_size, num_pages, free_ids, n_free,
-                         free_pos, weights, pos, info};
+                         free_pos, count, weights, pos, info};
   const cudaError_t e = launch_page_release(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "page release kernel");
   return ok();

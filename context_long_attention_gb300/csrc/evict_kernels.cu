@@ -369,7 +369,12 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MovePara
   const int lane = threadIdx.x & 31, warp = part * (kMoveThreads / 32) + (threadIdx.x >> 5);
   const int step = p.splits * (kMoveThreads / 32);
   wait_for_earlier_kernels();
-  const int n = min(__ldcg(a.count + pair), a.max_moves);
+  int n = min(__ldcg(a.count + pair), a.max_moves);
+  if (a.B) {  // a request whole: none of it moves where a shard's choice did not fit
+    bool unfit = false;
+    for (int r = lane; r < a.C; r += 32) unfit |= __ldcg(a.count + r * a.B + pair % a.B) < 0;
+    if (__any_sync(0xffffffffu, unfit)) n = 0;
+  }
   const int vec = a.row_bytes / 16;
   for (long long j0 = warp; j0 < n; j0 += 32 * step) {
     const long long mine = j0 + lane * step;
@@ -420,9 +425,9 @@ struct ReleaseParams {
 // Every block sums over the requests for itself, as page_slots_kernel does;
 // then a warp a pair hands back its pages and clears the rows that it leaves.
 __global__ void __launch_bounds__(kReleaseThreads) page_release_kernel(const ReleaseParams p) {
-  extern __shared__ int32_t s_before[];  // [B] pages released before request b
+  extern __shared__ int32_t s_before[];  // [B] pages released before request b; -1: it stays as it is
   __shared__ uint32_t w_sum[kReleaseWarps];
-  __shared__ int w_bad[kReleaseWarps];
+  __shared__ int w_bad[kReleaseWarps], w_stay[kReleaseWarps];
   const ReleaseArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.B, C = a.C;
   wait_for_earlier_kernels();
@@ -440,8 +445,15 @@ __global__ void __launch_bounds__(kReleaseThreads) page_release_kernel(const Rel
     return K < L ? pages_before(have, C) - pages_before(page_count(p.by_c, p.by_page, K), C) : 0;
   };
   uint32_t sum = 0;
-  int bad = 0;
-  for (int b = b0; b < b1; ++b) sum = sat_add(sum, released(b, &bad));
+  int bad = 0, stay = 0;
+  for (int b = b0; b < b1; ++b) {
+    bool unfit = false;  // a shard's choice did not fit
+    if (a.count)
+      for (int r = 0; r < C; ++r) unfit |= __ldcg(a.count + r * B + b) < 0;
+    s_before[b] = unfit ? -1 : 0;
+    if (unfit) ++stay;
+    else sum = sat_add(sum, released(b, &bad));
+  }
   uint32_t in = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -449,25 +461,30 @@ __global__ void __launch_bounds__(kReleaseThreads) page_release_kernel(const Rel
     if (lane >= d) in = sat_add(in, x);
   }
   bad = __reduce_or_sync(0xffffffffu, bad);
+  stay = __reduce_add_sync(0xffffffffu, stay);
   if (lane == 31) {
     w_sum[warp] = in;
     w_bad[warp] = bad;
+    w_stay[warp] = stay;
   }
   __syncthreads();
   uint32_t before = 0, total = 0;
+  stay = 0;
 #pragma unroll
   for (int w = 0; w < kReleaseWarps; ++w) {
     if (w == warp) before = total;
     total = sat_add(total, w_sum[w]);
     bad |= w_bad[w];
+    stay += w_stay[w];
   }
   if (pos < 0 || pos > a.n_free || total > (uint32_t)pos) bad |= CP_SLOTS_NO_PAGES;
   if (blockIdx.x == 0 && tid == 0)
-    *reinterpret_cast<int4*>(a.info) = bad ? make_int4(bad, pos, 0, 0) : make_int4(0, pos - (int)total, (int)total, 0);
+    *reinterpret_cast<int4*>(a.info) = bad ? make_int4(bad, pos, 0, 0) : make_int4(0, pos - (int)total, (int)total, stay);
   if (bad) return;
   // nothing saturated: the sum is at most *free_pos
   int at = (int)(before + in - sum);
   for (int b = b0; b < b1; ++b) {
+    if (s_before[b] < 0) continue;
     s_before[b] = at;
     int ignored = 0;
     at += released(b, &ignored);
@@ -477,7 +494,7 @@ __global__ void __launch_bounds__(kReleaseThreads) page_release_kernel(const Rel
   for (int u = blockIdx.x * kReleaseWarps + warp; u < B * C; u += gridDim.x * kReleaseWarps) {
     const int b = p.by_c(u), r = u - b * C;
     const int L = a.ctx_len[b], K = a.keep_len[b];
-    if (K >= L) continue;
+    if (K >= L || s_before[b] < 0) continue;
     const PageCount have = page_count(p.by_c, p.by_page, L), want = page_count(p.by_c, p.by_page, K);
     const int q = p.by_c(K), rows = q + (r < K - q * C);  // the pair's new length
     const int h = pages_of(have, r), w = pages_of(want, r);

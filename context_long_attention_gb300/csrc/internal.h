@@ -330,6 +330,7 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s);
 struct MoveArgs {
   const int32_t *src, *dst, *count;
   int pairs, max_moves;
+  int C, B;                           // pairs r B + b; B = 0: each on its own
   void *k, *v;
   int row_bytes;
   uint32_t* words[3];                 // pools of one word a row (scales, weights, positions) or nullptr
@@ -344,6 +345,7 @@ struct ReleaseArgs {
   int32_t* free_ids;
   int n_free;
   const int32_t* free_pos;
+  const int32_t* count;               // [C * B], of cp_evict_select, or nullptr
   float* weights;                     // [pool_rows] or nullptr
   int32_t *pos, *info;                // [pool_rows] or nullptr; [4]
 };

@@ -806,21 +806,28 @@ cp_status cp_decode_weights(const void* host_plan, const void* dev_plan, cp_deco
  *   row_bytes each (a multiple of 16), and the words of scale_pool, weights and
  *   pos (each or NULL).  A pair of count <= 0 and a move of a row outside the pool
  *   are skipped.  All sources must differ from all destinations.
+ * cp_cache_move_ex: the same over the C B pairs of requests that move whole: where a
+ *   pair of a request has count < 0, none of its pairs moves.
  * cp_page_release: what the shorter requests no longer need.  The pages behind
  *   ceil(m / page_size) of every pair go back to free_ids, in the order of
  *   requests, shards, pages, at positions info[1] .. *free_pos - 1 (a list that
  *   cp_page_slots takes from at info[1]), their table entries become -1, and rows
  *   m .. of the pages that a pair held get weight 0 and position -1 (weights,
  *   pos: each or NULL), so that tokens appended there start at weight 0.
- *   info [4] int32, 16-byte aligned: {status, the next free_pos, pages released, 0}.
+ *   info [4] int32, 16-byte aligned: {status, the next free_pos, pages released,
+ *   requests that stay as they are (0 without count)}.
  *   A step that does not fit is reported as a sum of CP_SLOTS_BAD_LENGTH (a negative
  *   length), CP_SLOTS_TABLE_FULL (a pair of more than max_pages pages) and
  *   CP_SLOTS_NO_PAGES (*free_pos outside [0, n_free], or fewer than the released
  *   pages); nothing else is written then.  keep_len >= ctx_len releases nothing.
- *   Ids go back as they stand in the table, and a pair that cp_evict_select gave
- *   count -1 loses its last pages with whatever they hold: give such a request
- *   keep_len = ctx_len first.
- * No page may belong to two pairs in any of the three.
+ *   Ids go back as they stand in the table, and every request is taken to have moved.
+ * cp_page_release_ex: the same with the count [C B] of cp_evict_select (or NULL): a
+ *   request one of whose pairs has count < 0 stays as it is, its lengths, pages,
+ *   weights and positions unread and unwritten; info[3] counts such requests.  Behind
+ *   cp_cache_move_ex it still holds its ctx_len tokens, and all others keep_len.  Without
+ *   the two a pair of count -1 loses its last pages with whatever they hold, unless
+ *   the caller gives its request keep_len = ctx_len before the choice.
+ * No page may belong to two pairs in any of them.
  * Errors: as for cp_page_slots; max_moves < 1; C B max_moves >= 2^31; max_pages
  * x page_size > 2^30 for cp_evict_select (CP_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
@@ -831,9 +838,16 @@ cp_status cp_evict_select(int C, int B, const int32_t* ctx_len, const int32_t* k
 cp_status cp_cache_move(int pairs, int max_moves, const int32_t* src, const int32_t* dst, const int32_t* count,
                         void* k_pool, void* v_pool, int row_bytes, float* scale_pool, float* weights, int32_t* pos,
                         int64_t pool_rows, void* stream);
+cp_status cp_cache_move_ex(int C, int B, int max_moves, const int32_t* src, const int32_t* dst, const int32_t* count,
+                           void* k_pool, void* v_pool, int row_bytes, float* scale_pool, float* weights, int32_t* pos,
+                           int64_t pool_rows, void* stream);
 cp_status cp_page_release(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, int32_t* page_table,
                           int max_pages, int page_size, int num_pages, int32_t* free_ids, int n_free,
                           const int32_t* free_pos, float* weights, int32_t* pos, int32_t* info, void* stream);
+cp_status cp_page_release_ex(int C, int B, const int32_t* ctx_len, const int32_t* keep_len, int32_t* page_table,
+                             int max_pages, int page_size, int num_pages, int32_t* free_ids, int n_free,
+                             const int32_t* free_pos, const int32_t* count, float* weights, int32_t* pos, int32_t* info,
+                             void* stream);
 
 /* ---------------------------------------------------------------------------
  * cp_lse_merge — exact combine of P partial results ([CTX] §3.3; [V4] §5).
