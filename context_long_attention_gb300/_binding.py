@@ -1327,7 +1327,9 @@ def cp_prefill_weights(plan: PrefillPlan, q, k, lse, sm_scale=None, window: int 
     """The attention weight of every key of a prompt batch: out [KV] fp32, the sum
     over the queries that read it (``window``: over the last so many new tokens of
     each request) and all heads of exp(score - lse).  q [T, Hq, D], k [KV, Hkv, D]
-    as given to cp_prefill_attn, lse [T, Hq] as it returned it for all ranks."""
+    as given to cp_prefill_attn, lse [T, Hq] as it returned it for all ranks.  In the order
+    of k; eviction wants pool rows: weights[slots.long()] = out, with the slots that
+    cp_page_slots gave these tokens (+= for a prefix that has weights already)."""
     dev, dtype = q.get_device(), q.dtype
     T, KV = plan.header["T"], plan.header["KV"]
     if dtype is not _bf16 and dtype is not _f32:

@@ -753,7 +753,9 @@ cp_status cp_prefix_attn_paged(const void* host_plan, const void* dev_plan, cp_d
  *
  * cp_prefill_weights: the tokens of a prompt batch.  host_plan, dev_plan, q
  *   [T, Hq, D], k [KV, Hkv, D] as given to cp_prefill_attn and lse [T, Hq] as it
- *   returned it for all ranks (rank-major); out [KV] fp32 is written.  window = 0:
+ *   returned it for all ranks (rank-major); out [KV] fp32 is written, in the order of k:
+ *   where cp_page_slots gave the tokens their slots, token j's weight belongs at
+ *   weights[slots[j]] of a pool (its first one written there, a later chunk's added).  window = 0:
  *   every query; else the last `window` new tokens of every request.  dtype
  *   CP_BF16 (D = 64, 128: tensor cores) or CP_FP32 (D = 32, 64, 96, 128: CUDA cores).
  *   ws: cp_prefill_weights_workspace_size() bytes (NULL if that is 0).
