@@ -15,8 +15,9 @@
 //   warp 4     TMA producer    warp 5  MMA issuer and TMEM owner
 // E4M3: the codes are multiplied as they are stored.  A bf16 query row enters as two
 // E4M3 numbers, hi + lo / 16 of the row times a power of two that brings its largest
-// element to [128, 256): 4 + 4 significant bits hold bf16's 8, down to elements 2^-18
-// of the largest; the columns of hi and lo lie side by side in one product.
+// element to [128, 256): 4 + 4 significant bits hold bf16's 8 down to 2^-13 of the largest,
+// and smaller elements are off by up to 2^-21 of it; the columns of hi and lo lie side by
+// side in one product.
 // Measured: 16 requests of up to 32,768 tokens, 8 kv heads of 128 (470 MB of keys) 94 us,
 // 0.75 of HBM; 64 of up to 20,000 latent E4M3 entries 90 us, 0.6: a worker
 // meets 1.4 requests there, whose 64 query rows take some 5 us each.

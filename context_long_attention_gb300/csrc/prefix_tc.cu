@@ -25,7 +25,8 @@
 // P is rounded to bf16 for its product, its sum is not.
 // E4M3 (F8): S multiplies K's codes as they are stored, with the queries as two E4M3
 // numbers each, hi + lo of the row times a power of two that brings its largest element
-// to [128, 256) (4 + 4 significant bits hold bf16's 8, down to 2^-17 of the largest); V's
+// to [128, 256): 4 + 4 significant bits hold bf16's 8 down to 2^-9 of the largest, and
+// smaller elements are off by up to 2^-17 of it (E4M3's least step, 2^-9, halved); V's
 // codes become bf16 (exact; a NaN code NaN), since P needs the range that bf16 has: warps 18-21 convert them
 // and take the relay's part, but in blocks of up to 64 rows the softmax warps without rows
 // convert.  A token's scale multiplies its column of S and, once P's sum is taken, of P.
@@ -125,7 +126,8 @@ __device__ __forceinline__ void bf16_of_codes(uint32_t codes, uint32_t& lo, uint
   top = __vimax3_u16x2(top, m, n);
 }
 // Eight elements of a query row, whose 16 lanes stand side by side, as E4M3 hi and lo of
-// the row times 2^(7 - e), its largest magnitude in [2^e, 2^(e+1)); *inv = 2^(e - 7).
+// the row times 2^(7 - e), its largest magnitude in [2^e, 2^(e+1)); *inv = 2^(e - 7).  lo at
+// hi's own scale, so that both products add up in one accumulator.
 __device__ __forceinline__ void put_codes(const uint4& x, uint8_t* row, int swizzle, int piece, float* inv) {
   const uint32_t k = 0x7fff7fffu;  // magnitudes are ordered like their bits, two bf16 at a time
   uint32_t m = __vmaxu2(__vmaxu2(x.x & k, x.y & k), __vmaxu2(x.z & k, x.w & k));

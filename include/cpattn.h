@@ -692,6 +692,9 @@ cp_status cp_rope(int T, const int32_t* pos, const uint64_t* turns, int rot, int
  * q [N, Hq, D]; kv_dtype, shard_k, shard_v, shard_scale, head dims and pools as
  * for CP_DECODE_GQA.  On the tensor cores: bf16 with D = 64 or 128 and E4M3 with
  * D = 128, in shards or a pool; every other shape on the CUDA cores.
+ * Over E4M3 on the tensor cores a query row enters the products as two E4M3 numbers
+ * an element, which hold bf16's 8 bits down to 2^-9 of the row's largest element;
+ * smaller ones are off by up to 2^-17 of it.
  * n_workers: CTAs that the work is cut for (0 = the SM count), at most 65,536.
  * ws: cp_prefix_workspace_size() bytes (NULL if that is 0).
  * Errors: as for cp_decode_attn; CP_ERR_INVALID_ARG for members < 0, no query
@@ -765,7 +768,9 @@ cp_status cp_prefix_attn_paged(const void* host_plan, const void* dev_plan, cp_d
  *   other rows stay.  mode CP_DECODE_MLA: k_pool [pool_rows, 576], one kv head.
  *   On the tensor cores: bf16 at D = 64 or 128 and at 576 (MLA), E4M3 at D = 128
  *   and 576, with at most 64 query rows x heads a kv head and 96 KB of query
- *   operands; every other shape on the CUDA cores.
+ *   operands (25 kv heads of 128 and more take more); every other shape on the CUDA
+ *   cores.  Queries over E4M3 there: 8 bits down to 2^-13 of a row's largest element,
+ *   smaller ones off by up to 2^-21 of it.
  *   No page may belong to two pairs.
  * Errors: as for cp_prefill_attn and cp_decode_attn_paged; window < 0.
  * ------------------------------------------------------------------------- */
