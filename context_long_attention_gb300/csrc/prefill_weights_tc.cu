@@ -8,11 +8,11 @@
 // so a key's weight is a sum along its own TMEM lane and stays in a thread over its
 // queries.  The work of one head is the walk over (request, key block, query tile), tiles
 // before the block's first key left out; workers (one CTA an SM) take equal parts of
-// it.  Long prompts: each worker goes through its part once for every kv head (its
-// keys once, its queries head by head), so that all workers are at the same head
-// and the L2 holds its queries; every block's sums grow over the kv heads.  Short
-// ones (fewer than kLongSteps tiles a worker): the walk has the heads inside the key block
-// and is cut between heads, too.  A block's sums end in a row of their own, or in
+// it.  Head by head (long prompts, by_heads()): each worker goes through its part once for
+// every kv head (its keys once, its queries head by head), so that all workers are at the
+// same head and the L2 holds its queries; every block's sums grow over the kv heads.
+// Otherwise the walk has the heads inside the key block and is cut between
+// heads, too.  A block's sums end in a row of their own, or in
 // one of two part rows of each worker that shares the block with others, and a last
 // kernel adds the parts in the order of the workers: no atomics, the same order every time.
 //   warps 0-15  sums: warp w takes keys [32 (w % 4), +32) of M tile (w / 4) % 2 and
@@ -29,8 +29,8 @@
 // What bounds it: a step's products need 1,024 clk of the tensor cores, and 1,280 of
 // shared memory at 128 B a clk, as both operands come from there; its 32,768 exponentials
 // take the special function units as long as the products.  16,384 queries x 32 heads over 20,480 keys:
-// 1.44 ms, 1,140 TFLOP/s (1.28 ms with the sums' work left out); the last 64 queries of
-// nine prompts of up to 30,000 tokens: 138-147 us, a chain of short steps.
+// 1.41-1.44 ms, 1,145-1,170 TFLOP/s (head by head 1.44, and 1.28 with the sums' work left
+// out); the last 64 queries of nine prompts of up to 30,000 tokens: 138-147 us, a chain of short steps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -50,7 +50,6 @@ constexpr int kBuf = 128;    // TMEM columns of a score buffer
 constexpr int kSumWarps = 16, kThreads = 32 * (kSumWarps + 4);
 constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1, kWarpRelay = kSumWarps + 2;  // and the one after it
 constexpr int kLseSlots = 4;
-constexpr int kLongSteps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // KB buffers of a key block: two where a block meets few query tiles, one where it
@@ -672,8 +671,8 @@ __global__ void __launch_bounds__(kBlock) weights_join_kernel(const Params p) {
 }
 
 struct Layout {
-  long long total = 0;
-  int n_tiles = 0, n_blocks = 0, inner = 1, bq = 64;
+  long long total = 0;  // tiles of one head
+  int n_tiles = 0, n_blocks = 0, bq = 64;
   size_t base, tile_base, block_base, lse, full, part, bytes;
 };
 Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int workers) {
@@ -685,10 +684,6 @@ Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int wo
     l.total += tiles_before(r, r.nb);
     l.n_tiles += r.nq;
     l.n_blocks += (int)(((long long)r.pre + r.n + kBlock - 1) / kBlock);
-  }
-  if (l.bq == 64 || l.total < (long long)kLongSteps * workers) {
-    l.inner = Hq;
-    l.total *= Hq;
   }
   size_t at = 0;
   auto place = [&](size_t n) {
@@ -707,6 +702,21 @@ Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int wo
 }
 
 constexpr int kWorkers = 152;  // one an SM
+
+// Whether the workers go head by head.  A pass over a kv head costs them some 9 us (64 kv heads of
+// one, 12,288 queries: 1,734 us head by head, 1,134 with the heads inside), and saves 4 to
+// 10 % where all heads' queries are well past the L2's 129 MB: what a pass saves grows
+// with its steps, tiles of a worker x heads of a kv head, and they meet at some 172.  At D = 128,
+// head by head and heads inside, us (steps of a pass, MB of queries):
+//   32 heads / 8: 16,384 queries 1,025 and 984 (108, 134); 20,480: 1,538 and 1,501 (170, 168);
+//   24,576: 2,120 and 2,147 (244, 201); 28,672: 2,803 and 2,922; 49,152: 7,906 and 8,648
+//   64 / 8: 12,288: 1,173 and 1,135 (126, 201); 16,384: 1,926 and 1,961 (219, 268)
+//   64 / 2: 16,384: 1,863 and 1,962 (875, 268); 128 / 8: 9,216: 1,333 and 1,314 (143, 302)
+// At D = 64 a step's queries are half as long, and the heads inside were faster throughout
+// (64 / 8, 32,768 queries of 268 MB: 6,028 and 5,920; 49,152 of 403 MB: 13,130 and 13,034).
+bool by_heads(const Layout& l, int T, int Hq, int G, int D, int workers) {
+  return l.bq == 128 && D == 128 && l.total * G >= 172ll * workers && (long long)T * Hq * D * 2 >= 192ll << 20;
+}
 
 template <int D, int KB, int BQ>
 cudaError_t launch_d(const CUtensorMap& km, const CUtensorMap& qm, const Params& p, cudaStream_t s) {
@@ -728,8 +738,9 @@ cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t
   Params p;
   p.a = a;
   p.workers = kWorkers;
-  p.inner = l.inner;
-  p.total = l.total;
+  const bool heads = by_heads(l, h.T, a.Hq, a.G, D, kWorkers);
+  p.inner = heads ? 1 : a.Hq;
+  p.total = l.total * p.inner;
   p.bq = l.bq;
   p.n_tiles = l.n_tiles;
   p.base = reinterpret_cast<long long*>(w + l.base);
@@ -753,11 +764,10 @@ cudaError_t launch_prefill_weights_tc(const PrefillWeightsArgs& a, const int32_t
       return cudaErrorInvalidValue;
     e = launch_early(weights_lse_kernel, (unsigned)l.n_tiles, 256, 0, s, 1, p);
     if (e == cudaSuccess) {
-      const bool many = l.inner == 1 && l.bq == 128;  // (one head alone has inner == 1, too)
       if (D == 128)
-        e = many ? launch_d<128, 1, 128>(km, qm, p, s) : l.bq == 64 ? launch_d<128, 2, 64>(km, qm, p, s) : launch_d<128, 2, 128>(km, qm, p, s);
+        e = heads ? launch_d<128, 1, 128>(km, qm, p, s) : l.bq == 64 ? launch_d<128, 2, 64>(km, qm, p, s) : launch_d<128, 2, 128>(km, qm, p, s);
       else
-        e = many ? launch_d<64, 1, 128>(km, qm, p, s) : l.bq == 64 ? launch_d<64, 2, 64>(km, qm, p, s) : launch_d<64, 2, 128>(km, qm, p, s);
+        e = l.bq == 64 ? launch_d<64, 2, 64>(km, qm, p, s) : launch_d<64, 2, 128>(km, qm, p, s);
     }
   }
   if (e == cudaSuccess) e = launch_early(weights_join_kernel, (unsigned)l.n_blocks, kBlock, 0, s, 1, p);
