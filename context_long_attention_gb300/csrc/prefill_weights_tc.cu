@@ -29,8 +29,8 @@
 // What bounds it: a step's products need 1,024 clk of the tensor cores, and 1,280 of
 // shared memory at 128 B a clk, as both operands come from there; its 32,768 exponentials
 // take the special function units as long as the products.  16,384 queries x 32 heads over 20,480 keys:
-// 1.41-1.44 ms, 1,145-1,170 TFLOP/s (head by head 1.44, and 1.28 with the sums' work left
-// out); the last 64 queries of nine prompts of up to 30,000 tokens: 138-147 us, a chain of short steps.
+// 1.44 ms, 1,140 TFLOP/s (1.28 ms with the sums' work left out); the last 64 queries of
+// nine prompts of up to 30,000 tokens: 138-147 us, a chain of short steps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -704,18 +704,18 @@ Layout layout(const cp_req_desc* reqs, int R, int KV, int Hq, int window, int wo
 constexpr int kWorkers = 152;  // one an SM
 
 // Whether the workers go head by head.  A pass over a kv head costs them some 9 us (64 kv heads of
-// one, 12,288 queries: 1,734 us head by head, 1,134 with the heads inside), and saves 4 to
-// 10 % where all heads' queries are well past the L2's 129 MB: what a pass saves grows
-// with its steps, tiles of a worker x heads of a kv head, and they meet at some 172.  At D = 128,
-// head by head and heads inside, us (steps of a pass, MB of queries):
-//   32 heads / 8: 16,384 queries 1,025 and 984 (108, 134); 20,480: 1,538 and 1,501 (170, 168);
-//   24,576: 2,120 and 2,147 (244, 201); 28,672: 2,803 and 2,922; 49,152: 7,906 and 8,648
-//   64 / 8: 12,288: 1,173 and 1,135 (126, 201); 16,384: 1,926 and 1,961 (219, 268)
-//   64 / 2: 16,384: 1,863 and 1,962 (875, 268); 128 / 8: 9,216: 1,333 and 1,314 (143, 302)
+// one, 12,288 queries: 1,734 us head by head, 1,134 with the heads inside), and saves up to
+// 10 % where all heads' queries pass the L2's 129 MB: what a pass saves grows with its
+// steps, tiles of a worker x heads of a kv head.  At D = 128 on changing inputs, head by
+// head and heads inside, us (steps of a pass, MB of queries):
+//   32 heads / 8: 12,288 queries 639 and 580 (62, 101); 16,384: 1,022 and 1,000 (109, 134), behind
+//   4,096 more keys 1,452 and 1,473 (163, 134); 20,480: 1,538 and 1,540 (170, 168); 24,576:
+//   2,145 and 2,207 (245, 201); 28,672: 2,842 and 2,994 (333, 235)
+//   64 / 8: 12,288: 1,169 and 1,171 (124, 201); 16,384: 1,944 and 2,030 (219, 268)
 // At D = 64 a step's queries are half as long, and the heads inside were faster throughout
-// (64 / 8, 32,768 queries of 268 MB: 6,028 and 5,920; 49,152 of 403 MB: 13,130 and 13,034).
+// (32 / 8, 24,576 queries of 101 MB 1,816 and 1,738; 64 / 8, 49,152 of 403 MB 13,130 and 13,034).
 bool by_heads(const Layout& l, int T, int Hq, int G, int D, int workers) {
-  return l.bq == 128 && D == 128 && l.total * G >= 172ll * workers && (long long)T * Hq * D * 2 >= 192ll << 20;
+  return l.bq == 128 && D == 128 && l.total * G >= 130ll * workers && (long long)T * Hq * D * 2 >= 128ll << 20;
 }
 
 template <int D, int KB, int BQ>
