@@ -1021,8 +1021,9 @@ _f32 = torch.float32
 class RopeFreqs:
     """Frequencies of cp_rope: ``turns`` [rot / 2] int64 on the device, the
     angle that a pair turns by at each position in units of 2^-64 turn (modulo
-    one turn), and ``scale``, the factor on cos and sin.  ``inv_freq`` keeps the
-    radians a position in 64 bits."""
+    one turn; from the frequency in 64-bit floating point, so within 2^-52 of it), and
+    ``scale``, the factor on cos and sin.  ``inv_freq`` keeps the radians a position in
+    64 bits."""
 
     def __init__(self, inv_freq, scale: float = 1.0, device=None):
         self.inv_freq = np.asarray(inv_freq, dtype=np.float64)
@@ -1044,7 +1045,10 @@ def cp_rope_freqs(rot: int, base: float = 10000.0, scaling=None, device=None) ->
                 from `high` on, a linear blend between
       "yarn"    factor, original, beta_fast = 32, beta_slow = 1, mscale = 1: the blend is
                 linear in the pair's index between those of beta_fast and beta_slow turns,
-                and cos and sin carry 0.1 mscale ln(factor) + 1 (Peng et al., "YaRN", 2023)
+                and cos and sin carry 0.1 mscale ln(factor) + 1 (Peng et al., "YaRN", 2023);
+                for a model that has the factor in its softmax scale instead (an mscale_all_dim
+                equal to its mscale) mscale=0, which leaves cos and sin as they are, and
+                sm_scale times (0.1 mscale_all_dim ln(factor) + 1)^2
     """
     if rot < 2 or rot % 2 or not base > 1:
         raise ValueError(f"rot={rot}, base={base}: need an even rot >= 2 and a base above 1")

@@ -34,7 +34,7 @@
 // 48-50 us with the merge, 0.4 of HBM: 14 tiles of 1.5 us, at HBM's rate, and some 20 us of
 // plan and first loads, the last product, fp32 parts and merge.  300 x 64 heads behind
 // 85,000 keys in five groups: 119 us.  131,072 E4M3 keys: 16 x 32 heads 95 us, a chain of
-// 54 tiles of 1.4 us; 32 x 32 heads 134 us and 64 x 32 heads 190, bound by V's conversion (four warps).
+// 54 tiles of 1.4 us; 32 x 32 heads 136 us and 64 x 32 heads 182, bound by V's conversion (four warps).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,7 +57,9 @@ constexpr int kWarpTma = kSoftmaxWarps, kWarpMma = kSoftmaxWarps + 1, kWarpRelay
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
 // E4M3: in a block of up to so many rows half of the softmax warps have none, and convert V
-// (16 x 32 heads behind 131,072 tokens 135 -> 128 us).
+// instead of the relay's four (32 heads behind 131,072 tokens: one request 133 us without
+// them and 92 with, 16 requests 135 and 95; behind 16,384 35 and 33).  Larger blocks leave a
+// quarter without rows at most.
 constexpr int kHelpRows = 64;
 
 template <int D, bool F8>
@@ -252,7 +254,7 @@ __device__ __noinline__ void process(const Params& p, const Maps<MAXC>& maps, Sh
   constexpr int NC = NS / 2;           // of one half of a row
   // Score columns in registers at a time: all of a half's and their P need more registers than
   // a thread has (80 over E4M3, with its further warps: 64 x 32 heads behind 131,072 tokens took
-  // 516 us and take 190, 16 x 32 heads 117 and 96; bf16, 96 registers: 300 x 64 heads 124 and 119)
+  // 516 us and take 182, 16 x 32 heads 117 and 95; bf16, 96 registers: 300 x 64 heads 124 and 119)
   constexpr int NB = 16;
   // a half row's P sum that can hide a P above 2^8
   constexpr float kSpecSum = NC * 256.f;

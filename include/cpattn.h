@@ -86,7 +86,10 @@ typedef enum {
  * tables at the word offsets the header gives.  The host part (header and
  * tables) is written by the host into `host_plan` and copied, in stream
  * order, to the front of `dev_plan`; per-token arrays exist only in
- * `dev_plan` and are written there by a device kernel.
+ * `dev_plan` and are written there by a device kernel.  A kernel may read the
+ * header's tables in dev_plan before the kernel ahead of it in the stream has ended: what
+ * fills them is a copy (the plan call's, or a cudaMemcpyAsync of the caller's),
+ * never a kernel right before the call.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t magic;      /* CP_PLAN_MAGIC */
