@@ -117,7 +117,7 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // Four E4M3 codes as bf16, two words of two.  With the code's exponent and mantissa at
 // bf16's place a code is 2^-120 of its value (subnormal codes are subnormal bf16),
 // and the product with 2^120 is exact.
-// *top: the largest magnitude so far, two at a time in the upper bytes of halves.
+// top: the largest magnitude so far, of two columns of codes in the upper bytes of halves.
 __device__ __forceinline__ void bf16_of_codes(uint32_t codes, uint32_t& lo, uint32_t& hi, uint32_t& top) {
   const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);  // codes in the upper bytes of halves
   const uint32_t m = a & 0x7f007f00u, n = b & 0x7f007f00u;
